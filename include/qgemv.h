@@ -528,6 +528,208 @@ qgemv_status qgemv_q4_0_gather_f32(const qgemv_gather_f32_matrix *mats, int n_ma
                                    int n_ids, int n_experts, qgemv_wlayout layout, int T, void *ws,
                                    size_t ws_bytes, qgemv_stream_t stream);
 
+/* ---- Between the GEMVs of a decode step: rotary positions with the write
+ * into a key/value cache, attention over the cache, and the rules applied
+ * to the logits before a token is taken (minfer README "How it works": RoPE,
+ * GQA attention over a cache, device-side argmax; M17: a verify step runs
+ * several positions of one sequence at once). */
+
+/* Element types of these calls' tensors. */
+typedef enum { QGEMV_F32 = 0, QGEMV_F16 = 1, QGEMV_BF16 = 2 } qgemv_dtype;
+
+/* A paged key/value cache: n_pages pages of page_size rows, each row holding
+ * n_heads heads of head_dim elements of `type` (QGEMV_F16 or QGEMV_BF16).
+ * Row r of page g, head h starts at k (or v) + g * page_stride +
+ * r * row_stride + h * head_stride elements; a head's elements are
+ * contiguous.  So both [page][row][head] and [page][head][row] orders work.
+ * A flat row index ("slot") is g * page_size + r.  page_size is a power of
+ * two (at least 1); head_dim % 8 == 0, 8 <= head_dim <= 256.  k and v are
+ * 16-byte aligned and the strides multiples of 8 elements; the rows of
+ * different (page, row, head) must not overlap. */
+typedef struct {
+    void *k;
+    void *v;
+    qgemv_dtype type;
+    int64_t n_pages;
+    int page_size;
+    int n_heads;
+    int head_dim;
+    int64_t page_stride;
+    int64_t row_stride;
+    int64_t head_stride;
+} qgemv_kv_cache;
+
+/* Which elements of a head's first rot_dim form the pairs (x, y):
+ * HALF: x = e[i], y = e[i + rot_dim / 2];  INTERLEAVED: x = e[2i], y = e[2i + 1]. */
+typedef enum { QGEMV_ROPE_HALF = 0, QGEMV_ROPE_INTERLEAVED = 1 } qgemv_rope_layout;
+
+/* Scaling of the frequencies theta_i = base^(-2i / rot_dim), i < rot_dim / 2,
+ * for contexts longer than the trained length L = orig_len:
+ *   PLAIN : as they are.
+ *   LINEAR: theta_i / factor (positions squeezed into the trained range).
+ *   BANDS : by wavelength, with t = L theta_i / (2 pi) turns over the trained
+ *           length and s = clamp((t - low) / (high - low), 0, 1):
+ *           theta_i ((1 - s) / factor + s).
+ *   YARN  : by pair index, with pair(t) = rot_dim ln(L / (2 pi t)) / (2 ln base),
+ *           a = max(0, floor(pair(high))), b = min(rot_dim - 1, ceil(pair(low))) and
+ *           w = clamp((i - a) / max(b - a, 0.001), 0, 1):
+ *           theta_i (1 - w) + theta_i / factor * w.
+ * factor >= 1.  BANDS and YARN need orig_len > 0 and 0 < low < high (usual
+ * values: 1 and 4, 1 and 32). */
+typedef enum {
+    QGEMV_ROPE_PLAIN = 0,
+    QGEMV_ROPE_LINEAR = 1,
+    QGEMV_ROPE_BANDS = 2,
+    QGEMV_ROPE_YARN = 3
+} qgemv_rope_scaling;
+
+typedef struct {
+    int rot_dim; /* elements of a head that rotate: even, 2..256 */
+    qgemv_rope_layout layout;
+    qgemv_rope_scaling scaling;
+    double base;     /* > 1 */
+    double factor;   /* ignored by PLAIN */
+    double orig_len; /* BANDS, YARN */
+    double low, high;
+    double mscale;   /* multiplies cosine and sine; 0 means 1, for YARN 0.1 ln(factor) + 1 */
+} qgemv_rope_config;
+
+/* The frequencies in the form the kernel takes (host memory, no pointers:
+ * copy it freely).  turns[i] = theta_i / (2 pi) in units of 2^-64 turns
+ * (from a 53-bit theta): the angle's fraction of a turn is the low 64 bits
+ * of pos * turns[i], a product without rounding, so that long contexts lose
+ * nothing. */
+typedef struct {
+    uint64_t turns[128];
+    float mscale;
+    int rot_dim;
+    int layout;
+} qgemv_rope_plan;
+
+/* Fill *plan from *cfg (host only, no device work). */
+qgemv_status qgemv_rope_init(const qgemv_rope_config *cfg, qgemv_rope_plan *plan);
+
+/* Rotary positions and the cache write, one launch.  For every token
+ * t < n_tokens at position pos[t] (int32, device):
+ *   q_out[t][h] = rotated q[t][h], h < n_q_heads, in q_type (rounded once);
+ *   cache row slots[t] (int32, device): k = rotated k[t][h], v = v[t][h],
+ *   h < cache->n_heads, rounded once to the cache's type.
+ * A pair becomes (x c - y s, x s + y c) with c, s = mscale * cos, sin of
+ * pos[t] * theta_i, all in fp32; elements from rot_dim on are copied.
+ * slots[t] == -1 writes no row; another slot outside the cache writes none
+ * either and records QGEMV_ERR_BAD_ID.  Two tokens must not name one slot.
+ * q, k, v are [t][h][head_dim] of in_type with the given strides in elements
+ * between tokens (heads are head_dim apart), as the parts of one QKV
+ * product's output are.  q may be NULL (k and v only), or k and v both
+ * (q only; slots is then ignored).  q_out may be q itself (same type and
+ * stride); otherwise outputs must not overlap inputs.  Pointers are aligned
+ * to their elements; with head_dim and rot_dim multiples of 8, 16-byte
+ * aligned bases and strides, 16-byte accesses are used. */
+qgemv_status qgemv_rope_kv(const qgemv_rope_plan *plan, const void *q, const void *k, const void *v,
+                           qgemv_dtype in_type, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                           const int32_t *pos, const int32_t *slots, int64_t n_tokens, int n_q_heads, int head_dim,
+                           void *q_out, qgemv_dtype q_type, int64_t q_out_stride, const qgemv_kv_cache *cache,
+                           qgemv_stream_t stream);
+
+/* A batch of n_seqs sequences whose contexts begin with the same prefix.
+ * Sequence b's context is the prefix's prefix_len rows, then its own
+ * suffix_len[b] rows.  Row j of the prefix is row j % page_size of page
+ * prefix_pages[j / page_size]; row j of suffix b is row j % page_size of
+ * page suffix_pages[b * suffix_pages_stride + j / page_size] (all int32,
+ * device; entries past a length are not read).  So a page belongs to the
+ * prefix or to one suffix, and both may end inside a page.
+ * Each sequence has n_q queries (1..8), the last n_q tokens of its context:
+ * query i sees the prefix and its suffix rows j <= suffix_len[b] - n_q + i.
+ * A length outside [0, max_suffix] counts as the nearer end and a page
+ * outside the cache as absent (its rows are not seen); both record
+ * QGEMV_ERR_BAD_ID.  n_q_heads is a multiple of the cache's n_heads; query
+ * head h reads cache head h / (n_q_heads / n_heads). */
+typedef struct {
+    int n_seqs;
+    int n_q;
+    int n_q_heads;
+    int prefix_len;
+    const int32_t *prefix_pages;
+    const int32_t *suffix_len;
+    const int32_t *suffix_pages;
+    int64_t suffix_pages_stride;
+    int max_suffix; /* bound on suffix_len, for the launch's shape and the workspace */
+    float scale;    /* of the scores; 0 means 1 / sqrt(head_dim) */
+} qgemv_attn_batch;
+
+/* Workspace bytes of qgemv_attn_prefix (0 for an invalid batch). */
+size_t qgemv_attn_workspace_bytes(const qgemv_attn_batch *batch, const qgemv_kv_cache *cache);
+
+/* o[b * n_q + i][h] = softmax over the rows the query sees of scale * q.k,
+ * times v (minfer README: GQA attention with split keys, partial results
+ * combined).  The prefix's keys and values are read once for all sequences.
+ * q and o are [token][head][head_dim] with strides in elements between
+ * tokens and heads, q of the cache's type, 16-byte aligned with strides
+ * multiples of 8; o of the cache's type or fp32.  A query that sees no row
+ * gives zeros.  lse (or NULL) receives the natural logarithm of the sum of
+ * exp(scale * q.k), fp32 [token][n_q_heads], -infinity for such a query.
+ * Scores, maxima, sums and outputs are accumulated in fp32; the softmax
+ * weights enter the product with v rounded to the cache's type, as matrix
+ * operands.  Rows that a query does not see never reach its result, whatever
+ * they hold.  Results do not depend on the order in which the GPU runs the
+ * parts.  ws: qgemv_attn_workspace_bytes, 16-byte aligned. */
+qgemv_status qgemv_attn_prefix(const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                               const qgemv_kv_cache *cache, const qgemv_attn_batch *batch, void *o,
+                               qgemv_dtype o_type, int64_t o_token_stride, int64_t o_head_stride, float *lse_or_null,
+                               void *ws, size_t ws_bytes, qgemv_stream_t stream);
+
+/* Rules on the logits of `rows` rows over a vocabulary of `vocab` tokens.
+ * Every pointer is a device pointer and may be NULL (that rule is then off).
+ *   history [r][history_stride] int64, history_len [r] int32: the row's
+ *     tokens so far, entries from history_len[r] on unread; c = how often a
+ *     token occurs.  Ids outside [0, vocab) are passed over.
+ *   repetition, frequency, presence [r] fp32: for a token with c > 0,
+ *     x = x > 0 ? x / repetition : x * repetition, then x -= frequency * c,
+ *     then x -= presence.
+ *   bias_ids [r][bias_stride] int64, bias [r][bias_stride] fp32, bias_len
+ *     [r] int32: x += bias of the token's entry; where a list names a token
+ *     twice the later entry counts.
+ *   mask [r][mask_stride] 32-bit words: token t is allowed when bit t % 32
+ *     of word t / 32 is set; others become -infinity, whatever x was.
+ * The rules apply in this order, each step one fp32 operation rounded to
+ * nearest.  max_history and max_bias bound the lengths (history < 2^20,
+ * bias <= 4095); a length outside [0, bound] counts as the nearer end and
+ * records QGEMV_ERR_BAD_ID. */
+typedef struct {
+    int rows;
+    int64_t vocab;
+    const int64_t *history;
+    int64_t history_stride;
+    const int32_t *history_len;
+    int max_history;
+    const float *repetition;
+    const float *frequency;
+    const float *presence;
+    const int64_t *bias_ids;
+    const float *bias;
+    int64_t bias_stride;
+    const int32_t *bias_len;
+    int max_bias;
+    const uint32_t *mask;
+    int64_t mask_stride;
+} qgemv_logits_spec;
+
+/* Workspace bytes of qgemv_logits_rules (0 for an invalid shape); it uses
+ * only the counter area. */
+size_t qgemv_logits_workspace_bytes(const qgemv_logits_spec *spec);
+
+/* Apply the rules to logits[r][x_stride] (fp32, f16 or bf16) and find each
+ * row's best token.  out (or NULL) receives the results in the same type,
+ * rows out_stride elements apart; it may be `logits` itself (same stride)
+ * and must not overlap it otherwise.  idx (int64 [rows]) and val (fp32
+ * [rows]), both or neither NULL, receive the lowest token whose fp32 result
+ * is maximal (-0 == +0, returned as +0; NaN is passed over) and that result;
+ * a row without a result above -infinity gives -1 and -infinity.  One launch
+ * per 1024 rows. */
+qgemv_status qgemv_logits_rules(const void *logits, qgemv_dtype type, int64_t x_stride, const qgemv_logits_spec *spec,
+                                void *out, int64_t out_stride, int64_t *idx, float *val, void *ws, size_t ws_bytes,
+                                qgemv_stream_t stream);
+
 /* Test hook: the exact per-block integer sums the GEMV kernels form,
  * isums[T][N][K/32] int32 (device), from the same unpack / int8-dot code. */
 qgemv_status qgemv_debug_block_isums(const void *W, qgemv_wlayout layout, const void *xq,

@@ -59,6 +59,45 @@ class GatherF32Matrix(ctypes.Structure):
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
 
 
+F32, F16, BF16 = 0, 1, 2
+_DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}
+
+
+class KvCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("type", ctypes.c_int), ("n_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int), ("n_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("layout", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("orig_len", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("mscale", ctypes.c_double)]
+
+
+class RopePlan(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_uint64 * 128), ("mscale", ctypes.c_float), ("rot_dim", ctypes.c_int),
+                ("layout", ctypes.c_int)]
+
+
+class AttnBatchStruct(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("n_q", ctypes.c_int), ("n_q_heads", ctypes.c_int),
+                ("prefix_len", ctypes.c_int), ("prefix_pages", ctypes.c_void_p), ("suffix_len", ctypes.c_void_p),
+                ("suffix_pages", ctypes.c_void_p), ("suffix_pages_stride", ctypes.c_int64),
+                ("max_suffix", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class LogitsSpec(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("vocab", ctypes.c_int64), ("history", ctypes.c_void_p),
+                ("history_stride", ctypes.c_int64), ("history_len", ctypes.c_void_p), ("max_history", ctypes.c_int),
+                ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("bias_stride", ctypes.c_int64),
+                ("bias_len", ctypes.c_void_p), ("max_bias", ctypes.c_int), ("mask", ctypes.c_void_p),
+                ("mask_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 _VP, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
@@ -108,6 +147,13 @@ _SIGS = {
     "qgemv_gs64_workspace_bytes": ([_I64, _I64, _I32], _SZ),
     "qgemv_gs64": ([_VP, _VP, _VP, _VP, _I64, _I64, _I32, _VP, _SZ, _VP], _I32),
     "qgemv_gs64_f32": ([_VP, _VP, _VP, _I64, _I64, _I32, _VP, _SZ, _VP], _I32),
+    "qgemv_rope_init": ([ctypes.POINTER(RopeConfig), ctypes.POINTER(RopePlan)], _I32),
+    "qgemv_rope_kv": ([_VP, _VP, _VP, _VP, _I32, _I64, _I64, _I64, _VP, _VP, _I64, _I32, _I32, _VP, _I32, _I64, _VP,
+                       _VP], _I32),
+    "qgemv_attn_workspace_bytes": ([_VP, _VP], _SZ),
+    "qgemv_attn_prefix": ([_VP, _I64, _I64, _VP, _VP, _VP, _I32, _I64, _I64, _VP, _VP, _SZ, _VP], _I32),
+    "qgemv_logits_workspace_bytes": ([_VP], _SZ),
+    "qgemv_logits_rules": ([_VP, _I32, _I64, _VP, _VP, _I64, _VP, _VP, _VP, _SZ, _VP], _I32),
     "qgemv_debug_block_isums": ([_VP, _I32, _VP, _VP, _I64, _I64, _I32, _VP], _I32),
     "qgemv_debug_block_isums_tc": ([_VP, _I32, _VP, _VP, _I64, _I64, _I32, _I32, _VP], _I32),
     "qgemv_debug_stream_read": ([_VP, _SZ, _I32, _I32, _I32, _I32, _VP, _VP], _I32),
@@ -432,6 +478,196 @@ def gather_f32_workspace_bytes(mats: ctypes.Array, n_ids: int, T: int) -> int:
 def gemv_gather_f32(mats: ctypes.Array, ids, n_experts: int, layout: int, T: int, ws, stream=None):
     _check(lib().qgemv_q4_0_gather_f32(mats, len(mats), _ptr(ids), ids.numel(), n_experts, layout, T, _ptr(ws),
                                        ws.numel(), _stream(stream)), "qgemv_q4_0_gather_f32")
+
+
+# ---------------------------------------------- between the GEMVs of a step
+
+def rope_plan(rot_dim: int, base: float, layout: str = "half", scaling: str = "plain", factor: float = 1.0,
+              orig_len: float = 0.0, low: float | None = None, high: float | None = None,
+              mscale: float = 0.0) -> RopePlan:
+    """Frequencies of rotary positions (host; keep it across calls).  low and
+    high default to 1 and 4 for "bands", 1 and 32 for "yarn"; mscale 0 means
+    1, for "yarn" 0.1 ln(factor) + 1."""
+    if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+        raise ValueError(f"rope_plan: layout {layout!r}, scaling {scaling!r}")
+    cfg = RopeConfig(rot_dim, ROPE_LAYOUTS[layout], ROPE_SCALINGS[scaling], base, factor, orig_len,
+                     1.0 if low is None else low, (4.0 if scaling == "bands" else 32.0) if high is None else high, mscale)
+    plan = RopePlan()
+    _check(lib().qgemv_rope_init(ctypes.byref(cfg), ctypes.byref(plan)), "qgemv_rope_init")
+    plan.address = ctypes.addressof(plan)
+    return plan
+
+
+class KvCache:
+    """A paged cache: k and v f16 or bf16 tensors [pages][page_size][heads][head_dim]
+    of the same strides (elements of a head contiguous).  For pages laid out
+    [pages][heads][page_size][head_dim] pass k.transpose(1, 2), v.transpose(1, 2)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.stride(3) != 1:
+            raise ValueError("KvCache: k and v [pages][page_size][heads][head_dim] of one type and the same strides")
+        assert k.is_cuda and v.is_cuda and k.dtype in (torch.float16, torch.bfloat16)
+        self.k, self.v = k, v
+        self.struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], k.shape[0], k.shape[1], k.shape[2],
+                                    k.shape[3], k.stride(0), k.stride(1), k.stride(2))
+        self.address = ctypes.addressof(self.struct)
+
+
+def _heads(x, what: str):
+    """A [tokens][heads][head_dim] tensor whose heads are contiguous and adjacent."""
+    if not x.is_cuda or x.dim() != 3 or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+        raise ValueError(f"{what}: a CUDA tensor [tokens][heads][head_dim] with adjacent heads")
+    return x.data_ptr(), x.stride(0)
+
+
+def _i32(x, what: str, n: int | None = None):
+    if x is None:
+        return None
+    if not x.is_cuda or x.dtype != torch.int32 or not x.is_contiguous() or (n is not None and x.numel() < n):
+        raise ValueError(f"{what}: a contiguous int32 CUDA tensor" + (f" of {n}" if n is not None else ""))
+    return x.data_ptr()
+
+
+def rope_kv(plan: RopePlan, xq, xk, xv, pos, slots=None, cache: KvCache | None = None, out=None, stream=None):
+    """Rotate q [tokens][heads][head_dim] into `out` (default: a new tensor of the
+    cache's type, or of q's without a cache) and k, v [tokens][kv heads][head_dim] into
+    the cache rows `slots` (-1: none).  xq, or xk and xv, may be None.  Returns out."""
+    some = xq if xq is not None else xk
+    n, d = some.shape[0], some.shape[2]
+    qp = qs = kp = ks = vp = vs = op = os_ = 0
+    hq = 0
+    if xk is not None:
+        kp, ks = _heads(xk, "rope_kv: k")
+        vp, vs = _heads(xv, "rope_kv: v")
+        if xv.shape != xk.shape or xv.dtype != xk.dtype or xk.dtype != some.dtype or xk.shape[0] != n or \
+                xk.shape[2] != d or xk.shape[1] != cache.struct.n_heads:
+            raise ValueError("rope_kv: k and v of q's type and tokens, with the cache's heads")
+    if xq is not None:
+        qp, qs = _heads(xq, "rope_kv: q")
+        hq = xq.shape[1]
+        if out is None:
+            out = torch.empty((n, hq, d), dtype=cache.k.dtype if cache is not None else xq.dtype, device=xq.device)
+        op, os_ = _heads(out, "rope_kv: out")
+        if out.shape != xq.shape:
+            raise ValueError("rope_kv: out has q's shape")
+    _check(lib().qgemv_rope_kv(plan.address, qp, kp, vp, _DTYPES[some.dtype], qs, ks, vs, _i32(pos, "rope_kv: pos", n),
+                               _i32(slots, "rope_kv: slots", n), n, hq, d, op,
+                               _DTYPES[out.dtype] if out is not None else F32, os_,
+                               cache.address if cache is not None else None, _stream(stream)), "qgemv_rope_kv")
+    return out
+
+
+class AttnBatch:
+    """Sequences that share a prefix, over a cache (see qgemv_attn_batch): the
+    tables and lengths are device tensors that later calls read again, so a
+    decode loop updates them in place.  scale None: 1 / sqrt(head_dim)."""
+
+    def __init__(self, n_seqs: int, n_q: int, n_heads: int, cache: KvCache, prefix_len: int, prefix_pages, suffix_len,
+                 suffix_pages, max_suffix: int, scale: float | None = None):
+        page = cache.struct.page_size
+        own = 0
+        if max_suffix > 0:
+            if suffix_pages.dim() != 2 or suffix_pages.shape[0] != n_seqs or suffix_pages.stride(1) != 1 or \
+                    suffix_pages.shape[1] * page < max_suffix or not suffix_pages.is_cuda or \
+                    suffix_pages.dtype != torch.int32:
+                raise ValueError("AttnBatch: suffix_pages int32 [n_seqs][pages that hold max_suffix rows]")
+            own = suffix_pages.data_ptr()
+        self.cache, self.tables = cache, (prefix_pages, suffix_len, suffix_pages)
+        self.n_seqs, self.n_q, self.n_heads = n_seqs, n_q, n_heads
+        self.struct = AttnBatchStruct(
+            n_seqs, n_q, n_heads, prefix_len,
+            _i32(prefix_pages, "AttnBatch: prefix_pages", -(-prefix_len // page)) if prefix_len else None,
+            _i32(suffix_len, "AttnBatch: suffix_len", n_seqs), own, suffix_pages.stride(0) if own else 0, max_suffix,
+            0.0 if scale is None else scale)
+        self.address = ctypes.addressof(self.struct)
+
+    def workspace_bytes(self) -> int:
+        return int(lib().qgemv_attn_workspace_bytes(self.address, self.cache.address))
+
+
+def attn_prefix(xq, batch: AttnBatch, ws, out=None, lse=None, stream=None):
+    """Attention of q [n_seqs][n_q][heads][head_dim] (or [tokens][heads][head_dim]) over the
+    batch's contexts; out (the cache's type or fp32, q's shape; default: a new tensor
+    of the cache's type); lse fp32 [tokens][heads] or None."""
+    c, b = batch.cache.struct, batch.struct
+    d = c.head_dim
+    if xq.numel() != b.n_seqs * b.n_q * b.n_q_heads * d or xq.shape[-1] != d or xq.shape[-2] != b.n_q_heads or \
+            not xq.is_cuda or xq.dtype != batch.cache.k.dtype:
+        raise ValueError("attn_prefix: q [n_seqs][n_q][heads][head_dim] of the cache's type")
+    if out is None:
+        out = torch.empty(xq.shape, dtype=xq.dtype, device=xq.device)
+    strides = []
+    for x in (xq, out):
+        st = x.stride()
+        if st[-1] != 1 or (x.dim() == 4 and x.shape[0] > 1 and st[0] != x.shape[1] * st[1]) or x.dim() not in (3, 4):
+            raise ValueError("attn_prefix: q and out with contiguous heads and evenly spaced tokens")
+        strides.append((st[-3], st[-2]))
+    if out.shape != xq.shape or not out.is_cuda:
+        raise ValueError("attn_prefix: out has q's shape")
+    _check(lib().qgemv_attn_prefix(xq.data_ptr(), strides[0][0], strides[0][1], batch.cache.address, batch.address,
+                                   out.data_ptr(), _DTYPES[out.dtype], strides[1][0], strides[1][1], _ptr(lse),
+                                   _ptr(ws), ws.numel(), _stream(stream)), "qgemv_attn_prefix")
+    return out
+
+
+class LogitsRules:
+    """Rules on logits of `rows` rows over `vocab` tokens (see
+    qgemv_logits_spec): device tensors that later calls read again, so a
+    decode loop appends to `history` and counts up `history_len` in place.
+    history int64 [rows][most], history_len int32 [rows]; repetition, frequency, presence
+    fp32 [rows]; bias_ids int64, bias fp32 [rows][most], bias_len int32 [rows];
+    mask int32 [rows][vocab / 32 rounded up] (or one row for all)."""
+
+    def __init__(self, rows: int, vocab: int, history=None, history_len=None, repetition=None, frequency=None,
+                 presence=None, bias_ids=None, bias=None, bias_len=None, mask=None):
+        self.rows, self.vocab = rows, vocab
+        self.tensors = (history, history_len, repetition, frequency, presence, bias_ids, bias, bias_len, mask)
+
+        def table(x, dtype, what, one_row=False):
+            if x is None:
+                return None, 0, 0
+            if not x.is_cuda or x.dtype != dtype or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1) or \
+                    (x.shape[0] != rows and not (one_row and x.shape[0] == 1)):
+                raise ValueError(f"LogitsRules: {what} [rows][..] {dtype}")
+            return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else 0, x.shape[1]
+
+        def row(x, what):
+            if x is None:
+                return None
+            if not x.is_cuda or x.dtype != torch.float32 or not x.is_contiguous() or x.numel() != rows:
+                raise ValueError(f"LogitsRules: {what} fp32 [rows]")
+            return x.data_ptr()
+
+        hp, hs, hn = table(history, torch.int64, "history")
+        ip, is_, n_ids = table(bias_ids, torch.int64, "bias_ids")
+        bp, bs, bn = table(bias, torch.float32, "bias")
+        mp, ms, mn = table(mask, torch.int32, "mask", one_row=True)
+        if (is_, n_ids) != (bs, bn) or (mask is not None and mn * 32 < vocab):
+            raise ValueError("LogitsRules: bias_ids and bias of one shape and stride; mask with a bit per token")
+        self.struct = LogitsSpec(rows, vocab, hp, hs, _i32(history_len, "LogitsRules: history_len", rows), hn,
+                                 row(repetition, "repetition"), row(frequency, "frequency"), row(presence, "presence"),
+                                 ip, bp, bs, _i32(bias_len, "LogitsRules: bias_len", rows), bn, mp, ms)
+        self.address = ctypes.addressof(self.struct)
+
+    def workspace_bytes(self) -> int:
+        return int(lib().qgemv_logits_workspace_bytes(self.address))
+
+
+def logits_rules(x, rules: LogitsRules, ws, out=None, idx=None, val=None, stream=None):
+    """Apply the rules to x [rows][vocab] (fp32, f16, bf16); out (None: not
+    written; may be x) receives the results in x's type.  Returns each row's best
+    token (int64, -1 for none) and its value (fp32)."""
+    if not x.is_cuda or x.dim() != 2 or x.shape != (rules.rows, rules.vocab) or x.stride(1) != 1 or \
+            (out is not None and (out.shape != x.shape or out.dtype != x.dtype or out.stride(1) != 1 or not out.is_cuda)):
+        raise ValueError("logits_rules: x (and out) CUDA tensors [rows][vocab]")
+    idx = idx if idx is not None else torch.empty(rules.rows, dtype=torch.int64, device=x.device)
+    val = val if val is not None else torch.empty(rules.rows, dtype=torch.float32, device=x.device)
+    if idx.numel() != rules.rows or idx.dtype != torch.int64 or val.numel() != rules.rows or val.dtype != torch.float32:
+        raise ValueError("logits_rules: idx int64 and val fp32 of rows")
+    _check(lib().qgemv_logits_rules(x.data_ptr(), _DTYPES[x.dtype], x.stride(0), rules.address,
+                                    out.data_ptr() if out is not None else None, out.stride(0) if out is not None else 0,
+                                    _ptr(idx), _ptr(val), _ptr(ws), ws.numel(), _stream(stream)), "qgemv_logits_rules")
+    return idx, val
 
 
 def block_isums(W, layout: int, xq, N: int, K: int, T: int, stream=None) -> torch.Tensor:

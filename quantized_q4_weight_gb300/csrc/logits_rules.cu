@@ -1,0 +1,258 @@
+// logits_rules.cu -- penalties for repeated tokens, biases and grammar masks
+// on logits, with the argmax of the result (minfer README "How it works":
+// device-side argmax; the rules come between the lm_head and that argmax).
+//
+// Per row, with c the token's count in the row's history:
+//   x = c > 0 ? (x > 0 ? x / rep : x * rep) : x;  x -= freq * c;
+//   x -= pres * [c > 0];  x += bias;  x = -inf where the mask's bit is 0.
+//
+// A block takes a slice of one row's vocabulary.  The tokens that a history
+// or a bias list touches are few, so the block keeps one bit per token of
+// its slice (touched or not) and one 32-bit word for the touched ones:
+//   bits 0..19: the count c;  bits 20..31: 1 + the entry of the bias list.
+// The words are never cleared as a whole: a first pass over the two lists
+// sets a token's bit and zeroes its word, a second one raises the words
+// (atomicMax of the bias entry: the last entry counts; then atomicAdd of
+// the counts).  All of that is integer arithmetic, so the order in which
+// threads run changes nothing.  Then the logits stream through once, 16
+// bytes a load, four or eight mask and touched bits at a time.
+//
+// What bounds it: memory for many rows (logits read and written once); for
+// one row, the latency of the chain launch, lists, logits, merge, which is
+// why the slices get small then.  Every slice reads its row's whole lists
+// (from L2); slices of 16384 tokens keep that under a tenth of the row's
+// own bytes for histories of a thousand tokens.
+#include "decode_ops.h"
+#include "qgemv_internal.cuh"
+
+namespace qg {
+namespace {
+
+constexpr int LG_THREADS = 512;
+constexpr int LG_SLICE_MAX = 16384;  // 64 KB of words: three blocks per multiprocessor
+constexpr int LG_SLICE_MIN = 2048;   // one 16-byte load of fp32 a thread
+constexpr unsigned LG_COUNT_MASK = (1u << 20) - 1;
+
+__device__ __forceinline__ float lg_to_f(float v) { return v; }
+__device__ __forceinline__ float lg_to_f(__half v) { return __half2float(v); }
+__device__ __forceinline__ float lg_to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void lg_from_f(float &o, float v) { o = v; }
+__device__ __forceinline__ void lg_from_f(__half &o, float v) { o = __float2half_rn(v); }
+__device__ __forceinline__ void lg_from_f(__nv_bfloat16 &o, float v) { o = __float2bfloat16_rn(v); }
+
+// A float's bits in an order that unsigned comparison respects.
+__device__ __forceinline__ unsigned ordered(float f)
+{
+    const unsigned u = __float_as_uint(f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float from_ordered(unsigned o)
+{
+    return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+
+template <typename T>
+struct alignas(16) Chunk {
+    T e[16 / sizeof(T)];
+};
+
+__device__ __forceinline__ int bounded_length(const int32_t *len, long long r, int most, unsigned *status)
+{
+    const int n = __ldg(len + r);
+    if (n < 0 || n > most) {
+        if (threadIdx.x == 0) atomicCAS(status, 0u, ST_BAD_ID);
+        return n < 0 ? 0 : most;
+    }
+    return n;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(LG_THREADS) logits_kernel(const __grid_constant__ LogitsParams p)
+{
+    constexpr int E = 16 / sizeof(T);
+    extern __shared__ __align__(16) unsigned lg_smem[];
+    __shared__ unsigned long long s_best[LG_THREADS / 32];
+    unsigned *words = lg_smem;                  // [slice]
+    unsigned *touched = lg_smem + p.slice;      // [slice / 32]
+    const int tid = threadIdx.x;
+    const long long r = blockIdx.y;
+
+    pdl_launch_dependents();
+    for (int i = tid; i < p.slice / 32; i += LG_THREADS) touched[i] = 0;
+    pdl_wait();
+
+    const T *x = static_cast<const T *>(p.x) + r * p.x_stride;
+    T *out = p.out ? static_cast<T *>(p.out) + r * p.out_stride : nullptr;
+    // The row in 16-byte chunks of memory: chunk c holds tokens c E - shift ..
+    // + E - 1.  The slice is a range of chunks, its first token t0 (the
+    // first chunk's tokens below 0 and the last one's from vocab on are not
+    // there: such chunks go element by element).
+    const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    const bool out_vec = out && (reinterpret_cast<uintptr_t>(out) & 15) / sizeof(T) == static_cast<unsigned>(shift);
+    const long long t0 = static_cast<long long>(blockIdx.x) * p.slice - shift;
+    const long long t1 = min(p.vocab, t0 + p.slice);
+
+    const int nh = p.hist ? bounded_length(p.hist_len, r, p.max_hist, p.status) : 0;
+    const int nb = p.bias ? bounded_length(p.bias_len, r, p.max_bias, p.status) : 0;
+    const long long *hist = p.hist + r * p.hist_stride;
+    const long long *bid = p.bias_ids + r * p.bias_stride;
+    const float *bias = p.bias + r * p.bias_stride;
+    const float rep = p.rep ? __ldg(p.rep + r) : 1.0f;
+    const float freq = p.freq ? __ldg(p.freq + r) : 0.0f;
+    const float pres = p.pres ? __ldg(p.pres + r) : 0.0f;
+    const long long lo = max(t0, 0ll);
+
+    if (nh | nb) {
+        __syncthreads();
+        for (int i = tid; i < nh + nb; i += LG_THREADS) {
+            const long long t = i < nh ? __ldg(hist + i) : __ldg(bid + (i - nh));
+            if (t >= lo && t < t1) {
+                const int l = static_cast<int>(t - t0);
+                words[l] = 0;
+                atomicOr(&touched[l >> 5], 1u << (l & 31));
+            }
+        }
+        __syncthreads();
+        for (int i = tid; i < nb; i += LG_THREADS) {
+            const long long t = __ldg(bid + i);
+            if (t >= lo && t < t1) atomicMax(&words[t - t0], static_cast<unsigned>(i + 1) << 20);
+        }
+        __syncthreads();
+        for (int i = tid; i < nh; i += LG_THREADS) {
+            const long long t = __ldg(hist + i);
+            if (t >= lo && t < t1) atomicAdd(&words[t - t0], 1u);
+        }
+    }
+    __syncthreads();
+
+    auto rule = [&](float v, int l) {  // the touched token t0 + l
+        const unsigned w = words[l], c = w & LG_COUNT_MASK, b = w >> 20;
+        if (c) {
+            v = v > 0.0f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
+            v = __fsub_rn(v, __fmul_rn(freq, static_cast<float>(c)));
+            v = __fsub_rn(v, pres);
+        }
+        return b ? __fadd_rn(v, __ldg(bias + (b - 1))) : v;
+    };
+
+    const float NEG = __int_as_float(0xFF800000);
+    float best = NEG;
+    long long best_t = 0;
+    const uint32_t *mask = p.mask ? p.mask + r * p.mask_stride : nullptr;
+    const long long mask_last = (p.vocab - 1) >> 5;
+    const int chunks = static_cast<int>((t1 - t0 + E - 1) / E);
+    for (int ch = tid; ch < chunks; ch += LG_THREADS) {
+        const int l0 = ch * E;
+        const long long t = t0 + l0;
+        const unsigned hit = touched[l0 >> 5] >> (l0 & 31);
+        if (t >= 0 && t + E <= p.vocab) {
+            Chunk<T> in = *reinterpret_cast<const Chunk<T> *>(x + t);
+            unsigned allow = 0xFFFFFFFFu;
+            if (mask) {
+                const long long w = t >> 5;
+                const unsigned w0 = __ldg(mask + w);
+                const unsigned w1 = w < mask_last ? __ldg(mask + w + 1) : 0u;
+                allow = __funnelshift_r(w0, w1, static_cast<unsigned>(t) & 31u);
+            }
+            float f[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[e] = lg_to_f(in.e[e]);
+            if (hit & ((1u << E) - 1)) {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (hit >> e & 1) f[e] = rule(f[e], l0 + e);
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (!(allow >> e & 1)) f[e] = NEG;
+                if (f[e] > best) {
+                    best = f[e];
+                    best_t = t + e;
+                }
+            }
+            if (out) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) lg_from_f(in.e[e], f[e]);
+                if (out_vec) {
+                    *reinterpret_cast<Chunk<T> *>(out + t) = in;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) out[t + e] = in.e[e];
+                }
+            }
+        } else {
+            for (int e = 0; e < E; ++e) {
+                const long long te = t + e;
+                if (te < 0 || te >= p.vocab) continue;
+                float f = lg_to_f(x[te]);
+                if (hit >> e & 1) f = rule(f, l0 + e);
+                if (mask && !(__ldg(mask + (te >> 5)) >> (te & 31) & 1)) f = NEG;
+                if (f > best) {
+                    best = f;
+                    best_t = te;
+                }
+                if (out) lg_from_f(out[te], f);
+            }
+        }
+    }
+    if (!p.idx) return;
+
+    // The best of the block, then of the row: a key orders by value, then by
+    // the lower token; 0 stands for none.  Maxima do not depend on the order.
+    unsigned long long key = 0;
+    if (best > NEG)
+        key = static_cast<unsigned long long>(ordered(best + 0.0f)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(best_t));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, key, d);
+        key = o > key ? o : key;
+    }
+    if ((tid & 31) == 0) s_best[tid >> 5] = key;
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll
+        for (int w = 1; w < LG_THREADS / 32; ++w) key = s_best[w] > key ? s_best[w] : key;
+        if (gridDim.x > 1) {
+            if (key) atomicMax(&p.keys[r], key);
+            __threadfence();
+            if (atomicAdd(&p.cnt[r], 1u) + 1 < gridDim.x) return;
+            __threadfence();
+            key = atomicExch(&p.keys[r], 0ull);  // the last block: both words are zero again
+            p.cnt[r] = 0;
+        }
+        p.idx[r] = key ? static_cast<long long>(0xFFFFFFFFu - static_cast<unsigned>(key)) : -1;
+        p.val[r] = key ? from_ordered(static_cast<unsigned>(key >> 32)) : NEG;
+    }
+}
+
+template <typename T>
+cudaError_t launch_t(LogitsParams &p, int rows, int sms, cudaStream_t st)
+{
+    // Slices: about two blocks per multiprocessor in all, within the bounds
+    // above.  A row that does not start on 16 bytes has one chunk more.
+    const long long span = p.vocab + 16 / sizeof(T) - 1;
+    long long want = (2ll * sms + rows - 1) / rows;
+    long long slice = (span + want - 1) / want;
+    slice = (slice + 31) / 32 * 32;
+    slice = slice < LG_SLICE_MIN ? LG_SLICE_MIN : slice > LG_SLICE_MAX ? LG_SLICE_MAX : slice;
+    p.slice = static_cast<int>(slice);
+    const size_t smem = 4 * slice + slice / 8;
+    const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               4 * LG_SLICE_MAX + LG_SLICE_MAX / 8);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(logits_kernel<T>, dim3(static_cast<unsigned>((span + slice - 1) / slice), rows), LG_THREADS, smem,
+                      st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_logits(LogitsParams &p, qgemv_dtype type, int rows, int sms, cudaStream_t st)
+{
+    switch (type) {
+    case QGEMV_F32: return launch_t<float>(p, rows, sms, st);
+    case QGEMV_F16: return launch_t<__half>(p, rows, sms, st);
+    default: return launch_t<__nv_bfloat16>(p, rows, sms, st);
+    }
+}
+
+}  // namespace qg

@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "../../include/qgemv.h"
+#include "decode_ops.h"
 #include "gemv_kernel.cuh"
 #include "qgemv_launch.h"
 
@@ -484,6 +485,20 @@ qgemv_status run_single(const void *W, qgemv_wlayout layout, const void *xq, flo
 }  // namespace
 
 // =====================================================================
+namespace qg {
+
+qgemv_status device_props(int *sms, unsigned **status)
+{
+    DevInfo d;
+    const qgemv_status s = device_info(d);
+    if (s != QGEMV_OK) return s;
+    *sms = d.sms;
+    *status = d.status;
+    return QGEMV_OK;
+}
+
+}  // namespace qg
+
 extern "C" {
 
 const char *qgemv_status_string(qgemv_status s)

@@ -1,0 +1,312 @@
+// rope_kv.cu -- rotary positions on q and k with the write into the paged
+// cache (minfer README "How it works": RoPE between the QKV product and the
+// attention).
+//
+// A pair (x, y) at position p with frequency theta becomes
+// (x c - y s, x s + y c), c = mscale cos(p theta), s = mscale sin(p theta).
+// In fp32 the product p theta alone would be off by up to p theta 2^-24
+// radians (4e-3 at position 131072), so the angle is formed in integers: the
+// plan holds theta / (2 pi) in units of 2^-64 turns, and the low 64 bits of
+// p * turns are the fraction of a turn, exact but for the frequency's own
+// rounding (p 2^-65 turns).  Its top 32 bits as a signed number of half
+// turns / 2^31 go to sincospif: the angle is off by less than 1e-6 radians
+// at every 32-bit position.
+//
+// What bounds it: memory for prompts (each element is read and written once,
+// 3 flops per element), launch and load latency for a few tokens.  A block
+// takes one token; a thread keeps one place within the head (four pairs: one
+// or two 16-byte loads) and walks the heads, so that its sines are formed
+// once and its loads of several heads are in flight together.  Few tokens
+// instead spread the heads over blocks, one head a thread: more blocks, the
+// sines repeated.
+#include "decode_ops.h"
+#include "qgemv_internal.cuh"
+
+namespace qg {
+namespace {
+
+constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_UNROLL = 4;  // heads in flight per thread
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f<float>(float v)
+{
+    return v;
+}
+template <>
+__device__ __forceinline__ float to_f<__half>(__half v)
+{
+    return __half2float(v);
+}
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v)
+{
+    return __bfloat162float(v);
+}
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v)
+{
+    return v;
+}
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v)
+{
+    return __float2half_rn(v);
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v)
+{
+    return __float2bfloat16_rn(v);
+}
+
+// Four consecutive elements (8 or 16 bytes, aligned to their size).
+template <typename T>
+struct alignas(4 * sizeof(T)) Four {
+    T e[4];
+};
+
+// cos and sin of position * theta, by the turns' fraction.
+__device__ __forceinline__ void angle(int pos, unsigned long long turns, float mscale, float &c, float &s)
+{
+    const unsigned long long frac = static_cast<unsigned long long>(static_cast<long long>(pos)) * turns;
+    const int half_turns = static_cast<int>(static_cast<unsigned>(frac >> 32));
+    float sn, cs;
+    sincospif(static_cast<float>(half_turns) * 4.656612873077393e-10f, &sn, &cs);  // * 2^-31
+    c = cs * mscale;
+    s = sn * mscale;
+}
+
+// Where head h of token t comes from and goes to.
+template <typename TI, typename TQ, typename TC>
+struct HeadRef {
+    const TI *src;
+    TQ *dq;   // q heads
+    TC *dc;   // k and v heads (nullptr: no row)
+    bool rotate;
+    bool live;
+};
+
+template <typename TI, typename TQ, typename TC>
+__device__ __forceinline__ HeadRef<TI, TQ, TC> head_ref(const RopeParams &p, long long t, int h, long long row_off)
+{
+    HeadRef<TI, TQ, TC> r;
+    r.dq = nullptr;
+    r.dc = nullptr;
+    r.rotate = true;
+    if (h < p.hq) {
+        r.src = static_cast<const TI *>(p.q) + t * p.q_stride + static_cast<long long>(h) * p.d;
+        r.dq = static_cast<TQ *>(p.q_out) + t * p.q_out_stride + static_cast<long long>(h) * p.d;
+        r.live = true;
+    } else if (h < p.hq + p.hkv) {
+        const int g = h - p.hq;
+        r.src = static_cast<const TI *>(p.k) + t * p.k_stride + static_cast<long long>(g) * p.d;
+        r.live = row_off >= 0;
+        if (r.live) r.dc = static_cast<TC *>(p.ck) + row_off + g * p.head_stride;
+    } else {
+        const int g = h - p.hq - p.hkv;
+        r.src = static_cast<const TI *>(p.v) + t * p.v_stride + static_cast<long long>(g) * p.d;
+        r.live = row_off >= 0 && g < p.hkv;
+        r.rotate = false;
+        if (r.live) r.dc = static_cast<TC *>(p.cv) + row_off + g * p.head_stride;
+    }
+    return r;
+}
+
+// The token's cache row in elements from the cache's base, -1 for none.
+__device__ __forceinline__ long long cache_row(const RopeParams &p, long long t)
+{
+    if (p.hkv == 0) return -1;
+    const int slot = __ldg(p.slots + t);
+    if (slot < 0 || slot >= p.n_slots) {
+        if (slot != -1 && threadIdx.x == 0) atomicCAS(p.status, 0u, ST_BAD_ID);
+        return -1;
+    }
+    return static_cast<long long>(slot >> p.page_shift) * p.page_stride +
+           static_cast<long long>(slot & ((1 << p.page_shift) - 1)) * p.row_stride;
+}
+
+// Eight elements of a head a thread: unit j < rot / 8 is four pairs (HALF:
+// elements 4j.. and rot/2 + 4j..; interleaved: 8j..), later units are copied.
+template <typename TI, typename TQ, typename TC, bool HALF>
+__global__ void __launch_bounds__(ROPE_THREADS) rope_vec_kernel(const __grid_constant__ RopeParams p)
+{
+    pdl_launch_dependents();
+    const int units = p.d >> 3;
+    const int j = static_cast<int>(threadIdx.x) % units, hb = static_cast<int>(threadIdx.x) / units;
+    const long long t = blockIdx.x;
+    const int heads = p.hq + 2 * p.hkv;
+    const bool rot_unit = 8 * j < p.rot;
+    const int a = HALF && rot_unit ? 4 * j : 8 * j;                  // first four elements
+    const int b = HALF && rot_unit ? p.rot / 2 + 4 * j : 8 * j + 4;  // second four
+    pdl_wait();
+    const long long row_off = cache_row(p, t);
+    float c[4], s[4];
+    bool have = false;
+    const int step = p.heads_per_block * static_cast<int>(gridDim.y);
+    for (int h0 = hb + p.heads_per_block * static_cast<int>(blockIdx.y); h0 < heads; h0 += ROPE_UNROLL * step) {
+        HeadRef<TI, TQ, TC> r[ROPE_UNROLL];
+        Four<TI> x[ROPE_UNROLL], y[ROPE_UNROLL];
+#pragma unroll
+        for (int u = 0; u < ROPE_UNROLL; ++u) {
+            const int h = h0 + u * step;
+            r[u].live = false;
+            if (h < heads) {
+                r[u] = head_ref<TI, TQ, TC>(p, t, h, row_off);
+                if (r[u].live) {
+                    x[u] = *reinterpret_cast<const Four<TI> *>(r[u].src + a);
+                    y[u] = *reinterpret_cast<const Four<TI> *>(r[u].src + b);
+                }
+            }
+        }
+        if (!have && rot_unit) {
+            const int pos = __ldg(p.pos + t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) angle(pos, p.turns[4 * j + i], p.mscale, c[i], s[i]);
+            have = true;
+        }
+#pragma unroll
+        for (int u = 0; u < ROPE_UNROLL; ++u) {
+            if (!r[u].live) continue;
+            float fx[4], fy[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                fx[i] = to_f(x[u].e[i]);
+                fy[i] = to_f(y[u].e[i]);
+            }
+            if (r[u].rotate && rot_unit) {
+                if constexpr (HALF) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float px = fx[i], py = fy[i];
+                        fx[i] = px * c[i] - py * s[i];
+                        fy[i] = px * s[i] + py * c[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float px = fx[2 * i], py = fx[2 * i + 1];
+                        fx[2 * i] = px * c[i] - py * s[i];
+                        fx[2 * i + 1] = px * s[i] + py * c[i];
+                        const float qx = fy[2 * i], qy = fy[2 * i + 1];
+                        fy[2 * i] = qx * c[i + 2] - qy * s[i + 2];
+                        fy[2 * i + 1] = qx * s[i + 2] + qy * c[i + 2];
+                    }
+                }
+            }
+            if (r[u].dq) {
+                Four<TQ> ox, oy;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    ox.e[i] = from_f<TQ>(fx[i]);
+                    oy.e[i] = from_f<TQ>(fy[i]);
+                }
+                *reinterpret_cast<Four<TQ> *>(r[u].dq + a) = ox;
+                *reinterpret_cast<Four<TQ> *>(r[u].dq + b) = oy;
+            } else {
+                Four<TC> ox, oy;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    ox.e[i] = from_f<TC>(fx[i]);
+                    oy.e[i] = from_f<TC>(fy[i]);
+                }
+                *reinterpret_cast<Four<TC> *>(r[u].dc + a) = ox;
+                *reinterpret_cast<Four<TC> *>(r[u].dc + b) = oy;
+            }
+        }
+    }
+}
+
+// One pair of a head a thread, any alignment and even sizes.
+template <typename TI, typename TQ, typename TC, bool HALF>
+__global__ void __launch_bounds__(ROPE_THREADS) rope_any_kernel(const __grid_constant__ RopeParams p)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long t = blockIdx.x;
+    const int heads = p.hq + 2 * p.hkv, pairs = p.d >> 1, rpairs = p.rot >> 1;
+    const long long row_off = cache_row(p, t);
+    const int pos = __ldg(p.pos + t);
+    const int first = static_cast<int>(blockIdx.y * ROPE_THREADS + threadIdx.x);
+    for (int i = first; i < heads * pairs; i += ROPE_THREADS * static_cast<int>(gridDim.y)) {
+        const int h = i / pairs, j = i - h * pairs;
+        const HeadRef<TI, TQ, TC> r = head_ref<TI, TQ, TC>(p, t, h, row_off);
+        if (!r.live) continue;
+        const bool rot_pair = j < rpairs;
+        const int a = HALF && rot_pair ? j : 2 * j, b = HALF && rot_pair ? rpairs + j : 2 * j + 1;
+        float x = to_f(r.src[a]), y = to_f(r.src[b]);
+        if (r.rotate && rot_pair) {
+            float c, s;
+            angle(pos, p.turns[j], p.mscale, c, s);
+            const float px = x, py = y;
+            x = px * c - py * s;
+            y = px * s + py * c;
+        }
+        if (r.dq) {
+            r.dq[a] = from_f<TQ>(x);
+            r.dq[b] = from_f<TQ>(y);
+        } else {
+            r.dc[a] = from_f<TC>(x);
+            r.dc[b] = from_f<TC>(y);
+        }
+    }
+}
+
+template <typename TI, typename TQ, typename TC, bool HALF>
+cudaError_t launch4(RopeParams &p, bool vec, long long n, int sms, cudaStream_t st)
+{
+    const int heads = p.hq + 2 * p.hkv;
+    const unsigned nx = static_cast<unsigned>(n);
+    if (vec) {
+        const int units = p.d / 8;
+        p.heads_per_block = ROPE_THREADS / units;
+        const int chunks = (heads + p.heads_per_block - 1) / p.heads_per_block;
+        // blocks that share a token repeat its sines; they pay while the tokens alone leave multiprocessors idle
+        const unsigned ny = static_cast<unsigned>(n * chunks <= 2ll * sms ? chunks : 1);
+        return launch_pdl(rope_vec_kernel<TI, TQ, TC, HALF>, dim3(nx, ny), p.heads_per_block * units, 0, st, p);
+    }
+    const int chunks = (heads * (p.d / 2) + ROPE_THREADS - 1) / ROPE_THREADS;
+    const unsigned ny = static_cast<unsigned>(n * chunks <= 2ll * sms ? chunks : 1);
+    return launch_pdl(rope_any_kernel<TI, TQ, TC, HALF>, dim3(nx, ny), ROPE_THREADS, 0, st, p);
+}
+
+template <typename TI, typename TQ, typename TC>
+cudaError_t launch3(RopeParams &p, bool half, bool vec, long long n, int sms, cudaStream_t st)
+{
+    return half ? launch4<TI, TQ, TC, true>(p, vec, n, sms, st) : launch4<TI, TQ, TC, false>(p, vec, n, sms, st);
+}
+
+template <typename TI, typename TQ>
+cudaError_t launch2(RopeParams &p, qgemv_dtype cache, bool half, bool vec, long long n, int sms, cudaStream_t st)
+{
+    return cache == QGEMV_F16 ? launch3<TI, TQ, __half>(p, half, vec, n, sms, st)
+                              : launch3<TI, TQ, __nv_bfloat16>(p, half, vec, n, sms, st);
+}
+
+template <typename TI>
+cudaError_t launch1(RopeParams &p, qgemv_dtype qo, qgemv_dtype cache, bool half, bool vec, long long n, int sms,
+                    cudaStream_t st)
+{
+    switch (qo) {
+    case QGEMV_F32: return launch2<TI, float>(p, cache, half, vec, n, sms, st);
+    case QGEMV_F16: return launch2<TI, __half>(p, cache, half, vec, n, sms, st);
+    default: return launch2<TI, __nv_bfloat16>(p, cache, half, vec, n, sms, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(RopeParams &p, qgemv_dtype in, qgemv_dtype q_out, qgemv_dtype cache, bool half_layout, bool vec,
+                        long long n_tokens, int sms, cudaStream_t st)
+{
+    switch (in) {
+    case QGEMV_F32: return launch1<float>(p, q_out, cache, half_layout, vec, n_tokens, sms, st);
+    case QGEMV_F16: return launch1<__half>(p, q_out, cache, half_layout, vec, n_tokens, sms, st);
+    default: return launch1<__nv_bfloat16>(p, q_out, cache, half_layout, vec, n_tokens, sms, st);
+    }
+}
+
+}  // namespace qg

@@ -1,0 +1,199 @@
+"""The argument checks of the operators between the GEMVs: a refused call
+returns its status before any CUDA call, so these run without a GPU.  Pointers
+are numbers that nothing follows."""
+import ctypes
+
+import pytest
+
+import quantized_q4_weight_gb300 as q
+
+OK, INVALID, MISALIGNED, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3, 4
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def L():
+    from quantized_q4_weight_gb300 import _build
+    _build.build()
+    return q.lib()
+
+
+def cache(**kw):
+    f = dict(k=BIG, v=2 * BIG, type=q.BF16, n_pages=100, page_size=16, n_heads=2, head_dim=128, page_stride=4096,
+             row_stride=256, head_stride=128)
+    f.update(kw)
+    return q.KvCacheStruct(**f)
+
+
+BAD_CACHES = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(type=q.F32), INVALID), (dict(type=9), INVALID),
+              (dict(n_pages=0), INVALID), (dict(page_size=0), INVALID), (dict(page_size=24), INVALID),
+              (dict(n_heads=0), INVALID), (dict(head_dim=12), INVALID), (dict(head_dim=264), INVALID),
+              (dict(head_dim=0), INVALID), (dict(page_stride=-8), INVALID), (dict(row_stride=1 << 62), INVALID),
+              (dict(k=BIG + 8), MISALIGNED), (dict(row_stride=260), MISALIGNED), (dict(head_stride=129), MISALIGNED)]
+
+
+def test_rope_init(L):
+    def init(**kw):
+        f = dict(rot_dim=128, layout=0, scaling=0, base=1e4, factor=2.0, orig_len=4096.0, low=1.0, high=4.0, mscale=0.0)
+        f.update(kw)
+        plan = q.RopePlan()
+        return L.qgemv_rope_init(ctypes.byref(q.RopeConfig(**f)), ctypes.byref(plan)), plan
+
+    nan, inf = float("nan"), float("inf")
+    for bad in (dict(rot_dim=0), dict(rot_dim=7), dict(rot_dim=258), dict(layout=2), dict(scaling=4), dict(scaling=-1),
+                dict(base=1.0), dict(base=nan), dict(base=inf), dict(mscale=nan), dict(scaling=1, factor=0.5),
+                dict(scaling=1, factor=inf), dict(scaling=2, orig_len=0.0), dict(scaling=2, low=4.0),
+                dict(scaling=3, low=0.0), dict(scaling=3, high=inf), dict(scaling=3, orig_len=nan)):
+        assert init(**bad)[0] == INVALID, bad
+    assert L.qgemv_rope_init(None, ctypes.byref(q.RopePlan())) == INVALID
+    s, p = init()
+    assert s == OK and p.mscale == 1.0 and p.rot_dim == 128
+    # the frequencies in whole units of 2^-64 turns, to the 53 bits of a double
+    import math
+    for i in range(64):
+        want = 1e4 ** (-2 * i / 128) / (2 * math.pi) * 2 ** 64
+        assert abs(p.turns[i] - want) <= 2.0 ** -50 * want + 0.5
+    assert all(p.turns[i] == 0 for i in range(64, 128))
+    assert abs(init(scaling=3, factor=4.0, high=32.0)[1].mscale - (0.1 * math.log(4) + 1)) < 1e-6
+    assert init(scaling=3, factor=4.0, high=32.0, mscale=1.5)[1].mscale == 1.5
+    lin, plain = init(scaling=1, factor=4.0)[1], init()[1]
+    assert all(abs(lin.turns[i] * 4 - plain.turns[i]) <= 2.0 ** -50 * plain.turns[i] + 4 for i in range(64))
+    # the ramps' ends: short wavelengths keep their frequency, long ones are divided
+    for sc, hi in ((2, 4.0), (3, 32.0)):
+        p = init(scaling=sc, factor=8.0, high=hi)[1]
+        assert p.turns[0] == plain.turns[0] and abs(p.turns[63] * 8 - plain.turns[63]) <= 2.0 ** -50 * plain.turns[63] + 8
+        assert all(p.turns[i] >= p.turns[i + 1] for i in range(63))
+
+
+def rope(L, c=None, **kw):
+    plan = q.rope_plan(kw.pop("rot", 128), 1e4)
+    f = dict(plan=plan.address, q=4096, k=BIG // 2, v=BIG // 2 + (1 << 30), t=q.F32, qs=1536, ks=256, vs=256, pos=1 << 34,
+             slots=1 << 35, n=10, hq=12, d=128, o=1 << 36, ot=q.BF16, os=1536)
+    f.update(kw)
+    c = cache() if c is None else c
+    return L.qgemv_rope_kv(f["plan"], f["q"], f["k"], f["v"], f["t"], f["qs"], f["ks"], f["vs"], f["pos"], f["slots"],
+                           f["n"], f["hq"], f["d"], f["o"], f["ot"], f["os"], ctypes.addressof(c) if c else None, None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(plan=None), INVALID), (dict(q=None, k=None, v=None), INVALID), (dict(v=None), INVALID),
+    (dict(k=None), INVALID), (dict(pos=None), INVALID), (dict(slots=None), INVALID), (dict(t=3), INVALID),
+    (dict(ot=-1), INVALID), (dict(o=None), INVALID), (dict(n=0), INVALID), (dict(n=1 << 32), INVALID),
+    (dict(hq=0), INVALID), (dict(d=127), INVALID), (dict(d=64), INVALID), (dict(rot=256), INVALID),
+    (dict(qs=1535), INVALID), (dict(os=100), INVALID), (dict(qs=-1536), INVALID), (dict(ks=1 << 60), INVALID),
+    (dict(q=4098), MISALIGNED), (dict(o=(1 << 36) + 1), MISALIGNED), (dict(k=BIG // 2 + 2), MISALIGNED),
+    (dict(pos=(1 << 34) + 2), MISALIGNED), (dict(slots=(1 << 35) + 1), MISALIGNED),
+    (dict(o=4096, ot=q.BF16), INVALID),                 # over q with another type
+    (dict(o=4096 + 4, ot=q.F32), INVALID),              # shifted over q
+    (dict(o=BIG), INVALID), (dict(q=2 * BIG), INVALID), (dict(k=BIG), INVALID),      # over the cache
+    (dict(o=BIG // 2), INVALID), (dict(o=1 << 34), INVALID), (dict(o=1 << 35), INVALID)])
+def test_rope_refusals(L, bad, status):
+    assert rope(L, **bad) == status
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHES + [(dict(n_pages=1 << 28, page_size=16, page_stride=0), INVALID)])
+def test_rope_refuses_caches(L, bad, status):
+    assert rope(L, cache(**bad)) == status
+
+
+def attn(L, c=None, b=None, ws_bytes=BIG // 4, **kw):
+    f = dict(q=1 << 30, qt=1536, qh=128, o=1 << 31, ot=q.BF16, os=1536, oh=128, lse=1 << 32, ws=1 << 38)
+    f.update(kw)
+    c = cache() if c is None else c
+    b = batch() if b is None else b
+    return L.qgemv_attn_prefix(f["q"], f["qt"], f["qh"], ctypes.addressof(c), ctypes.addressof(b), f["o"], f["ot"],
+                               f["os"], f["oh"], f["lse"], f["ws"], ws_bytes, None)
+
+
+def batch(**kw):
+    f = dict(n_seqs=4, n_q=2, n_q_heads=12, prefix_len=100, prefix_pages=4096, suffix_len=8192, suffix_pages=1 << 16,
+             suffix_pages_stride=10, max_suffix=150, scale=0.0)
+    f.update(kw)
+    return q.AttnBatchStruct(**f)
+
+
+def attn_ws(L, b, c):
+    return L.qgemv_attn_workspace_bytes(ctypes.addressof(b), ctypes.addressof(c))
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_attn_refuses_caches(L, bad, status):
+    assert attn(L, c=cache(**bad)) == status
+    assert attn_ws(L, batch(), cache(**bad)) == 0
+
+
+@pytest.mark.parametrize("bad", [dict(n_seqs=0), dict(n_q=0), dict(n_q=9), dict(n_q_heads=0), dict(n_q_heads=13),
+                                 dict(prefix_len=-1), dict(prefix_len=2 ** 31 - 1), dict(max_suffix=-1),
+                                 dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
+                                 dict(n_seqs=1 << 20, n_q=8, n_q_heads=4096)])
+def test_attn_refuses_batches(L, bad):
+    assert attn(L, b=batch(**bad)) == INVALID
+    assert attn_ws(L, batch(**bad), cache()) == 0
+
+
+@pytest.mark.parametrize("bad", [dict(prefix_pages=None), dict(suffix_len=None), dict(suffix_pages=None),
+                                 dict(suffix_pages_stride=-1)])
+def test_attn_refuses_tables(L, bad):
+    assert attn(L, b=batch(**bad)) == INVALID
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(q=None), INVALID), (dict(o=None), INVALID), (dict(ot=q.F16), INVALID), (dict(ot=7), INVALID),
+    (dict(qt=-8), INVALID), (dict(os=1 << 60), INVALID), (dict(q=(1 << 30) + 8), MISALIGNED), (dict(qt=1540), MISALIGNED),
+    (dict(qh=100), MISALIGNED), (dict(o=(1 << 31) + 1), MISALIGNED), (dict(lse=(1 << 32) + 2), MISALIGNED),
+    (dict(ws=None), WORKSPACE), (dict(ws_bytes=20000), WORKSPACE), (dict(ws=(1 << 38) + 8), MISALIGNED),
+    (dict(o=1 << 30), INVALID), (dict(o=1 << 38), INVALID), (dict(o=BIG), INVALID), (dict(lse=1 << 31), INVALID),
+    (dict(lse=1 << 38), INVALID), (dict(ws=1 << 30), INVALID), (dict(o=8192), INVALID)])
+def test_attn_refusals(L, bad, status):
+    assert attn(L, **bad) == status
+
+
+def test_attn_workspace_grows_with_the_batch(L):
+    def need(**kw):
+        return attn_ws(L, batch(**kw), cache())
+    assert need() > 16384
+    assert need(prefix_len=0, max_suffix=0) == 16384 and need(n_seqs=8, prefix_len=100000) > need(prefix_len=100000) / 2
+
+
+def logits(L, ws_bytes=16384, s=None, **kw):
+    f = dict(x=1 << 30, t=q.F32, xs=1000, o=1 << 31, os=1000, idx=1 << 32, val=1 << 33, ws=1 << 38)
+    f.update(kw)
+    s = spec() if s is None else s
+    return L.qgemv_logits_rules(f["x"], f["t"], f["xs"], ctypes.addressof(s), f["o"], f["os"], f["idx"], f["val"],
+                                f["ws"], ws_bytes, None)
+
+
+def spec(**kw):
+    f = dict(rows=3, vocab=1000, history=4096, history_stride=50, history_len=8192, max_history=50, repetition=16384,
+             frequency=16640, presence=16896, bias_ids=20480, bias=24576, bias_stride=4, bias_len=28672, max_bias=4,
+             mask=32768, mask_stride=32)
+    f.update(kw)
+    return q.LogitsSpec(**f)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(rows=0), INVALID), (dict(vocab=0), INVALID), (dict(vocab=1 << 31), INVALID), (dict(history=None), INVALID),
+    (dict(history_len=None), INVALID), (dict(max_history=-1), INVALID), (dict(max_history=1 << 20), INVALID),
+    (dict(history_stride=-1), INVALID), (dict(bias=None), INVALID), (dict(bias_ids=None), INVALID),
+    (dict(bias_len=None), INVALID), (dict(max_bias=4096), INVALID), (dict(mask_stride=31), INVALID),
+    (dict(history=4100), MISALIGNED), (dict(bias_ids=20484), MISALIGNED), (dict(mask=32769), MISALIGNED),
+    (dict(repetition=16385), MISALIGNED), (dict(history_len=8193), MISALIGNED), (dict(bias_len=28673), MISALIGNED),
+    (dict(bias=24577), MISALIGNED), (dict(mask=1 << 31), INVALID), (dict(history=1 << 32), INVALID)])
+def test_logits_refuses_specs(L, bad, status):
+    assert logits(L, s=spec(**bad)) == status
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(x=None), INVALID), (dict(t=5), INVALID), (dict(idx=None), INVALID), (dict(val=None), INVALID),
+    (dict(o=None, idx=None, val=None), INVALID), (dict(xs=999), INVALID), (dict(os=999), INVALID),
+    (dict(x=(1 << 30) + 2), MISALIGNED), (dict(o=(1 << 31) + 1), MISALIGNED), (dict(idx=(1 << 32) + 4), MISALIGNED),
+    (dict(val=(1 << 33) + 2), MISALIGNED), (dict(ws=None), WORKSPACE), (dict(ws_bytes=16383), WORKSPACE),
+    (dict(ws=(1 << 38) + 4), MISALIGNED), (dict(o=(1 << 30) + 4), INVALID), (dict(o=1 << 30, os=1004), INVALID),
+    (dict(val=1 << 32), INVALID), (dict(idx=1 << 31), INVALID), (dict(ws=1 << 30), INVALID)])
+def test_logits_refusals(L, bad, status):
+    assert logits(L, **bad) == status
+
+
+def test_logits_workspace(L):
+    for s, want in ((spec(), 16384), (spec(rows=0), 0)):
+        assert L.qgemv_logits_workspace_bytes(ctypes.addressof(s)) == want

@@ -1,0 +1,284 @@
+"""Attention over a shared prefix and own suffixes (qgemv_attn_prefix)
+against the softmax in 64 bits, sequence by sequence.
+
+Tolerance, from the arithmetic, with u half a unit of the cache's type at 1,
+w the exact weights and A = sum w |v|:
+  - a score is off by at most e = (d + 8) 2^-24 scale sum |q k| (fp32 sums of
+    exact products) and 2^-21 from the base-2 exponential and its argument;
+  - each weight enters the product with v rounded: u relative, and for fp16
+    2^-25 absolute below its normal range, relative to the part's maximum;
+  - sums of n terms in fp32: n 2^-24, here below 2^-12 A even at 10000 keys
+    since partial sums are short (tiles of 64, parts, then parts together).
+So |o - o64| <= (u + 2 (e + 2^-21) + 2^-12) A + n 2^-25 max |v| [fp16] and half a
+unit of the output; lse is off by e + 2^-20 + 2^-12.
+"""
+import math
+
+import pytest
+import torch
+
+import quantized_q4_weight_gb300 as q
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+HALF_UNIT = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from quantized_q4_weight_gb300 import _build
+    _build.build()
+
+
+class Case:
+    def __init__(self, b, nq, hq, hkv, d, prefix, lens, page=16, dtype=torch.bfloat16, seed=0, spread=1.5, poison=True,
+                 heads_first=False, max_suffix=None, q_pad=0, scale=None):
+        g = torch.Generator(device=DEV)
+        g.manual_seed(seed)
+        self.b, self.nq, self.hq, self.hkv, self.d, self.prefix, self.lens, self.page = b, nq, hq, hkv, d, prefix, lens, page
+        self.scale = d ** -0.5 if scale is None else scale
+        top = max(lens) if max_suffix is None else max_suffix
+        per = -(-max(top, 1) // page)
+        pre = -(-prefix // page)
+        pages = pre + b * per + 3
+        shape = (pages, hkv, page, d) if heads_first else (pages, page, hkv, d)
+        kv = [torch.randn(shape, generator=g, device=DEV).to(dtype) for _ in range(2)]
+        if heads_first:
+            kv = [x.transpose(1, 2) for x in kv]
+        self.k, self.v = kv
+        order = torch.randperm(pages, generator=g, device=DEV).to(torch.int32)
+        self.prefix_pages, self.suffix_pages = order[:pre].clone(), order[pre:pre + b * per].view(b, per).clone()
+        self.len_t = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        x = spread * torch.randn((b * nq, hq * d + q_pad), generator=g, device=DEV)
+        self.q = x.to(dtype)[:, :hq * d].unflatten(1, (hq, d))
+        if poison:  # rows that nobody has: the pages' ends and the pages left over
+            used = torch.zeros((pages, page), dtype=torch.bool, device=DEV)
+            for table, n in [(self.prefix_pages, prefix)] + [(self.suffix_pages[i], n) for i, n in enumerate(lens)]:
+                j = torch.arange(n, device=DEV)
+                used[table.long()[j // page], j % page] = True
+            self.k[~used] = float("nan")
+            self.v[~used] = float("inf")
+        self.cache = q.KvCache(self.k, self.v)
+        self.batch = q.AttnBatch(b, nq, hq, self.cache, prefix, self.prefix_pages if pre else None, self.len_t,
+                                 self.suffix_pages, top, scale=scale)
+        self.ws = q.new_workspace(self.batch.workspace_bytes())
+
+    def rows(self, i):
+        """Keys and values of sequence i's context, float64 [rows][hkv][d]."""
+        out = []
+        for x in (self.k, self.v):
+            parts = []
+            for table, n in ((self.prefix_pages, self.prefix), (self.suffix_pages[i], self.lens[i])):
+                j = torch.arange(n, device=DEV)
+                parts.append(x[table.long()[j // self.page], j % self.page] if n else x[:0, 0])
+            out.append(torch.cat(parts).double())
+        return out
+
+    def exact(self):
+        """(o, A, lse, e): float64 outputs, sum w |v|, log of the sum, bound of a score's error."""
+        b, nq, hq, hkv, d = self.b, self.nq, self.hq, self.hkv, self.d
+        o = torch.zeros((b, nq, hq, d), dtype=torch.float64, device=DEV)
+        A, lse, worst = torch.zeros_like(o), torch.full((b, nq, hq), float("-inf"), dtype=torch.float64, device=DEV), 0.0
+        for i in range(b):
+            k, v = self.rows(i)
+            for t in range(nq):
+                n = self.prefix + self.lens[i] - nq + t + 1
+                if n <= 0:
+                    continue
+                for h in range(hq):
+                    x = self.q[i * nq + t, h].double()
+                    kk, vv = k[:n, h // (hq // hkv)], v[:n, h // (hq // hkv)]
+                    s = self.scale * (kk * x).sum(1)
+                    worst = max(worst, float((self.scale * (kk * x).abs().sum(1)).max()))
+                    w = torch.softmax(s, 0)
+                    o[i, t, h] = w @ vv
+                    A[i, t, h] = w @ vv.abs()
+                    lse[i, t, h] = torch.logsumexp(s, 0)
+        return o, A, lse, (d + 8) * 2.0 ** -24 * worst
+
+    def run(self, **kw):
+        return q.attn_prefix(self.q, self.batch, self.ws, **kw)
+
+    def check(self, out_type=None, o=None):
+        lse = torch.full((self.b * self.nq, self.hq), 5.0, device=DEV)
+        out = torch.full(self.q.shape, 3.0, dtype=out_type or self.k.dtype, device=DEV) if o is None else o
+        self.run(out=out, lse=lse)
+        torch.cuda.synchronize()
+        assert q.device_status() == 0
+        ref, A, l64, e = self.exact()
+        u, uo = HALF_UNIT[self.k.dtype], HALF_UNIT[out.dtype]
+        keys = self.prefix + max(self.lens)
+        vmax = 6.0
+        tol = (u + 2 * (e + 2.0 ** -21) + 2.0 ** -12) * A + uo * ref.abs() + 1e-30
+        if self.k.dtype == torch.float16:
+            tol = tol + keys * 2.0 ** -25 * vmax * (A > 0)
+        got = out.double().view(ref.shape)
+        assert bool(torch.isfinite(got).all())
+        assert bool(((got - ref).abs() <= tol).all()), float(((got - ref).abs() - tol).max())
+        gl = lse.double().view(l64.shape)
+        none = torch.isinf(l64)
+        assert bool((gl[none] == float("-inf")).all()) and bool((got[none] == 0).all())
+        assert bool(((gl - l64)[~none].abs() <= e + 2.0 ** -20 + 2.0 ** -12 + 2.0 ** -22 * l64[~none].abs()).all())
+        return out, lse
+
+
+@pytest.mark.parametrize("prefix", [0, 1, 63, 64, 65, 130, 1000])
+@pytest.mark.parametrize("lens", [[0, 1, 2], [64, 63, 65], [200, 0, 37]])
+def test_lengths(prefix, lens):
+    Case(3, 1, 6, 2, 64, prefix, lens, seed=prefix + lens[0]).check()
+
+
+@pytest.mark.parametrize("nq", [1, 2, 3, 5, 8])
+@pytest.mark.parametrize("hq,hkv", [(12, 2), (16, 2), (8, 8), (16, 1), (5, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_and_heads(nq, hq, hkv, d):
+    Case(3, nq, hq, hkv, d, 150, [0, nq, 90], seed=nq * hq + d).check()
+
+
+@pytest.mark.parametrize("d", [8, 24, 40, 64, 72, 96, 128, 136, 192, 256])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_head_sizes(d, dtype):
+    for nq, hq in ((1, 4), (3, 16), (8, 12)):        # 2, 24 and 48 rows a sequence and cache head
+        Case(2, nq, hq, 2, d, 100, [40, 77], dtype=dtype, seed=d + nq).check()
+
+
+@pytest.mark.parametrize("page", [1, 2, 16, 64, 256])
+@pytest.mark.parametrize("heads_first", [False, True])
+def test_pages(page, heads_first):
+    Case(3, 2, 6, 2, 64, 333, [5, 100, 257], page=page, heads_first=heads_first, seed=page).check()
+
+
+@pytest.mark.parametrize("b,nq,hq,hkv,prefix,top", [(1, 1, 2, 2, 5000, 30), (1, 1, 12, 2, 0, 9000), (2, 1, 32, 8, 700, 40),
+                                                    (40, 1, 8, 1, 300, 50), (24, 4, 16, 2, 513, 20),
+                                                    (64, 2, 4, 2, 129, 300)])
+def test_shapes_of_batches(b, nq, hq, hkv, prefix, top):
+    lens = [(i * 7919) % (top + 1) for i in range(b)]
+    lens[0] = top
+    Case(b, nq, hq, hkv, 64, prefix, lens, seed=b).check()
+
+
+def test_tall_row_tiles_over_a_long_prefix():
+    # many rows per cache head: several tiles of rows share the prefix, the last one part full
+    for b, nq, hq, hkv, d, prefix in ((35, 4, 16, 2, 128, 1500), (33, 8, 8, 1, 64, 2049), (70, 1, 32, 8, 128, 777),
+                                      (9, 8, 32, 2, 128, 640)):
+        Case(b, nq, hq, hkv, d, prefix, [nq + i % 5 for i in range(b)], page=64, seed=b).check()
+    Case(40, 4, 8, 2, 96, 1000, [4] * 40, page=32, dtype=torch.float16, seed=5).check()
+
+
+def test_fp32_outputs_strides_and_scale():
+    c = Case(3, 3, 6, 2, 128, 90, [3, 50, 9], dtype=torch.float16, q_pad=64, seed=3)
+    wide = torch.full((9, 6 * 128 + 8), 4.0, device=DEV)
+    o, _ = c.check(o=wide[:, :768].unflatten(1, (6, 128)))
+    assert bool((wide[:, 768:] == 4).all())
+    heads = torch.zeros((6, 9, 128), dtype=torch.float16, device=DEV).transpose(0, 1)   # [tokens][heads] by strides
+    c.check(o=heads)
+    Case(2, 1, 4, 2, 64, 70, [9, 30], scale=0.4, seed=4).check(out_type=torch.float32)
+
+
+def test_sharp_scores_and_a_dominating_key():
+    c = Case(2, 2, 4, 2, 64, 500, [10, 30], spread=12.0, seed=6)
+    c.check()
+    c = Case(2, 1, 4, 2, 64, 500, [10, 30], seed=7)
+    c.k[c.prefix_pages.long()[3], 5] = 30.0 * c.q[0, 0]  # one key far above the others for some rows
+    c.check()
+
+
+def test_no_key_at_all():
+    for lens, nq in (([0, 0], 1), ([0, 2], 5)):
+        c = Case(2, nq, 4, 2, 64, 0, lens, max_suffix=16, seed=8)
+        out, lse = c.check()
+        assert bool((out.view(2, nq, 4, 64)[0] == 0).all()) and bool((lse.view(2, nq, 4)[0] == float("-inf")).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_what_a_query_does_not_see_does_not_reach_it(bad):
+    c = Case(2, 4, 6, 2, 64, 70, [30, 66], seed=9)
+    clean = c.run().clone()
+    for i in range(2):       # each sequence's last token: only its last query sees it
+        j = c.lens[i] - 1
+        c.v[c.suffix_pages[i, j // 16].long(), j % 16] = bad
+        c.k[c.suffix_pages[i, j // 16].long(), j % 16] = bad
+    out = c.run()
+    torch.cuda.synchronize()
+    a, b = out.view(2, 4, 6, 64), clean.view(2, 4, 6, 64)
+    assert torch.equal(a[:, :3], b[:, :3])
+    assert not bool(torch.isfinite(a[:, 3]).all())
+
+
+def test_the_same_bits_again_and_with_other_sequences_beside():
+    c = Case(5, 2, 8, 2, 64, 2000, [600, 3, 0, 64, 250], seed=10)
+    first = c.run().clone()
+    for _ in range(5):
+        assert torch.equal(c.run(), first)
+
+
+def test_lengths_and_tables_change_in_place():
+    """A decode loop counts its device lengths up and calls again."""
+    c = Case(2, 1, 6, 2, 64, 40, [60, 64], max_suffix=100, poison=False, seed=11)
+    for lens in ([1, 30], [100, 0], [65, 99]):
+        c.len_t.copy_(torch.tensor(lens, dtype=torch.int32))
+        c.lens = lens
+        c.check()
+
+
+def test_pages_and_lengths_outside_are_recorded_and_unseen():
+    c = Case(2, 1, 4, 2, 64, 64, [40, 20], page=16, seed=12)
+    keep = c.prefix_pages.clone()
+    for bad in (-1, c.cache.struct.n_pages, 2 ** 31 - 1):
+        c.prefix_pages.copy_(keep)
+        c.prefix_pages[3] = bad
+        out = c.run()
+        assert q.device_status() == 7
+        # as if the prefix ended before its last page
+        c.prefix_pages.copy_(keep)
+        short = q.AttnBatch(2, 1, 4, c.cache, 48, c.prefix_pages, c.len_t, c.suffix_pages, 40)
+        want = q.attn_prefix(c.q, short, c.ws)
+        assert q.device_status() == 0
+        assert float((out.float() - want.float()).abs().max()) <= 2.0 ** -7 * float(want.float().abs().max())
+    c.len_t[0] = 41          # above max_suffix: counts as 40
+    want = c.exact()[0]
+    out = c.run()
+    assert q.device_status() == 7
+    assert float((out.double().view(want.shape) - want).abs().max()) < 2.0 ** -6
+    c.len_t[0] = -3          # counts as 0
+    out = c.run()
+    assert q.device_status() == 7
+    c.len_t[0], c.lens = 0, [0, 20]
+    assert torch.equal(out, c.run()) and q.device_status() == 0
+
+
+def test_another_stream_and_two_workspaces():
+    a, b = Case(4, 1, 8, 2, 128, 3000, [50] * 4, seed=13), Case(4, 1, 8, 2, 128, 3000, [70] * 4, seed=14)
+    wa, wb = a.run().clone(), b.run().clone()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    oa, ob = torch.empty_like(wa), torch.empty_like(wb)
+    for _ in range(10):
+        a.run(out=oa, stream=s1)
+        b.run(out=ob, stream=s2)
+    torch.cuda.synchronize()
+    assert torch.equal(oa, wa) and torch.equal(ob, wb)
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^32 elements, its rows at the far end."""
+    page, hkv, d = 256, 8, 128
+    pages = 2 ** 32 // (page * hkv * d) + 40
+    if torch.cuda.mem_get_info()[0] < 4 * pages * page * hkv * d * 2:
+        pytest.skip("needs 40 GB of device memory")
+    k = torch.zeros((pages, page, hkv, d), dtype=torch.float16, device=DEV)
+    v = torch.zeros_like(k)
+    small = Case(2, 2, 16, hkv, d, 500, [300, 77], page=page, dtype=torch.float16, poison=False, seed=15)
+    n = small.k.shape[0]
+    k[-n:], v[-n:] = small.k, small.v
+    cache = q.KvCache(k, v)
+    shift = pages - n
+    batch = q.AttnBatch(2, 2, 16, cache, 500, small.prefix_pages + shift, small.len_t, small.suffix_pages + shift, 300)
+    got = q.attn_prefix(small.q, batch, small.ws)
+    assert torch.equal(got, small.run()) and q.device_status() == 0
+    # and the cache write there
+    plan = q.rope_plan(d, 1e4)
+    x = torch.randn((3, hkv, d), device=DEV)
+    slots = torch.tensor([pages * page - 1, 5, (pages - 1) * page], dtype=torch.int32, device=DEV)
+    q.rope_kv(plan, None, x, x, torch.zeros(3, dtype=torch.int32, device=DEV), slots, cache)
+    assert torch.equal(v.view(-1, hkv, d)[slots.long()], x.half()) and q.device_status() == 0
