@@ -638,8 +638,9 @@ qgemv_status qgemv_rope_kv(const qgemv_rope_plan *plan, const void *q, const voi
  * page suffix_pages[b * suffix_pages_stride + j / page_size] (all int32,
  * device; entries past a length are not read).  So a page belongs to the
  * prefix or to one suffix, and both may end inside a page.
- * Each sequence has n_q queries (1..8), the last n_q tokens of its context:
- * query i sees the prefix and its suffix rows j <= suffix_len[b] - n_q + i.
+ * Each sequence has n_q queries (1..8), the last n_q tokens of its suffix:
+ * query i sees the whole prefix and its suffix rows
+ * j <= suffix_len[b] - n_q + i (none where that is negative).
  * A length outside [0, max_suffix] counts as the nearer end and a page
  * outside the cache as absent (its rows are not seen); both record
  * QGEMV_ERR_BAD_ID.  n_q_heads is a multiple of the cache's n_heads; query

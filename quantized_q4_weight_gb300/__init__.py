@@ -2,6 +2,9 @@
 Q8_0-activation decode GEMV on one GB300.
 
 Argument marshalling only: every step runs in the library's CUDA kernels.
+Most calls go through ctypes; those of the decode step between its GEMVs
+(rope_kv, attn_prefix, logits_rules) through the compiled _binding.so,
+because their kernels are shorter than the marshalling.
 Tensors supply device pointers; work is enqueued on the current torch CUDA
 stream.  The library is loaded from this directory (libqgemv.so, built by
 ``quantized_q4_weight_gb300._build.build()``); if it is missing, every call
@@ -184,21 +187,40 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_ext = None
+
+
+def _load_binding():
+    """The compiled binding (raises if it has not been built)."""
+    global _ext
+    if _ext is None:
+        lib()
+        if not os.path.exists(_build.BINDING):
+            raise RuntimeError(f"the binding is not built ({_build.BINDING} missing): run "
+                               "quantized_q4_weight_gb300._build.build() first")
+        from . import _binding as ext
+        _ext = ext
+    return _ext
+
+
 def _check(code: int, what: str):
     if code != 0:
         raise QgemvError(code, what)
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    """A stream's handle; by default the current stream's (read as a number:
+    building a Stream object takes longer than a small kernel)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t):
     if t is None:
         return None
     assert t.is_cuda and t.is_contiguous(), "tensors must be contiguous CUDA tensors"
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 # ----------------------------------------------------------------- sizes
@@ -513,18 +535,11 @@ class KvCache:
         self.address = ctypes.addressof(self.struct)
 
 
-def _heads(x, what: str):
-    """A [tokens][heads][head_dim] tensor whose heads are contiguous and adjacent."""
-    if not x.is_cuda or x.dim() != 3 or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
-        raise ValueError(f"{what}: a CUDA tensor [tokens][heads][head_dim] with adjacent heads")
-    return x.data_ptr(), x.stride(0)
-
-
-def _i32(x, what: str, n: int | None = None):
+def _i32(x, what: str, n: int):
     if x is None:
         return None
-    if not x.is_cuda or x.dtype != torch.int32 or not x.is_contiguous() or (n is not None and x.numel() < n):
-        raise ValueError(f"{what}: a contiguous int32 CUDA tensor" + (f" of {n}" if n is not None else ""))
+    if x.dtype is not torch.int32 or not x.is_cuda or not x.is_contiguous() or x.numel() < n:
+        raise ValueError(f"{what}: a contiguous int32 CUDA tensor of {n}")
     return x.data_ptr()
 
 
@@ -532,29 +547,11 @@ def rope_kv(plan: RopePlan, xq, xk, xv, pos, slots=None, cache: KvCache | None =
     """Rotate q [tokens][heads][head_dim] into `out` (default: a new tensor of the
     cache's type, or of q's without a cache) and k, v [tokens][kv heads][head_dim] into
     the cache rows `slots` (-1: none).  xq, or xk and xv, may be None.  Returns out."""
-    some = xq if xq is not None else xk
-    n, d = some.shape[0], some.shape[2]
-    qp = qs = kp = ks = vp = vs = op = os_ = 0
-    hq = 0
-    if xk is not None:
-        kp, ks = _heads(xk, "rope_kv: k")
-        vp, vs = _heads(xv, "rope_kv: v")
-        if xv.shape != xk.shape or xv.dtype != xk.dtype or xk.dtype != some.dtype or xk.shape[0] != n or \
-                xk.shape[2] != d or xk.shape[1] != cache.struct.n_heads:
-            raise ValueError("rope_kv: k and v of q's type and tokens, with the cache's heads")
-    if xq is not None:
-        qp, qs = _heads(xq, "rope_kv: q")
-        hq = xq.shape[1]
-        if out is None:
-            out = torch.empty((n, hq, d), dtype=cache.k.dtype if cache is not None else xq.dtype, device=xq.device)
-        op, os_ = _heads(out, "rope_kv: out")
-        if out.shape != xq.shape:
-            raise ValueError("rope_kv: out has q's shape")
-    _check(lib().qgemv_rope_kv(plan.address, qp, kp, vp, _DTYPES[some.dtype], qs, ks, vs, _i32(pos, "rope_kv: pos", n),
-                               _i32(slots, "rope_kv: slots", n), n, hq, d, op,
-                               _DTYPES[out.dtype] if out is not None else F32, os_,
-                               cache.address if cache is not None else None, _stream(stream)), "qgemv_rope_kv")
-    return out
+    r = (_ext or _load_binding()).rope_kv(plan.address, xq, xk, xv, pos, slots, None if cache is None else cache.address, out,
+                                     None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        _check(r, "qgemv_rope_kv")
+    return r
 
 
 class AttnBatch:
@@ -589,25 +586,11 @@ def attn_prefix(xq, batch: AttnBatch, ws, out=None, lse=None, stream=None):
     """Attention of q [n_seqs][n_q][heads][head_dim] (or [tokens][heads][head_dim]) over the
     batch's contexts; out (the cache's type or fp32, q's shape; default: a new tensor
     of the cache's type); lse fp32 [tokens][heads] or None."""
-    c, b = batch.cache.struct, batch.struct
-    d = c.head_dim
-    if xq.numel() != b.n_seqs * b.n_q * b.n_q_heads * d or xq.shape[-1] != d or xq.shape[-2] != b.n_q_heads or \
-            not xq.is_cuda or xq.dtype != batch.cache.k.dtype:
-        raise ValueError("attn_prefix: q [n_seqs][n_q][heads][head_dim] of the cache's type")
-    if out is None:
-        out = torch.empty(xq.shape, dtype=xq.dtype, device=xq.device)
-    strides = []
-    for x in (xq, out):
-        st = x.stride()
-        if st[-1] != 1 or (x.dim() == 4 and x.shape[0] > 1 and st[0] != x.shape[1] * st[1]) or x.dim() not in (3, 4):
-            raise ValueError("attn_prefix: q and out with contiguous heads and evenly spaced tokens")
-        strides.append((st[-3], st[-2]))
-    if out.shape != xq.shape or not out.is_cuda:
-        raise ValueError("attn_prefix: out has q's shape")
-    _check(lib().qgemv_attn_prefix(xq.data_ptr(), strides[0][0], strides[0][1], batch.cache.address, batch.address,
-                                   out.data_ptr(), _DTYPES[out.dtype], strides[1][0], strides[1][1], _ptr(lse),
-                                   _ptr(ws), ws.numel(), _stream(stream)), "qgemv_attn_prefix")
-    return out
+    r = (_ext or _load_binding()).attn_prefix(xq, batch.cache.address, batch.address, ws, out, lse,
+                                         None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        _check(r, "qgemv_attn_prefix")
+    return r
 
 
 class LogitsRules:
@@ -657,17 +640,11 @@ def logits_rules(x, rules: LogitsRules, ws, out=None, idx=None, val=None, stream
     """Apply the rules to x [rows][vocab] (fp32, f16, bf16); out (None: not
     written; may be x) receives the results in x's type.  Returns each row's best
     token (int64, -1 for none) and its value (fp32)."""
-    if not x.is_cuda or x.dim() != 2 or x.shape != (rules.rows, rules.vocab) or x.stride(1) != 1 or \
-            (out is not None and (out.shape != x.shape or out.dtype != x.dtype or out.stride(1) != 1 or not out.is_cuda)):
-        raise ValueError("logits_rules: x (and out) CUDA tensors [rows][vocab]")
-    idx = idx if idx is not None else torch.empty(rules.rows, dtype=torch.int64, device=x.device)
-    val = val if val is not None else torch.empty(rules.rows, dtype=torch.float32, device=x.device)
-    if idx.numel() != rules.rows or idx.dtype != torch.int64 or val.numel() != rules.rows or val.dtype != torch.float32:
-        raise ValueError("logits_rules: idx int64 and val fp32 of rows")
-    _check(lib().qgemv_logits_rules(x.data_ptr(), _DTYPES[x.dtype], x.stride(0), rules.address,
-                                    out.data_ptr() if out is not None else None, out.stride(0) if out is not None else 0,
-                                    _ptr(idx), _ptr(val), _ptr(ws), ws.numel(), _stream(stream)), "qgemv_logits_rules")
-    return idx, val
+    r = (_ext or _load_binding()).logits_rules(x, rules.address, ws, out, idx, val,
+                                          None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        _check(r, "qgemv_logits_rules")
+    return r
 
 
 def block_isums(W, layout: int, xq, N: int, K: int, T: int, stream=None) -> torch.Tensor:

@@ -1,8 +1,10 @@
-"""Builds libqgemv.so in-tree with nvcc for sm_103a.
+"""Builds libqgemv.so in-tree with nvcc for sm_103a, and the Python binding
+_binding.so with the host compiler.
 
-Each translation unit compiles in its own nvcc process (in parallel), then
-nvcc links them into one shared library with the CUDA runtime linked
-statically.  A build is skipped when the library is newer than every source.
+Each translation unit compiles in its own process (in parallel), then nvcc
+links the CUDA ones into one shared library with the CUDA runtime linked
+statically, and the binding is linked against that library and torch.  A
+build is skipped when both are newer than every source.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqgemv.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -40,14 +45,14 @@ def sources() -> list[str]:
 
 
 def _deps() -> list[str]:
-    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return (sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -56,6 +61,20 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
+
+    def run(cmd, what):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+    def compile_binding() -> str:
+        from torch.utils import cpp_extension as ce
+        obj = os.path.join(BUILD_DIR, "binding.o")
+        inc = [f"-I{d}" for d in [*ce.include_paths(), sysconfig.get_paths()["include"],
+                                  os.path.join(os.path.dirname(os.path.dirname(cc)), "include")]]
+        run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", *inc, "-c", BINDING_SRC, "-o", obj],
+            f"compiling {BINDING_SRC}")
+        return obj
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
@@ -68,14 +87,22 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding_obj = binding.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    from torch.utils import cpp_extension as ce
+    tmp = BINDING + ".tmp"
+    dirs = [f"-L{d}" for d in ce.library_paths()] + [f"-Wl,-rpath,{d}" for d in ce.library_paths()]
+    run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, binding_obj, f"-L{PKG}", "-lqgemv", "-Wl,-rpath,$ORIGIN",
+         *dirs, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], "linking the binding")
+    os.replace(tmp, BINDING)
     return LIB
 
 

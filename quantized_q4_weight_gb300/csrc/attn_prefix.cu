@@ -616,8 +616,9 @@ cudaError_t launch_part(const AttnParams &p, cudaStream_t st)
 {
     const long long blocks = p.p_blocks + static_cast<long long>(p.n_seqs) * p.hkv * p.s_tiles * p.s_splits;
     if (blocks == 0) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(attn_part_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               AttnCfg<DP>::SMEM);
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e =
+        allow_smem(reinterpret_cast<const void *>(attn_part_kernel<T, DP>), AttnCfg<DP>::SMEM, done);
     if (e != cudaSuccess) return e;
     return launch_pdl(attn_part_kernel<T, DP>, dim3(static_cast<unsigned>(blocks)), AT_THREADS, AttnCfg<DP>::SMEM, st, p);
 }

@@ -10,12 +10,28 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/qgemv.h"
 
 namespace qg {
 
 // Multiprocessors and the status word of the current device (qgemv_api.cu).
 qgemv_status device_props(int *sms, unsigned **status);
+
+// Allow a kernel `bytes` of dynamic shared memory, once per device (`done`:
+// one bit per device, a static of the caller's; a second setting is harmless).
+inline cudaError_t allow_smem(const void *kernel, size_t bytes, std::atomic<unsigned long long> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Launch with programmatic dependent launch: the kernel may start while the
 // preceding one drains and touches memory only after its griddepcontrol.wait.

@@ -237,8 +237,9 @@ cudaError_t launch_t(LogitsParams &p, int rows, int sms, cudaStream_t st)
     slice = slice < LG_SLICE_MIN ? LG_SLICE_MIN : slice > LG_SLICE_MAX ? LG_SLICE_MAX : slice;
     p.slice = static_cast<int>(slice);
     const size_t smem = 4 * slice + slice / 8;
-    const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               4 * LG_SLICE_MAX + LG_SLICE_MAX / 8);
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(logits_kernel<T>),
+                                     4 * LG_SLICE_MAX + LG_SLICE_MAX / 8, done);
     if (e != cudaSuccess) return e;
     return launch_pdl(logits_kernel<T>, dim3(static_cast<unsigned>((span + slice - 1) / slice), rows), LG_THREADS, smem,
                       st, p);

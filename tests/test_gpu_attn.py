@@ -82,7 +82,7 @@ class Case:
         for i in range(b):
             k, v = self.rows(i)
             for t in range(nq):
-                n = self.prefix + self.lens[i] - nq + t + 1
+                n = self.prefix + max(0, self.lens[i] - nq + t + 1)
                 if n <= 0:
                     continue
                 for h in range(hq):
@@ -282,3 +282,11 @@ def test_offsets_past_32_bits():
     slots = torch.tensor([pages * page - 1, 5, (pages - 1) * page], dtype=torch.int32, device=DEV)
     q.rope_kv(plan, None, x, x, torch.zeros(3, dtype=torch.int32, device=DEV), slots, cache)
     assert torch.equal(v.view(-1, hkv, d)[slots.long()], x.half()) and q.device_status() == 0
+
+
+def test_four_dimensional_views():
+    for b, nq in ((4, 1), (1, 4), (3, 2)):
+        c = Case(b, nq, 6, 2, 64, 50, [nq + 3] * b, q_pad=256, seed=b)
+        want, _ = c.check()
+        got = q.attn_prefix(c.q.unflatten(0, (b, nq)), c.batch, c.ws)
+        assert torch.equal(got.view(want.shape), want)
