@@ -27,6 +27,8 @@
 // four warps 16 of a tile's keys and merge the warps at the end, so that all
 // warps work and each key is read from shared memory once; taller tiles (64
 // rows) give each warp 16 rows.
+#include <type_traits>
+
 #include "decode_ops.h"
 #include "qgemv_internal.cuh"
 
@@ -479,8 +481,10 @@ __global__ void __launch_bounds__(AT_THREADS, DP == 256 ? 1 : 2) attn_part_kerne
 {
     using C = AttnCfg<DP>;
     extern __shared__ __align__(128) uint8_t smem[];
-    pdl_launch_dependents();
     pdl_wait();
+    // Only now: the prefix kernel on tcgen05, launched next, does not wait
+    // for this one, so it must not start before what this one waited for.
+    pdl_launch_dependents();
     Part w;
     int id = blockIdx.x, tile_rows;
     if (id < p.p_blocks) {  // row tiles innermost: blocks that run together share their keys in L2
@@ -629,6 +633,10 @@ cudaError_t launch_type(const AttnParams &p, qgemv_dtype o_type, cudaStream_t st
     const cudaError_t e = p.d <= 64 ? launch_part<T, 64>(p, st) : p.d <= 128 ? launch_part<T, 128>(p, st)
                                                                              : launch_part<T, 256>(p, st);
     if (e != cudaSuccess) return e;
+    if (p.t_mode) {
+        const cudaError_t t = launch_attn_tc(p, std::is_same<T, __half>::value ? QGEMV_F16 : QGEMV_BF16, st);
+        if (t != cudaSuccess) return t;
+    }
     const dim3 grid(static_cast<unsigned>(p.n_seqs * p.n_q * p.hq));
     return o_type == QGEMV_F32 ? launch_pdl(attn_combine_kernel<T, float>, grid, AT_THREADS, 0, st, p)
                                : launch_pdl(attn_combine_kernel<T, T>, grid, AT_THREADS, 0, st, p);

@@ -1,0 +1,559 @@
+// attn_tc.cu -- the prefix part of the shared-prefix attention on the
+// fifth-generation tensor cores, for batches with many rows per cache head
+// (see attn_prefix.cu for the parts and how they are combined).
+//
+// With R rows per cache head the prefix takes 4 R d operations per key
+// against 4 d bytes read: from a few hundred rows on the matrix products
+// bound it, at a rate that mma.sync reaches a quarter of.
+//
+// A block (one per multiprocessor) takes a range of keys of one cache head
+// and two "streams" of 128 rows, each with its own scores S and weighted sum
+// O in tensor memory (128 columns each):
+//   rows mode: the streams are two row tiles over the same keys;
+//   keys mode (at most 128 rows): one row tile, and the streams take
+//   alternate key tiles and leave two parts.
+// Per stream and tile of 128 keys:
+//   S = Q K^T (tcgen05.mma, both operands from shared memory), read back row
+//   by row: thread i of the stream's four warps owns row i, so maxima and
+//   sums need no shuffles; P = 2^(S scale - m), rounded to the cache's type,
+//   goes over S's own columns (two elements a column); O += P V with P from
+//   tensor memory and V from shared memory.
+// One thread issues the products, alternating between the streams, so that
+// one stream's products run while the other's weights are computed.
+//
+// The reference m of a row is its running maximum, but follows it only when
+// that rises by more than 2^8: O is rescaled (in tensor memory, by the row's
+// own thread) in few tiles instead of all, and the weights stay below 2^8,
+// exact in scale.  l sums the unrounded weights in fp32.
+//
+// K and V tiles share a ring of buffers in the 128-byte-swizzled layout the
+// products read: rows of 64 elements, halves of the head side by side.  K is
+// the K-major operand of S, V the same bytes as the MN-major operand of O.
+// Four producer warps fill the ring with 16-byte cp.async copies, since a
+// page may hold fewer rows than a tile and its rows may have any stride.
+//
+// Registers: the launch has 512 threads of 128; the row threads take 184,
+// the other two warp groups 72 each: 256 * 184 + 256 * 72 = 65536.
+//
+// Every wait is bounded: a block that gives up records QGEMV_ERR_TIMEOUT,
+// waits for its copies and products in flight and frees its tensor memory.
+#include <type_traits>
+
+#include "decode_ops.h"
+#include "qgemv_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace qg {
+namespace {
+
+constexpr int AC_THREADS = 512;   // warps 0-3, 4-7: rows of streams 0, 1; 8-11: producers; 12: products
+constexpr int AC_KEYS = 128;      // keys of a tile
+constexpr int AC_ROWS = 128;      // rows of a stream
+constexpr int AC_MASKS = 8;       // tiles whose presence masks are kept, per stream: the ring holds fewer
+constexpr float AC_RISE = 8.0f;   // rise of the maximum (base 2) that moves the reference
+constexpr float AC_NEG = -1e30f;
+
+template <int DP>
+struct TcCfg {
+    static constexpr int HALF = AC_KEYS * 128;            // 64 elements of 128 rows
+    static constexpr int TILE = HALF * DP / 64;           // a K or V tile; also 128 rows of Q
+    static constexpr int NBUF = DP == 64 ? 8 : 5;
+    static constexpr int LAG = DP == 64 ? 4 : 2;          // buffers in flight behind the one being issued
+    static constexpr int OFF_RING = 2 * TILE;
+    static constexpr int OFF_BAR = OFF_RING + NBUF * TILE;
+    static constexpr int NBAR = 2 * NBUF + 6;
+    static constexpr int OFF_MASK = OFF_BAR + 8 * NBAR;   // [stream][AC_MASKS][4] words
+    static constexpr int SMEM = (OFF_MASK + 2 * AC_MASKS * 16 + 15) / 16 * 16 + 1024;  // aligned up to 1024 at run time
+};
+static_assert(TcCfg<128>::SMEM <= 227 * 1024, "shared memory of the prefix kernel");
+
+// Tensor-memory columns of a stream's scores (weights over them) and sums.
+__device__ __forceinline__ constexpr uint32_t col_s(int s) { return 128u * s; }
+__device__ __forceinline__ constexpr uint32_t col_o(int s) { return 256u + 128u * s; }
+
+// D = A (shared memory) x B (shared memory) [+ D].
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_t, uint64_t adesc, uint64_t bdesc, uint32_t idesc, int accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_t),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of a 128-byte-swizzled operand: groups of 8 rows 1024 bytes
+// apart (stride byte offset); `lead` separates the 64-element halves of an
+// MN-major operand (unused by a K-major one).
+__device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t lead)
+{
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lead >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void tc_ld32(uint32_t taddr, float *d)
+{
+    unsigned r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) d[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_st32(uint32_t taddr, const unsigned *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ac_ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// a * b + c and a + b on pairs (two IEEE operations each).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tadd.rn.f32x2 rd, ra, rb;\n\t"
+        "mov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+template <typename T>
+__device__ __forceinline__ unsigned pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ unsigned pack2<__half>(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const unsigned *>(&h);
+}
+template <>
+__device__ __forceinline__ unsigned pack2<__nv_bfloat16>(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const unsigned *>(&h);
+}
+
+__device__ __forceinline__ void ac_cp16(uint32_t dst, const void *src, bool take)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+
+// Byte offset of 16-byte chunk c of row r: halves of 8 chunks, 128-byte rows, swizzled.
+__device__ __forceinline__ uint32_t ac_off(int r, int c)
+{
+    return static_cast<uint32_t>((c >> 3) * (AC_KEYS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// A block's work, the same for all roles.
+struct TcWork {
+    int head, k0, k1;
+    int tiles;       // key tiles of the range
+    int n[2];        // tiles of each stream
+    int row0[2];     // first row
+    int nrows;       // rows from row0[0] on that exist (both streams together in rows mode)
+    bool by_keys;
+    // key tile of a stream's i-th step
+    __device__ __forceinline__ int tile(int s, int i) const { return by_keys ? 2 * i + s : i; }
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_constant__ AttnParams p)
+{
+    using C = TcCfg<DP>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    __shared__ int s_absent;
+    uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint64_t *empty = full + C::NBUF;
+    uint64_t *s_full = empty + C::NBUF, *p_full = s_full + 2, *pv_done = p_full + 2;
+    unsigned *masks = reinterpret_cast<unsigned *>(smem + C::OFF_MASK);
+    volatile int *abort_flag = &s_abort;
+
+    if (tid == 0) {
+        s_abort = 0;
+        s_absent = 0;
+        for (int i = 0; i < C::NBUF; ++i) {
+            mbar_init(&full[i], 128);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&pv_done[i], 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = s_tmem;
+
+    TcWork w;
+    {
+        int id = blockIdx.x;
+        const int rt = id % p.t_tiles;
+        id /= p.t_tiles;
+        w.head = id % p.hkv;
+        const int split = id / p.hkv;
+        w.by_keys = p.t_mode == 2;
+        w.k0 = split * p.t_keys;
+        w.k1 = min(p.prefix_len, w.k0 + p.t_keys);
+        w.tiles = (w.k1 - w.k0 + AC_KEYS - 1) / AC_KEYS;
+        w.row0[0] = rt * (w.by_keys ? AC_ROWS : 2 * AC_ROWS);
+        w.row0[1] = w.row0[0] + (w.by_keys ? 0 : AC_ROWS);
+        w.nrows = min(p.rows - w.row0[0], w.by_keys ? AC_ROWS : 2 * AC_ROWS);
+        w.n[0] = w.by_keys ? (w.tiles + 1) / 2 : w.tiles;
+        w.n[1] = w.by_keys ? w.tiles / 2 : w.nrows > AC_ROWS ? w.tiles : 0;
+    }
+    if (p.t_wait) pdl_wait();
+    pdl_launch_dependents();
+
+    if (warp >= 8 && warp < 12) {
+        // ------------------------------------------------ producers
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        const int pw = warp - 8;
+        const T *kb = static_cast<const T *>(p.k) + static_cast<long long>(w.head) * p.head_stride;
+        const T *vb = static_cast<const T *>(p.v) + static_cast<long long>(w.head) * p.head_stride;
+        // this lane's key of key tile t: its cache row, -1 when absent
+        auto find = [&](int t) -> long long {
+            const int j = w.k0 + t * AC_KEYS + 32 * pw + lane;
+            if (j >= w.k1) return -1;
+            const int page = __ldg(p.prefix_pages + (j >> p.page_shift));
+            if (page < 0 || page >= p.n_pages) {
+                atomicCAS(p.status, 0u, ST_BAD_ID);
+                s_absent = 1;
+                return -1;
+            }
+            return static_cast<long long>(page) * p.page_stride +
+                   static_cast<long long>(j & ((1 << p.page_shift) - 1)) * p.row_stride;
+        };
+        int n = 0;        // buffers issued
+        bool ok = true;
+        constexpr int CH = DP / 8, RPI = 32 / CH;  // chunks of a row, rows per warp instruction
+        const int c = lane % CH;
+        const bool c_in = c * 8 < p.d;
+        auto arrive = [&](int b) {
+            fence_proxy_async_smem();
+            mbar_arrive(&full[b % C::NBUF]);
+        };
+        auto rows_in = [&](uint32_t dst, const T *base, long long off) {
+#pragma unroll 4
+            for (int i = 0; i < 32 / RPI; ++i) {
+                const int rr = i * RPI + lane / CH;
+                const long long o = __shfl_sync(0xFFFFFFFFu, off, rr);
+                const bool take = o >= 0 && c_in;
+                ac_cp16(dst + ac_off(32 * pw + rr, c), base + (take ? o + c * 8 : 0), take);
+            }
+        };
+        auto fill = [&](const T *base, long long off) {
+            const int b = n % C::NBUF;
+            if (n >= C::NBUF && ok)
+                ok = mbar_wait_bounded(&empty[b], static_cast<unsigned>((n / C::NBUF - 1) & 1), abort_flag, p.status,
+                                       WAIT_LIMIT_NS);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) return;
+            rows_in(smem_addr(smem + C::OFF_RING) + b * C::TILE, base, off);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (n >= C::LAG) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(C::LAG) : "memory");
+                arrive(n - C::LAG);
+            }
+            ++n;
+        };
+        auto present = [&](int s, int i, long long off) {
+            const unsigned m = __ballot_sync(0xFFFFFFFFu, off >= 0);
+            if (lane == 0) masks[(s * AC_MASKS + (i & (AC_MASKS - 1))) * 4 + pw] = m;
+        };
+        // Q with the first buffer: rows past the batch are zeros
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (s == 1 && w.by_keys) break;
+            const int r = 32 * pw + lane + (s ? AC_ROWS : 0);
+            long long off = -1;
+            if (r < w.nrows) {
+                const int row = w.row0[0] + r, tok = row / p.group, g = row - tok * p.group;
+                off = tok * p.q_token_stride + (static_cast<long long>(w.head) * p.group + g) * p.q_head_stride;
+            }
+            rows_in(smem_addr(smem) + s * C::TILE, static_cast<const T *>(p.q), off);
+        }
+        const bool two = w.by_keys;  // the streams have keys of their own
+        long long cur[2], nxt[2];
+        cur[0] = find(w.tile(0, 0));
+        cur[1] = two && w.n[1] > 0 ? find(w.tile(1, 0)) : -1;
+        present(0, 0, cur[0]);
+        if (!two || w.n[1] > 0) present(1, 0, two ? cur[1] : cur[0]);
+        fill(kb, cur[0]);
+        if (two && w.n[1] > 0) fill(kb, cur[1]);
+        for (int i = 0; i < w.n[0] && ok; ++i) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (s == 1 && !two) break;
+                nxt[s] = i + 1 < w.n[s] ? find(w.tile(s, i + 1)) : -1;
+                if (i < w.n[s]) fill(vb, cur[s]);
+                if (i + 1 < w.n[s]) {
+                    present(s, i + 1, nxt[s]);
+                    if (!two) present(1, i + 1, nxt[s]);
+                    fill(kb, nxt[s]);
+                }
+                cur[s] = nxt[s];
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");  // no copy outlives the role
+        if (ok)
+            for (int b = n > C::LAG ? n - C::LAG : 0; b < n; ++b) arrive(b);
+    } else if (warp >= 12) {
+        // ------------------------------------------------ products
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 12 && lane == 0) {
+            constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+            constexpr uint32_t IDESC = (1u << 4) | (fmt << 7) | (fmt << 10) | ((128u >> 4) << 24);
+            constexpr uint32_t IDESC_S = IDESC | ((AC_KEYS / 8u) << 17);
+            constexpr uint32_t IDESC_O = IDESC | (1u << 16) | ((DP / 8u) << 17);  // B is MN-major
+            const uint32_t q_s = smem_addr(smem), ring = smem_addr(smem + C::OFF_RING);
+            int pos = 0;
+            bool ok = true;
+            auto acquire = [&]() -> int {  // the next buffer, once it is full
+                const int b = pos % C::NBUF;
+                ok = ok && mbar_wait_bounded(&full[b], static_cast<unsigned>((pos / C::NBUF) & 1), abort_flag, p.status,
+                                             WAIT_LIMIT_NS);
+                tc_fence_after();
+                ++pos;
+                return b;
+            };
+            auto scores = [&](int s, int b) {
+                const uint32_t qa = q_s + (w.by_keys ? 0 : s * C::TILE), ka = ring + b * C::TILE;
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ++ks) {
+                    const uint32_t o = (ks >> 2) * C::HALF + (ks & 3) * 32;
+                    tc_mma_ss(tm + col_s(s), tc_desc(qa + o, 16), tc_desc(ka + o, 16), IDESC_S, ks > 0);
+                }
+                tc_commit(&s_full[s]);
+            };
+            auto sums = [&](int s, int i, int b) {
+                ok = ok && mbar_wait_bounded(&p_full[s], static_cast<unsigned>(i & 1), abort_flag, p.status, WAIT_LIMIT_NS);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t va = ring + b * C::TILE;
+#pragma unroll
+                for (int ks = 0; ks < AC_KEYS / 16; ++ks)
+                    tc_mma(tm + col_o(s), tm + col_s(s) + ks * 8, tc_desc(va + ks * 2048, C::HALF), IDESC_O, i > 0 || ks > 0);
+                tc_commit(&pv_done[s]);
+            };
+            int done[2] = {0, 0}, scored[2] = {0, 0};  // products committed per stream, for the drain
+            int kbuf = acquire(), vbuf = 0;
+            if (ok) {
+                scores(0, kbuf);
+                scored[0] = 1;
+                if (w.by_keys) {
+                    tc_commit(&empty[kbuf]);
+                    if (w.n[1] > 0) kbuf = acquire();
+                }
+                if (w.n[1] > 0 && ok) {
+                    scores(1, kbuf);
+                    scored[1] = 1;
+                }
+                if (!w.by_keys || w.n[1] > 0) tc_commit(&empty[kbuf]);
+            }
+            for (int i = 0; i < w.n[0] && ok; ++i) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const bool own = w.by_keys || s == 0;                // takes its buffers itself
+                    const bool last = w.by_keys || s == 1 || w.n[1] == 0;  // and is their last reader
+                    if (i < w.n[s] && ok) {
+                        if (own) vbuf = acquire();
+                        if (ok) sums(s, i, vbuf);
+                        if (!ok) break;
+                        done[s] = i + 1;
+                        if (last) tc_commit(&empty[vbuf]);
+                    }
+                    if (i + 1 < w.n[s] && ok) {
+                        if (own) kbuf = acquire();
+                        if (!ok) break;
+                        scores(s, kbuf);
+                        scored[s] = i + 2;
+                        if (last) tc_commit(&empty[kbuf]);
+                    }
+                }
+            }
+            if (!ok) {  // after an abort: wait (bounded) for the products in flight
+                for (int s = 0; s < 2; ++s) {
+                    if (scored[s]) mbar_drain(&s_full[s], static_cast<unsigned>((scored[s] - 1) & 1));
+                    if (done[s]) mbar_drain(&pv_done[s], static_cast<unsigned>((done[s] - 1) & 1));
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ rows
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        const int s = warp >> 2, wq = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+        const uint32_t ts = tm + col_s(s) + lanes, to = tm + col_o(s) + lanes;
+        const int r = (w.by_keys ? 0 : s * AC_ROWS) + 32 * wq + lane;  // row of the block
+        float m = AC_NEG;
+        float2 l2 = make_float2(0.0f, 0.0f);
+        bool ok = true;
+        for (int i = 0; i < w.n[s] && ok; ++i) {
+            ok = mbar_wait_bounded(&s_full[s], static_cast<unsigned>(i & 1), abort_flag, p.status, WAIT_LIMIT_NS);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            float x[AC_KEYS];
+#pragma unroll
+            for (int c = 0; c < AC_KEYS; c += 32) tc_ld32(ts + c, x + c);
+            tc_wait_ld();
+            if (w.k0 + (w.tile(s, i) + 1) * AC_KEYS > w.k1 || *static_cast<volatile int *>(&s_absent)) {
+                const unsigned *mk = masks + (s * AC_MASKS + (i & (AC_MASKS - 1))) * 4;
+#pragma unroll
+                for (int c = 0; c < AC_KEYS; c += 32) {
+                    const unsigned bits = mk[c >> 5];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!(bits >> e & 1)) x[c + e] = -INFINITY;
+                }
+            }
+            float m0 = fmaxf(x[0], x[1]), m1 = fmaxf(x[2], x[3]);
+#pragma unroll
+            for (int c = 4; c < AC_KEYS; c += 4) {
+                m0 = fmaxf(m0, fmaxf(x[c], x[c + 1]));
+                m1 = fmaxf(m1, fmaxf(x[c + 2], x[c + 3]));
+            }
+            const float mx = fmaxf(fmaxf(m0, m1) * p.scale_log2, AC_NEG);
+            if (i == 0) {
+                m = mx;
+            } else {
+                const bool rise = mx > m + AC_RISE;
+                if (__any_sync(0xFFFFFFFFu, rise)) {
+                    // O holds the sums of the tiles before: rescale it once they are complete
+                    ok = mbar_wait_bounded(&pv_done[s], static_cast<unsigned>((i - 1) & 1), abort_flag, p.status,
+                                           WAIT_LIMIT_NS);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float f = rise ? ac_ex2(m - mx) : 1.0f;
+                    if (rise) m = mx;
+                    l2.x *= f;
+                    l2.y *= f;
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 32) {
+                        float o[32];
+                        tc_ld32(to + c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= f;
+                        tc_st32(to + c, reinterpret_cast<const unsigned *>(o));
+                    }
+                    tc_wait_st();
+                }
+            }
+            unsigned pk[AC_KEYS / 2];
+            const float2 sc = make_float2(p.scale_log2, p.scale_log2), nm = make_float2(-m, -m);
+#pragma unroll
+            for (int c = 0; c < AC_KEYS; c += 2) {
+                const float2 a = fma2(make_float2(x[c], x[c + 1]), sc, nm);
+                const float2 e = make_float2(ac_ex2(a.x), ac_ex2(a.y));
+                l2 = add2(l2, e);
+                pk[c / 2] = pack2<T>(e.x, e.y);
+            }
+            tc_st32(ts, pk);
+            tc_st32(ts + 32, pk + 32);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[s]);
+        }
+        // the part: row by row, 16 bytes a lane
+        const bool have = w.n[s] > 0;
+        if (have && ok) {
+            ok = mbar_wait_bounded(&pv_done[s], static_cast<unsigned>((w.n[s] - 1) & 1), abort_flag, p.status,
+                                   WAIT_LIMIT_NS);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            tc_fence_after();
+        }
+        const int split = blockIdx.x / (p.t_tiles * p.hkv);
+        const int slot = w.by_keys ? 2 * split + s : split;
+        const bool mine = r < w.nrows;
+        const long long at = (static_cast<long long>(slot) * p.hkv + w.head) * p.rows + w.row0[0] + r;
+        if (ok && (have || w.by_keys)) {  // a stream without keys leaves an empty part
+            if (mine) p.part_ml[at] = make_float2(have ? m : AC_NEG, l2.x + l2.y);
+#pragma unroll
+            for (int c = 0; c < DP; c += 32) {
+                float o[32];
+                if (have) {
+                    tc_ld32(to + c, o);
+                    tc_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    if (mine && c + e < p.d)
+                        *reinterpret_cast<float4 *>(p.part_o + at * p.d + c + e) =
+                            make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
+    // The suffix parts' launch may still be running: this one, which the
+    // combining launch waits for, ends after it.
+    pdl_wait();
+}
+
+template <typename T, int DP>
+cudaError_t launch_t(const AttnParams &p, cudaStream_t st)
+{
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(attn_tc_kernel<T, DP>), TcCfg<DP>::SMEM, done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attn_tc_kernel<T, DP>, dim3(static_cast<unsigned>(p.t_blocks)), AC_THREADS, TcCfg<DP>::SMEM, st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnParams &p, qgemv_dtype type, cudaStream_t st)
+{
+    if (type == QGEMV_F16) return p.d <= 64 ? launch_t<__half, 64>(p, st) : launch_t<__half, 128>(p, st);
+    return p.d <= 64 ? launch_t<__nv_bfloat16, 64>(p, st) : launch_t<__nv_bfloat16, 128>(p, st);
+}
+
+}  // namespace qg

@@ -77,6 +77,7 @@ struct AttnPlan {
     int rows, group;
     int p_tile, p_tiles, p_splits, p_keys;
     int s_tile, s_tiles, s_splits, s_keys;
+    int t_mode, t_tiles, t_splits, t_keys;
     long long part_rows;  // partial rows: slots * heads * rows
     long long ws_bytes;
 };
@@ -119,6 +120,26 @@ qgemv_status plan_attn(const qgemv_attn_batch *b, const qgemv_kv_cache *c, AttnP
     long long splits = std::min(std::max(1ll, ceil_div(p_units, 2)), std::max(1ll, kSlots / p_base));
     a.p_keys = static_cast<int>(p_units ? ceil_div(p_units, splits) * 64 : 64);
     a.p_splits = static_cast<int>(ceil_div(b->prefix_len, a.p_keys));
+    // or the tcgen05 kernel for tall batches: one block per multiprocessor,
+    // the split whose last wave ends first (a block costs about two tiles of
+    // 128 keys before and after its own)
+    a.t_mode = a.t_tiles = a.t_splits = a.t_keys = 0;
+    if (a.rows > 64 && c->head_dim <= 128 && b->prefix_len >= 512) {
+        a.t_mode = a.rows <= 128 ? 2 : 1;
+        a.t_tiles = static_cast<int>(ceil_div(a.rows, 256));
+        const long long units = ceil_div(b->prefix_len, 128), base = static_cast<long long>(c->n_heads) * a.t_tiles;
+        const int streams = a.t_mode == 2 ? 2 : 1;
+        long long best = 0, best_cost = INT64_MAX;
+        for (long long n = 1; n <= units && n <= 512; ++n) {
+            const long long each = ceil_div(units, n);
+            const long long cost = ceil_div(base * ceil_div(units, each), 152) * (ceil_div(each, streams) + 2);
+            if (cost < best_cost) best_cost = cost, best = n;
+        }
+        a.t_keys = static_cast<int>(ceil_div(units, best) * 128);
+        a.t_splits = static_cast<int>(ceil_div(b->prefix_len, a.t_keys));
+        if (base * a.t_splits > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
+        a.p_splits = a.t_splits * streams;  // the parts a row has from the prefix
+    }
     splits = std::min(std::max(1ll, ceil_div(s_units, 2)), std::max(ceil_div(s_units, 16), kSlots / s_base));
     a.s_keys = static_cast<int>(s_units ? ceil_div(s_units, splits) * 64 : 64);
     a.s_splits = static_cast<int>(ceil_div(s_most, a.s_keys));
@@ -357,7 +378,13 @@ qgemv_status qgemv_attn_prefix(const void *q, int64_t q_token_stride, int64_t q_
     p.s_tiles = a.s_tiles;
     p.s_splits = a.s_splits;
     p.s_keys = a.s_keys;
-    p.p_blocks = p.hkv * a.p_tiles * a.p_splits;
+    p.p_blocks = a.t_mode ? 0 : p.hkv * a.p_tiles * a.p_splits;
+    p.t_mode = a.t_mode;
+    p.t_tiles = a.t_tiles;
+    p.t_splits = a.t_splits;
+    p.t_keys = a.t_keys;
+    p.t_blocks = p.hkv * a.t_tiles * a.t_splits;
+    p.t_wait = a.s_splits == 0;
     uint8_t *w = static_cast<uint8_t *>(ws) + kCounterArea;
     p.part_o = reinterpret_cast<float *>(w);
     p.part_ml = reinterpret_cast<float2 *>(w + a.part_rows * 4 * d);

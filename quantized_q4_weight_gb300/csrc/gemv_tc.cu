@@ -42,6 +42,7 @@
 
 #include "gemv_kernel.cuh"
 #include "qgemv_launch.h"
+#include "tc_ptx.cuh"
 
 namespace qg {
 
@@ -95,9 +96,6 @@ static_assert(sizeof(TcParams) <= 32764, "kernel parameters are limited to 32764
 
 // ------------------------------------------------------------ tcgen05 helpers
 
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
 // A row's 16 A-operand words into 16 columns of tensor memory.
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const unsigned (&a)[16])
 {
@@ -108,8 +106,6 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const unsigned (&a)[16])
         "r"(a[10]), "r"(a[11]), "r"(a[12]), "r"(a[13]), "r"(a[14]), "r"(a[15])
         : "memory");
 }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 __device__ __forceinline__ void tc_ld8(uint32_t taddr, float (&d)[8])
 {
     unsigned r[8];
@@ -122,24 +118,7 @@ __device__ __forceinline__ void tc_ld8(uint32_t taddr, float (&d)[8])
     for (int i = 0; i < 8; ++i) d[i] = __uint_as_float(r[i]);
 }
 
-// D = A (tensor memory) x B (shared-memory descriptor) [+ D]; kind::f16.
-__device__ __forceinline__ void tc_mma(uint32_t d_t, uint32_t a_t, uint64_t bdesc, uint32_t idesc, int accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_t),
-        "r"(a_t), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// One arrival on `bar` once every MMA this thread issued before has completed.
-__device__ __forceinline__ void tc_commit(uint64_t *bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
-}
-
-// The same two, issued by one elected lane of a converged warp (the whole
+// tc_mma and tc_commit, issued by one elected lane of a converged warp (the whole
 // warp runs the issuing loop, so its operands are warp-uniform).
 __device__ __forceinline__ void tc_mma_elect(uint32_t d_t, uint32_t a_t, uint64_t bdesc, uint32_t idesc, int accumulate)
 {
@@ -158,11 +137,6 @@ __device__ __forceinline__ void tc_commit_elect(uint64_t *bar)
         "elect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
         : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // Instruction descriptor: f16 A and B (K-major), f32 D, M = 128, N = 16.
