@@ -118,27 +118,6 @@ __device__ __forceinline__ void tc_ld8(uint32_t taddr, float (&d)[8])
     for (int i = 0; i < 8; ++i) d[i] = __uint_as_float(r[i]);
 }
 
-// tc_mma and tc_commit, issued by one elected lane of a converged warp (the whole
-// warp runs the issuing loop, so its operands are warp-uniform).
-__device__ __forceinline__ void tc_mma_elect(uint32_t d_t, uint32_t a_t, uint64_t bdesc, uint32_t idesc, int accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred e, p;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_t),
-        "r"(a_t), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void tc_commit_elect(uint64_t *bar)
-{
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
-        : "memory");
-}
-
 // Instruction descriptor: f16 A and B (K-major), f32 D, M = 128, N = 16.
 constexpr uint32_t TC_IDESC = (1u << 4) | ((16u >> 3) << 17) | ((128u >> 4) << 24);
 
