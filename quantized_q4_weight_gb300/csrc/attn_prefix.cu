@@ -532,24 +532,31 @@ __device__ __forceinline__ void put(__nv_bfloat16 *o, float v) { *o = __float2bf
 __device__ __forceinline__ float get(const __half *v) { return __half2float(*v); }
 __device__ __forceinline__ float get(const __nv_bfloat16 *v) { return __bfloat162float(*v); }
 
-// One block per row.  Warp w takes every fourth part; a lane has elements
-// lane + 32 i of the head.
-template <typename T, typename TO>
-__global__ void __launch_bounds__(AT_THREADS) attn_combine_kernel(const __grid_constant__ AttnParams p)
+constexpr int CB_WARPS = 8;   // warps of a combining block
+constexpr int CB_BATCH = 4;   // parts whose loads are in flight per warp
+
+// W warps per row, 8 / W rows per block.  A row's warp w takes every W-th
+// part, CB_BATCH of them in flight; a lane has four adjacent elements of each
+// 128 (E in all).  Few rows: the latency of the parts' loads bounds it, so a
+// row has all eight warps.  Many rows: the parts' bytes (from L2) do, and one
+// warp a row saves the merge through shared memory.
+template <typename T, typename TO, int W, int E>
+__global__ void __launch_bounds__(CB_WARPS * 32) attn_combine_kernel(const __grid_constant__ AttnParams p)
 {
-    constexpr int E = 8;  // up to 256 / 32 elements a lane
-    __shared__ float s_o[4][256];
-    __shared__ float2 s_ml[4];
+    __shared__ float s_o[W > 1 ? W : 1][W > 1 ? 32 * E : 1];
+    __shared__ float2 s_ml[W];
     pdl_launch_dependents();
-    pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int tok = blockIdx.x / p.hq, h = blockIdx.x - tok * p.hq;
+    const int lane = threadIdx.x & 31, warp = W > 1 ? threadIdx.x >> 5 : 0;
+    const int out_row = W > 1 ? blockIdx.x : blockIdx.x * CB_WARPS + (threadIdx.x >> 5);
+    if (out_row >= p.n_seqs * p.n_q * p.hq) return;  // W == 1 only: no barrier follows
+    const int tok = out_row / p.hq, h = out_row - tok * p.hq;
     const int g = h / p.group, b = tok / p.n_q, i = tok - b * p.n_q;
     const int row = tok * p.group + (h - g * p.group);
+    pdl_wait();
     const int len = suffix_length(p, b);
     const int shared_by_all = max(0, len - p.n_q + 1);
     const int parts = p.p_splits + (shared_by_all + p.s_keys - 1) / p.s_keys;
-    if (h == 0 && i == 0 && threadIdx.x == 0 && __ldg(p.suffix_len + b) != len) atomicCAS(p.status, 0u, ST_BAD_ID);
+    if (h == 0 && i == 0 && warp == 0 && lane == 0 && __ldg(p.suffix_len + b) != len) atomicCAS(p.status, 0u, ST_BAD_ID);
     float m = AT_NEG, l = 0.0f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
@@ -561,18 +568,37 @@ __global__ void __launch_bounds__(AT_THREADS) attn_combine_kernel(const __grid_c
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = o[e] * c + op[e] * cp;
     };
-    for (int s = warp; s < parts; s += 4) {
-        const long long at = (static_cast<long long>(s) * p.hkv + g) * p.rows + row;
-        const float2 ml = p.part_ml[at];
-        float op[E];
+    // element e of this lane is at lane 4 + 128 (e / 4) + e % 4
+    const long long stride = static_cast<long long>(p.hkv) * p.rows, first = static_cast<long long>(g) * p.rows + row;
+    for (int s0 = warp; s0 < parts; s0 += W * CB_BATCH) {
+        float2 ml[CB_BATCH];
+        float op[CB_BATCH][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) op[e] = lane + 32 * e < p.d ? p.part_o[at * p.d + lane + 32 * e] : 0.0f;
-        add(ml.x, ml.y, op);
+        for (int u = 0; u < CB_BATCH; ++u) {
+            const int s = s0 + u * W;
+            ml[u] = make_float2(AT_NEG, 0.0f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) op[u][e] = 0.0f;
+            if (s < parts) {
+                const long long at = first + s * stride;
+                ml[u] = p.part_ml[at];
+#pragma unroll
+                for (int e = 0; e < E; e += 4) {
+                    const int c = 4 * lane + 32 * e;
+                    if (c < p.d) {
+                        const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * p.d + c);
+                        op[u][e] = v.x, op[u][e + 1] = v.y, op[u][e + 2] = v.z, op[u][e + 3] = v.w;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < CB_BATCH; ++u) add(ml[u].x, ml[u].y, op[u]);
     }
     // the suffix rows that only the later queries see, one a step
     const T *q = static_cast<const T *>(p.q) + tok * p.q_token_stride + h * p.q_head_stride;
     const int32_t *table = p.suffix_pages + b * p.suffix_pages_stride;
-    for (int j = shared_by_all + warp; j <= len - p.n_q + i; j += 4) {
+    for (int j = shared_by_all + warp; j <= len - p.n_q + i; j += W) {
         const long long off = key_row(p, table, j);
         if (off < 0) continue;
         const T *k = static_cast<const T *>(p.k) + off + g * p.head_stride;
@@ -580,7 +606,7 @@ __global__ void __launch_bounds__(AT_THREADS) attn_combine_kernel(const __grid_c
         float dot = 0.0f, op[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int c = lane + 32 * e;
+            const int c = 4 * lane + 128 * (e / 4) + e % 4;
             op[e] = 0.0f;
             if (c < p.d) {
                 dot = fmaf(get(q + c), get(k + c), dot);
@@ -591,28 +617,55 @@ __global__ void __launch_bounds__(AT_THREADS) attn_combine_kernel(const __grid_c
         for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
         add(dot * p.scale_log2, 1.0f, op);
     }
+    TO *out = static_cast<TO *>(p.o) + tok * p.o_token_stride + h * p.o_head_stride;
+    float mx = m, total = l;
+    if constexpr (W == 1) {
+        const float inv = 1.0f / total;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][lane + 32 * e] = o[e];
-    if (lane == 0) s_ml[warp] = make_float2(m, l);
-    __syncthreads();
-    float mx = s_ml[0].x, total = 0.0f, c[4];
+        for (int e = 0; e < E; ++e) {
+            const int c = 4 * lane + 128 * (e / 4) + e % 4;
+            if (c < p.d) put(out + c, total == 0.0f ? 0.0f : o[e] * inv);
+        }
+    } else {
 #pragma unroll
-    for (int u = 1; u < 4; ++u) mx = fmaxf(mx, s_ml[u].x);
+        for (int e = 0; e < E; e += 4)
+            *reinterpret_cast<float4 *>(&s_o[warp][4 * lane + 32 * e]) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        if (lane == 0) s_ml[warp] = make_float2(m, l);
+        __syncthreads();
+        float c[W];
+        mx = s_ml[0].x;
+        total = 0.0f;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        c[u] = ex2(s_ml[u].x - mx);
-        total += s_ml[u].y * c[u];
+        for (int u = 1; u < W; ++u) mx = fmaxf(mx, s_ml[u].x);
+#pragma unroll
+        for (int u = 0; u < W; ++u) {
+            c[u] = ex2(s_ml[u].x - mx);
+            total += s_ml[u].y * c[u];
+        }
+        const int e = threadIdx.x;
+        if (e < p.d) {
+            float v = 0.0f;
+#pragma unroll
+            for (int u = 0; u < W; ++u) v = fmaf(s_o[u][e], c[u], v);
+            put(out + e, total == 0.0f ? 0.0f : v * (1.0f / total));
+        }
     }
-    const float inv = 1.0f / total;
-    for (int e = threadIdx.x; e < p.d; e += AT_THREADS) {
-        float v = 0.0f;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) v = fmaf(s_o[u][e], c[u], v);
-        put(static_cast<TO *>(p.o) + tok * p.o_token_stride + h * p.o_head_stride + e, total == 0.0f ? 0.0f : v * inv);
-    }
-    if (p.lse && threadIdx.x == 0)
+    if (p.lse && warp == 0 && lane == 0)
         p.lse[static_cast<long long>(tok) * p.hq + h] =
             total != 0.0f ? (mx + log2f(total)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <typename T, typename TO>
+cudaError_t launch_combine(const AttnParams &p, cudaStream_t st)
+{
+    const unsigned rows = static_cast<unsigned>(p.n_seqs * p.n_q * p.hq);
+    // eight warps a row up to four waves of blocks (152 multiprocessors, eight blocks each)
+    if (rows <= 608)
+        return p.d <= 128 ? launch_pdl(attn_combine_kernel<T, TO, 8, 4>, dim3(rows), CB_WARPS * 32, 0, st, p)
+                          : launch_pdl(attn_combine_kernel<T, TO, 8, 8>, dim3(rows), CB_WARPS * 32, 0, st, p);
+    const dim3 grid((rows + CB_WARPS - 1) / CB_WARPS);
+    return p.d <= 128 ? launch_pdl(attn_combine_kernel<T, TO, 1, 4>, grid, CB_WARPS * 32, 0, st, p)
+                      : launch_pdl(attn_combine_kernel<T, TO, 1, 8>, grid, CB_WARPS * 32, 0, st, p);
 }
 
 template <typename T, int DP>
@@ -637,9 +690,7 @@ cudaError_t launch_type(const AttnParams &p, qgemv_dtype o_type, cudaStream_t st
         const cudaError_t t = launch_attn_tc(p, std::is_same<T, __half>::value ? QGEMV_F16 : QGEMV_BF16, st);
         if (t != cudaSuccess) return t;
     }
-    const dim3 grid(static_cast<unsigned>(p.n_seqs * p.n_q * p.hq));
-    return o_type == QGEMV_F32 ? launch_pdl(attn_combine_kernel<T, float>, grid, AT_THREADS, 0, st, p)
-                               : launch_pdl(attn_combine_kernel<T, T>, grid, AT_THREADS, 0, st, p);
+    return o_type == QGEMV_F32 ? launch_combine<T, float>(p, st) : launch_combine<T, T>(p, st);
 }
 
 }  // namespace

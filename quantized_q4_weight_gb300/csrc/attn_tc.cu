@@ -8,25 +8,23 @@
 //
 // A block (one per multiprocessor) takes a range of keys of one cache head
 // and two "streams" of 128 rows, each with its own scores S and weighted sum
-// O in tensor memory (2 x 64 and 128 columns):
+// O in tensor memory (128 columns each):
 //   rows mode: the streams are two row tiles over the same keys;
 //   keys mode (at most 128 rows): one row tile, and the streams take
 //   alternate key tiles and leave two parts.
-// Per stream and step of 64 keys (half a tile of the ring):
+// Per stream and tile of 128 keys:
 //   S = Q K^T (tcgen05.mma, both operands from shared memory), read back row
 //   by row: thread i of the stream's four warps owns row i, so maxima and
 //   sums need no shuffles; P = 2^(S scale - m), rounded to the cache's type,
 //   goes over S's own columns (two elements a column); O += P V with P from
 //   tensor memory and V from shared memory.
-// One thread issues the products.  S is double-buffered: the scores of step
-// j + 2 are issued behind the sums of step j, so the row threads find their
-// next scores ready, and the products of four steps in flight cover the
-// weights' latency.  (With one S of 128 keys a stream the row threads waited
-// for their own products: 257 us instead of the figure below at 1024 rows x
-// 8 heads x 65536 keys of 128 elements.)  The price: with N = 64 the scores
-// read Q twice as often, 96 KB of shared memory a tile and stream instead of
-// 64, so that shared memory (320 KB a tile of two streams, 2500 cycles)
-// bounds the kernel, at 82 % of the products' own 2048 cycles.
+// One warp issues the products, alternating between the streams, so that one
+// stream's products run while the other's weights are computed; a stream's
+// weights go over in two halves, and the sums of the first start while the
+// second forms.  (Scores of 64 keys, double-buffered, were slower, 274 us
+// against 239 at 1024 rows x 8 heads x 65536 keys of 128 elements: with N = 64
+// a product takes 49 cycles instead of 32, bound by its operands' shared-memory
+// reads, and the waits double.)
 //
 // The reference m of a row is its running maximum, but follows it only when
 // that rises by more than 2^8: O is rescaled (in tensor memory, by the row's
@@ -55,7 +53,6 @@ namespace {
 
 constexpr int AC_THREADS = 512;   // warps 0-3, 4-7: rows of streams 0, 1; 8-11: producers; 12: products
 constexpr int AC_KEYS = 128;      // keys of a tile
-constexpr int AC_STEP = 64;       // keys of a step: half a tile
 constexpr int AC_ROWS = 128;      // rows of a stream
 constexpr int AC_MASKS = 8;       // tiles whose presence masks are kept, per stream: the ring holds fewer
 constexpr float AC_RISE = 8.0f;   // rise of the maximum (base 2) that moves the reference
@@ -69,14 +66,14 @@ struct TcCfg {
     static constexpr int LAG = DP == 64 ? 4 : 2;          // buffers in flight behind the one being issued
     static constexpr int OFF_RING = 2 * TILE;
     static constexpr int OFF_BAR = OFF_RING + NBUF * TILE;
-    static constexpr int NBAR = 2 * NBUF + 12;
+    static constexpr int NBAR = 2 * NBUF + 8;
     static constexpr int OFF_MASK = OFF_BAR + 8 * NBAR;   // [stream][AC_MASKS][4] words
     static constexpr int SMEM = (OFF_MASK + 2 * AC_MASKS * 16 + 15) / 16 * 16 + 1024;  // aligned up to 1024 at run time
 };
 static_assert(TcCfg<128>::SMEM <= 227 * 1024, "shared memory of the prefix kernel");
 
-// Tensor-memory columns of a stream's scores of step j (weights over them) and sums.
-__device__ __forceinline__ uint32_t col_s(int s, int j) { return 128u * s + 64u * (j & 1); }
+// Tensor-memory columns of a stream's scores (weights over their first half) and sums.
+__device__ __forceinline__ constexpr uint32_t col_s(int s) { return 128u * s; }
 __device__ __forceinline__ constexpr uint32_t col_o(int s) { return 256u + 128u * s; }
 
 // Four products D = A x B [+ D] along K: A and B in shared memory, 32 bytes a
@@ -205,19 +202,10 @@ __device__ __forceinline__ uint32_t ac_off(int r, int c)
     return static_cast<uint32_t>((c >> 3) * (AC_KEYS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// Bounded wait of a converged warp.  One lane polls (a warp's 32 polls are 32
-// accesses of shared memory, and a dozen waiting warps took a third of the
-// kernel's time with them), at first without the clock, whose reading takes
-// longer than most of these waits.
+// Bounded wait of a converged warp.
 __device__ __forceinline__ bool ac_wait(uint64_t *bar, unsigned parity, volatile int *abort_flag, unsigned *status)
 {
-    int ok = 1;
-    if ((threadIdx.x & 31) == 0) {
-        ok = 0;
-        for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
-        if (!ok) ok = mbar_wait_bounded(bar, parity, abort_flag, status, WAIT_LIMIT_NS);
-    }
-    return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;  // and orders what the other lanes read behind the wait
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, status, WAIT_LIMIT_NS)) != 0;
 }
 
 // A block's work, the same for all roles.
@@ -244,7 +232,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *empty = full + C::NBUF;
-    uint64_t *s_full = empty + C::NBUF, *p_full = s_full + 4, *pv_done = p_full + 4;  // [stream][step & 1]
+    uint64_t *s_full = empty + C::NBUF, *p_full = s_full + 2, *pv_done = p_full + 4;  // [stream]; [stream][half]; [stream]
     unsigned *masks = reinterpret_cast<unsigned *>(smem + C::OFF_MASK);
     volatile int *abort_flag = &s_abort;
 
@@ -255,9 +243,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_con
             mbar_init(&full[i], 128);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[2 * i], 4);
+            mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&pv_done[i], 1);
         }
         fence_mbar_init();
@@ -390,7 +379,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_con
         if (warp == 12) {
             constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
             constexpr uint32_t IDESC = (1u << 4) | (fmt << 7) | (fmt << 10) | ((128u >> 4) << 24);
-            constexpr uint32_t IDESC_S = IDESC | ((AC_STEP / 8u) << 17);
+            constexpr uint32_t IDESC_S = IDESC | ((AC_KEYS / 8u) << 17);
             constexpr uint32_t IDESC_O = IDESC | (1u << 16) | ((DP / 8u) << 17);  // B is MN-major
             const uint32_t q_s = smem_addr(smem), ring = smem_addr(smem + C::OFF_RING);
             int pos = 0;
@@ -402,57 +391,56 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_con
                 ++pos;
                 return __shfl_sync(0xFFFFFFFFu, b, 0);
             };
-            auto scores = [&](int s, int j, int b) {  // step j, from the half j & 1 of buffer b's keys
-                const uint32_t qa = q_s + (w.by_keys ? 0 : s * C::TILE);
-                const uint32_t ka = ring + b * C::TILE + (j & 1) * AC_STEP * 128;
+            auto scores = [&](int s, int b) {
+                const uint32_t qa = q_s + (w.by_keys ? 0 : s * C::TILE), ka = ring + b * C::TILE;
 #pragma unroll
                 for (int hf = 0; hf < DP / 64; ++hf)
-                    tc_mma4_ss(tm + col_s(s, j), tc_desc(qa + hf * C::HALF, 16), tc_desc(ka + hf * C::HALF, 16), IDESC_S, hf);
-                tc_commit_elect(&s_full[2 * s + (j & 1)]);
+                    tc_mma4_ss(tm + col_s(s), tc_desc(qa + hf * C::HALF, 16), tc_desc(ka + hf * C::HALF, 16), IDESC_S, hf);
+                tc_commit_elect(&s_full[s]);
             };
-            auto sums = [&](int s, int j, int b) {
-                ok = ok && ac_wait(&p_full[2 * s + (j & 1)], static_cast<unsigned>((j >> 1) & 1), abort_flag,
-                                             p.status);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t va = ring + b * C::TILE + (j & 1) * AC_STEP * 128;
-                tc_mma4_ts(tm + col_o(s), tm + col_s(s, j), tc_desc(va, C::HALF), IDESC_O, j > 0);
-                tc_commit_elect(&pv_done[2 * s + (j & 1)]);
+            auto sums = [&](int s, int i, int b) {
+                const uint32_t va = ring + b * C::TILE;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    ok = ok && ac_wait(&p_full[2 * s + hf], static_cast<unsigned>(i & 1), abort_flag, p.status);
+                    if (!ok) return;
+                    tc_fence_after();
+                    tc_mma4_ts(tm + col_o(s), tm + col_s(s) + 32 * hf, tc_desc(va + hf * AC_KEYS / 2 * 128, C::HALF), IDESC_O,
+                               i > 0 || hf > 0);
+                }
+                if (i == w.n[s] - 1) tc_commit_elect(&pv_done[s]);
             };
-            int done[2] = {0, 0}, scored[2] = {0, 0};  // steps committed per stream, for the drain
-            int kbuf[2] = {0, 0}, vbuf[2] = {0, 0};    // the streams' current buffers
-            const int n[2] = {2 * w.n[0], 2 * w.n[1]};  // steps
-            // One stream's products of step j: the sums with step j's weights, then
-            // the scores of step j + 2 into the columns that those weights leave.
-            // j = -2, -1: the first two scores.
-            auto turn = [&](int s, int j) {
+            int scored[2] = {0, 0}, summed[2] = {0, 0};  // tiles issued per stream, for the drain
+            int kbuf = 0, vbuf = 0;                      // the current buffers
+            // One stream's products of tile i: the sums with its weights, then the
+            // scores of the next tile over the columns that those weights leave.
+            // i = -1: the first scores.
+            auto turn = [&](int s, int i) {
                 const bool own = w.by_keys || s == 0;                  // takes its buffers itself
                 const bool last = w.by_keys || s == 1 || w.n[1] == 0;  // and is their last reader
-                if (j >= 0 && j < n[s]) {
-                    if (!(j & 1)) vbuf[s] = own ? acquire() : vbuf[0];
-                    if (ok) sums(s, j, vbuf[s]);
+                if (i >= 0 && i < w.n[s]) {
+                    if (own) vbuf = acquire();
+                    if (ok) sums(s, i, vbuf);
                     if (!ok) return;
-                    done[s] = j + 1;
-                    if (last && (j & 1)) tc_commit_elect(&empty[vbuf[s]]);
+                    summed[s] = i + 1;
+                    if (last) tc_commit_elect(&empty[vbuf]);
                 }
-                if (j + 2 < n[s]) {
-                    if (!(j & 1)) kbuf[s] = own ? acquire() : kbuf[0];
+                if (i + 1 < w.n[s]) {
+                    if (own) kbuf = acquire();
                     if (!ok) return;
-                    scores(s, j + 2, kbuf[s]);
-                    scored[s] = j + 3;
-                    if (last && (j & 1)) tc_commit_elect(&empty[kbuf[s]]);
+                    scores(s, kbuf);
+                    scored[s] = i + 2;
+                    if (last) tc_commit_elect(&empty[kbuf]);
                 }
             };
-            for (int j = -2; j < n[0] && ok; ++j) {
-                turn(0, j);
-                if (ok) turn(1, j);
+            for (int i = -1; i < w.n[0] && ok; ++i) {
+                turn(0, i);
+                if (ok) turn(1, i);
             }
             if (!ok && lane == 0) {  // after an abort: wait (bounded) for the products in flight
                 for (int s = 0; s < 2; ++s) {
-                    for (int j = scored[s] > 2 ? scored[s] - 2 : 0; j < scored[s]; ++j)
-                        mbar_drain(&s_full[2 * s + (j & 1)], static_cast<unsigned>((j >> 1) & 1));
-                    if (done[s])
-                        mbar_drain(&pv_done[2 * s + ((done[s] - 1) & 1)], static_cast<unsigned>(((done[s] - 1) >> 1) & 1));
+                    if (scored[s]) mbar_drain(&s_full[s], static_cast<unsigned>((scored[s] - 1) & 1));
+                    if (summed[s] && summed[s] == w.n[s]) mbar_drain(&pv_done[s], 0);
                 }
             }
         }
@@ -467,45 +455,40 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_con
         float m = AC_NEG;
         float2 l2 = make_float2(0.0f, 0.0f);
         bool ok = true;
-        const int steps = 2 * w.n[s];
-        for (int j = 0; j < steps && ok; ++j) {
-            ok = ac_wait(&s_full[2 * s + (j & 1)], static_cast<unsigned>((j >> 1) & 1), abort_flag, p.status);
+        for (int i = 0; i < w.n[s] && ok; ++i) {
+            ok = ac_wait(&s_full[s], static_cast<unsigned>(i & 1), abort_flag, p.status);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t ts = tm + col_s(s, j) + lanes;
-            float x[AC_STEP];
-            tc_ld32(ts, x);
-            tc_ld32(ts + 32, x + 32);
-            tc_wait_ld();
-            if (w.k0 + (w.tile(s, j >> 1) + 1) * AC_KEYS > w.k1 || *static_cast<volatile int *>(&s_absent)) {
-                const unsigned *mk = masks + (s * AC_MASKS + ((j >> 1) & (AC_MASKS - 1))) * 4 + 2 * (j & 1);
+            const uint32_t ts = tm + col_s(s) + lanes;
+            float x[AC_KEYS];
 #pragma unroll
-                for (int c = 0; c < AC_STEP; c += 32) {
+            for (int c = 0; c < AC_KEYS; c += 32) tc_ld32(ts + c, x + c);
+            tc_wait_ld();
+            if (w.k0 + (w.tile(s, i) + 1) * AC_KEYS > w.k1 || *static_cast<volatile int *>(&s_absent)) {
+                const unsigned *mk = masks + (s * AC_MASKS + (i & (AC_MASKS - 1))) * 4;
+#pragma unroll
+                for (int c = 0; c < AC_KEYS; c += 32) {
                     const unsigned bits = mk[c >> 5];
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (!(bits >> e & 1)) x[c + e] = -INFINITY;
                 }
             }
-            float m0 = fmaxf(x[0], x[1]), m1 = fmaxf(x[2], x[3]);
+            float mm[4];
 #pragma unroll
-            for (int c = 4; c < AC_STEP; c += 4) {
-                m0 = fmaxf(m0, fmaxf(x[c], x[c + 1]));
-                m1 = fmaxf(m1, fmaxf(x[c + 2], x[c + 3]));
-            }
-            const float mx = fmaxf(fmaxf(m0, m1) * p.scale_log2, AC_NEG);
-            if (j == 0) {
+            for (int e = 0; e < 4; ++e) mm[e] = fmaxf(x[2 * e], x[2 * e + 1]);
+#pragma unroll
+            for (int c = 8; c < AC_KEYS; c += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mm[e] = fmaxf(mm[e], fmaxf(x[c + 2 * e], x[c + 2 * e + 1]));
+            const float mx = fmaxf(fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * p.scale_log2, AC_NEG);
+            if (i == 0) {
                 m = mx;
             } else {
                 const bool rise = mx > m + AC_RISE;
                 if (__any_sync(0xFFFFFFFFu, rise)) {
-                    // O holds the sums of the steps before: rescale it once they are complete
-                    // (the scores of step j came after the sums of step j - 2, so this
-                    // barrier's phase before the awaited one is over)
-                    ok = ac_wait(&pv_done[2 * s + ((j - 1) & 1)], static_cast<unsigned>(((j - 1) >> 1) & 1),
-                                           abort_flag, p.status);
-                    if (!ok) break;
-                    tc_fence_after();
+                    // O holds the sums of the tiles before; they are complete: the
+                    // scores of this tile were issued after them
                     const float f = rise ? ac_ex2(m - mx) : 1.0f;
                     if (rise) m = mx;
                     l2.x *= f;
@@ -522,26 +505,28 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_con
                     tc_wait_st();
                 }
             }
-            unsigned pk[AC_STEP / 2];
             const float2 sc = make_float2(p.scale_log2, p.scale_log2), nm = make_float2(-m, -m);
 #pragma unroll
-            for (int c = 0; c < AC_STEP; c += 2) {
-                const float2 a = fma2(make_float2(x[c], x[c + 1]), sc, nm);
-                const float2 e = make_float2(ac_ex2(a.x), ac_ex2(a.y));
-                l2 = add2(l2, e);
-                pk[c / 2] = pack2<T>(e.x, e.y);
+            for (int hf = 0; hf < 2; ++hf) {  // the first half's sums start while the second half's weights form
+                unsigned pk[32];
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) {
+                    const float2 a = fma2(make_float2(x[64 * hf + c], x[64 * hf + c + 1]), sc, nm);
+                    const float2 e = make_float2(ac_ex2(a.x), ac_ex2(a.y));
+                    l2 = add2(l2, e);
+                    pk[c / 2] = pack2<T>(e.x, e.y);
+                }
+                tc_st32(ts + 32 * hf, pk);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * s + hf]);
             }
-            tc_st32(ts, pk);
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * s + (j & 1)]);
         }
         // the part: row by row, 16 bytes a lane
         const bool have = w.n[s] > 0;
         if (have && ok) {
-            ok = ac_wait(&pv_done[2 * s + ((steps - 1) & 1)], static_cast<unsigned>(((steps - 1) >> 1) & 1),
-                                   abort_flag, p.status);
+            ok = ac_wait(&pv_done[s], 0, abort_flag, p.status);
             tc_fence_after();
         }
         const int split = blockIdx.x / (p.t_tiles * p.hkv);

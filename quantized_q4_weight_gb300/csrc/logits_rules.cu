@@ -28,9 +28,11 @@
 namespace qg {
 namespace {
 
-constexpr int LG_THREADS = 512;
-constexpr int LG_SLICE_MAX = 16384;  // 64 KB of words: three blocks per multiprocessor
-constexpr int LG_SLICE_MIN = 2048;   // one 16-byte load of fp32 a thread
+constexpr int LG_THREADS = 256;
+constexpr int LG_SLICE_MAX = 8192;   // 32 KB of words: six blocks per multiprocessor
+constexpr int LG_SLICE_MIN = 1024;   // one 16-byte load of fp32 a thread
+constexpr int LG_AHEAD = 1;          // chunks in flight per thread
+constexpr int LG_KEEP = 4;           // list entries kept per thread: 1024 of a row's
 constexpr unsigned LG_COUNT_MASK = (1u << 20) - 1;
 
 __device__ __forceinline__ float lg_to_f(float v) { return v; }
@@ -56,9 +58,28 @@ struct alignas(16) Chunk {
     T e[16 / sizeof(T)];
 };
 
-__device__ __forceinline__ int bounded_length(const int32_t *len, long long r, int most, unsigned *status)
+// A chunk that is read once (it may be written in place, so not through the
+// read-only path).
+template <typename T>
+__device__ __forceinline__ Chunk<T> ld_stream(const Chunk<T> *a)
 {
-    const int n = __ldg(len + r);
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(a));
+    Chunk<T> c;
+    memcpy(&c, &v, 16);
+    return c;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 as_uint4(const Chunk<T> &c)
+{
+    uint4 v;
+    memcpy(&v, &c, 16);
+    return v;
+}
+
+// A list's length within its bound; a length outside is recorded.
+__device__ __forceinline__ int bounded(int n, int most, unsigned *status)
+{
     if (n < 0 || n > most) {
         if (threadIdx.x == 0) atomicCAS(status, 0u, ST_BAD_ID);
         return n < 0 ? 0 : most;
@@ -67,7 +88,7 @@ __device__ __forceinline__ int bounded_length(const int32_t *len, long long r, i
 }
 
 template <typename T>
-__global__ void __launch_bounds__(LG_THREADS) logits_kernel(const __grid_constant__ LogitsParams p)
+__global__ void __launch_bounds__(LG_THREADS, 6) logits_kernel(const __grid_constant__ LogitsParams p)
 {
     constexpr int E = 16 / sizeof(T);
     extern __shared__ __align__(16) unsigned lg_smem[];
@@ -92,8 +113,36 @@ __global__ void __launch_bounds__(LG_THREADS) logits_kernel(const __grid_constan
     const long long t0 = static_cast<long long>(blockIdx.x) * p.slice - shift;
     const long long t1 = min(p.vocab, t0 + p.slice);
 
-    const int nh = p.hist ? bounded_length(p.hist_len, r, p.max_hist, p.status) : 0;
-    const int nb = p.bias ? bounded_length(p.bias_len, r, p.max_bias, p.status) : 0;
+    // Chunks [c_lo, c_hi) of the slice lie in the row as a whole; the first
+    // chunk of the row and the last may not.  They go LG_AHEAD at a time, their
+    // loads and mask words first; the first ones are on their way while the
+    // lists are read.  A slice is counted in 32 bits from t0.
+    const uint32_t *mask = p.mask ? p.mask + r * p.mask_stride : nullptr;
+    const int tokens = static_cast<int>(t1 - t0);  // below 0 for a slice past the row
+    const int c_lo = t0 < 0 ? 1 : 0, c_hi = tokens < 0 ? 0 : tokens / E;
+    const Chunk<T> *xc = reinterpret_cast<const Chunk<T> *>(x + t0);
+    const int bit0 = static_cast<int>(t0);  // a token's mask bit is bit0 + its place
+    Chunk<T> in[LG_AHEAD];
+    unsigned allow[LG_AHEAD];
+    auto fetch = [&](int ch0) {
+#pragma unroll
+        for (int u = 0; u < LG_AHEAD; ++u) {
+            const int ch = ch0 + u * LG_THREADS;
+            allow[u] = 0xFFFFFFFFu;
+            if (ch < c_hi && ch >= c_lo) {
+                in[u] = ld_stream(xc + ch);
+                if (mask) {
+                    const int bit = bit0 + ch * E;
+                    allow[u] = __ldg(mask + (bit >> 5)) >> (bit & 31);
+                    // a chunk of a row that is not aligned may run into the next word
+                    if ((bit & 31) + E > 32) allow[u] |= __ldg(mask + (bit >> 5) + 1) << (32 - (bit & 31));
+                }
+            }
+        }
+    };
+    const int len_h = p.hist ? __ldg(p.hist_len + r) : 0, len_b = p.bias ? __ldg(p.bias_len + r) : 0;
+    fetch(tid);
+    const int nh = bounded(len_h, p.max_hist, p.status), nb = bounded(len_b, p.max_bias, p.status);
     const long long *hist = p.hist + r * p.hist_stride;
     const long long *bid = p.bias_ids + r * p.bias_stride;
     const float *bias = p.bias + r * p.bias_stride;
@@ -103,25 +152,45 @@ __global__ void __launch_bounds__(LG_THREADS) logits_kernel(const __grid_constan
     const long long lo = max(t0, 0ll);
 
     if (nh | nb) {
+        // the lists' first entries stay in registers between the passes
+        long long id[LG_KEEP];
+#pragma unroll
+        for (int u = 0; u < LG_KEEP; ++u) {
+            const int i = tid + u * LG_THREADS;
+            id[u] = i < nh ? __ldg(hist + i) : i < nh + nb ? __ldg(bid + (i - nh)) : -1;
+        }
         __syncthreads();
-        for (int i = tid; i < nh + nb; i += LG_THREADS) {
-            const long long t = i < nh ? __ldg(hist + i) : __ldg(bid + (i - nh));
+        auto touch = [&](long long t) {
             if (t >= lo && t < t1) {
-                const int l = static_cast<int>(t - t0);
+                const int l = static_cast<int>(t) - bit0;
                 words[l] = 0;
                 atomicOr(&touched[l >> 5], 1u << (l & 31));
             }
-        }
+        };
+#pragma unroll
+        for (int u = 0; u < LG_KEEP; ++u) touch(id[u]);
+        for (int i = tid + LG_KEEP * LG_THREADS; i < nh + nb; i += LG_THREADS)
+            touch(i < nh ? __ldg(hist + i) : __ldg(bid + (i - nh)));
         __syncthreads();
-        for (int i = tid; i < nb; i += LG_THREADS) {
-            const long long t = __ldg(bid + i);
+        // a bias entry i of token t, then an occurrence of t
+        auto entry = [&](long long t, int i) {
             if (t >= lo && t < t1) atomicMax(&words[t - t0], static_cast<unsigned>(i + 1) << 20);
-        }
-        __syncthreads();
-        for (int i = tid; i < nh; i += LG_THREADS) {
-            const long long t = __ldg(hist + i);
+        };
+        auto occurs = [&](long long t) {
             if (t >= lo && t < t1) atomicAdd(&words[t - t0], 1u);
+        };
+        if (nb) {
+#pragma unroll
+            for (int u = 0; u < LG_KEEP; ++u)
+                if (tid + u * LG_THREADS >= nh) entry(id[u], tid + u * LG_THREADS - nh);
+            for (int i = tid + LG_KEEP * LG_THREADS; i < nh + nb; i += LG_THREADS)
+                if (i >= nh) entry(__ldg(bid + (i - nh)), i - nh);
+            __syncthreads();
         }
+#pragma unroll
+        for (int u = 0; u < LG_KEEP; ++u)
+            if (tid + u * LG_THREADS < nh) occurs(id[u]);
+        for (int i = tid + LG_KEEP * LG_THREADS; i < nh; i += LG_THREADS) occurs(__ldg(hist + i));
     }
     __syncthreads();
 
@@ -137,71 +206,71 @@ __global__ void __launch_bounds__(LG_THREADS) logits_kernel(const __grid_constan
 
     const float NEG = __int_as_float(0xFF800000);
     float best = NEG;
-    long long best_t = 0;
-    const uint32_t *mask = p.mask ? p.mask + r * p.mask_stride : nullptr;
-    const long long mask_last = (p.vocab - 1) >> 5;
-    const int chunks = static_cast<int>((t1 - t0 + E - 1) / E);
-    for (int ch = tid; ch < chunks; ch += LG_THREADS) {
-        const int l0 = ch * E;
-        const long long t = t0 + l0;
-        const unsigned hit = touched[l0 >> 5] >> (l0 & 31);
-        if (t >= 0 && t + E <= p.vocab) {
-            Chunk<T> in = *reinterpret_cast<const Chunk<T> *>(x + t);
-            unsigned allow = 0xFFFFFFFFu;
-            if (mask) {
-                const long long w = t >> 5;
-                const unsigned w0 = __ldg(mask + w);
-                const unsigned w1 = w < mask_last ? __ldg(mask + w + 1) : 0u;
-                allow = __funnelshift_r(w0, w1, static_cast<unsigned>(t) & 31u);
-            }
+    int best_l = 0;
+    Chunk<T> *oc = reinterpret_cast<Chunk<T> *>(out + t0);
+    for (int ch0 = tid; ch0 < c_hi; ch0 += LG_AHEAD * LG_THREADS) {
+        if (ch0 != tid) fetch(ch0);
+#pragma unroll
+        for (int u = 0; u < LG_AHEAD; ++u) {
+            const int ch = ch0 + u * LG_THREADS;
+            if (ch >= c_hi || ch < c_lo) continue;
+            const int l0 = ch * E;
+            const unsigned hit = touched[l0 >> 5] >> (l0 & 31) & ((1u << E) - 1);
             float f[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) f[e] = lg_to_f(in.e[e]);
-            if (hit & ((1u << E) - 1)) {
+            for (int e = 0; e < E; ++e) f[e] = lg_to_f(in[u].e[e]);
+            if (hit) {
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     if (hit >> e & 1) f[e] = rule(f[e], l0 + e);
             }
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (!(allow >> e & 1)) f[e] = NEG;
-                if (f[e] > best) {
-                    best = f[e];
-                    best_t = t + e;
-                }
+            for (int e = 0; e < E; ++e)
+                if (!(allow[u] >> e & 1)) f[e] = NEG;
+            float top = f[0];
+#pragma unroll
+            for (int e = 1; e < E; ++e) top = fmaxf(top, f[e]);  // passes NaN over
+            if (top > best) {
+                best = top;
+                int first = E - 1;
+#pragma unroll
+                for (int e = E - 2; e >= 0; --e) first = f[e] == top ? e : first;
+                best_l = l0 + first;
             }
             if (out) {
+                Chunk<T> o;
 #pragma unroll
-                for (int e = 0; e < E; ++e) lg_from_f(in.e[e], f[e]);
+                for (int e = 0; e < E; ++e) lg_from_f(o.e[e], f[e]);
                 if (out_vec) {
-                    *reinterpret_cast<Chunk<T> *>(out + t) = in;
+                    __stcs(reinterpret_cast<uint4 *>(oc + ch), as_uint4(o));
                 } else {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) out[t + e] = in.e[e];
+                    for (int e = 0; e < E; ++e) out[t0 + l0 + e] = o.e[e];
                 }
-            }
-        } else {
-            for (int e = 0; e < E; ++e) {
-                const long long te = t + e;
-                if (te < 0 || te >= p.vocab) continue;
-                float f = lg_to_f(x[te]);
-                if (hit >> e & 1) f = rule(f, l0 + e);
-                if (mask && !(__ldg(mask + (te >> 5)) >> (te & 31) & 1)) f = NEG;
-                if (f > best) {
-                    best = f;
-                    best_t = te;
-                }
-                if (out) lg_from_f(out[te], f);
             }
         }
     }
+    // the row's ends, a token a thread
+    auto single = [&](int l) {
+        float f = lg_to_f(x[t0 + l]);
+        if (touched[l >> 5] >> (l & 31) & 1) f = rule(f, l);
+        const int bit = bit0 + l;
+        if (mask && !(__ldg(mask + (bit >> 5)) >> (bit & 31) & 1)) f = NEG;
+        if (f > best || (f == best && l < best_l && best > NEG)) {
+            best = f;
+            best_l = l;
+        }
+        if (out) lg_from_f(out[t0 + l], f);
+    };
+    if (c_lo && tid < min(E, tokens) && t0 + tid >= 0) single(tid);
+    if (tokens > 0 && c_hi >= c_lo && tid < tokens - c_hi * E) single(c_hi * E + tid);
     if (!p.idx) return;
 
     // The best of the block, then of the row: a key orders by value, then by
     // the lower token; 0 stands for none.  Maxima do not depend on the order.
     unsigned long long key = 0;
     if (best > NEG)
-        key = static_cast<unsigned long long>(ordered(best + 0.0f)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(best_t));
+        key = static_cast<unsigned long long>(ordered(best + 0.0f)) << 32 | (0xFFFFFFFFu - static_cast<unsigned>(bit0 + best_l));
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
         const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, key, d);

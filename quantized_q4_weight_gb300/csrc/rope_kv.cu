@@ -15,10 +15,10 @@
 // What bounds it: memory for prompts (each element is read and written once,
 // 3 flops per element), launch and load latency for a few tokens.  A block
 // takes one token; a thread keeps one place within the head (four pairs: one
-// or two 16-byte loads) and walks the heads, so that its sines are formed
-// once and its loads of several heads are in flight together.  Few tokens
-// instead spread the heads over blocks, one head a thread: more blocks, the
-// sines repeated.
+// or two 16-byte loads) and walks the heads, with the loads of several heads
+// in flight.  The token's sines are formed once, a thread each, and passed
+// through shared memory while those loads run.  Few tokens spread the heads
+// over blocks, one head a thread: more blocks, the sines repeated.
 #include "decode_ops.h"
 #include "qgemv_internal.cuh"
 
@@ -80,40 +80,40 @@ __device__ __forceinline__ void angle(int pos, unsigned long long turns, float m
     s = sn * mscale;
 }
 
-// Where head h of token t comes from and goes to.
-template <typename TI, typename TQ, typename TC>
-struct HeadRef {
-    const TI *src;
-    TQ *dq;   // q heads
-    TC *dc;   // k and v heads (nullptr: no row)
-    bool rotate;
-    bool live;
-};
-
-template <typename TI, typename TQ, typename TC>
-__device__ __forceinline__ HeadRef<TI, TQ, TC> head_ref(const RopeParams &p, long long t, int h, long long row_off)
+// Head h of token t: the q heads, then k's, then v's.  Where it comes from
+// (nullptr: a k or v head without a cache row), and where it goes.
+template <typename TI>
+__device__ __forceinline__ const TI *head_src(const RopeParams &p, long long t, int h, bool row)
 {
-    HeadRef<TI, TQ, TC> r;
-    r.dq = nullptr;
-    r.dc = nullptr;
-    r.rotate = true;
-    if (h < p.hq) {
-        r.src = static_cast<const TI *>(p.q) + t * p.q_stride + static_cast<long long>(h) * p.d;
-        r.dq = static_cast<TQ *>(p.q_out) + t * p.q_out_stride + static_cast<long long>(h) * p.d;
-        r.live = true;
-    } else if (h < p.hq + p.hkv) {
-        const int g = h - p.hq;
-        r.src = static_cast<const TI *>(p.k) + t * p.k_stride + static_cast<long long>(g) * p.d;
-        r.live = row_off >= 0;
-        if (r.live) r.dc = static_cast<TC *>(p.ck) + row_off + g * p.head_stride;
-    } else {
-        const int g = h - p.hq - p.hkv;
-        r.src = static_cast<const TI *>(p.v) + t * p.v_stride + static_cast<long long>(g) * p.d;
-        r.live = row_off >= 0 && g < p.hkv;
-        r.rotate = false;
-        if (r.live) r.dc = static_cast<TC *>(p.cv) + row_off + g * p.head_stride;
+    if (h < p.hq) return static_cast<const TI *>(p.q) + t * p.q_stride + h * p.d;
+    if (!row) return nullptr;
+    if (h < p.hq + p.hkv) return static_cast<const TI *>(p.k) + t * p.k_stride + (h - p.hq) * p.d;
+    return static_cast<const TI *>(p.v) + t * p.v_stride + (h - p.hq - p.hkv) * p.d;
+}
+template <typename TQ>
+__device__ __forceinline__ TQ *q_dst(const RopeParams &p, long long t, int h)
+{
+    return static_cast<TQ *>(p.q_out) + t * p.q_out_stride + h * p.d;
+}
+template <typename TC>
+__device__ __forceinline__ TC *kv_dst(const RopeParams &p, int h, long long row_off)
+{
+    const int g = h - p.hq;
+    return g < p.hkv ? static_cast<TC *>(p.ck) + row_off + g * p.head_stride
+                     : static_cast<TC *>(p.cv) + row_off + (g - p.hkv) * p.head_stride;
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *at, int a, int b, const float (&x)[4], const float (&y)[4])
+{
+    Four<T> ox, oy;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        ox.e[i] = from_f<T>(x[i]);
+        oy.e[i] = from_f<T>(y[i]);
     }
-    return r;
+    *reinterpret_cast<Four<T> *>(at + a) = ox;
+    *reinterpret_cast<Four<T> *>(at + b) = oy;
 }
 
 // The token's cache row in elements from the cache's base, -1 for none.
@@ -132,8 +132,9 @@ __device__ __forceinline__ long long cache_row(const RopeParams &p, long long t)
 // Eight elements of a head a thread: unit j < rot / 8 is four pairs (HALF:
 // elements 4j.. and rot/2 + 4j..; interleaved: 8j..), later units are copied.
 template <typename TI, typename TQ, typename TC, bool HALF>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_vec_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(ROPE_THREADS, 4) rope_vec_kernel(const __grid_constant__ RopeParams p)
 {
+    __shared__ __align__(16) float s_c[128], s_s[128];
     pdl_launch_dependents();
     const int units = p.d >> 3;
     const int j = static_cast<int>(threadIdx.x) % units, hb = static_cast<int>(threadIdx.x) / units;
@@ -143,41 +144,45 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_vec_kernel(const __grid_con
     const int a = HALF && rot_unit ? 4 * j : 8 * j;                  // first four elements
     const int b = HALF && rot_unit ? p.rot / 2 + 4 * j : 8 * j + 4;  // second four
     pdl_wait();
+    const int pos = __ldg(p.pos + t);
     const long long row_off = cache_row(p, t);
     float c[4], s[4];
     bool have = false;
     const int step = p.heads_per_block * static_cast<int>(gridDim.y);
-    for (int h0 = hb + p.heads_per_block * static_cast<int>(blockIdx.y); h0 < heads; h0 += ROPE_UNROLL * step) {
-        HeadRef<TI, TQ, TC> r[ROPE_UNROLL];
+    // every thread passes the barrier below in its first turn, with heads or without
+    for (int h0 = hb + p.heads_per_block * static_cast<int>(blockIdx.y); h0 < heads || !have; h0 += ROPE_UNROLL * step) {
         Four<TI> x[ROPE_UNROLL], y[ROPE_UNROLL];
 #pragma unroll
         for (int u = 0; u < ROPE_UNROLL; ++u) {
             const int h = h0 + u * step;
-            r[u].live = false;
-            if (h < heads) {
-                r[u] = head_ref<TI, TQ, TC>(p, t, h, row_off);
-                if (r[u].live) {
-                    x[u] = *reinterpret_cast<const Four<TI> *>(r[u].src + a);
-                    y[u] = *reinterpret_cast<const Four<TI> *>(r[u].src + b);
-                }
+            const TI *src = h < heads ? head_src<TI>(p, t, h, row_off >= 0) : nullptr;
+            if (src) {
+                x[u] = *reinterpret_cast<const Four<TI> *>(src + a);
+                y[u] = *reinterpret_cast<const Four<TI> *>(src + b);
             }
         }
-        if (!have && rot_unit) {
-            const int pos = __ldg(p.pos + t);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) angle(pos, p.turns[4 * j + i], p.mscale, c[i], s[i]);
+        if (!have) {
+            for (int i = threadIdx.x; i < p.rot / 2; i += blockDim.x) angle(pos, p.turns[i], p.mscale, s_c[i], s_s[i]);
+            __syncthreads();
+            if (rot_unit) {
+                const float4 cc = *reinterpret_cast<const float4 *>(s_c + 4 * j);
+                const float4 ss = *reinterpret_cast<const float4 *>(s_s + 4 * j);
+                c[0] = cc.x, c[1] = cc.y, c[2] = cc.z, c[3] = cc.w;
+                s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
+            }
             have = true;
         }
 #pragma unroll
         for (int u = 0; u < ROPE_UNROLL; ++u) {
-            if (!r[u].live) continue;
+            const int h = h0 + u * step;
+            if (h >= heads || (h >= p.hq && row_off < 0)) break;  // the heads that follow have no row either
             float fx[4], fy[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 fx[i] = to_f(x[u].e[i]);
                 fy[i] = to_f(y[u].e[i]);
             }
-            if (r[u].rotate && rot_unit) {
+            if (rot_unit && h < p.hq + p.hkv) {
                 if constexpr (HALF) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -197,25 +202,10 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_vec_kernel(const __grid_con
                     }
                 }
             }
-            if (r[u].dq) {
-                Four<TQ> ox, oy;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    ox.e[i] = from_f<TQ>(fx[i]);
-                    oy.e[i] = from_f<TQ>(fy[i]);
-                }
-                *reinterpret_cast<Four<TQ> *>(r[u].dq + a) = ox;
-                *reinterpret_cast<Four<TQ> *>(r[u].dq + b) = oy;
-            } else {
-                Four<TC> ox, oy;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    ox.e[i] = from_f<TC>(fx[i]);
-                    oy.e[i] = from_f<TC>(fy[i]);
-                }
-                *reinterpret_cast<Four<TC> *>(r[u].dc + a) = ox;
-                *reinterpret_cast<Four<TC> *>(r[u].dc + b) = oy;
-            }
+            if (h < p.hq)
+                store8(q_dst<TQ>(p, t, h), a, b, fx, fy);
+            else
+                store8(kv_dst<TC>(p, h, row_off), a, b, fx, fy);
         }
     }
 }
@@ -233,24 +223,26 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_any_kernel(const __grid_con
     const int first = static_cast<int>(blockIdx.y * ROPE_THREADS + threadIdx.x);
     for (int i = first; i < heads * pairs; i += ROPE_THREADS * static_cast<int>(gridDim.y)) {
         const int h = i / pairs, j = i - h * pairs;
-        const HeadRef<TI, TQ, TC> r = head_ref<TI, TQ, TC>(p, t, h, row_off);
-        if (!r.live) continue;
+        const TI *src = head_src<TI>(p, t, h, row_off >= 0);
+        if (!src) continue;
         const bool rot_pair = j < rpairs;
         const int a = HALF && rot_pair ? j : 2 * j, b = HALF && rot_pair ? rpairs + j : 2 * j + 1;
-        float x = to_f(r.src[a]), y = to_f(r.src[b]);
-        if (r.rotate && rot_pair) {
+        float x = to_f(src[a]), y = to_f(src[b]);
+        if (rot_pair && h < p.hq + p.hkv) {
             float c, s;
             angle(pos, p.turns[j], p.mscale, c, s);
             const float px = x, py = y;
             x = px * c - py * s;
             y = px * s + py * c;
         }
-        if (r.dq) {
-            r.dq[a] = from_f<TQ>(x);
-            r.dq[b] = from_f<TQ>(y);
+        if (h < p.hq) {
+            TQ *dst = q_dst<TQ>(p, t, h);
+            dst[a] = from_f<TQ>(x);
+            dst[b] = from_f<TQ>(y);
         } else {
-            r.dc[a] = from_f<TC>(x);
-            r.dc[b] = from_f<TC>(y);
+            TC *dst = kv_dst<TC>(p, h, row_off);
+            dst[a] = from_f<TC>(x);
+            dst[b] = from_f<TC>(y);
         }
     }
 }
