@@ -491,11 +491,12 @@ __global__ void __launch_bounds__(AT_THREADS, DP == 256 ? 1 : 2) attn_part_kerne
         const int rt = id % p.p_tiles;
         id /= p.p_tiles;
         w.head = id % p.hkv;
-        w.slot = id / p.hkv;
+        const int split = id / p.hkv;
+        w.slot = p.p_first + split;
         w.row0 = rt * p.p_tile;
         w.nrows = min(p.p_tile, p.rows - w.row0);
         w.table = p.prefix_pages;
-        w.k0 = w.slot * p.p_keys;
+        w.k0 = p.t_len + split * p.p_keys;
         w.k1 = min(p.prefix_len, w.k0 + p.p_keys);
         tile_rows = p.p_tile;
     } else {
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(AT_THREADS, DP == 256 ? 1 : 2) attn_part_kerne
         w.head = id % p.hkv;
         id /= p.hkv;
         const int b = id % p.n_seqs, chunk = id / p.n_seqs;
-        w.slot = p.p_splits + chunk;
+        w.slot = p.p_first + p.p_splits + chunk;
         const int per = p.n_q * p.group;
         w.row0 = b * per + rt * p.s_tile;
         w.nrows = min(p.s_tile, per - rt * p.s_tile);
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(CB_WARPS * 32) attn_combine_kernel(const __gri
     pdl_wait();
     const int len = suffix_length(p, b);
     const int shared_by_all = max(0, len - p.n_q + 1);
-    const int parts = p.p_splits + (shared_by_all + p.s_keys - 1) / p.s_keys;
+    const int parts = p.p_first + p.p_splits + (shared_by_all + p.s_keys - 1) / p.s_keys;
     if (h == 0 && i == 0 && warp == 0 && lane == 0 && __ldg(p.suffix_len + b) != len) atomicCAS(p.status, 0u, ST_BAD_ID);
     float m = AT_NEG, l = 0.0f, o[E];
 #pragma unroll

@@ -34,14 +34,21 @@
 // K and V tiles share a ring of buffers in the 128-byte-swizzled layout the
 // products read: rows of 64 elements, halves of the head side by side.  K is
 // the K-major operand of S, V the same bytes as the MN-major operand of O.
-// Four producer warps fill the ring with 16-byte cp.async copies, since a
-// page may hold fewer rows than a tile and its rows may have any stride.
+// One warp fills the ring with TMA copies of a page's rows (or of 128 of
+// them), through tensor maps of the cache; a page that is not there is a
+// coordinate past the tensor, which reads as zeros.  The range is whole tiles:
+// what a prefix has beyond them goes to attn_prefix.cu's blocks.  (Filled by
+// four warps with 16-byte cp.async copies the ring cost a third of the
+// instructions of the kernel.)
 //
-// Registers: the launch has 512 threads of 128; the row threads take 168,
-// the other two warp groups 88 each: 256 * 168 + 256 * 88 = 65536.
+// Registers: the launch has 384 threads of 168; the row threads take 208,
+// the other warps 88: 256 * 208 + 128 * 88 = 384 * 168.
 //
 // Every wait is bounded: a block that gives up records QGEMV_ERR_TIMEOUT,
 // waits for its copies and products in flight and frees its tensor memory.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <type_traits>
 
 #include "decode_ops.h"
@@ -51,7 +58,7 @@
 namespace qg {
 namespace {
 
-constexpr int AC_THREADS = 512;   // warps 0-3, 4-7: rows of streams 0, 1; 8-11: producers; 12: products
+constexpr int AC_THREADS = 384;   // warps 0-3, 4-7: rows of streams 0, 1; 8: products; 9: keys and values
 constexpr int AC_KEYS = 128;      // keys of a tile
 constexpr int AC_ROWS = 128;      // rows of a stream
 constexpr int AC_MASKS = 8;       // tiles whose presence masks are kept, per stream: the ring holds fewer
@@ -63,10 +70,9 @@ struct TcCfg {
     static constexpr int HALF = AC_KEYS * 128;            // 64 elements of 128 rows
     static constexpr int TILE = HALF * DP / 64;           // a K or V tile; also 128 rows of Q
     static constexpr int NBUF = DP == 64 ? 8 : 5;
-    static constexpr int LAG = DP == 64 ? 4 : 2;          // buffers in flight behind the one being issued
     static constexpr int OFF_RING = 2 * TILE;
     static constexpr int OFF_BAR = OFF_RING + NBUF * TILE;
-    static constexpr int NBAR = 2 * NBUF + 8;
+    static constexpr int NBAR = 2 * NBUF + 9;
     static constexpr int OFF_MASK = OFF_BAR + 8 * NBAR;   // [stream][AC_MASKS][4] words
     static constexpr int SMEM = (OFF_MASK + 2 * AC_MASKS * 16 + 15) / 16 * 16 + 1024;  // aligned up to 1024 at run time
 };
@@ -150,6 +156,17 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const unsigned *r)
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// A box of the 4-D tensor at (x, row, head, page) into shared memory, counted on `bar`.
+__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, int x, int row, int head, int page,
+                                          uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(row), "r"(head), "r"(page), "r"(smem_addr(bar))
+        : "memory");
+}
+
 __device__ __forceinline__ float ac_ex2(float x)
 {
     float y;
@@ -210,7 +227,7 @@ __device__ __forceinline__ bool ac_wait(uint64_t *bar, unsigned parity, volatile
 
 // A block's work, the same for all roles.
 struct TcWork {
-    int head, k0, k1;
+    int head, k0;
     int tiles;       // key tiles of the range
     int n[2];        // tiles of each stream
     int row0[2];     // first row
@@ -221,7 +238,9 @@ struct TcWork {
 };
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(AC_THREADS, 1)
+    attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap)
 {
     using C = TcCfg<DP>;
     extern __shared__ uint8_t smem_raw[];
@@ -232,7 +251,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *empty = full + C::NBUF;
-    uint64_t *s_full = empty + C::NBUF, *p_full = s_full + 2, *pv_done = p_full + 4;  // [stream]; [stream][half]; [stream]
+    uint64_t *s_full = empty + C::NBUF, *p_full = s_full + 2, *pv_done = p_full + 4,  // [stream]; [stream][half]; [stream]
+             *q_full = pv_done + 2;
     unsigned *masks = reinterpret_cast<unsigned *>(smem + C::OFF_MASK);
     volatile int *abort_flag = &s_abort;
 
@@ -240,7 +260,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_con
         s_abort = 0;
         s_absent = 0;
         for (int i = 0; i < C::NBUF; ++i) {
-            mbar_init(&full[i], 128);
+            mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -249,9 +269,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_con
             mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&pv_done[i], 1);
         }
+        mbar_init(q_full, 2 * AC_ROWS);
         fence_mbar_init();
     }
-    if (warp == 12) {
+    if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)),
                      "r"(512)
                      : "memory");
@@ -271,8 +292,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_con
         const int split = id / p.hkv;
         w.by_keys = p.t_mode == 2;
         w.k0 = split * p.t_keys;
-        w.k1 = min(p.prefix_len, w.k0 + p.t_keys);
-        w.tiles = (w.k1 - w.k0 + AC_KEYS - 1) / AC_KEYS;
+        w.tiles = (min(p.t_len, w.k0 + p.t_keys) - w.k0) / AC_KEYS;
         w.row0[0] = rt * (w.by_keys ? AC_ROWS : 2 * AC_ROWS);
         w.row0[1] = w.row0[0] + (w.by_keys ? 0 : AC_ROWS);
         w.nrows = min(p.rows - w.row0[0], w.by_keys ? AC_ROWS : 2 * AC_ROWS);
@@ -282,176 +302,181 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_con
     if (p.t_wait) pdl_wait();
     pdl_launch_dependents();
 
-    if (warp >= 8 && warp < 12) {
-        // ------------------------------------------------ producers
+    if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        const int pw = warp - 8;
-        const T *kb = static_cast<const T *>(p.k) + static_cast<long long>(w.head) * p.head_stride;
-        const T *vb = static_cast<const T *>(p.v) + static_cast<long long>(w.head) * p.head_stride;
-        // this lane's key of key tile t: its cache row, -1 when absent
-        auto find = [&](int t) -> long long {
-            const int j = w.k0 + t * AC_KEYS + 32 * pw + lane;
-            if (j >= w.k1) return -1;
-            const int page = __ldg(p.prefix_pages + (j >> p.page_shift));
-            if (page < 0 || page >= p.n_pages) {
-                atomicCAS(p.status, 0u, ST_BAD_ID);
-                s_absent = 1;
-                return -1;
+        if (warp == 9) {
+            // ------------------------------------------------ keys and values
+            // A tile is boxes of `box` rows (a page, or the tile), 64 elements wide;
+            // lane i copies box i % boxes of half i / boxes.
+            const int box = min(1 << p.page_shift, AC_KEYS), boxes = AC_KEYS / box;
+            const bool copies = lane < boxes * (DP / 64);
+            const int half = lane / boxes, mine = lane - half * boxes;
+            const uint32_t dst = half * C::HALF + mine * box * 128;
+            // this lane's page of key tile t, n_pages (beyond the tensor: zeros) when it is not there
+            auto find = [&](int t) -> int {
+                const int page = __ldg(p.prefix_pages + ((w.k0 + t * AC_KEYS + (mine & (boxes - 1)) * box) >> p.page_shift));
+                return page >= 0 && page < p.n_pages ? page : static_cast<int>(p.n_pages);
+            };
+            int n = 0;  // buffers issued
+            bool ok = true;
+            auto fill = [&](const CUtensorMap *map, int t, int page) {
+                const int b = n % C::NBUF;
+                if (n >= C::NBUF) ok = ac_wait(&empty[b], static_cast<unsigned>((n / C::NBUF - 1) & 1), abort_flag, p.status);
+                if (!ok) return;
+                if (lane == 0) mbar_arrive_expect_tx(&full[b], C::TILE);
+                __syncwarp();
+                if (copies)
+                    tma_load4(smem_addr(smem + C::OFF_RING) + b * C::TILE + dst, map, 64 * half,
+                              (w.k0 + t * AC_KEYS) & ((1 << p.page_shift) - 1), w.head, page, &full[b]);
+                ++n;
+            };
+            // which keys of a tile are there, for the row threads
+            auto present = [&](int s, int i, int page) {
+                const unsigned there = __ballot_sync(0xFFFFFFFFu, page < p.n_pages);
+                if (there != 0xFFFFFFFFu && lane == 0) {
+                    atomicCAS(p.status, 0u, ST_BAD_ID);
+                    *static_cast<volatile int *>(&s_absent) = 1;
+                }
+                if (lane < 4) {
+                    unsigned bits = 0;
+                    for (int e = 0; e < 32; ++e) bits |= (there >> ((32 * lane + e) / box) & 1u) << e;
+                    masks[(s * AC_MASKS + (i & (AC_MASKS - 1))) * 4 + lane] = bits;
+                }
+                __syncwarp();
+            };
+            const bool two = w.by_keys;  // the streams have keys of their own
+            int cur[2], nxt[2];          // pages of the streams' tiles i and i + 1
+            cur[0] = find(w.tile(0, 0));
+            cur[1] = two && w.n[1] > 0 ? find(w.tile(1, 0)) : 0;
+            present(0, 0, cur[0]);
+            if (!two) present(1, 0, cur[0]);
+            if (two && w.n[1] > 0) present(1, 0, cur[1]);
+            fill(&kmap, w.tile(0, 0), cur[0]);
+            if (two && w.n[1] > 0) fill(&kmap, w.tile(1, 0), cur[1]);
+            nxt[0] = w.n[0] > 1 ? find(w.tile(0, 1)) : 0;
+            nxt[1] = two && w.n[1] > 1 ? find(w.tile(1, 1)) : 0;
+            for (int i = 0; i < w.n[0] && ok; ++i) {
+    #pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (s == 1 && !two) break;
+                    const int after = i + 2 < w.n[s] ? find(w.tile(s, i + 2)) : 0;  // on its way meanwhile
+                    if (i < w.n[s]) fill(&vmap, w.tile(s, i), cur[s]);
+                    if (i + 1 < w.n[s] && ok) {
+                        present(s, i + 1, nxt[s]);
+                        if (!two) present(1, i + 1, nxt[s]);
+                        fill(&kmap, w.tile(s, i + 1), nxt[s]);
+                    }
+                    cur[s] = nxt[s];
+                    nxt[s] = after;
+                }
             }
-            return static_cast<long long>(page) * p.page_stride +
-                   static_cast<long long>(j & ((1 << p.page_shift) - 1)) * p.row_stride;
-        };
-        int n = 0;        // buffers issued
-        bool ok = true;
-        constexpr int CH = DP / 8, RPI = 32 / CH;  // chunks of a row, rows per warp instruction
-        const int c = lane % CH;
-        const bool c_in = c * 8 < p.d;
-        auto arrive = [&](int b) {
-            fence_proxy_async_smem();
-            mbar_arrive(&full[b % C::NBUF]);
-        };
-        auto rows_in = [&](uint32_t dst, const T *base, long long off) {
-#pragma unroll 4
-            for (int i = 0; i < 32 / RPI; ++i) {
-                const int rr = i * RPI + lane / CH;
-                const long long o = __shfl_sync(0xFFFFFFFFu, off, rr);
-                const bool take = o >= 0 && c_in;
-                ac_cp16(dst + ac_off(32 * pw + rr, c), base + (take ? o + c * 8 : 0), take);
+            // After an abort: wait (bounded) for the copies in flight.  A buffer's
+            // earlier fills were complete before it was filled again.
+            if (!ok && lane == 0)
+                for (int b = n > C::NBUF ? n - C::NBUF : 0; b < n; ++b)
+                    mbar_drain(&full[b % C::NBUF], static_cast<unsigned>((b / C::NBUF) & 1));
+            __syncwarp();
+        } else if (warp == 8) {
+            // ------------------------------------------------ products
+            {
+                constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+                constexpr uint32_t IDESC = (1u << 4) | (fmt << 7) | (fmt << 10) | ((128u >> 4) << 24);
+                constexpr uint32_t IDESC_S = IDESC | ((AC_KEYS / 8u) << 17);
+                constexpr uint32_t IDESC_O = IDESC | (1u << 16) | ((DP / 8u) << 17);  // B is MN-major
+                const uint32_t q_s = smem_addr(smem), ring = smem_addr(smem + C::OFF_RING);
+                int pos = 0;
+                bool ok = true;
+                auto acquire = [&]() -> int {  // the next buffer, once it is full
+                    const int b = pos % C::NBUF;
+                    ok = ok && ac_wait(&full[b], static_cast<unsigned>((pos / C::NBUF) & 1), abort_flag, p.status);
+                    tc_fence_after();
+                    ++pos;
+                    return __shfl_sync(0xFFFFFFFFu, b, 0);
+                };
+                auto scores = [&](int s, int b) {
+                    const uint32_t qa = q_s + (w.by_keys ? 0 : s * C::TILE), ka = ring + b * C::TILE;
+    #pragma unroll
+                    for (int hf = 0; hf < DP / 64; ++hf)
+                        tc_mma4_ss(tm + col_s(s), tc_desc(qa + hf * C::HALF, 16), tc_desc(ka + hf * C::HALF, 16), IDESC_S, hf);
+                    tc_commit_elect(&s_full[s]);
+                };
+                auto sums = [&](int s, int i, int b) {
+                    const uint32_t va = ring + b * C::TILE;
+    #pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        ok = ok && ac_wait(&p_full[2 * s + hf], static_cast<unsigned>(i & 1), abort_flag, p.status);
+                        if (!ok) return;
+                        tc_fence_after();
+                        tc_mma4_ts(tm + col_o(s), tm + col_s(s) + 32 * hf, tc_desc(va + hf * AC_KEYS / 2 * 128, C::HALF), IDESC_O,
+                                   i > 0 || hf > 0);
+                    }
+                    if (i == w.n[s] - 1) tc_commit_elect(&pv_done[s]);
+                };
+                int scored[2] = {0, 0}, summed[2] = {0, 0};  // tiles issued per stream, for the drain
+                int kbuf = 0, vbuf = 0;                      // the current buffers
+                // One stream's products of tile i: the sums with its weights, then the
+                // scores of the next tile over the columns that those weights leave.
+                // i = -1: the first scores.
+                auto turn = [&](int s, int i) {
+                    const bool own = w.by_keys || s == 0;                  // takes its buffers itself
+                    const bool last = w.by_keys || s == 1 || w.n[1] == 0;  // and is their last reader
+                    if (i >= 0 && i < w.n[s]) {
+                        if (own) vbuf = acquire();
+                        if (ok) sums(s, i, vbuf);
+                        if (!ok) return;
+                        summed[s] = i + 1;
+                        if (last) tc_commit_elect(&empty[vbuf]);
+                    }
+                    if (i + 1 < w.n[s]) {
+                        if (own) kbuf = acquire();
+                        if (!ok) return;
+                        scores(s, kbuf);
+                        scored[s] = i + 2;
+                        if (last) tc_commit_elect(&empty[kbuf]);
+                    }
+                };
+                ok = ac_wait(q_full, 0, abort_flag, p.status);
+                for (int i = -1; i < w.n[0] && ok; ++i) {
+                    turn(0, i);
+                    if (ok) turn(1, i);
+                }
+                if (!ok && lane == 0) {  // after an abort: wait (bounded) for the products in flight
+                    for (int s = 0; s < 2; ++s) {
+                        if (scored[s]) mbar_drain(&s_full[s], static_cast<unsigned>((scored[s] - 1) & 1));
+                        if (summed[s] && summed[s] == w.n[s]) mbar_drain(&pv_done[s], 0);
+                    }
+                }
             }
-        };
-        auto fill = [&](const T *base, long long off) {
-            const int b = n % C::NBUF;
-            if (n >= C::NBUF && ok)
-                ok = ac_wait(&empty[b], static_cast<unsigned>((n / C::NBUF - 1) & 1), abort_flag, p.status);
-            if (!ok) return;
-            rows_in(smem_addr(smem + C::OFF_RING) + b * C::TILE, base, off);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            if (n >= C::LAG) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(C::LAG) : "memory");
-                arrive(n - C::LAG);
-            }
-            ++n;
-        };
-        auto present = [&](int s, int i, long long off) {
-            const unsigned m = __ballot_sync(0xFFFFFFFFu, off >= 0);
-            if (lane == 0) masks[(s * AC_MASKS + (i & (AC_MASKS - 1))) * 4 + pw] = m;
-        };
-        // Q with the first buffer: rows past the batch are zeros
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (s == 1 && w.by_keys) break;
-            const int r = 32 * pw + lane + (s ? AC_ROWS : 0);
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------ rows
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int s = warp >> 2, wq = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+        const uint32_t to = tm + col_o(s) + lanes;
+        const int r = (w.by_keys ? 0 : s * AC_ROWS) + 32 * wq + lane;  // row of the block
+        // Q: the stream's warps copy its tile, 32 rows each; rows past the batch are zeros
+        if (!(s && w.by_keys)) {
+            constexpr int CH = DP / 8, RPI = 32 / CH;  // chunks of a row, rows per instruction
             long long off = -1;
             if (r < w.nrows) {
                 const int row = w.row0[0] + r, tok = row / p.group, g = row - tok * p.group;
                 off = tok * p.q_token_stride + (static_cast<long long>(w.head) * p.group + g) * p.q_head_stride;
             }
-            rows_in(smem_addr(smem) + s * C::TILE, static_cast<const T *>(p.q), off);
-        }
-        const bool two = w.by_keys;  // the streams have keys of their own
-        long long cur[2], nxt[2];
-        cur[0] = find(w.tile(0, 0));
-        cur[1] = two && w.n[1] > 0 ? find(w.tile(1, 0)) : -1;
-        present(0, 0, cur[0]);
-        if (!two || w.n[1] > 0) present(1, 0, two ? cur[1] : cur[0]);
-        fill(kb, cur[0]);
-        if (two && w.n[1] > 0) fill(kb, cur[1]);
-        for (int i = 0; i < w.n[0] && ok; ++i) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (s == 1 && !two) break;
-                nxt[s] = i + 1 < w.n[s] ? find(w.tile(s, i + 1)) : -1;
-                if (i < w.n[s]) fill(vb, cur[s]);
-                if (i + 1 < w.n[s]) {
-                    present(s, i + 1, nxt[s]);
-                    if (!two) present(1, i + 1, nxt[s]);
-                    fill(kb, nxt[s]);
-                }
-                cur[s] = nxt[s];
+            const int c = lane % CH;
+#pragma unroll 4
+            for (int i = 0; i < 32 / RPI; ++i) {
+                const int rr = i * RPI + lane / CH;
+                const long long o = __shfl_sync(0xFFFFFFFFu, off, rr);
+                const bool take = o >= 0 && c * 8 < p.d;
+                ac_cp16(smem_addr(smem) + s * C::TILE + ac_off(32 * wq + rr, c),
+                        static_cast<const T *>(p.q) + (take ? o + c * 8 : 0), take);
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");  // no copy outlives the role
-        if (ok)
-            for (int b = n > C::LAG ? n - C::LAG : 0; b < n; ++b) arrive(b);
-    } else if (warp >= 12) {
-        // ------------------------------------------------ products
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        if (warp == 12) {
-            constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-            constexpr uint32_t IDESC = (1u << 4) | (fmt << 7) | (fmt << 10) | ((128u >> 4) << 24);
-            constexpr uint32_t IDESC_S = IDESC | ((AC_KEYS / 8u) << 17);
-            constexpr uint32_t IDESC_O = IDESC | (1u << 16) | ((DP / 8u) << 17);  // B is MN-major
-            const uint32_t q_s = smem_addr(smem), ring = smem_addr(smem + C::OFF_RING);
-            int pos = 0;
-            bool ok = true;
-            auto acquire = [&]() -> int {  // the next buffer, once it is full
-                const int b = pos % C::NBUF;
-                ok = ok && ac_wait(&full[b], static_cast<unsigned>((pos / C::NBUF) & 1), abort_flag, p.status);
-                tc_fence_after();
-                ++pos;
-                return __shfl_sync(0xFFFFFFFFu, b, 0);
-            };
-            auto scores = [&](int s, int b) {
-                const uint32_t qa = q_s + (w.by_keys ? 0 : s * C::TILE), ka = ring + b * C::TILE;
-#pragma unroll
-                for (int hf = 0; hf < DP / 64; ++hf)
-                    tc_mma4_ss(tm + col_s(s), tc_desc(qa + hf * C::HALF, 16), tc_desc(ka + hf * C::HALF, 16), IDESC_S, hf);
-                tc_commit_elect(&s_full[s]);
-            };
-            auto sums = [&](int s, int i, int b) {
-                const uint32_t va = ring + b * C::TILE;
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    ok = ok && ac_wait(&p_full[2 * s + hf], static_cast<unsigned>(i & 1), abort_flag, p.status);
-                    if (!ok) return;
-                    tc_fence_after();
-                    tc_mma4_ts(tm + col_o(s), tm + col_s(s) + 32 * hf, tc_desc(va + hf * AC_KEYS / 2 * 128, C::HALF), IDESC_O,
-                               i > 0 || hf > 0);
-                }
-                if (i == w.n[s] - 1) tc_commit_elect(&pv_done[s]);
-            };
-            int scored[2] = {0, 0}, summed[2] = {0, 0};  // tiles issued per stream, for the drain
-            int kbuf = 0, vbuf = 0;                      // the current buffers
-            // One stream's products of tile i: the sums with its weights, then the
-            // scores of the next tile over the columns that those weights leave.
-            // i = -1: the first scores.
-            auto turn = [&](int s, int i) {
-                const bool own = w.by_keys || s == 0;                  // takes its buffers itself
-                const bool last = w.by_keys || s == 1 || w.n[1] == 0;  // and is their last reader
-                if (i >= 0 && i < w.n[s]) {
-                    if (own) vbuf = acquire();
-                    if (ok) sums(s, i, vbuf);
-                    if (!ok) return;
-                    summed[s] = i + 1;
-                    if (last) tc_commit_elect(&empty[vbuf]);
-                }
-                if (i + 1 < w.n[s]) {
-                    if (own) kbuf = acquire();
-                    if (!ok) return;
-                    scores(s, kbuf);
-                    scored[s] = i + 2;
-                    if (last) tc_commit_elect(&empty[kbuf]);
-                }
-            };
-            for (int i = -1; i < w.n[0] && ok; ++i) {
-                turn(0, i);
-                if (ok) turn(1, i);
-            }
-            if (!ok && lane == 0) {  // after an abort: wait (bounded) for the products in flight
-                for (int s = 0; s < 2; ++s) {
-                    if (scored[s]) mbar_drain(&s_full[s], static_cast<unsigned>((scored[s] - 1) & 1));
-                    if (summed[s] && summed[s] == w.n[s]) mbar_drain(&pv_done[s], 0);
-                }
-            }
-        }
-        __syncwarp();
-    } else {
-        // ------------------------------------------------ rows
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-        const int s = warp >> 2, wq = warp & 3;
-        const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-        const uint32_t to = tm + col_o(s) + lanes;
-        const int r = (w.by_keys ? 0 : s * AC_ROWS) + 32 * wq + lane;  // row of the block
+        mbar_arrive(q_full);
         float m = AC_NEG;
         float2 l2 = make_float2(0.0f, 0.0f);
         bool ok = true;
@@ -464,7 +489,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_con
 #pragma unroll
             for (int c = 0; c < AC_KEYS; c += 32) tc_ld32(ts + c, x + c);
             tc_wait_ld();
-            if (w.k0 + (w.tile(s, i) + 1) * AC_KEYS > w.k1 || *static_cast<volatile int *>(&s_absent)) {
+            if (*static_cast<volatile int *>(&s_absent)) {
                 const unsigned *mk = masks + (s * AC_MASKS + (i & (AC_MASKS - 1))) * 4;
 #pragma unroll
                 for (int c = 0; c < AC_KEYS; c += 32) {
@@ -556,28 +581,73 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_tc_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 12)
+    if (warp == 8)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
     // The suffix parts' launch may still be running: this one, which the
     // combining launch waits for, ends after it.
     pdl_wait();
 }
 
+// The driver's encoder of tensor maps, looked up once.
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder()
+{
+    static std::atomic<void *> fn{nullptr};
+    void *f = fn.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+}
+
+// The cache as [page][head][row][element], boxes of up to 128 rows of 64 elements.
+bool encode(CUtensorMap *map, const AttnParams &p, const void *base, qgemv_dtype type)
+{
+    const auto fn = map_encoder();
+    if (!fn) return false;
+    const cuuint32_t rows = 1u << p.page_shift;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.d), rows, static_cast<cuuint64_t>(p.hkv),
+                                static_cast<cuuint64_t>(p.n_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(2 * p.row_stride), static_cast<cuuint64_t>(2 * p.head_stride),
+                                   static_cast<cuuint64_t>(2 * p.page_stride)};
+    const cuuint32_t box[4] = {64, rows < AC_KEYS ? rows : AC_KEYS, 1, 1}, ones[4] = {1, 1, 1, 1};
+    return fn(map, type == QGEMV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+              const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int DP>
-cudaError_t launch_t(const AttnParams &p, cudaStream_t st)
+cudaError_t launch_t(const AttnParams &p, qgemv_dtype type, cudaStream_t st)
 {
     static std::atomic<unsigned long long> done{0};
     const cudaError_t e = allow_smem(reinterpret_cast<const void *>(attn_tc_kernel<T, DP>), TcCfg<DP>::SMEM, done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_tc_kernel<T, DP>, dim3(static_cast<unsigned>(p.t_blocks)), AC_THREADS, TcCfg<DP>::SMEM, st, p);
+    CUtensorMap kmap, vmap;
+    if (!encode(&kmap, p, p.k, type) || !encode(&vmap, p, p.v, type)) return cudaErrorInvalidValue;
+    return launch_pdl(attn_tc_kernel<T, DP>, dim3(static_cast<unsigned>(p.t_blocks)), AC_THREADS, TcCfg<DP>::SMEM, st, p,
+                      kmap, vmap);
 }
+
+// A stride that a tensor map takes: positive, a multiple of 16 bytes, below 2^40.
+inline bool map_stride(long long elements) { return elements > 0 && elements % 8 == 0 && 2 * elements < (1ll << 40); }
 
 }  // namespace
 
+bool attn_tc_takes(const qgemv_kv_cache &c)
+{
+    return c.head_dim <= 128 && c.page_size >= 8 && map_stride(c.row_stride) && map_stride(c.head_stride) &&
+           map_stride(c.page_stride);
+}
+
 cudaError_t launch_attn_tc(const AttnParams &p, qgemv_dtype type, cudaStream_t st)
 {
-    if (type == QGEMV_F16) return p.d <= 64 ? launch_t<__half, 64>(p, st) : launch_t<__half, 128>(p, st);
-    return p.d <= 64 ? launch_t<__nv_bfloat16, 64>(p, st) : launch_t<__nv_bfloat16, 128>(p, st);
+    if (type == QGEMV_F16) return p.d <= 64 ? launch_t<__half, 64>(p, type, st) : launch_t<__half, 128>(p, type, st);
+    return p.d <= 64 ? launch_t<__nv_bfloat16, 64>(p, type, st) : launch_t<__nv_bfloat16, 128>(p, type, st);
 }
 
 }  // namespace qg

@@ -77,7 +77,7 @@ struct AttnPlan {
     int rows, group;
     int p_tile, p_tiles, p_splits, p_keys;
     int s_tile, s_tiles, s_splits, s_keys;
-    int t_mode, t_tiles, t_splits, t_keys;
+    int t_mode, t_tiles, t_splits, t_keys, t_len, p_first;
     long long part_rows;  // partial rows: slots * heads * rows
     long long ws_bytes;
 };
@@ -106,8 +106,6 @@ qgemv_status plan_attn(const qgemv_attn_batch *b, const qgemv_kv_cache *c, AttnP
     a.rows = b->n_seqs * b->n_q * a.group;
     a.p_tile = attn_tile_rows(a.rows, c->head_dim);
     a.p_tiles = static_cast<int>(ceil_div(a.rows, a.p_tile));
-    const long long p_units = ceil_div(b->prefix_len, 64);
-    const long long p_base = static_cast<long long>(c->n_heads) * a.p_tiles;
     // a suffix's rows that all its queries see
     const long long s_most = std::max(0, b->max_suffix - b->n_q + 1);
     const long long s_units = ceil_div(s_most, 64);
@@ -116,18 +114,15 @@ qgemv_status plan_attn(const qgemv_attn_batch *b, const qgemv_kv_cache *c, AttnP
     a.s_tiles = static_cast<int>(ceil_div(per, a.s_tile));
     const long long s_base = static_cast<long long>(b->n_seqs) * c->n_heads * a.s_tiles;
 
-    // ranges of the prefix: enough to fill the slots, of two tiles at least
-    long long splits = std::min(std::max(1ll, ceil_div(p_units, 2)), std::max(1ll, kSlots / p_base));
-    a.p_keys = static_cast<int>(p_units ? ceil_div(p_units, splits) * 64 : 64);
-    a.p_splits = static_cast<int>(ceil_div(b->prefix_len, a.p_keys));
-    // or the tcgen05 kernel for tall batches: one block per multiprocessor,
-    // the split whose last wave ends first (a block costs about two tiles of
-    // 128 keys before and after its own)
-    a.t_mode = a.t_tiles = a.t_splits = a.t_keys = 0;
-    if (a.rows > 64 && c->head_dim <= 128 && b->prefix_len >= 512) {
+    // The tcgen05 kernel for tall batches takes the prefix's whole tiles of 128
+    // keys: one block per multiprocessor, the split whose last wave ends first (a
+    // block costs about two tiles before and after its own).
+    a.t_mode = a.t_tiles = a.t_splits = a.t_keys = a.t_len = a.p_first = 0;
+    if (a.rows > 64 && b->prefix_len >= 512 && attn_tc_takes(*c)) {
         a.t_mode = a.rows <= 128 ? 2 : 1;
         a.t_tiles = static_cast<int>(ceil_div(a.rows, 256));
-        const long long units = ceil_div(b->prefix_len, 128), base = static_cast<long long>(c->n_heads) * a.t_tiles;
+        a.t_len = b->prefix_len / 128 * 128;
+        const long long units = a.t_len / 128, base = static_cast<long long>(c->n_heads) * a.t_tiles;
         const int streams = a.t_mode == 2 ? 2 : 1;
         long long best = 0, best_cost = INT64_MAX;
         for (long long n = 1; n <= units && n <= 512; ++n) {
@@ -136,15 +131,21 @@ qgemv_status plan_attn(const qgemv_attn_batch *b, const qgemv_kv_cache *c, AttnP
             if (cost < best_cost) best_cost = cost, best = n;
         }
         a.t_keys = static_cast<int>(ceil_div(units, best) * 128);
-        a.t_splits = static_cast<int>(ceil_div(b->prefix_len, a.t_keys));
+        a.t_splits = static_cast<int>(ceil_div(a.t_len, a.t_keys));
+        a.p_first = a.t_splits * streams;
         if (base * a.t_splits > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
-        a.p_splits = a.t_splits * streams;  // the parts a row has from the prefix
     }
+    // ranges of the (rest of the) prefix: enough to fill the slots, of two tiles at least
+    const long long rest = b->prefix_len - a.t_len, p_units = ceil_div(rest, 64);
+    const long long p_base = static_cast<long long>(c->n_heads) * a.p_tiles;
+    long long splits = std::min(std::max(1ll, ceil_div(p_units, 2)), std::max(1ll, kSlots / p_base));
+    a.p_keys = static_cast<int>(p_units ? ceil_div(p_units, splits) * 64 : 64);
+    a.p_splits = static_cast<int>(ceil_div(rest, a.p_keys));
     splits = std::min(std::max(1ll, ceil_div(s_units, 2)), std::max(ceil_div(s_units, 16), kSlots / s_base));
     a.s_keys = static_cast<int>(s_units ? ceil_div(s_units, splits) * 64 : 64);
     a.s_splits = static_cast<int>(ceil_div(s_most, a.s_keys));
     if (p_base * a.p_splits + s_base * a.s_splits > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
-    a.part_rows = static_cast<long long>(a.p_splits + a.s_splits) * c->n_heads * a.rows;
+    a.part_rows = static_cast<long long>(a.p_first + a.p_splits + a.s_splits) * c->n_heads * a.rows;
     a.ws_bytes = kCounterArea + a.part_rows * (4ll * c->head_dim + 8);
     return QGEMV_OK;
 }
@@ -378,13 +379,15 @@ qgemv_status qgemv_attn_prefix(const void *q, int64_t q_token_stride, int64_t q_
     p.s_tiles = a.s_tiles;
     p.s_splits = a.s_splits;
     p.s_keys = a.s_keys;
-    p.p_blocks = a.t_mode ? 0 : p.hkv * a.p_tiles * a.p_splits;
+    p.p_first = a.p_first;
+    p.p_blocks = p.hkv * a.p_tiles * a.p_splits;
+    p.t_len = a.t_len;
     p.t_mode = a.t_mode;
     p.t_tiles = a.t_tiles;
     p.t_splits = a.t_splits;
     p.t_keys = a.t_keys;
     p.t_blocks = p.hkv * a.t_tiles * a.t_splits;
-    p.t_wait = a.s_splits == 0;
+    p.t_wait = p.p_blocks == 0 && a.s_splits == 0;
     uint8_t *w = static_cast<uint8_t *>(ws) + kCounterArea;
     p.part_o = reinterpret_cast<float *>(w);
     p.part_ml = reinterpret_cast<float2 *>(w + a.part_rows * 4 * d);

@@ -126,12 +126,14 @@ struct AttnParams {
     // parts: the prefix in p_splits ranges of p_keys keys for row tiles of
     // p_tile rows, every suffix in ranges of s_keys keys for tiles of s_tile
     int p_tile, p_tiles, p_splits, p_keys;
+    int p_first;               // slots before the prefix part's own: the tcgen05 kernel's
     int s_tile, s_tiles, s_splits, s_keys;
     int p_blocks;              // blocks of the prefix part
     // the prefix part on tcgen05 instead (attn_tc.cu; p_blocks is 0 then):
     // mode 1: pairs of 128-row tiles, one slot per split; 2: one row tile,
     // two slots per split; 0: not used
     int t_mode, t_tiles, t_splits, t_keys, t_blocks;
+    int t_len;                 // keys that it takes: whole tiles of the prefix; the blocks above take the rest
     int t_wait;                // no launch of this call precedes it
     float *part_o;             // [slot][hkv][rows][d] sums weighted with 2^(score - m)
     float2 *part_ml;           // [slot][hkv][rows] (m, l)
@@ -142,6 +144,7 @@ struct AttnParams {
 };
 // Rows of a tile for a part with `rows` rows per cache head (attn_prefix.cu).
 int attn_tile_rows(int rows, int d);
+bool attn_tc_takes(const qgemv_kv_cache &c);  // whether a cache's layout suits it
 cudaError_t launch_attn_tc(const AttnParams &p, qgemv_dtype type, cudaStream_t st);
 cudaError_t launch_attn(const AttnParams &p, qgemv_dtype type, qgemv_dtype o_type, cudaStream_t st);
 
