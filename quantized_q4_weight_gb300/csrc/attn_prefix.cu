@@ -383,9 +383,15 @@ struct Block {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
 
-    __device__ __forceinline__ long long out_row(int row) const
+    // Place of a row's (m, l); of its elements 4 c4 .. of the sums.
+    __device__ __forceinline__ long long ml_at(int row) const
     {
         return (static_cast<long long>(w.slot) * p.hkv + w.head) * p.rows + row;
+    }
+    __device__ __forceinline__ float4 *o_at(int row, int c4) const
+    {
+        return p.part_o + (static_cast<long long>(w.slot) * p.hkv + w.head) * p.rows * (p.d >> 2) + row * p.o_row +
+               c4 * p.o_four;
     }
 
     // Tall tiles: warp i has rows 16 i ..
@@ -405,15 +411,12 @@ struct Block {
         for (int hh = 0; hh < 2; ++hh) {
             const int r = 16 * warp + (lane >> 2) + 8 * hh;
             if (r >= w.nrows) continue;
-            const long long row = out_row(w.row0 + r);
-            if ((lane & 3) == 0) p.part_ml[row] = make_float2(a.m[0][hh], a.l[0][hh]);
+            if ((lane & 3) == 0) p.part_ml[ml_at(w.row0 + r)] = make_float2(a.m[0][hh], a.l[0][hh]);
 #pragma unroll
-            for (int n = 0; n < DP / 8; ++n) {
-                const int c = 8 * n + 2 * (lane & 3);
-                if (c < p.d)
-                    *reinterpret_cast<float2 *>(p.part_o + row * p.d + c) =
+            for (int n = 0; n < DP / 8; ++n)
+                if (8 * n < p.d)
+                    reinterpret_cast<float2 *>(o_at(w.row0 + r, 2 * n + ((lane & 2) >> 1)))[lane & 1] =
                         make_float2(a.o[0][n][2 * hh], a.o[0][n][2 * hh + 1]);
-            }
         }
     }
 
@@ -452,7 +455,7 @@ struct Block {
                 for (int u = 0; u < 4; ++u) l += red[u * 32 + r].y * ex2(red[u * 32 + r].x - mx);
                 const float c = ex2(a.m[i][hh] - mx);
                 if (warp == 0 && (lane & 3) == 0 && r < w.nrows)
-                    p.part_ml[out_row(w.row0 + r)] = make_float2(mx, l);
+                    p.part_ml[ml_at(w.row0 + r)] = make_float2(mx, l);
 #pragma unroll
                 for (int n = 0; n < DP / 8; ++n)
                     *reinterpret_cast<float2 *>(acc + (warp * 16 * MT + r) * DP + 8 * n + 2 * (lane & 3)) =
@@ -471,7 +474,7 @@ struct Block {
                 v.z += x.z;
                 v.w += x.w;
             }
-            *reinterpret_cast<float4 *>(p.part_o + out_row(w.row0 + r) * p.d + c) = v;
+            *o_at(w.row0 + r, c >> 2) = v;
         }
     }
 };
@@ -527,146 +530,200 @@ __global__ void __launch_bounds__(AT_THREADS, DP == 256 ? 1 : 2) attn_part_kerne
 
 // ------------------------------------------------------------- combining
 
-__device__ __forceinline__ void put(float *o, float v) { *o = v; }
-__device__ __forceinline__ void put(__half *o, float v) { *o = __float2half_rn(v); }
-__device__ __forceinline__ void put(__nv_bfloat16 *o, float v) { *o = __float2bfloat16_rn(v); }
-__device__ __forceinline__ float get(const __half *v) { return __half2float(*v); }
-__device__ __forceinline__ float get(const __nv_bfloat16 *v) { return __bfloat162float(*v); }
-
-constexpr int CB_WARPS = 8;   // warps of a combining block
-constexpr int CB_BATCH = 4;   // parts whose loads are in flight per warp
-
-// W warps per row, 8 / W rows per block.  A row's warp w takes every W-th
-// part, CB_BATCH of them in flight; a lane has four adjacent elements of each
-// 128 (E in all).  Few rows: the latency of the parts' loads bounds it, so a
-// row has all eight warps.  Many rows: the parts' bytes (from L2) do, and one
-// warp a row saves the merge through shared memory.
-template <typename T, typename TO, int W, int E>
-__global__ void __launch_bounds__(CB_WARPS * 32) attn_combine_kernel(const __grid_constant__ AttnParams p)
+__device__ __forceinline__ void put4(float *o, float4 v)
 {
-    __shared__ float s_o[W > 1 ? W : 1][W > 1 ? 32 * E : 1];
-    __shared__ float2 s_ml[W];
-    pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = W > 1 ? threadIdx.x >> 5 : 0;
-    const int out_row = W > 1 ? blockIdx.x : blockIdx.x * CB_WARPS + (threadIdx.x >> 5);
-    if (out_row >= p.n_seqs * p.n_q * p.hq) return;  // W == 1 only: no barrier follows
-    const int tok = out_row / p.hq, h = out_row - tok * p.hq;
-    const int g = h / p.group, b = tok / p.n_q, i = tok - b * p.n_q;
-    const int row = tok * p.group + (h - g * p.group);
-    pdl_wait();
-    const int len = suffix_length(p, b);
-    const int shared_by_all = max(0, len - p.n_q + 1);
-    const int parts = p.p_first + p.p_splits + (shared_by_all + p.s_keys - 1) / p.s_keys;
-    if (h == 0 && i == 0 && warp == 0 && lane == 0 && __ldg(p.suffix_len + b) != len) atomicCAS(p.status, 0u, ST_BAD_ID);
-    float m = AT_NEG, l = 0.0f, o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    if ((reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+        *reinterpret_cast<float4 *>(o) = v;
+    } else {
+        o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+    }
+}
+template <typename TO>
+__device__ __forceinline__ void put4(TO *o, float4 v)
+{
+    const unsigned a = Mma<TO>::pack(v.x, v.y), b = Mma<TO>::pack(v.z, v.w);
+    if ((reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+        *reinterpret_cast<uint2 *>(o) = make_uint2(a, b);
+    } else {
+        unsigned short *h = reinterpret_cast<unsigned short *>(o);
+        h[0] = static_cast<unsigned short>(a), h[1] = static_cast<unsigned short>(a >> 16);
+        h[2] = static_cast<unsigned short>(b), h[3] = static_cast<unsigned short>(b >> 16);
+    }
+}
 
-    auto add = [&](float mp, float lp, const float (&op)[E]) {
+constexpr int CB_BATCH = 4;   // parts whose loads are in flight per thread
+
+__device__ __forceinline__ float4 get4(const __half *v)
+{
+    const uint2 u = *reinterpret_cast<const uint2 *>(v);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ float4 get4(const __nv_bfloat16 *v)
+{
+    const uint2 u = *reinterpret_cast<const uint2 *>(v);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+// A block combines ROWS rows of a cache head.
+//   ROWS = 1: a warp has 128 elements of the row and every splits-th part,
+//     eight warps in all: for few rows, where the loads' latency bounds it.
+//   ROWS = 8: lane % 8 is the row, a lane has one group of four elements, a
+//     warp 16 elements of the head, the block one warp per 16 elements.  For
+//     many rows, where the parts' bytes (from L2) do: after the tcgen05
+//     kernel, which has a row a thread, the parts lie with the rows innermost,
+//     so that it writes and this reads runs of 128 bytes and more.
+template <typename T, typename TO, int ROWS>
+__global__ void __launch_bounds__(512) attn_combine_kernel(const __grid_constant__ AttnParams p)
+{
+    constexpr int ZONE = 7;            // suffix rows that only the later queries see
+    constexpr int FOURS = 32 / ROWS;   // groups of four elements per warp
+    __shared__ float s_score[ZONE][ROWS];
+    __shared__ long long s_off[ZONE][ROWS];
+    extern __shared__ __align__(16) float4 s_acc[];  // [splits - 1][groups][32] sums, then as many (m, l)
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int groups = ((p.d >> 2) + FOURS - 1) / FOURS, splits = warps / groups;
+    const int cg = warp % groups, part0 = warp / groups;
+    const int g = blockIdx.y, row0 = blockIdx.x * ROWS;
+    const int rl = lane % ROWS, row = row0 + rl, c4 = FOURS * cg + lane / ROWS;
+    const bool live = row < p.rows, mine = live && 4 * c4 < p.d;
+    // the lane's row: token, query of its sequence, query head
+    auto shape = [&](int r, int &tok, int &i, int &h, int &len) {
+        tok = r / p.group;
+        h = g * p.group + r - tok * p.group;
+        const int b = tok / p.n_q;
+        i = tok - b * p.n_q;
+        len = suffix_length(p, b);
+    };
+    pdl_wait();
+    int tok = 0, i = 0, h = 0, len = 0;
+    if (live) shape(row, tok, i, h, len);
+    if (live && h == 0 && i == 0 && warp == 0 && lane < ROWS && __ldg(p.suffix_len + tok / p.n_q) != len)
+        atomicCAS(p.status, 0u, ST_BAD_ID);
+
+    // The rows that not all of a sequence's queries see: a warp per (key, row)
+    // takes the score (a lane finds each of its keys first), the lanes add the
+    // value below.
+    if (p.n_q > 1) {
+        const int count = (p.n_q - 1) * ROWS;
+        long long off = -1, q_at = 0;
+        const int e0 = warp + lane * warps;
+        if (e0 < count && row0 + e0 % ROWS < p.rows) {
+            int rt, ri, rh, rn;
+            shape(row0 + e0 % ROWS, rt, ri, rh, rn);
+            const int j = max(0, rn - p.n_q + 1) + e0 / ROWS;
+            if (j <= rn - p.n_q + ri) off = key_row(p, p.suffix_pages + rt / p.n_q * p.suffix_pages_stride, j);
+            q_at = rt * p.q_token_stride + rh * p.q_head_stride;
+        }
+        for (int n = 0; warp + n * warps < count; n += 4) {
+            float dot[4];
+            long long oo[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                oo[u] = __shfl_sync(0xFFFFFFFFu, off, min(n + u, 31));
+                const long long qq = __shfl_sync(0xFFFFFFFFu, q_at, min(n + u, 31));
+                dot[u] = 0.0f;
+                if (oo[u] >= 0 && n + u < 32) {
+                    const T *q = static_cast<const T *>(p.q) + qq;
+                    const T *k = static_cast<const T *>(p.k) + oo[u] + g * p.head_stride;
+                    for (int c = 4 * lane; c < p.d; c += 128) {
+                        const float4 a = get4(q + c), b = get4(k + c);
+                        dot[u] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, dot[u]))));
+                    }
+                }
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) dot[u] += __shfl_xor_sync(0xFFFFFFFFu, dot[u], d);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int e = warp + (n + u) * warps;
+                if (lane == 0 && e < count) {
+                    s_score[e / ROWS][e % ROWS] = dot[u] * p.scale_log2;
+                    s_off[e / ROWS][e % ROWS] = oo[u];
+                }
+            }
+        }
+        __syncthreads();
+    }
+
+    float m = AT_NEG, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](float mp, float lp, float4 op) {
         const float mn = fmaxf(m, mp), c = ex2(m - mn), cp = ex2(mp - mn);
         m = mn;
         l = l * c + lp * cp;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * c + op[e] * cp;
+        o.x = o.x * c + op.x * cp;
+        o.y = o.y * c + op.y * cp;
+        o.z = o.z * c + op.z * cp;
+        o.w = o.w * c + op.w * cp;
     };
-    // element e of this lane is at lane 4 + 128 (e / 4) + e % 4
-    const long long stride = static_cast<long long>(p.hkv) * p.rows, first = static_cast<long long>(g) * p.rows + row;
-    for (int s0 = warp; s0 < parts; s0 += W * CB_BATCH) {
+    const int shared_by_all = max(0, len - p.n_q + 1);
+    const int parts = live ? p.p_first + p.p_splits + (shared_by_all + p.s_keys - 1) / p.s_keys : 0;
+    const long long ml_stride = static_cast<long long>(p.hkv) * p.rows, ml0 = static_cast<long long>(g) * p.rows + row;
+    const long long o_stride = ml_stride * (p.d >> 2);
+    const long long o0 = static_cast<long long>(g) * p.rows * (p.d >> 2) + row * p.o_row + c4 * p.o_four;
+    const int most = __reduce_max_sync(0xFFFFFFFFu, parts);
+    for (int s0 = part0; s0 < most; s0 += splits * CB_BATCH) {
         float2 ml[CB_BATCH];
-        float op[CB_BATCH][E];
+        float4 op[CB_BATCH];
 #pragma unroll
         for (int u = 0; u < CB_BATCH; ++u) {
-            const int s = s0 + u * W;
+            const int s = s0 + u * splits;
             ml[u] = make_float2(AT_NEG, 0.0f);
-#pragma unroll
-            for (int e = 0; e < E; ++e) op[u][e] = 0.0f;
-            if (s < parts) {
-                const long long at = first + s * stride;
-                ml[u] = p.part_ml[at];
-#pragma unroll
-                for (int e = 0; e < E; e += 4) {
-                    const int c = 4 * lane + 32 * e;
-                    if (c < p.d) {
-                        const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * p.d + c);
-                        op[u][e] = v.x, op[u][e + 1] = v.y, op[u][e + 2] = v.z, op[u][e + 3] = v.w;
-                    }
-                }
+            op[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (s < parts && mine) {
+                ml[u] = p.part_ml[ml0 + s * ml_stride];
+                op[u] = p.part_o[o0 + s * o_stride];
             }
         }
 #pragma unroll
         for (int u = 0; u < CB_BATCH; ++u) add(ml[u].x, ml[u].y, op[u]);
     }
-    // the suffix rows that only the later queries see, one a step
-    const T *q = static_cast<const T *>(p.q) + tok * p.q_token_stride + h * p.q_head_stride;
-    const int32_t *table = p.suffix_pages + b * p.suffix_pages_stride;
-    for (int j = shared_by_all + warp; j <= len - p.n_q + i; j += W) {
-        const long long off = key_row(p, table, j);
-        if (off < 0) continue;
-        const T *k = static_cast<const T *>(p.k) + off + g * p.head_stride;
-        const T *v = static_cast<const T *>(p.v) + off + g * p.head_stride;
-        float dot = 0.0f, op[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int c = 4 * lane + 128 * (e / 4) + e % 4;
-            op[e] = 0.0f;
-            if (c < p.d) {
-                dot = fmaf(get(q + c), get(k + c), dot);
-                op[e] = get(v + c);
-            }
+    if (mine)
+        for (int u = part0; u < p.n_q - 1; u += splits) {
+            const long long off = s_off[u][rl];
+            if (off >= 0)
+                add(s_score[u][rl], 1.0f, get4(static_cast<const T *>(p.v) + off + g * p.head_stride + 4 * c4));
         }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
-        add(dot * p.scale_log2, 1.0f, op);
-    }
-    TO *out = static_cast<TO *>(p.o) + tok * p.o_token_stride + h * p.o_head_stride;
-    float mx = m, total = l;
-    if constexpr (W == 1) {
-        const float inv = 1.0f / total;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int c = 4 * lane + 128 * (e / 4) + e % 4;
-            if (c < p.d) put(out + c, total == 0.0f ? 0.0f : o[e] * inv);
+
+    if (splits > 1) {
+        float2 *s_ml = reinterpret_cast<float2 *>(s_acc + (splits - 1) * groups * 32);  // [splits - 1][groups][32]
+        if (part0 > 0) {
+            s_acc[((part0 - 1) * groups + cg) * 32 + lane] = o;
+            s_ml[((part0 - 1) * groups + cg) * 32 + lane] = make_float2(m, l);
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; e += 4)
-            *reinterpret_cast<float4 *>(&s_o[warp][4 * lane + 32 * e]) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        if (lane == 0) s_ml[warp] = make_float2(m, l);
         __syncthreads();
-        float c[W];
-        mx = s_ml[0].x;
-        total = 0.0f;
-#pragma unroll
-        for (int u = 1; u < W; ++u) mx = fmaxf(mx, s_ml[u].x);
-#pragma unroll
-        for (int u = 0; u < W; ++u) {
-            c[u] = ex2(s_ml[u].x - mx);
-            total += s_ml[u].y * c[u];
-        }
-        const int e = threadIdx.x;
-        if (e < p.d) {
-            float v = 0.0f;
-#pragma unroll
-            for (int u = 0; u < W; ++u) v = fmaf(s_o[u][e], c[u], v);
-            put(out + e, total == 0.0f ? 0.0f : v * (1.0f / total));
+        if (part0 > 0) return;
+        for (int u = 0; u < splits - 1; ++u) {
+            const float2 ml = s_ml[(u * groups + cg) * 32 + lane];
+            add(ml.x, ml.y, s_acc[(u * groups + cg) * 32 + lane]);
         }
     }
-    if (p.lse && warp == 0 && lane == 0)
-        p.lse[static_cast<long long>(tok) * p.hq + h] =
-            total != 0.0f ? (mx + log2f(total)) * 0.6931471805599453f : -INFINITY;
+    if (mine) {
+        TO *out = static_cast<TO *>(p.o) + tok * p.o_token_stride + h * p.o_head_stride + 4 * c4;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        put4(out, l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        if (p.lse && c4 == 0)
+            p.lse[static_cast<long long>(tok) * p.hq + h] = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
 }
 
 template <typename T, typename TO>
 cudaError_t launch_combine(const AttnParams &p, cudaStream_t st)
 {
-    const unsigned rows = static_cast<unsigned>(p.n_seqs * p.n_q * p.hq);
-    // eight warps a row up to four waves of blocks (152 multiprocessors, eight blocks each)
-    if (rows <= 608)
-        return p.d <= 128 ? launch_pdl(attn_combine_kernel<T, TO, 8, 4>, dim3(rows), CB_WARPS * 32, 0, st, p)
-                          : launch_pdl(attn_combine_kernel<T, TO, 8, 8>, dim3(rows), CB_WARPS * 32, 0, st, p);
-    const dim3 grid((rows + CB_WARPS - 1) / CB_WARPS);
-    return p.d <= 128 ? launch_pdl(attn_combine_kernel<T, TO, 1, 4>, grid, CB_WARPS * 32, 0, st, p)
-                      : launch_pdl(attn_combine_kernel<T, TO, 1, 8>, grid, CB_WARPS * 32, 0, st, p);
+    const dim3 rows(static_cast<unsigned>(p.rows), static_cast<unsigned>(p.hkv));
+    if (rows.x * rows.y <= 1024) {  // a row a block: up to seven blocks a multiprocessor
+        const int groups = (p.d + 127) / 128, splits = 8;
+        return launch_pdl(attn_combine_kernel<T, TO, 1>, rows, static_cast<unsigned>(groups * splits * 32),
+                          static_cast<size_t>((splits - 1) * groups * 32) * (sizeof(float4) + sizeof(float2)), st, p);
+    }
+    return launch_pdl(attn_combine_kernel<T, TO, 8>, dim3((rows.x + 7) / 8, rows.y),
+                      static_cast<unsigned>((p.d + 15) / 16 * 32), 0, st, p);
 }
 
 template <typename T, int DP>

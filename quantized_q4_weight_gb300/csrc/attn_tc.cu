@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                 if (lane == 0) mbar_arrive(&p_full[2 * s + hf]);
             }
         }
-        // the part: row by row, 16 bytes a lane
+        // the part: a row a lane, 16 bytes each
         const bool have = w.n[s] > 0;
         if (have && ok) {
             ok = ac_wait(&pv_done[s], 0, abort_flag, p.status);
@@ -557,9 +557,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         const int split = blockIdx.x / (p.t_tiles * p.hkv);
         const int slot = w.by_keys ? 2 * split + s : split;
         const bool mine = r < w.nrows;
-        const long long at = (static_cast<long long>(slot) * p.hkv + w.head) * p.rows + w.row0[0] + r;
+        const long long slab = static_cast<long long>(slot) * p.hkv + w.head;
+        const int row = w.row0[0] + r;
         if (ok && (have || w.by_keys)) {  // a stream without keys leaves an empty part
-            if (mine) p.part_ml[at] = make_float2(have ? m : AC_NEG, l2.x + l2.y);
+            if (mine) p.part_ml[slab * p.rows + row] = make_float2(have ? m : AC_NEG, l2.x + l2.y);
 #pragma unroll
             for (int c = 0; c < DP; c += 32) {
                 float o[32];
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                     if (mine && c + e < p.d)
-                        *reinterpret_cast<float4 *>(p.part_o + at * p.d + c + e) =
+                        p.part_o[(slab * (p.d >> 2) + ((c + e) >> 2)) * p.rows + row] =
                             make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
         }

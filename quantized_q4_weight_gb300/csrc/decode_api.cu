@@ -116,7 +116,8 @@ qgemv_status plan_attn(const qgemv_attn_batch *b, const qgemv_kv_cache *c, AttnP
 
     // The tcgen05 kernel for tall batches takes the prefix's whole tiles of 128
     // keys: one block per multiprocessor, the split whose last wave ends first (a
-    // block costs about two tiles before and after its own).
+    // block costs about two tiles before and after its own, and a part of 8192
+    // rows, written and read again, about one).
     a.t_mode = a.t_tiles = a.t_splits = a.t_keys = a.t_len = a.p_first = 0;
     if (a.rows > 64 && b->prefix_len >= 512 && attn_tc_takes(*c)) {
         a.t_mode = a.rows <= 128 ? 2 : 1;
@@ -126,8 +127,9 @@ qgemv_status plan_attn(const qgemv_attn_batch *b, const qgemv_kv_cache *c, AttnP
         const int streams = a.t_mode == 2 ? 2 : 1;
         long long best = 0, best_cost = INT64_MAX;
         for (long long n = 1; n <= units && n <= 512; ++n) {
-            const long long each = ceil_div(units, n);
-            const long long cost = ceil_div(base * ceil_div(units, each), 152) * (ceil_div(each, streams) + 2);
+            const long long each = ceil_div(units, n), ranges = ceil_div(units, each);
+            const long long cost = ceil_div(base * ranges, 152) * (ceil_div(each, streams) + 2) * 8192 +
+                                   ranges * streams * a.rows * c->n_heads;
             if (cost < best_cost) best_cost = cost, best = n;
         }
         a.t_keys = static_cast<int>(ceil_div(units, best) * 128);
@@ -389,7 +391,9 @@ qgemv_status qgemv_attn_prefix(const void *q, int64_t q_token_stride, int64_t q_
     p.t_blocks = p.hkv * a.t_tiles * a.t_splits;
     p.t_wait = p.p_blocks == 0 && a.s_splits == 0;
     uint8_t *w = static_cast<uint8_t *>(ws) + kCounterArea;
-    p.part_o = reinterpret_cast<float *>(w);
+    p.part_o = reinterpret_cast<float4 *>(w);
+    p.o_row = a.t_mode ? 1 : d / 4;
+    p.o_four = a.t_mode ? a.rows : 1;
     p.part_ml = reinterpret_cast<float2 *>(w + a.part_rows * 4 * d);
     p.o = o;
     p.o_token_stride = o_token_stride;
