@@ -576,7 +576,7 @@ __device__ __forceinline__ float4 get4(const __nv_bfloat16 *v)
 //     kernel, which has a row a thread, the parts lie with the rows innermost,
 //     so that it writes and this reads runs of 128 bytes and more.
 template <typename T, typename TO, int ROWS>
-__global__ void __launch_bounds__(512) attn_combine_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(1024) attn_combine_kernel(const __grid_constant__ AttnParams p)
 {
     constexpr int ZONE = 7;            // suffix rows that only the later queries see
     constexpr int FOURS = 32 / ROWS;   // groups of four elements per warp
@@ -716,14 +716,19 @@ __global__ void __launch_bounds__(512) attn_combine_kernel(const __grid_constant
 template <typename T, typename TO>
 cudaError_t launch_combine(const AttnParams &p, cudaStream_t st)
 {
-    const dim3 rows(static_cast<unsigned>(p.rows), static_cast<unsigned>(p.hkv));
-    if (rows.x * rows.y <= 1024) {  // a row a block: up to seven blocks a multiprocessor
-        const int groups = (p.d + 127) / 128, splits = 8;
-        return launch_pdl(attn_combine_kernel<T, TO, 1>, rows, static_cast<unsigned>(groups * splits * 32),
-                          static_cast<size_t>((splits - 1) * groups * 32) * (sizeof(float4) + sizeof(float2)), st, p);
-    }
-    return launch_pdl(attn_combine_kernel<T, TO, 8>, dim3((rows.x + 7) / 8, rows.y),
-                      static_cast<unsigned>((p.d + 15) / 16 * 32), 0, st, p);
+    const unsigned rows = static_cast<unsigned>(p.rows), heads = static_cast<unsigned>(p.hkv);
+    // a row a block up to seven blocks a multiprocessor, unless the rows are innermost
+    const bool one = p.o_four == 1 && rows * heads <= 1024;
+    const int groups = one ? (p.d + 127) / 128 : (p.d + 15) / 16;
+    const dim3 grid(one ? rows : (rows + 7) / 8, heads);
+    // warps that share a row's parts: as many as fill the multiprocessors about once
+    const unsigned blocks = grid.x * grid.y;
+    int splits = one ? 8 : blocks <= 152 ? 4 : blocks <= 304 ? 2 : 1;
+    while (splits > 1 && groups * splits > 32) splits /= 2;
+    const unsigned threads = static_cast<unsigned>(groups * splits * 32);
+    const size_t smem = static_cast<size_t>((splits - 1) * groups * 32) * (sizeof(float4) + sizeof(float2));
+    return one ? launch_pdl(attn_combine_kernel<T, TO, 1>, grid, threads, smem, st, p)
+               : launch_pdl(attn_combine_kernel<T, TO, 8>, grid, threads, smem, st, p);
 }
 
 template <typename T, int DP>

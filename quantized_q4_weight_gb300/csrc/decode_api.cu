@@ -137,13 +137,13 @@ qgemv_status plan_attn(const qgemv_attn_batch *b, const qgemv_kv_cache *c, AttnP
         a.p_first = a.t_splits * streams;
         if (base * a.t_splits > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
     }
-    // ranges of the (rest of the) prefix: enough to fill the slots, of two tiles at least
+    // ranges of the (rest of the) prefix: enough to fill the slots
     const long long rest = b->prefix_len - a.t_len, p_units = ceil_div(rest, 64);
     const long long p_base = static_cast<long long>(c->n_heads) * a.p_tiles;
-    long long splits = std::min(std::max(1ll, ceil_div(p_units, 2)), std::max(1ll, kSlots / p_base));
+    long long splits = std::min(std::max(1ll, p_units), std::max(1ll, kSlots / p_base));
     a.p_keys = static_cast<int>(p_units ? ceil_div(p_units, splits) * 64 : 64);
     a.p_splits = static_cast<int>(ceil_div(rest, a.p_keys));
-    splits = std::min(std::max(1ll, ceil_div(s_units, 2)), std::max(ceil_div(s_units, 16), kSlots / s_base));
+    splits = std::min(std::max(1ll, s_units), std::max(ceil_div(s_units, 16), kSlots / s_base));
     a.s_keys = static_cast<int>(s_units ? ceil_div(s_units, splits) * 64 : 64);
     a.s_splits = static_cast<int>(ceil_div(s_most, a.s_keys));
     if (p_base * a.p_splits + s_base * a.s_splits > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
