@@ -482,15 +482,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         float m = AC_NEG;
         float2 l2 = make_float2(0.0f, 0.0f);
         bool ok = true;
-        // Turn -1 runs the loop's instructions before the first scores are there
-        // (on whatever the columns hold, leaving nothing): fetched cold, they
-        // made the first tile two to five times as long as the others.
-        for (int i = -1; i < w.n[s] && ok; ++i) {
-            if (i >= 0) {
-                ok = ac_wait(&s_full[s], static_cast<unsigned>(i & 1), abort_flag, p.status);
-                if (!ok) break;
-                tc_fence_after();
-            }
+        for (int i = 0; i < w.n[s] && ok; ++i) {
+            ok = ac_wait(&s_full[s], static_cast<unsigned>(i & 1), abort_flag, p.status);
+            if (!ok) break;
+            tc_fence_after();
             const uint32_t ts = tm + col_s(s) + lanes;
             float x[AC_KEYS];
 #pragma unroll
@@ -514,9 +509,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mm[e] = fmaxf(mm[e], fmaxf(x[c + 2 * e], x[c + 2 * e + 1]));
             const float mx = fmaxf(fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * p.scale_log2, AC_NEG);
-            if (i <= 0) {
+            if (i == 0) {
                 m = mx;
-                l2 = make_float2(0.0f, 0.0f);
             } else {
                 const bool rise = mx > m + AC_RISE;
                 if (__any_sync(0xFFFFFFFFu, rise)) {
@@ -549,13 +543,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                     l2 = add2(l2, e);
                     pk[c / 2] = pack2<T>(e.x, e.y);
                 }
-                if (i >= 0) {
-                    tc_st32(ts + 32 * hf, pk);
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[2 * s + hf]);
-                }
+                tc_st32(ts + 32 * hf, pk);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * s + hf]);
             }
         }
         // the part: a row a lane, 16 bytes each

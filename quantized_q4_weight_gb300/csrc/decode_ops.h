@@ -137,7 +137,7 @@ struct AttnParams {
     int t_wait;                // no launch of this call precedes it
     float4 *part_o;            // [slot][hkv] sums weighted with 2^(score - m), a row's elements 4 c .. at
                                //   row * o_row + c * o_four: rows innermost after the tcgen05 kernel, else outermost
-    int o_row, o_four;
+    long long o_row, o_four;
     float2 *part_ml;           // [slot][hkv][rows] (m, l)
     void *o;
     long long o_token_stride, o_head_stride;

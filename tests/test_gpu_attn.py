@@ -290,3 +290,109 @@ def test_four_dimensional_views():
         want, _ = c.check()
         got = q.attn_prefix(c.q.unflatten(0, (b, nq)), c.batch, c.ws)
         assert torch.equal(got.view(want.shape), want)
+
+
+def test_a_captured_step_follows_its_lengths():
+    """Rotary positions with the cache write and the attention in a CUDA graph,
+    replayed as the device's lengths, slots and positions move on."""
+    c = Case(3, 1, 6, 2, 64, 200, [1, 2, 3], max_suffix=40, poison=False, seed=20)
+    plan = q.rope_plan(64, 1e4)
+    x = torch.randn((3, (6 + 4) * 64), device=DEV)
+    parts = (x[:, :384].unflatten(1, (6, 64)), x[:, 384:512].unflatten(1, (2, 64)), x[:, 512:].unflatten(1, (2, 64)))
+    pos = torch.zeros(3, dtype=torch.int32, device=DEV)
+    slots = torch.zeros(3, dtype=torch.int32, device=DEV)
+    rq, out = torch.empty((3, 6, 64), dtype=torch.bfloat16, device=DEV), torch.empty((3, 6, 64), dtype=torch.bfloat16, device=DEV)
+
+    def step():
+        q.rope_kv(plan, *parts, pos, slots, c.cache, out=rq)
+        q.attn_prefix(rq, c.batch, c.ws, out=out)
+
+    def place():
+        j = (c.len_t - 1).long()
+        slots.copy_(c.suffix_pages[torch.arange(3, device=DEV), j // 16] * 16 + (j % 16).int())
+        pos.copy_(200 + j.int())
+
+    place()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for n in range(4):
+        c.len_t += 1
+        x.normal_()
+        place()
+        g.replay()
+        got = out.clone()
+        step()
+        assert torch.equal(out, got)
+        c.lens = c.len_t.tolist()
+        c.q = rq
+        ref, A, _, e = c.exact()
+        assert bool(((got.double().view(ref.shape) - ref).abs() <= (2.0 ** -8 + 2 * e + 2.0 ** -11) * A + 2.0 ** -8 * ref.abs()).all())
+    assert q.device_status() == 0
+
+
+# Many rows over a long prefix: six tiles of 64 rows and keys per slot of 304, the tcgen05 kernel.
+@pytest.mark.parametrize("b,nq,hq,hkv,d,prefix,page,heads_first,dtype", [
+    (12, 4, 16, 2, 128, 13000, 16, False, torch.bfloat16),     # 384 rows a head: a pair of tiles, and one and its absent half
+    (9, 4, 16, 2, 128, 24064, 64, True, torch.float16),        # 288: the second tile of a pair part full; whole tiles of keys
+    (10, 1, 56, 8, 128, 7700, 8, False, torch.bfloat16),       # 70: one row tile, its streams over alternate keys
+    (16, 1, 64, 8, 64, 7425, 32, False, torch.float16),        # 128: the same, full, heads of 64
+    (20, 2, 10, 2, 96, 15001, 256, False, torch.bfloat16),     # 200 rows, heads of 96
+    (33, 8, 4, 1, 40, 23700, 128, True, torch.float16),        # 1056 rows, heads of 40
+])
+def test_tall_batches_over_long_prefixes(b, nq, hq, hkv, d, prefix, page, heads_first, dtype):
+    c = Case(b, nq, hq, hkv, d, prefix, [nq + (7 * i) % 90 for i in range(b)], page=page, dtype=dtype,
+             heads_first=heads_first, seed=b + d)
+    c.check()
+    first = c.run().clone()
+    for _ in range(3):
+        assert torch.equal(c.run(), first)
+
+
+def test_tall_batches_with_sharp_scores():
+    """Maxima that rise by far more than 2^8 from tile to tile: the sums are rescaled."""
+    c = Case(12, 4, 16, 2, 128, 13000, [4] * 12, page=64, dtype=torch.bfloat16, spread=20.0, seed=31)
+    c.check()
+    c = Case(12, 4, 16, 2, 128, 13000, [4] * 12, page=64, dtype=torch.float16, seed=32)
+    for j in (5000, 9999, 12900):
+        c.k[c.prefix_pages.long()[j // 64], j % 64] *= 1 + j / 3000
+    c.check()
+
+
+def test_tall_batches_with_absent_pages():
+    b, prefix, page = 12, 13000, 16
+    c = Case(b, 4, 16, 2, 128, prefix, [4] * b, page=page, seed=33)
+    keep = c.prefix_pages.clone()
+    gone = [0, 17, 400, 811]
+    c.prefix_pages[gone] = torch.tensor([-1, c.cache.struct.n_pages, 2 ** 31 - 1, -7], dtype=torch.int32, device=DEV)
+    out = c.run()
+    torch.cuda.synchronize()
+    assert q.device_status() == 7
+    rest = torch.cat([keep[[i for i in range(prefix // page) if i not in gone]], keep[-1:]])
+    c.prefix_pages.copy_(keep)
+    c.prefix_pages, c.prefix = rest, prefix - page * len(gone)
+    ref, A, _, e = c.exact()
+    got = out.double().view(ref.shape)
+    assert bool(((got - ref).abs() <= (2.0 ** -8 + 2 * e + 2.0 ** -11) * A + 2.0 ** -8 * ref.abs()).all())
+
+
+def test_tall_batches_without_suffixes_and_after_other_work():
+    """No suffix part precedes the prefix kernel, and what it reads was written just before."""
+    c = Case(40, 1, 64, 8, 128, 8000, [0] * 40, page=32, max_suffix=0, seed=34)
+    c.check()
+    src = [x.clone() for x in (c.k, c.v)]
+    for i in range(5):
+        c.k.zero_()
+        c.v.zero_()
+        big = torch.empty(1 << 28, device=DEV).zero_()
+        c.k.copy_(src[0])
+        c.v.copy_(src[1])
+        out = c.run()
+    assert torch.equal(out, c.run())
+    c.check()
+    del big

@@ -201,3 +201,26 @@ def test_lengths_outside_their_bounds_are_recorded():
         gi, gv = call(x, e)
         assert q.device_status() == 7
         assert np.array_equal(gi.cpu().numpy(), idx) and np.array_equal(gv.cpu().numpy(), val)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,V,hist,bias", [(64, 120007, 600, 30), (300, 50257, 3000, 200), (40, 151936, 0, 0),
+                                           (90, 70001, 9000, 64), (60, 99999, 20000, 4000), (1024, 8191, 33, 5)])
+def test_many_rows_in_ranges(R, V, hist, bias, dtype):
+    """Enough tokens for the blocks to take ranges that cross rows, lists of every size class."""
+    x, d = make(R, V, hist, bias, dtype, R + V)
+    check(x, d)
+
+
+def test_many_rows_in_place_and_strided():
+    x, d = make(100, 60001, 100, 9, torch.float16, 77)
+    want, idx, _ = reference(x.float().numpy(), **d)
+    xd = x.to(DEV)
+    gi, _ = call(x, d, out=xd, xd=xd)
+    assert torch.equal(xd.cpu(), torch.from_numpy(want).half()) and np.array_equal(gi.cpu().numpy(), idx)
+    wide = torch.full((100, 60021), 5.0, dtype=torch.float16, device=DEV)
+    wide[:, 5:60006] = x.to(DEV)
+    outw = torch.full((100, 60100), 6.0, dtype=torch.float16, device=DEV)
+    gi, _ = call(x, d, out=outw[:, 6:60007], xd=wide[:, 5:60006])
+    assert torch.equal(outw[:, 6:60007].cpu(), torch.from_numpy(want).half()) and np.array_equal(gi.cpu().numpy(), idx)
+    assert torch.all(outw[:, :6] == 6) and torch.all(outw[:, 60007:] == 6)
