@@ -10,7 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -84,6 +84,23 @@ int64_t heads(const at::Tensor &t, const char *what)
     return t.stride(0);
 }
 
+// A new contiguous tensor beside another (without a way through the
+// dispatcher: it is a third of a call).
+at::Tensor beside(const at::Tensor &t, at::IntArrayRef sizes, at::ScalarType type)
+{
+    return at::detail::empty_cuda(sizes, type, t.device(), std::nullopt);
+}
+
+// The same for a part of another tensor's memory, from `offset` elements of `type` on.
+at::Tensor part_of(const at::Tensor &whole, at::ScalarType type, int64_t n, int64_t offset)
+{
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
+                                                            c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    t.unsafeGetTensorImpl()->set_storage_offset(offset);
+    return t;
+}
+
 template <typename F>
 PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F f) noexcept
 {
@@ -130,7 +147,7 @@ PyObject *rope_kv(PyObject *, PyObject *const *a, Py_ssize_t n) noexcept
         if (q) {
             qs = heads(*q, "rope_kv: q [tokens][heads][head_dim] with adjacent heads");
             if (!out) {
-                made = at::empty(q->sizes(), q->options().dtype(cache ? scalar_of(cache->type) : q->scalar_type()));
+                made = beside(*q, q->sizes(), cache ? scalar_of(cache->type) : q->scalar_type());
                 out = &made;
             }
             need(out->sizes() == q->sizes(), "rope_kv: out of q's shape");
@@ -182,7 +199,7 @@ PyObject *attn_prefix(PyObject *, PyObject *const *a, Py_ssize_t n) noexcept
         token_strides(*q, *batch, cache->head_dim, qt, qh);
         at::Tensor made;
         if (!out) {
-            made = at::empty(q->sizes(), q->options());
+            made = beside(*q, q->sizes(), q->scalar_type());
             out = &made;
         }
         token_strides(*out, *batch, cache->head_dim, ot, oh);
@@ -214,14 +231,18 @@ PyObject *logits_rules(PyObject *, PyObject *const *a, Py_ssize_t n) noexcept
             need(out->sizes() == x->sizes() && out->stride(1) == 1 && out->scalar_type() == x->scalar_type(),
                  "logits_rules: out of x's shape and type");
         at::Tensor made_idx, made_val;
-        if (!idx) {
-            made_idx = at::empty({spec->rows}, x->options().dtype(at::kLong));
-            idx = &made_idx;
+        if (!idx && !val) {  // one allocation for both
+            const int64_t rows = spec->rows;
+            const at::Tensor both = beside(*x, {rows + (rows + 1) / 2}, at::kLong);
+            made_idx = part_of(both, at::kLong, rows, 0);
+            made_val = part_of(both, at::kFloat, rows, 2 * rows);
+        } else if (!idx) {
+            made_idx = beside(*x, {spec->rows}, at::kLong);
+        } else if (!val) {
+            made_val = beside(*x, {spec->rows}, at::kFloat);
         }
-        if (!val) {
-            made_val = at::empty({spec->rows}, x->options().dtype(at::kFloat));
-            val = &made_val;
-        }
+        if (!idx) idx = &made_idx;
+        if (!val) val = &made_val;
         need(idx->scalar_type() == at::kLong && idx->is_contiguous() && idx->numel() == spec->rows &&
                  val->scalar_type() == at::kFloat && val->is_contiguous() && val->numel() == spec->rows,
              "logits_rules: idx int64 and val fp32 [rows]");

@@ -224,3 +224,20 @@ def test_many_rows_in_place_and_strided():
     gi, _ = call(x, d, out=outw[:, 6:60007], xd=wide[:, 5:60006])
     assert torch.equal(outw[:, 6:60007].cpu(), torch.from_numpy(want).half()) and np.array_equal(gi.cpu().numpy(), idx)
     assert torch.all(outw[:, :6] == 6) and torch.all(outw[:, 60007:] == 6)
+
+
+def test_results_made_by_the_call_are_tensors_of_their_own_kind():
+    x, d = make(3, 500, 10, 2, torch.float32, 9)
+    gi, gv = call(x, d)
+    idx, val = torch.empty(3, dtype=torch.int64, device=DEV), torch.empty(3, device=DEV)
+    t = {k: (None if v is None else torch.from_numpy(v).to(DEV)) for k, v in d.items()}
+    rules = q.LogitsRules(3, 500, history=t["hist"], history_len=t["hist_len"], repetition=t["rep"], frequency=t["freq"],
+                          presence=t["pres"], bias_ids=t["bias_ids"], bias=t["bias"], bias_len=t["bias_len"], mask=t["mask"])
+    ws = q.new_workspace(rules.workspace_bytes())
+    for kw in (dict(idx=idx), dict(val=val), dict(idx=idx, val=val)):
+        a, b = q.logits_rules(x.to(DEV), rules, ws, **kw)
+        assert torch.equal(a, gi) and torch.equal(b, gv)
+        assert ("idx" not in kw or a is idx) and ("val" not in kw or b is val)
+    assert gi.dtype == torch.int64 and gv.dtype == torch.float32 and gi.shape == gv.shape == (3,) and gi.is_contiguous()
+    assert torch.equal(gi + 1 - 1, gi) and (gv * 2).shape == (3,) and gi.cpu().tolist() == gi.tolist()
+    assert gi.device == x.to(DEV).device and not gv.requires_grad
