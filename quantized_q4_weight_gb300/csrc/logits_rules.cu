@@ -275,10 +275,14 @@ __global__ void __launch_bounds__(LG_THREADS, 6) logits_kernel(const __grid_cons
         float f[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) f[e] = lg_to_f(in.e[e]);
-        if (hit) {
+        for (unsigned rest = hit; rest; rest &= rest - 1) {  // one at a time: the rule's code once
+            const int at = __ffs(rest) - 1;
+            float v = f[0];
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (hit >> e & 1) f[e] = rule(f[e], l0 + e);
+            for (int e = 1; e < E; ++e) v = e == at ? f[e] : v;
+            v = rule(v, l0 + at);
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[e] = e == at ? v : f[e];
         }
 #pragma unroll
         for (int e = 0; e < E; ++e)

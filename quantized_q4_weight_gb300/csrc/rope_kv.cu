@@ -25,8 +25,8 @@
 namespace qg {
 namespace {
 
-constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_UNROLL = 4;  // heads in flight per thread
+constexpr int ROPE_THREADS = 128;
+constexpr int ROPE_UNROLL = 3;  // heads in flight per thread
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v);
@@ -132,7 +132,7 @@ __device__ __forceinline__ long long cache_row(const RopeParams &p, long long t)
 // Eight elements of a head a thread: unit j < rot / 8 is four pairs (HALF:
 // elements 4j.. and rot/2 + 4j..; interleaved: 8j..), later units are copied.
 template <typename TI, typename TQ, typename TC, bool HALF>
-__global__ void __launch_bounds__(ROPE_THREADS, 4) rope_vec_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(ROPE_THREADS, 8) rope_vec_kernel(const __grid_constant__ RopeParams p)
 {
     __shared__ __align__(16) float s_c[128], s_s[128];
     pdl_launch_dependents();
