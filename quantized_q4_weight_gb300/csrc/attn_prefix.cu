@@ -576,7 +576,7 @@ __device__ __forceinline__ float4 get4(const __nv_bfloat16 *v)
 //     kernel, which has a row a thread, the parts lie with the rows innermost,
 //     so that it writes and this reads runs of 128 bytes and more.
 template <typename T, typename TO, int ROWS>
-__global__ void __launch_bounds__(1024) attn_combine_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(ROWS == 1 ? 512 : 1024) attn_combine_kernel(const __grid_constant__ AttnParams p)
 {
     constexpr int ZONE = 7;            // suffix rows that only the later queries see
     constexpr int FOURS = 32 / ROWS;   // groups of four elements per warp
@@ -603,6 +603,30 @@ __global__ void __launch_bounds__(1024) attn_combine_kernel(const __grid_constan
     if (live) shape(row, tok, i, h, len);
     if (live && h == 0 && i == 0 && warp == 0 && lane < ROWS && __ldg(p.suffix_len + tok / p.n_q) != len)
         atomicCAS(p.status, 0u, ST_BAD_ID);
+
+    const int shared_by_all = max(0, len - p.n_q + 1);
+    const int parts = live ? p.p_first + p.p_splits + (shared_by_all + p.s_keys - 1) / p.s_keys : 0;
+    const long long ml_stride = static_cast<long long>(p.hkv) * p.rows, ml0 = static_cast<long long>(g) * p.rows + row;
+    const long long o_stride = ml_stride * (p.d >> 2);
+    const long long o0 = static_cast<long long>(g) * p.rows * (p.d >> 2) + row * p.o_row + c4 * p.o_four;
+    const int most = __reduce_max_sync(0xFFFFFFFFu, parts);
+    float2 ml[CB_BATCH];
+    float4 op[CB_BATCH];
+    auto fetch = [&](int s0) {
+#pragma unroll
+        for (int u = 0; u < CB_BATCH; ++u) {
+            const int s = s0 + u * splits;
+            ml[u] = make_float2(AT_NEG, 0.0f);
+            op[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (s < parts && mine) {
+                ml[u] = p.part_ml[ml0 + s * ml_stride];
+                op[u] = p.part_o[o0 + s * o_stride];
+            }
+        }
+    };
+    // Few rows: on their way during what follows.  (With eight rows a block the
+    // registers that this takes spill, which costs more.)
+    if (ROWS == 1) fetch(part0);
 
     // The rows that not all of a sequence's queries see: a warp per (key, row)
     // takes the score (a lane finds each of its keys first), the lanes add the
@@ -662,25 +686,8 @@ __global__ void __launch_bounds__(1024) attn_combine_kernel(const __grid_constan
         o.z = o.z * c + op.z * cp;
         o.w = o.w * c + op.w * cp;
     };
-    const int shared_by_all = max(0, len - p.n_q + 1);
-    const int parts = live ? p.p_first + p.p_splits + (shared_by_all + p.s_keys - 1) / p.s_keys : 0;
-    const long long ml_stride = static_cast<long long>(p.hkv) * p.rows, ml0 = static_cast<long long>(g) * p.rows + row;
-    const long long o_stride = ml_stride * (p.d >> 2);
-    const long long o0 = static_cast<long long>(g) * p.rows * (p.d >> 2) + row * p.o_row + c4 * p.o_four;
-    const int most = __reduce_max_sync(0xFFFFFFFFu, parts);
     for (int s0 = part0; s0 < most; s0 += splits * CB_BATCH) {
-        float2 ml[CB_BATCH];
-        float4 op[CB_BATCH];
-#pragma unroll
-        for (int u = 0; u < CB_BATCH; ++u) {
-            const int s = s0 + u * splits;
-            ml[u] = make_float2(AT_NEG, 0.0f);
-            op[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (s < parts && mine) {
-                ml[u] = p.part_ml[ml0 + s * ml_stride];
-                op[u] = p.part_o[o0 + s * o_stride];
-            }
-        }
+        if (ROWS != 1 || s0 != part0) fetch(s0);
 #pragma unroll
         for (int u = 0; u < CB_BATCH; ++u) add(ml[u].x, ml[u].y, op[u]);
     }
