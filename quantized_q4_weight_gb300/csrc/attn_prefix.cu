@@ -26,7 +26,16 @@
 // tiles of up to 16 or 32 rows (a suffix's few queries) give each of the
 // four warps 16 of a tile's keys and merge the warps at the end, so that all
 // warps work and each key is read from shared memory once; taller tiles (64
-// rows) give each warp 16 rows.
+// rows) give each warp 16 rows.  Tall batches over long prefixes are attn_tc.cu's.
+//
+// What bounds it: memory for long suffixes (64 sequences of up to 2048 own
+// keys, 8 heads of 128: 269 MB in 52 us, 5.2 TB/s, the SMs idle for a fifth of
+// it at the end, where the next launch starts); the chain length, page, key,
+// products, part, and then the combining launch, for small batches (two
+// sequences on 160 keys 5.5 us, eight on 4096 9.7 us, 16 of up to 1500 own keys
+// of 2 heads of 64 7.5 us, of which 3.8 are the combining launch on its own).
+// So parts are single tiles of 64 keys as long as they fit the slots: with two
+// at least, the first two took 6.5 and 10.4 us.
 #include <type_traits>
 
 #include "decode_ops.h"

@@ -21,10 +21,19 @@
 // One warp issues the products, alternating between the streams, so that one
 // stream's products run while the other's weights are computed; a stream's
 // weights go over in two halves, and the sums of the first start while the
-// second forms.  (Scores of 64 keys, double-buffered, were slower, 274 us
-// against 239 at 1024 rows x 8 heads x 65536 keys of 128 elements: with N = 64
-// a product takes 49 cycles instead of 32, bound by its operands' shared-memory
-// reads, and the waits double.)
+// second forms.
+//
+// Measured: 1024 rows x 8 heads x 65536 keys of 128 elements 186 us, 1.48
+// PFLOP/s (0.79 of the measured bf16 rate), products 69 % of the time; 320
+// rows x 2 heads x 32749 keys 20 us.  A pair of tiles of 128 keys takes 2850
+// cycles, the products' own 2048: the rest is handing over between the row
+// threads and the products, twice a tile and stream.  A block of few tiles
+// spends 3 us before its first scores (tensor memory, page table, first keys)
+// and 2 on its part.
+// Tried and slower at the first size: scores of 64 keys, double-buffered (274
+// against 239 us then: with N = 64 a product takes 49 cycles instead of 32,
+// bound by its operands' shared-memory reads, and the waits double); a warp
+// per stream for the products (250); one lane polling a barrier for its warp.
 //
 // The reference m of a row is its running maximum, but follows it only when
 // that rises by more than 2^8: O is rescaled (in tensor memory, by the row's

@@ -70,7 +70,7 @@ struct RopeParams {
     unsigned *status;
     unsigned long long turns[128];
 };
-// vec: 16-byte accesses everywhere; small_grid_sms: multiprocessors.
+// vec: every address and stride suits 16-byte accesses.
 cudaError_t launch_rope(RopeParams &p, qgemv_dtype in, qgemv_dtype q_out, qgemv_dtype cache, bool half_layout, bool vec,
                         long long n_tokens, int sms, cudaStream_t st);
 

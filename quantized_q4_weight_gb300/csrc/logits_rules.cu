@@ -22,7 +22,7 @@
 // few rows have small slices (as few as 1024 tokens).  Many rows have slices
 // of 8192, since every slice reads its row's whole lists before it can begin.
 // 192 rows of 151936 fp32, histories up to 2048, 64 biases, masked, written:
-// 57 us, 4.2 TB/s (a copy of the logits takes 37); 48 without lists and mask.
+// 55 us, 4.3 TB/s (a copy of the logits takes 37); 48 without lists and mask.
 // 1 row 4.6 us, 5 rows of 50257 bf16, histories up to 2000, 6.8 us.
 // Tried there and slower: slices of 4096 (69) or 16384 tokens, more loads in
 // flight per thread (58), contiguous ranges per block with words at the rank
