@@ -494,9 +494,12 @@ __global__ void __launch_bounds__(AT_THREADS, DP == 256 ? 1 : 2) attn_part_kerne
     using C = AttnCfg<DP>;
     extern __shared__ __align__(128) uint8_t smem[];
     pdl_wait();
-    // Only now: the prefix kernel on tcgen05, launched next, does not wait
-    // for this one, so it must not start before what this one waited for.
-    pdl_launch_dependents();
+    // Only now: the prefix kernel on tcgen05, launched next, does not wait for
+    // this one, so it must not start before what this one waited for.  The
+    // combining launch comes in as these blocks end: let in here, its blocks take
+    // their issue slots (eight samples: 10.3 us a call in a stream instead of
+    // 9.4; let in after the last product 10.0).
+    if (p.t_mode) pdl_launch_dependents();
     Part w;
     int id = blockIdx.x, tile_rows;
     if (id < p.p_blocks) {  // row tiles innermost: blocks that run together share their keys in L2
@@ -592,7 +595,6 @@ __global__ void __launch_bounds__(ROWS == 1 ? 512 : 1024) attn_combine_kernel(co
     __shared__ float s_score[ZONE][ROWS];
     __shared__ long long s_off[ZONE][ROWS];
     extern __shared__ __align__(16) float4 s_acc[];  // [splits - 1][groups][32] sums, then as many (m, l)
-    pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int groups = ((p.d >> 2) + FOURS - 1) / FOURS, splits = warps / groups;
     const int cg = warp % groups, part0 = warp / groups;
@@ -707,6 +709,7 @@ __global__ void __launch_bounds__(ROWS == 1 ? 512 : 1024) attn_combine_kernel(co
                 add(s_score[u][rl], 1.0f, get4(static_cast<const T *>(p.v) + off + g * p.head_stride + 4 * c4));
         }
 
+    pdl_launch_dependents();  // the next kernel may come while the rows are written
     if (splits > 1) {
         float2 *s_ml = reinterpret_cast<float2 *>(s_acc + (splits - 1) * groups * 32);  // [splits - 1][groups][32]
         if (part0 > 0) {
