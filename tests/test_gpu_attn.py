@@ -396,3 +396,24 @@ def test_tall_batches_without_suffixes_and_after_other_work():
     assert torch.equal(out, c.run())
     c.check()
     del big
+
+
+def test_a_long_prefix_written_by_the_launch_before():
+    """The prefix kernel does not wait for the suffix parts, and must still see
+    what the launch before those wrote: here the whole prefix, by rope_kv."""
+    b, prefix, page, hkv, d = 12, 13000, 64, 2, 128
+    c = Case(b, 4, 16, hkv, d, prefix, [60 + i for i in range(b)], page=page, poison=False, seed=40)
+    want = c.run().clone()
+    j = torch.arange(prefix, device=DEV)
+    rows = (c.prefix_pages.long()[j // page] * page + j % page)
+    k, v = (x.view(-1, hkv, d)[rows].clone() for x in (c.k, c.v))
+    slots, zero = rows.to(torch.int32), torch.zeros(prefix, dtype=torch.int32, device=DEV)
+    plan = q.rope_plan(d, 1e4)            # position 0 everywhere: copied as they are
+    junk = torch.full_like(k, 50.0)
+    for _ in range(20):
+        q.rope_kv(plan, None, junk, junk, zero, slots, c.cache)
+        c.run()
+        q.rope_kv(plan, None, k, v, zero, slots, c.cache)
+        out = c.run()
+        assert torch.equal(out, want)
+    assert q.device_status() == 0
