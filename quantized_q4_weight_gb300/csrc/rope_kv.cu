@@ -24,7 +24,10 @@
 // TB/s, as a copy; blocks of 256 threads with four heads in flight 106, sines
 // formed by every thread for itself 152, blocks of 64 threads 88 (but 1021
 // tokens of 14 + 2 + 2 heads of 64: 3.4 us instead of 2.9).  One token 2.1 us,
-// the time between launches.
+// the time between launches.  16122 tokens of 14 + 2 + 2 heads of 64, bf16:
+// 20 us (memory alone: 11), bound by the wait for a token's loads.  Several
+// tokens in a wide block instead of narrow blocks: 6168 of 16 + 2 + 2 heads of
+// 128, f16, 15.7 us instead of 13.8, and 2 to 5 % on most other sizes.
 #include "decode_ops.h"
 #include "qgemv_internal.cuh"
 
@@ -32,7 +35,10 @@ namespace qg {
 namespace {
 
 constexpr int ROPE_THREADS = 128;
-constexpr int ROPE_UNROLL = 3;  // heads in flight per thread
+// Heads in flight per thread: 96 bytes of loads, whatever the type.  With three
+// of 16 bits 6168 tokens of 16 + 2 + 2 heads of 128 take 18.0 us, with six 13.8.
+template <typename T>
+constexpr int ROPE_UNROLL = sizeof(T) == 4 ? 3 : 6;
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v);
@@ -69,11 +75,44 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v)
     return __float2bfloat16_rn(v);
 }
 
-// Four consecutive elements (8 or 16 bytes, aligned to their size).
+// Four consecutive elements as they lie in memory (8 or 16 bytes, aligned to
+// their size): whole words, which with the 16-byte accesses below bring 7970
+// tokens of 32 + 8 + 8 heads of 128, bf16, interleaved, from 51 to 36 us.
 template <typename T>
-struct alignas(4 * sizeof(T)) Four {
-    T e[4];
+struct Four {
+    uint2 w;
 };
+template <>
+struct Four<float> {
+    float4 w;
+};
+
+__device__ __forceinline__ void unpack(const Four<float> &v, float (&f)[4])
+{
+    f[0] = v.w.x, f[1] = v.w.y, f[2] = v.w.z, f[3] = v.w.w;
+}
+__device__ __forceinline__ void unpack(const Four<__half> &v, float (&f)[4])
+{
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.w.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.w.y));
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+}
+__device__ __forceinline__ void unpack(const Four<__nv_bfloat16> &v, float (&f)[4])
+{
+    f[0] = __uint_as_float(v.w.x << 16), f[1] = __uint_as_float(v.w.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.w.y << 16), f[3] = __uint_as_float(v.w.y & 0xffff0000u);
+}
+__device__ __forceinline__ void pack(const float (&f)[4], Four<float> &v) { v.w = make_float4(f[0], f[1], f[2], f[3]); }
+__device__ __forceinline__ void pack(const float (&f)[4], Four<__half> &v)
+{
+    const __half2 a = __floats2half2_rn(f[0], f[1]), b = __floats2half2_rn(f[2], f[3]);
+    v.w = make_uint2(*reinterpret_cast<const unsigned *>(&a), *reinterpret_cast<const unsigned *>(&b));
+}
+__device__ __forceinline__ void pack(const float (&f)[4], Four<__nv_bfloat16> &v)
+{
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    v.w = make_uint2(*reinterpret_cast<const unsigned *>(&a), *reinterpret_cast<const unsigned *>(&b));
+}
 
 // cos and sin of position * theta, by the turns' fraction.
 __device__ __forceinline__ void angle(int pos, unsigned long long turns, float mscale, float &c, float &s)
@@ -109,17 +148,31 @@ __device__ __forceinline__ TC *kv_dst(const RopeParams &p, int h, long long row_
                      : static_cast<TC *>(p.cv) + row_off + (g - p.hkv) * p.head_stride;
 }
 
-template <typename T>
+// A thread's two fours of a head.  Interleaved they are neighbours, and 16-bit
+// ones travel as one 16-byte access: full sectors instead of halves.
+template <typename T, bool HALF>
+__device__ __forceinline__ void load8(const T *at, int a, int b, Four<T> &x, Four<T> &y)
+{
+    if constexpr (!HALF && sizeof(T) == 2) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(at + a);
+        x.w = make_uint2(w.x, w.y), y.w = make_uint2(w.z, w.w);
+    } else {
+        x = *reinterpret_cast<const Four<T> *>(at + a);
+        y = *reinterpret_cast<const Four<T> *>(at + b);
+    }
+}
+template <typename T, bool HALF>
 __device__ __forceinline__ void store8(T *at, int a, int b, const float (&x)[4], const float (&y)[4])
 {
     Four<T> ox, oy;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        ox.e[i] = from_f<T>(x[i]);
-        oy.e[i] = from_f<T>(y[i]);
+    pack(x, ox);
+    pack(y, oy);
+    if constexpr (!HALF && sizeof(T) == 2) {
+        *reinterpret_cast<uint4 *>(at + a) = make_uint4(ox.w.x, ox.w.y, oy.w.x, oy.w.y);
+    } else {
+        *reinterpret_cast<Four<T> *>(at + a) = ox;
+        *reinterpret_cast<Four<T> *>(at + b) = oy;
     }
-    *reinterpret_cast<Four<T> *>(at + a) = ox;
-    *reinterpret_cast<Four<T> *>(at + b) = oy;
 }
 
 // The token's cache row in elements from the cache's base, -1 for none.
@@ -141,6 +194,7 @@ template <typename TI, typename TQ, typename TC, bool HALF>
 __global__ void __launch_bounds__(ROPE_THREADS, 8) rope_vec_kernel(const __grid_constant__ RopeParams p)
 {
     __shared__ __align__(16) float s_c[128], s_s[128];
+    constexpr int UNROLL = ROPE_UNROLL<TI>;
     pdl_launch_dependents();
     const int units = p.d >> 3;
     const int j = static_cast<int>(threadIdx.x) % units, hb = static_cast<int>(threadIdx.x) / units;
@@ -156,16 +210,13 @@ __global__ void __launch_bounds__(ROPE_THREADS, 8) rope_vec_kernel(const __grid_
     bool have = false;
     const int step = p.heads_per_block * static_cast<int>(gridDim.y);
     // every thread passes the barrier below in its first turn, with heads or without
-    for (int h0 = hb + p.heads_per_block * static_cast<int>(blockIdx.y); h0 < heads || !have; h0 += ROPE_UNROLL * step) {
-        Four<TI> x[ROPE_UNROLL], y[ROPE_UNROLL];
+    for (int h0 = hb + p.heads_per_block * static_cast<int>(blockIdx.y); h0 < heads || !have; h0 += UNROLL * step) {
+        Four<TI> x[UNROLL], y[UNROLL];
 #pragma unroll
-        for (int u = 0; u < ROPE_UNROLL; ++u) {
+        for (int u = 0; u < UNROLL; ++u) {
             const int h = h0 + u * step;
             const TI *src = h < heads ? head_src<TI>(p, t, h, row_off >= 0) : nullptr;
-            if (src) {
-                x[u] = *reinterpret_cast<const Four<TI> *>(src + a);
-                y[u] = *reinterpret_cast<const Four<TI> *>(src + b);
-            }
+            if (src) load8<TI, HALF>(src, a, b, x[u], y[u]);
         }
         if (!have) {
             for (int i = threadIdx.x; i < p.rot / 2; i += blockDim.x) angle(pos, p.turns[i], p.mscale, s_c[i], s_s[i]);
@@ -179,15 +230,12 @@ __global__ void __launch_bounds__(ROPE_THREADS, 8) rope_vec_kernel(const __grid_
             have = true;
         }
 #pragma unroll
-        for (int u = 0; u < ROPE_UNROLL; ++u) {
+        for (int u = 0; u < UNROLL; ++u) {
             const int h = h0 + u * step;
             if (h >= heads || (h >= p.hq && row_off < 0)) break;  // the heads that follow have no row either
             float fx[4], fy[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                fx[i] = to_f(x[u].e[i]);
-                fy[i] = to_f(y[u].e[i]);
-            }
+            unpack(x[u], fx);
+            unpack(y[u], fy);
             if (rot_unit && h < p.hq + p.hkv) {
                 if constexpr (HALF) {
 #pragma unroll
@@ -209,9 +257,9 @@ __global__ void __launch_bounds__(ROPE_THREADS, 8) rope_vec_kernel(const __grid_
                 }
             }
             if (h < p.hq)
-                store8(q_dst<TQ>(p, t, h), a, b, fx, fy);
+                store8<TQ, HALF>(q_dst<TQ>(p, t, h), a, b, fx, fy);
             else
-                store8(kv_dst<TC>(p, h, row_off), a, b, fx, fy);
+                store8<TC, HALF>(kv_dst<TC>(p, h, row_off), a, b, fx, fy);
         }
     }
 }
@@ -264,6 +312,16 @@ cudaError_t launch4(RopeParams &p, bool vec, long long n, int sms, cudaStream_t 
         const int chunks = (heads + p.heads_per_block - 1) / p.heads_per_block;
         // blocks that share a token repeat its sines; they pay while the tokens alone leave multiprocessors idle
         const unsigned ny = static_cast<unsigned>(n * chunks <= 2ll * sms ? chunks : 1);
+        // Many tokens: a block no wider than its heads fill, the same in each of
+        // its turns, and more blocks beside it: 16122 tokens of 14 + 2 + 2 heads
+        // of 64, bf16, 33.6 -> 20 us; 6168 of 16 + 2 + 2 of 128, f16, 17.6 ->
+        // 13.8.  Tokens for fewer than ten blocks a multiprocessor keep wide
+        // ones: 1277 of 12 + 2 + 2 of 128, bf16, 5.1 us instead of 5.9.
+        constexpr int U = ROPE_UNROLL<TI>;
+        if (n >= 10ll * sms) {
+            const int turns = (heads + U * p.heads_per_block - 1) / (U * p.heads_per_block);
+            p.heads_per_block = (heads + U * turns - 1) / (U * turns);
+        }
         return launch_pdl(rope_vec_kernel<TI, TQ, TC, HALF>, dim3(nx, ny), p.heads_per_block * units, 0, st, p);
     }
     const int chunks = (heads * (p.d / 2) + ROPE_THREADS - 1) / ROPE_THREADS;

@@ -112,6 +112,15 @@ def test_layouts_and_heads(n, layout, hq, hkv, d, rot):
     run(n, hq, hkv, d, rot, layout, torch.float32, torch.bfloat16, torch.bfloat16, {}, seed=n + d)
 
 
+# Enough tokens for blocks as narrow as their heads fill, with heads that leave
+# a last turn short, in each layout and width of input.
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("tin", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("hq,hkv,d,rot", [(14, 2, 64, 16), (13, 3, 96, 96), (1, 1, 8, 8), (5, 2, 256, 64), (41, 5, 128, 64)])
+def test_many_tokens(layout, tin, hq, hkv, d, rot):
+    run(1723, hq, hkv, d, rot, layout, tin, torch.bfloat16, torch.float16, {}, top=30000, page=32, seed=hq + d)
+
+
 @pytest.mark.parametrize("tin", [torch.float32, torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("tq", [torch.float32, torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("tc", [torch.float16, torch.bfloat16])
