@@ -644,42 +644,44 @@ __global__ void __launch_bounds__(ROWS == 1 ? 512 : 1024) attn_combine_kernel(co
     // value below.
     if (p.n_q > 1) {
         const int count = (p.n_q - 1) * ROWS;
-        long long off = -1, q_at = 0;
-        const int e0 = warp + lane * warps;
-        if (e0 < count && row0 + e0 % ROWS < p.rows) {
-            int rt, ri, rh, rn;
-            shape(row0 + e0 % ROWS, rt, ri, rh, rn);
-            const int j = max(0, rn - p.n_q + 1) + e0 / ROWS;
-            if (j <= rn - p.n_q + ri) off = key_row(p, p.suffix_pages + rt / p.n_q * p.suffix_pages_stride, j);
-            q_at = rt * p.q_token_stride + rh * p.q_head_stride;
-        }
-        for (int n = 0; warp + n * warps < count; n += 4) {
-            float dot[4];
-            long long oo[4];
+        for (int base = 0; warp + base * warps < count; base += 32) {  // 32 of the warp's at a time
+            long long off = -1, q_at = 0;
+            const int e0 = warp + (base + lane) * warps;
+            if (e0 < count && row0 + e0 % ROWS < p.rows) {
+                int rt, ri, rh, rn;
+                shape(row0 + e0 % ROWS, rt, ri, rh, rn);
+                const int j = max(0, rn - p.n_q + 1) + e0 / ROWS;
+                if (j <= rn - p.n_q + ri) off = key_row(p, p.suffix_pages + rt / p.n_q * p.suffix_pages_stride, j);
+                q_at = rt * p.q_token_stride + rh * p.q_head_stride;
+            }
+            for (int n = 0; n < 32 && warp + (base + n) * warps < count; n += 4) {
+                float dot[4];
+                long long oo[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                oo[u] = __shfl_sync(0xFFFFFFFFu, off, min(n + u, 31));
-                const long long qq = __shfl_sync(0xFFFFFFFFu, q_at, min(n + u, 31));
-                dot[u] = 0.0f;
-                if (oo[u] >= 0 && n + u < 32) {
-                    const T *q = static_cast<const T *>(p.q) + qq;
-                    const T *k = static_cast<const T *>(p.k) + oo[u] + g * p.head_stride;
-                    for (int c = 4 * lane; c < p.d; c += 128) {
-                        const float4 a = get4(q + c), b = get4(k + c);
-                        dot[u] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, dot[u]))));
+                for (int u = 0; u < 4; ++u) {
+                    oo[u] = __shfl_sync(0xFFFFFFFFu, off, n + u);
+                    const long long qq = __shfl_sync(0xFFFFFFFFu, q_at, n + u);
+                    dot[u] = 0.0f;
+                    if (oo[u] >= 0) {
+                        const T *q = static_cast<const T *>(p.q) + qq;
+                        const T *k = static_cast<const T *>(p.k) + oo[u] + g * p.head_stride;
+                        for (int c = 4 * lane; c < p.d; c += 128) {
+                            const float4 a = get4(q + c), b = get4(k + c);
+                            dot[u] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, dot[u]))));
+                        }
                     }
                 }
-            }
 #pragma unroll
-            for (int d = 16; d; d >>= 1)
+                for (int d = 16; d; d >>= 1)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) dot[u] += __shfl_xor_sync(0xFFFFFFFFu, dot[u], d);
+                    for (int u = 0; u < 4; ++u) dot[u] += __shfl_xor_sync(0xFFFFFFFFu, dot[u], d);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int e = warp + (n + u) * warps;
-                if (lane == 0 && e < count) {
-                    s_score[e / ROWS][e % ROWS] = dot[u] * p.scale_log2;
-                    s_off[e / ROWS][e % ROWS] = oo[u];
+                for (int u = 0; u < 4; ++u) {
+                    const int e = warp + (base + n + u) * warps;
+                    if (lane == 0 && e < count) {
+                        s_score[e / ROWS][e % ROWS] = dot[u] * p.scale_log2;
+                        s_off[e / ROWS][e % ROWS] = oo[u];
+                    }
                 }
             }
         }

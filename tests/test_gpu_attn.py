@@ -157,6 +157,13 @@ def test_shapes_of_batches(b, nq, hq, hkv, prefix, top):
     Case(b, nq, hq, hkv, 64, prefix, lens, seed=b).check()
 
 
+# More (key, row) pairs of the rows that only later queries see than a warp has
+# lanes: narrow heads, many queries a sequence, blocks of one warp.
+@pytest.mark.parametrize("d", [8, 16])
+def test_many_queries_of_narrow_heads(d):
+    Case(80, 8, 4, 1, d, 70, [(i * 7919) % 41 for i in range(80)], seed=d).check()
+
+
 def test_tall_row_tiles_over_a_long_prefix():
     # many rows per cache head: several tiles of rows share the prefix, the last one part full
     for b, nq, hq, hkv, d, prefix in ((35, 4, 16, 2, 128, 1500), (33, 8, 8, 1, 64, 2049), (70, 1, 32, 8, 128, 777),
