@@ -32,8 +32,8 @@
 // keys, 8 heads of 128: 269 MB in 52 us, 5.2 TB/s, the SMs idle for a fifth of
 // it at the end, where the next launch starts); the chain length, page, key,
 // products, part, and then the combining launch, for small batches (two
-// sequences on 160 keys 5.5 us, eight on 4096 9.7 us, 16 of up to 1500 own keys
-// of 2 heads of 64 7.5 us, of which 3.8 are the combining launch on its own).
+// sequences on 160 keys 5.5 us, eight on 4096 9.1 us, 16 of up to 1500 own keys
+// of 2 heads of 64 7.4 us, of which 3.8 are the combining launch on its own).
 // So parts are single tiles of 64 keys as long as they fit the slots: with two
 // at least, the first two took 6.5 and 10.4 us.
 #include <type_traits>
@@ -488,8 +488,13 @@ struct Block {
     }
 };
 
+// Heads of up to 64 leave room for a third block on a multiprocessor: 47
+// sequences of 4 queries on 2057 keys take 18.3 us instead of 20.5, 64 of one on
+// 3700 12.4 instead of 15.9 (15 of 4 on 777: 11.1 instead of 10.3).  The plan
+// still counts two, so that the third has room for what the ranges leave over:
+// with ranges for 420 blocks the second of these takes 15.9 again.
 template <typename T, int DP>
-__global__ void __launch_bounds__(AT_THREADS, DP == 256 ? 1 : 2) attn_part_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(AT_THREADS, DP == 256 ? 1 : DP == 64 ? 3 : 2) attn_part_kernel(const __grid_constant__ AttnParams p)
 {
     using C = AttnCfg<DP>;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -745,6 +750,14 @@ cudaError_t launch_combine(const AttnParams &p, cudaStream_t st)
     // warps that share a row's parts: as many as fill the multiprocessors about once
     const unsigned blocks = grid.x * grid.y;
     int splits = one ? 8 : blocks <= 152 ? 4 : blocks <= 304 ? 2 : 1;
+    // but none without a batch of parts of its own, and past one wave of warps
+    // (16 a multiprocessor) none with fewer than four batches: with eight warps
+    // whatever the parts, 480 rows of 31 parts took 15.1 us a call instead of 13.5,
+    // 960 of 20 parts 18.9 instead of 15.0, and two sequences on 160 keys 5.8
+    // instead of 5.5.
+    const int parts = p.p_first + p.p_splits + p.s_splits;
+    const long long warps = one ? static_cast<long long>(rows) * heads * groups : 0;
+    while (splits > 1 && splits / 2 * (warps * splits <= 16 * 152 ? CB_BATCH : 4 * CB_BATCH) >= parts) splits /= 2;
     while (splits > 1 && groups * splits > 32) splits /= 2;
     const unsigned threads = static_cast<unsigned>(groups * splits * 32);
     const size_t smem = static_cast<size_t>((splits - 1) * groups * 32) * (sizeof(float4) + sizeof(float2));

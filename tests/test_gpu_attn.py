@@ -164,6 +164,16 @@ def test_many_queries_of_narrow_heads(d):
     Case(80, 8, 4, 1, d, 70, [(i * 7919) % 41 for i in range(80)], seed=d).check()
 
 
+# Few parts for the warps that combine them, one and more waves of rows.
+@pytest.mark.parametrize("b,nq,hq,hkv,d,prefix,top", [(15, 4, 14, 2, 64, 193, 584), (60, 1, 16, 1, 128, 2000, 200),
+                                                      (19, 2, 14, 2, 64, 873, 79), (30, 1, 16, 2, 128, 5000, 200),
+                                                      (6, 8, 8, 8, 256, 300, 100), (50, 3, 16, 2, 32, 10, 90)])
+def test_rows_of_few_parts(b, nq, hq, hkv, d, prefix, top):
+    lens = [(i * 7919) % (top + 1) for i in range(b)]
+    lens[0] = top
+    Case(b, nq, hq, hkv, d, prefix, lens, seed=b).check()
+
+
 def test_tall_row_tiles_over_a_long_prefix():
     # many rows per cache head: several tiles of rows share the prefix, the last one part full
     for b, nq, hq, hkv, d, prefix in ((35, 4, 16, 2, 128, 1500), (33, 8, 8, 1, 64, 2049), (70, 1, 32, 8, 128, 777),
