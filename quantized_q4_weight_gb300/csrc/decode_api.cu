@@ -115,8 +115,9 @@ qgemv_status plan_attn(const qgemv_attn_batch *b, const qgemv_kv_cache *c, AttnP
     const long long s_base = static_cast<long long>(b->n_seqs) * c->n_heads * a.s_tiles;
 
     // The tcgen05 kernel takes the whole tiles of 128 keys of the prefixes of
-    // tall batches: more rows than one of the other kernel's row tiles, and at
-    // least six of its tiles of 64 keys and rows per slot.  Measured (us a call,
+    // tall batches: a whole tile at least, more rows than one of the other
+    // kernel's row tiles, and at least six of its tiles of 64 keys and rows per
+    // slot (which a batch of 1824 row tiles has at 64 keys).  Measured (us a call,
     // tcgen05 / mma.sync; rows per cache head, cache heads, keys): 96 x 8: 18.5 /
     // 16.2 at 2048, 22.1 / 25.2 at 8192; 256 x 8: 21.8 / 23.5 at 2048, 47 / 114
     // at 32768; 128 x 2: 28 / 25 at 32768; 192 x 1: 19 / 15 there; 448 x 2, heads
@@ -125,8 +126,8 @@ qgemv_status plan_attn(const qgemv_attn_batch *b, const qgemv_kv_cache *c, AttnP
     // block costs about two tiles before and after its own, and a part of 8192
     // rows, written and read again, about one).
     a.t_mode = a.t_tiles = a.t_splits = a.t_keys = a.t_len = a.p_first = 0;
-    if (a.rows > 64 && static_cast<long long>(a.p_tiles) * c->n_heads * (b->prefix_len / 64) >= 6 * kSlots &&
-        attn_tc_takes(*c)) {
+    if (a.rows > 64 && b->prefix_len >= 128 &&
+        static_cast<long long>(a.p_tiles) * c->n_heads * (b->prefix_len / 64) >= 6 * kSlots && attn_tc_takes(*c)) {
         a.t_mode = a.rows <= 128 ? 2 : 1;
         a.t_tiles = static_cast<int>(ceil_div(a.rows, 256));
         a.t_len = b->prefix_len / 128 * 128;

@@ -197,3 +197,22 @@ def test_logits_refusals(L, bad, status):
 def test_logits_workspace(L):
     for s, want in ((spec(), 16384), (spec(rows=0), 0)):
         assert L.qgemv_logits_workspace_bytes(ctypes.addressof(s)) == want
+
+
+# Tall batches on short prefixes: rows enough for the tcgen05 kernel, prefixes below,
+# at and above its tile of 128 keys, and row tiles just below and above the
+# rule's 1824 (6 * 304) per 64 keys.
+TALL = [(n_seqs, n_q, heads, kv) for kv, heads, n_q in ((8, 64, 8), (8, 64, 4), (8, 32, 8), (32, 32, 8), (1, 64, 8))
+        for n_seqs in (1824 // kv * 64 // (n_q * heads // kv) + d for d in (-1, 0, 1, 8))]
+
+
+@pytest.mark.parametrize("n_seqs,n_q,heads,kv", TALL)
+def test_tall_batches_on_short_prefixes_have_a_plan(L, n_seqs, n_q, heads, kv):
+    c = cache(n_heads=kv, page_stride=2048 * kv, row_stride=128 * kv)
+    for prefix in (0, 1, 63, 64, 65, 100, 127, 128, 129, 191, 192, 255, 256, 257):
+        b = batch(n_seqs=n_seqs, n_q=n_q, n_q_heads=heads, prefix_len=prefix)
+        rows = n_seqs * n_q * heads                 # a partial row: head_dim sums, maximum and sum in fp32
+        parts = (attn_ws(L, b, c) - 16384) / (rows * (4 * 128 + 8))
+        # at least one part a row for the suffix and one for a prefix, at most one per 64 keys each
+        assert parts == int(parts)
+        assert 1 + (prefix > 0) <= parts <= -(-prefix // 64) + -(-149 // 64), (prefix, parts)

@@ -434,3 +434,46 @@ def test_a_long_prefix_written_by_the_launch_before():
         out = c.run()
         assert torch.equal(out, want)
     assert q.device_status() == 0
+
+
+class Wide(Case):
+    """A case of many sequences: the same reference, all sequences and heads at once."""
+
+    def exact(self):
+        b, nq, hkv, d, top = self.b, self.nq, self.hkv, self.d, max(max(self.lens), 1)
+        grp = self.hq // hkv
+        x = self.q.double().view(b, nq, hkv, grp, d)
+        j = torch.arange(self.prefix, device=DEV)
+        shared = [t[self.prefix_pages.long()[j // self.page], j % self.page].double() for t in (self.k, self.v)]
+        j = torch.arange(top, device=DEV).expand(b, top)
+        there = j < torch.tensor(self.lens, device=DEV)[:, None]
+        own = [torch.where(there[:, :, None, None], t[self.suffix_pages.long().gather(1, j // self.page), j % self.page].double(), 0.0)
+               for t in (self.k, self.v)]
+        last = torch.tensor(self.lens, device=DEV)[:, None] - nq + torch.arange(nq, device=DEV)     # [b, nq]
+        hidden = (torch.arange(top, device=DEV) > last[:, :, None])[:, :, None, None, :]
+
+        def scores(q_, ks, ko):
+            s = torch.cat([torch.einsum("bqhgd,khd->bqhgk", q_, ks), torch.einsum("bqhgd,bkhd->bqhgk", q_, ko)], -1)
+            return self.scale * s
+
+        s = scores(x, shared[0], own[0])
+        s[..., self.prefix:] = s[..., self.prefix:].masked_fill(hidden, float("-inf"))
+        mag = scores(x.abs(), shared[0].abs(), own[0].abs())
+        none = torch.isinf(s).all(-1, keepdim=True)
+        w = torch.softmax(s, -1).masked_fill(none, 0.0)
+
+        def weighted(vs, vo):
+            return torch.einsum("bqhgk,khd->bqhgd", w[..., :self.prefix], vs) + torch.einsum("bqhgk,bkhd->bqhgd", w[..., self.prefix:], vo)
+
+        shape = (b, nq, self.hq)
+        return weighted(*(t for t in (shared[1], own[1]))).reshape(*shape, d), \
+            weighted(shared[1].abs(), own[1].abs()).reshape(*shape, d), torch.logsumexp(s, -1).view(shape), \
+            (d + 8) * 2.0 ** -24 * float(mag.max())
+
+
+# So many rows that the tcgen05 kernel's share of work is met by one tile of 64
+# keys: prefixes below, at and above the tile of 128 that it takes.
+@pytest.mark.parametrize("prefix", [64, 100, 127, 128, 129, 200])
+def test_very_tall_batches_on_short_prefixes(prefix):
+    for b, nq, hq, hkv in ((228, 8, 64, 8), (227, 8, 64, 8), (456, 4, 64, 8)):
+        Wide(b, nq, hq, hkv, 64, prefix, [(5 * i) % 12 for i in range(b)], seed=prefix + b).check()
