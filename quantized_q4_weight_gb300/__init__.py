@@ -84,6 +84,11 @@ class RopePlan(ctypes.Structure):
     _fields_ = [("turns", ctypes.c_uint64 * 128), ("mscale", ctypes.c_float), ("rot_dim", ctypes.c_int),
                 ("layout", ctypes.c_int)]
 
+    @property
+    def address(self) -> int:
+        """Where this plan lies, for a direct call of the C function (a copy lies elsewhere)."""
+        return ctypes.addressof(self)
+
 
 class AttnBatchStruct(ctypes.Structure):
     _fields_ = [("n_seqs", ctypes.c_int), ("n_q", ctypes.c_int), ("n_q_heads", ctypes.c_int),
@@ -516,11 +521,18 @@ def rope_plan(rot_dim: int, base: float, layout: str = "half", scaling: str = "p
                      1.0 if low is None else low, (4.0 if scaling == "bands" else 32.0) if high is None else high, mscale)
     plan = RopePlan()
     _check(lib().qgemv_rope_init(ctypes.byref(cfg), ctypes.byref(plan)), "qgemv_rope_init")
-    plan.address = ctypes.addressof(plan)
     return plan
 
 
-class KvCache:
+class _Described:
+    """Has `struct`, what the C call takes."""
+
+    @property
+    def address(self) -> int:
+        return ctypes.addressof(self.struct)
+
+
+class KvCache(_Described):
     """A paged cache: k and v f16 or bf16 tensors [pages][page_size][heads][head_dim]
     of the same strides (elements of a head contiguous).  For pages laid out
     [pages][heads][page_size][head_dim] pass k.transpose(1, 2), v.transpose(1, 2)."""
@@ -532,7 +544,6 @@ class KvCache:
         self.k, self.v = k, v
         self.struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], k.shape[0], k.shape[1], k.shape[2],
                                     k.shape[3], k.stride(0), k.stride(1), k.stride(2))
-        self.address = ctypes.addressof(self.struct)
 
 
 def _i32(x, what: str, n: int):
@@ -547,14 +558,14 @@ def rope_kv(plan: RopePlan, xq, xk, xv, pos, slots=None, cache: KvCache | None =
     """Rotate q [tokens][heads][head_dim] into `out` (default: a new tensor of the
     cache's type, or of q's without a cache) and k, v [tokens][kv heads][head_dim] into
     the cache rows `slots` (-1: none).  xq, or xk and xv, may be None.  Returns out."""
-    r = (_ext or _load_binding()).rope_kv(plan.address, xq, xk, xv, pos, slots, None if cache is None else cache.address, out,
-                                     None if stream is None else stream.cuda_stream)
+    r = (_ext or _load_binding()).rope_kv(plan, xq, xk, xv, pos, slots, None if cache is None else cache.struct, out,
+                                          None if stream is None else stream.cuda_stream)
     if type(r) is int:
         _check(r, "qgemv_rope_kv")
     return r
 
 
-class AttnBatch:
+class AttnBatch(_Described):
     """Sequences that share a prefix, over a cache (see qgemv_attn_batch): the
     tables and lengths are device tensors that later calls read again, so a
     decode loop updates them in place.  scale None: 1 / sqrt(head_dim)."""
@@ -576,7 +587,6 @@ class AttnBatch:
             _i32(prefix_pages, "AttnBatch: prefix_pages", -(-prefix_len // page)) if prefix_len else None,
             _i32(suffix_len, "AttnBatch: suffix_len", n_seqs), own, suffix_pages.stride(0) if own else 0, max_suffix,
             0.0 if scale is None else scale)
-        self.address = ctypes.addressof(self.struct)
 
     def workspace_bytes(self) -> int:
         return int(lib().qgemv_attn_workspace_bytes(self.address, self.cache.address))
@@ -586,14 +596,14 @@ def attn_prefix(xq, batch: AttnBatch, ws, out=None, lse=None, stream=None):
     """Attention of q [n_seqs][n_q][heads][head_dim] (or [tokens][heads][head_dim]) over the
     batch's contexts; out (the cache's type or fp32, q's shape; default: a new tensor
     of the cache's type); lse fp32 [tokens][heads] or None."""
-    r = (_ext or _load_binding()).attn_prefix(xq, batch.cache.address, batch.address, ws, out, lse,
-                                         None if stream is None else stream.cuda_stream)
+    r = (_ext or _load_binding()).attn_prefix(xq, batch.cache.struct, batch.struct, ws, out, lse,
+                                              None if stream is None else stream.cuda_stream)
     if type(r) is int:
         _check(r, "qgemv_attn_prefix")
     return r
 
 
-class LogitsRules:
+class LogitsRules(_Described):
     """Rules on logits of `rows` rows over `vocab` tokens (see
     qgemv_logits_spec): device tensors that later calls read again, so a
     decode loop appends to `history` and counts up `history_len` in place.
@@ -630,7 +640,6 @@ class LogitsRules:
         self.struct = LogitsSpec(rows, vocab, hp, hs, _i32(history_len, "LogitsRules: history_len", rows), hn,
                                  row(repetition, "repetition"), row(frequency, "frequency"), row(presence, "presence"),
                                  ip, bp, bs, _i32(bias_len, "LogitsRules: bias_len", rows), bn, mp, ms)
-        self.address = ctypes.addressof(self.struct)
 
     def workspace_bytes(self) -> int:
         return int(lib().qgemv_logits_workspace_bytes(self.address))
@@ -640,8 +649,8 @@ def logits_rules(x, rules: LogitsRules, ws, out=None, idx=None, val=None, stream
     """Apply the rules to x [rows][vocab] (fp32, f16, bf16); out (None: not
     written; may be x) receives the results in x's type.  Returns each row's best
     token (int64, -1 for none) and its value (fp32)."""
-    r = (_ext or _load_binding()).logits_rules(x, rules.address, ws, out, idx, val,
-                                          None if stream is None else stream.cuda_stream)
+    r = (_ext or _load_binding()).logits_rules(x, rules.struct, ws, out, idx, val,
+                                               None if stream is None else stream.cuda_stream)
     if type(r) is int:
         _check(r, "qgemv_logits_rules")
     return r

@@ -39,14 +39,35 @@ const at::Tensor *tensor(PyObject *o, const char *what)
     return &t;
 }
 
+// A structure of the C ABI where the Python object keeps it (a ctypes
+// structure's buffer, held during the call), nullptr for None.  An address
+// kept beside the object instead would outlive it in the object's copies.
 template <typename S>
-const S *address(PyObject *o)
-{
-    if (o == Py_None) return nullptr;
-    const void *p = PyLong_AsVoidPtr(o);
-    if (!p && PyErr_Occurred()) throw Refused("an address");
-    return static_cast<const S *>(p);
-}
+class Structure {
+public:
+    Structure(PyObject *o, const char *what)
+    {
+        if (o == Py_None) return;
+        if (PyObject_GetBuffer(o, &view_, PyBUF_SIMPLE) != 0) {
+            PyErr_Clear();
+            throw Refused(what);
+        }
+        if (view_.len != static_cast<Py_ssize_t>(sizeof(S)) || reinterpret_cast<uintptr_t>(view_.buf) % alignof(S)) {
+            PyBuffer_Release(&view_);
+            throw Refused(what);
+        }
+    }
+    ~Structure()
+    {
+        if (view_.buf) PyBuffer_Release(&view_);
+    }
+    Structure(const Structure &) = delete;
+    Structure &operator=(const Structure &) = delete;
+    const S *get() const { return static_cast<const S *>(view_.buf); }
+
+private:
+    Py_buffer view_ = {};
+};
 
 qgemv_stream_t stream_of(PyObject *o, const at::Tensor &t)
 {
@@ -124,11 +145,13 @@ PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F f) noexcept
 PyObject *rope_kv(PyObject *, PyObject *const *a, Py_ssize_t n) noexcept
 {
     return guarded(n, 9, [&]() -> PyObject * {
-        const auto *plan = address<qgemv_rope_plan>(a[0]);
+        const Structure<qgemv_rope_plan> plan_at(a[0], "rope_kv: plan");
+        const Structure<qgemv_kv_cache> cache_at(a[6], "rope_kv: cache");
+        const auto *plan = plan_at.get();
+        const auto *cache = cache_at.get();
         const at::Tensor *q = tensor(a[1], "rope_kv: q"), *k = tensor(a[2], "rope_kv: k"), *v = tensor(a[3], "rope_kv: v"),
                          *pos = tensor(a[4], "rope_kv: pos"), *slots = tensor(a[5], "rope_kv: slots"),
                          *out = tensor(a[7], "rope_kv: out");
-        const auto *cache = address<qgemv_kv_cache>(a[6]);
         const at::Tensor *some = q ? q : k;
         need(some && pos && !k == !v, "rope_kv: q, or k and v, and pos");
         need(some->dim() == 3, "rope_kv: [tokens][heads][head_dim]");
@@ -188,10 +211,12 @@ void token_strides(const at::Tensor &t, const qgemv_attn_batch &b, int d, int64_
 PyObject *attn_prefix(PyObject *, PyObject *const *a, Py_ssize_t n) noexcept
 {
     return guarded(n, 7, [&]() -> PyObject * {
+        const Structure<qgemv_kv_cache> cache_at(a[1], "attn_prefix: cache");
+        const Structure<qgemv_attn_batch> batch_at(a[2], "attn_prefix: batch");
         const at::Tensor *q = tensor(a[0], "attn_prefix: q"), *ws = tensor(a[3], "attn_prefix: ws"),
                          *out = tensor(a[4], "attn_prefix: out"), *lse = tensor(a[5], "attn_prefix: lse");
-        const auto *cache = address<qgemv_kv_cache>(a[1]);
-        const auto *batch = address<qgemv_attn_batch>(a[2]);
+        const auto *cache = cache_at.get();
+        const auto *batch = batch_at.get();
         need(q && ws && cache && batch, "attn_prefix: q, a batch and its workspace");
         need(type_of(*q, "attn_prefix: q of the cache's type") == cache->type, "attn_prefix: q of the cache's type");
         need(ws->is_contiguous(), "attn_prefix: a contiguous workspace");
@@ -219,10 +244,11 @@ PyObject *attn_prefix(PyObject *, PyObject *const *a, Py_ssize_t n) noexcept
 PyObject *logits_rules(PyObject *, PyObject *const *a, Py_ssize_t n) noexcept
 {
     return guarded(n, 7, [&]() -> PyObject * {
+        const Structure<qgemv_logits_spec> spec_at(a[1], "logits_rules: rules");
         const at::Tensor *x = tensor(a[0], "logits_rules: x"), *ws = tensor(a[2], "logits_rules: ws"),
                          *out = tensor(a[3], "logits_rules: out"), *idx = tensor(a[4], "logits_rules: idx"),
                          *val = tensor(a[5], "logits_rules: val");
-        const auto *spec = address<qgemv_logits_spec>(a[1]);
+        const auto *spec = spec_at.get();
         need(x && ws && spec, "logits_rules: x, rules and a workspace");
         need(x->dim() == 2 && x->size(0) == spec->rows && x->size(1) == spec->vocab && x->stride(1) == 1,
              "logits_rules: x [rows][vocab]");

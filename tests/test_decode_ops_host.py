@@ -1,7 +1,10 @@
 """The argument checks of the operators between the GEMVs: a refused call
 returns its status before any CUDA call, so these run without a GPU.  Pointers
 are numbers that nothing follows."""
+import copy
 import ctypes
+import gc
+import pickle
 
 import pytest
 
@@ -216,3 +219,52 @@ def test_tall_batches_on_short_prefixes_have_a_plan(L, n_seqs, n_q, heads, kv):
         # at least one part a row for the suffix and one for a prefix, at most one per 64 keys each
         assert parts == int(parts)
         assert 1 + (prefix > 0) <= parts <= -(-prefix // 64) + -(-149 // 64), (prefix, parts)
+
+
+def plan_copies(p):
+    yield copy.copy(p)
+    yield copy.deepcopy(p)
+    yield pickle.loads(pickle.dumps(p))
+    yield copy.deepcopy({"model": [p]})["model"][0]
+
+
+def test_copies_of_a_rope_plan_are_plans_of_their_own():
+    p = q.rope_plan(96, 1e5, layout="interleaved", scaling="yarn", factor=4.0, orig_len=8192)
+    want = bytes(p)
+    copies = list(plan_copies(p))
+    assert len({x.address for x in [p, *copies]}) == 5
+    del p
+    gc.collect()
+    others = [q.rope_plan(8, 10.0 + i) for i in range(200)]     # would take the freed memory
+    for x in copies:
+        assert x.address == ctypes.addressof(x) and ctypes.string_at(x.address, ctypes.sizeof(x)) == want
+    assert all(o.rot_dim == 8 for o in others)
+
+
+def test_a_plan_filled_through_the_c_call_is_a_plan(L):
+    plan = q.RopePlan()
+    cfg = q.RopeConfig(rot_dim=64, layout=0, scaling=0, base=1e4)
+    assert L.qgemv_rope_init(ctypes.byref(cfg), ctypes.byref(plan)) == OK
+    assert plan.address == ctypes.addressof(plan) and bytes(plan) == bytes(q.rope_plan(64, 1e4))
+
+
+def test_the_binding_takes_the_structures_themselves():
+    """A plan is read where it lies at the call; something else is refused by its size."""
+    ext = q._load_binding()
+    none = [None] * 8
+    for x in (q.rope_plan(64, 1e4), *plan_copies(q.rope_plan(64, 1e4))):
+        with pytest.raises(ValueError, match="q, or k and v"):
+            ext.rope_kv(x, *none)
+    for bad in (q.KvCacheStruct(), b"1234", 4096, "x"):
+        with pytest.raises(ValueError, match="plan"):
+            ext.rope_kv(bad, *none)
+    plan = q.rope_plan(64, 1e4)
+    for bad in (plan, b"", 4096):
+        with pytest.raises(ValueError, match="cache"):
+            ext.rope_kv(plan, *none[:5], bad, None, None)
+        with pytest.raises(ValueError, match="cache"):
+            ext.attn_prefix(None, bad, None, None, None, None, None)
+        with pytest.raises(ValueError, match="batch"):
+            ext.attn_prefix(None, q.KvCacheStruct(), bad, None, None, None, None)
+        with pytest.raises(ValueError, match="rules"):
+            ext.logits_rules(None, bad, None, None, None, None, None)
