@@ -557,7 +557,9 @@ def _i32(x, what: str, n: int):
 def rope_kv(plan: RopePlan, xq, xk, xv, pos, slots=None, cache: KvCache | None = None, out=None, stream=None):
     """Rotate q [tokens][heads][head_dim] into `out` (default: a new tensor of the
     cache's type, or of q's without a cache) and k, v [tokens][kv heads][head_dim] into
-    the cache rows `slots` (-1: none).  xq, or xk and xv, may be None.  Returns out."""
+    the cache rows `slots` (-1: none).  xq, or xk and xv, may be None.  Returns out.
+    In this call and those below a result made by the call is `stream`'s memory, as of
+    tensors made with that stream current."""
     r = (_ext or _load_binding()).rope_kv(plan, xq, xk, xv, pos, slots, None if cache is None else cache.struct, out,
                                           None if stream is None else stream.cuda_stream)
     if type(r) is int:

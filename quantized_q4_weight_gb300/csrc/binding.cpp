@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -69,11 +70,19 @@ private:
     Py_buffer view_ = {};
 };
 
+// The handle of a stream argument (an integer).
+void *handle(PyObject *o)
+{
+    void *p = PyLong_AsVoidPtr(o);
+    if (!p && PyErr_Occurred()) throw Refused("a stream's handle");
+    return p;
+}
+
 qgemv_stream_t stream_of(PyObject *o, const at::Tensor &t)
 {
     if (o == Py_None)
         return reinterpret_cast<qgemv_stream_t>(c10::cuda::getCurrentCUDAStream(t.device().index()).stream());
-    return reinterpret_cast<qgemv_stream_t>(PyLong_AsVoidPtr(o));
+    return reinterpret_cast<qgemv_stream_t>(handle(o));
 }
 
 qgemv_dtype type_of(const at::Tensor &t, const char *what)
@@ -106,9 +115,14 @@ int64_t heads(const at::Tensor &t, const char *what)
 }
 
 // A new contiguous tensor beside another (without a way through the
-// dispatcher: it is a third of a call).
-at::Tensor beside(const at::Tensor &t, at::IntArrayRef sizes, at::ScalarType type)
+// dispatcher: it is a third of a call), from the memory of the stream that
+// the call runs on: a block that the current stream has just let go may still
+// be in use there.
+at::Tensor beside(const at::Tensor &t, at::IntArrayRef sizes, at::ScalarType type, PyObject *stream)
 {
+    if (stream == Py_None) return at::detail::empty_cuda(sizes, type, t.device(), std::nullopt);
+    const c10::cuda::CUDAStreamGuard there(
+        c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle(stream)), t.device().index()));
     return at::detail::empty_cuda(sizes, type, t.device(), std::nullopt);
 }
 
@@ -170,7 +184,7 @@ PyObject *rope_kv(PyObject *, PyObject *const *a, Py_ssize_t n) noexcept
         if (q) {
             qs = heads(*q, "rope_kv: q [tokens][heads][head_dim] with adjacent heads");
             if (!out) {
-                made = beside(*q, q->sizes(), cache ? scalar_of(cache->type) : q->scalar_type());
+                made = beside(*q, q->sizes(), cache ? scalar_of(cache->type) : q->scalar_type(), a[8]);
                 out = &made;
             }
             need(out->sizes() == q->sizes(), "rope_kv: out of q's shape");
@@ -224,7 +238,7 @@ PyObject *attn_prefix(PyObject *, PyObject *const *a, Py_ssize_t n) noexcept
         token_strides(*q, *batch, cache->head_dim, qt, qh);
         at::Tensor made;
         if (!out) {
-            made = beside(*q, q->sizes(), q->scalar_type());
+            made = beside(*q, q->sizes(), q->scalar_type(), a[6]);
             out = &made;
         }
         token_strides(*out, *batch, cache->head_dim, ot, oh);
@@ -259,13 +273,13 @@ PyObject *logits_rules(PyObject *, PyObject *const *a, Py_ssize_t n) noexcept
         at::Tensor made_idx, made_val;
         if (!idx && !val) {  // one allocation for both
             const int64_t rows = spec->rows;
-            const at::Tensor both = beside(*x, {rows + (rows + 1) / 2}, at::kLong);
+            const at::Tensor both = beside(*x, {rows + (rows + 1) / 2}, at::kLong, a[6]);
             made_idx = part_of(both, at::kLong, rows, 0);
             made_val = part_of(both, at::kFloat, rows, 2 * rows);
         } else if (!idx) {
-            made_idx = beside(*x, {spec->rows}, at::kLong);
+            made_idx = beside(*x, {spec->rows}, at::kLong, a[6]);
         } else if (!val) {
-            made_val = beside(*x, {spec->rows}, at::kFloat);
+            made_val = beside(*x, {spec->rows}, at::kFloat, a[6]);
         }
         if (!idx) idx = &made_idx;
         if (!val) val = &made_val;
