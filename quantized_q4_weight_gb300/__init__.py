@@ -221,6 +221,16 @@ def _stream(stream=None):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _result(shape, dtype, beside, stream):
+    """A new tensor on `beside`'s device for a call on `stream` (None: the current one),
+    from that stream's memory: a block that the current stream has just let go may
+    still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=beside.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=beside.device)
+
+
 def _ptr(t):
     if t is None:
         return None
@@ -250,13 +260,13 @@ def new_workspace(nbytes: int, device=None) -> torch.Tensor:
 # ----------------------------------------------------------------- calls
 
 def pack_q4_0(w_ggml: torch.Tensor, N: int, K: int, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    out = out if out is not None else torch.empty(q4_0_bytes(N, K), dtype=torch.uint8, device=w_ggml.device)
+    out = out if out is not None else _result(q4_0_bytes(N, K), torch.uint8, w_ggml, stream)
     _check(lib().qgemv_pack_q4_0(_ptr(w_ggml), _ptr(out), N, K, _stream(stream)), "qgemv_pack_q4_0")
     return out
 
 
 def unpack_q4_0(w_packed: torch.Tensor, N: int, K: int, out: torch.Tensor | None = None, stream=None):
-    out = out if out is not None else torch.empty(q4_0_bytes(N, K), dtype=torch.uint8, device=w_packed.device)
+    out = out if out is not None else _result(q4_0_bytes(N, K), torch.uint8, w_packed, stream)
     _check(lib().qgemv_unpack_q4_0(_ptr(w_packed), _ptr(out), N, K, _stream(stream)), "qgemv_unpack_q4_0")
     return out
 
@@ -264,27 +274,27 @@ def unpack_q4_0(w_packed: torch.Tensor, N: int, K: int, out: torch.Tensor | None
 def quantize_q8_0(x: torch.Tensor, R: int, K: int, batch: int = 1, out: torch.Tensor | None = None, stream=None):
     """x fp32 [batch, R, K] (any shape with that many elements) -> planar Q8_0 bytes."""
     assert x.dtype == torch.float32 and x.numel() == batch * R * K
-    out = out if out is not None else torch.empty(batch * xq_bytes(R, K), dtype=torch.uint8, device=x.device)
+    out = out if out is not None else _result(batch * xq_bytes(R, K), torch.uint8, x, stream)
     _check(lib().qgemv_quantize_q8_0(_ptr(x), _ptr(out), R, K, batch, _stream(stream)), "qgemv_quantize_q8_0")
     return out
 
 
 def gemv(W, layout: int, xq, N: int, K: int, T: int, ws, y=None, stream=None) -> torch.Tensor:
-    y = y if y is not None else torch.empty((T, N), dtype=torch.float32, device=W.device)
+    y = y if y is not None else _result((T, N), torch.float32, W, stream)
     _check(lib().qgemv_q4_0(_ptr(W), layout, _ptr(xq), _ptr(y), N, K, T, _ptr(ws), ws.numel(), _stream(stream)),
            "qgemv_q4_0")
     return y
 
 
 def gemv_f32(W, layout: int, x, N: int, K: int, T: int, ws, y=None, stream=None) -> torch.Tensor:
-    y = y if y is not None else torch.empty((T, N), dtype=torch.float32, device=W.device)
+    y = y if y is not None else _result((T, N), torch.float32, W, stream)
     _check(lib().qgemv_q4_0_f32(_ptr(W), layout, _ptr(x), _ptr(y), N, K, T, _ptr(ws), ws.numel(), _stream(stream)),
            "qgemv_q4_0_f32")
     return y
 
 
 def gemv_argmax(W, layout: int, xq, N: int, K: int, T: int, ws, y=None, idx=None, stream=None):
-    idx = idx if idx is not None else torch.empty(T, dtype=torch.int64, device=W.device)
+    idx = idx if idx is not None else _result(T, torch.int64, W, stream)
     _check(lib().qgemv_q4_0_argmax(_ptr(W), layout, _ptr(xq), _ptr(y), _ptr(idx), N, K, T, _ptr(ws), ws.numel(),
                                    _stream(stream)), "qgemv_q4_0_argmax")
     return idx
@@ -292,7 +302,7 @@ def gemv_argmax(W, layout: int, xq, N: int, K: int, T: int, ws, y=None, idx=None
 
 def gemv_argmax_f32(W, layout: int, x, N: int, K: int, T: int, ws, y=None, idx=None, stream=None):
     """Argmax of W . x over rows for fp32 x[T][K] (quantised inside the kernel)."""
-    idx = idx if idx is not None else torch.empty(T, dtype=torch.int64, device=W.device)
+    idx = idx if idx is not None else _result(T, torch.int64, W, stream)
     _check(lib().qgemv_q4_0_argmax_f32(_ptr(W), layout, _ptr(x), _ptr(y), _ptr(idx), N, K, T, _ptr(ws), ws.numel(),
                                        _stream(stream)), "qgemv_q4_0_argmax_f32")
     return idx
@@ -300,8 +310,8 @@ def gemv_argmax_f32(W, layout: int, x, N: int, K: int, T: int, ws, y=None, idx=N
 
 def gemv_top2(W, layout: int, xq, N: int, K: int, T: int, ws, y=None, idx2=None, val2=None, stream=None):
     """The two best rows per token and their outputs: (idx2 int64 [T][2], val2 fp32 [T][2])."""
-    idx2 = idx2 if idx2 is not None else torch.empty((T, 2), dtype=torch.int64, device=W.device)
-    val2 = val2 if val2 is not None else torch.empty((T, 2), dtype=torch.float32, device=W.device)
+    idx2 = idx2 if idx2 is not None else _result((T, 2), torch.int64, W, stream)
+    val2 = val2 if val2 is not None else _result((T, 2), torch.float32, W, stream)
     _check(lib().qgemv_q4_0_top2(_ptr(W), layout, _ptr(xq), _ptr(y), _ptr(idx2), _ptr(val2), N, K, T, _ptr(ws),
                                  ws.numel(), _stream(stream)), "qgemv_q4_0_top2")
     return idx2, val2
@@ -309,8 +319,8 @@ def gemv_top2(W, layout: int, xq, N: int, K: int, T: int, ws, y=None, idx2=None,
 
 def gemv_top2_f32(W, layout: int, x, N: int, K: int, T: int, ws, y=None, idx2=None, val2=None, stream=None):
     """gemv_top2 for fp32 x[T][K] (quantised inside the kernel)."""
-    idx2 = idx2 if idx2 is not None else torch.empty((T, 2), dtype=torch.int64, device=W.device)
-    val2 = val2 if val2 is not None else torch.empty((T, 2), dtype=torch.float32, device=W.device)
+    idx2 = idx2 if idx2 is not None else _result((T, 2), torch.int64, W, stream)
+    val2 = val2 if val2 is not None else _result((T, 2), torch.float32, W, stream)
     _check(lib().qgemv_q4_0_top2_f32(_ptr(W), layout, _ptr(x), _ptr(y), _ptr(idx2), _ptr(val2), N, K, T, _ptr(ws),
                                      ws.numel(), _stream(stream)), "qgemv_q4_0_top2_f32")
     return idx2, val2
@@ -320,9 +330,9 @@ def verify_f32(W, layout: int, x, tokens, N: int, K: int, T: int, ws, idx2=None,
                stream=None):
     """A verify step in one launch: the top-2 rows of W . x per position and the
     committed count of the verify rule on (tokens, idx2[:, 0])."""
-    idx2 = idx2 if idx2 is not None else torch.empty((T, 2), dtype=torch.int64, device=W.device)
-    val2 = val2 if val2 is not None else torch.empty((T, 2), dtype=torch.float32, device=W.device)
-    n_commit = n_commit if n_commit is not None else torch.empty(1, dtype=torch.int32, device=W.device)
+    idx2 = idx2 if idx2 is not None else _result((T, 2), torch.int64, W, stream)
+    val2 = val2 if val2 is not None else _result((T, 2), torch.float32, W, stream)
+    n_commit = n_commit if n_commit is not None else _result(1, torch.int32, W, stream)
     _check(lib().qgemv_q4_0_verify_f32(_ptr(W), layout, _ptr(x), _ptr(tokens), _ptr(idx2), _ptr(val2), _ptr(n_commit),
                                        N, K, T, _ptr(ws), ws.numel(), _stream(stream)), "qgemv_q4_0_verify_f32")
     return idx2, val2, n_commit
@@ -335,7 +345,7 @@ def verify_commit(tokens, pred, n_commit=None, stream=None):
     idx2[:, 0] of gemv_top2)."""
     T = tokens.numel()
     assert pred.dim() == 1 and pred.numel() == T and tokens.is_contiguous()
-    n_commit = n_commit if n_commit is not None else torch.empty(1, dtype=torch.int32, device=tokens.device)
+    n_commit = n_commit if n_commit is not None else _result(1, torch.int32, tokens, stream)
     _check(lib().qgemv_verify_commit(_ptr(tokens), ctypes.c_void_p(pred.data_ptr()), pred.stride(0), T,
                                      _ptr(n_commit), _stream(stream)), "qgemv_verify_commit")
     return n_commit
@@ -347,7 +357,7 @@ def ffn_workspace_bytes(d_model: int, d_ff: int, T: int) -> int:
 
 def ffn(W_gate, W_up, W_down, layout: int, x, d_model: int, d_ff: int, T: int, ws, y=None, stream=None):
     """y[T][d_model] = W_down . Q8_0(SiLU(W_gate . x) * (W_up . x)) for fp32 x[T][d_model]."""
-    y = y if y is not None else torch.empty((T, d_model), dtype=torch.float32, device=x.device)
+    y = y if y is not None else _result((T, d_model), torch.float32, x, stream)
     _check(lib().qgemv_q4_0_ffn(_ptr(W_gate), _ptr(W_up), _ptr(W_down), layout, _ptr(x), _ptr(y), d_model, d_ff, T,
                                 _ptr(ws), ws.numel(), _stream(stream)), "qgemv_q4_0_ffn")
     return y
@@ -356,7 +366,7 @@ def ffn(W_gate, W_up, W_down, layout: int, x, d_model: int, d_ff: int, T: int, w
 def ffn_residual(W_gate, W_up, W_down, layout: int, x, residual, d_model: int, d_ff: int, T: int, ws, y=None,
                  stream=None):
     """y = residual + W_down . Q8_0(SiLU(W_gate . x) * (W_up . x)); residual may be y."""
-    y = y if y is not None else torch.empty((T, d_model), dtype=torch.float32, device=x.device)
+    y = y if y is not None else _result((T, d_model), torch.float32, x, stream)
     _check(lib().qgemv_q4_0_ffn_residual(_ptr(W_gate), _ptr(W_up), _ptr(W_down), layout, _ptr(x), _ptr(residual),
                                          _ptr(y), d_model, d_ff, T, _ptr(ws), ws.numel(), _stream(stream)),
            "qgemv_q4_0_ffn_residual")
@@ -365,7 +375,7 @@ def ffn_residual(W_gate, W_up, W_down, layout: int, x, residual, d_model: int, d
 
 def silu_mul_q8(g, u, T: int, F: int, hq=None, stream=None):
     """Test hook: planar Q8_0 codes of SiLU(g) * u (g, u fp32 [T][F])."""
-    hq = hq if hq is not None else torch.empty(xq_bytes(T, F), dtype=torch.uint8, device=g.device)
+    hq = hq if hq is not None else _result(xq_bytes(T, F), torch.uint8, g, stream)
     _check(lib().qgemv_debug_silu_mul_q8(_ptr(g), _ptr(u), _ptr(hq), T, F, _stream(stream)), "qgemv_debug_silu_mul_q8")
     return hq
 
@@ -376,27 +386,27 @@ def q8_0_bytes(N: int, K: int) -> int:
 
 def pack_q8_0(w_ggml: torch.Tensor, N: int, K: int, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """GGML Q8_0 weights (uint8 [34 N K/32]) -> the device layout (same bytes)."""
-    out = out if out is not None else torch.empty(q8_0_bytes(N, K), dtype=torch.uint8, device=w_ggml.device)
+    out = out if out is not None else _result(q8_0_bytes(N, K), torch.uint8, w_ggml, stream)
     _check(lib().qgemv_pack_q8_0(_ptr(w_ggml), _ptr(out), N, K, _stream(stream)), "qgemv_pack_q8_0")
     return out
 
 
 def unpack_q8_0(w_packed: torch.Tensor, N: int, K: int, out: torch.Tensor | None = None, stream=None):
-    out = out if out is not None else torch.empty(q8_0_bytes(N, K), dtype=torch.uint8, device=w_packed.device)
+    out = out if out is not None else _result(q8_0_bytes(N, K), torch.uint8, w_packed, stream)
     _check(lib().qgemv_unpack_q8_0(_ptr(w_packed), _ptr(out), N, K, _stream(stream)), "qgemv_unpack_q8_0")
     return out
 
 
 def requant_f32_q4_0(w: torch.Tensor, N: int, K: int, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """fp32 weights [N][K] -> GGML Q4_0 blocks (uint8 [18 N K/32]), GGML's q4_0 encoder."""
-    out = out if out is not None else torch.empty(q4_0_bytes(N, K), dtype=torch.uint8, device=w.device)
+    out = out if out is not None else _result(q4_0_bytes(N, K), torch.uint8, w, stream)
     _check(lib().qgemv_requant_f32_q4_0(_ptr(w), _ptr(out), N, K, _stream(stream)), "qgemv_requant_f32_q4_0")
     return out
 
 
 def requant_q8_0_q4_0(w_q8: torch.Tensor, N: int, K: int, out: torch.Tensor | None = None, stream=None):
     """GGML Q8_0 weights (uint8 [34 N K/32]) -> GGML Q4_0 blocks (uint8 [18 N K/32])."""
-    out = out if out is not None else torch.empty(q4_0_bytes(N, K), dtype=torch.uint8, device=w_q8.device)
+    out = out if out is not None else _result(q4_0_bytes(N, K), torch.uint8, w_q8, stream)
     _check(lib().qgemv_requant_q8_0_q4_0(_ptr(w_q8), _ptr(out), N, K, _stream(stream)), "qgemv_requant_q8_0_q4_0")
     return out
 
@@ -407,7 +417,7 @@ def q8_0_workspace_bytes(N: int, K: int, T: int) -> int:
 
 def gemv_q8_0(W, xq, N: int, K: int, T: int, ws=None, y=None, stream=None) -> torch.Tensor:
     """y[T][N] for packed Q8_0 weights and planar Q8_0 activations."""
-    y = y if y is not None else torch.empty((T, N), dtype=torch.float32, device=W.device)
+    y = y if y is not None else _result((T, N), torch.float32, W, stream)
     _check(lib().qgemv_q8_0(_ptr(W), _ptr(xq), _ptr(y), N, K, T, _ptr(ws), 0 if ws is None else ws.numel(),
                             _stream(stream)), "qgemv_q8_0")
     return y
@@ -659,7 +669,7 @@ def logits_rules(x, rules: LogitsRules, ws, out=None, idx=None, val=None, stream
 
 
 def block_isums(W, layout: int, xq, N: int, K: int, T: int, stream=None) -> torch.Tensor:
-    out = torch.empty((T, N, K // QK), dtype=torch.int32, device=W.device)
+    out = _result((T, N, K // QK), torch.int32, W, stream)
     _check(lib().qgemv_debug_block_isums(_ptr(W), layout, _ptr(xq), _ptr(out), N, K, T, _stream(stream)),
            "qgemv_debug_block_isums")
     return out
@@ -671,22 +681,22 @@ def gs64_bytes(N: int, K: int) -> int:
 
 def pack_gs64(wq, wscale, N: int, K: int, stream=None) -> torch.Tensor:
     """Row planes (nibbles [N][K/64][32] uint8, scales [N][K/64] fp32) -> packed device layout."""
-    out = torch.empty(gs64_bytes(N, K), dtype=torch.uint8, device=wq.device)
+    out = _result(gs64_bytes(N, K), torch.uint8, wq, stream)
     _check(lib().qgemv_pack_gs64(_ptr(wq), _ptr(wscale), _ptr(out), N, K, _stream(stream)), "qgemv_pack_gs64")
     return out
 
 
 def unpack_gs64(W, N: int, K: int, stream=None):
-    wq = torch.empty((N, K // 64, 32), dtype=torch.uint8, device=W.device)
-    ws = torch.empty((N, K // 64), dtype=torch.float32, device=W.device)
+    wq = _result((N, K // 64, 32), torch.uint8, W, stream)
+    ws = _result((N, K // 64), torch.float32, W, stream)
     _check(lib().qgemv_unpack_gs64(_ptr(W), _ptr(wq), _ptr(ws), N, K, _stream(stream)), "qgemv_unpack_gs64")
     return wq, ws
 
 
 def quantize_vec_i8(x, R: int, K: int, stream=None):
     """fp32 x [R][K] -> (int8 codes [R][K], fp32 scales [R]), one scale per row."""
-    q = torch.empty((R, K), dtype=torch.int8, device=x.device)
-    s = torch.empty(R, dtype=torch.float32, device=x.device)
+    q = _result((R, K), torch.int8, x, stream)
+    s = _result(R, torch.float32, x, stream)
     _check(lib().qgemv_quantize_vec_i8(_ptr(x), _ptr(q), _ptr(s), R, K, _stream(stream)), "qgemv_quantize_vec_i8")
     return q, s
 
@@ -702,7 +712,7 @@ def gs64_workspace_bytes(N: int, K: int, T: int) -> int:
 
 def gemv_gs64(W, q, s, N: int, K: int, T: int, ws=None, y=None, stream=None) -> torch.Tensor:
     if y is None:
-        y = torch.empty((T, N), dtype=torch.float32, device=W.device)
+        y = _result((T, N), torch.float32, W, stream)
     _check(lib().qgemv_gs64(_ptr(W), _ptr(q), _ptr(s), _ptr(y), N, K, T, _ptr(ws) if ws is not None else None,
                             ws.numel() if ws is not None else 0, _stream(stream)), "qgemv_gs64")
     return y
@@ -711,7 +721,7 @@ def gemv_gs64(W, q, s, N: int, K: int, T: int, ws=None, y=None, stream=None) -> 
 def gemv_gs64_f32(W, x, N: int, K: int, T: int, ws=None, y=None, stream=None) -> torch.Tensor:
     """gs64 GEMV on fp32 activations, quantised per vector inside the launch."""
     if y is None:
-        y = torch.empty((T, N), dtype=torch.float32, device=W.device)
+        y = _result((T, N), torch.float32, W, stream)
     _check(lib().qgemv_gs64_f32(_ptr(W), _ptr(x), _ptr(y), N, K, T, _ptr(ws) if ws is not None else None,
                                 ws.numel() if ws is not None else 0, _stream(stream)), "qgemv_gs64_f32")
     return y
@@ -719,7 +729,7 @@ def gemv_gs64_f32(W, x, N: int, K: int, T: int, ws=None, y=None, stream=None) ->
 
 def block_isums_tc(W, layout: int, xq, N: int, K: int, T: int, f16_image: bool, stream=None) -> torch.Tensor:
     """The tensor-core path's block sums (see qgemv_debug_block_isums_tc)."""
-    out = torch.empty((T, N, K // QK), dtype=torch.int32, device=W.device)
+    out = _result((T, N, K // QK), torch.int32, W, stream)
     _check(lib().qgemv_debug_block_isums_tc(_ptr(W), layout, _ptr(xq), _ptr(out), N, K, T, 1 if f16_image else 0,
                                             _stream(stream)), "qgemv_debug_block_isums_tc")
     return out

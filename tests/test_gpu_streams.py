@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import quantized_q4_weight_gb300 as q
+import synth
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -80,3 +81,17 @@ def test_results_on_the_default_stream_by_name():
     assert torch.cuda.current_stream() == before      # the call leaves the current stream as it was
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(again, want)
+
+
+def test_products_on_a_stream_of_their_own():
+    N, K, T = 512, 256, 3
+    w = q.pack_q4_0(torch.from_numpy(synth.q4_0_weights(1, N, K).reshape(-1)).to(DEV), N, K)
+    x, ws = torch.randn((T, K), device=DEV), q.new_workspace(q.workspace_bytes(N, K, T))
+    xq = q.quantize_q8_0(x, T, K)
+    for call in (lambda s: [q.gemv_f32(w, q.W_PACKED, x, N, K, T, ws, stream=s)],
+                 lambda s: [q.gemv(w, q.W_PACKED, xq, N, K, T, ws, stream=s)],
+                 lambda s: [q.gemv_argmax_f32(w, q.W_PACKED, x, N, K, T, ws, stream=s)],
+                 lambda s: list(q.gemv_top2_f32(w, q.W_PACKED, x, N, K, T, ws, stream=s)),
+                 lambda s: [q.unpack_q4_0(w, N, K, stream=s)],
+                 lambda s: list(q.quantize_vec_i8(x, T, K, stream=s))):
+        on_a_busy_device(call)
