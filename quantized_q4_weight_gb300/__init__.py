@@ -660,7 +660,8 @@ class LogitsRules(_Described):
 def logits_rules(x, rules: LogitsRules, ws, out=None, idx=None, val=None, stream=None):
     """Apply the rules to x [rows][vocab] (fp32, f16, bf16); out (None: not
     written; may be x) receives the results in x's type.  Returns each row's best
-    token (int64, -1 for none) and its value (fp32)."""
+    token (int64, -1 for none) and its value (fp32); a loop that passes idx and val
+    saves their allocation, 0.5 to 1 us a call."""
     r = (_ext or _load_binding()).logits_rules(x, rules.struct, ws, out, idx, val,
                                                None if stream is None else stream.cuda_stream)
     if type(r) is int:

@@ -126,16 +126,6 @@ at::Tensor beside(const at::Tensor &t, at::IntArrayRef sizes, at::ScalarType typ
     return at::detail::empty_cuda(sizes, type, t.device(), std::nullopt);
 }
 
-// The same for a part of another tensor's memory, from `offset` elements of `type` on.
-at::Tensor part_of(const at::Tensor &whole, at::ScalarType type, int64_t n, int64_t offset)
-{
-    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
-                                                            c10::scalarTypeToTypeMeta(type));
-    t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
-    t.unsafeGetTensorImpl()->set_storage_offset(offset);
-    return t;
-}
-
 template <typename F>
 PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F f) noexcept
 {
@@ -271,16 +261,8 @@ PyObject *logits_rules(PyObject *, PyObject *const *a, Py_ssize_t n) noexcept
             need(out->sizes() == x->sizes() && out->stride(1) == 1 && out->scalar_type() == x->scalar_type(),
                  "logits_rules: out of x's shape and type");
         at::Tensor made_idx, made_val;
-        if (!idx && !val) {  // one allocation for both
-            const int64_t rows = spec->rows;
-            const at::Tensor both = beside(*x, {rows + (rows + 1) / 2}, at::kLong, a[6]);
-            made_idx = part_of(both, at::kLong, rows, 0);
-            made_val = part_of(both, at::kFloat, rows, 2 * rows);
-        } else if (!idx) {
-            made_idx = beside(*x, {spec->rows}, at::kLong, a[6]);
-        } else if (!val) {
-            made_val = beside(*x, {spec->rows}, at::kFloat, a[6]);
-        }
+        if (!idx) made_idx = beside(*x, {spec->rows}, at::kLong, a[6]);
+        if (!val) made_val = beside(*x, {spec->rows}, at::kFloat, a[6]);
         if (!idx) idx = &made_idx;
         if (!val) val = &made_val;
         need(idx->scalar_type() == at::kLong && idx->is_contiguous() && idx->numel() == spec->rows &&

@@ -241,3 +241,17 @@ def test_results_made_by_the_call_are_tensors_of_their_own_kind():
     assert gi.dtype == torch.int64 and gv.dtype == torch.float32 and gi.shape == gv.shape == (3,) and gi.is_contiguous()
     assert torch.equal(gi + 1 - 1, gi) and (gv * 2).shape == (3,) and gi.cpu().tolist() == gi.tolist()
     assert gi.device == x.to(DEV).device and not gv.requires_grad
+
+
+def test_results_made_by_the_call_are_saved_together():
+    """Index and value have storages of their own: one type a storage, as a file of tensors wants it."""
+    import io
+    x, d = make(3, 500, 10, 2, torch.float32, 12)
+    gi, gv = call(x, d)
+    assert gi.untyped_storage().data_ptr() != gv.untyped_storage().data_ptr()
+    assert gi.untyped_storage().nbytes() == 24 and gv.untyped_storage().nbytes() == 12
+    f = io.BytesIO()
+    torch.save((gi, gv), f)
+    f.seek(0)
+    a, b = torch.load(f)
+    assert torch.equal(a, gi) and torch.equal(b, gv)
