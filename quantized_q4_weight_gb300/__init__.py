@@ -634,7 +634,12 @@ class LogitsRules(_Described):
             if not x.is_cuda or x.dtype != dtype or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1) or \
                     (x.shape[0] != rows and not (one_row and x.shape[0] == 1)):
                 raise ValueError(f"LogitsRules: {what} [rows][..] {dtype}")
-            return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else 0, x.shape[1]
+            return x.data_ptr(), x.stride(0) if x.shape[0] > 1 and x.shape[1] > 0 else 0, x.shape[1]
+
+        def list_at(address, lengths):
+            # A list without columns has no memory, but its rule is on: any address
+            # tells the library so, and nothing is read there.
+            return address if address or lengths is None else lengths.data_ptr() & ~7
 
         def row(x, what):
             if x is None:
@@ -644,8 +649,10 @@ class LogitsRules(_Described):
             return x.data_ptr()
 
         hp, hs, hn = table(history, torch.int64, "history")
+        hp = None if history is None else list_at(hp, history_len)
         ip, is_, n_ids = table(bias_ids, torch.int64, "bias_ids")
         bp, bs, bn = table(bias, torch.float32, "bias")
+        ip, bp = (None if bias_ids is None else list_at(ip, bias_len)), (None if bias is None else list_at(bp, bias_len))
         mp, ms, mn = table(mask, torch.int32, "mask", one_row=True)
         if (is_, n_ids) != (bs, bn) or (mask is not None and mn * 32 < vocab):
             raise ValueError("LogitsRules: bias_ids and bias of one shape and stride; mask with a bit per token")

@@ -255,3 +255,25 @@ def test_results_made_by_the_call_are_saved_together():
     f.seek(0)
     a, b = torch.load(f)
     assert torch.equal(a, gi) and torch.equal(b, gv)
+
+
+@pytest.mark.parametrize("which", ["hist", "bias", "both"])
+def test_lists_without_columns(which):
+    """The first step of a loop: a history or bias list with room for nothing touches nothing."""
+    x, d = make(3, 700, 4, 3, torch.float32, 13)
+    for name in ("hist", "bias_ids", "bias"):
+        if which == "both" or name.startswith(which):
+            d[name] = np.ascontiguousarray(d[name][:, :0])
+    for name, kind in (("hist_len", "hist"), ("bias_len", "bias")):
+        if which in (kind, "both"):
+            d[name][:] = 0
+    check(x, d)
+    # a length past the bound counts as the bound, and is recorded
+    e = dict(d)
+    name = "bias_len" if which == "bias" else "hist_len"
+    e[name] = d[name].copy()
+    e[name][1] = 1
+    _, idx, val = reference(x.float().numpy(), **d)
+    gi, gv = call(x, e)
+    assert q.device_status() == 7
+    assert np.array_equal(gi.cpu().numpy(), idx) and np.array_equal(gv.cpu().numpy(), val)
