@@ -53,8 +53,9 @@
 // Registers: the launch has 384 threads of 168; the row threads take 208,
 // the other warps 88: 256 * 208 + 128 * 88 = 384 * 168.
 //
-// Every wait is bounded: a block that gives up records QGEMV_ERR_TIMEOUT,
-// waits for its copies and products in flight and frees its tensor memory.
+// Every wait is bounded: a block that gives up records QGEMV_ERR_TIMEOUT and
+// frees its tensor memory.  Every block first waits (bounded) for its copies and
+// products in flight, in their warps, which have nothing else to do by then.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -81,7 +82,7 @@ struct TcCfg {
     static constexpr int NBUF = DP == 64 ? 8 : 5;
     static constexpr int OFF_RING = 2 * TILE;
     static constexpr int OFF_BAR = OFF_RING + NBUF * TILE;
-    static constexpr int NBAR = 2 * NBUF + 9;
+    static constexpr int NBAR = 2 * NBUF + 10;
     static constexpr int OFF_MASK = OFF_BAR + 8 * NBAR;   // [stream][AC_MASKS][4] words
     static constexpr int SMEM = (OFF_MASK + 2 * AC_MASKS * 16 + 15) / 16 * 16 + 1024;  // aligned up to 1024 at run time
 };
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *empty = full + C::NBUF;
     uint64_t *s_full = empty + C::NBUF, *p_full = s_full + 2, *pv_done = p_full + 4,  // [stream]; [stream][half]; [stream]
-             *q_full = pv_done + 2;
+             *q_full = pv_done + 2, *drained = q_full + 1;
     unsigned *masks = reinterpret_cast<unsigned *>(smem + C::OFF_MASK);
     volatile int *abort_flag = &s_abort;
 
@@ -281,6 +282,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             mbar_init(&pv_done[i], 1);
         }
         mbar_init(q_full, 2 * AC_ROWS);
+        mbar_init(drained, 1);
         fence_mbar_init();
     }
     if (warp == 8) {
@@ -381,9 +383,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                     nxt[s] = after;
                 }
             }
-            // After an abort: wait (bounded) for the copies in flight.  A buffer's
-            // earlier fills were complete before it was filled again.
-            if (!ok && lane == 0)
+            // The copies in flight end before the block does (bounded), also where
+            // another warp gives up after this one is done.  A buffer's earlier fills
+            // were complete before it was filled again.
+            if (lane == 0)
                 for (int b = n > C::NBUF ? n - C::NBUF : 0; b < n; ++b)
                     mbar_drain(&full[b % C::NBUF], static_cast<unsigned>((b / C::NBUF) & 1));
             __syncwarp();
@@ -423,7 +426,6 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                     }
                     if (i == w.n[s] - 1) tc_commit_elect(&pv_done[s]);
                 };
-                int scored[2] = {0, 0}, summed[2] = {0, 0};  // tiles issued per stream, for the drain
                 int kbuf = 0, vbuf = 0;                      // the current buffers
                 // One stream's products of tile i: the sums with its weights, then the
                 // scores of the next tile over the columns that those weights leave.
@@ -435,14 +437,12 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                         if (own) vbuf = acquire();
                         if (ok) sums(s, i, vbuf);
                         if (!ok) return;
-                        summed[s] = i + 1;
                         if (last) tc_commit_elect(&empty[vbuf]);
                     }
                     if (i + 1 < w.n[s]) {
                         if (own) kbuf = acquire();
                         if (!ok) return;
                         scores(s, kbuf);
-                        scored[s] = i + 2;
                         if (last) tc_commit_elect(&empty[kbuf]);
                     }
                 };
@@ -451,12 +451,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                     turn(0, i);
                     if (ok) turn(1, i);
                 }
-                if (!ok && lane == 0) {  // after an abort: wait (bounded) for the products in flight
-                    for (int s = 0; s < 2; ++s) {
-                        if (scored[s]) mbar_drain(&s_full[s], static_cast<unsigned>((scored[s] - 1) & 1));
-                        if (summed[s] && summed[s] == w.n[s]) mbar_drain(&pv_done[s], 0);
-                    }
-                }
+                // The products in flight end before the block does, by a commit of its
+                // own (bounded): after an abort, half of a tile's sums, or sums that no
+                // scores follow yet, have no other.
+                tc_commit_elect(drained);
+                if (lane == 0) mbar_drain(drained, 0);
             }
             __syncwarp();
         }
