@@ -673,7 +673,9 @@ size_t qgemv_attn_workspace_bytes(const qgemv_attn_batch *batch, const qgemv_kv_
  * weights enter the product with v rounded to the cache's type, as matrix
  * operands.  Rows that a query does not see never reach its result, whatever
  * they hold.  Results do not depend on the order in which the GPU runs the
- * parts.  ws: qgemv_attn_workspace_bytes, 16-byte aligned. */
+ * parts.  ws: qgemv_attn_workspace_bytes, 16-byte aligned.  o, lse and ws
+ * overlap neither one another nor what is read (the page tables' entries
+ * that the lengths reach among it). */
 qgemv_status qgemv_attn_prefix(const void *q, int64_t q_token_stride, int64_t q_head_stride,
                                const qgemv_kv_cache *cache, const qgemv_attn_batch *batch, void *o,
                                qgemv_dtype o_type, int64_t o_token_stride, int64_t o_head_stride, float *lse_or_null,

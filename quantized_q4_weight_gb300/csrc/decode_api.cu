@@ -21,7 +21,7 @@ inline Span span(const void *p, long long bytes)
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
     return Span{a, a + static_cast<uintptr_t>(bytes)};
 }
-inline bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
+inline bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
 
 inline bool type_ok(int t) { return t == QGEMV_F32 || t == QGEMV_F16 || t == QGEMV_BF16; }
 inline int type_bytes(qgemv_dtype t) { return t == QGEMV_F32 ? 4 : 2; }
@@ -345,16 +345,15 @@ qgemv_status qgemv_attn_prefix(const void *q, int64_t q_token_stride, int64_t q_
     const Span so = span(o, ((tokens - 1) * o_token_stride + heads1 * o_head_stride + d) * ob);
     const Span sq = span(q, ((tokens - 1) * q_token_stride + heads1 * q_head_stride + d) * 2);
     const Span sw = span(ws, a.ws_bytes), sk = cache_span(cache, cache->k), sv = cache_span(cache, cache->v);
+    const Span se = span(lse_or_null, lse_or_null ? 4 * tokens * b.n_q_heads : 0);
     const Span sl = span(b.suffix_len, 4ll * b.n_seqs);
-    if (overlap(so, sq) || overlap(so, sw) || overlap(so, sk) || overlap(so, sv) || overlap(so, sl) ||
-        overlap(sw, sq) || overlap(sw, sk) || overlap(sw, sv) || overlap(sw, sl))
-        return QGEMV_ERR_INVALID_ARG;
-    if (lse_or_null) {
-        const Span se = span(lse_or_null, 4 * tokens * b.n_q_heads);
-        if (overlap(se, so) || overlap(se, sq) || overlap(se, sw) || overlap(se, sk) || overlap(se, sv) ||
-            overlap(se, sl))
-            return QGEMV_ERR_INVALID_ARG;
-    }
+    const Span sp = span(b.prefix_pages, 4 * ceil_div(b.prefix_len, cache->page_size));
+    const long long own = ceil_div(b.max_suffix, cache->page_size);  // pages of a suffix
+    const Span ss = own ? strided(b.suffix_pages, b.n_seqs, b.suffix_pages_stride, own, 4) : Span{0, 0};
+    for (const Span out : {so, se, sw})
+        for (const Span in : {sq, sk, sv, sl, sp, ss})
+            if (overlap(out, in)) return QGEMV_ERR_INVALID_ARG;
+    if (overlap(so, se) || overlap(so, sw) || overlap(se, sw)) return QGEMV_ERR_INVALID_ARG;
 
     AttnParams p = {};
     p.q = q;

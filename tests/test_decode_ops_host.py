@@ -268,3 +268,27 @@ def test_the_binding_takes_the_structures_themselves():
             ext.attn_prefix(None, q.KvCacheStruct(), bad, None, None, None, None)
         with pytest.raises(ValueError, match="rules"):
             ext.logits_rules(None, bad, None, None, None, None, None)
+
+
+ACCEPTED = "past the checks"
+
+
+def outcome(status):
+    """A refusal's status; whatever the device says, or its absence, is past the checks."""
+    return status if status in (INVALID, MISALIGNED, UNSUPPORTED, WORKSPACE) else ACCEPTED
+
+
+@pytest.mark.parametrize("over", ["o", "lse", "ws"])
+def test_attn_refuses_outputs_over_its_page_tables(L, over):
+    # q, o, suffix lengths and tables far apart; 4 sequences, 7 pages of prefix, 10 of suffix each
+    at = dict(o=1 << 31, lse=1 << 32, ws=1 << 38)[over]
+    assert outcome(attn(L)) == ACCEPTED
+    assert attn(L, b=batch(prefix_pages=at)) == INVALID
+    assert attn(L, b=batch(prefix_pages=at - 7 * 4 + 4)) == INVALID
+    assert outcome(attn(L, b=batch(prefix_pages=at - 7 * 4))) == ACCEPTED
+    assert attn(L, b=batch(suffix_pages=at)) == INVALID
+    assert attn(L, b=batch(suffix_pages=at - 4 * 40 + 4)) == INVALID
+    assert outcome(attn(L, b=batch(suffix_pages=at - 4 * 40))) == ACCEPTED
+    # tables that are not read may lie anywhere
+    assert outcome(attn(L, b=batch(prefix_len=0, prefix_pages=at))) == ACCEPTED
+    assert outcome(attn(L, b=batch(max_suffix=0, suffix_pages=at))) == ACCEPTED
