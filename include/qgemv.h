@@ -673,7 +673,8 @@ size_t qgemv_attn_workspace_bytes(const qgemv_attn_batch *batch, const qgemv_kv_
  * weights enter the product with v rounded to the cache's type, as matrix
  * operands.  Rows that a query does not see never reach its result, whatever
  * they hold.  Results do not depend on the order in which the GPU runs the
- * parts.  ws: qgemv_attn_workspace_bytes, 16-byte aligned.  o, lse and ws
+ * parts.  ws: qgemv_attn_workspace_bytes, 16-byte aligned.  The heads of o
+ * lie apart from one another; o, lse and ws
  * overlap neither one another nor what is read (the page tables' entries
  * that the lengths reach among it). */
 qgemv_status qgemv_attn_prefix(const void *q, int64_t q_token_stride, int64_t q_head_stride,

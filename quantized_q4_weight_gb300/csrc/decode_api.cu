@@ -33,6 +33,19 @@ inline Span strided(const void *p, long long n, long long stride, long long last
     return span(p, ((n - 1) * stride + last) * bytes);
 }
 
+// Whether n1 x n2 pieces of d elements at i * s1 + j * s2 lie apart from one another.
+inline bool pieces_apart(long long n1, long long s1, long long n2, long long s2, long long d)
+{
+    if ((n1 == 1 || s1 >= (n2 - 1) * s2 + d) && (n2 == 1 || s2 >= d)) return true;  // the usual orders
+    if ((n2 == 1 || s2 >= (n1 - 1) * s1 + d) && (n1 == 1 || s1 >= d)) return true;
+    if (n1 > 1 && s1 < d) return false;
+    for (long long j = 1; j < n2; ++j) {  // a piece j steps along, against those nearest to it
+        const long long at = j * s2, i = s1 ? std::min(at / s1, n1 - 1) : 0;
+        if (at - i * s1 < d || (i + 1 < n1 && (i + 1) * s1 - at < d)) return false;
+    }
+    return true;
+}
+
 constexpr long long kMaxExtent = 1ll << 46;  // elements of a tensor: products of strides and counts stay in 64 bits
 
 // A product of non-negative counts and strides that stays below kMaxExtent.
@@ -331,7 +344,8 @@ qgemv_status qgemv_attn_prefix(const void *q, int64_t q_token_stride, int64_t q_
     const int d = cache->head_dim, ob = type_bytes(o_type);
     if (!extent_ok(tokens, q_token_stride) || !extent_ok(b.n_q_heads, q_head_stride) ||
         !extent_ok(tokens, o_token_stride) || !extent_ok(b.n_q_heads, o_head_stride) ||
-        !extent_ok(b.n_seqs, b.suffix_pages_stride))
+        !extent_ok(b.n_seqs, b.suffix_pages_stride) ||
+        !pieces_apart(tokens, o_token_stride, b.n_q_heads, o_head_stride, d))
         return QGEMV_ERR_INVALID_ARG;
     if (!aligned(q, 16) || q_token_stride % 8 || q_head_stride % 8 || !aligned(o, ob) || !aligned(b.suffix_len, 4) ||
         !aligned(b.prefix_pages, 4) || !aligned(b.suffix_pages, 4) || !aligned(lse_or_null, 4))

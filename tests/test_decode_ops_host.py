@@ -292,3 +292,36 @@ def test_attn_refuses_outputs_over_its_page_tables(L, over):
     # tables that are not read may lie anywhere
     assert outcome(attn(L, b=batch(prefix_len=0, prefix_pages=at))) == ACCEPTED
     assert outcome(attn(L, b=batch(max_suffix=0, suffix_pages=at))) == ACCEPTED
+
+
+def test_attn_refuses_outputs_that_overlap_themselves(L):
+    # 8 tokens of 12 heads of 128: any order of tokens and heads with distinct pieces
+    for os, oh in ((1536, 128), (128, 1024), (2000, 160), (136, 1200), (3072 // 2, 128), (128 * 12 + 8, 128),
+                   (256, 8 * 256 + 128), (320, 8 * 320 - 160)):
+        assert outcome(attn(L, os=os, oh=oh)) == ACCEPTED, (os, oh)
+    # pieces of two lattices between one another: 12 heads 128 * 16 apart, tokens 128 apart, and interleaved pairs
+    assert outcome(attn(L, os=128, oh=2048)) == ACCEPTED
+    assert outcome(attn(L, b=batch(n_seqs=1, n_q=2, n_q_heads=4), os=384, oh=256 * 3)) == ACCEPTED
+    assert outcome(attn(L, b=batch(n_seqs=1, n_q=2, n_q_heads=4), os=384, oh=256)) == ACCEPTED
+    for os, oh in ((0, 128), (1536, 0), (1535, 128), (1536, 127), (127, 1024), (128, 1023), (1024, 128), (128, 128),
+                   (256, 256), (384, 256), (3 * 128, 2 * 128)):
+        assert attn(L, os=os, oh=oh, ot=q.BF16) == INVALID, (os, oh)
+    # a stride that nothing is reached with does not count
+    assert outcome(attn(L, b=batch(n_seqs=1, n_q=1), os=0)) == ACCEPTED
+    assert outcome(attn(L, c=cache(n_heads=1), b=batch(n_q_heads=1), os=128, oh=0)) == ACCEPTED
+
+
+def test_attn_overlap_rule_against_counting(L):
+    """The rule against a count of the elements, over small lattices."""
+    import random
+    rng = random.Random(4)
+    seen = [0, 0]
+    for _ in range(400):
+        n, heads = rng.randint(1, 6), rng.choice([2, 4, 6])
+        os, oh = rng.randint(0, 40), rng.randint(0, 40)
+        places = [t * os + h * oh for t in range(n) for h in range(heads)]
+        distinct = all(abs(a - b) >= 8 for i, a in enumerate(places) for b in places[:i])
+        got = outcome(attn(L, c=cache(head_dim=8), b=batch(n_seqs=n, n_q=1, n_q_heads=heads), os=os, oh=oh))
+        assert got == (ACCEPTED if distinct else INVALID), (n, heads, os, oh)
+        seen[distinct] += 1
+    assert min(seen) > 50
