@@ -33,6 +33,32 @@ inline Span strided(const void *p, long long n, long long stride, long long last
     return span(p, ((n - 1) * stride + last) * bytes);
 }
 
+// n rows of `width` bytes, `stride` bytes apart.
+struct Rows {
+    const void *p;
+    long long n, stride, width;
+};
+
+// Whether two sets of rows share bytes.  Parts of one row buffer interleave.
+bool rows_overlap(const Rows &a, const Rows &b)
+{
+    const auto all = [](const Rows &r) { return span(r.p, (r.n - 1) * r.stride + r.width); };
+    if (!overlap(all(a), all(b))) return false;
+    // row u of b begins b0 + u * b.stride after row 0 of a
+    const long long b0 = static_cast<long long>(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+    // whether a row at `at` meets one of the rows first + i * stride, 0 <= i < n: the first that ends behind its begin
+    const auto meets = [&](long long at, long long first, long long stride, long long n) {
+        const long long i = at < first + b.width || !stride ? 0 : (at - first - b.width) / stride + 1;
+        return i < n && first + i * stride < at + a.width && first + i * stride + b.width > at;
+    };
+    // of one stride: only the difference of the row numbers matters
+    if (a.stride == b.stride) return meets(0, b0 - (a.n - 1) * b.stride, b.stride, a.n + b.n - 1);
+    if (a.n > 65536) return true;  // not looked through
+    for (long long t = 0; t < a.n; ++t)
+        if (meets(t * a.stride, b0, b.stride, b.n)) return true;
+    return false;
+}
+
 // Whether n1 x n2 pieces of d elements at i * s1 + j * s2 lie apart from one another.
 inline bool pieces_apart(long long n1, long long s1, long long n2, long long s2, long long d)
 {
@@ -250,10 +276,8 @@ qgemv_status qgemv_rope_kv(const qgemv_rope_plan *plan, const void *q, const voi
         if (!aligned(q, ib) || !aligned(q_out, qb)) return QGEMV_ERR_MISALIGNED;
         const bool in_place = q_out == q && q_type == in_type && (q_out_stride == q_stride || n_tokens == 1);
         const Span so = strided(q_out, n_tokens, q_out_stride, w, qb);
-        if (!in_place && overlap(so, strided(q, n_tokens, q_stride, w, ib))) {
-            // the parts of one row buffer interleave: only their bytes must be apart
+        if (!in_place && rows_overlap(Rows{q_out, n_tokens, q_out_stride * qb, w * qb}, Rows{q, n_tokens, q_stride * ib, w * ib}))
             return QGEMV_ERR_INVALID_ARG;
-        }
         if (overlap(so, span(pos, 4 * n_tokens))) return QGEMV_ERR_INVALID_ARG;
     }
     if (k) {
@@ -273,8 +297,10 @@ qgemv_status qgemv_rope_kv(const qgemv_rope_plan *plan, const void *q, const voi
             const long long qw = static_cast<long long>(n_q_heads) * head_dim;
             const Span sq = strided(q, n_tokens, q_stride, qw, ib), so = strided(q_out, n_tokens, q_out_stride, qw, qb);
             if (overlap(sq, sk) || overlap(sq, sv) || overlap(so, sk) || overlap(so, sv)) return QGEMV_ERR_INVALID_ARG;
-            if (q_out != q && (overlap(so, strided(k, n_tokens, k_stride, w, ib)) ||
-                               overlap(so, strided(v, n_tokens, v_stride, w, ib))))
+            // also in place: a block may write a token's q before another reads its k and v
+            const Rows ro{q_out, n_tokens, q_out_stride * qb, qw * qb};
+            if (rows_overlap(ro, Rows{k, n_tokens, k_stride * ib, w * ib}) ||
+                rows_overlap(ro, Rows{v, n_tokens, v_stride * ib, w * ib}))
                 return QGEMV_ERR_INVALID_ARG;
             if (overlap(so, span(slots, 4 * n_tokens))) return QGEMV_ERR_INVALID_ARG;
         }

@@ -325,3 +325,54 @@ def test_attn_overlap_rule_against_counting(L):
         assert got == (ACCEPTED if distinct else INVALID), (n, heads, os, oh)
         seen[distinct] += 1
     assert min(seen) > 50
+
+
+def fused(L, n=10, **kw):
+    """rope on the parts of one fp32 QKV buffer of 12 + 2 + 2 heads of 128, rows 2048 elements apart."""
+    at = 1 << 30
+    f = dict(q=at, k=at + 4 * 1536, v=at + 4 * 1792, qs=2048, ks=2048, vs=2048, n=n, ot=q.F32, o=1 << 36, os=1536)
+    f.update(kw)
+    return rope(L, **f)
+
+
+def test_rope_in_a_fused_buffer(L):
+    at = 1 << 30
+    assert outcome(fused(L)) == ACCEPTED
+    assert outcome(fused(L, o=at, os=2048)) == ACCEPTED                      # in place
+    # in place over k or v: the write of a q head and the read of a k head would race
+    assert fused(L, o=at, os=2048, k=at) == INVALID
+    assert fused(L, o=at, os=2048, v=at) == INVALID
+    assert fused(L, o=at, os=2048, k=at + 4 * 1535) == INVALID
+    assert fused(L, o=at, os=2048, k=at + 4 * (2048 * 3 + 1400)) == INVALID     # another token's q
+    assert fused(L, o=at, os=2048, v=at - 4 * 255) == INVALID
+    assert outcome(fused(L, o=at, os=2048, v=at - 4 * 256)) == ACCEPTED
+    # one token, in place over k
+    assert fused(L, n=1, o=at, os=0, k=at + 4 * 1280) == INVALID
+    # a result between the rows of its inputs touches none of them
+    assert outcome(fused(L, qs=4096, ks=4096, vs=4096, o=at + 4 * 2048, os=4096)) == ACCEPTED
+    assert outcome(fused(L, qs=4096, ks=4096, vs=4096, o=at + 4 * 2048 + 2 * 1024, os=8192, ot=q.BF16)) == ACCEPTED
+    assert fused(L, qs=4096, ks=4096, vs=4096, o=at + 4 * 2047, os=4096) == INVALID
+    assert fused(L, qs=4096, ks=4096, vs=4096, o=at + 4 * 2561, os=4096) == INVALID
+
+
+def test_rope_overlap_rule_against_counting(L):
+    """Rows of k against rows of the result, each of any stride, against a count of the bytes."""
+    import random
+    rng = random.Random(5)
+    seen = [0, 0]
+    c = cache(head_dim=8, n_heads=1, row_stride=8, page_stride=128)
+    for _ in range(600):
+        n, hq = rng.randint(1, 5), rng.randint(1, 3)
+        os, ks = rng.randint(8 * hq, 60), rng.randint(0, 60)
+        if rng.random() < 0.5:
+            ks = os = max(os, ks)
+        ot = rng.choice([q.F32, q.F16])
+        ob = 4 if ot == q.F32 else 2
+        off = 4 * rng.randint(-100, 100)
+        written = {t * os * ob + i for t in range(n) for i in range(8 * hq * ob)}
+        read = {off + t * ks * 4 + i for t in range(n) for i in range(8 * 4)}
+        got = outcome(rope(L, c, rot=8, d=8, hq=hq, n=n, qs=8 * hq, o=1 << 36, os=os, ot=ot, k=(1 << 36) + off, ks=ks,
+                           v=1 << 33, vs=8))
+        assert got == (INVALID if written & read else ACCEPTED), (n, hq, os, ks, ot, off)
+        seen[bool(written & read)] += 1
+    assert min(seen) > 100
