@@ -106,7 +106,13 @@ class SharedPrompt:
         # the prompt's last token is the first step's input, so it opens every sample's own suffix
         self.m, self.shared = model, prompt.numel() - 1
         pre, own = -(-self.shared // page), -(-most // page)
-        assert 1 <= samples <= T_MAX and pre + samples * own <= m.layers[0]["cache"].k.shape[0]
+        if not (1 <= samples <= T_MAX and most >= 1 and prompt.numel() >= 1):
+            raise ValueError(f"1..{T_MAX} samples of at least one token each, after a prompt of at least one")
+        if page % T_MAX:
+            raise ValueError(f"pages of {page} rows: a chunk of {T_MAX} tokens must lie in one page")
+        if pre + samples * own > m.layers[0]["cache"].k.shape[0]:
+            raise ValueError("the model's cache has too few pages for the prompt and the samples")
+        self.left = most  # steps that the samples' pages and histories have room for
         self.prefix_pages = torch.arange(pre, dtype=torch.int32, device=DEV)
         self.own_pages = pre + torch.arange(samples * own, dtype=torch.int32, device=DEV).view(samples, own)
         self.lens = torch.zeros(samples, dtype=torch.int32, device=DEV)
@@ -143,6 +149,9 @@ class SharedPrompt:
 
     def step(self):
         """One token for every sample; returns them (int64 [samples])."""
+        if self.left == 0:
+            raise RuntimeError("the samples' pages are full")
+        self.left -= 1
         m, page = self.m, self.m.page
         pos = self.shared + self.lens
         own = self.own_pages[self.rows, (self.lens // page).long()]
@@ -170,7 +179,7 @@ def main():
     s.step()
     torch.cuda.synchronize()
     t = time.perf_counter()
-    out = [s.step().clone() for _ in range(a.tokens - 1)]
+    out = [s.step().clone() for _ in range(a.tokens)]
     torch.cuda.synchronize()
     t = time.perf_counter() - t
     assert q.device_status() == 0

@@ -111,3 +111,31 @@ def test_decode_matches_the_plain_forms(ex, monkeypatch):
         ref.tokens = tokens[i]
         err = (got[i] - ref.last_logits).norm(dim=1) / ref.last_logits.norm(dim=1)
         assert float(err.max()) < 6 / 127, (i, float(err.max()))
+
+
+SMALL = dict(d_model=256, d_ff=512, heads=4, kv_heads=2, head_dim=64, vocab=2000, layers=1, rope_base=1e4)
+
+
+@pytest.mark.parametrize("most", [1, 16, 17])
+def test_a_step_past_the_samples_pages_is_refused(ex, most):
+    """Before anything is launched: the page and history of a further token do not exist."""
+    s = ex.SharedPrompt(ex.Model(pages=16, **SMALL), torch.arange(20, device="cuda"), 2, most)
+    for _ in range(most):
+        s.step()
+    lens = s.lens.clone()
+    with pytest.raises(RuntimeError, match="full"):
+        s.step()
+    assert torch.equal(s.lens, lens) and q.device_status() == 0
+
+
+def test_prompts_and_pages_that_do_not_fit_are_refused(ex):
+    m = ex.Model(pages=16, **SMALL)
+    prompt = torch.arange(20, device="cuda")
+    for args in ((prompt, 9, 4), (prompt, 0, 4), (prompt, 2, 0), (prompt[:0], 2, 4), (prompt, 8, 40)):
+        with pytest.raises(ValueError):
+            ex.SharedPrompt(m, *args)
+    with pytest.raises(ValueError, match="one page"):
+        ex.SharedPrompt(ex.Model(pages=64, page_size=4, **SMALL), prompt, 2, 4)
+    s = ex.SharedPrompt(m, prompt[:1], 2, 4)          # a prompt of one token: nothing is shared
+    s.step()
+    assert q.device_status() == 0
