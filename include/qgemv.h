@@ -671,7 +671,8 @@ size_t qgemv_attn_workspace_bytes(const qgemv_attn_batch *batch, const qgemv_kv_
  * exp(scale * q.k), fp32 [token][n_q_heads], -infinity for such a query.
  * Scores, maxima, sums and outputs are accumulated in fp32; the softmax
  * weights enter the product with v rounded to the cache's type, as matrix
- * operands.  Rows that a query does not see never reach its result, whatever
+ * operands, for an fp32 o too (f16: to half a unit of it, or 2^-31 of the row's
+ * largest weight).  Rows that a query does not see never reach its result, whatever
  * they hold.  Results do not depend on the order in which the GPU runs the
  * parts.  ws: qgemv_attn_workspace_bytes, 16-byte aligned.  The heads of o
  * lie apart from one another; o, lse and ws

@@ -49,6 +49,14 @@ constexpr int AT_KEYS = 64;    // keys of a stage
 constexpr int AT_RING = 8;     // row-offset ring (tiles)
 constexpr float AT_NEG = -1e30f;  // below every finite score; differences of it stay finite
 
+// Weights are taken 2^AT_LIFT times as large where they enter the product with
+// v as f16, which has no exponents below 2^-24: the largest is 1024 instead of 1,
+// and what is 2^-35 of it still counts, not 2^-25 (a part of 1024 keys may hold one
+// that stands that far above the others).  m holds the reference, so sums and
+// parts know nothing of it.  bf16 has fp32's exponents.
+template <typename T>
+constexpr float AT_LIFT = std::is_same<T, __half>::value ? 10.0f : 0.0f;
+
 template <int DP>
 struct AttnCfg {
     static constexpr int STAGES = DP == 64 ? 4 : DP == 128 ? 3 : 2;
@@ -236,7 +244,7 @@ struct WarpTile {
                 for (int n = 0; n < 2 * NK; ++n) mx = fmaxf(mx, fmaxf(s[i][n][2 * hh], s[i][n][2 * hh + 1]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-                const float mn = fmaxf(m[i][hh], mx * scale_log2);
+                const float mn = fmaxf(m[i][hh], mx * scale_log2 - AT_LIFT<T>);
                 const float c = ex2(m[i][hh] - mn);
                 float sum = 0.0f;
 #pragma unroll
@@ -245,8 +253,9 @@ struct WarpTile {
                     const float w1 = ex2(fmaf(s[i][n][2 * hh + 1], scale_log2, -mn));
                     sum += w0 + w1;
                     // The weights enter the product with v as its type's operands, off by
-                    // half a unit of it at most (the largest, 1, by nothing): as much as
-                    // one value of v.  The sum keeps them whole, so lse loses nothing.
+                    // half a unit of it at most (the largest, a power of two, by nothing):
+                    // as much as one value of v, with an fp32 output too.  The sum keeps
+                    // them whole, so lse loses nothing.
                     pf[i][n >> 1][2 * (n & 1) + hh] = Mma<T>::pack(w0, w1);
                 }
                 m[i][hh] = mn;

@@ -37,8 +37,9 @@
 //
 // The reference m of a row is its running maximum, but follows it only when
 // that rises by more than 2^8: O is rescaled (in tensor memory, by the row's
-// own thread) in few tiles instead of all, and the weights stay below 2^8,
-// exact in scale.  l sums the unrounded weights in fp32.
+// own thread) in few tiles instead of all, and the weights stay below 2^8 (f16:
+// 2^14), exact in scale.  They enter the product with v rounded to the cache's
+// type; l sums the unrounded weights in fp32.
 //
 // K and V tiles share a ring of buffers in the 128-byte-swizzled layout the
 // products read: rows of 64 elements, halves of the head side by side.  K is
@@ -74,6 +75,10 @@ constexpr int AC_ROWS = 128;      // rows of a stream
 constexpr int AC_MASKS = 8;       // tiles whose presence masks are kept, per stream: the ring holds fewer
 constexpr float AC_RISE = 8.0f;   // rise of the maximum (base 2) that moves the reference
 constexpr float AC_NEG = -1e30f;
+// f16 weights lie 2^6 times as high, below 2^14 with the rise (see AT_LIFT in
+// attn_prefix.cu): what is 2^-31 of the largest or more counts.
+template <typename T>
+constexpr float AC_LIFT = std::is_same<T, __half>::value ? 6.0f : 0.0f;
 
 template <int DP>
 struct TcCfg {
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             for (int c = 8; c < AC_KEYS; c += 8)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mm[e] = fmaxf(mm[e], fmaxf(x[c + 2 * e], x[c + 2 * e + 1]));
-            const float mx = fmaxf(fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * p.scale_log2, AC_NEG);
+            const float mx = fmaxf(fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * p.scale_log2, AC_NEG) - AC_LIFT<T>;
             if (i == 0) {
                 m = mx;
             } else {

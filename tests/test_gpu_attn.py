@@ -477,3 +477,41 @@ class Wide(Case):
 def test_very_tall_batches_on_short_prefixes(prefix):
     for b, nq, hq, hkv in ((228, 8, 64, 8), (227, 8, 64, 8), (456, 4, 64, 8)):
         Wide(b, nq, hq, hkv, 64, prefix, [(5 * i) % 12 for i in range(b)], seed=prefix + b).check()
+
+
+# One key far above all others, whose values are all that there is to see.  The
+# weights of the others are 2^-27 of the largest: below f16's exponents when the
+# largest is 1, and a sum of a thousand of them is what the result consists of.
+# Tolerance: that of the module without its n 2^-25, instead of which a weight is
+# off by at most 2^-31 of the row's largest, w_max; so n 2^-31 w_max max |v|.
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("b,nq,hq,hkv,d,prefix,own,every", [
+    (40, 1, 16, 8, 64, 0, 1024, 1 << 20),        # ranges of 1024 own keys, the first key far above
+    (40, 1, 16, 8, 128, 0, 1024, 1 << 20),
+    (3, 8, 8, 8, 256, 0, 1024, 64),
+    (2, 1, 64, 2, 64, 4000, 2, 64),              # 64 rows: tiles of 16 rows a warp
+    (12, 4, 16, 2, 128, 13000, 4, 128),          # the tcgen05 kernel, one such key in every tile
+    (16, 1, 64, 8, 64, 7425, 8, 128),
+])
+def test_weights_far_below_the_largest_count(b, nq, hq, hkv, d, prefix, own, every, dtype):
+    c = Wide(b, nq, hq, hkv, d, prefix, [own] * b, page=64, dtype=dtype, poison=False, seed=b, scale=math.log(2.0))
+    c.q.zero_()
+    c.q[..., 0] = 1.0
+    c.k.zero_()
+    c.v.copy_(50 + 50 * torch.rand(c.v.shape, device=DEV))
+    for table, n in [(c.prefix_pages, prefix)] + [(t, own) for t in c.suffix_pages]:
+        j = torch.arange(0, n if prefix == 0 or table is c.prefix_pages else 0, every, device=DEV)
+        c.k[table.long()[j // 64], j % 64, :, 0] = 27.0
+        c.v[table.long()[j // 64], j % 64] = 0.0
+    out = torch.empty(c.q.shape, device=DEV)
+    c.run(out=out)
+    ref, A, lse, e = c.exact()
+    assert q.device_status() == 0
+    u, n = HALF_UNIT[dtype], prefix + own
+    w_max = torch.exp(27.0 * math.log(2.0) - lse)[..., None]
+    tol = (u + 2 * (e + 2.0 ** -21) + 2.0 ** -12 + 2.0 ** -24) * A
+    if dtype == torch.float16:
+        tol = tol + n * 2.0 ** -31 * w_max * 100.0
+    got = out.double().view(ref.shape)
+    assert bool((tol < ref / 4).all())               # so zeros would not do
+    assert bool(((got - ref).abs() <= tol).all()), float(((got - ref).abs() / ref).max())
