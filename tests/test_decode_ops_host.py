@@ -376,3 +376,37 @@ def test_rope_overlap_rule_against_counting(L):
         assert got == (INVALID if written & read else ACCEPTED), (n, hq, os, ks, ot, off)
         seen[bool(written & read)] += 1
     assert min(seen) > 100
+
+
+def test_attn_workspace_against_bounds(L):
+    """Over sizes on both sides of every threshold: a whole number of partial rows a row,
+    at least one for each kind of keys there is and at most one per 64 keys (per
+    stream of 128 rows where two streams share the key tiles), and no less for more
+    sequences, more rows to a head or longer contexts than a small part of them needs."""
+    import random
+    rng = random.Random(6)
+    kinds = set()
+    for _ in range(4000):
+        kv, group, nq, d = rng.choice([1, 2, 8, 32]), rng.choice([1, 4, 7, 16]), rng.randint(1, 8), rng.choice([64, 128, 192, 256])
+        n = int(2 ** rng.uniform(0, 9))
+        prefix = rng.choice([0, 1, 63, 64, 100, 127, 128, 129, int(2 ** rng.uniform(0, 18))])
+        own = rng.choice([0, 1, nq - 1, nq, 64, 100, int(2 ** rng.uniform(0, 16))])
+        c = cache(n_heads=kv, head_dim=d, row_stride=kv * d, page_stride=16 * kv * d, head_stride=d)
+        b = batch(n_seqs=n, n_q=nq, n_q_heads=kv * group, prefix_len=prefix, max_suffix=own)
+        rows = n * nq * kv * group
+        bytes_ = attn_ws(L, b, c)
+        assert bytes_ >= 16384
+        parts, rest = divmod(bytes_ - 16384, rows * (4 * d + 8))
+        assert rest == 0
+        shared = max(0, own - nq + 1)
+        assert (prefix > 0) + (shared > 0) <= parts <= -(-prefix // 64) + -(-shared // 64) + 1, (n, nq, kv, group, prefix, own)
+        # attn_prefix asks for exactly this much
+        at = dict(q=1 << 40, o=1 << 41, lse=1 << 42, ws=1 << 43, qt=kv * group * d, qh=d, os=kv * group * d, oh=d)
+        c.k, c.v = 1 << 44, 1 << 45
+        assert attn(L, c=c, b=b, ws_bytes=bytes_ - 1, **at) == WORKSPACE
+        assert outcome(attn(L, c=c, b=b, ws_bytes=bytes_, **at)) == ACCEPTED
+        kinds.add((prefix > 0, shared > 0, n * nq * group > 64, parts > 2))
+    assert len(kinds) >= 12
+    # more of anything never needs less than the keys and rows themselves ask for
+    sizes = [attn_ws(L, batch(n_seqs=n, prefix_len=100000), cache()) for n in (1, 2, 4, 8, 16, 32)]
+    assert sizes == sorted(sizes) and sizes[-1] > sizes[0]

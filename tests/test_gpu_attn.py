@@ -515,3 +515,59 @@ def test_weights_far_below_the_largest_count(b, nq, hq, hkv, d, prefix, own, eve
     got = out.double().view(ref.shape)
     assert bool((tol < ref / 4).all())               # so zeros would not do
     assert bool(((got - ref).abs() <= tol).all()), float(((got - ref).abs() / ref).max())
+
+
+@pytest.mark.parametrize("b,nq,hq,hkv,d,prefix", [(5, 2, 8, 2, 64, 2000), (3, 1, 12, 2, 128, 160), (12, 4, 16, 2, 128, 13000),
+                                                  (10, 1, 56, 8, 128, 7700), (40, 3, 8, 2, 96, 300)])
+def test_other_sequences_beside(b, nq, hq, hkv, d, prefix):
+    """A sequence's result is its own: the same bits whatever the others of its batch
+    hold, and within both errors' bounds of its result in a batch of another size."""
+    top = 150
+    c = Case(b, nq, hq, hkv, d, prefix, [(i * 37) % (top + 1) for i in range(b)], max_suffix=top, poison=False, seed=b + d)
+    o, lse = (t.clone() for t in c.check())
+    mine = 1
+    keep = c.q.view(b, nq, hq, d)[mine].clone()
+    # other queries, lengths, own keys and values in all but one sequence
+    c.q.normal_()
+    c.q.view(b, nq, hq, d)[mine] = keep
+    for i in range(b):
+        if i != mine:
+            rows = c.suffix_pages[i].long()
+            c.k[rows], c.v[rows] = torch.randn_like(c.k[rows]), float("nan")
+            c.v[rows[:2]] = 5.0
+            c.len_t[i] = (11 * i + 3) % (2 * c.page)
+    lse2 = torch.empty_like(lse)
+    o2 = c.run(lse=lse2)
+    assert torch.equal(o2.view(b, nq, hq, d)[mine], o.view(b, nq, hq, d)[mine])
+    assert torch.equal(lse2.view(b, nq, hq)[mine], lse.view(b, nq, hq)[mine])
+    # alone: another split of its keys
+    alone = q.AttnBatch(1, nq, hq, c.cache, prefix, c.prefix_pages, c.len_t[mine:mine + 1].clone(),
+                        c.suffix_pages[mine:mine + 1].clone(), top)
+    a = q.attn_prefix(keep, alone, q.new_workspace(alone.workspace_bytes()))
+    assert q.device_status() == 0
+    c.b, c.lens, c.q = 1, [c.lens[mine]], keep
+    c.suffix_pages = c.suffix_pages[mine:mine + 1]
+    ref, A, _, e = c.exact()
+    tol = (2.0 ** -8 + 2 * (e + 2.0 ** -21) + 2.0 ** -12) * A + 2.0 ** -8 * ref.abs() + 1e-30
+    for got in (a, o2.view(b, nq, hq, d)[mine]):
+        assert bool(((got.double().view(ref.shape) - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("b", [16, 17])      # 128 rows a head: streams over alternate keys; 136: pairs of row tiles
+def test_offsets_past_32_bits_through_tensor_maps(b):
+    """A cache of more than 2^32 elements, a tall batch's long prefix at its far end."""
+    page, hkv, d, prefix = 256, 8, 128, 7700
+    pages = 2 ** 32 // (page * hkv * d) + 60
+    if torch.cuda.mem_get_info()[0] < 4 * pages * page * hkv * d * 2:
+        pytest.skip("needs 40 GB of device memory")
+    small = Case(b, 4, 16, hkv, d, prefix, [4 + i for i in range(b)], page=page, dtype=torch.float16, poison=False, seed=b)
+    n = small.k.shape[0]
+    k = torch.zeros((pages, page, hkv, d), dtype=torch.float16, device=DEV)
+    v = torch.zeros_like(k)
+    k[-n:], v[-n:] = small.k, small.v
+    shift = pages - n
+    batch = q.AttnBatch(b, 4, 16, q.KvCache(k, v), prefix, small.prefix_pages + shift, small.len_t, small.suffix_pages + shift,
+                        max(small.lens))
+    got = q.attn_prefix(small.q, batch, small.ws)
+    assert torch.equal(got, small.run()) and q.device_status() == 0
+    small.check()
