@@ -152,8 +152,8 @@ __device__ __forceinline__ long long key_row(const AttnParams &p, const int32_t 
            static_cast<long long>(j & ((1 << p.page_shift) - 1)) * p.row_stride;
 }
 
-// The suffix rows that every query of a sequence sees: all but the last
-// n_q - 1 (never negative).
+// A sequence's suffix length within its bounds.  All its queries see all but
+// the last n_q - 1 of these rows.
 __device__ __forceinline__ int suffix_length(const AttnParams &p, int b)
 {
     const int n = __ldg(p.suffix_len + b);

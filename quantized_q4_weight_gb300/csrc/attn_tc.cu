@@ -599,8 +599,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
     tc_fence_after();
     if (warp == 8)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
-    // The suffix parts' launch may still be running: this one, which the
-    // combining launch waits for, ends after it.
+    // The part launch may still be running: this one, which the combining launch
+    // waits for, ends after it (see launch_pdl).
     pdl_wait();
 }
 

@@ -35,6 +35,10 @@ inline cudaError_t allow_smem(const void *kernel, size_t bytes, std::atomic<unsi
 
 // Launch with programmatic dependent launch: the kernel may start while the
 // preceding one drains and touches memory only after its griddepcontrol.wait.
+// The one exception, the prefix kernel behind the attention's part launch
+// (attn_tc.cu), rests on two conditions: that launch lets it in only after its
+// own wait, so what came before is complete, and the prefix kernel waits before it
+// ends, so that its successor's wait covers both.
 template <typename... Params, typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
                               Args &&...args)
@@ -129,12 +133,12 @@ struct AttnParams {
     int p_first;               // slots before the prefix part's own: the tcgen05 kernel's
     int s_tile, s_tiles, s_splits, s_keys;
     int p_blocks;              // blocks of the prefix part
-    // the prefix part on tcgen05 instead (attn_tc.cu; p_blocks is 0 then):
-    // mode 1: pairs of 128-row tiles, one slot per split; 2: one row tile,
-    // two slots per split; 0: not used
+    // the prefix's whole tiles of 128 keys on tcgen05 (attn_tc.cu), the blocks
+    // above take what is left of it; mode 1: pairs of 128-row tiles, one slot per
+    // split; 2: one row tile, two slots per split; 0: not used
     int t_mode, t_tiles, t_splits, t_keys, t_blocks;
-    int t_len;                 // keys that it takes: whole tiles of the prefix; the blocks above take the rest
-    int t_wait;                // no launch of this call precedes it
+    int t_len;                 // keys that it takes
+    int t_wait;                // no launch of this call precedes it (no rest, no suffix)
     float4 *part_o;            // [slot][hkv] sums weighted with 2^(score - m), a row's elements 4 c .. at
                                //   row * o_row + c * o_four: rows innermost after the tcgen05 kernel, else outermost
     long long o_row, o_four;
