@@ -6,7 +6,8 @@
 // call on top of the 4 us of the launch.
 //
 // A function returns its result, or the status code (an int) of a refused
-// call; tensors of a wrong shape or type raise ValueError.
+// call; tensors of a wrong shape or type raise ValueError, a result that does
+// not fit the device torch's OutOfMemoryError, as from the package's other calls.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -126,6 +127,15 @@ at::Tensor beside(const at::Tensor &t, at::IntArrayRef sizes, at::ScalarType typ
     return at::detail::empty_cuda(sizes, type, t.device(), std::nullopt);
 }
 
+void raise_out_of_memory(const char *what)
+{
+    PyObject *torch = PyImport_ImportModule("torch");
+    PyObject *type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type) PyErr_SetString(type, what);
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
+}
+
 template <typename F>
 PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F f) noexcept
 {
@@ -137,6 +147,8 @@ PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F f) noexcept
         return f();
     } catch (const Refused &e) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, e.what());
+    } catch (const c10::OutOfMemoryError &e) {
+        raise_out_of_memory(e.what_without_backtrace());
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     } catch (...) {

@@ -235,3 +235,13 @@ def test_heads_before_rows_and_another_stream():
     want[slots.long()] = x.half()       # position 0: no rotation
     assert torch.equal(k.transpose(1, 2).reshape(-1, hkv, d), want)
     assert torch.equal(v.transpose(1, 2).reshape(-1, hkv, d), want)
+
+
+def test_a_result_that_does_not_fit_is_out_of_memory():
+    """As torch raises it: a caller that frees something and tries again catches that type."""
+    x = torch.zeros((1, 4, 256), device=DEV).expand(1 << 30, 4, 256)      # 4 TB of results
+    pos = torch.zeros((1,), dtype=torch.int32, device=DEV)
+    with pytest.raises(torch.cuda.OutOfMemoryError):
+        q.rope_kv(q.rope_plan(64, 1e4), x, None, None, pos)
+    y = torch.randn((1, 4, 256), device=DEV)
+    assert torch.equal(q.rope_kv(q.rope_plan(64, 1e4), y, None, None, pos), y) and q.device_status() == 0
