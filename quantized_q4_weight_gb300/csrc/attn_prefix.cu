@@ -244,7 +244,8 @@ struct WarpTile {
                 for (int n = 0; n < 2 * NK; ++n) mx = fmaxf(mx, fmaxf(s[i][n][2 * hh], s[i][n][2 * hh + 1]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-                const float mn = fmaxf(m[i][hh], mx * scale_log2 - AT_LIFT<T>);
+                // rounded up, so that no weight exceeds 2^AT_LIFT however large the scores
+                const float mn = fmaxf(m[i][hh], __fadd_ru(__fmul_ru(mx, scale_log2), -AT_LIFT<T>));
                 const float c = ex2(m[i][hh] - mn);
                 float sum = 0.0f;
 #pragma unroll

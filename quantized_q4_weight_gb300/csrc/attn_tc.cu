@@ -521,11 +521,13 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             for (int c = 8; c < AC_KEYS; c += 8)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mm[e] = fmaxf(mm[e], fmaxf(x[c + 2 * e], x[c + 2 * e + 1]));
-            const float mx = fmaxf(fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * p.scale_log2, AC_NEG) - AC_LIFT<T>;
+            // rounded up, and the rise's bound down, so that the weights stay below 2^(rise + lift) for scores of any size
+            const float top = fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3]));
+            const float mx = __fadd_ru(fmaxf(__fmul_ru(top, p.scale_log2), AC_NEG), -AC_LIFT<T>);
             if (i == 0) {
                 m = mx;
             } else {
-                const bool rise = mx > m + AC_RISE;
+                const bool rise = mx > __fadd_rd(m, AC_RISE);
                 if (__any_sync(0xFFFFFFFFu, rise)) {
                     // O holds the sums of the tiles before; they are complete: the
                     // scores of this tile were issued after them

@@ -571,3 +571,60 @@ def test_offsets_past_32_bits_through_tensor_maps(b):
     got = q.attn_prefix(small.q, batch, small.ws)
     assert torch.equal(got, small.run()) and q.device_status() == 0
     small.check()
+
+
+# Scores so large that rounding the largest one's product with the scale moves it
+# by whole units: tied keys must still share the weight, and nothing may overflow.
+# The scores are exact in fp32 (one product each), the others lie 2^20 below, so
+# the result is the mean of the tied keys' values: of 16-bit values times one
+# weight, half a unit of it (u A) and the sums' roundings apart.
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("b,nq,hq,hkv,d,prefix,own", [(3, 2, 4, 2, 64, 300, 40), (2, 1, 64, 2, 128, 500, 10),
+                                                      (12, 4, 16, 2, 128, 13000, 4), (16, 1, 64, 8, 64, 7425, 8)])
+def test_tied_scores_of_any_size(b, nq, hq, hkv, d, prefix, own, dtype):
+    for size in (2.0 ** 20, 2.0 ** 24, 2.0 ** 26, 2.0 ** 27):
+        c = Wide(b, nq, hq, hkv, d, prefix, [own] * b, page=64, dtype=dtype, poison=False, seed=b, scale=0.3)
+        kk = 2.0 ** 14                               # q stays within f16 at every size
+        # q k scale log2(e) from size / 2 to size, in as many steps as there are rows
+        steps = torch.linspace(0.5, 1.0, c.q.shape[0] * hq, device=DEV).view(c.q.shape[0], hq)
+        c.q.zero_()
+        c.q[..., 0] = (size / (kk * 0.3 * 1.4427) * steps).to(dtype)
+        c.k.zero_()
+        j = torch.arange(0, prefix, 7, device=DEV)
+        c.k[c.prefix_pages.long()[j // 64], j % 64, :, 0] = kk
+        out = torch.empty(c.q.shape, device=DEV)
+        lse = torch.empty((b * nq, hq), device=DEV)
+        c.run(out=out, lse=lse)
+        assert q.device_status() == 0
+        tied = c.v[c.prefix_pages.long()[j // 64], j % 64].double()
+        want = tied.mean(0).repeat_interleave(hq // hkv, 0).expand(b * nq, hq, d)
+        mag = tied.abs().mean(0).repeat_interleave(hq // hkv, 0)
+        assert bool(((out.double() - want).abs() <= (HALF_UNIT[dtype] + 2.0 ** -12) * mag).all()), size
+        l64 = 0.3 * kk * c.q[..., 0].double() + math.log(j.numel())
+        assert bool(((lse.double() - l64).abs() <= 2.0 ** -22 * l64).all()), size
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_a_maximum_that_rises_little_at_large_scores(dtype):
+    """Scores near 2^26.1 in powers of two, a later one 6.9 above the first tile's: less
+    than the rise that moves the tcgen05 kernel's reference, but with the roundings of
+    both products with the scale (up to 4 each) more.  Both scores are exact in fp32;
+    the result is (v2 + w v1) / (1 + w) with w = exp(-0.3 * 16), to half a unit of the
+    weights and the sums' 2^-12."""
+    c = Wide(12, 4, 16, 2, 128, 13000, [4] * 12, page=64, dtype=dtype, poison=False, seed=50, scale=0.3)
+    c.q.zero_()
+    c.q[..., 0], c.q[..., 1] = 16384.0, 1.0
+    c.k.zero_()
+    place = [(c.prefix_pages.long()[j // 64], j % 64) for j in (5, 300)]
+    for at, low in zip(place, (0.0, 16.0)):
+        c.k[at][:, 0], c.k[at][:, 1] = 10240.0, low
+    out, lse = torch.empty(c.q.shape, device=DEV), torch.empty((48, 16), device=DEV)
+    c.run(out=out, lse=lse)
+    assert q.device_status() == 0
+    v1, v2 = (c.v[at].double() for at in place)
+    w = math.exp(-4.8)
+    want, mag = (v2 + w * v1) / (1 + w), (v2.abs() + w * v1.abs()) / (1 + w)
+    want, mag = (t.repeat_interleave(8, 0).expand(48, 16, 128) for t in (want, mag))
+    assert bool(((out.double() - want).abs() <= (HALF_UNIT[dtype] + 2.0 ** -12) * mag).all())
+    l64 = 0.3 * (16384.0 * 10240.0 + 16.0) + math.log1p(w)
+    assert bool(((lse.double() - l64).abs() <= 2.0 ** -22 * l64).all())
