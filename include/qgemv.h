@@ -667,8 +667,9 @@ size_t qgemv_attn_workspace_bytes(const qgemv_attn_batch *batch, const qgemv_kv_
  * q and o are [token][head][head_dim] with strides in elements between
  * tokens and heads, q of the cache's type, 16-byte aligned with strides
  * multiples of 8; o of the cache's type or fp32.  A query that sees no row,
- * or none whose score (in powers of two) lies above -1e30, gives zeros.  lse (or NULL) receives the natural logarithm of the sum of
- * exp(scale * q.k), fp32 [token][n_q_heads], -infinity for such a query.
+ * or none whose score (in powers of two) lies above -1e30, gives zeros.  lse
+ * (or NULL) receives the natural logarithm of the sum of exp(scale * q.k),
+ * fp32 [token][n_q_heads], -infinity for such a query.
  * Scores, maxima, sums and outputs are accumulated in fp32; the softmax
  * weights enter the product with v rounded to the cache's type, as matrix
  * operands, for an fp32 o too (f16: to half a unit of it, or 2^-31 of the row's

@@ -759,7 +759,7 @@ cudaError_t launch_combine(const AttnParams &p, cudaStream_t st)
     const dim3 grid(one ? rows : (rows + 7) / 8, heads);
     // warps that share a row's parts: as many as fill the multiprocessors about once
     const unsigned blocks = grid.x * grid.y;
-    int splits = one ? 8 : blocks <= 152 ? 4 : blocks <= 304 ? 2 : 1;
+    int splits = one ? 8 : blocks <= ATTN_SMS ? 4 : blocks <= 2 * ATTN_SMS ? 2 : 1;
     // but none without a batch of parts of its own, and past one wave of warps
     // (16 a multiprocessor) none with fewer than four batches: with eight warps
     // whatever the parts, 480 rows of 31 parts took 15.1 us a call instead of 13.5,
@@ -767,7 +767,7 @@ cudaError_t launch_combine(const AttnParams &p, cudaStream_t st)
     // instead of 5.5.
     const int parts = p.p_first + p.p_splits + p.s_splits;
     const long long warps = one ? static_cast<long long>(rows) * heads * groups : 0;
-    while (splits > 1 && splits / 2 * (warps * splits <= 16 * 152 ? CB_BATCH : 4 * CB_BATCH) >= parts) splits /= 2;
+    while (splits > 1 && splits / 2 * (warps * splits <= 16 * ATTN_SMS ? CB_BATCH : 4 * CB_BATCH) >= parts) splits /= 2;
     while (splits > 1 && groups * splits > 32) splits /= 2;
     const unsigned threads = static_cast<unsigned>(groups * splits * 32);
     const size_t smem = static_cast<size_t>((splits - 1) * groups * 32) * (sizeof(float4) + sizeof(float2));

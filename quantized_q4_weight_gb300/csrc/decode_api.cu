@@ -136,11 +136,10 @@ qgemv_status check_batch(const qgemv_attn_batch *b, const qgemv_kv_cache *c)
     return QGEMV_OK;
 }
 
-// The split of a launch.  Depends on the sizes alone (the workspace query
-// has no device), for 152 multiprocessors with two blocks each.
+// The split of a launch, for two blocks a multiprocessor.
 qgemv_status plan_attn(const qgemv_attn_batch *b, const qgemv_kv_cache *c, AttnPlan &a)
 {
-    constexpr long long kSlots = 304;
+    constexpr long long kSlots = 2 * ATTN_SMS;
     a.group = b->n_q_heads / c->n_heads;
     a.rows = b->n_seqs * b->n_q * a.group;
     a.p_tile = attn_tile_rows(a.rows, c->head_dim);
@@ -174,9 +173,9 @@ qgemv_status plan_attn(const qgemv_attn_batch *b, const qgemv_kv_cache *c, AttnP
         const int streams = a.t_mode == 2 ? 2 : 1;
         long long best = 1, best_cost = INT64_MAX;
         for (int waves = 1; waves <= 16; ++waves) {  // the most ranges whose blocks make so many waves
-            const long long n = std::min(units, std::max(1ll, waves * 152ll / base));
+            const long long n = std::min(units, std::max(1ll, waves * static_cast<long long>(ATTN_SMS) / base));
             const long long each = ceil_div(units, n), ranges = ceil_div(units, each);
-            const long long cost = ceil_div(base * ranges, 152) * (ceil_div(each, streams) + 2) * 8192 +
+            const long long cost = ceil_div(base * ranges, ATTN_SMS) * (ceil_div(each, streams) + 2) * 8192 +
                                    ranges * streams * a.rows * c->n_heads;
             if (cost < best_cost) best_cost = cost, best = n;
         }

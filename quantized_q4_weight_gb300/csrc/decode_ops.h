@@ -148,6 +148,11 @@ struct AttnParams {
     float *lse;
     unsigned *status;
 };
+// Multiprocessors that the attention's splits are made for (a GB300's).  Not the
+// device's own count: the workspace query knows no device, and the order in
+// which a row's parts are added, so its bits, follows from the sizes alone.
+constexpr int ATTN_SMS = 152;
+
 // Rows of a tile for a part with `rows` rows per cache head (attn_prefix.cu).
 int attn_tile_rows(int rows, int d);
 bool attn_tc_takes(const qgemv_kv_cache &c);  // whether a cache's layout suits it
