@@ -24,8 +24,8 @@
 // second forms.
 //
 // Measured: 1024 rows x 8 heads x 65536 keys of 128 elements 186 us, 1.48
-// PFLOP/s (0.79 of the measured bf16 rate), products 69 % of the time; 320
-// rows x 2 heads x 32749 keys 20 us.  A pair of tiles of 128 keys takes 2850
+// PFLOP/s (0.76 of the measured bf16 burst rate, 0.87 of the sustained one),
+// products 64 % of the time; 320 rows x 2 heads x 32749 keys 20 us.  A pair of tiles of 128 keys takes 2850
 // cycles, the products' own 2048: the rest is handing over between the row
 // threads and the products, twice a tile and stream.  A block of few tiles
 // spends 3 us before its first scores (tensor memory, page table, first keys)

@@ -264,7 +264,10 @@ __global__ void __launch_bounds__(ROPE_THREADS, 8) rope_vec_kernel(const __grid_
     }
 }
 
-// One pair of a head a thread, any alignment and even sizes.
+// One pair of a head a thread, any alignment and even sizes.  Bound by its
+// instructions: a sine for every pair of every head, and accesses of one element.
+// 16384 tokens of 32 + 8 + 8 heads of 128, fp32, take 361 us (the bytes alone 90),
+// 16122 of 14 + 2 + 2 of 64, bf16, 75 (11); one token 2.0, as with wide accesses.
 template <typename TI, typename TQ, typename TC, bool HALF>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_any_kernel(const __grid_constant__ RopeParams p)
 {
