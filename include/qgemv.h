@@ -736,6 +736,204 @@ qgemv_status qgemv_logits_rules(const void *logits, qgemv_dtype type, int64_t x_
                                 void *out, int64_t out_stride, int64_t *idx, float *val, void *ws, size_t ws_bytes,
                                 qgemv_stream_t stream);
 
+/* Norms of q and k, head by head, before the rotation (RMS norm):
+ * y[i] = x[i] / sqrt(mean of x^2 over the head + eps) * weight[i].
+ * q_weight and k_weight: fp32 [head_dim], device, 4-byte aligned; eps > 0. */
+typedef struct {
+    const float *q_weight;
+    const float *k_weight;
+    float eps;
+} qgemv_qk_norm;
+
+/* qgemv_rope_kv with q and k normed first, all in one pass: the norm's
+ * statistics, its result and the rotation stay in fp32, rounded once at the end.
+ * v is copied.  Without a cache (cache NULL; v and slots are then ignored)
+ * the rotated k goes to k_out [t][h][head_dim], n_k_heads heads, of q_type,
+ * k_out_stride elements between tokens: for a cache that another call writes
+ * (qgemv_kv8_append).  With a cache k_out is ignored and n_k_heads must be the
+ * cache's.  head_dim is even and at most 256; the other rules are
+ * qgemv_rope_kv's; q_out and k_out must not overlap the weights or each other. */
+qgemv_status qgemv_norm_rope_kv(const qgemv_rope_plan *plan, const qgemv_qk_norm *norm, const void *q, const void *k,
+                                const void *v, qgemv_dtype in_type, int64_t q_stride, int64_t k_stride,
+                                int64_t v_stride, const int32_t *pos, const int32_t *slots, int64_t n_tokens,
+                                int n_q_heads, int n_k_heads, int head_dim, void *q_out, qgemv_dtype q_type,
+                                int64_t q_out_stride, void *k_out, int64_t k_out_stride, const qgemv_kv_cache *cache,
+                                qgemv_stream_t stream);
+
+/* A paged key/value cache of 8-bit codes, with one fp32 scale for each block of
+ * block_size rows and head: a value is code * scale.  Codes are int8
+ * (-127..127) or e4m3 (four exponent bits, three fraction bits, +-448 at most).
+ * Row r of page g, head h starts at k (or v) + g * page_stride +
+ * r * row_stride + h * head_stride bytes; a head's codes are contiguous.  Its
+ * scale is k_scale (or v_scale)[g * scale_page_stride + (r / block_size) *
+ * scale_block_stride + h * scale_head_stride].  page_size and block_size are
+ * powers of two, 16 <= block_size <= page_size; head_dim % 16 == 0,
+ * 16 <= head_dim <= 256.  k and v are 16-byte aligned and their strides
+ * multiples of 16; different places must not overlap. */
+typedef enum { QGEMV_CODE_INT8 = 0, QGEMV_CODE_E4M3 = 1 } qgemv_code_type;
+typedef struct {
+    void *k;
+    void *v;
+    float *k_scale;
+    float *v_scale;
+    qgemv_code_type type;
+    int64_t n_pages;
+    int page_size;
+    int block_size;
+    int n_heads;
+    int head_dim;
+    int64_t page_stride;
+    int64_t row_stride;
+    int64_t head_stride;
+    int64_t scale_page_stride;
+    int64_t scale_block_stride;
+    int64_t scale_head_stride;
+} qgemv_kv8_cache;
+
+/* A batch over such a cache.  Sequence b has lens[b] rows; row j is row
+ * j % page_size of page pages[b * pages_stride + j / page_size] (int32, device;
+ * entries past a length are not read).  A length outside [0, max_len] counts as
+ * the nearer end and a page outside the cache as absent (its rows are neither
+ * written nor seen); both record QGEMV_ERR_BAD_ID.
+ * Each sequence has n_q queries (1..8), the last n_q of its rows: query i is at
+ * p = lens[b] - n_q + i and sees the rows j <= p, with a window > 0 only those
+ * with j > p - window or j < sinks.  n_q_heads is a multiple of the cache's
+ * n_heads; query head h reads cache head h / (n_q_heads / n_heads).  n_q,
+ * n_q_heads, window, sinks and scale are the attention's; qgemv_kv8_append uses
+ * n_q alone (and only without `first`). */
+typedef struct {
+    int n_seqs;
+    int n_q;
+    int n_q_heads;
+    int max_len;
+    const int32_t *lens;
+    const int32_t *pages;
+    int64_t pages_stride;
+    int window; /* 0: all rows */
+    int sinks;  /* first rows that stay visible under a window */
+    float scale; /* of the scores; 0 means 1 / sqrt(head_dim) */
+} qgemv_kv8_batch;
+
+/* Write the last rows of every sequence.  Sequence b's are tokens
+ * first[b] .. first[b + 1] - 1 of k and v (first: int32 [n_seqs + 1], device),
+ * or, with first NULL, tokens b * n_q .. b * n_q + n_q - 1; they become its rows
+ * lens[b] - n .. lens[b] - 1.  k and v are [token][head][head_dim] of in_type,
+ * heads head_dim apart, tokens k_stride and v_stride elements apart, n_tokens in
+ * all; max_new bounds the tokens of a sequence.  A sequence with more tokens
+ * than max_new or than rows, or with tokens outside [0, n_tokens), is left as it
+ * is and records QGEMV_ERR_BAD_ID.
+ * For every block with new rows and every head, k and v each, with s the
+ * block's scale if it held rows of the sequence before, else 0, and Q = 127 or 448:
+ *   s' = max(s, max |x| / Q) over the new rows' values x;
+ *   a new value's code is x * (1 / s') rounded to the nearest code, ties to even;
+ *   where s' > s an old code c becomes c * (s * (1 / s')), rounded the same.
+ * Each step is one fp32 operation; codes are held to +-Q; s' = 0 gives codes
+ * 0, and NaN counts as 0 in the maximum and becomes code 0.  An infinite value
+ * gives its block an infinite scale.  Rows from lens[b] on are left as they are.
+ * Two sequences must not share a page that is written. */
+qgemv_status qgemv_kv8_append(const void *k, const void *v, qgemv_dtype in_type, int64_t k_stride, int64_t v_stride,
+                              int64_t n_tokens, const qgemv_kv8_cache *cache, const qgemv_kv8_batch *batch,
+                              const int32_t *first, int max_new, qgemv_stream_t stream);
+
+/* Workspace bytes of qgemv_attn_kv8 (0 for an invalid batch). */
+size_t qgemv_attn_kv8_workspace_bytes(const qgemv_kv8_batch *batch, const qgemv_kv8_cache *cache);
+
+/* o[b * n_q + i][h] = softmax over the rows the query sees of scale * q.k,
+ * times v.  q and o are [token][head][head_dim] with strides in elements
+ * between tokens and heads, q f16 or bf16, 16-byte aligned with strides
+ * multiples of 8; o of q's type or fp32.  A query that sees no row, or none
+ * whose score (in powers of two) lies above -1e30, gives zeros.  lse (or NULL)
+ * receives the natural logarithm of the sum of exp(scale * q.k), fp32
+ * [token][n_q_heads], -infinity for such a query.
+ * Scores, maxima, sums and outputs are accumulated in fp32.  The matrix
+ * operands are f16: codes are exact in it; q's bf16 values are, down to 2^-14 of
+ * the row's largest (smaller ones to 2^-25 of it); a softmax weight times its
+ * block's scale of v is rounded to it (to 2^-34 of the row's largest at least).
+ * What rows that a query does not see hold never reaches it; NaN codes of e4m3,
+ * which qgemv_kv8_append never writes, make the results of those that see them
+ * meaningless.  Results do not depend on the order in which the GPU runs the
+ * parts.  ws: qgemv_attn_kv8_workspace_bytes, 16-byte aligned.  The heads of o
+ * lie apart from one another; o, lse and ws overlap neither one another nor what
+ * is read. */
+qgemv_status qgemv_attn_kv8(const void *q, qgemv_dtype q_type, int64_t q_token_stride, int64_t q_head_stride,
+                            const qgemv_kv8_cache *cache, const qgemv_kv8_batch *batch, void *o, qgemv_dtype o_type,
+                            int64_t o_token_stride, int64_t o_head_stride, float *lse_or_null, void *ws,
+                            size_t ws_bytes, qgemv_stream_t stream);
+
+/* A step of beam search: n_groups searches of n_beams beams each (1..16) over a
+ * vocabulary, n_best (1..32) continuations wanted of each search.
+ *   scores [n_groups][n_beams] fp32: the beams' running scores (sums of logarithms
+ *     of probabilities); -infinity for a beam that is not alive.
+ *   done [n_groups][n_beams] int32 or NULL: a token for a beam that has ended (its
+ *     one continuation, at its running score; its logits are not read), -1 for
+ *     the others. */
+typedef struct {
+    int n_groups;
+    int n_beams;
+    int n_best;
+    int64_t vocab;
+    const float *scores;
+    const int32_t *done;
+} qgemv_beam_spec;
+
+/* Workspace bytes of qgemv_beam_select (0 for an invalid shape). */
+size_t qgemv_beam_workspace_bytes(const qgemv_beam_spec *spec);
+
+/* The best continuations of each search.  Row r = group * n_beams + beam of
+ * logits (fp32, f16 or bf16, rows x_stride elements apart) gives token t
+ *   s(r, t) = scores[r] + x[r][t] - log(sum over u of exp(x[r][u])).
+ * score, token and parent [n_groups][n_best] (fp32, int64, int32) receive the
+ * n_best largest, best first, with their tokens and rows r.  Among equal
+ * logits of a row the lower token comes first, among equal s of two rows the
+ * lower row; s is compared as formed from fp32 maxima and sums in 64 bits,
+ * rounded once for `score`.  Logits of -infinity and NaN continue nothing and
+ * count nothing in the sum; a row with a logit of +infinity, a NaN score or none
+ * above -infinity, continues nothing.  Places without a continuation get
+ * -infinity, -1, -1.  ws: qgemv_beam_workspace_bytes, 16-byte aligned, its first
+ * 16 KB zero before the first use (they are zero again after each call). */
+qgemv_status qgemv_beam_select(const void *logits, qgemv_dtype type, int64_t x_stride, const qgemv_beam_spec *spec,
+                               float *score, int64_t *token, int32_t *parent, void *ws, size_t ws_bytes,
+                               qgemv_stream_t stream);
+
+/* Reorder sequences by parent, as after a step of beam search, or to begin
+ * several sequences from one.  For every i < n_out with p = parents[i]:
+ *   lens_out[i] = n = lens[p];
+ *   pages_out[i][j] = pages[p][j] for j < n / page_size (shared pages);
+ *   pages_out[i][n / page_size] = fresh[i], a page of the row's own for its next
+ *     row, and the n % page_size rows that the parent's page there holds are copied
+ *     to it, in every cache (with the scales of their blocks).
+ * fresh[i] == -1 keeps the parent's page there instead (nothing is copied; no
+ * entry is written where n % page_size == 0), fresh[i] equal to the parent's page
+ * copies nothing.  Entries from there on are left as they are, and so is row i
+ * where parents[i] is -1.  parents and fresh: int32 [n_out]; lens: int32 [n_in];
+ * pages: int32 [n_in][pages_stride], pages_out [n_out][out_stride], n_columns
+ * entries a row in both.
+ * A parent outside [-1, n_in) counts as -1, a length outside
+ * [0, n_columns * page_size] as the nearer end, a page of fresh outside the caches as
+ * -1, a parent's page outside them as one without rows: each records
+ * QGEMV_ERR_BAD_ID.  Where the row is full (n == n_columns * page_size) fresh is
+ * ignored.  Pages that fresh names must be different and, but for a row's own
+ * parent's, must not be pages that another row is copied from. */
+typedef struct {
+    int n_in;
+    int n_out;
+    int n_columns;
+    const int32_t *parents;
+    const int32_t *lens;
+    const int32_t *pages;
+    int64_t pages_stride;
+    const int32_t *fresh;
+    int32_t *pages_out;
+    int64_t out_stride;
+    int32_t *lens_out;
+} qgemv_fork;
+
+/* n_caches caches (layers) of one kind, of the same page count, page size and block
+ * size: 16-bit ones or 8-bit ones, the other pointer NULL.  Host arrays, read
+ * during the call.  One launch for each 64 caches. */
+qgemv_status qgemv_fork_pages(const qgemv_fork *fork, const qgemv_kv_cache *caches, const qgemv_kv8_cache *caches8,
+                              int n_caches, qgemv_stream_t stream);
+
 /* Test hook: the exact per-block integer sums the GEMV kernels form,
  * isums[T][N][K/32] int32 (device), from the same unpack / int8-dot code. */
 qgemv_status qgemv_debug_block_isums(const void *W, qgemv_wlayout layout, const void *xq,

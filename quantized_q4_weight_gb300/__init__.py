@@ -3,8 +3,9 @@ Q8_0-activation decode GEMV on one GB300.
 
 Argument marshalling only: every step runs in the library's CUDA kernels.
 Most calls go through ctypes; those of the decode step between its GEMVs
-(rope_kv, attn_prefix, logits_rules) through the compiled _binding.so,
-because their kernels are shorter than the marshalling.
+(rope_kv, attn_prefix, logits_rules and those over an 8-bit cache and of beam
+search) through the compiled _binding.so, because their kernels are shorter than
+the marshalling.
 Tensors supply device pointers; work is enqueued on the current torch CUDA
 stream.  The library is loaded from this directory (libqgemv.so, built by
 ``quantized_q4_weight_gb300._build.build()``); if it is missing, every call
@@ -64,6 +65,8 @@ class GatherF32Matrix(ctypes.Structure):
 
 F32, F16, BF16 = 0, 1, 2
 _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+CODE_INT8, CODE_E4M3 = 0, 1
+_CODES = {torch.int8: CODE_INT8, torch.float8_e4m3fn: CODE_E4M3}
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}
 
@@ -95,6 +98,36 @@ class AttnBatchStruct(ctypes.Structure):
                 ("prefix_len", ctypes.c_int), ("prefix_pages", ctypes.c_void_p), ("suffix_len", ctypes.c_void_p),
                 ("suffix_pages", ctypes.c_void_p), ("suffix_pages_stride", ctypes.c_int64),
                 ("max_suffix", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class QkNormStruct(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class Kv8CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("type", ctypes.c_int), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int), ("block_size", ctypes.c_int),
+                ("n_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("scale_page_stride", ctypes.c_int64),
+                ("scale_block_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64)]
+
+
+class Kv8BatchStruct(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("n_q", ctypes.c_int), ("n_q_heads", ctypes.c_int), ("max_len", ctypes.c_int),
+                ("lens", ctypes.c_void_p), ("pages", ctypes.c_void_p), ("pages_stride", ctypes.c_int64),
+                ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class BeamSpec(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int), ("n_beams", ctypes.c_int), ("n_best", ctypes.c_int), ("vocab", ctypes.c_int64),
+                ("scores", ctypes.c_void_p), ("done", ctypes.c_void_p)]
+
+
+class ForkStruct(ctypes.Structure):
+    _fields_ = [("n_in", ctypes.c_int), ("n_out", ctypes.c_int), ("n_columns", ctypes.c_int), ("parents", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("pages", ctypes.c_void_p), ("pages_stride", ctypes.c_int64),
+                ("fresh", ctypes.c_void_p), ("pages_out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("lens_out", ctypes.c_void_p)]
 
 
 class LogitsSpec(ctypes.Structure):
@@ -162,6 +195,14 @@ _SIGS = {
     "qgemv_attn_prefix": ([_VP, _I64, _I64, _VP, _VP, _VP, _I32, _I64, _I64, _VP, _VP, _SZ, _VP], _I32),
     "qgemv_logits_workspace_bytes": ([_VP], _SZ),
     "qgemv_logits_rules": ([_VP, _I32, _I64, _VP, _VP, _I64, _VP, _VP, _VP, _SZ, _VP], _I32),
+    "qgemv_norm_rope_kv": ([_VP, _VP, _VP, _VP, _VP, _I32, _I64, _I64, _I64, _VP, _VP, _I64, _I32, _I32, _I32, _VP, _I32,
+                            _I64, _VP, _I64, _VP, _VP], _I32),
+    "qgemv_kv8_append": ([_VP, _VP, _I32, _I64, _I64, _I64, _VP, _VP, _VP, _I32, _VP], _I32),
+    "qgemv_attn_kv8_workspace_bytes": ([_VP, _VP], _SZ),
+    "qgemv_attn_kv8": ([_VP, _I32, _I64, _I64, _VP, _VP, _VP, _I32, _I64, _I64, _VP, _VP, _SZ, _VP], _I32),
+    "qgemv_beam_workspace_bytes": ([_VP], _SZ),
+    "qgemv_beam_select": ([_VP, _I32, _I64, _VP, _VP, _VP, _VP, _VP, _SZ, _VP], _I32),
+    "qgemv_fork_pages": ([_VP, _VP, _VP, _I32, _VP], _I32),
     "qgemv_debug_block_isums": ([_VP, _I32, _VP, _VP, _I64, _I64, _I32, _VP], _I32),
     "qgemv_debug_block_isums_tc": ([_VP, _I32, _VP, _VP, _I64, _I64, _I32, _I32, _VP], _I32),
     "qgemv_debug_stream_read": ([_VP, _SZ, _I32, _I32, _I32, _I32, _VP, _VP], _I32),
@@ -674,6 +715,151 @@ def logits_rules(x, rules: LogitsRules, ws, out=None, idx=None, val=None, stream
     if type(r) is int:
         _check(r, "qgemv_logits_rules")
     return r
+
+
+# ------------------------------------- over an 8-bit cache, and beam search
+
+class QkNorm(_Described):
+    """Weights fp32 [head_dim] and eps of the norms of q and k, head by head (see
+    qgemv_qk_norm); one may be None where that side is not rotated."""
+
+    def __init__(self, q_weight, k_weight, eps: float = 1e-6):
+        for w in (q_weight, k_weight):
+            if w is not None and (not w.is_cuda or w.dtype != torch.float32 or w.dim() != 1 or not w.is_contiguous()):
+                raise ValueError("QkNorm: weights fp32 [head_dim], contiguous")
+        if q_weight is not None and k_weight is not None and q_weight.numel() != k_weight.numel():
+            raise ValueError("QkNorm: weights of one head_dim")
+        self.weights = (q_weight, k_weight)
+        some = k_weight if q_weight is None else q_weight
+        self.head_dim = 0 if some is None else some.numel()
+        self.struct = QkNormStruct(None if q_weight is None else q_weight.data_ptr(),
+                                   None if k_weight is None else k_weight.data_ptr(), eps)
+
+
+def norm_rope_kv(plan: RopePlan, norm: QkNorm, xq, xk, xv=None, pos=None, slots=None, cache: KvCache | None = None,
+                 out=None, k_out=None, stream=None):
+    """rope_kv with q and k normed head by head first.  Without a cache the rotated k goes to
+    k_out (of out's type, default for out too), and v is the caller's to write
+    (kv8_append); xv and slots are then None.  Returns out."""
+    if (xk if xq is None else xq).shape[-1] != norm.head_dim:
+        raise ValueError("norm_rope_kv: norm of q's and k's head_dim")
+    r = (_ext or _load_binding()).norm_rope_kv(plan, norm.struct, xq, xk, xv, pos, slots,
+                                               None if cache is None else cache.struct, out, k_out,
+                                               None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        _check(r, "qgemv_norm_rope_kv")
+    return r
+
+
+class Kv8Cache(_Described):
+    """A paged cache of 8-bit codes: k and v int8 or float8_e4m3fn [pages][page_size][heads][head_dim] of the same
+    strides, k_scale and v_scale fp32 [pages][page_size / block_size][heads] of the same strides (see
+    qgemv_kv8_cache; other orders by transposed views, as KvCache)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.stride(3) != 1 or \
+                k.dtype not in _CODES:
+            raise ValueError("Kv8Cache: k and v int8 or float8_e4m3fn [pages][page_size][heads][head_dim] of the same strides")
+        if k_scale.dim() != 3 or k_scale.shape != v_scale.shape or k_scale.stride() != v_scale.stride() or \
+                k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or k_scale.shape[0] != k.shape[0] or \
+                k_scale.shape[2] != k.shape[2] or k_scale.shape[1] < 1 or k.shape[1] % k_scale.shape[1]:
+            raise ValueError("Kv8Cache: k_scale and v_scale fp32 [pages][page_size / block_size][heads] of the same strides")
+        if not (k.is_cuda and all(x.device == k.device for x in (v, k_scale, v_scale))):
+            raise ValueError("Kv8Cache: CUDA tensors of one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.struct = Kv8CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _CODES[k.dtype],
+                                     k.shape[0], k.shape[1], k.shape[1] // k_scale.shape[1], k.shape[2], k.shape[3],
+                                     k.stride(0), k.stride(1), k.stride(2), *k_scale.stride())
+
+
+class Kv8Batch(_Described):
+    """Sequences over an 8-bit cache (see qgemv_kv8_batch): lens int32 [n_seqs] and pages int32 [n_seqs][pages that
+    hold max_len rows] are device tensors that later calls read again, so a decode loop updates them in
+    place.  window 0: every row is visible; sinks: first rows visible under a window; scale None: 1 / sqrt(head_dim)."""
+
+    def __init__(self, n_seqs: int, n_q: int, n_heads: int, cache: Kv8Cache, lens, pages, max_len: int, window: int = 0,
+                 sinks: int = 0, scale: float | None = None):
+        if max_len > 0 and (pages.dim() != 2 or pages.shape[0] != n_seqs or (pages.shape[1] > 1 and pages.stride(1) != 1) or
+                            pages.shape[1] * cache.struct.page_size < max_len or not pages.is_cuda or
+                            pages.dtype != torch.int32):
+            raise ValueError("Kv8Batch: pages int32 [n_seqs][pages that hold max_len rows]")
+        self.cache, self.tables = cache, (lens, pages)
+        self.n_seqs, self.n_q, self.n_heads = n_seqs, n_q, n_heads
+        self.struct = Kv8BatchStruct(n_seqs, n_q, n_heads, max_len, _i32(lens, "Kv8Batch: lens", n_seqs),
+                                     pages.data_ptr() if max_len > 0 else None, pages.stride(0) if max_len > 0 else 0,
+                                     window, sinks, 0.0 if scale is None else scale)
+
+    def workspace_bytes(self) -> int:
+        """Of attn_kv8."""
+        return int(lib().qgemv_attn_kv8_workspace_bytes(self.address, self.cache.address))
+
+
+def kv8_append(xk, xv, batch: Kv8Batch, first=None, max_new: int | None = None, stream=None) -> None:
+    """Write k and v [tokens][kv heads][head_dim] (fp32, f16, bf16) as the last rows of the batch's sequences, whose lens
+    count them already: n_q of each, or, with first int32 [n_seqs + 1], tokens first[b] .. first[b + 1] - 1 of
+    sequence b, at most max_new of each (default: all of them)."""
+    r = (_ext or _load_binding()).kv8_append(xk, xv, batch.cache.struct, batch.struct, first, max_new,
+                                             None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        _check(r, "qgemv_kv8_append")
+
+
+def attn_kv8(xq, batch: Kv8Batch, ws, out=None, lse=None, stream=None):
+    """Attention of q [n_seqs][n_q][heads][head_dim] (or [tokens][heads][head_dim]; f16 or bf16) over the batch's rows; out
+    (q's type or fp32, q's shape; default: a new tensor of q's type); lse fp32 [tokens][heads] or None."""
+    r = (_ext or _load_binding()).attn_kv8(xq, batch.cache.struct, batch.struct, ws, out, lse,
+                                           None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        _check(r, "qgemv_attn_kv8")
+    return r
+
+
+class BeamStep(_Described):
+    """A step of `groups` beam searches of `beams` beams each (see qgemv_beam_spec): scores fp32 [groups][beams] and done
+    int32 [groups][beams] (or None) are device tensors that later calls read again."""
+
+    def __init__(self, groups: int, beams: int, vocab: int, n_best: int, scores, done=None):
+        for x, dtype, what in ((scores, torch.float32, "scores fp32"), (done, torch.int32, "done int32")):
+            if x is not None and (not x.is_cuda or x.dtype != dtype or not x.is_contiguous() or x.numel() != groups * beams):
+                raise ValueError(f"BeamStep: {what} [groups][beams], contiguous")
+        self.groups, self.beams, self.vocab, self.n_best, self.tensors = groups, beams, vocab, n_best, (scores, done)
+        self.struct = BeamSpec(groups, beams, n_best, vocab, scores.data_ptr(), None if done is None else done.data_ptr())
+
+    def workspace_bytes(self) -> int:
+        return int(lib().qgemv_beam_workspace_bytes(self.address))
+
+
+def beam_select(x, step: BeamStep, ws, score=None, token=None, parent=None, stream=None):
+    """The n_best best continuations of each search on logits x [groups * beams][vocab] (fp32, f16, bf16), best first: their
+    scores (fp32), tokens (int64) and rows of x (int32), each [groups][n_best]; -infinity, -1, -1 for none."""
+    r = (_ext or _load_binding()).beam_select(x, step.struct, ws, score, token, parent,
+                                              None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        _check(r, "qgemv_beam_select")
+    return r
+
+
+class PagePool:
+    """The caches of all layers, KvCache or Kv8Cache, of one shape: what fork_pages copies in."""
+
+    def __init__(self, caches):
+        caches = list(caches)
+        if not caches or any(type(c) is not type(caches[0]) for c in caches) or \
+                not isinstance(caches[0], (KvCache, Kv8Cache)):
+            raise ValueError("PagePool: caches, all KvCache or all Kv8Cache")
+        self.caches = caches
+        self.eight_bit = isinstance(caches[0], Kv8Cache)
+        self.structs = ((Kv8CacheStruct if self.eight_bit else KvCacheStruct) * len(caches))(*[c.struct for c in caches])
+
+
+def fork_pages(pool: PagePool, parents, lens, pages, fresh, pages_out, lens_out, stream=None) -> None:
+    """Reorder sequences by parent (see qgemv_fork): row i of pages_out and lens_out becomes a child of row parents[i] of
+    pages int32 [rows][columns] and lens int32 [rows], sharing its whole pages; fresh[i] becomes the page of its next row,
+    with the rows of the parent's partly filled page copied to it in every cache of the pool."""
+    r = (_ext or _load_binding()).fork_pages(pool.structs, pool.eight_bit, parents, lens, pages, fresh, pages_out, lens_out,
+                                             None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        _check(r, "qgemv_fork_pages")
 
 
 def block_isums(W, layout: int, xq, N: int, K: int, T: int, stream=None) -> torch.Tensor:

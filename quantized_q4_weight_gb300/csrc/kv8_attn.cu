@@ -1,0 +1,724 @@
+// kv8_attn.cu -- attention over a paged cache of 8-bit codes with a scale for
+// each block of rows and head, under a sliding window with first rows that stay
+// visible (minfer README "How it works": GQA attention whose keys are split
+// over blocks and whose partial results are combined).
+//
+//   s_j = scale ks_j (q . c_j),  o = sum_j 2^(s_j) vs_j d_j / sum_j 2^(s_j)
+// with codes c_j of k and d_j of v, scales ks_j and vs_j of their blocks, and
+// log2 e folded into scale.  Scales enter where a score or a weight is
+// formed, never element by element: w_j = 2^(s_j + log2 vs_j - m) is the matrix
+// operand of the product with d_j, with m a running reference near the largest
+// s_j + log2 vs_j of the row, and l sums w_j / vs_j in fp32.  So a row's largest
+// contribution has the operand's full precision however the scales differ.
+// m is raised only when a weight would pass 2^14 (it is then put 2^10 below the
+// largest): after the first tiles almost never, which saves the shuffles of a
+// maximum and the scaling of the sums for each tile.
+//
+// The products are transposed: scores = K Q^T and sums = V^T P^T, keys or
+// elements of a head on the 16 rows of mma.sync, the few query rows of a cache head
+// on its 8 columns, so that a group of up to 8 heads wastes nothing.  A thread's
+// operands of K are 16 consecutive bytes of a row (the order of d in the
+// contraction is free, Q's fragments have the same), of V 16 consecutive bytes of
+// each of four rows, joined by byte permutations.  The weights pass from the one
+// layout to the other by movmatrix.
+//
+// A warp streams tiles of 16 keys through a ring of its own in shared
+// memory, by cp.async: every thread copies exactly the bytes that it will read, so
+// only the scales need a barrier (of the warp).  The eight warps of a block take
+// a unit's tiles in turn and merge at its end.  A unit is a sequence, cache
+// head and tile of query rows.  Ragged batches are balanced on the device: the
+// tiles of all units in one line are cut into as many equal ranges as there are
+// blocks; a unit that a range's end cuts leaves its sums in the workspace (two
+// parts a block at most), and a second launch joins them.  Units of few tiles get
+// a block each and need no second launch.
+#include "kv8_ops.h"
+#include "qgemv_internal.cuh"
+
+namespace qg {
+namespace {
+
+constexpr int K8_WARPS = 8, K8_THREADS = 32 * K8_WARPS;
+constexpr float K8_NEG = -1e30f;   // below every finite score; differences of it stay finite
+constexpr float K8_LIFT = 10.0f;   // a new reference lies so far below the largest score
+constexpr float K8_SLACK = 14.0f;  // weights reach 2^14 before it moves (f16 ends at 2^16)
+
+template <int DP, int NT>
+struct K8Cfg {
+    static constexpr int KC = DP >= 64 ? DP / 64 : 1;     // 64-element chunks of a row of K
+    static constexpr int VB = DP == 64 ? 8 : 16;          // bytes of a row of V that a thread takes at once
+    static constexpr int VC = DP / (8 * VB);              // such pieces
+    static constexpr int MT = VC * VB / 2;                // 16-row tiles of the sums: DP / 16
+    static constexpr int TILE = 2 * KV8_KEYS * DP;        // bytes of a tile, K and V
+    static constexpr int BLOCKS = DP == 256 || (DP == 128 && NT > 2) ? 1 : 2;
+    static constexpr int STAGES = DP == 64 ? 6 : DP == 128 && NT > 2 ? 6 : 3;
+    static constexpr bool QREG = DP * NT <= 256;          // Q's fragments in registers
+    static constexpr int OFF_META = K8_WARPS * STAGES * TILE;            // per warp and stage: j0, ks, vs
+    static constexpr int OFF_Q = OFF_META + K8_WARPS * STAGES * 16;
+    static constexpr int OFF_QS = OFF_Q + 8 * NT * DP * 2;
+    static constexpr int OFF_ML = OFF_QS + 8 * NT * 4;
+    static constexpr int SMEM = OFF_ML + K8_WARPS * 8 * NT * 8;
+    static_assert(STAGES >= NT, "the warps' sums fit the ring");
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp8(uint32_t dst, const void *src, bool take)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(take ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void *src, bool take)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(take ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mma(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0, unsigned b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ unsigned movm(unsigned a)
+{
+    unsigned d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+__device__ __forceinline__ unsigned pack(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const unsigned *>(&h);
+}
+
+// Four codes as f16, exactly: bytes 0 and 1 to lo, 2 and 3 to hi.
+template <int CODE>
+__device__ __forceinline__ void cvt4(unsigned w, unsigned &lo, unsigned &hi)
+{
+    if constexpr (CODE == QGEMV_CODE_INT8) {
+        w ^= 0x80808080u;  // 0..255; 0x6400 | b is 1024 + b
+        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+        const unsigned x = __byte_perm(w, 0x64646464u, 0x4140), y = __byte_perm(w, 0x64646464u, 0x4342);
+        const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&x), off);
+        const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&y), off);
+        lo = *reinterpret_cast<const unsigned *>(&a), hi = *reinterpret_cast<const unsigned *>(&b);
+    } else {
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    }
+}
+// e4m3's NaN codes (a row that no one has written may hold them) as 0.
+__device__ __forceinline__ unsigned without_nan(unsigned w)
+{
+    return w & ~__vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+}
+
+// What a sequence's queries see of it, in tiles: the tiles of the first rows,
+// then all from the earliest query's window on.
+struct Seen {
+    int n;      // rows
+    int lead;   // tiles before the gap
+    int gap;    // tiles left out
+    int tiles;
+
+    __device__ __forceinline__ Seen(const Kv8AttnParams &p, int len)
+    {
+        n = len < 0 ? 0 : len > p.max_len ? p.max_len : len;
+        const int first = p.window ? max(0, n - p.n_q + 1 - p.window) : 0;
+        lead = (min(p.sinks, first) + KV8_KEYS - 1) / KV8_KEYS;
+        gap = max(0, first / KV8_KEYS - lead);
+        tiles = (n + KV8_KEYS - 1) / KV8_KEYS - gap;
+    }
+    __device__ __forceinline__ int tile(int i) const { return i < lead ? i : i + gap; }
+};
+
+template <typename T>
+__device__ __forceinline__ void put4(T *o, float4 v);
+template <>
+__device__ __forceinline__ void put4<float>(float *o, float4 v)
+{
+    o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+}
+template <>
+__device__ __forceinline__ void put4<__half>(__half *o, float4 v)
+{
+    o[0] = __float2half_rn(v.x), o[1] = __float2half_rn(v.y), o[2] = __float2half_rn(v.z), o[3] = __float2half_rn(v.w);
+}
+template <>
+__device__ __forceinline__ void put4<__nv_bfloat16>(__nv_bfloat16 *o, float4 v)
+{
+    o[0] = __float2bfloat16_rn(v.x), o[1] = __float2bfloat16_rn(v.y);
+    o[2] = __float2bfloat16_rn(v.z), o[3] = __float2bfloat16_rn(v.w);
+}
+
+// Four elements, from 4 * c on, of row `row` of sequence b and cache head h.
+__device__ __forceinline__ void store_o(const Kv8AttnParams &p, int b, int h, int row, int c, float4 v)
+{
+    const long long token = static_cast<long long>(b) * p.n_q + row / p.group;
+    const long long at = token * p.o_token_stride + (h * p.group + row % p.group) * p.o_head_stride + 4 * c;
+    if (p.o_type == QGEMV_F32)
+        put4(static_cast<float *>(p.o) + at, v);
+    else if (p.o_type == QGEMV_F16)
+        put4(static_cast<__half *>(p.o) + at, v);
+    else
+        put4(static_cast<__nv_bfloat16 *>(p.o) + at, v);
+}
+__device__ __forceinline__ void store_lse(const Kv8AttnParams &p, int b, int h, int row, float m, float l)
+{
+    if (!p.lse) return;
+    const long long token = static_cast<long long>(b) * p.n_q + row / p.group;
+    p.lse[token * p.hq + h * p.group + row % p.group] =
+        l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// A sequence without rows: zeros for `rows` rows from row0 on of head h.
+__device__ __forceinline__ void store_none(const Kv8AttnParams &p, int b, int h, int row0, int rows)
+{
+    const int quads = p.d / 4;
+    for (int i = threadIdx.x; i < rows * quads; i += K8_THREADS) {
+        const int row = row0 + i / quads, c = i % quads;
+        store_o(p, b, h, row, c, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        if (c == 0) store_lse(p, b, h, row, 0.0f, 0.0f);
+    }
+}
+
+template <int CODE, int DP, int NT>
+__global__ void __launch_bounds__(K8_THREADS, K8Cfg<DP, NT>::BLOCKS) kv8_attn_kernel(const __grid_constant__ Kv8AttnParams p)
+{
+    using C = K8Cfg<DP, NT>;
+    extern __shared__ __align__(128) uint8_t k8_smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t s_base = smem_addr(k8_smem);
+    const uint32_t s_ring = s_base + warp * C::STAGES * C::TILE;
+    const uint32_t s_meta = s_base + C::OFF_META + warp * C::STAGES * 16;
+    float *s_qs = reinterpret_cast<float *>(k8_smem + C::OFF_QS);
+    float2 *s_ml = reinterpret_cast<float2 *>(k8_smem + C::OFF_ML);
+
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // The block's range [lo, hi) of the line of all units' tiles, and the
+    // sequence it begins in.  Units: sequence, then head, then tile of query rows.
+    const int per_seq = p.hkv * p.row_tiles;
+    long long lo, hi, range = 0, seq_at;  // seq_at: where sequence b's tiles begin
+    int b;
+    if (p.balanced) {
+        // every warp adds all sequences' tiles up, each lane a run of them
+        const int run = (p.n_seqs + 31) / 32;
+        long long mine = 0;
+        for (int i = lane * run; i < min(p.n_seqs, (lane + 1) * run); ++i) {
+            const int n = __ldg(p.lens + i);
+            mine += Seen(p, n).tiles;
+            if ((n < 0 || n > p.max_len) && blockIdx.x == 0 && warp == 0) atomicCAS(p.status, 0u, ST_BAD_ID);
+        }
+        long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const long long total = __shfl_sync(0xFFFFFFFFu, upto, 31) * per_seq;
+        range = max(static_cast<long long>(KV8_SPLIT_MIN), (total + p.grid - 1) / p.grid);
+        lo = blockIdx.x * range, hi = min(total, lo + range);
+        // the first lane whose run ends behind lo walks its run
+        const unsigned behind = __ballot_sync(0xFFFFFFFFu, upto * per_seq > lo);
+        const int owner = behind ? __ffs(behind) - 1 : 0;
+        int at = lane * run;
+        long long begin = upto - mine;
+        if (lane == owner && lo < total) {
+            for (;; ++at) {
+                const int n = Seen(p, __ldg(p.lens + at)).tiles;
+                if ((begin + n) * per_seq > lo) break;
+                begin += n;
+            }
+        }
+        b = __shfl_sync(0xFFFFFFFFu, at, owner);
+        seq_at = __shfl_sync(0xFFFFFFFFu, begin, owner) * per_seq;
+        for (int i = blockIdx.x; i < p.n_seqs; i += p.grid)
+            if (Seen(p, __ldg(p.lens + i)).n == 0)
+                for (int h = 0; h < p.hkv; ++h) store_none(p, i, h, 0, p.rows);
+        if (tid == 0) p.parts[blockIdx.x] = make_int4(0, 0, 0, 0);
+        if (lo >= total) return;
+    } else {
+        b = blockIdx.x / per_seq;
+        const int n = __ldg(p.lens + b), u = blockIdx.x % per_seq;
+        const Seen seen(p, n);
+        if ((n < 0 || n > p.max_len) && tid == 0) atomicCAS(p.status, 0u, ST_BAD_ID);
+        if (seen.n == 0) {
+            const int row0 = u % p.row_tiles * p.tile_rows;
+            store_none(p, b, u / p.row_tiles, row0, min(p.tile_rows, p.rows - row0));
+            return;
+        }
+        seq_at = 0;
+        lo = static_cast<long long>(u) * seen.tiles, hi = lo + seen.tiles;
+    }
+
+    Seen seen(p, __ldg(p.lens + b));
+    int unit = static_cast<int>((lo - seq_at) / seen.tiles);
+    long long pos = lo;
+    while (pos < hi) {
+        const long long u0 = seq_at + static_cast<long long>(unit) * seen.tiles;
+        const int i0 = static_cast<int>(pos - u0), i1 = static_cast<int>(min(static_cast<long long>(seen.tiles), hi - u0));
+        const int h = unit / p.row_tiles, row0 = unit % p.row_tiles * p.tile_rows;
+        const int rows = min(p.tile_rows, p.rows - row0);
+
+        // ---- the warp's tiles i0 + warp, + 8, ... on their way
+        const int32_t *table = p.pages + b * p.pages_stride;
+        const uint8_t *kh = p.c.k + h * p.c.head_stride, *vh = p.c.v + h * p.c.head_stride;
+        const float *ksh = p.c.ks + h * p.c.scale_head, *vsh = p.c.vs + h * p.c.scale_head;
+        auto page_of = [&](int i) { return i < i1 ? __ldg(table + (seen.tile(i) * KV8_KEYS >> p.c.page_shift)) : 0; };
+        int ahead = i0 + warp, page = page_of(ahead), slot = 0;
+        auto issue = [&]() {
+            if (ahead < i1) {
+                const int j0 = seen.tile(ahead) * KV8_KEYS, in_page = j0 & ((1 << p.c.page_shift) - 1);
+                const bool here = page >= 0 && page < p.c.n_pages;
+                const int left = here ? seen.n - j0 : 0;  // rows of the tile that the sequence has
+                const long long at = here ? page * p.c.page_stride + in_page * p.c.row_stride : 0;
+                const uint32_t dst = s_ring + slot * C::TILE;
+                const uint8_t *kr = kh + at + g * p.c.row_stride, *vr = vh + at + 2 * t * p.c.row_stride;
+#pragma unroll
+                for (int c = 0; c < C::KC; ++c) {
+                    const int e = 64 * c + 16 * t;
+                    cp16(dst + (2 * c) * 512 + lane * 16, kr + e, g < left && e < p.d);
+                    cp16(dst + (2 * c + 1) * 512 + lane * 16, kr + 8 * p.c.row_stride + e, g + 8 < left && e < p.d);
+                }
+                const uint32_t dv = dst + KV8_KEYS * DP;
+#pragma unroll
+                for (int c = 0; c < C::VC; ++c) {
+                    const int e = 8 * C::VB * c + C::VB * g;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = (r & 1) + 8 * (r >> 1);  // beside 2 t
+                        const bool take = 2 * t + row < left && e < p.d;
+                        const uint32_t to = dv + (4 * c + r) * 32 * C::VB + lane * C::VB;
+                        if constexpr (C::VB == 16)
+                            cp16(to, vr + row * p.c.row_stride + e, take);
+                        else
+                            cp8(to, vr + row * p.c.row_stride + e, take);
+                    }
+                }
+                const uint32_t meta = s_meta + slot * 16;
+                const long long sc = here ? page * p.c.scale_page + (in_page >> p.c.block_shift) * p.c.scale_block : 0;
+                if (lane == 0) cp4(meta + 4, ksh + sc, here);
+                if (lane == 1) cp4(meta + 8, vsh + sc, here);
+                if (lane == 2) {
+                    asm volatile("st.shared.s32 [%0], %1;" ::"r"(meta), "r"(here ? j0 : -1) : "memory");
+                    if (!here) atomicCAS(p.status, 0u, ST_BAD_ID);
+                }
+                ahead += K8_WARPS;
+                page = page_of(ahead);
+            }
+            cp_commit();
+            slot = slot + 1 == C::STAGES ? 0 : slot + 1;
+        };
+#pragma unroll
+        for (int s = 0; s < C::STAGES - 1; ++s) issue();
+
+        // ---- the unit's queries, in f16; bf16 rows divided by a power of two
+        for (int r = warp; r < 8 * NT; r += K8_WARPS) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            const int row = row0 + r;
+            if (r < rows && 8 * lane < p.d) {
+                const long long token = static_cast<long long>(b) * p.n_q + row / p.group;
+                w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + token * p.q_token_stride +
+                                                          (h * p.group + row % p.group) * p.q_head_stride + 8 * lane));
+            }
+            float qs = p.scale_log2;
+            if (p.q_bf16) {
+                unsigned u[4] = {w.x, w.y, w.z, w.w};
+                unsigned top = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = max(top, max((u[i] << 16) & 0x7FFFFFFFu, u[i] & 0x7FFF0000u));
+                top = __reduce_max_sync(0xFFFFFFFFu, top);
+                // the power of two of the row's largest value; infinities and NaN as they are
+                int e = static_cast<int>(top >> 23);
+                if (e == 255 || top == 0) e = 127;
+                e = min(max(e, 2), 252);
+                const float down = __uint_as_float(static_cast<unsigned>(254 - e) << 23);  // 2^(127 - e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    u[i] = pack(__uint_as_float(u[i] << 16) * down, __uint_as_float(u[i] & 0xFFFF0000u) * down);
+                w = make_uint4(u[0], u[1], u[2], u[3]);
+                qs *= __uint_as_float(static_cast<unsigned>(e) << 23);
+            }
+            // chunk c of a row lies at c ^ (row & 1): the fragments' reads meet no bank twice
+            if (8 * lane < DP) *reinterpret_cast<uint4 *>(k8_smem + C::OFF_Q + r * DP * 2 + ((lane ^ (r & 1)) << 4)) = w;
+            if (lane == 0) s_qs[r] = qs;
+        }
+        __syncthreads();
+
+        auto load_q = [&](int j, int c, unsigned (&f)[8]) {  // 16 elements 64 c + 16 t .. of row 8 j + g
+            const uint32_t at = s_base + C::OFF_Q + (8 * j + g) * DP * 2;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint4 v = lds128(at + (((8 * c + 2 * t + x) ^ (g & 1)) << 4));
+                f[4 * x] = v.x, f[4 * x + 1] = v.y, f[4 * x + 2] = v.z, f[4 * x + 3] = v.w;
+            }
+        };
+        unsigned qf[C::QREG ? NT : 1][C::QREG ? C::KC : 1][8];
+        if constexpr (C::QREG) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int c = 0; c < C::KC; ++c) load_q(j, c, qf[j][c]);
+        }
+        // per thread: rows 8 j + 2 t + e
+        float qs[NT][2], m[NT][2], l[NT][2], o[NT][C::MT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                qs[j][e] = s_qs[8 * j + 2 * t + e];
+                m[j][e] = K8_NEG, l[j][e] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[j][i][e] = 0.0f;
+        }
+
+        int rd = 0;
+        for (int i = i0 + warp; i < i1; i += K8_WARPS) {
+            issue();
+            cp_wait<C::STAGES - 1>();
+            __syncwarp();
+            const uint32_t src = s_ring + rd * C::TILE, meta = s_meta + rd * 16;
+            int j0;
+            float ks, vs;
+            asm volatile("ld.shared.s32 %0, [%1];" : "=r"(j0) : "r"(meta));
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks) : "r"(meta + 4));
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(meta + 8));
+            rd = rd + 1 == C::STAGES ? 0 : rd + 1;
+            if (j0 < 0) {  // its page is not there
+                __syncwarp();
+                continue;
+            }
+            const bool whole = j0 + KV8_KEYS - 1 <= seen.n - p.n_q &&
+                               (!p.window || j0 > seen.n - 1 - p.window || j0 + KV8_KEYS - 1 < p.sinks);
+
+            // ---- scores of 16 keys
+            float s[NT][4];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[j][e] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < C::KC; ++c) {
+                const uint4 x = lds128(src + (2 * c) * 512 + lane * 16), y = lds128(src + (2 * c + 1) * 512 + lane * 16);
+                const unsigned xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+                unsigned a[4][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    cvt4<CODE>(xw[k], a[k][0], a[k][2]);
+                    cvt4<CODE>(yw[k], a[k][1], a[k][3]);
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    unsigned f[8];
+                    if constexpr (C::QREG) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) f[k] = qf[j][c][k];
+                    } else {
+                        load_q(j, c, f);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mma(s[j], a[k][0], a[k][1], a[k][2], a[k][3], f[2 * k], f[2 * k + 1]);
+                }
+            }
+
+            // ---- weights.  A block of zeros has scale 0: any other does for its codes
+            vs = vs < 8.673617e-19f ? 8.673617e-19f : vs;  // 2^-60
+            const float lv = log2f(vs), inv = 1.0f / vs;
+            float f[NT][2];
+            bool over = false;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f[j][e] = ks * qs[j][e];
+                    const float at = lv - m[j][e];
+                    if (!whole) {
+                        const int q_pos = seen.n - p.n_q + (row0 + 8 * j + 2 * t + e) / p.group;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int key = j0 + g + 8 * k;
+                            const bool sees = key <= q_pos && (!p.window || key > q_pos - p.window || key < p.sinks);
+                            s[j][2 * k + e] = sees ? fmaf(s[j][2 * k + e], f[j][e], lv) : -INFINITY;
+                            over |= s[j][2 * k + e] - m[j][e] > K8_SLACK;
+                        }
+                    } else {
+                        over |= fmaxf(s[j][e] * f[j][e], s[j][2 + e] * f[j][e]) + at > K8_SLACK;
+                    }
+                }
+            if (__any_sync(0xFFFFFFFFu, over) || !whole) {
+                // exact scores, and the references with them
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (whole) {
+                            s[j][e] = fmaf(s[j][e], f[j][e], lv);
+                            s[j][2 + e] = fmaf(s[j][2 + e], f[j][e], lv);
+                        }
+                        float mx = fmaxf(s[j][e], s[j][2 + e]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+                        if (mx - m[j][e] > K8_SLACK) {
+                            const float mn = mx - K8_LIFT, c = ex2(m[j][e] - mn);
+                            m[j][e] = mn;
+                            l[j][e] *= c;
+#pragma unroll
+                            for (int i = 0; i < C::MT; ++i) o[j][i][e] *= c, o[j][i][2 + e] *= c;
+                        }
+                        s[j][e] = ex2(s[j][e] - m[j][e]);
+                        s[j][2 + e] = ex2(s[j][2 + e] - m[j][e]);
+                    }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float at = lv - m[j][e];
+                        s[j][e] = ex2(fmaf(s[j][e], f[j][e], at));
+                        s[j][2 + e] = ex2(fmaf(s[j][2 + e], f[j][e], at));
+                    }
+            }
+            unsigned pb[NT][2];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float sum = s[j][e] + s[j][2 + e];
+                    // a row that sees none of the tile takes nothing from its scale either
+                    if (whole || sum != 0.0f) l[j][e] = fmaf(sum, inv, l[j][e]);
+                }
+                // The weights are operands in f16: off by half a unit of it.  l keeps them whole.
+                pb[j][0] = movm(pack(s[j][0], s[j][1]));
+                pb[j][1] = movm(pack(s[j][2], s[j][3]));
+            }
+
+            // ---- weighted sums of v
+            const uint32_t sv = src + KV8_KEYS * DP;
+#pragma unroll
+            for (int c = 0; c < C::VC; ++c) {
+                constexpr int W = C::VB / 4;
+                unsigned v[4][W];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t at = sv + (4 * c + r) * 32 * C::VB + lane * C::VB;
+                    if constexpr (W == 4) {
+                        const uint4 x = lds128(at);
+                        v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
+                    } else {
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[r][0]), "=r"(v[r][1]) : "r"(at));
+                    }
+                }
+                if (CODE == QGEMV_CODE_E4M3 && !whole) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int k = 0; k < W; ++k) v[r][k] = without_nan(v[r][k]);
+                }
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        // elements 4 k + 2 x and + 1 of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
+                        unsigned a0, a1, a2, a3;
+                        cvt4<CODE>(__byte_perm(v[0][k], v[1][k], x ? 0x7362 : 0x5140), a0, a1);
+                        cvt4<CODE>(__byte_perm(v[2][k], v[3][k], x ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+                            mma(o[j][(C::VB / 2) * c + 2 * k + x], a0, a1, a2, a3, pb[j][0], pb[j][1]);
+                    }
+            }
+        }
+
+        // ---- the warps' sums through the ring
+        cp_wait<0>();
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[j][e];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+                const int r = 8 * j + 2 * t + e;
+                if (g == 0) s_ml[warp * 8 * NT + r] = make_float2(m[j][e], sum);
+                // elements VB g .. of the row, in quads; quad c of a row lies at c ^ t: no bank twice
+                float4 *to = reinterpret_cast<float4 *>(k8_smem) + (warp * 8 * NT + r) * (DP / 4);
+#pragma unroll
+                for (int c = 0; c < C::VC; ++c)
+#pragma unroll
+                    for (int k = 0; k < C::VB / 4; ++k) {
+                        const int i = (C::VB / 2) * c + 2 * k;
+                        to[(2 * C::VB * c + C::VB / 4 * g + k) ^ t] =
+                            make_float4(o[j][i][e], o[j][i][2 + e], o[j][i + 1][e], o[j][i + 1][2 + e]);
+                    }
+            }
+        __syncthreads();
+        const bool whole_unit = i0 == 0 && i1 == seen.tiles;
+        const int part = 2 * static_cast<int>(blockIdx.x) + (pos != lo);
+        for (int x = tid; x < rows * (DP / 4); x += K8_THREADS) {
+            const int r = x / (DP / 4), c = x % (DP / 4);
+            float top = K8_NEG;
+#pragma unroll
+            for (int w = 0; w < K8_WARPS; ++w) top = fmaxf(top, s_ml[w * 8 * NT + r].x);
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float total = 0.0f;
+#pragma unroll
+            for (int w = 0; w < K8_WARPS; ++w) {
+                const float2 ml = s_ml[w * 8 * NT + r];
+                const float by = ex2(ml.x - top);
+                const float4 v = reinterpret_cast<const float4 *>(k8_smem)[(w * 8 * NT + r) * (DP / 4) + (c ^ ((r >> 1) & 3))];
+                total = fmaf(ml.y, by, total);
+                sum.x = fmaf(v.x, by, sum.x), sum.y = fmaf(v.y, by, sum.y);
+                sum.z = fmaf(v.z, by, sum.z), sum.w = fmaf(v.w, by, sum.w);
+            }
+            if (4 * c >= p.d) continue;
+            if (whole_unit) {
+                const float by = total == 0.0f ? 0.0f : 1.0f / total;
+                store_o(p, b, h, row0 + r, c, make_float4(sum.x * by, sum.y * by, sum.z * by, sum.w * by));
+                if (c == 0) store_lse(p, b, h, row0 + r, top, total);
+            } else {
+                const long long at = static_cast<long long>(part) * 8 * NT + r;
+                *reinterpret_cast<float4 *>(p.part_o + at * p.d + 4 * c) = sum;
+                if (c == 0) p.part_ml[at] = make_float2(top, total);
+            }
+        }
+        // the unit begins here and ends in a later block's range
+        if (tid == 0 && i0 == 0 && i1 < seen.tiles)
+            p.parts[blockIdx.x] = make_int4(b, unit, part, static_cast<int>((u0 + seen.tiles - 1) / range - blockIdx.x) + 1);
+        pos = u0 + i1;
+        if (pos >= hi) break;
+        __syncthreads();  // the ring is free again
+        if (++unit == per_seq) {
+            unit = 0;
+            seq_at += static_cast<long long>(per_seq) * seen.tiles;
+            do {
+                seen = Seen(p, __ldg(p.lens + ++b));  // one with rows follows, as pos < hi
+            } while (seen.tiles == 0);
+        }
+    }
+}
+
+// Joins the parts of the units that the ranges cut: block x those of the unit
+// that block x of the launch before left to its successors, which hold it as their
+// first.  combine_warps warps a row, each every so many parts.
+__global__ void __launch_bounds__(K8_THREADS) kv8_combine_kernel(const __grid_constant__ Kv8AttnParams p, int tile_pad)
+{
+    __shared__ float4 s_o[K8_WARPS][64];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int4 u = p.parts[blockIdx.x];
+    if (u.w == 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = p.combine_warps;
+    const int r = blockIdx.y * (K8_WARPS / per) + warp / per, sub = warp % per;
+    const int h = u.y / p.row_tiles, row0 = u.y % p.row_tiles * p.tile_rows;
+    const bool there = r < min(p.tile_rows, p.rows - row0);
+    auto at = [&](int i) {
+        return static_cast<long long>(i == 0 ? u.z : 2 * (static_cast<int>(blockIdx.x) + i)) * tile_pad + r;
+    };
+    float top = K8_NEG, total = 0.0f;
+    float4 sum[2] = {};
+    if (there) {
+        for (int i = lane; i < u.w; i += 32) top = fmaxf(top, p.part_ml[at(i)].x);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        for (int i = lane; i < u.w; i += 32) {
+            const float2 ml = p.part_ml[at(i)];
+            total = fmaf(ml.y, ex2(ml.x - top), total);
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
+        const int quads = p.d / 4;
+#pragma unroll 4
+        for (int i = sub; i < u.w; i += per) {
+            const long long a = at(i);
+            const float by = ex2(p.part_ml[a].x - top);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (lane + 32 * k < quads) {
+                    const float4 v = *reinterpret_cast<const float4 *>(p.part_o + a * p.d + 4 * (lane + 32 * k));
+                    sum[k].x = fmaf(v.x, by, sum[k].x), sum[k].y = fmaf(v.y, by, sum[k].y);
+                    sum[k].z = fmaf(v.z, by, sum[k].z), sum[k].w = fmaf(v.w, by, sum[k].w);
+                }
+        }
+    }
+    if (per > 1) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) s_o[warp][lane + 32 * k] = sum[k];
+        __syncthreads();
+        if (sub == 0)
+            for (int w = 1; w < per; ++w)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float4 v = s_o[warp + w][lane + 32 * k];
+                    sum[k].x += v.x, sum[k].y += v.y, sum[k].z += v.z, sum[k].w += v.w;
+                }
+    }
+    if (!there || sub) return;
+    const float by = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (4 * (lane + 32 * k) < p.d)
+            store_o(p, u.x, h, row0 + r, lane + 32 * k, make_float4(sum[k].x * by, sum[k].y * by, sum[k].z * by, sum[k].w * by));
+    if (lane == 0) store_lse(p, u.x, h, row0 + r, top, total);
+}
+
+template <int CODE, int DP, int NT>
+cudaError_t launch_nt(const Kv8AttnParams &p, cudaStream_t st)
+{
+    using C = K8Cfg<DP, NT>;
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kv8_attn_kernel<CODE, DP, NT>), C::SMEM, done);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kv8_attn_kernel<CODE, DP, NT>, dim3(static_cast<unsigned>(p.grid)), K8_THREADS, C::SMEM, st, p);
+    if (e != cudaSuccess || !p.balanced) return e;
+    const int rows = K8_WARPS / p.combine_warps;  // of a block
+    return launch_pdl(kv8_combine_kernel, dim3(static_cast<unsigned>(p.grid), static_cast<unsigned>((p.tile_rows + rows - 1) / rows)),
+                      K8_THREADS, 0, st, p, 8 * NT);
+}
+
+template <int CODE, int DP>
+cudaError_t launch_dp(const Kv8AttnParams &p, cudaStream_t st)
+{
+    const int nt = (p.tile_rows + 7) / 8;
+    if constexpr (DP < 256) {
+        if (nt == 4) return launch_nt<CODE, DP, 4>(p, st);
+        if (nt == 3) return launch_nt<CODE, DP, 3>(p, st);
+    }
+    return nt == 2 ? launch_nt<CODE, DP, 2>(p, st) : launch_nt<CODE, DP, 1>(p, st);
+}
+
+template <int CODE>
+cudaError_t launch_code(const Kv8AttnParams &p, cudaStream_t st)
+{
+    return p.d <= 64 ? launch_dp<CODE, 64>(p, st) : p.d <= 128 ? launch_dp<CODE, 128>(p, st) : launch_dp<CODE, 256>(p, st);
+}
+
+}  // namespace
+
+int kv8_tile_rows(int d) { return d <= 128 ? 32 : 16; }
+int kv8_blocks(int d, int nt) { return d > 128 || (d > 64 && nt > 2) ? 1 : 2; }
+
+cudaError_t launch_kv8_attn(const Kv8AttnParams &p, qgemv_code_type code, cudaStream_t st)
+{
+    return code == QGEMV_CODE_INT8 ? launch_code<QGEMV_CODE_INT8>(p, st) : launch_code<QGEMV_CODE_E4M3>(p, st);
+}
+
+}  // namespace qg

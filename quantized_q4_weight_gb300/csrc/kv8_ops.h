@@ -1,0 +1,118 @@
+// kv8_ops.h -- internal interface between the C ABI (kv8_api.cu) and the
+// kernels of a step over an 8-bit cache and of beam search: norms with the
+// rotation (norm_rope.cu), the cache write (kv8_append.cu), attention over the
+// cache (kv8_attn.cu), the beams' best continuations (beam_select.cu) and the
+// reordering of pages (fork_pages.cu).
+#pragma once
+
+#include "decode_ops.h"
+
+namespace qg {
+
+// ------------------------------------------------------- norm and rotation
+
+struct NormRopeParams {
+    RopeParams r;             // without a cache: slots null, ck = k_out, page_shift -1, row_stride = k_out_stride
+    const float *q_weight, *k_weight;
+    float eps;
+    int v_heads;              // hkv, or 0 without a cache
+};
+cudaError_t launch_norm_rope(NormRopeParams &p, qgemv_dtype in, qgemv_dtype q_out, qgemv_dtype k_out, bool half_layout,
+                             bool vec, long long n_tokens, int sms, cudaStream_t st);
+
+// ------------------------------------------------------------ 8-bit cache
+
+// Where a row's codes and a block's scale lie.
+struct Kv8Layout {
+    uint8_t *k, *v;
+    float *ks, *vs;
+    long long page_stride, row_stride, head_stride;     // bytes
+    long long scale_page, scale_block, scale_head;      // floats
+    long long n_pages;
+    int page_shift, block_shift;
+};
+
+struct Kv8AppendParams {
+    Kv8Layout c;
+    const void *k, *v;
+    long long k_stride, v_stride;
+    long long n_tokens;
+    const int32_t *first, *lens, *pages;
+    long long pages_stride;
+    int n_new, max_new, max_len, blocks;  // n_new: without `first`; blocks: that max_new rows can touch
+    int n_seqs, hkv, d;
+    int pieces;                           // threads' pieces of 8 elements a row: d / 8
+    unsigned *status;
+};
+cudaError_t launch_kv8_append(const Kv8AppendParams &p, qgemv_dtype in, qgemv_code_type code, bool vec, cudaStream_t st);
+
+struct Kv8AttnParams {
+    Kv8Layout c;
+    const void *q;
+    long long q_token_stride, q_head_stride;
+    int q_bf16;
+    const int32_t *lens, *pages;
+    long long pages_stride;
+    int n_seqs, n_q, hq, hkv, group, d;
+    int max_len, window, sinks;
+    int rows, row_tiles, tile_rows;  // of a sequence and cache head: n_q * group, in row_tiles of tile_rows
+    float scale_log2;
+    int balanced, grid;              // ranges of all tiles over `grid` blocks, or a block for each unit
+    int4 *parts;                     // [grid] the unit that a block leaves to its successors (kv8_attn.cu)
+    float *part_o;                   // [2 grid][tile rows, padded][d]
+    float2 *part_ml;                 // [2 grid][tile rows, padded]
+    int combine_warps;               // warps for a row of the combining launch
+    void *o;
+    int o_type;                      // qgemv_dtype
+    long long o_token_stride, o_head_stride;
+    float *lse;
+    unsigned *status;
+};
+constexpr int KV8_KEYS = 16;         // keys of a tile
+constexpr int KV8_SPLIT_MIN = 16;    // tiles of a range at least
+// Rows that a tile of row_tiles holds at most for a head_dim, and blocks a
+// multiprocessor for tiles of nt * 8 rows.
+int kv8_tile_rows(int d);
+int kv8_blocks(int d, int nt);
+cudaError_t launch_kv8_attn(const Kv8AttnParams &p, qgemv_code_type code, cudaStream_t st);
+
+// ------------------------------------------------------------------- beams
+
+struct BeamParams {
+    const void *x;
+    long long x_stride, vocab;
+    const float *scores;
+    const int32_t *done;
+    float *score;
+    long long *token;
+    int32_t *parent;
+    int beams, n_best, row0;      // row0: of the launch's first group (parents are rows of all groups)
+    int slices, slice;            // of a row; elements of one
+    unsigned *cnt;                // [groups] arrivals, zero between launches
+    float2 *part_ml;              // [rows][slices] maximum, sum of exponentials
+    uint2 *part;                  // [rows][slices][n_best] value's bits, token; best first
+};
+constexpr int BEAM_GROUPS = 4080;  // groups of a launch: their arrivals fit the counter area before its last 64 bytes
+constexpr int BEAM_SLICE_MAX = 8192;
+int beam_slice(long long rows, long long vocab);  // elements of a slice
+cudaError_t launch_beam(const BeamParams &p, qgemv_dtype type, int groups, cudaStream_t st);
+
+// ------------------------------------------------------------------- pages
+
+// One array of pages of all caches of a launch: codes or elements, or scales.
+struct ForkParams {
+    qgemv_fork f;
+    int n_arrays, page_shift, block_shift;      // block_shift -1: no scales
+    int heads, head_bytes;                      // a multiple of 16
+    long long n_pages;
+    long long page_stride[64], row_stride[64], head_stride[64];    // bytes, of each cache
+    void *base[128];                            // k and v of each cache
+    float *scale[128];
+    long long scale_page[64], scale_block[64], scale_head[64];
+    int first;                                  // this launch writes tables and lengths
+    unsigned *status;
+};
+constexpr int FORK_CACHES = 64;
+cudaError_t launch_fork(const ForkParams &p, int sms, cudaStream_t st);
+
+}  // namespace qg
