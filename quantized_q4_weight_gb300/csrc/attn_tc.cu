@@ -57,14 +57,12 @@
 // Every wait is bounded: a block that gives up records QGEMV_ERR_TIMEOUT and
 // frees its tensor memory.  Every block first waits (bounded) for its copies and
 // products in flight, in their warps, which have nothing else to do by then.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <type_traits>
 
 #include "decode_ops.h"
 #include "qgemv_internal.cuh"
 #include "tc_ptx.cuh"
+#include "tma.cuh"
 
 namespace qg {
 namespace {
@@ -170,17 +168,6 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const unsigned *r)
         : "memory");
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-// A box of the 4-D tensor at (x, row, head, page) into shared memory, counted on `bar`.
-__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, int x, int row, int head, int page,
-                                          uint64_t *bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(row), "r"(head), "r"(page), "r"(smem_addr(bar))
-        : "memory");
-}
 
 __device__ __forceinline__ float ac_ex2(float x)
 {
@@ -604,22 +591,6 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
     // The part launch may still be running: this one, which the combining launch
     // waits for, ends after it (see launch_pdl).
     pdl_wait();
-}
-
-// The driver's encoder of tensor maps, looked up once.
-PFN_cuTensorMapEncodeTiled_v12000 map_encoder()
-{
-    static std::atomic<void *> fn{nullptr};
-    void *f = fn.load(std::memory_order_acquire);
-    if (!f) {
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            return nullptr;
-        fn.store(f, std::memory_order_release);
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
 }
 
 // The cache as [page][head][row][element], boxes of up to 128 rows of 64 elements.

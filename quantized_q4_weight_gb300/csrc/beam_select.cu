@@ -2,34 +2,36 @@
 // the vocabulary (minfer README "How it works": device-side argmax; here of many).
 //
 //   s(r, t) = run[r] + x[r][t] - lse[r],  lse[r] = M + log(sum exp(x[r][t] - M))
-// Within a row the order of s is that of x, so a block that holds a slice of a
-// row needs no sum to find the slice's n best: it keeps its values in registers,
-// leaves their maximum, their sum of exponentials and their n best in order, and
-// the last block of a search to arrive joins them, forms s in 64 bits and takes the
-// n best of all.  Nothing depends on which block that is.
+// Within a row the order of s is that of x, so a block that streams a slice of a
+// row needs no sum to find the slice's n best.  It leaves their keys in order, the
+// slice's maximum and its sum of exponentials; the last block of a search to
+// arrive joins them, forms s in 64 bits and takes the n best of all.  Nothing depends on
+// which block that is.
 //
-// The n best of a block's values: every warp orders its lanes' largest values
-// (a bitonic network of shuffles); the n-th largest of all threads' largest is no
-// more than the n-th largest value, so the few values from there on are
-// collected and ranked by counting.  Where equal values overflow the list, the n
-// best are taken one at a time instead.
+// A key holds a logit's bits in an order that integers have, and the token upside
+// down, so that a larger key is a larger logit or a lower token.  Each warp keeps the n
+// best keys it has met in its lanes, in order.  A value is compared with the n-th of
+// them (or a better n-th that another warp has shown), which few pass: those are
+// collected in shared memory and inserted one by one, a ballot and a shuffle each.  The
+// first values of a warp go by the n-th largest of the lanes' largest (a bitonic network
+// of shuffles), a bound that lets few more than n through.
 //
-// What bounds it: memory for many rows (logits read once); the chain launch,
-// logits, ranks, arrival, join for one search, so few rows have small slices.
+// What bounds it: memory for many rows (logits read once; a maximum, a product, an
+// exponential and a sum for each); the chain launch, logits, insertions, arrival, join for
+// one search, so few rows have small slices.
 #include "kv8_ops.h"
 #include "qgemv_internal.cuh"
 
 namespace qg {
 namespace {
 
-constexpr int BM_THREADS = 256, BM_WARPS = BM_THREADS / 32;
-constexpr int BM_VALUES = BEAM_SLICE_MAX / BM_THREADS;  // of a thread: 32
-constexpr int BM_LIST = 512;                            // values that are ranked by counting
+constexpr int BM_THREADS = 256, BM_WARPS = BM_THREADS / 32, BM_BLOCKS = 4;
+constexpr int BM_CHUNKS = 4;   // 16-byte chunks of a thread's batch; as many are on their way
+constexpr int BM_LIST = 64;    // keys of a warp that wait for their insertion
 constexpr int BM_BEAMS = 16;
+constexpr float LOG2E = 1.4426950408889634f;
 
-__device__ __forceinline__ float bm_f(float v) { return v; }
-__device__ __forceinline__ float bm_f(__half v) { return __half2float(v); }
-__device__ __forceinline__ float bm_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+typedef unsigned long long Key;
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -43,82 +45,119 @@ __device__ __forceinline__ unsigned ordered(float f)
     const unsigned u = __float_as_uint(f + 0.0f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-
-// The n-th largest (n <= 32) of 256 threads' values `v`, a lower bound of the n-th
-// largest of anything that they are the largest of.  s: [BM_WARPS][32] and a word.
-__device__ __forceinline__ float nth_of_threads(float v, int n, float (*s)[32], float *s_bound)
+__device__ __forceinline__ float from_ordered(unsigned o)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ Key key_of(float v, unsigned token)
+{
+    return static_cast<Key>(ordered(v)) << 32 | (0xFFFFFFFFu - token);
+}
+__device__ __forceinline__ float value_of(Key k) { return from_ordered(static_cast<unsigned>(k >> 32)); }
+__device__ __forceinline__ unsigned token_of(Key k) { return 0xFFFFFFFFu - static_cast<unsigned>(k); }
+
+// Elements of a 16-byte chunk as floats, and the largest of them (NaN passed over).
+template <typename T>
+struct Chunk16;
+template <>
+struct Chunk16<float> {
+    static constexpr int E = 4;
+    static __device__ __forceinline__ float at(const uint4 &w, int i)
+    {
+        return __uint_as_float(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w);
+    }
+    static __device__ __forceinline__ float largest(const uint4 &w)
+    {
+        return fmaxf(fmaxf(at(w, 0), at(w, 1)), fmaxf(at(w, 2), at(w, 3)));
+    }
+};
+template <>
+struct Chunk16<__half> {
+    static constexpr int E = 8;
+    static __device__ __forceinline__ __half2 pair(const uint4 &w, int i)
+    {
+        const unsigned u = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+        return *reinterpret_cast<const __half2 *>(&u);
+    }
+    static __device__ __forceinline__ float at(const uint4 &w, int i)
+    {
+        return i & 1 ? __high2float(pair(w, i >> 1)) : __low2float(pair(w, i >> 1));
+    }
+    static __device__ __forceinline__ float largest(const uint4 &w)
+    {
+        const __half2 m = __hmax2(__hmax2(pair(w, 0), pair(w, 1)), __hmax2(pair(w, 2), pair(w, 3)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+};
+template <>
+struct Chunk16<__nv_bfloat16> {
+    static constexpr int E = 8;
+    static __device__ __forceinline__ unsigned word(const uint4 &w, int i) { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
+    static __device__ __forceinline__ __nv_bfloat162 pair(const uint4 &w, int i)
+    {
+        const unsigned u = word(w, i);
+        return *reinterpret_cast<const __nv_bfloat162 *>(&u);
+    }
+    static __device__ __forceinline__ float at(const uint4 &w, int i)
+    {
+        return __uint_as_float(i & 1 ? word(w, i >> 1) & 0xFFFF0000u : word(w, i >> 1) << 16);
+    }
+    static __device__ __forceinline__ float largest(const uint4 &w)
+    {
+        const __nv_bfloat162 m = __hmax2(__hmax2(pair(w, 0), pair(w, 1)), __hmax2(pair(w, 2), pair(w, 3)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+};
+
+// The n-th largest of a warp's 32 values.
+template <typename V>
+__device__ __forceinline__ V nth_of_warp(V v, int n)
+{
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
         for (int d = k >> 1; d; d >>= 1) {
-            const float o = __shfl_xor_sync(0xFFFFFFFFu, v, d);
-            const bool down = (lane & k) == 0, low = (lane & d) == 0;  // k = 32: descending over the warp
-            v = down == low ? fmaxf(v, o) : fminf(v, o);
+            const V o = __shfl_xor_sync(0xFFFFFFFFu, v, d);
+            const bool larger = ((lane & k) == 0) == ((lane & d) == 0);  // k = 32: falling over the warp
+            v = (o > v) == larger ? o : v;
         }
-    s[warp][lane] = v;
-    __syncthreads();
-    // a value's rank: its place in its own list, and in each other list the values that come before it
-    int rank = lane;
-#pragma unroll
-    for (int w = 0; w < BM_WARPS; ++w) {
-        int at = 0;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) {  // the first `at` of list w come before
-            if (at + d <= 32) {
-                const float o = s[w][at + d - 1];
-                if (o > v || (o == v && w < warp)) at += d;
-            }
-        }
-        rank += w == warp ? 0 : at;
-    }
-    if (rank == n - 1) *s_bound = v;
-    __syncthreads();
-    return *s_bound;
+    return __shfl_sync(0xFFFFFFFFu, v, n - 1);
 }
 
-// The largest key of the block, to all threads.  s: [BM_WARPS].
-__device__ __forceinline__ unsigned long long block_largest(unsigned long long key, unsigned long long *s)
-{
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, key, d);
-        key = o > key ? o : key;
-    }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = key;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < BM_WARPS; ++w) key = s[w] > key ? s[w] : key;
-    return key;
-}
+// The warp's best keys, falling over the lanes (0: none).
+struct Best {
+    Key mine = 0;
 
-// A candidate of the join: s, then the lower row, the larger logit, the lower token.
-struct Cand {
-    double s;
-    unsigned row, x, token;  // x: ordered bits
-
-    __device__ __forceinline__ bool before(const Cand &o) const
+    __device__ __forceinline__ void insert(Key k)  // the same for all lanes, none of the list's
     {
-        if (s != o.s) return s > o.s;
-        if (row != o.row) return row < o.row;
-        if (x != o.x) return x > o.x;
-        return token < o.token;
+        const int at = __popc(__ballot_sync(0xFFFFFFFFu, mine > k));
+        const Key up = __shfl_up_sync(0xFFFFFFFFu, mine, 1);
+        const int lane = threadIdx.x & 31;
+        mine = lane < at ? mine : lane == at ? k : up;
     }
+    __device__ __forceinline__ Key nth(int n) const { return __shfl_sync(0xFFFFFFFFu, mine, n - 1); }
 };
 
+// How many of a falling list of `n` are above k.
+template <typename K>
+__device__ __forceinline__ int above(const K *list, int n, K k)
+{
+    int at = 0;
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        if (at + d <= n && list[at + d - 1] > k) at += d;
+    return at + (at < n && list[at] > k);
+}
+
 struct BeamShared {
-    float sorted[BM_WARPS][32];
-    float bound, red[BM_WARPS];
-    unsigned long long best[BM_WARPS];
-    int count, last;
+    Key lists[BM_BEAMS][32];        // of the warps, then of the join's rows
+    Key wait[BM_WARPS][BM_LIST];
+    Key shown;                      // the best n-th key of a warp
+    float m[BM_BEAMS], sum[BM_BEAMS];
+    int count[BM_BEAMS];
     double lse[BM_BEAMS];
-    float run[BM_BEAMS];
-    union {
-        unsigned long long keys[BM_LIST];
-        Cand list[BM_LIST];
-    };
+    int last;
 };
 
 // The join of group gi of the launch, by the block that arrived last.
@@ -126,119 +165,114 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long r0 = static_cast<long long>(gi) * p.beams;
-    const double NONE = -__longlong_as_double(0x7FF0000000000000ll);
-    for (int w = warp; w < p.beams; w += BM_WARPS) {
+    const int per = p.slices * p.n_best;
+    constexpr int ROWS = BM_BEAMS / BM_WARPS;  // of a warp
+    Best best[ROWS];
+    // each row's n best keys, maximum and sum
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) {
+        const int w = warp + q * BM_WARPS;
+        if (w >= p.beams) break;
+        const Key *part = p.part + (r0 + w) * per;
         const float2 *ml = p.part_ml + (r0 + w) * p.slices;
         float m = -INFINITY, sum = 0.0f;
-        for (int i = lane; i < p.slices; i += 32) m = fmaxf(m, ml[i].x);
+        float2 mine = lane < p.slices ? ml[lane] : make_float2(-INFINITY, 0.0f);
+        if (p.slices == 1) {
+            best[q].mine = lane < p.n_best ? part[lane] : 0;
+        } else {
+            Key kth = 0;
+            for (int i0 = 0; i0 < per; i0 += 128) {
+                Key k[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) k[u] = i0 + 32 * u + lane < per ? part[i0 + 32 * u + lane] : 0;
+                if (i0 == 0) {
+                    const Key a = k[0] > k[1] ? k[0] : k[1], b = k[2] > k[3] ? k[2] : k[3];
+                    kth = nth_of_warp(a > b ? a : b, p.n_best);
+                    kth -= kth != 0;  // it may be among them itself
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    for (unsigned in = __ballot_sync(0xFFFFFFFFu, k[u] > kth); in; in &= in - 1) {
+                        const Key c = __shfl_sync(0xFFFFFFFFu, k[u], __ffs(in) - 1);
+                        if (c > kth) {
+                            best[q].insert(c);
+                            const Key n = best[q].nth(p.n_best);
+                            kth = n > kth ? n : kth;
+                        }
+                    }
+            }
+        }
+        for (int i = lane; i < p.slices; i += 32) m = fmaxf(m, i == lane ? mine.x : ml[i].x);
 #pragma unroll
         for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        if (m > -INFINITY)
-            for (int i = lane; i < p.slices; i += 32) sum = fmaf(ml[i].y, expf(ml[i].x - m), sum);
+        for (int i = lane; i < p.slices; i += 32) {
+            const float2 v = i == lane ? mine : ml[i];
+            if (v.x > -INFINITY) sum = fmaf(v.y, expf(v.x - m), sum);
+        }
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        if (lane == 0) {
-            const float run = __ldg(p.scores + r0 + w);
-            // +infinity among the logits, none above -infinity, or a NaN score: no continuation
-            const bool none = !(m < INFINITY) || !(m > -INFINITY) || !(run > -INFINITY);
-            s.lse[w] = none ? -NONE : static_cast<double>(m) + log(static_cast<double>(sum));
-            s.run[w] = none ? 0.0f : run;
-        }
-    }
-    if (tid == 0) s.count = 0;
-    __syncthreads();
-
-    const int per = p.slices * p.n_best, total = p.beams * per;
-    const uint2 *part = p.part + r0 * per;
-    auto cand = [&](int i, Cand &c) {  // whether there is one
-        const uint2 v = part[i];
-        const int w = i / per;
-        const float x = __uint_as_float(v.x);
-        c.s = static_cast<double>(x) - s.lse[w] + static_cast<double>(s.run[w]);
-        c.row = w, c.x = ordered(x), c.token = v.y;
-        return v.y != 0xFFFFFFFFu && c.s > NONE;
-    };
-    // in 32 bits first, with room for their rounding: a few survive
-    auto rough = [&](int i) {
-        const uint2 v = part[i];
-        const int w = i / per;
-        return v.y == 0xFFFFFFFFu ? -INFINITY : __uint_as_float(v.x) - static_cast<float>(s.lse[w]) + s.run[w];
-    };
-    float top = -INFINITY;
-    for (int i = tid; i < total; i += BM_THREADS) top = fmaxf(top, rough(i));
-    float bound = nth_of_threads(top, p.n_best, s.sorted, &s.bound);
-    if (bound > -INFINITY && bound < INFINITY) {
-        float off = fabsf(bound);
-        for (int w = 0; w < p.beams; ++w) off = fmaxf(off, fmaxf(fabsf(static_cast<float>(s.lse[w])) < INFINITY ? fabsf(static_cast<float>(s.lse[w])) : 0.0f, fabsf(s.run[w])));
-        // x, lse, run and two sums, each within 2^-24 of at most 4 * off
-        bound -= off * 4.0f * 6.0e-7f;
-    }
-    for (int i = tid; i < total; i += BM_THREADS) {
-        const float f = rough(i);
-        Cand c;
-        if (f >= bound && f > -INFINITY && cand(i, c)) {
-            const int at = atomicAdd(&s.count, 1);
-            if (at < BM_LIST) s.list[at] = c;
-        }
+        if (lane == 0) s.m[w] = m, s.sum[w] = sum;
     }
     __syncthreads();
-    const int count = s.count;
+    const double INF = __longlong_as_double(0x7FF0000000000000ll);
+    if (tid < p.beams) {
+        const float m = s.m[tid], run = __ldg(p.scores + r0 + tid);
+        // +infinity among the logits, none above -infinity, or a NaN score: no continuation
+        const bool none = !(m < INFINITY) || !(m > -INFINITY) || !(run > -INFINITY);
+        s.lse[tid] = none ? INF : static_cast<double>(m) + log(static_cast<double>(s.sum[tid]));
+        s.m[tid] = none ? 0.0f : run;
+    }
+    __syncthreads();
+    double score[ROWS];
+    Key order[ROWS];  // of the scores: their bits in an order that integers have
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) {
+        const int w = warp + q * BM_WARPS;
+        if (w >= p.beams) break;
+        score[q] = static_cast<double>(value_of(best[q].mine)) - s.lse[w] + static_cast<double>(s.m[w]);
+        const long long b = __double_as_longlong(score[q] + 0.0);
+        order[q] = b < 0 ? ~static_cast<Key>(b) : static_cast<Key>(b) | 0x8000000000000000ull;
+        if (best[q].mine == 0 || lane >= p.n_best || !(score[q] > -INF)) order[q] = 0;
+        s.lists[w][lane] = order[q];
+        const int count = __popc(__ballot_sync(0xFFFFFFFFu, order[q] != 0));
+        if (lane == 0) s.count[w] = count;
+    }
+    __syncthreads();
     const long long out = static_cast<long long>(gi) * p.n_best;
-    auto put = [&](int k, const Cand &c) {
-        p.score[out + k] = static_cast<float>(c.s);
-        p.token[out + k] = c.token;
-        p.parent[out + k] = static_cast<int32_t>(p.row0 + r0 + c.row);
-    };
-    auto put_none = [&](int k) {
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) {
+        const int w = warp + q * BM_WARPS;
+        if (w >= p.beams) break;
+        if (order[q] == 0) continue;
+        // equal scores of other rows: the lower row comes first
+        int rank = lane;
+        for (int o = 0; o < p.beams; ++o)
+            if (o != w) rank += above(s.lists[o], s.count[o], order[q] - (o < w));
+        if (rank < p.n_best) {
+            p.score[out + rank] = static_cast<float>(score[q]);
+            p.token[out + rank] = token_of(best[q].mine);
+            p.parent[out + rank] = static_cast<int32_t>(p.row0 + r0 + w);
+        }
+    }
+    int count = 0;
+    for (int w = 0; w < p.beams; ++w) count += s.count[w];
+    for (int k = count + tid; k < p.n_best; k += BM_THREADS) {
         p.score[out + k] = -INFINITY;
         p.token[out + k] = -1;
         p.parent[out + k] = -1;
-    };
-    if (count <= BM_LIST) {
-        for (int i = tid; i < count; i += BM_THREADS) {
-            const Cand c = s.list[i];
-            int rank = 0;
-            for (int k = 0; k < count; ++k) rank += s.list[k].before(c);
-            if (rank < p.n_best) put(rank, c);
-        }
-        for (int k = count + tid; k < p.n_best; k += BM_THREADS) put_none(k);
-        return;
-    }
-    // more equal values than the list holds: one at a time
-    Cand last;
-    for (int k = 0; k < p.n_best; ++k) {
-        Cand best;
-        bool have = false;
-        for (int i = tid; i < total; i += BM_THREADS) {
-            Cand c;
-            if (cand(i, c) && (k == 0 || last.before(c)) && (!have || c.before(best))) best = c, have = true;
-        }
-        __syncthreads();
-        if (!have) best.s = NONE, best.row = 0xFFFFFFFFu, best.x = 0, best.token = 0xFFFFFFFFu;
-        s.list[tid] = best;
-        __syncthreads();
-        for (int d = BM_THREADS / 2; d; d >>= 1) {
-            if (tid < d && s.list[tid + d].before(s.list[tid])) s.list[tid] = s.list[tid + d];
-            __syncthreads();
-        }
-        last = s.list[0];
-        if (tid == 0) {
-            if (last.row != 0xFFFFFFFFu)
-                put(k, last);
-            else
-                put_none(k);
-        }
     }
 }
 
 // Block (slice, row).
 template <typename T>
-__global__ void __launch_bounds__(BM_THREADS, 3) beam_kernel(const __grid_constant__ BeamParams p)
+__global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __grid_constant__ BeamParams p)
 {
-    constexpr int E = 16 / sizeof(T), CHUNKS = BM_VALUES / E;
+    using C = Chunk16<T>;
+    constexpr int E = C::E;
     __shared__ BeamShared s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long r = blockIdx.y;
+    if (tid == 0) s.shown = 0;
     pdl_launch_dependents();
     pdl_wait();
 
@@ -246,91 +280,168 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_kernel(const __grid_consta
     const int done = p.done ? __ldg(p.done + r) : -1;
     if (done >= 0) {
         // one continuation, at the running score: logit 0, sum of exponentials 1
-        if (tid < p.n_best) p.part[out * p.n_best + tid] = make_uint2(0u, blockIdx.x == 0 && tid == 0 ? done : 0xFFFFFFFFu);
+        if (tid < p.n_best) p.part[out * p.n_best + tid] = blockIdx.x == 0 && tid == 0 ? key_of(0.0f, done) : 0;
         if (tid == 0) p.part_ml[out] = blockIdx.x == 0 ? make_float2(0.0f, 1.0f) : make_float2(-INFINITY, 0.0f);
     } else {
         // The row in 16-byte chunks of memory: chunk c holds tokens c E - shift .. + E - 1.
         const T *x = static_cast<const T *>(p.x) + r * p.x_stride;
         const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
         const long long t0 = static_cast<long long>(blockIdx.x) * p.slice - shift;
-        float v[BM_VALUES];
-#pragma unroll
-        for (int k = 0; k < CHUNKS; ++k) {
-            const int l = (k * BM_THREADS + tid) * E;  // place in the slice
+        auto fetch = [&](int l) {  // the chunk at place l of the slice; -infinity beyond its ends
             const long long t = t0 + l;
-            if (l < p.slice && t >= 0 && t + E <= p.vocab) {
-                const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(x + t));
-                T e[E];
-                memcpy(e, &w, 16);
+            if (l < p.slice && t >= 0 && t + E <= p.vocab) return __ldcs(reinterpret_cast<const uint4 *>(x + t));
+            T e[E];
 #pragma unroll
-                for (int i = 0; i < E; ++i) v[k * E + i] = bm_f(e[i]);
-            } else {
+            for (int i = 0; i < E; ++i)
+                e[i] = l < p.slice && t + i >= 0 && t + i < p.vocab ? x[t + i] : static_cast<T>(-INFINITY);
+            uint4 w;
+            memcpy(&w, e, 16);
+            return w;
+        };
+        auto pick = [](const uint4 (&c)[BM_CHUNKS], int k) {
+            uint4 w = c[0];
 #pragma unroll
-                for (int i = 0; i < E; ++i)
-                    v[k * E + i] = l < p.slice && t + i >= 0 && t + i < p.vocab ? bm_f(x[t + i]) : -INFINITY;
+            for (int i = 1; i < BM_CHUNKS; ++i) w = i == k ? c[i] : w;
+            return w;
+        };
+        constexpr int BATCH = BM_THREADS * BM_CHUNKS * E;
+        uint4 next[BM_CHUNKS];
+#pragma unroll
+        for (int k = 0; k < BM_CHUNKS; ++k) next[k] = fetch((k * BM_THREADS + tid) * E);
+        __syncthreads();  // s.shown
+        Best best;
+        Key kth = 0;
+        float m = -INFINITY, sum = 0.0f;
+        const int span = static_cast<int>(min(static_cast<long long>(p.slice), p.vocab - t0));
+        for (int l0 = 0; l0 < span; l0 += BATCH) {
+            uint4 cur[BM_CHUNKS];
+#pragma unroll
+            for (int k = 0; k < BM_CHUNKS; ++k) cur[k] = next[k];
+            if (l0 + BATCH < span) {
+#pragma unroll
+                for (int k = 0; k < BM_CHUNKS; ++k) next[k] = fetch(l0 + BATCH + (k * BM_THREADS + tid) * E);
             }
-        }
-        float top = -INFINITY;
+            float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < BM_VALUES; ++k) {
-            v[k] = v[k] == v[k] ? v[k] : -INFINITY;
-            top = fmaxf(top, v[k]);
-        }
-        if (tid == 0) s.count = 0;
-        const float bound = nth_of_threads(top, p.n_best, s.sorted, &s.bound);
-        float m = s.sorted[0][0];
-#pragma unroll
-        for (int w = 1; w < BM_WARPS; ++w) m = fmaxf(m, s.sorted[w][0]);
+            for (int k = 0; k < BM_CHUNKS; ++k) top = fmaxf(top, C::largest(cur[k]));
 
-        // the values from the bound on, and the sum
-        float sum = 0.0f;
-        const float m2 = m * 1.4426950408889634f;
-#pragma unroll
-        for (int k = 0; k < BM_VALUES; ++k) {
-            if (v[k] >= bound && v[k] > -INFINITY) {
-                const int at = atomicAdd(&s.count, 1);
-                const unsigned token = static_cast<unsigned>(t0 + (k / E * BM_THREADS + tid) * E + k % E);
-                if (at < BM_LIST) s.keys[at] = static_cast<unsigned long long>(ordered(v[k])) << 32 | (0xFFFFFFFFu - token);
+            // the sum, against the thread's own running maximum
+            if (top > m) {
+                sum *= ex2((m - top) * LOG2E);
+                m = top;
             }
-            sum += ex2(fmaf(v[k], 1.4426950408889634f, -m2));
+            if (m > -INFINITY) {
+                const float m2 = m * LOG2E, before = sum;
+#pragma unroll
+                for (int k = 0; k < BM_CHUNKS; ++k)
+#pragma unroll
+                    for (int i = 0; i < E; ++i) sum += ex2(fmaf(C::at(cur[k], i), LOG2E, -m2));
+                if (!(sum < INFINITY)) {  // a NaN among them counts nothing
+                    sum = before;
+#pragma unroll 1
+                    for (int k = 0; k < BM_CHUNKS; ++k) {
+                        const uint4 c = pick(cur, k);
+#pragma unroll
+                        for (int i = 0; i < E; ++i) {
+                            const float v = C::at(c, i);
+                            if (v == v) sum += ex2(fmaf(v, LOG2E, -m2));
+                        }
+                    }
+                }
+            }
+
+            // keys above the n-th
+            const Key shown = *static_cast<volatile Key *>(&s.shown);
+            if (shown > kth) kth = shown - 1;  // the key itself may be one of this warp's
+            float bound = kth ? value_of(kth) : -INFINITY;
+            if (!__any_sync(0xFFFFFFFFu, top >= bound && top > -INFINITY)) continue;
+            unsigned bound_token = token_of(kth);
+            if (l0 == 0) {
+                const float b = nth_of_warp(top, p.n_best);
+                if (b > bound) bound = b, bound_token = 0xFFFFFFFFu;
+            }
+            // Few come here, so the code is short rather than unrolled: kernels of one
+            // batch wait for their instructions.
+            int count = 0, k = 0;
+            auto flush = [&]() {
+                __syncwarp();
+                for (int i = 0; i < count; ++i) {
+                    const Key key = s.wait[warp][i];
+                    if (key > kth) {
+                        best.insert(key);
+                        const Key n = best.nth(p.n_best);
+                        kth = n > kth ? n : kth;
+                    }
+                }
+                count = 0;
+                __syncwarp();
+            };
+            unsigned mine = 0;  // the thread's elements of chunk k - 1 that wait
+            uint4 c = cur[0];
+            unsigned t = 0;
+            for (;;) {
+                if (!__any_sync(0xFFFFFFFFu, mine)) {
+                    if (k == BM_CHUNKS) break;
+                    c = pick(cur, k);
+                    t = static_cast<unsigned>(t0 + l0 + (k * BM_THREADS + tid) * E);
+                    ++k;
+                    const float c_top = C::largest(c);
+                    if (!__any_sync(0xFFFFFFFFu, c_top >= bound && c_top > -INFINITY)) continue;
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        const float v = C::at(c, i);
+                        if (v > -INFINITY && (v > bound || (v == bound && t + i <= bound_token))) mine |= 1u << i;
+                    }
+                    continue;
+                }
+                const unsigned in = __ballot_sync(0xFFFFFFFFu, mine != 0);
+                if (mine) {
+                    const int i = __ffs(mine) - 1;
+                    mine &= mine - 1;
+                    float v = C::at(c, 0);
+#pragma unroll
+                    for (int e = 1; e < E; ++e) v = e == i ? C::at(c, e) : v;
+                    s.wait[warp][count + __popc(in & ((1u << lane) - 1))] = key_of(v, t + i);
+                }
+                count += __popc(in);
+                if (count > BM_LIST - 32) flush();
+            }
+            flush();
+            const Key n = best.nth(p.n_best);
+            if (lane == 0 && n > shown) atomicMax(&s.shown, n);
         }
+
+        // the warps' lists, maxima and sums
+        float wm = m;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xFFFFFFFFu, wm, d));
+        sum = m > -INFINITY ? sum * ex2((m - wm) * LOG2E) : 0.0f;
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        if (lane == 0) s.red[warp] = sum;
+        if (lane >= p.n_best) best.mine = 0;
+        s.lists[warp][lane] = best.mine;
+        const int count = __popc(__ballot_sync(0xFFFFFFFFu, best.mine != 0));
+        if (lane == 0) s.m[warp] = wm, s.sum[warp] = sum, s.count[warp] = count;
         __syncthreads();
-        const int count = s.count;
-        uint2 *part = p.part + out * p.n_best;
-        auto put = [&](int k, unsigned long long key) {
-            const unsigned o = static_cast<unsigned>(key >> 32);
-            part[k] = make_uint2(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o, 0xFFFFFFFFu - static_cast<unsigned>(key));
-        };
-        if (count <= BM_LIST) {
-            for (int i = tid; i < count; i += BM_THREADS) {
-                const unsigned long long key = s.keys[i];
-                int rank = 0;
-                for (int k = 0; k < count; ++k) rank += s.keys[k] > key;
-                if (rank < p.n_best) put(rank, key);
-            }
-            for (int k = count + tid; k < p.n_best; k += BM_THREADS) part[k] = make_uint2(0u, 0xFFFFFFFFu);
-        } else {
-            unsigned long long last = ~0ull;
-            for (int k = 0; k < p.n_best; ++k) {
-                unsigned long long key = 0;
+        int all = 0;
 #pragma unroll
-                for (int i = 0; i < BM_VALUES; ++i) {
-                    const unsigned token = static_cast<unsigned>(t0 + (i / E * BM_THREADS + tid) * E + i % E);
-                    const unsigned long long mine = static_cast<unsigned long long>(ordered(v[i])) << 32 | (0xFFFFFFFFu - token);
-                    if (v[i] > -INFINITY && mine < last && mine > key) key = mine;
-                }
-                last = block_largest(key, s.best);
-                if (tid == 0) put(k, last);  // the bound says that there are n
-            }
+        for (int w = 0; w < BM_WARPS; ++w) all += s.count[w];
+        if (best.mine) {
+            int rank = lane;
+#pragma unroll
+            for (int w = 0; w < BM_WARPS; ++w)
+                if (w != warp) rank += above(s.lists[w], s.count[w], best.mine);
+            if (rank < p.n_best) p.part[out * p.n_best + rank] = best.mine;
         }
+        if (tid >= all && tid < p.n_best) p.part[out * p.n_best + tid] = 0;
         if (tid == 0) {
-            float all = s.red[0];
+            float bm = s.m[0], total = 0.0f;
 #pragma unroll
-            for (int w = 1; w < BM_WARPS; ++w) all += s.red[w];
-            p.part_ml[out] = make_float2(m, m > -INFINITY ? all : 0.0f);
+            for (int w = 1; w < BM_WARPS; ++w) bm = fmaxf(bm, s.m[w]);
+#pragma unroll
+            for (int w = 0; w < BM_WARPS; ++w)
+                if (s.m[w] > -INFINITY) total = fmaf(s.sum[w], ex2((s.m[w] - bm) * LOG2E), total);
+            p.part_ml[out] = make_float2(bm, total);
         }
     }
 
@@ -358,12 +469,17 @@ cudaError_t launch_t(const BeamParams &p, int groups, cudaStream_t st)
 
 }  // namespace
 
-// About two blocks for each of 152 multiprocessors, in whole chunks a thread.
-int beam_slice(long long rows, long long vocab)
+// The number of slices whose last wave of blocks ends first.  A block costs about
+// as much as 8192 elements beside its own, a slice more for the join about 64.
+int beam_slices(long long rows, long long vocab)
 {
-    const long long want = (2 * ATTN_SMS + rows - 1) / rows;
-    const long long slice = ((vocab + want - 1) / want + 2047) / 2048 * 2048;
-    return static_cast<int>(slice < 2048 ? 2048 : slice > BEAM_SLICE_MAX ? BEAM_SLICE_MAX : slice);
+    constexpr long long SLOTS = BM_BLOCKS * ATTN_SMS;
+    long long best = 1, best_cost = INT64_MAX;
+    for (long long n = 1; n <= 64 && (n == 1 || vocab / n >= 2048); ++n) {
+        const long long cost = (rows * n + SLOTS - 1) / SLOTS * (vocab / n + 8192) + 64 * n;
+        if (cost < best_cost) best_cost = cost, best = n;
+    }
+    return static_cast<int>(best);
 }
 
 cudaError_t launch_beam(const BeamParams &p, qgemv_dtype type, int groups, cudaStream_t st)

@@ -25,6 +25,8 @@ qgemv_status check_cache8(const qgemv_kv8_cache *c)
         !extent_ok(c->n_heads, c->head_stride) || !extent_ok(c->n_pages, c->scale_page_stride) ||
         !extent_ok(c->page_size / c->block_size, c->scale_block_stride) || !extent_ok(c->n_heads, c->scale_head_stride))
         return QGEMV_ERR_INVALID_ARG;
+    if ((c->n_pages > 1 && c->page_stride == 0) || c->row_stride == 0 || (c->n_heads > 1 && c->head_stride == 0))
+        return QGEMV_ERR_INVALID_ARG;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % 16 || c->row_stride % 16 || c->head_stride % 16 ||
         !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
         return QGEMV_ERR_MISALIGNED;
@@ -90,6 +92,10 @@ qgemv_status check_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c)
         return QGEMV_ERR_INVALID_ARG;
     if (static_cast<long long>(b->n_seqs) * b->n_q * b->n_q_heads > (1ll << 27)) return QGEMV_ERR_INVALID_ARG;
     if (!(b->scale >= 0.0f) || std::isinf(b->scale)) return QGEMV_ERR_INVALID_ARG;
+    // the strides of a tensor map end there
+    constexpr long long kMapStride = 1ll << 40;
+    if (c->page_stride >= kMapStride || c->row_stride >= kMapStride || c->head_stride >= kMapStride)
+        return QGEMV_ERR_UNSUPPORTED;
     return QGEMV_OK;
 }
 // The tables' entries that lengths may reach.
@@ -121,7 +127,7 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     // Balanced ranges cost a walk over all lengths and a second launch.  Units of up
     // to four tiles a warp are a block each instead, and so are those of very many
     // sequences, which spread over the multiprocessors well enough by themselves.
-    a.balanced = tiles > 32 && b->n_seqs <= 1024;
+    a.balanced = tiles > 24 && b->n_seqs <= 1024;
     a.ml_at = a.parts_at = kCounterArea;
     a.ws_bytes = kCounterArea;
     a.combine_warps = 1;
@@ -130,10 +136,13 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
         a.grid = static_cast<int>(units);
         return QGEMV_OK;
     }
-    const long long most = static_cast<long long>(ATTN_SMS) * kv8_blocks(c->head_dim, nt);
-    a.grid = static_cast<int>(std::min(most, ceil_div(units * tiles, KV8_SPLIT_MIN)));
-    // parts of a unit: about grid / units; few are joined by a warp for each row, many by all of a block
-    const long long parts = a.grid / std::min<long long>(units, a.grid);
+    // the line of all sequences' tiles in ranges, a block for each range, cache head and tile of rows
+    const long long per_seq = units / b->n_seqs, blocks = static_cast<long long>(ATTN_SMS) * kv8_blocks(c->head_dim, nt);
+    const long long ranges = std::min(std::max(1ll, blocks / per_seq), ceil_div(b->n_seqs * tiles, KV8_SPLIT_MIN));
+    if (ranges * per_seq > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
+    a.grid = static_cast<int>(ranges * per_seq);
+    // parts of a sequence: about ranges / n_seqs; few are joined by a warp for each row, many by all of a block
+    const long long parts = ranges / std::min<long long>(b->n_seqs, ranges);
     while (a.combine_warps < 8 && 2 * a.combine_warps <= parts) a.combine_warps *= 2;
     a.parts_at = kCounterArea;
     a.ml_at = a.parts_at + 16ll * a.grid;
@@ -153,8 +162,9 @@ bool plan_beam(const qgemv_beam_spec *s, BeamPlan &a)
         s->n_best > 32 || s->vocab < 1 || s->vocab > (1 << 26))
         return false;
     const long long rows = static_cast<long long>(std::min(s->n_groups, BEAM_GROUPS)) * s->n_beams;  // of a launch
-    a.slice = beam_slice(rows, s->vocab);
-    a.slices = static_cast<int>(ceil_div(s->vocab + 7, a.slice));  // a row may begin 7 elements into a 16-byte chunk
+    // a row may begin 7 elements into a 16-byte chunk
+    a.slice = static_cast<int>(ceil_div(ceil_div(s->vocab + 7, beam_slices(rows, s->vocab)), 2048) * 2048);
+    a.slices = static_cast<int>(ceil_div(s->vocab + 7, a.slice));
     a.ml_at = kCounterArea;
     a.part_at = a.ml_at + 8ll * rows * a.slices;
     a.ws_bytes = (a.part_at + 8ll * rows * a.slices * s->n_best + 15) / 16 * 16;
@@ -467,7 +477,7 @@ qgemv_status qgemv_beam_select(const void *logits, qgemv_dtype type, int64_t x_s
     p.slices = a.slices;
     p.cnt = static_cast<unsigned *>(ws);
     p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + a.ml_at);
-    p.part = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(ws) + a.part_at);
+    p.part = reinterpret_cast<unsigned long long *>(static_cast<uint8_t *>(ws) + a.part_at);
     for (int g = 0; g < c.n_groups; g += BEAM_GROUPS) {
         const long long r = static_cast<long long>(g) * c.n_beams, o = static_cast<long long>(g) * c.n_best;
         p.x = static_cast<const uint8_t *>(logits) + r * x_stride * eb;

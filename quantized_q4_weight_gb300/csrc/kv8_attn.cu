@@ -33,42 +33,41 @@
 // a block each and need no second launch.
 #include "kv8_ops.h"
 #include "qgemv_internal.cuh"
+#include "tma.cuh"
 
 namespace qg {
 namespace {
 
-constexpr int K8_WARPS = 8, K8_THREADS = 32 * K8_WARPS;
+constexpr int KC_WARPS = 8, KC_THREADS = 32 * KC_WARPS;  // of a block of the combining launch
 constexpr float K8_NEG = -1e30f;   // below every finite score; differences of it stay finite
 constexpr float K8_LIFT = 10.0f;   // a new reference lies so far below the largest score
 constexpr float K8_SLACK = 14.0f;  // weights reach 2^14 before it moves (f16 ends at 2^16)
 
+// DP: head_dim rounded up to 64, 128 or 256; NT: tiles of 8 query rows.
 template <int DP, int NT>
 struct K8Cfg {
-    static constexpr int KC = DP >= 64 ? DP / 64 : 1;     // 64-element chunks of a row of K
+    static constexpr int KC = DP / 64;                    // 64-element chunks of a row of K
     static constexpr int VB = DP == 64 ? 8 : 16;          // bytes of a row of V that a thread takes at once
     static constexpr int VC = DP / (8 * VB);              // such pieces
     static constexpr int MT = VC * VB / 2;                // 16-row tiles of the sums: DP / 16
-    static constexpr int TILE = 2 * KV8_KEYS * DP;        // bytes of a tile, K and V
-    static constexpr int BLOCKS = DP == 256 || (DP == 128 && NT > 2) ? 1 : 2;
-    static constexpr int STAGES = DP == 64 ? 6 : DP == 128 && NT > 2 ? 6 : 3;
-    static constexpr bool QREG = DP * NT <= 256;          // Q's fragments in registers
-    static constexpr int OFF_META = K8_WARPS * STAGES * TILE;            // per warp and stage: j0, ks, vs
-    static constexpr int OFF_Q = OFF_META + K8_WARPS * STAGES * 16;
+    static constexpr int ROW = DP == 64 ? 64 : 128;       // bytes of a row of a copied box
+    static constexpr int BOX = KV8_KEYS * ROW;            // of a tile's box; K has DP / ROW of them, then V
+    static constexpr int TILE = 2 * KV8_KEYS * DP;
+    static constexpr int BLOCKS = kv8_blocks(DP, NT);
+    static constexpr int WARPS = kv8_warps(DP, NT), THREADS = 32 * WARPS;
+    static constexpr int STAGES = DP == 64 ? (NT > 2 ? 4 : 3) : DP == 128 && BLOCKS == 1 ? 3 : 2;
+    static constexpr bool QREG = DP * NT <= 128;          // Q's fragments in registers
+    static constexpr int OFF_META = WARPS * STAGES * TILE;               // per warp and stage: ks, vs of both halves
+    static constexpr int OFF_Q = OFF_META + WARPS * STAGES * 16;
     static constexpr int OFF_QS = OFF_Q + 8 * NT * DP * 2;
     static constexpr int OFF_ML = OFF_QS + 8 * NT * 4;
-    static constexpr int SMEM = OFF_ML + K8_WARPS * 8 * NT * 8;
-    static_assert(STAGES >= NT, "the warps' sums fit the ring");
+    static constexpr int OFF_BAR = OFF_ML + WARPS * 8 * NT * 8;  // per warp and stage
+    static constexpr int SMEM = OFF_BAR + WARPS * STAGES * 8 + 1024;  // boxes begin at 1024 bytes: the swizzle's period
+    static_assert(2 * STAGES >= NT, "the warps' sums fit the ring");
+    static_assert(BLOCKS * (SMEM + 2048) <= 228 * 1024, "the blocks fit a multiprocessor");
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp8(uint32_t dst, const void *src, bool take)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(take ? 8 : 0) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void *src, bool take)
+__device__ __forceinline__ void cp4_if(uint32_t dst, const void *src, bool take)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(take ? 4 : 0) : "memory");
 }
@@ -82,6 +81,18 @@ __device__ __forceinline__ float ex2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x)
+{
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ void mma(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0, unsigned b1)
@@ -124,6 +135,22 @@ __device__ __forceinline__ void cvt4(unsigned w, unsigned &lo, unsigned &hi)
 __device__ __forceinline__ unsigned without_nan(unsigned w)
 {
     return w & ~__vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+}
+
+// Boxes lie in shared memory with the 16-byte chunks of a row swizzled (by the row's
+// number, or its half with 64-byte rows).  The product's rows 0 .. 7 are these rows
+// of a box's eight, so that neither the reads of K (a row for four lanes, four chunks of it)
+// nor those of V (every second row, half of its chunks) meet a bank twice.
+template <int DP>
+__device__ __forceinline__ int box_row(int k)
+{
+    return DP == 64 ? k ^ (k >> 1 & 1) : (k & 1) << 2 | k >> 1;
+}
+// Byte offset of chunk c of row r.
+template <int DP>
+__device__ __forceinline__ int box_off(int r, int c)
+{
+    return DP == 64 ? r * 64 + ((c ^ (r >> 1 & 3)) << 4) : r * 128 + ((c ^ (r & 7)) << 4);
 }
 
 // What a sequence's queries see of it, in tiles: the tiles of the first rows,
@@ -188,7 +215,7 @@ __device__ __forceinline__ void store_lse(const Kv8AttnParams &p, int b, int h, 
 __device__ __forceinline__ void store_none(const Kv8AttnParams &p, int b, int h, int row0, int rows)
 {
     const int quads = p.d / 4;
-    for (int i = threadIdx.x; i < rows * quads; i += K8_THREADS) {
+    for (int i = threadIdx.x; i < rows * quads; i += blockDim.x) {
         const int row = row0 + i / quads, c = i % quads;
         store_o(p, b, h, row, c, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
         if (c == 0) store_lse(p, b, h, row, 0.0f, 0.0f);
@@ -196,10 +223,13 @@ __device__ __forceinline__ void store_none(const Kv8AttnParams &p, int b, int h,
 }
 
 template <int CODE, int DP, int NT>
-__global__ void __launch_bounds__(K8_THREADS, K8Cfg<DP, NT>::BLOCKS) kv8_attn_kernel(const __grid_constant__ Kv8AttnParams p)
+__global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS) kv8_attn_kernel(
+    const __grid_constant__ Kv8AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map)
 {
     using C = K8Cfg<DP, NT>;
-    extern __shared__ __align__(128) uint8_t k8_smem[];
+    extern __shared__ __align__(16) uint8_t k8_raw[];
+    __shared__ int s_abort;
+    uint8_t *k8_smem = k8_raw + ((1024 - (smem_addr(k8_raw) & 1023)) & 1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const uint32_t s_base = smem_addr(k8_smem);
     const uint32_t s_ring = s_base + warp * C::STAGES * C::TILE;
@@ -207,13 +237,26 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<DP, NT>::BLOCKS) kv8_attn_ke
     float *s_qs = reinterpret_cast<float *>(k8_smem + C::OFF_QS);
     float2 *s_ml = reinterpret_cast<float2 *>(k8_smem + C::OFF_ML);
 
+    uint64_t *full = reinterpret_cast<uint64_t *>(k8_smem + C::OFF_BAR) + warp * C::STAGES;
+    volatile int *abort_flag = &s_abort;
+
     pdl_launch_dependents();
+    if (lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(warp & 1 ? &v_map : &k_map) : "memory");
+#pragma unroll
+        for (int i = 0; i < C::STAGES; ++i) mbar_init(full + i, 1);
+        fence_mbar_init();
+    }
+    if (tid == 0) s_abort = 0;
+    __syncthreads();
     pdl_wait();
 
-    // The block's range [lo, hi) of the line of all units' tiles, and the
-    // sequence it begins in.  Units: sequence, then head, then tile of query rows.
-    const int per_seq = p.hkv * p.row_tiles;
-    long long lo, hi, range = 0, seq_at;  // seq_at: where sequence b's tiles begin
+    // The block's range [lo, hi) of the line of all sequences' tiles, the sequence
+    // that it begins in and where that one's tiles begin.
+    const int per_seq = p.hkv * p.row_tiles, unit = blockIdx.x % per_seq;
+    const int h = unit / p.row_tiles, row0 = unit % p.row_tiles * p.tile_rows;
+    const int rows = min(p.tile_rows, p.rows - row0);
+    long long lo, hi, range = 0, seq_at;
     int b;
     if (p.balanced) {
         // every warp adds all sequences' tiles up, each lane a run of them
@@ -230,105 +273,108 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<DP, NT>::BLOCKS) kv8_attn_ke
             const long long v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
             if (lane >= o) upto += v;
         }
-        const long long total = __shfl_sync(0xFFFFFFFFu, upto, 31) * per_seq;
-        range = max(static_cast<long long>(KV8_SPLIT_MIN), (total + p.grid - 1) / p.grid);
-        lo = blockIdx.x * range, hi = min(total, lo + range);
+        const long long total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        const int ranges = p.grid / per_seq;
+        range = max(static_cast<long long>(KV8_SPLIT_MIN), (total + ranges - 1) / ranges);
+        lo = blockIdx.x / per_seq * range, hi = min(total, lo + range);
         // the first lane whose run ends behind lo walks its run
-        const unsigned behind = __ballot_sync(0xFFFFFFFFu, upto * per_seq > lo);
+        const unsigned behind = __ballot_sync(0xFFFFFFFFu, upto > lo);
         const int owner = behind ? __ffs(behind) - 1 : 0;
         int at = lane * run;
-        long long begin = upto - mine;
+        seq_at = upto - mine;
         if (lane == owner && lo < total) {
             for (;; ++at) {
                 const int n = Seen(p, __ldg(p.lens + at)).tiles;
-                if ((begin + n) * per_seq > lo) break;
-                begin += n;
+                if (seq_at + n > lo) break;
+                seq_at += n;
             }
         }
         b = __shfl_sync(0xFFFFFFFFu, at, owner);
-        seq_at = __shfl_sync(0xFFFFFFFFu, begin, owner) * per_seq;
+        seq_at = __shfl_sync(0xFFFFFFFFu, seq_at, owner);
         for (int i = blockIdx.x; i < p.n_seqs; i += p.grid)
             if (Seen(p, __ldg(p.lens + i)).n == 0)
-                for (int h = 0; h < p.hkv; ++h) store_none(p, i, h, 0, p.rows);
+                for (int k = 0; k < p.hkv; ++k) store_none(p, i, k, 0, p.rows);
         if (tid == 0) p.parts[blockIdx.x] = make_int4(0, 0, 0, 0);
         if (lo >= total) return;
     } else {
         b = blockIdx.x / per_seq;
-        const int n = __ldg(p.lens + b), u = blockIdx.x % per_seq;
-        const Seen seen(p, n);
+        const int n = __ldg(p.lens + b);
         if ((n < 0 || n > p.max_len) && tid == 0) atomicCAS(p.status, 0u, ST_BAD_ID);
+        const Seen seen(p, n);
         if (seen.n == 0) {
-            const int row0 = u % p.row_tiles * p.tile_rows;
-            store_none(p, b, u / p.row_tiles, row0, min(p.tile_rows, p.rows - row0));
+            store_none(p, b, h, row0, rows);
             return;
         }
-        seq_at = 0;
-        lo = static_cast<long long>(u) * seen.tiles, hi = lo + seen.tiles;
+        lo = seq_at = 0, hi = seen.tiles;
     }
 
     Seen seen(p, __ldg(p.lens + b));
-    int unit = static_cast<int>((lo - seq_at) / seen.tiles);
     long long pos = lo;
+    // where in a box the thread's bytes of K lie (of 64 elements each) and those of V (of two rows)
+    const int pg = box_row<DP>(g);
+    const uint32_t k_off0 = box_off<DP>(pg, t), k_off1 = box_off<DP>(pg, 4 + t);
+    const uint32_t v_off0 = DP == 64 ? box_off<DP>(box_row<DP>(2 * t), g >> 1) + 8 * (g & 1) : box_off<DP>(box_row<DP>(2 * t), pg);
+    const uint32_t v_off1 =
+        DP == 64 ? box_off<DP>(box_row<DP>(2 * t + 1), g >> 1) + 8 * (g & 1) : box_off<DP>(box_row<DP>(2 * t + 1), pg);
+    const int v_unit = DP == 64 ? g : pg;  // of VB elements of a head
+    // the warp's ring: tiles on their way and taken, the next to write and to read, the
+    // phases to wait for, and whether pages are there (a bit for each stage, and half of it)
+    int sent = 0, taken = 0, slot = 0, rd = 0;
+    unsigned phases = 0, absent = 0;
+    bool ok = true;
     while (pos < hi) {
-        const long long u0 = seq_at + static_cast<long long>(unit) * seen.tiles;
-        const int i0 = static_cast<int>(pos - u0), i1 = static_cast<int>(min(static_cast<long long>(seen.tiles), hi - u0));
-        const int h = unit / p.row_tiles, row0 = unit % p.row_tiles * p.tile_rows;
-        const int rows = min(p.tile_rows, p.rows - row0);
+        const int i0 = static_cast<int>(pos - seq_at), i1 = static_cast<int>(min(static_cast<long long>(seen.tiles), hi - seq_at));
 
-        // ---- the warp's tiles i0 + warp, + 8, ... on their way
+        // ---- the warp's tiles i0 + warp, + WARPS, ... on their way
         const int32_t *table = p.pages + b * p.pages_stride;
-        const uint8_t *kh = p.c.k + h * p.c.head_stride, *vh = p.c.v + h * p.c.head_stride;
-        const float *ksh = p.c.ks + h * p.c.scale_head, *vsh = p.c.vs + h * p.c.scale_head;
-        auto page_of = [&](int i) { return i < i1 ? __ldg(table + (seen.tile(i) * KV8_KEYS >> p.c.page_shift)) : 0; };
-        int ahead = i0 + warp, page = page_of(ahead), slot = 0;
+        const float *st = (lane & 1 ? p.c.vs : p.c.ks) + h * p.c.scale_head;  // lanes 0 .. 3: k and v of the halves
+        const bool split = p.c.page_shift == 4;  // a tile's halves lie on pages of their own
+        auto page_of = [&](int i, int half) {
+            const int j = seen.tile(i) * KV8_KEYS + 16 * half;
+            return i < i1 && j < seen.n ? __ldg(table + (j >> p.c.page_shift)) : 0;
+        };
+        // a lane for each box: of K and V, of each 128 elements, of each half where it is split
+        constexpr int WIDE = DP / C::ROW;
+        const bool box_v = lane & 1;
+        const int box_x = (lane >> 1) % WIDE, box_half = (lane >> 1) / WIDE;
+        const bool boxes = lane < 2 * WIDE * (split ? 2 : 1);
+        const uint32_t box_to = s_ring + (box_v ? KV8_KEYS * DP : 0) + box_x * C::BOX + box_half * 16 * C::ROW;
+        int ahead = i0 + warp;
+        int page = page_of(ahead, 0), page1 = split ? page_of(ahead, 1) : page;
         auto issue = [&]() {
-            if (ahead < i1) {
+            if (ahead < i1 && ok) {
                 const int j0 = seen.tile(ahead) * KV8_KEYS, in_page = j0 & ((1 << p.c.page_shift) - 1);
-                const bool here = page >= 0 && page < p.c.n_pages;
-                const int left = here ? seen.n - j0 : 0;  // rows of the tile that the sequence has
-                const long long at = here ? page * p.c.page_stride + in_page * p.c.row_stride : 0;
-                const uint32_t dst = s_ring + slot * C::TILE;
-                const uint8_t *kr = kh + at + g * p.c.row_stride, *vr = vh + at + 2 * t * p.c.row_stride;
-#pragma unroll
-                for (int c = 0; c < C::KC; ++c) {
-                    const int e = 64 * c + 16 * t;
-                    cp16(dst + (2 * c) * 512 + lane * 16, kr + e, g < left && e < p.d);
-                    cp16(dst + (2 * c + 1) * 512 + lane * 16, kr + 8 * p.c.row_stride + e, g + 8 < left && e < p.d);
+                const unsigned n_pages = static_cast<unsigned>(p.c.n_pages);
+                const bool here = static_cast<unsigned>(page) < n_pages, here1 = static_cast<unsigned>(page1) < n_pages;
+                absent = (absent & ~(3u << 2 * slot)) | (static_cast<unsigned>(!here) | static_cast<unsigned>(!here1) << 1) << 2 * slot;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(full + slot, C::TILE);
+                    if (!here || !here1) atomicCAS(p.status, 0u, ST_BAD_ID);
                 }
-                const uint32_t dv = dst + KV8_KEYS * DP;
-#pragma unroll
-                for (int c = 0; c < C::VC; ++c) {
-                    const int e = 8 * C::VB * c + C::VB * g;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = (r & 1) + 8 * (r >> 1);  // beside 2 t
-                        const bool take = 2 * t + row < left && e < p.d;
-                        const uint32_t to = dv + (4 * c + r) * 32 * C::VB + lane * C::VB;
-                        if constexpr (C::VB == 16)
-                            cp16(to, vr + row * p.c.row_stride + e, take);
-                        else
-                            cp8(to, vr + row * p.c.row_stride + e, take);
-                    }
+                __syncwarp();
+                if (boxes) {  // a page that is not there reads as zeros: beyond the tensor
+                    const int at = box_half ? here1 ? page1 : static_cast<int>(n_pages) : here ? page : static_cast<int>(n_pages);
+                    tma_load4(box_to + slot * C::TILE, box_v ? &v_map : &k_map, box_x * C::ROW, in_page, h, at, full + slot);
                 }
-                const uint32_t meta = s_meta + slot * 16;
-                const long long sc = here ? page * p.c.scale_page + (in_page >> p.c.block_shift) * p.c.scale_block : 0;
-                if (lane == 0) cp4(meta + 4, ksh + sc, here);
-                if (lane == 1) cp4(meta + 8, vsh + sc, here);
-                if (lane == 2) {
-                    asm volatile("st.shared.s32 [%0], %1;" ::"r"(meta), "r"(here ? j0 : -1) : "memory");
-                    if (!here) atomicCAS(p.status, 0u, ST_BAD_ID);
+                if (lane < 4) {
+                    const int row = split ? 0 : in_page + 16 * (lane >> 1), pg = lane & 2 ? page1 : page;
+                    const bool take = j0 + 16 * (lane >> 1) < seen.n && (lane & 2 ? here1 : here);
+                    const long long sc = pg * p.c.scale_page + (row >> p.c.block_shift) * p.c.scale_block;
+                    cp4_if(s_meta + slot * 16 + lane * 4, st + (take ? sc : 0), take);
                 }
-                ahead += K8_WARPS;
-                page = page_of(ahead);
+                ++sent;
+                slot = slot + 1 == C::STAGES ? 0 : slot + 1;
+                ahead += C::WARPS;
+                page = page_of(ahead, 0);
+                page1 = split ? page_of(ahead, 1) : page;
             }
             cp_commit();
-            slot = slot + 1 == C::STAGES ? 0 : slot + 1;
         };
-#pragma unroll
+#pragma unroll 1
         for (int s = 0; s < C::STAGES - 1; ++s) issue();
 
         // ---- the unit's queries, in f16; bf16 rows divided by a power of two
-        for (int r = warp; r < 8 * NT; r += K8_WARPS) {
+        for (int r = warp; r < 8 * NT; r += C::WARPS) {
             uint4 w = make_uint4(0, 0, 0, 0);
             const int row = row0 + r;
             if (r < rows && 8 * lane < p.d) {
@@ -390,165 +436,194 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<DP, NT>::BLOCKS) kv8_attn_ke
                 for (int e = 0; e < 4; ++e) o[j][i][e] = 0.0f;
         }
 
-        int rd = 0;
-        for (int i = i0 + warp; i < i1; i += K8_WARPS) {
-            issue();
-            cp_wait<C::STAGES - 1>();
-            __syncwarp();
-            const uint32_t src = s_ring + rd * C::TILE, meta = s_meta + rd * 16;
-            int j0;
-            float ks, vs;
-            asm volatile("ld.shared.s32 %0, [%1];" : "=r"(j0) : "r"(meta));
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks) : "r"(meta + 4));
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(meta + 8));
-            rd = rd + 1 == C::STAGES ? 0 : rd + 1;
-            if (j0 < 0) {  // its page is not there
-                __syncwarp();
-                continue;
-            }
-            const bool whole = j0 + KV8_KEYS - 1 <= seen.n - p.n_q &&
-                               (!p.window || j0 > seen.n - 1 - p.window || j0 + KV8_KEYS - 1 < p.sinks);
-
-            // ---- scores of 16 keys
-            float s[NT][4];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[j][e] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < C::KC; ++c) {
-                const uint4 x = lds128(src + (2 * c) * 512 + lane * 16), y = lds128(src + (2 * c + 1) * 512 + lane * 16);
-                const unsigned xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-                unsigned a[4][4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    cvt4<CODE>(xw[k], a[k][0], a[k][2]);
-                    cvt4<CODE>(yw[k], a[k][1], a[k][3]);
-                }
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    unsigned f[8];
-                    if constexpr (C::QREG) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) f[k] = qf[j][c][k];
-                    } else {
-                        load_q(j, c, f);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) mma(s[j], a[k][0], a[k][1], a[k][2], a[k][3], f[2 * k], f[2 * k + 1]);
-                }
-            }
-
-            // ---- weights.  A block of zeros has scale 0: any other does for its codes
-            vs = vs < 8.673617e-19f ? 8.673617e-19f : vs;  // 2^-60
-            const float lv = log2f(vs), inv = 1.0f / vs;
-            float f[NT][2];
-            bool over = false;
+        // The references that a tile with sums s (-infinity: not seen) asks for.
+        auto raise = [&](const float (&s)[2][NT][4], const float (&ks)[2], const float (&lv)[2]) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    f[j][e] = ks * qs[j][e];
-                    const float at = lv - m[j][e];
-                    if (!whole) {
-                        const int q_pos = seen.n - p.n_q + (row0 + 8 * j + 2 * t + e) / p.group;
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const int key = j0 + g + 8 * k;
-                            const bool sees = key <= q_pos && (!p.window || key > q_pos - p.window || key < p.sinks);
-                            s[j][2 * k + e] = sees ? fmaf(s[j][2 * k + e], f[j][e], lv) : -INFINITY;
-                            over |= s[j][2 * k + e] - m[j][e] > K8_SLACK;
+                            const float v = s[x][j][2 * k + e];
+                            mx = fmaxf(mx, v == -INFINITY ? v : fmaf(v, ks[x] * qs[j][e], lv[x]));
                         }
-                    } else {
-                        over |= fmaxf(s[j][e] * f[j][e], s[j][2 + e] * f[j][e]) + at > K8_SLACK;
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+                    if (mx - m[j][e] > K8_SLACK) {
+                        const float mn = mx - K8_LIFT, by = ex2(m[j][e] - mn);
+                        m[j][e] = mn;
+                        l[j][e] *= by;
+#pragma unroll
+                        for (int i = 0; i < C::MT; ++i) o[j][i][e] *= by, o[j][i][2 + e] *= by;
                     }
                 }
-            if (__any_sync(0xFFFFFFFFu, over) || !whole) {
-                // exact scores, and the references with them
+        };
+
+#pragma unroll 1
+        for (int i = i0 + warp; i < i1; i += C::WARPS) {
+            issue();
+            cp_wait<C::STAGES - 1>();
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(full + rd, phases >> rd & 1, abort_flag, p.status, WAIT_LIMIT_NS)) && ok;
+            if (!ok) break;
+            const uint32_t src = s_ring + rd * C::TILE;
+            float ks[2], vs[2], lv[2], inv[2];
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(ks[0]), "=f"(vs[0]), "=f"(ks[1]), "=f"(vs[1])
+                         : "r"(s_meta + rd * 16));
+            const unsigned gone = absent >> 2 * rd & 3;  // halves whose page is not there
+            phases ^= 1u << rd;
+            ++taken;
+            rd = rd + 1 == C::STAGES ? 0 : rd + 1;
+            const int j0 = seen.tile(i) * KV8_KEYS;
+            const bool whole = j0 + KV8_KEYS - 1 <= seen.n - p.n_q && !gone &&
+                               (!p.window || j0 > seen.n - 1 - p.window || j0 + KV8_KEYS - 1 < p.sinks);
+
+            // ---- scores of 2 x 16 keys
+            float s[2][NT][4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (whole) {
-                            s[j][e] = fmaf(s[j][e], f[j][e], lv);
-                            s[j][2 + e] = fmaf(s[j][2 + e], f[j][e], lv);
-                        }
-                        float mx = fmaxf(s[j][e], s[j][2 + e]);
+                    for (int e = 0; e < 4; ++e) s[x][j][e] = 0.0f;
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-                        if (mx - m[j][e] > K8_SLACK) {
-                            const float mn = mx - K8_LIFT, c = ex2(m[j][e] - mn);
-                            m[j][e] = mn;
-                            l[j][e] *= c;
+            for (int c = 0; c < C::KC; ++c)
 #pragma unroll
-                            for (int i = 0; i < C::MT; ++i) o[j][i][e] *= c, o[j][i][2 + e] *= c;
-                        }
-                        s[j][e] = ex2(s[j][e] - m[j][e]);
-                        s[j][2 + e] = ex2(s[j][2 + e] - m[j][e]);
+                for (int h2 = 0; h2 < 2; ++h2) {
+                    const uint32_t at = src + (DP == 64 ? 0 : c >> 1) * C::BOX + 16 * h2 * C::ROW + ((c & 1) ? k_off1 : k_off0);
+                    const uint4 x = lds128(at), y = lds128(at + 8 * C::ROW);
+                    const unsigned xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+                    unsigned a[4][4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        cvt4<CODE>(xw[k], a[k][0], a[k][2]);
+                        cvt4<CODE>(yw[k], a[k][1], a[k][3]);
                     }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        unsigned f[8];
+                        if constexpr (C::QREG) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) f[k] = qf[j][c][k];
+                        } else {
+                            load_q(j, c, f);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma(s[h2][j], a[k][0], a[k][1], a[k][2], a[k][3], f[2 * k], f[2 * k + 1]);
+                    }
+                }
+
+            // ---- weights.  A block of zeros has scale 0: any other does for its codes
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                vs[x] = vs[x] < 8.673617e-19f ? 8.673617e-19f : vs[x];  // 2^-60
+                lv[x] = lg2(vs[x]), inv[x] = rcp(vs[x]);
+            }
+            bool up = true;
+            if (whole) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float f = ks[x] * qs[j][e], at = lv[x] - m[j][e];
+                            top = fmaxf(top, fmaxf(fmaf(s[x][j][e], f, at), fmaf(s[x][j][2 + e], f, at)));
+                        }
+                up = __any_sync(0xFFFFFFFFu, top > K8_SLACK);
             } else {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float at = lv - m[j][e];
-                        s[j][e] = ex2(fmaf(s[j][e], f[j][e], at));
-                        s[j][2 + e] = ex2(fmaf(s[j][2 + e], f[j][e], at));
+                        const int q_pos = seen.n - p.n_q + (row0 + 8 * j + 2 * t + e) / p.group;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int key = j0 + 16 * x + pg + 8 * k;
+                                const bool sees = key <= q_pos && (!p.window || key > q_pos - p.window || key < p.sinks) &&
+                                                  !(gone >> x & 1);
+                                if (!sees) s[x][j][2 * k + e] = -INFINITY;
+                            }
                     }
             }
-            unsigned pb[NT][2];
+            if (up) raise(s, ks, lv);
+            unsigned pb[2][NT][2];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float sum = s[j][e] + s[j][2 + e];
-                    // a row that sees none of the tile takes nothing from its scale either
-                    if (whole || sum != 0.0f) l[j][e] = fmaf(sum, inv, l[j][e]);
+                for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = ks[x] * qs[j][e], at = lv[x] - m[j][e];
+                        float a = fmaf(s[x][j][e], f, at), b = fmaf(s[x][j][2 + e], f, at);
+                        if (!whole) {
+                            a = s[x][j][e] == -INFINITY ? -INFINITY : a;
+                            b = s[x][j][2 + e] == -INFINITY ? -INFINITY : b;
+                        }
+                        s[x][j][e] = a = ex2(a);
+                        s[x][j][2 + e] = b = ex2(b);
+                        // a row that sees none of the half takes nothing from its scale either
+                        if (whole || a + b != 0.0f) l[j][e] = fmaf(a + b, inv[x], l[j][e]);
+                    }
+                    // The weights are operands in f16: off by half a unit of it.  l keeps them whole.
+                    pb[x][j][0] = movm(pack(s[x][j][0], s[x][j][1]));
+                    pb[x][j][1] = movm(pack(s[x][j][2], s[x][j][3]));
                 }
-                // The weights are operands in f16: off by half a unit of it.  l keeps them whole.
-                pb[j][0] = movm(pack(s[j][0], s[j][1]));
-                pb[j][1] = movm(pack(s[j][2], s[j][3]));
-            }
 
             // ---- weighted sums of v
-            const uint32_t sv = src + KV8_KEYS * DP;
 #pragma unroll
-            for (int c = 0; c < C::VC; ++c) {
-                constexpr int W = C::VB / 4;
-                unsigned v[4][W];
+            for (int c = 0; c < C::VC; ++c)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint32_t at = sv + (4 * c + r) * 32 * C::VB + lane * C::VB;
-                    if constexpr (W == 4) {
-                        const uint4 x = lds128(at);
-                        v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
-                    } else {
-                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[r][0]), "=r"(v[r][1]) : "r"(at));
+                for (int h2 = 0; h2 < 2; ++h2) {
+                    constexpr int W = C::VB / 4;
+                    unsigned v[4][W];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t at = src + KV8_KEYS * DP + c * C::BOX + (16 * h2 + 8 * (r >> 1)) * C::ROW + (r & 1 ? v_off1 : v_off0);
+                        if constexpr (W == 4) {
+                            const uint4 x = lds128(at);
+                            v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
+                        } else {
+                            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[r][0]), "=r"(v[r][1]) : "r"(at));
+                        }
                     }
-                }
-                if (CODE == QGEMV_CODE_E4M3 && !whole) {
+                    if (CODE == QGEMV_CODE_E4M3 && !whole) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
+                        for (int r = 0; r < 4; ++r)
 #pragma unroll
-                        for (int k = 0; k < W; ++k) v[r][k] = without_nan(v[r][k]);
-                }
-#pragma unroll
-                for (int k = 0; k < W; ++k)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        // elements 4 k + 2 x and + 1 of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
-                        unsigned a0, a1, a2, a3;
-                        cvt4<CODE>(__byte_perm(v[0][k], v[1][k], x ? 0x7362 : 0x5140), a0, a1);
-                        cvt4<CODE>(__byte_perm(v[2][k], v[3][k], x ? 0x7362 : 0x5140), a2, a3);
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-                            mma(o[j][(C::VB / 2) * c + 2 * k + x], a0, a1, a2, a3, pb[j][0], pb[j][1]);
+                            for (int k = 0; k < W; ++k) v[r][k] = without_nan(v[r][k]);
                     }
-            }
+#pragma unroll
+                    for (int k = 0; k < W; ++k)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            // elements 4 k + 2 x and + 1 of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
+                            unsigned a0, a1, a2, a3;
+                            cvt4<CODE>(__byte_perm(v[0][k], v[1][k], x ? 0x7362 : 0x5140), a0, a1);
+                            cvt4<CODE>(__byte_perm(v[2][k], v[3][k], x ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+                                mma(o[j][(C::VB / 2) * c + 2 * k + x], a0, a1, a2, a3, pb[h2][j][0], pb[h2][j][1]);
+                        }
+                }
+            __syncwarp();
         }
 
         // ---- the warps' sums through the ring
         cp_wait<0>();
+        // after a wait that ran out: the copies in flight end, bounded, before the ring is anything else
+        for (; taken < sent; ++taken) {
+            mbar_drain(full + rd, phases >> rd & 1);
+            phases ^= 1u << rd;
+            rd = rd + 1 == C::STAGES ? 0 : rd + 1;
+        }
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -559,29 +634,29 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<DP, NT>::BLOCKS) kv8_attn_ke
                 for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
                 const int r = 8 * j + 2 * t + e;
                 if (g == 0) s_ml[warp * 8 * NT + r] = make_float2(m[j][e], sum);
-                // elements VB g .. of the row, in quads; quad c of a row lies at c ^ t: no bank twice
+                // elements of its unit of the row, in quads; quad c of a row lies at c ^ t: no bank twice
                 float4 *to = reinterpret_cast<float4 *>(k8_smem) + (warp * 8 * NT + r) * (DP / 4);
 #pragma unroll
                 for (int c = 0; c < C::VC; ++c)
 #pragma unroll
                     for (int k = 0; k < C::VB / 4; ++k) {
                         const int i = (C::VB / 2) * c + 2 * k;
-                        to[(2 * C::VB * c + C::VB / 4 * g + k) ^ t] =
+                        to[(2 * C::VB * c + C::VB / 4 * v_unit + k) ^ t] =
                             make_float4(o[j][i][e], o[j][i][2 + e], o[j][i + 1][e], o[j][i + 1][2 + e]);
                     }
             }
         __syncthreads();
         const bool whole_unit = i0 == 0 && i1 == seen.tiles;
         const int part = 2 * static_cast<int>(blockIdx.x) + (pos != lo);
-        for (int x = tid; x < rows * (DP / 4); x += K8_THREADS) {
+        for (int x = tid; x < rows * (DP / 4); x += C::THREADS) {
             const int r = x / (DP / 4), c = x % (DP / 4);
             float top = K8_NEG;
 #pragma unroll
-            for (int w = 0; w < K8_WARPS; ++w) top = fmaxf(top, s_ml[w * 8 * NT + r].x);
+            for (int w = 0; w < C::WARPS; ++w) top = fmaxf(top, s_ml[w * 8 * NT + r].x);
             float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             float total = 0.0f;
 #pragma unroll
-            for (int w = 0; w < K8_WARPS; ++w) {
+            for (int w = 0; w < C::WARPS; ++w) {
                 const float2 ml = s_ml[w * 8 * NT + r];
                 const float by = ex2(ml.x - top);
                 const float4 v = reinterpret_cast<const float4 *>(k8_smem)[(w * 8 * NT + r) * (DP / 4) + (c ^ ((r >> 1) & 3))];
@@ -600,38 +675,38 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<DP, NT>::BLOCKS) kv8_attn_ke
                 if (c == 0) p.part_ml[at] = make_float2(top, total);
             }
         }
-        // the unit begins here and ends in a later block's range
+        // the sequence begins here and ends in a later block's range
         if (tid == 0 && i0 == 0 && i1 < seen.tiles)
-            p.parts[blockIdx.x] = make_int4(b, unit, part, static_cast<int>((u0 + seen.tiles - 1) / range - blockIdx.x) + 1);
-        pos = u0 + i1;
+            p.parts[blockIdx.x] = make_int4(b, unit, part, static_cast<int>((seq_at + seen.tiles - 1) / range) -
+                                                               static_cast<int>(blockIdx.x) / per_seq + 1);
+        pos = seq_at + i1;
         if (pos >= hi) break;
-        __syncthreads();  // the ring is free again
-        if (++unit == per_seq) {
-            unit = 0;
-            seq_at += static_cast<long long>(per_seq) * seen.tiles;
-            do {
-                seen = Seen(p, __ldg(p.lens + ++b));  // one with rows follows, as pos < hi
-            } while (seen.tiles == 0);
-        }
+        fence_proxy_async_smem();
+        __syncthreads();  // the ring is free again, for copies too
+        seq_at += seen.tiles;
+        do {
+            seen = Seen(p, __ldg(p.lens + ++b));  // one with rows follows, as pos < hi
+        } while (seen.tiles == 0);
     }
 }
 
 // Joins the parts of the units that the ranges cut: block x those of the unit
 // that block x of the launch before left to its successors, which hold it as their
 // first.  combine_warps warps a row, each every so many parts.
-__global__ void __launch_bounds__(K8_THREADS) kv8_combine_kernel(const __grid_constant__ Kv8AttnParams p, int tile_pad)
+__global__ void __launch_bounds__(KC_THREADS) kv8_combine_kernel(const __grid_constant__ Kv8AttnParams p, int tile_pad)
 {
-    __shared__ float4 s_o[K8_WARPS][64];
+    __shared__ float4 s_o[KC_WARPS][64];
     pdl_launch_dependents();
     pdl_wait();
     const int4 u = p.parts[blockIdx.x];
+    const int per_seq = p.hkv * p.row_tiles;
     if (u.w == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = p.combine_warps;
-    const int r = blockIdx.y * (K8_WARPS / per) + warp / per, sub = warp % per;
+    const int r = blockIdx.y * (KC_WARPS / per) + warp / per, sub = warp % per;
     const int h = u.y / p.row_tiles, row0 = u.y % p.row_tiles * p.tile_rows;
     const bool there = r < min(p.tile_rows, p.rows - row0);
     auto at = [&](int i) {
-        return static_cast<long long>(i == 0 ? u.z : 2 * (static_cast<int>(blockIdx.x) + i)) * tile_pad + r;
+        return static_cast<long long>(i == 0 ? u.z : 2 * (static_cast<int>(blockIdx.x) + i * per_seq)) * tile_pad + r;
     };
     float top = K8_NEG, total = 0.0f;
     float4 sum[2] = {};
@@ -680,6 +755,23 @@ __global__ void __launch_bounds__(K8_THREADS) kv8_combine_kernel(const __grid_co
     if (lane == 0) store_lse(p, u.x, h, row0 + r, top, total);
 }
 
+// A cache's codes as [page][head][row][element], boxes of up to 32 rows of 128 elements.
+bool encode(CUtensorMap *map, const Kv8AttnParams &p, const void *base)
+{
+    const auto fn = map_encoder();
+    if (!fn) return false;
+    const cuuint32_t rows = 1u << p.c.page_shift;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.d), rows, static_cast<cuuint64_t>(p.hkv),
+                                static_cast<cuuint64_t>(p.c.n_pages)};
+    // a stride that nothing is reached by may be any
+    const auto stride = [](long long s, long long n) { return static_cast<cuuint64_t>(n > 1 ? s : 16); };
+    const cuuint64_t strides[3] = {stride(p.c.row_stride, rows), stride(p.c.head_stride, p.hkv), stride(p.c.page_stride, p.c.n_pages)};
+    const cuuint32_t box[4] = {p.d <= 64 ? 64u : 128u, rows < KV8_KEYS ? rows : KV8_KEYS, 1, 1}, ones[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box, ones,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, p.d <= 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int CODE, int DP, int NT>
 cudaError_t launch_nt(const Kv8AttnParams &p, cudaStream_t st)
 {
@@ -687,11 +779,13 @@ cudaError_t launch_nt(const Kv8AttnParams &p, cudaStream_t st)
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(kv8_attn_kernel<CODE, DP, NT>), C::SMEM, done);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kv8_attn_kernel<CODE, DP, NT>, dim3(static_cast<unsigned>(p.grid)), K8_THREADS, C::SMEM, st, p);
+    CUtensorMap k_map, v_map;
+    if (!encode(&k_map, p, p.c.k) || !encode(&v_map, p, p.c.v)) return cudaErrorInvalidValue;
+    e = launch_pdl(kv8_attn_kernel<CODE, DP, NT>, dim3(static_cast<unsigned>(p.grid)), C::THREADS, C::SMEM, st, p, k_map, v_map);
     if (e != cudaSuccess || !p.balanced) return e;
-    const int rows = K8_WARPS / p.combine_warps;  // of a block
+    const int rows = KC_WARPS / p.combine_warps;  // of a block
     return launch_pdl(kv8_combine_kernel, dim3(static_cast<unsigned>(p.grid), static_cast<unsigned>((p.tile_rows + rows - 1) / rows)),
-                      K8_THREADS, 0, st, p, 8 * NT);
+                      KC_THREADS, 0, st, p, 8 * NT);
 }
 
 template <int CODE, int DP>
@@ -712,9 +806,6 @@ cudaError_t launch_code(const Kv8AttnParams &p, cudaStream_t st)
 }
 
 }  // namespace
-
-int kv8_tile_rows(int d) { return d <= 128 ? 32 : 16; }
-int kv8_blocks(int d, int nt) { return d > 128 || (d > 64 && nt > 2) ? 1 : 2; }
 
 cudaError_t launch_kv8_attn(const Kv8AttnParams &p, qgemv_code_type code, cudaStream_t st)
 {

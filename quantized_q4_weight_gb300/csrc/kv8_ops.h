@@ -68,12 +68,13 @@ struct Kv8AttnParams {
     float *lse;
     unsigned *status;
 };
-constexpr int KV8_KEYS = 16;         // keys of a tile
-constexpr int KV8_SPLIT_MIN = 16;    // tiles of a range at least
-// Rows that a tile of row_tiles holds at most for a head_dim, and blocks a
-// multiprocessor for tiles of nt * 8 rows.
-int kv8_tile_rows(int d);
-int kv8_blocks(int d, int nt);
+constexpr int KV8_KEYS = 32;         // keys of a tile
+constexpr int KV8_SPLIT_MIN = 12;    // tiles of a range at least
+// Rows of a tile at most, and, for tiles of 8 nt rows, blocks a multiprocessor
+// and warps a block.
+constexpr int kv8_tile_rows(int d) { return d <= 128 ? 32 : 16; }
+constexpr int kv8_blocks(int d, int nt) { return d > 128 || (d > 64 && nt > 2) ? 1 : 2; }
+constexpr int kv8_warps(int d, int nt) { return (d <= 64 && nt <= 2) || (d > 64 && d <= 128 && nt > 2) ? 8 : 6; }
 cudaError_t launch_kv8_attn(const Kv8AttnParams &p, qgemv_code_type code, cudaStream_t st);
 
 // ------------------------------------------------------------------- beams
@@ -87,14 +88,13 @@ struct BeamParams {
     long long *token;
     int32_t *parent;
     int beams, n_best, row0;      // row0: of the launch's first group (parents are rows of all groups)
-    int slices, slice;            // of a row; elements of one
+    int slices, slice;            // of a row; elements of one, a multiple of 2048
     unsigned *cnt;                // [groups] arrivals, zero between launches
     float2 *part_ml;              // [rows][slices] maximum, sum of exponentials
-    uint2 *part;                  // [rows][slices][n_best] value's bits, token; best first
+    unsigned long long *part;     // [rows][slices][n_best] keys, best first; 0: none
 };
 constexpr int BEAM_GROUPS = 4080;  // groups of a launch: their arrivals fit the counter area before its last 64 bytes
-constexpr int BEAM_SLICE_MAX = 8192;
-int beam_slice(long long rows, long long vocab);  // elements of a slice
+int beam_slices(long long rows, long long vocab);  // slices of a row
 cudaError_t launch_beam(const BeamParams &p, qgemv_dtype type, int groups, cudaStream_t st);
 
 // ------------------------------------------------------------------- pages
