@@ -108,7 +108,7 @@ inline Span table_span(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c)
 // Launch shape and workspace of the attention.
 struct Kv8Plan {
     int group, rows, row_tiles, tile_rows, tile_pad;
-    int balanced, grid, combine_warps;
+    int balanced, grid, combine_lanes, by_unit;
     long long ml_at, parts_at, ws_bytes;
 };
 
@@ -127,10 +127,11 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     // Balanced ranges cost a walk over all lengths and a second launch.  Units of up
     // to four tiles a warp are a block each instead, and so are those of very many
     // sequences, which spread over the multiprocessors well enough by themselves.
-    a.balanced = tiles > 24 && b->n_seqs <= 1024;
+    a.balanced = tiles > 24 && b->n_seqs <= 1024 && b->n_seqs * tiles < (1ll << 30);
     a.ml_at = a.parts_at = kCounterArea;
     a.ws_bytes = kCounterArea;
-    a.combine_warps = 1;
+    a.combine_lanes = 1;
+    a.by_unit = 0;
     if (!a.balanced) {
         if (units > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
         a.grid = static_cast<int>(units);
@@ -141,10 +142,10 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     const long long ranges = std::min(std::max(1ll, blocks / per_seq), ceil_div(b->n_seqs * tiles, KV8_SPLIT_MIN));
     if (ranges * per_seq > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
     a.grid = static_cast<int>(ranges * per_seq);
-    // parts of a sequence: about ranges / n_seqs; few are joined by a warp for each row, many by all of a block
+    // parts of a sequence: about ranges / n_seqs, and of a long one up to ranges.  A group takes four at once.
     const long long parts = ranges / std::min<long long>(b->n_seqs, ranges);
-    while (a.combine_warps < 8 && 2 * a.combine_warps <= parts) a.combine_warps *= 2;
-    a.parts_at = kCounterArea;
+    while (a.combine_lanes < 32 && 2 * a.combine_lanes < parts) a.combine_lanes *= 2;
+    a.by_unit = units <= a.grid;
     a.ml_at = a.parts_at + 16ll * a.grid;
     const long long o_at = a.ml_at + 16ll * a.grid * a.tile_pad;
     a.ws_bytes = o_at + 8ll * a.grid * a.tile_pad * c->head_dim;
@@ -420,7 +421,8 @@ qgemv_status qgemv_attn_kv8(const void *q, qgemv_dtype q_type, int64_t q_token_s
     p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
     p.balanced = a.balanced;
     p.grid = a.grid;
-    p.combine_warps = a.combine_warps;
+    p.combine_lanes = a.combine_lanes;
+    p.parts_by_unit = a.by_unit;
     uint8_t *at = static_cast<uint8_t *>(ws);
     p.parts = reinterpret_cast<int4 *>(at + a.parts_at);
     p.part_ml = reinterpret_cast<float2 *>(at + a.ml_at);

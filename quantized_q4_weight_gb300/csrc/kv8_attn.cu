@@ -38,7 +38,7 @@
 namespace qg {
 namespace {
 
-constexpr int KC_WARPS = 8, KC_THREADS = 32 * KC_WARPS;  // of a block of the combining launch
+constexpr int KC_THREADS = 256;    // of a block of the combining launch
 constexpr float K8_NEG = -1e30f;   // below every finite score; differences of it stay finite
 constexpr float K8_LIFT = 10.0f;   // a new reference lies so far below the largest score
 constexpr float K8_SLACK = 14.0f;  // weights reach 2^14 before it moves (f16 ends at 2^16)
@@ -94,6 +94,34 @@ __device__ __forceinline__ float rcp(float x)
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// Two fp32 operations at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tadd.rn.f32x2 rd, ra, rb;\n\t"
+        "mov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmul.rn.f32x2 rd, ra, rb;\n\t"
+        "mov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 __device__ __forceinline__ void mma(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0, unsigned b1)
 {
@@ -256,27 +284,25 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
     const int per_seq = p.hkv * p.row_tiles, unit = blockIdx.x % per_seq;
     const int h = unit / p.row_tiles, row0 = unit % p.row_tiles * p.tile_rows;
     const int rows = min(p.tile_rows, p.rows - row0);
-    long long lo, hi, range = 0, seq_at;
-    int b;
+    int lo, hi, range = 0, seq_at, b;  // in tiles: all of them fit 31 bits
     if (p.balanced) {
         // every warp adds all sequences' tiles up, each lane a run of them
         const int run = (p.n_seqs + 31) / 32;
-        long long mine = 0;
+        int mine = 0;
         for (int i = lane * run; i < min(p.n_seqs, (lane + 1) * run); ++i) {
             const int n = __ldg(p.lens + i);
             mine += Seen(p, n).tiles;
             if ((n < 0 || n > p.max_len) && blockIdx.x == 0 && warp == 0) atomicCAS(p.status, 0u, ST_BAD_ID);
         }
-        long long upto = mine;
+        int upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
             if (lane >= o) upto += v;
         }
-        const long long total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-        const int ranges = p.grid / per_seq;
-        range = max(static_cast<long long>(KV8_SPLIT_MIN), (total + ranges - 1) / ranges);
-        lo = blockIdx.x / per_seq * range, hi = min(total, lo + range);
+        const int total = __shfl_sync(0xFFFFFFFFu, upto, 31), ranges = p.grid / per_seq;
+        range = max(KV8_SPLIT_MIN, (total + ranges - 1) / ranges);
+        lo = static_cast<int>(blockIdx.x) / per_seq * range, hi = min(total, lo + range);
         // the first lane whose run ends behind lo walks its run
         const unsigned behind = __ballot_sync(0xFFFFFFFFu, upto > lo);
         const int owner = behind ? __ffs(behind) - 1 : 0;
@@ -292,9 +318,12 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
         b = __shfl_sync(0xFFFFFFFFu, at, owner);
         seq_at = __shfl_sync(0xFFFFFFFFu, seq_at, owner);
         for (int i = blockIdx.x; i < p.n_seqs; i += p.grid)
-            if (Seen(p, __ldg(p.lens + i)).n == 0)
+            if (Seen(p, __ldg(p.lens + i)).n == 0) {
                 for (int k = 0; k < p.hkv; ++k) store_none(p, i, k, 0, p.rows);
-        if (tid == 0) p.parts[blockIdx.x] = make_int4(0, 0, 0, 0);
+                if (p.parts_by_unit)
+                    for (int k = tid; k < per_seq; k += C::THREADS) p.parts[i * per_seq + k] = make_int4(0, 0, 0, 0);
+            }
+        if (!p.parts_by_unit && tid == 0) p.parts[blockIdx.x] = make_int4(0, 0, 0, 0);
         if (lo >= total) return;
     } else {
         b = blockIdx.x / per_seq;
@@ -309,7 +338,7 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
     }
 
     Seen seen(p, __ldg(p.lens + b));
-    long long pos = lo;
+    int pos = lo;
     // where in a box the thread's bytes of K lie (of 64 elements each) and those of V (of two rows)
     const int pg = box_row<DP>(g);
     const uint32_t k_off0 = box_off<DP>(pg, t), k_off1 = box_off<DP>(pg, 4 + t);
@@ -323,7 +352,7 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
     unsigned phases = 0, absent = 0;
     bool ok = true;
     while (pos < hi) {
-        const int i0 = static_cast<int>(pos - seq_at), i1 = static_cast<int>(min(static_cast<long long>(seen.tiles), hi - seq_at));
+        const int i0 = pos - seq_at, i1 = min(seen.tiles, hi - seq_at);
 
         // ---- the warp's tiles i0 + warp, + WARPS, ... on their way
         const int32_t *table = p.pages + b * p.pages_stride;
@@ -370,18 +399,28 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
             }
             cp_commit();
         };
+        // the unit's queries on their way too
+        constexpr int QR = (8 * NT + C::WARPS - 1) / C::WARPS;  // rows of a warp
+        uint4 q_raw[QR];
+#pragma unroll
+        for (int k = 0; k < QR; ++k) {
+            const int r = warp + k * C::WARPS, row = row0 + r;
+            q_raw[k] = make_uint4(0, 0, 0, 0);
+            if (r < rows && 8 * lane < p.d) {
+                const long long token = static_cast<long long>(b) * p.n_q + row / p.group;
+                q_raw[k] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + token * p.q_token_stride +
+                                                                 (h * p.group + row % p.group) * p.q_head_stride + 8 * lane));
+            }
+        }
 #pragma unroll 1
         for (int s = 0; s < C::STAGES - 1; ++s) issue();
 
-        // ---- the unit's queries, in f16; bf16 rows divided by a power of two
-        for (int r = warp; r < 8 * NT; r += C::WARPS) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            const int row = row0 + r;
-            if (r < rows && 8 * lane < p.d) {
-                const long long token = static_cast<long long>(b) * p.n_q + row / p.group;
-                w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + token * p.q_token_stride +
-                                                          (h * p.group + row % p.group) * p.q_head_stride + 8 * lane));
-            }
+        // ---- queries in f16; bf16 rows divided by a power of two
+#pragma unroll
+        for (int k = 0; k < QR; ++k) {
+            const int r = warp + k * C::WARPS;
+            if (r >= 8 * NT) break;
+            uint4 w = q_raw[k];
             float qs = p.scale_log2;
             if (p.q_bf16) {
                 unsigned u[4] = {w.x, w.y, w.z, w.w};
@@ -406,11 +445,11 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
         }
         __syncthreads();
 
+        const uint32_t q_at = s_base + C::OFF_Q + g * DP * 2 + 32 * t, q_x = (g & 1) << 4;
         auto load_q = [&](int j, int c, unsigned (&f)[8]) {  // 16 elements 64 c + 16 t .. of row 8 j + g
-            const uint32_t at = s_base + C::OFF_Q + (8 * j + g) * DP * 2;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const uint4 v = lds128(at + (((8 * c + 2 * t + x) ^ (g & 1)) << 4));
+                const uint4 v = lds128(q_at + (16 * x ^ q_x) + 8 * j * DP * 2 + 128 * c);
                 f[4 * x] = v.x, f[4 * x + 1] = v.y, f[4 * x + 2] = v.z, f[4 * x + 3] = v.w;
             }
         };
@@ -436,20 +475,13 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                 for (int e = 0; e < 4; ++e) o[j][i][e] = 0.0f;
         }
 
-        // The references that a tile with sums s (-infinity: not seen) asks for.
-        auto raise = [&](const float (&s)[2][NT][4], const float (&ks)[2], const float (&lv)[2]) {
+        // The references that a tile with exponents s (-infinity: not seen) asks for.
+        auto raise = [&](const float (&s)[2][NT][4]) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float v = s[x][j][2 * k + e];
-                            mx = fmaxf(mx, v == -INFINITY ? v : fmaf(v, ks[x] * qs[j][e], lv[x]));
-                        }
+                    float mx = fmaxf(fmaxf(s[0][j][e], s[0][j][2 + e]), fmaxf(s[1][j][e], s[1][j][2 + e]));
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
                     if (mx - m[j][e] > K8_SLACK) {
@@ -523,6 +555,18 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                 vs[x] = vs[x] < 8.673617e-19f ? 8.673617e-19f : vs[x];  // 2^-60
                 lv[x] = lg2(vs[x]), inv[x] = rcp(vs[x]);
             }
+            // exponents in place of the sums
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const float2 f = mul2(make_float2(ks[x], ks[x]), make_float2(qs[j][0], qs[j][1]));
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float2 a = fma2(make_float2(s[x][j][2 * k], s[x][j][2 * k + 1]), f, make_float2(lv[x], lv[x]));
+                        s[x][j][2 * k] = a.x, s[x][j][2 * k + 1] = a.y;
+                    }
+                }
             bool up = true;
             if (whole) {
                 float top = -INFINITY;
@@ -530,11 +574,7 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float f = ks[x] * qs[j][e], at = lv[x] - m[j][e];
-                            top = fmaxf(top, fmaxf(fmaf(s[x][j][e], f, at), fmaf(s[x][j][2 + e], f, at)));
-                        }
+                        top = fmaxf(top, fmaxf(fmaxf(s[0][j][e], s[0][j][2 + e]), fmaxf(s[1][j][e], s[1][j][2 + e])) - m[j][e]);
                 up = __any_sync(0xFFFFFFFFu, top > K8_SLACK);
             } else {
 #pragma unroll
@@ -553,28 +593,23 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                             }
                     }
             }
-            if (up) raise(s, ks, lv);
+            if (up) raise(s);
             unsigned pb[2][NT][2];
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float f = ks[x] * qs[j][e], at = lv[x] - m[j][e];
-                        float a = fmaf(s[x][j][e], f, at), b = fmaf(s[x][j][2 + e], f, at);
-                        if (!whole) {
-                            a = s[x][j][e] == -INFINITY ? -INFINITY : a;
-                            b = s[x][j][2 + e] == -INFINITY ? -INFINITY : b;
-                        }
-                        s[x][j][e] = a = ex2(a);
-                        s[x][j][2 + e] = b = ex2(b);
-                        // a row that sees none of the half takes nothing from its scale either
-                        if (whole || a + b != 0.0f) l[j][e] = fmaf(a + b, inv[x], l[j][e]);
-                    }
+                    const float2 down = make_float2(-m[j][0], -m[j][1]);
+                    float2 a = add2(make_float2(s[x][j][0], s[x][j][1]), down), b = add2(make_float2(s[x][j][2], s[x][j][3]), down);
+                    a = make_float2(ex2(a.x), ex2(a.y)), b = make_float2(ex2(b.x), ex2(b.y));
+                    const float2 sum = add2(a, b);
+                    const float2 add = mul2(sum, make_float2(inv[x], inv[x]));
+                    // a row that sees none of the half takes nothing from its scale either
+                    l[j][0] += whole || sum.x != 0.0f ? add.x : 0.0f;
+                    l[j][1] += whole || sum.y != 0.0f ? add.y : 0.0f;
                     // The weights are operands in f16: off by half a unit of it.  l keeps them whole.
-                    pb[x][j][0] = movm(pack(s[x][j][0], s[x][j][1]));
-                    pb[x][j][1] = movm(pack(s[x][j][2], s[x][j][3]));
+                    pb[x][j][0] = movm(pack(a.x, a.y));
+                    pb[x][j][1] = movm(pack(b.x, b.y));
                 }
 
             // ---- weighted sums of v
@@ -675,10 +710,11 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                 if (c == 0) p.part_ml[at] = make_float2(top, total);
             }
         }
-        // the sequence begins here and ends in a later block's range
-        if (tid == 0 && i0 == 0 && i1 < seen.tiles)
-            p.parts[blockIdx.x] = make_int4(b, unit, part, static_cast<int>((seq_at + seen.tiles - 1) / range) -
-                                                               static_cast<int>(blockIdx.x) / per_seq + 1);
+        // the sequence begins here: its parts, if it ends in a later block's range
+        if (tid == 0 && p.balanced && i0 == 0 && (p.parts_by_unit || i1 < seen.tiles)) {
+            const int n = (seq_at + seen.tiles - 1) / range - static_cast<int>(blockIdx.x) / per_seq + 1;
+            p.parts[p.parts_by_unit ? b * per_seq + unit : blockIdx.x] = make_int4(b, unit, part, i1 < seen.tiles ? n : 0);
+        }
         pos = seq_at + i1;
         if (pos >= hi) break;
         fence_proxy_async_smem();
@@ -690,69 +726,70 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
     }
 }
 
-// Joins the parts of the units that the ranges cut: block x those of the unit
-// that block x of the launch before left to its successors, which hold it as their
-// first.  combine_warps warps a row, each every so many parts.
+// Joins the parts of the units that the ranges cut: block x those of unit x, or, where
+// there are more units than blocks, of the one that block x of the launch before
+// left to its successors (which hold it as their first).  Eight threads take 32
+// elements of a row from every so many parts; `lanes` such groups, a power of two, share
+// a row's 32 elements, so that even 150 parts are a few loads one behind the other.
 __global__ void __launch_bounds__(KC_THREADS) kv8_combine_kernel(const __grid_constant__ Kv8AttnParams p, int tile_pad)
 {
-    __shared__ float4 s_o[KC_WARPS][64];
+    __shared__ float4 s_o[KC_THREADS];
+    __shared__ float2 s_ml[KC_THREADS];
+    const int lanes = p.combine_lanes, group = threadIdx.x >> 3, c = threadIdx.x & 7;
+    const int chunks = (p.d + 31) / 32, item = blockIdx.y * (KC_THREADS / 8 / lanes) + group / lanes;
+    const int r = item / chunks, at4 = item % chunks * 32 + 4 * c;  // row, element
     pdl_launch_dependents();
     pdl_wait();
     const int4 u = p.parts[blockIdx.x];
-    const int per_seq = p.hkv * p.row_tiles;
     if (u.w == 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = p.combine_warps;
-    const int r = blockIdx.y * (KC_WARPS / per) + warp / per, sub = warp % per;
+    const int per_seq = p.hkv * p.row_tiles;
     const int h = u.y / p.row_tiles, row0 = u.y % p.row_tiles * p.tile_rows;
-    const bool there = r < min(p.tile_rows, p.rows - row0);
-    auto at = [&](int i) {
-        return static_cast<long long>(i == 0 ? u.z : 2 * (static_cast<int>(blockIdx.x) + i * per_seq)) * tile_pad + r;
-    };
+    const bool there = r < min(p.tile_rows, p.rows - row0) && at4 < p.d;
     float top = K8_NEG, total = 0.0f;
-    float4 sum[2] = {};
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](float m, float l, const float4 &v) {
+        const float mn = fmaxf(top, m), old = ex2(top - mn), by = ex2(m - mn);
+        top = mn;
+        total = fmaf(l, by, total * old);
+        sum.x = fmaf(v.x, by, sum.x * old), sum.y = fmaf(v.y, by, sum.y * old);
+        sum.z = fmaf(v.z, by, sum.z * old), sum.w = fmaf(v.w, by, sum.w * old);
+    };
     if (there) {
-        for (int i = lane; i < u.w; i += 32) top = fmaxf(top, p.part_ml[at(i)].x);
+        constexpr int U = 4;
+        for (int i0 = group % lanes; i0 < u.w; i0 += U * lanes) {
+            float2 ml[U];
+            float4 v[U];
 #pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        for (int i = lane; i < u.w; i += 32) {
-            const float2 ml = p.part_ml[at(i)];
-            total = fmaf(ml.y, ex2(ml.x - top), total);
-        }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
-        const int quads = p.d / 4;
-#pragma unroll 4
-        for (int i = sub; i < u.w; i += per) {
-            const long long a = at(i);
-            const float by = ex2(p.part_ml[a].x - top);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (lane + 32 * k < quads) {
-                    const float4 v = *reinterpret_cast<const float4 *>(p.part_o + a * p.d + 4 * (lane + 32 * k));
-                    sum[k].x = fmaf(v.x, by, sum[k].x), sum[k].y = fmaf(v.y, by, sum[k].y);
-                    sum[k].z = fmaf(v.z, by, sum[k].z), sum[k].w = fmaf(v.w, by, sum[k].w);
+            for (int k = 0; k < U; ++k) {
+                const int i = i0 + k * lanes;
+                if (i < u.w) {
+                    const long long a = static_cast<long long>(i == 0 ? u.z : 2 * ((u.z >> 1) + i * per_seq)) * tile_pad + r;
+                    ml[k] = p.part_ml[a];
+                    v[k] = *reinterpret_cast<const float4 *>(p.part_o + a * p.d + at4);
                 }
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (i0 + k * lanes < u.w) add(ml[k].x, ml[k].y, v[k]);
         }
     }
-    if (per > 1) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) s_o[warp][lane + 32 * k] = sum[k];
-        __syncthreads();
-        if (sub == 0)
-            for (int w = 1; w < per; ++w)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float4 v = s_o[warp + w][lane + 32 * k];
-                    sum[k].x += v.x, sum[k].y += v.y, sum[k].z += v.z, sum[k].w += v.w;
-                }
+    if (lanes > 1) {
+        s_o[threadIdx.x] = sum;
+        s_ml[threadIdx.x] = make_float2(top, total);
+        for (int o = lanes >> 1; o; o >>= 1) {
+            __syncthreads();
+            if (group % lanes < o) {
+                const float2 ml = s_ml[threadIdx.x + 8 * o];
+                add(ml.x, ml.y, s_o[threadIdx.x + 8 * o]);
+                s_o[threadIdx.x] = sum;
+                s_ml[threadIdx.x] = make_float2(top, total);
+            }
+        }
     }
-    if (!there || sub) return;
+    if (!there || group % lanes) return;
     const float by = total == 0.0f ? 0.0f : 1.0f / total;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        if (4 * (lane + 32 * k) < p.d)
-            store_o(p, u.x, h, row0 + r, lane + 32 * k, make_float4(sum[k].x * by, sum[k].y * by, sum[k].z * by, sum[k].w * by));
-    if (lane == 0) store_lse(p, u.x, h, row0 + r, top, total);
+    store_o(p, u.x, h, row0 + r, at4 / 4, make_float4(sum.x * by, sum.y * by, sum.z * by, sum.w * by));
+    if (at4 == 0) store_lse(p, u.x, h, row0 + r, top, total);
 }
 
 // A cache's codes as [page][head][row][element], boxes of up to 32 rows of 128 elements.
@@ -783,8 +820,9 @@ cudaError_t launch_nt(const Kv8AttnParams &p, cudaStream_t st)
     if (!encode(&k_map, p, p.c.k) || !encode(&v_map, p, p.c.v)) return cudaErrorInvalidValue;
     e = launch_pdl(kv8_attn_kernel<CODE, DP, NT>, dim3(static_cast<unsigned>(p.grid)), C::THREADS, C::SMEM, st, p, k_map, v_map);
     if (e != cudaSuccess || !p.balanced) return e;
-    const int rows = KC_WARPS / p.combine_warps;  // of a block
-    return launch_pdl(kv8_combine_kernel, dim3(static_cast<unsigned>(p.grid), static_cast<unsigned>((p.tile_rows + rows - 1) / rows)),
+    const int items = KC_THREADS / 8 / p.combine_lanes, all = p.tile_rows * ((p.d + 31) / 32);  // of a block, of a unit
+    const int blocks = p.parts_by_unit ? p.n_seqs * p.hkv * p.row_tiles : p.grid;
+    return launch_pdl(kv8_combine_kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>((all + items - 1) / items)),
                       KC_THREADS, 0, st, p, 8 * NT);
 }
 

@@ -58,10 +58,11 @@ struct Kv8AttnParams {
     int rows, row_tiles, tile_rows;  // of a sequence and cache head: n_q * group, in row_tiles of tile_rows
     float scale_log2;
     int balanced, grid;              // ranges of all tiles over `grid` blocks, or a block for each unit
-    int4 *parts;                     // [grid] the unit that a block leaves to its successors (kv8_attn.cu)
+    int parts_by_unit;               // there are no more units than blocks
+    int4 *parts;                     // of each unit, or block: sequence, unit, first part, parts (0: none)
     float *part_o;                   // [2 grid][tile rows, padded][d]
     float2 *part_ml;                 // [2 grid][tile rows, padded]
-    int combine_warps;               // warps for a row of the combining launch
+    int combine_lanes;               // groups that share a row's elements in the combining launch: 1 .. 32
     void *o;
     int o_type;                      // qgemv_dtype
     long long o_token_stride, o_head_stride;
