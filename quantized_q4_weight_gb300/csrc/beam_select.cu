@@ -9,16 +9,17 @@
 // which block that is.
 //
 // A key holds a logit's bits in an order that integers have, and the token upside
-// down, so that a larger key is a larger logit or a lower token.  Each warp keeps the n
-// best keys it has met in its lanes, in order.  A value is compared with the n-th of
-// them (or a better n-th that another warp has shown), which few pass: those are
-// collected in shared memory and inserted one by one, a ballot and a shuffle each.  The
-// first values of a warp go by the n-th largest of the lanes' largest (a bitonic network
-// of shuffles), a bound that lets few more than n through.
+// down, so that a larger key is a larger logit or a lower token.  The block keeps the n
+// best keys it has met in shared memory, in order, and compares every value with the
+// n-th of them, which few pass; those are appended, and from time to time ranked together
+// with the best by counting.  The first values go by the n-th largest of the threads'
+// largest (a bitonic network of shuffles for each warp, then a search in the others' lists),
+// a bound that lets few more than n through.  More equal or rising values than the
+// list holds are taken n at a time, each by a maximum over the block.
 //
 // What bounds it: memory for many rows (logits read once; a maximum, a product, an
-// exponential and a sum for each); the chain launch, logits, insertions, arrival, join for
-// one search, so few rows have small slices.
+// exponential and a sum for each); the chain launch, logits, ranks, arrival, join for one
+// search, so few rows have small slices.
 #include "kv8_ops.h"
 #include "qgemv_internal.cuh"
 
@@ -27,7 +28,9 @@ namespace {
 
 constexpr int BM_THREADS = 256, BM_WARPS = BM_THREADS / 32, BM_BLOCKS = 4;
 constexpr int BM_CHUNKS = 4;   // 16-byte chunks of a thread's batch; as many are on their way
-constexpr int BM_LIST = 64;    // keys of a warp that wait for their insertion
+constexpr int BM_LIST = 512;   // keys of a block that are ranked at once
+constexpr int BM_FULL = 16;    // appended keys that are worth a ranking: it raises the bound
+constexpr int BM_WAIT = 64;    // keys of a warp in the join
 constexpr int BM_BEAMS = 16;
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -38,6 +41,33 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// Two fp32 operations at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tadd.rn.f32x2 rd, ra, rb;\n\t"
+        "mov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+// log(x) of a sum x > 0: the exponent's part in 64 bits, the rest, a logarithm
+// below 0.35, in 32 (off by 2^-25).
+__device__ __forceinline__ double log_of(float x)
+{
+    const int bits = __float_as_int(x), k = (bits - 0x3F3504F3) >> 23;  // x / 2^k in 0.707 .. 1.414
+    const float f = __int_as_float(bits - (k << 23));
+    return k * 0.6931471805599453 + static_cast<double>(logf(f));
 }
 // A float's bits in an order that unsigned comparison respects; -0 as +0.
 __device__ __forceinline__ unsigned ordered(float f)
@@ -56,7 +86,8 @@ __device__ __forceinline__ Key key_of(float v, unsigned token)
 __device__ __forceinline__ float value_of(Key k) { return from_ordered(static_cast<unsigned>(k >> 32)); }
 __device__ __forceinline__ unsigned token_of(Key k) { return 0xFFFFFFFFu - static_cast<unsigned>(k); }
 
-// Elements of a 16-byte chunk as floats, and the largest of them (NaN passed over).
+// Elements of a 16-byte chunk as floats (`at` for a constant place, `any` for a
+// variable one), and the largest of them (NaN passed over).
 template <typename T>
 struct Chunk16;
 template <>
@@ -66,6 +97,7 @@ struct Chunk16<float> {
     {
         return __uint_as_float(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w);
     }
+    static __device__ __forceinline__ float any(const uint4 &w, int i) { return at(w, i); }
     static __device__ __forceinline__ float largest(const uint4 &w)
     {
         return fmaxf(fmaxf(at(w, 0), at(w, 1)), fmaxf(at(w, 2), at(w, 3)));
@@ -82,6 +114,11 @@ struct Chunk16<__half> {
     static __device__ __forceinline__ float at(const uint4 &w, int i)
     {
         return i & 1 ? __high2float(pair(w, i >> 1)) : __low2float(pair(w, i >> 1));
+    }
+    static __device__ __forceinline__ float any(const uint4 &w, int i)
+    {
+        const __half2 p = pair(w, i >> 1);
+        return i & 1 ? __high2float(p) : __low2float(p);
     }
     static __device__ __forceinline__ float largest(const uint4 &w)
     {
@@ -102,6 +139,10 @@ struct Chunk16<__nv_bfloat16> {
     {
         return __uint_as_float(i & 1 ? word(w, i >> 1) & 0xFFFF0000u : word(w, i >> 1) << 16);
     }
+    static __device__ __forceinline__ float any(const uint4 &w, int i)
+    {
+        return __uint_as_float(word(w, i >> 1) << (i & 1 ? 0 : 16) & 0xFFFF0000u);
+    }
     static __device__ __forceinline__ float largest(const uint4 &w)
     {
         const __nv_bfloat162 m = __hmax2(__hmax2(pair(w, 0), pair(w, 1)), __hmax2(pair(w, 2), pair(w, 3)));
@@ -109,9 +150,9 @@ struct Chunk16<__nv_bfloat16> {
     }
 };
 
-// The n-th largest of a warp's 32 values.
+// A warp's 32 values falling over its lanes.
 template <typename V>
-__device__ __forceinline__ V nth_of_warp(V v, int n)
+__device__ __forceinline__ void sort_warp(V &v)
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -122,22 +163,71 @@ __device__ __forceinline__ V nth_of_warp(V v, int n)
             const bool larger = ((lane & k) == 0) == ((lane & d) == 0);  // k = 32: falling over the warp
             v = (o > v) == larger ? o : v;
         }
-    return __shfl_sync(0xFFFFFFFFu, v, n - 1);
 }
 
-// The warp's best keys, falling over the lanes (0: none).
-struct Best {
-    Key mine = 0;
-
-    __device__ __forceinline__ void insert(Key k)  // the same for all lanes, none of the list's
-    {
-        const int at = __popc(__ballot_sync(0xFFFFFFFFu, mine > k));
-        const Key up = __shfl_up_sync(0xFFFFFFFFu, mine, 1);
-        const int lane = threadIdx.x & 31;
-        mine = lane < at ? mine : lane == at ? k : up;
+// The n-th largest of the block's 256 values, to all threads.
+__device__ __forceinline__ float nth_of_block(float v, int n, float (*s)[32], float *s_bound)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    sort_warp(v);
+    s[warp][lane] = v;
+    __syncthreads();
+    // a value's rank: its place in its own list, and in each other list the values that come before it
+    int rank = lane;
+#pragma unroll
+    for (int w = 0; w < BM_WARPS; ++w) {
+        int at = 0;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            const float o = s[w][at + d - 1];
+            if (o > v || (o == v && w < warp)) at += d;
+        }
+        const float o = s[w][at];
+        rank += w == warp ? 0 : at + (o > v || (o == v && w < warp));
     }
-    __device__ __forceinline__ Key nth(int n) const { return __shfl_sync(0xFFFFFFFFu, mine, n - 1); }
-};
+    if (rank == n - 1) *s_bound = v;
+    __syncthreads();
+    return *s_bound;
+}
+
+// The best n of list[0 .. total), in order, to its front; THREADS threads, `t` of them this
+// one, `sync` their barrier, PER keys each.
+template <int THREADS, int PER, typename Sync>
+__device__ __forceinline__ void rank_keys(Key *list, int total, int n, int t, Sync sync)
+{
+    sync();
+    Key k[PER];
+    int rank[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) k[u] = t + u * THREADS < total ? list[t + u * THREADS] : 0, rank[u] = 0;
+    if (t < total)
+        for (int i = 0; i < total; ++i) {
+            const Key o = list[i];
+#pragma unroll
+            for (int u = 0; u < PER; ++u) rank[u] += o > k[u];
+        }
+    sync();
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+        if (t + u * THREADS < total && rank[u] < n) list[rank[u]] = k[u];
+    sync();
+}
+
+// The largest key of the block, to all threads.
+__device__ __forceinline__ Key block_largest(Key key, Key *s)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const Key o = __shfl_xor_sync(0xFFFFFFFFu, key, d);
+        key = o > key ? o : key;
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = key;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < BM_WARPS; ++w) key = s[w] > key ? s[w] : key;
+    return key;
+}
 
 // How many of a falling list of `n` are above k.
 template <typename K>
@@ -151,13 +241,19 @@ __device__ __forceinline__ int above(const K *list, int n, K k)
 }
 
 struct BeamShared {
-    Key lists[BM_BEAMS][32];        // of the warps, then of the join's rows
-    Key wait[BM_WARPS][BM_LIST];
-    Key shown;                      // the best n-th key of a warp
+    union {
+        Key list[BM_LIST];              // the best of the block so far, then those appended
+        Key wait[BM_WARPS][BM_WAIT];    // the same of a row's warp in the join
+    };
+    Key lists[BM_BEAMS][32];            // the join's rows
+    float sorted[BM_WARPS][32];
+    Key best[BM_WARPS];
+    float bound, red[BM_WARPS];
+    int total;                          // keys of the list
+    int last;
     float m[BM_BEAMS], sum[BM_BEAMS];
     int count[BM_BEAMS];
     double lse[BM_BEAMS];
-    int last;
 };
 
 // The join of group gi of the launch, by the block that arrived last.
@@ -167,7 +263,7 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
     const long long r0 = static_cast<long long>(gi) * p.beams;
     const int per = p.slices * p.n_best;
     constexpr int ROWS = BM_BEAMS / BM_WARPS;  // of a warp
-    Best best[ROWS];
+    Key best[ROWS];  // lane k: the row's k-th
     // each row's n best keys, maximum and sum
 #pragma unroll
     for (int q = 0; q < ROWS; ++q) {
@@ -178,29 +274,38 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
         float m = -INFINITY, sum = 0.0f;
         float2 mine = lane < p.slices ? ml[lane] : make_float2(-INFINITY, 0.0f);
         if (p.slices == 1) {
-            best[q].mine = lane < p.n_best ? part[lane] : 0;
+            best[q] = lane < p.n_best ? part[lane] : 0;
         } else {
-            Key kth = 0;
-            for (int i0 = 0; i0 < per; i0 += 128) {
-                Key k[4];
+            // the slices' first keys bound the n-th from below, where there are n
+            unsigned head = lane < p.slices ? static_cast<unsigned>(part[lane * p.n_best] >> 32) : 0;
+            sort_warp(head);
+            head = __shfl_sync(0xFFFFFFFFu, head, p.n_best - 1);
+            Key kth = head ? (static_cast<Key>(head) << 32) - 1 : 0;
+            Key *list = s.wait[warp];
+            int total = 0;
+            const auto rank = [&]() {
+                rank_keys<32, BM_WAIT / 32>(list, total, p.n_best, lane, [] { __syncwarp(); });
+                total = min(total, p.n_best);
+                if (total == p.n_best) kth = list[p.n_best - 1];
+            };
+            constexpr int U = 8;
+            for (int i0 = 0; i0 < per; i0 += 32 * U) {
+                Key k[U];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) k[u] = i0 + 32 * u + lane < per ? part[i0 + 32 * u + lane] : 0;
-                if (i0 == 0) {
-                    const Key a = k[0] > k[1] ? k[0] : k[1], b = k[2] > k[3] ? k[2] : k[3];
-                    kth = nth_of_warp(a > b ? a : b, p.n_best);
-                    kth -= kth != 0;  // it may be among them itself
+                for (int u = 0; u < U; ++u) k[u] = i0 + 32 * u + lane < per ? part[i0 + 32 * u + lane] : 0;
+#pragma unroll 1
+                for (int u = 0; u < U; ++u) {
+                    Key c = k[0];
+#pragma unroll
+                    for (int v = 1; v < U; ++v) c = u == v ? k[v] : c;
+                    if (total > BM_WAIT - 32) rank();
+                    const unsigned in = __ballot_sync(0xFFFFFFFFu, c > kth);
+                    if (c > kth) list[total + __popc(in & ((1u << lane) - 1))] = c;
+                    total += __popc(in);
                 }
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    for (unsigned in = __ballot_sync(0xFFFFFFFFu, k[u] > kth); in; in &= in - 1) {
-                        const Key c = __shfl_sync(0xFFFFFFFFu, k[u], __ffs(in) - 1);
-                        if (c > kth) {
-                            best[q].insert(c);
-                            const Key n = best[q].nth(p.n_best);
-                            kth = n > kth ? n : kth;
-                        }
-                    }
             }
+            rank();
+            best[q] = lane < total ? list[lane] : 0;
         }
         for (int i = lane; i < p.slices; i += 32) m = fmaxf(m, i == lane ? mine.x : ml[i].x);
 #pragma unroll
@@ -219,7 +324,7 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
         const float m = s.m[tid], run = __ldg(p.scores + r0 + tid);
         // +infinity among the logits, none above -infinity, or a NaN score: no continuation
         const bool none = !(m < INFINITY) || !(m > -INFINITY) || !(run > -INFINITY);
-        s.lse[tid] = none ? INF : static_cast<double>(m) + log(static_cast<double>(s.sum[tid]));
+        s.lse[tid] = none ? INF : static_cast<double>(m) + log_of(s.sum[tid]);
         s.m[tid] = none ? 0.0f : run;
     }
     __syncthreads();
@@ -229,10 +334,10 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
     for (int q = 0; q < ROWS; ++q) {
         const int w = warp + q * BM_WARPS;
         if (w >= p.beams) break;
-        score[q] = static_cast<double>(value_of(best[q].mine)) - s.lse[w] + static_cast<double>(s.m[w]);
+        score[q] = static_cast<double>(value_of(best[q])) - s.lse[w] + static_cast<double>(s.m[w]);
         const long long b = __double_as_longlong(score[q] + 0.0);
         order[q] = b < 0 ? ~static_cast<Key>(b) : static_cast<Key>(b) | 0x8000000000000000ull;
-        if (best[q].mine == 0 || lane >= p.n_best || !(score[q] > -INF)) order[q] = 0;
+        if (best[q] == 0 || lane >= p.n_best || !(score[q] > -INF)) order[q] = 0;
         s.lists[w][lane] = order[q];
         const int count = __popc(__ballot_sync(0xFFFFFFFFu, order[q] != 0));
         if (lane == 0) s.count[w] = count;
@@ -250,7 +355,7 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
             if (o != w) rank += above(s.lists[o], s.count[o], order[q] - (o < w));
         if (rank < p.n_best) {
             p.score[out + rank] = static_cast<float>(score[q]);
-            p.token[out + rank] = token_of(best[q].mine);
+            p.token[out + rank] = token_of(best[q]);
             p.parent[out + rank] = static_cast<int32_t>(p.row0 + r0 + w);
         }
     }
@@ -272,7 +377,6 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
     __shared__ BeamShared s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long r = blockIdx.y;
-    if (tid == 0) s.shown = 0;
     pdl_launch_dependents();
     pdl_wait();
 
@@ -306,24 +410,32 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
         };
         constexpr int BATCH = BM_THREADS * BM_CHUNKS * E;
         uint4 next[BM_CHUNKS];
+        auto fetch_batch = [&](int l0) {
+            if (l0 + BATCH <= p.slice && t0 + l0 >= 0 && t0 + l0 + BATCH <= p.vocab) {
+                const uint4 *from = reinterpret_cast<const uint4 *>(x + t0 + l0) + tid;
 #pragma unroll
-        for (int k = 0; k < BM_CHUNKS; ++k) next[k] = fetch((k * BM_THREADS + tid) * E);
-        __syncthreads();  // s.shown
-        Best best;
-        Key kth = 0;
-        float m = -INFINITY, sum = 0.0f;
+                for (int k = 0; k < BM_CHUNKS; ++k) next[k] = __ldcs(from + k * BM_THREADS);
+            } else {
+#pragma unroll
+                for (int k = 0; k < BM_CHUNKS; ++k) next[k] = fetch(l0 + (k * BM_THREADS + tid) * E);
+            }
+        };
+        fetch_batch(0);
+        float m = -INFINITY, sum = 0.0f, bound = -INFINITY;
+        unsigned bound_token = 0xFFFFFFFFu;  // a value equal to the bound counts up to this token
+        int have = 0, kept = 0;              // keys of the list that are the best so far, and with those after them
         const int span = static_cast<int>(min(static_cast<long long>(p.slice), p.vocab - t0));
         for (int l0 = 0; l0 < span; l0 += BATCH) {
             uint4 cur[BM_CHUNKS];
 #pragma unroll
             for (int k = 0; k < BM_CHUNKS; ++k) cur[k] = next[k];
-            if (l0 + BATCH < span) {
+            if (l0 + BATCH < span) fetch_batch(l0 + BATCH);
+            float tops[BM_CHUNKS];
 #pragma unroll
-                for (int k = 0; k < BM_CHUNKS; ++k) next[k] = fetch(l0 + BATCH + (k * BM_THREADS + tid) * E);
-            }
-            float top = -INFINITY;
+            for (int k = 0; k < BM_CHUNKS; ++k) tops[k] = C::largest(cur[k]);
+            float top = tops[0];
 #pragma unroll
-            for (int k = 0; k < BM_CHUNKS; ++k) top = fmaxf(top, C::largest(cur[k]));
+            for (int k = 1; k < BM_CHUNKS; ++k) top = fmaxf(top, tops[k]);
 
             // the sum, against the thread's own running maximum
             if (top > m) {
@@ -332,10 +444,16 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
             }
             if (m > -INFINITY) {
                 const float m2 = m * LOG2E, before = sum;
+                float2 two = make_float2(sum, 0.0f);
 #pragma unroll
                 for (int k = 0; k < BM_CHUNKS; ++k)
 #pragma unroll
-                    for (int i = 0; i < E; ++i) sum += ex2(fmaf(C::at(cur[k], i), LOG2E, -m2));
+                    for (int i = 0; i < E; i += 2) {
+                        const float2 e = fma2(make_float2(C::at(cur[k], i), C::at(cur[k], i + 1)), make_float2(LOG2E, LOG2E),
+                                              make_float2(-m2, -m2));
+                        two = add2(two, make_float2(ex2(e.x), ex2(e.y)));
+                    }
+                sum = two.x + two.y;
                 if (!(sum < INFINITY)) {  // a NaN among them counts nothing
                     sum = before;
 #pragma unroll 1
@@ -350,90 +468,85 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
                 }
             }
 
-            // keys above the n-th
-            const Key shown = *static_cast<volatile Key *>(&s.shown);
-            if (shown > kth) kth = shown - 1;  // the key itself may be one of this warp's
-            float bound = kth ? value_of(kth) : -INFINITY;
-            if (!__any_sync(0xFFFFFFFFu, top >= bound && top > -INFINITY)) continue;
-            unsigned bound_token = token_of(kth);
             if (l0 == 0) {
-                const float b = nth_of_warp(top, p.n_best);
-                if (b > bound) bound = b, bound_token = 0xFFFFFFFFu;
+                if (tid == 0) s.total = 0;
+                bound = nth_of_block(top, p.n_best, s.sorted, &s.bound);
             }
-            // Few come here, so the code is short rather than unrolled: kernels of one
-            // batch wait for their instructions.
-            int count = 0, k = 0;
-            auto flush = [&]() {
-                __syncwarp();
-                for (int i = 0; i < count; ++i) {
-                    const Key key = s.wait[warp][i];
-                    if (key > kth) {
-                        best.insert(key);
-                        const Key n = best.nth(p.n_best);
-                        kth = n > kth ? n : kth;
+            const auto taken = [&](float v, unsigned t) { return v > -INFINITY && (v > bound || (v == bound && t <= bound_token)); };
+            bool some = l0 == 0 || l0 + BATCH >= span;
+            if (top >= bound && top > -INFINITY) {
+                some = true;
+                // few come here, so the code is short rather than unrolled
+#pragma unroll 1
+                for (int k = 0; k < BM_CHUNKS; ++k) {
+                    float c_top = tops[0];
+#pragma unroll
+                    for (int i = 1; i < BM_CHUNKS; ++i) c_top = i == k ? tops[i] : c_top;
+                    if (!(c_top >= bound)) continue;
+                    const uint4 c = pick(cur, k);
+                    unsigned hits = 0;
+#pragma unroll
+                    for (int i = 0; i < E; ++i) hits |= C::at(c, i) >= bound ? 1u << i : 0;
+                    for (; hits; hits &= hits - 1) {
+                        const int i = __ffs(hits) - 1;
+                        const float v = C::any(c, i);
+                        const unsigned t = static_cast<unsigned>(t0 + l0 + (k * BM_THREADS + tid) * E + i);
+                        if (taken(v, t)) {
+                            const int at = atomicAdd(&s.total, 1);
+                            if (at < BM_LIST) s.list[at] = key_of(v, t);
+                        }
                     }
                 }
-                count = 0;
-                __syncwarp();
-            };
-            unsigned mine = 0;  // the thread's elements of chunk k - 1 that wait
-            uint4 c = cur[0];
-            unsigned t = 0;
-            for (;;) {
-                if (!__any_sync(0xFFFFFFFFu, mine)) {
-                    if (k == BM_CHUNKS) break;
-                    c = pick(cur, k);
-                    t = static_cast<unsigned>(t0 + l0 + (k * BM_THREADS + tid) * E);
-                    ++k;
-                    const float c_top = C::largest(c);
-                    if (!__any_sync(0xFFFFFFFFu, c_top >= bound && c_top > -INFINITY)) continue;
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        const float v = C::at(c, i);
-                        if (v > -INFINITY && (v > bound || (v == bound && t + i <= bound_token))) mine |= 1u << i;
-                    }
-                    continue;
-                }
-                const unsigned in = __ballot_sync(0xFFFFFFFFu, mine != 0);
-                if (mine) {
-                    const int i = __ffs(mine) - 1;
-                    mine &= mine - 1;
-                    float v = C::at(c, 0);
-#pragma unroll
-                    for (int e = 1; e < E; ++e) v = e == i ? C::at(c, e) : v;
-                    s.wait[warp][count + __popc(in & ((1u << lane) - 1))] = key_of(v, t + i);
-                }
-                count += __popc(in);
-                if (count > BM_LIST - 32) flush();
             }
-            flush();
-            const Key n = best.nth(p.n_best);
-            if (lane == 0 && n > shown) atomicMax(&s.shown, n);
+            if (!__syncthreads_or(some)) continue;
+            int total = s.total;
+            const bool over = total > BM_LIST;
+            if (over) {
+                // this batch again, one at a time: the largest key below the last
+                Key last = ~0ull;
+                int found = 0;
+                for (; found < p.n_best; ++found) {
+                    Key key = 0;
+#pragma unroll 1
+                    for (int k = 0; k < BM_CHUNKS; ++k) {
+                        const uint4 c = pick(cur, k);
+                        const unsigned t = static_cast<unsigned>(t0 + l0 + (k * BM_THREADS + tid) * E);
+#pragma unroll
+                        for (int i = 0; i < E; ++i) {
+                            const float v = C::at(c, i);
+                            const Key mine = key_of(v, t + i);
+                            if (taken(v, t + i) && mine < last && mine > key) key = mine;
+                        }
+                    }
+                    last = block_largest(key, s.best);
+                    if (last == 0) break;
+                    if (tid == 0) s.list[kept + found] = last;
+                }
+                total = kept + found;
+            }
+            if (total > have + BM_FULL || l0 == 0 || l0 + BATCH >= span || over) {
+                rank_keys<BM_THREADS, BM_LIST / BM_THREADS>(s.list, total, p.n_best, tid, [] { __syncthreads(); });
+                total = have = min(total, p.n_best);
+                if (tid == 0) s.total = have;
+                if (have == p.n_best) {
+                    bound = value_of(s.list[have - 1]);
+                    bound_token = token_of(s.list[have - 1]);
+                }
+            }
+            kept = total;
+            __syncthreads();
         }
 
-        // the warps' lists, maxima and sums
+        // the block's list, maximum and sum
         float wm = m;
 #pragma unroll
         for (int d = 16; d; d >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xFFFFFFFFu, wm, d));
         sum = m > -INFINITY ? sum * ex2((m - wm) * LOG2E) : 0.0f;
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        if (lane >= p.n_best) best.mine = 0;
-        s.lists[warp][lane] = best.mine;
-        const int count = __popc(__ballot_sync(0xFFFFFFFFu, best.mine != 0));
-        if (lane == 0) s.m[warp] = wm, s.sum[warp] = sum, s.count[warp] = count;
+        if (lane == 0) s.m[warp] = wm, s.sum[warp] = sum;
         __syncthreads();
-        int all = 0;
-#pragma unroll
-        for (int w = 0; w < BM_WARPS; ++w) all += s.count[w];
-        if (best.mine) {
-            int rank = lane;
-#pragma unroll
-            for (int w = 0; w < BM_WARPS; ++w)
-                if (w != warp) rank += above(s.lists[w], s.count[w], best.mine);
-            if (rank < p.n_best) p.part[out * p.n_best + rank] = best.mine;
-        }
-        if (tid >= all && tid < p.n_best) p.part[out * p.n_best + tid] = 0;
+        if (tid < p.n_best) p.part[out * p.n_best + tid] = tid < have ? s.list[tid] : 0;
         if (tid == 0) {
             float bm = s.m[0], total = 0.0f;
 #pragma unroll

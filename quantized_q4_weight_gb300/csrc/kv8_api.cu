@@ -108,7 +108,7 @@ inline Span table_span(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c)
 // Launch shape and workspace of the attention.
 struct Kv8Plan {
     int group, rows, row_tiles, tile_rows, tile_pad;
-    int balanced, grid, combine_lanes, by_unit;
+    int balanced, grid, combine_lanes, by_unit, aligned;
     long long ml_at, parts_at, ws_bytes;
 };
 
@@ -131,7 +131,7 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     a.ml_at = a.parts_at = kCounterArea;
     a.ws_bytes = kCounterArea;
     a.combine_lanes = 1;
-    a.by_unit = 0;
+    a.by_unit = a.aligned = 0;
     if (!a.balanced) {
         if (units > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
         a.grid = static_cast<int>(units);
@@ -139,13 +139,14 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     }
     // the line of all sequences' tiles in ranges, a block for each range, cache head and tile of rows
     const long long per_seq = units / b->n_seqs, blocks = static_cast<long long>(ATTN_SMS) * kv8_blocks(c->head_dim, nt);
-    const long long ranges = std::min(std::max(1ll, blocks / per_seq), ceil_div(b->n_seqs * tiles, KV8_SPLIT_MIN));
+    const long long ranges = std::min(std::max(1ll, blocks / per_seq), ceil_div(b->n_seqs * tiles, KV8_SPLIT_MIN) + b->n_seqs);
     if (ranges * per_seq > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
     a.grid = static_cast<int>(ranges * per_seq);
     // parts of a sequence: about ranges / n_seqs, and of a long one up to ranges.  A group takes four at once.
     const long long parts = ranges / std::min<long long>(b->n_seqs, ranges);
     while (a.combine_lanes < 32 && 2 * a.combine_lanes < parts) a.combine_lanes *= 2;
     a.by_unit = units <= a.grid;
+    a.aligned = 8ll * b->n_seqs <= ranges;
     a.ml_at = a.parts_at + 16ll * a.grid;
     const long long o_at = a.ml_at + 16ll * a.grid * a.tile_pad;
     a.ws_bytes = o_at + 8ll * a.grid * a.tile_pad * c->head_dim;
@@ -423,6 +424,7 @@ qgemv_status qgemv_attn_kv8(const void *q, qgemv_dtype q_type, int64_t q_token_s
     p.grid = a.grid;
     p.combine_lanes = a.combine_lanes;
     p.parts_by_unit = a.by_unit;
+    p.aligned = a.aligned;
     uint8_t *at = static_cast<uint8_t *>(ws);
     p.parts = reinterpret_cast<int4 *>(at + a.parts_at);
     p.part_ml = reinterpret_cast<float2 *>(at + a.ml_at);

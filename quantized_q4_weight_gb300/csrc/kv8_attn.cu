@@ -55,8 +55,9 @@ struct K8Cfg {
     static constexpr int TILE = 2 * KV8_KEYS * DP;
     static constexpr int BLOCKS = kv8_blocks(DP, NT);
     static constexpr int WARPS = kv8_warps(DP, NT), THREADS = 32 * WARPS;
-    static constexpr int STAGES = DP == 64 ? (NT > 2 ? 4 : 3) : DP == 128 && BLOCKS == 1 ? 3 : 2;
+    static constexpr int STAGES = DP == 64 ? (NT > 2 ? 4 : 3) : DP == 128 && NT > 2 ? 3 : 2;
     static constexpr bool QREG = DP * NT <= 128;          // Q's fragments in registers
+    static constexpr int XN = NT <= 3 ? 2 : 1;            // halves of a tile at once
     static constexpr int OFF_META = WARPS * STAGES * TILE;               // per warp and stage: ks, vs of both halves
     static constexpr int OFF_Q = OFF_META + WARPS * STAGES * 16;
     static constexpr int OFF_QS = OFF_Q + 8 * NT * DP * 2;
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
     const int rows = min(p.tile_rows, p.rows - row0);
     int lo, hi, range = 0, seq_at, b;  // in tiles: all of them fit 31 bits
     if (p.balanced) {
-        // every warp adds all sequences' tiles up, each lane a run of them
+        // Every warp adds all sequences' tiles up, each lane a run of them.
         const int run = (p.n_seqs + 31) / 32;
         int mine = 0;
         for (int i = lane * run; i < min(p.n_seqs, (lane + 1) * run); ++i) {
@@ -300,23 +301,44 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
             const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
             if (lane >= o) upto += v;
         }
-        const int total = __shfl_sync(0xFFFFFFFFu, upto, 31), ranges = p.grid / per_seq;
-        range = max(KV8_SPLIT_MIN, (total + ranges - 1) / ranges);
-        lo = static_cast<int>(blockIdx.x) / per_seq * range, hi = min(total, lo + range);
-        // the first lane whose run ends behind lo walks its run
-        const unsigned behind = __ballot_sync(0xFFFFFFFFu, upto > lo);
+        const int total = __shfl_sync(0xFFFFFFFFu, upto, 31), ranges = p.grid / per_seq, mine_no = blockIdx.x / per_seq;
+        int item = mine_no, most = ranges;  // what the walk looks for: the block's range, or its first tile
+        if (p.aligned) {
+            // few sequences: whole ranges for each, so that no block has two of them
+            range = max(KV8_SPLIT_MIN, (total + ranges - p.n_seqs - 1) / (ranges - p.n_seqs));
+            mine = 0;
+            for (int i = lane * run; i < min(p.n_seqs, (lane + 1) * run); ++i) mine += (Seen(p, __ldg(p.lens + i)).tiles + range - 1) / range;
+            upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            most = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        } else {
+            range = max(KV8_SPLIT_MIN, (total + ranges - 1) / ranges);
+            item = mine_no * range, most = total;
+        }
+        // the first lane whose run ends behind it walks its run
+        const unsigned behind = __ballot_sync(0xFFFFFFFFu, upto > item);
         const int owner = behind ? __ffs(behind) - 1 : 0;
         int at = lane * run;
         seq_at = upto - mine;
-        if (lane == owner && lo < total) {
+        if (lane == owner && item < most) {
             for (;; ++at) {
-                const int n = Seen(p, __ldg(p.lens + at)).tiles;
-                if (seq_at + n > lo) break;
+                int n = Seen(p, __ldg(p.lens + at)).tiles;
+                if (p.aligned) n = (n + range - 1) / range;
+                if (seq_at + n > item) break;
                 seq_at += n;
             }
         }
         b = __shfl_sync(0xFFFFFFFFu, at, owner);
         seq_at = __shfl_sync(0xFFFFFFFFu, seq_at, owner);
+        // from here on tiles are counted from where the sequence's begin (aligned), or along the line
+        lo = p.aligned ? (item - seq_at) * range : item;
+        seq_at = p.aligned ? 0 : seq_at;
+        hi = lo + range;
+        if (item < most) hi = min(hi, p.aligned ? Seen(p, __ldg(p.lens + b)).tiles : total);
         for (int i = blockIdx.x; i < p.n_seqs; i += p.grid)
             if (Seen(p, __ldg(p.lens + i)).n == 0) {
                 for (int k = 0; k < p.hkv; ++k) store_none(p, i, k, 0, p.rows);
@@ -324,7 +346,7 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                     for (int k = tid; k < per_seq; k += C::THREADS) p.parts[i * per_seq + k] = make_int4(0, 0, 0, 0);
             }
         if (!p.parts_by_unit && tid == 0) p.parts[blockIdx.x] = make_int4(0, 0, 0, 0);
-        if (lo >= total) return;
+        if (item >= most) return;
     } else {
         b = blockIdx.x / per_seq;
         const int n = __ldg(p.lens + b);
@@ -476,12 +498,13 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
         }
 
         // The references that a tile with exponents s (-infinity: not seen) asks for.
-        auto raise = [&](const float (&s)[2][NT][4]) {
+        auto raise = [&](const float (&s)[C::XN][NT][4]) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(fmaxf(s[0][j][e], s[0][j][2 + e]), fmaxf(s[1][j][e], s[1][j][2 + e]));
+                    float mx = fmaxf(s[0][j][e], s[0][j][2 + e]);
+                    if (C::XN == 2) mx = fmaxf(mx, fmaxf(s[C::XN - 1][j][e], s[C::XN - 1][j][2 + e]));
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
                     if (mx - m[j][e] > K8_SLACK) {
@@ -513,10 +536,20 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
             const bool whole = j0 + KV8_KEYS - 1 <= seen.n - p.n_q && !gone &&
                                (!p.window || j0 > seen.n - 1 - p.window || j0 + KV8_KEYS - 1 < p.sinks);
 
-            // ---- scores of 2 x 16 keys
-            float s[2][NT][4];
+            // ---- 16 keys after 16 keys, or both sixteens at once
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < 2; ++x) {
+                // a block of zeros has scale 0: any other does for its codes
+                vs[x] = vs[x] < 8.673617e-19f ? 8.673617e-19f : vs[x];  // 2^-60
+                lv[x] = lg2(vs[x]), inv[x] = rcp(vs[x]);
+            }
+#pragma unroll 1
+            for (int x0 = 0; x0 < 2; x0 += C::XN) {
+            auto scale_of = [&](const float (&v)[2], int x) { return C::XN == 2 ? v[x] : x0 ? v[1] : v[0]; };
+            // scores
+            float s[C::XN][NT][4];
+#pragma unroll
+            for (int x = 0; x < C::XN; ++x)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -524,8 +557,8 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
 #pragma unroll
             for (int c = 0; c < C::KC; ++c)
 #pragma unroll
-                for (int h2 = 0; h2 < 2; ++h2) {
-                    const uint32_t at = src + (DP == 64 ? 0 : c >> 1) * C::BOX + 16 * h2 * C::ROW + ((c & 1) ? k_off1 : k_off0);
+                for (int h2 = 0; h2 < C::XN; ++h2) {
+                    const uint32_t at = src + (DP == 64 ? 0 : c >> 1) * C::BOX + 16 * (x0 + h2) * C::ROW + ((c & 1) ? k_off1 : k_off0);
                     const uint4 x = lds128(at), y = lds128(at + 8 * C::ROW);
                     const unsigned xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
                     unsigned a[4][4];
@@ -548,22 +581,15 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                             mma(s[h2][j], a[k][0], a[k][1], a[k][2], a[k][3], f[2 * k], f[2 * k + 1]);
                     }
                 }
-
-            // ---- weights.  A block of zeros has scale 0: any other does for its codes
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                vs[x] = vs[x] < 8.673617e-19f ? 8.673617e-19f : vs[x];  // 2^-60
-                lv[x] = lg2(vs[x]), inv[x] = rcp(vs[x]);
-            }
             // exponents in place of the sums
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < C::XN; ++x)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const float2 f = mul2(make_float2(ks[x], ks[x]), make_float2(qs[j][0], qs[j][1]));
+                    const float2 f = mul2(make_float2(scale_of(ks, x), scale_of(ks, x)), make_float2(qs[j][0], qs[j][1]));
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float2 a = fma2(make_float2(s[x][j][2 * k], s[x][j][2 * k + 1]), f, make_float2(lv[x], lv[x]));
+                        const float2 a = fma2(make_float2(s[x][j][2 * k], s[x][j][2 * k + 1]), f, make_float2(scale_of(lv, x), scale_of(lv, x)));
                         s[x][j][2 * k] = a.x, s[x][j][2 * k + 1] = a.y;
                     }
                 }
@@ -574,7 +600,11 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        top = fmaxf(top, fmaxf(fmaxf(s[0][j][e], s[0][j][2 + e]), fmaxf(s[1][j][e], s[1][j][2 + e])) - m[j][e]);
+                        {
+                        float mx = fmaxf(s[0][j][e], s[0][j][2 + e]);
+                        if (C::XN == 2) mx = fmaxf(mx, fmaxf(s[C::XN - 1][j][e], s[C::XN - 1][j][2 + e]));
+                        top = fmaxf(top, mx - m[j][e]);
+                    }
                 up = __any_sync(0xFFFFFFFFu, top > K8_SLACK);
             } else {
 #pragma unroll
@@ -583,27 +613,27 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                     for (int e = 0; e < 2; ++e) {
                         const int q_pos = seen.n - p.n_q + (row0 + 8 * j + 2 * t + e) / p.group;
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
+                        for (int x = 0; x < C::XN; ++x)
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const int key = j0 + 16 * x + pg + 8 * k;
+                                const int key = j0 + 16 * (x0 + x) + pg + 8 * k;
                                 const bool sees = key <= q_pos && (!p.window || key > q_pos - p.window || key < p.sinks) &&
-                                                  !(gone >> x & 1);
+                                                  !(gone >> (x0 + x) & 1);
                                 if (!sees) s[x][j][2 * k + e] = -INFINITY;
                             }
                     }
             }
             if (up) raise(s);
-            unsigned pb[2][NT][2];
+            unsigned pb[C::XN][NT][2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < C::XN; ++x)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     const float2 down = make_float2(-m[j][0], -m[j][1]);
                     float2 a = add2(make_float2(s[x][j][0], s[x][j][1]), down), b = add2(make_float2(s[x][j][2], s[x][j][3]), down);
                     a = make_float2(ex2(a.x), ex2(a.y)), b = make_float2(ex2(b.x), ex2(b.y));
                     const float2 sum = add2(a, b);
-                    const float2 add = mul2(sum, make_float2(inv[x], inv[x]));
+                    const float2 add = mul2(sum, make_float2(scale_of(inv, x), scale_of(inv, x)));
                     // a row that sees none of the half takes nothing from its scale either
                     l[j][0] += whole || sum.x != 0.0f ? add.x : 0.0f;
                     l[j][1] += whole || sum.y != 0.0f ? add.y : 0.0f;
@@ -612,16 +642,16 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                     pb[x][j][1] = movm(pack(b.x, b.y));
                 }
 
-            // ---- weighted sums of v
+            // weighted sums of v
 #pragma unroll
             for (int c = 0; c < C::VC; ++c)
 #pragma unroll
-                for (int h2 = 0; h2 < 2; ++h2) {
+                for (int h2 = 0; h2 < C::XN; ++h2) {
                     constexpr int W = C::VB / 4;
                     unsigned v[4][W];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const uint32_t at = src + KV8_KEYS * DP + c * C::BOX + (16 * h2 + 8 * (r >> 1)) * C::ROW + (r & 1 ? v_off1 : v_off0);
+                        const uint32_t at = src + KV8_KEYS * DP + c * C::BOX + (16 * (x0 + h2) + 8 * (r >> 1)) * C::ROW + (r & 1 ? v_off1 : v_off0);
                         if constexpr (W == 4) {
                             const uint4 x = lds128(at);
                             v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
@@ -648,6 +678,7 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                                 mma(o[j][(C::VB / 2) * c + 2 * k + x], a0, a1, a2, a3, pb[h2][j][0], pb[h2][j][1]);
                         }
                 }
+            }
             __syncwarp();
         }
 
@@ -712,7 +743,7 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
         }
         // the sequence begins here: its parts, if it ends in a later block's range
         if (tid == 0 && p.balanced && i0 == 0 && (p.parts_by_unit || i1 < seen.tiles)) {
-            const int n = (seq_at + seen.tiles - 1) / range - static_cast<int>(blockIdx.x) / per_seq + 1;
+            const int n = (seq_at + seen.tiles - 1) / range - (p.aligned ? 0 : static_cast<int>(blockIdx.x) / per_seq) + 1;
             p.parts[p.parts_by_unit ? b * per_seq + unit : blockIdx.x] = make_int4(b, unit, part, i1 < seen.tiles ? n : 0);
         }
         pos = seq_at + i1;

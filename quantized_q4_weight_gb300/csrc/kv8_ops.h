@@ -58,6 +58,7 @@ struct Kv8AttnParams {
     int rows, row_tiles, tile_rows;  // of a sequence and cache head: n_q * group, in row_tiles of tile_rows
     float scale_log2;
     int balanced, grid;              // ranges of all tiles over `grid` blocks, or a block for each unit
+    int aligned;                     // ranges begin with their sequence: there are eight times as many as sequences
     int parts_by_unit;               // there are no more units than blocks
     int4 *parts;                     // of each unit, or block: sequence, unit, first part, parts (0: none)
     float *part_o;                   // [2 grid][tile rows, padded][d]
@@ -70,12 +71,15 @@ struct Kv8AttnParams {
     unsigned *status;
 };
 constexpr int KV8_KEYS = 32;         // keys of a tile
-constexpr int KV8_SPLIT_MIN = 12;    // tiles of a range at least
+constexpr int KV8_SPLIT_MIN = 6;     // tiles of a range at least: one for each warp
 // Rows of a tile at most, and, for tiles of 8 nt rows, blocks a multiprocessor
 // and warps a block.
 constexpr int kv8_tile_rows(int d) { return d <= 128 ? 32 : 16; }
 constexpr int kv8_blocks(int d, int nt) { return d > 128 || (d > 64 && nt > 2) ? 1 : 2; }
-constexpr int kv8_warps(int d, int nt) { return (d <= 64 && nt <= 2) || (d > 64 && d <= 128 && nt > 2) ? 8 : 6; }
+constexpr int kv8_warps(int d, int nt)
+{
+    return d > 64 && d <= 128 && nt > 2 ? 8 : d <= 64 && nt <= 2 ? 8 : 6;
+}
 cudaError_t launch_kv8_attn(const Kv8AttnParams &p, qgemv_code_type code, cudaStream_t st);
 
 // ------------------------------------------------------------------- beams
