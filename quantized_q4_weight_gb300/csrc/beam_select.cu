@@ -12,10 +12,10 @@
 // down, so that a larger key is a larger logit or a lower token.  The block keeps the n
 // best keys it has met in shared memory, in order, and compares every value with the
 // n-th of them, which few pass; those are appended, and from time to time ranked together
-// with the best by counting.  The first values go by the n-th largest of the threads'
-// largest (a bitonic network of shuffles for each warp, then a search in the others' lists),
-// a bound that lets few more than n through.  More equal or rising values than the
-// list holds are taken n at a time, each by a maximum over the block.
+// with the best by counting.  The first values go by the lowest of the warps' (n / 8)-th
+// largest lanes, which n values of the block reach and not many more.  More equal or rising
+// values than the list holds are read again and taken n at a time, each by a maximum over
+// the block.
 //
 // What bounds it: memory for many rows (logits read once; a maximum, a product, an
 // exponential and a sum for each); the chain launch, logits, ranks, arrival, join for one
@@ -32,6 +32,7 @@ constexpr int BM_LIST = 512;   // keys of a block that are ranked at once
 constexpr int BM_FULL = 16;    // appended keys that are worth a ranking: it raises the bound
 constexpr int BM_WAIT = 64;    // keys of a warp in the join
 constexpr int BM_BEAMS = 16;
+constexpr int BM_SLICES = 64;  // of a row at most
 constexpr float LOG2E = 1.4426950408889634f;
 
 typedef unsigned long long Key;
@@ -86,8 +87,9 @@ __device__ __forceinline__ Key key_of(float v, unsigned token)
 __device__ __forceinline__ float value_of(Key k) { return from_ordered(static_cast<unsigned>(k >> 32)); }
 __device__ __forceinline__ unsigned token_of(Key k) { return 0xFFFFFFFFu - static_cast<unsigned>(k); }
 
-// Elements of a 16-byte chunk as floats (`at` for a constant place, `any` for a
-// variable one), and the largest of them (NaN passed over).
+// Elements of a 16-byte chunk as floats, and the largest of them (NaN passed over); of a
+// batch, a bit for each element that reaches a bound (a value of the type), and where
+// such an element is: chunk, place in it.
 template <typename T>
 struct Chunk16;
 template <>
@@ -97,11 +99,20 @@ struct Chunk16<float> {
     {
         return __uint_as_float(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w);
     }
-    static __device__ __forceinline__ float any(const uint4 &w, int i) { return at(w, i); }
     static __device__ __forceinline__ float largest(const uint4 &w)
     {
         return fmaxf(fmaxf(at(w, 0), at(w, 1)), fmaxf(at(w, 2), at(w, 3)));
     }
+    static __device__ __forceinline__ unsigned reach(const uint4 (&c)[BM_CHUNKS], float bound)
+    {
+        unsigned bits = 0;
+#pragma unroll
+        for (int k = 0; k < 4 * BM_CHUNKS; ++k) bits |= at(c[k >> 2], k & 3) >= bound ? 1u << k : 0;
+        return bits;
+    }
+    static __device__ __forceinline__ int2 place(int bit) { return make_int2(bit >> 2, bit & 3); }
+    static __device__ __forceinline__ float value(unsigned word, int) { return __uint_as_float(word); }
+    static __device__ __forceinline__ int word(int i) { return i; }
 };
 template <>
 struct Chunk16<__half> {
@@ -115,39 +126,59 @@ struct Chunk16<__half> {
     {
         return i & 1 ? __high2float(pair(w, i >> 1)) : __low2float(pair(w, i >> 1));
     }
-    static __device__ __forceinline__ float any(const uint4 &w, int i)
-    {
-        const __half2 p = pair(w, i >> 1);
-        return i & 1 ? __high2float(p) : __low2float(p);
-    }
     static __device__ __forceinline__ float largest(const uint4 &w)
     {
         const __half2 m = __hmax2(__hmax2(pair(w, 0), pair(w, 1)), __hmax2(pair(w, 2), pair(w, 3)));
         return fmaxf(__low2float(m), __high2float(m));
+    }    // bit w: the lower element of word w, bit 16 + w its upper one
+    static __device__ __forceinline__ unsigned reach(const uint4 (&c)[BM_CHUNKS], float bound)
+    {
+        const __half2 b = __half2half2(__float2half_rn(bound));
+        unsigned bits = 0;
+#pragma unroll
+        for (int k = 0; k < 4 * BM_CHUNKS; ++k) bits |= __hge2_mask(pair(c[k >> 2], k & 3), b) & 0x10001u << k;
+        return bits;
     }
+    static __device__ __forceinline__ int2 place(int bit) { return make_int2(bit >> 2 & 3, 2 * (bit & 3) + (bit >> 4)); }
+    static __device__ __forceinline__ float value(unsigned word, int i)
+    {
+        const __half2 p = *reinterpret_cast<const __half2 *>(&word);
+        return i & 1 ? __high2float(p) : __low2float(p);
+    }
+    static __device__ __forceinline__ int word(int i) { return i >> 1; }
 };
 template <>
 struct Chunk16<__nv_bfloat16> {
     static constexpr int E = 8;
-    static __device__ __forceinline__ unsigned word(const uint4 &w, int i) { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
+    static __device__ __forceinline__ unsigned part(const uint4 &w, int i) { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
     static __device__ __forceinline__ __nv_bfloat162 pair(const uint4 &w, int i)
     {
-        const unsigned u = word(w, i);
+        const unsigned u = part(w, i);
         return *reinterpret_cast<const __nv_bfloat162 *>(&u);
     }
     static __device__ __forceinline__ float at(const uint4 &w, int i)
     {
-        return __uint_as_float(i & 1 ? word(w, i >> 1) & 0xFFFF0000u : word(w, i >> 1) << 16);
-    }
-    static __device__ __forceinline__ float any(const uint4 &w, int i)
-    {
-        return __uint_as_float(word(w, i >> 1) << (i & 1 ? 0 : 16) & 0xFFFF0000u);
+        return __uint_as_float(i & 1 ? part(w, i >> 1) & 0xFFFF0000u : part(w, i >> 1) << 16);
     }
     static __device__ __forceinline__ float largest(const uint4 &w)
     {
         const __nv_bfloat162 m = __hmax2(__hmax2(pair(w, 0), pair(w, 1)), __hmax2(pair(w, 2), pair(w, 3)));
         return fmaxf(__low2float(m), __high2float(m));
+    }    // bit w: the lower element of word w, bit 16 + w its upper one
+    static __device__ __forceinline__ unsigned reach(const uint4 (&c)[BM_CHUNKS], float bound)
+    {
+        const __nv_bfloat162 b = __bfloat162bfloat162(__float2bfloat16_rn(bound));
+        unsigned bits = 0;
+#pragma unroll
+        for (int k = 0; k < 4 * BM_CHUNKS; ++k) bits |= __hge2_mask(pair(c[k >> 2], k & 3), b) & 0x10001u << k;
+        return bits;
     }
+    static __device__ __forceinline__ int2 place(int bit) { return make_int2(bit >> 2 & 3, 2 * (bit & 3) + (bit >> 4)); }
+    static __device__ __forceinline__ float value(unsigned word, int i)
+    {
+        return __uint_as_float(word << (i & 1 ? 0 : 16) & 0xFFFF0000u);
+    }
+    static __device__ __forceinline__ int word(int i) { return i >> 1; }
 };
 
 // A warp's 32 values falling over its lanes.
@@ -165,29 +196,31 @@ __device__ __forceinline__ void sort_warp(V &v)
         }
 }
 
-// The n-th largest of the block's 256 values, to all threads.
-__device__ __forceinline__ float nth_of_block(float v, int n, float (*s)[32], float *s_bound)
+// A bound that at least n of the block's values reach, to all threads, given each
+// thread's largest value v and that the first `warps` warps have values: the lowest of
+// those warps' ceil(n / warps)-th, or, where one has too few above -infinity, the highest
+// of the warps' n-th.
+__device__ __forceinline__ float low_bound(float v, int n, int warps, unsigned (*s)[BM_WARPS])
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    sort_warp(v);
-    s[warp][lane] = v;
-    __syncthreads();
-    // a value's rank: its place in its own list, and in each other list the values that come before it
-    int rank = lane;
-#pragma unroll
-    for (int w = 0; w < BM_WARPS; ++w) {
-        int at = 0;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            const float o = s[w][at + d - 1];
-            if (o > v || (o == v && w < warp)) at += d;
+    unsigned u = ordered(v), top = 0;
+    const auto next = [&](int count) {  // the largest `count` times, each taken out
+        for (int k = 0; k < count; ++k) {
+            top = __reduce_max_sync(0xFFFFFFFFu, u);
+            if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, u == top)) - 1) u = 0;
         }
-        const float o = s[w][at];
-        rank += w == warp ? 0 : at + (o > v || (o == v && w < warp));
-    }
-    if (rank == n - 1) *s_bound = v;
+    };
+    const int each = (n + warps - 1) / warps;
+    next(each);
+    if (lane == 0) s[0][warp] = warp < warps ? top : 0xFFFFFFFFu;
     __syncthreads();
-    return *s_bound;
+    const float low = from_ordered(__reduce_min_sync(0xFFFFFFFFu, s[0][lane & (BM_WARPS - 1)]));
+    if (low > -INFINITY) return low;
+    next(n - each);
+    if (lane == 0) s[1][warp] = top;
+    __syncthreads();
+    const unsigned high = __reduce_max_sync(0xFFFFFFFFu, s[1][lane & (BM_WARPS - 1)]);
+    return high ? from_ordered(high) : -INFINITY;
 }
 
 // The best n of list[0 .. total), in order, to its front; THREADS threads, `t` of them this
@@ -246,9 +279,8 @@ struct BeamShared {
         Key wait[BM_WARPS][BM_WAIT];    // the same of a row's warp in the join
     };
     Key lists[BM_BEAMS][32];            // the join's rows
-    float sorted[BM_WARPS][32];
     Key best[BM_WARPS];
-    float bound, red[BM_WARPS];
+    unsigned first[2][BM_WARPS];
     int total;                          // keys of the list
     int last;
     float m[BM_BEAMS], sum[BM_BEAMS];
@@ -272,12 +304,22 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
         const Key *part = p.part + (r0 + w) * per;
         const float2 *ml = p.part_ml + (r0 + w) * p.slices;
         float m = -INFINITY, sum = 0.0f;
-        float2 mine = lane < p.slices ? ml[lane] : make_float2(-INFINITY, 0.0f);
+        float2 mine[BM_SLICES / 32];
+#pragma unroll
+        for (int u = 0; u < BM_SLICES / 32; ++u)
+            mine[u] = lane + 32 * u < p.slices ? __ldcg(ml + lane + 32 * u) : make_float2(-INFINITY, 0.0f);
         if (p.slices == 1) {
-            best[q] = lane < p.n_best ? part[lane] : 0;
+            best[q] = lane < p.n_best ? __ldcg(part + lane) : 0;
         } else {
+            constexpr int U = 10;
+            Key k[U];
+            auto fetch = [&](int i0) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) k[u] = i0 + 32 * u + lane < per ? __ldcg(part + i0 + 32 * u + lane) : 0;
+            };
             // the slices' first keys bound the n-th from below, where there are n
-            unsigned head = lane < p.slices ? static_cast<unsigned>(part[lane * p.n_best] >> 32) : 0;
+            unsigned head = lane < p.slices ? static_cast<unsigned>(__ldcg(part + lane * p.n_best) >> 32) : 0;
+            fetch(0);
             sort_warp(head);
             head = __shfl_sync(0xFFFFFFFFu, head, p.n_best - 1);
             Key kth = head ? (static_cast<Key>(head) << 32) - 1 : 0;
@@ -288,11 +330,8 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
                 total = min(total, p.n_best);
                 if (total == p.n_best) kth = list[p.n_best - 1];
             };
-            constexpr int U = 8;
             for (int i0 = 0; i0 < per; i0 += 32 * U) {
-                Key k[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) k[u] = i0 + 32 * u + lane < per ? part[i0 + 32 * u + lane] : 0;
+                if (i0) fetch(i0);
 #pragma unroll 1
                 for (int u = 0; u < U; ++u) {
                     Key c = k[0];
@@ -307,13 +346,13 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
             rank();
             best[q] = lane < total ? list[lane] : 0;
         }
-        for (int i = lane; i < p.slices; i += 32) m = fmaxf(m, i == lane ? mine.x : ml[i].x);
+#pragma unroll
+        for (int u = 0; u < BM_SLICES / 32; ++u) m = fmaxf(m, mine[u].x);
 #pragma unroll
         for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        for (int i = lane; i < p.slices; i += 32) {
-            const float2 v = i == lane ? mine : ml[i];
-            if (v.x > -INFINITY) sum = fmaf(v.y, expf(v.x - m), sum);
-        }
+#pragma unroll
+        for (int u = 0; u < BM_SLICES / 32; ++u)
+            if (mine[u].x > -INFINITY) sum = fmaf(mine[u].y, expf(mine[u].x - m), sum);
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
         if (lane == 0) s.m[w] = m, s.sum[w] = sum;
@@ -351,6 +390,7 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
         if (order[q] == 0) continue;
         // equal scores of other rows: the lower row comes first
         int rank = lane;
+#pragma unroll 4
         for (int o = 0; o < p.beams; ++o)
             if (o != w) rank += above(s.lists[o], s.count[o], order[q] - (o < w));
         if (rank < p.n_best) {
@@ -423,22 +463,20 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
         fetch_batch(0);
         float m = -INFINITY, sum = 0.0f, bound = -INFINITY;
         unsigned bound_token = 0xFFFFFFFFu;  // a value equal to the bound counts up to this token
-        int have = 0, kept = 0;              // keys of the list that are the best so far, and with those after them
+        int have = 0, kept = 0, since = 0;   // keys of the list that are the best so far, and with those after them; where it was
+                                             // looked at last
         const int span = static_cast<int>(min(static_cast<long long>(p.slice), p.vocab - t0));
         for (int l0 = 0; l0 < span; l0 += BATCH) {
             uint4 cur[BM_CHUNKS];
 #pragma unroll
             for (int k = 0; k < BM_CHUNKS; ++k) cur[k] = next[k];
             if (l0 + BATCH < span) fetch_batch(l0 + BATCH);
-            float tops[BM_CHUNKS];
+            float top = C::largest(cur[0]);
 #pragma unroll
-            for (int k = 0; k < BM_CHUNKS; ++k) tops[k] = C::largest(cur[k]);
-            float top = tops[0];
-#pragma unroll
-            for (int k = 1; k < BM_CHUNKS; ++k) top = fmaxf(top, tops[k]);
+            for (int k = 1; k < BM_CHUNKS; ++k) top = fmaxf(top, C::largest(cur[k]));
 
-            // the sum, against the thread's own running maximum
-            if (top > m) {
+            // the sum, against the thread's first maximum, or one that stands far above it
+            if (top > m + 40.0f) {
                 sum *= ex2((m - top) * LOG2E);
                 m = top;
             }
@@ -470,47 +508,39 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
 
             if (l0 == 0) {
                 if (tid == 0) s.total = 0;
-                bound = nth_of_block(top, p.n_best, s.sorted, &s.bound);
+                bound = low_bound(top, p.n_best, min(BM_WARPS, (span + 32 * E - 1) / (32 * E)), s.first);
             }
             const auto taken = [&](float v, unsigned t) { return v > -INFINITY && (v > bound || (v == bound && t <= bound_token)); };
-            bool some = l0 == 0 || l0 + BATCH >= span;
             if (top >= bound && top > -INFINITY) {
-                some = true;
-                // few come here, so the code is short rather than unrolled
-#pragma unroll 1
-                for (int k = 0; k < BM_CHUNKS; ++k) {
-                    float c_top = tops[0];
-#pragma unroll
-                    for (int i = 1; i < BM_CHUNKS; ++i) c_top = i == k ? tops[i] : c_top;
-                    if (!(c_top >= bound)) continue;
-                    const uint4 c = pick(cur, k);
-                    unsigned hits = 0;
-#pragma unroll
-                    for (int i = 0; i < E; ++i) hits |= C::at(c, i) >= bound ? 1u << i : 0;
-                    for (; hits; hits &= hits - 1) {
-                        const int i = __ffs(hits) - 1;
-                        const float v = C::any(c, i);
-                        const unsigned t = static_cast<unsigned>(t0 + l0 + (k * BM_THREADS + tid) * E + i);
-                        if (taken(v, t)) {
-                            const int at = atomicAdd(&s.total, 1);
-                            if (at < BM_LIST) s.list[at] = key_of(v, t);
-                        }
+                for (unsigned bits = C::reach(cur, bound); bits; bits &= bits - 1) {
+                    const int2 at = C::place(__ffs(bits) - 1);
+                    const uint4 c = pick(cur, at.x);
+                    const int w = C::word(at.y);
+                    const float v = C::value(w == 0 ? c.x : w == 1 ? c.y : w == 2 ? c.z : c.w, at.y);
+                    const unsigned t = static_cast<unsigned>(t0 + l0 + (at.x * BM_THREADS + tid) * E + at.y);
+                    if (taken(v, t)) {
+                        const int i = atomicAdd(&s.total, 1);
+                        if (i < BM_LIST) s.list[i] = key_of(v, t);
                     }
                 }
             }
-            if (!__syncthreads_or(some)) continue;
+            // the list is looked at after the first two batches, every fourth, and the last
+            const int no = l0 / BATCH;
+            const bool first = no == 0, end = l0 + BATCH >= span;
+            if (!(no < 2 || end || (no & 3) == 3)) continue;
+            __syncthreads();
             int total = s.total;
             const bool over = total > BM_LIST;
             if (over) {
-                // this batch again, one at a time: the largest key below the last
+                // all since the last look again, one at a time: the largest key below the last
                 Key last = ~0ull;
                 int found = 0;
                 for (; found < p.n_best; ++found) {
                     Key key = 0;
 #pragma unroll 1
-                    for (int k = 0; k < BM_CHUNKS; ++k) {
-                        const uint4 c = pick(cur, k);
-                        const unsigned t = static_cast<unsigned>(t0 + l0 + (k * BM_THREADS + tid) * E);
+                    for (int l = since + tid * E; l < l0 + BATCH; l += BM_THREADS * E) {
+                        const uint4 c = fetch(l);
+                        const unsigned t = static_cast<unsigned>(t0 + l);
 #pragma unroll
                         for (int i = 0; i < E; ++i) {
                             const float v = C::at(c, i);
@@ -524,7 +554,7 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
                 }
                 total = kept + found;
             }
-            if (total > have + BM_FULL || l0 == 0 || l0 + BATCH >= span || over) {
+            if (total > have + BM_FULL || first || end || over) {
                 rank_keys<BM_THREADS, BM_LIST / BM_THREADS>(s.list, total, p.n_best, tid, [] { __syncthreads(); });
                 total = have = min(total, p.n_best);
                 if (tid == 0) s.total = have;
@@ -534,6 +564,7 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
                 }
             }
             kept = total;
+            since = l0 + BATCH;
             __syncthreads();
         }
 
@@ -560,17 +591,16 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
 
     // the last of the group's blocks joins them
     const int gi = static_cast<int>(r / p.beams);
-    __threadfence();
     __syncthreads();
     if (tid == 0) {
         const unsigned blocks = static_cast<unsigned>(p.beams) * static_cast<unsigned>(p.slices);
+        __threadfence();
         s.last = atomicAdd(&p.cnt[gi], 1u) + 1 == blocks;
         if (s.last) p.cnt[gi] = 0;
+        __threadfence();
     }
     __syncthreads();
-    if (!s.last) return;
-    __threadfence();
-    join(p, gi, s);
+    if (s.last) join(p, gi, s);
 }
 
 template <typename T>
@@ -588,7 +618,7 @@ int beam_slices(long long rows, long long vocab)
 {
     constexpr long long SLOTS = BM_BLOCKS * ATTN_SMS;
     long long best = 1, best_cost = INT64_MAX;
-    for (long long n = 1; n <= 64 && (n == 1 || vocab / n >= 2048); ++n) {
+    for (long long n = 1; n <= BM_SLICES && (n == 1 || vocab / n >= 2048); ++n) {
         const long long cost = (rows * n + SLOTS - 1) / SLOTS * (vocab / n + 8192) + 64 * n;
         if (cost < best_cost) best_cost = cost, best = n;
     }
