@@ -323,13 +323,16 @@ qgemv_status qgemv_kv8_append(const void *k, const void *v, qgemv_dtype in_type,
                 if (overlap(in, out)) return QGEMV_ERR_INVALID_ARG;
     const int most = static_cast<int>(std::min<long long>(std::min<long long>(max_new, n_tokens), b.max_len));
     if (n_tokens == 0 || max_new == 0) return QGEMV_OK;
+    if (n_tokens == 1) k_stride = v_stride = 0;
+    if (k_stride > INT32_MAX || v_stride > INT32_MAX || cache->row_stride > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
 
     Kv8AppendParams p = {};
     p.c = layout_of(cache);
     p.k = k;
     p.v = v;
-    p.k_stride = k_stride;
-    p.v_stride = v_stride;
+    p.k_stride = static_cast<int>(k_stride);
+    p.v_stride = static_cast<int>(v_stride);
+    p.code_row = static_cast<int>(cache->row_stride);
     p.n_tokens = n_tokens;
     p.first = first;
     p.lens = b.lens;

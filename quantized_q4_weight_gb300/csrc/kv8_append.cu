@@ -5,13 +5,17 @@
 // x, s the scale of the rows it held before (0 without any); codes of the new rows
 // rn(x * (1 / s')), and, where s' > s, old codes c become rn(c * (s * (1 / s'))).
 //
-// A thread block takes one block of one head, so nobody else touches the codes and
-// the scale that it reads and writes anew, and no atomics are needed.  The new rows
+// A thread block takes a block of one head after the other, so nobody else touches the
+// codes and the scale that it reads and writes anew, and no atomics are needed.  The new rows
 // stay in registers between the maximum and the codes (up to NR pieces of eight
 // elements a thread; more are read a second time, from L2).
 //
 // What bounds it: memory for prompts (rows read once, a code written for each
 // element), for single tokens the chain of dependent loads: lengths, page, row, scale.
+#include <float.h>
+
+#include <type_traits>
+
 #include "kv8_ops.h"
 #include "qgemv_internal.cuh"
 
@@ -59,16 +63,54 @@ __device__ __forceinline__ Eight<T> load8(const T *x)
     return v;
 }
 
+// The largest |x| of eight, as the bits of a non-negative number of the type, which order
+// as the numbers do; NaN lies above infinity.
+__device__ __forceinline__ unsigned largest_bits(const Eight<float> &v, unsigned top)
+{
+    const unsigned u[8] = {v.w[0].x, v.w[0].y, v.w[0].z, v.w[0].w, v.w[1].x, v.w[1].y, v.w[1].z, v.w[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, u[i] & 0x7FFFFFFFu);
+    return top;
+}
+template <typename T>
+__device__ __forceinline__ unsigned largest_bits(const Eight<T> &v, unsigned top)  // in both halves of `top`
+{
+    const unsigned u[4] = {v.w[0].x, v.w[0].y, v.w[0].z, v.w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, u[i] & 0x7FFF7FFFu);
+    return top;
+}
+template <typename T>
+__device__ __forceinline__ float from_bits(unsigned top);
+template <>
+__device__ __forceinline__ float from_bits<float>(unsigned top)
+{
+    return __uint_as_float(top);
+}
+template <>
+__device__ __forceinline__ float from_bits<__half>(unsigned top)
+{
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(max(top & 0xFFFFu, top >> 16))));
+}
+template <>
+__device__ __forceinline__ float from_bits<__nv_bfloat16>(unsigned top)
+{
+    return __uint_as_float(max(top & 0xFFFFu, top >> 16) << 16);
+}
+
 template <int CODE>
 constexpr float KA_TOP = CODE == QGEMV_CODE_INT8 ? 127.0f : 448.0f;
 
-// Four values (already over their scale) as codes; NaN as 0.
-template <int CODE>
+// Four values (already over their scale) as codes.  CAREFUL: NaN as 0, values beyond
+// the codes as the last one; without it they are neither NaN nor above KA_TOP by more than a
+// rounding.
+template <int CODE, bool CAREFUL>
 __device__ __forceinline__ unsigned encode4(const float *f)
 {
     float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = f[i] == f[i] ? fminf(fmaxf(f[i], -KA_TOP<CODE>), KA_TOP<CODE>) : 0.0f;
+    for (int i = 0; i < 4; ++i)
+        v[i] = !CAREFUL ? f[i] : f[i] == f[i] ? fminf(fmaxf(f[i], -KA_TOP<CODE>), KA_TOP<CODE>) : 0.0f;
     if constexpr (CODE == QGEMV_CODE_INT8) {
         // 1.5 * 2^23 + v ends, rounded to nearest even, in v as two's complement
         unsigned u[4];
@@ -100,17 +142,16 @@ __device__ __forceinline__ void decode4(unsigned w, float *f)
 }
 
 // Block x: sequence x / blocks, its (x % blocks)-th block with new rows; block y:
-// head y / 2, k or v.
-template <typename T, int CODE, bool VEC, int THREADS>
+// `items` of the heads of k and v (item 2 h is head h's k, 2 h + 1 its v), one
+// after the other, the next one's rows on their way meanwhile.
+template <typename T, int CODE, bool VEC, int THREADS, bool MANY>
 __global__ void __launch_bounds__(THREADS) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p)
 {
-    __shared__ float s_top[THREADS / 32];
+    __shared__ unsigned s_top[2][THREADS / 32];
     const int tid = threadIdx.x;
     pdl_launch_dependents();
     pdl_wait();
     const int b = blockIdx.x / p.blocks, jb = blockIdx.x % p.blocks;
-    const int h = blockIdx.y >> 1;
-    const bool is_v = blockIdx.y & 1;
     const int len = __ldg(p.lens + b);
     const long long t0 = p.first ? __ldg(p.first + b) : static_cast<long long>(b) * p.n_new;
     const long long t1 = p.first ? __ldg(p.first + b + 1) : t0 + p.n_new;
@@ -132,76 +173,150 @@ __global__ void __launch_bounds__(THREADS) kv8_append_kernel(const __grid_consta
         return;
     }
     const int in_page = start & ((1 << p.c.page_shift) - 1);
-    uint8_t *codes = (is_v ? p.c.v : p.c.k) + page * p.c.page_stride + in_page * p.c.row_stride + h * p.c.head_stride;
-    float *scale = (is_v ? p.c.vs : p.c.ks) + page * p.c.scale_page + (in_page >> p.c.block_shift) * p.c.scale_block +
-                   h * p.c.scale_head;
-    const long long stride = is_v ? p.v_stride : p.k_stride;
-    const T *x = static_cast<const T *>(is_v ? p.v : p.k) + (t0 + (lo - old)) * stride + static_cast<long long>(h) * p.d;
-    const float was = old > start ? *scale : 0.0f;
-
+    const long long code_at = page * p.c.page_stride + in_page * p.c.row_stride;
+    const long long scale_at = page * p.c.scale_page + (in_page >> p.c.block_shift) * p.c.scale_block;
+    const long long token = t0 + (lo - old);
     const int total = (hi - lo) * p.pieces;
-    Eight<T> held[KA_PIECES];
-    float top = 0.0f;
-    auto largest = [&](const Eight<T> &v) {
-        float f[8];
-        spread(v, f);
+    // the thread's first pieces, the same of every head
+    int row[KA_PIECES], col[KA_PIECES];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));  // passes NaN over
-    };
-    auto at = [&](int i) { return x + i / p.pieces * stride + i % p.pieces * 8; };
-#pragma unroll
-    for (int u = 0; u < KA_PIECES; ++u)
-        if (tid + u * THREADS < total) held[u] = load8<T, VEC>(at(tid + u * THREADS));
-#pragma unroll
-    for (int u = 0; u < KA_PIECES; ++u)
-        if (tid + u * THREADS < total) largest(held[u]);
-    for (int i = tid + KA_PIECES * THREADS; i < total; i += THREADS) largest(load8<T, VEC>(at(i)));
-    // non-negative floats order as their bits do
-    top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
-    if ((tid & 31) == 0) s_top[tid >> 5] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) top = fmaxf(top, s_top[w]);
+    for (int u = 0; u < KA_PIECES; ++u) {
+        const int i = tid + u * THREADS;  // below 1024, and a row has 32 pieces at most: the product's top is the quotient
+        row[u] = i * p.per_piece >> 16, col[u] = (i - row[u] * p.pieces) * 8;
+    }
 
-    const float now = fmaxf(was, __fdiv_rn(top, KA_TOP<CODE>));
-    const float inv = now > 0.0f ? __fdiv_rn(1.0f, now) : 0.0f;
-    auto write = [&](const Eight<T> &v, int i) {
-        float f[8];
-        spread(v, f);
+    const T *xk = static_cast<const T *>(p.k) + token * p.k_stride, *xv = static_cast<const T *>(p.v) + token * p.v_stride;
+    Eight<T> next[KA_PIECES];
+    float next_was = 0.0f;
+    auto fetch = [&](int item) {
+        const T *x = (item & 1 ? xv : xk) + static_cast<long long>(item >> 1) * p.d;
+        const int stride = item & 1 ? p.v_stride : p.k_stride;
+        if (old > start) next_was = __ldcg((item & 1 ? p.c.vs : p.c.ks) + scale_at + (item >> 1) * p.c.scale_head);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], inv);
-        *reinterpret_cast<uint2 *>(codes + (lo - start + i / p.pieces) * p.c.row_stride + i % p.pieces * 8) =
-            make_uint2(encode4<CODE>(f), encode4<CODE>(f + 4));
+        for (int u = 0; u < KA_PIECES; ++u)
+            if (tid + u * THREADS < total) next[u] = load8<T, VEC>(x + static_cast<long long>(row[u]) * stride + col[u]);
     };
+    const int item0 = MANY ? blockIdx.y * p.items : blockIdx.y, item1 = MANY ? min(item0 + p.items, 2 * p.hkv) : item0 + 1;
+    fetch(item0);
+    for (int item = item0; item < item1; ++item) {
+        const bool is_v = item & 1;
+        const int h = item >> 1;
+        uint8_t *codes = (is_v ? p.c.v : p.c.k) + code_at + h * p.c.head_stride;
+        float *scale = (is_v ? p.c.vs : p.c.ks) + scale_at + h * p.c.scale_head;
+        const int stride = is_v ? p.v_stride : p.k_stride;
+        const T *x = (is_v ? xv : xk) + static_cast<long long>(h) * p.d;
+        Eight<T> held[KA_PIECES];
 #pragma unroll
-    for (int u = 0; u < KA_PIECES; ++u)
-        if (tid + u * THREADS < total) write(held[u], tid + u * THREADS);
-    for (int i = tid + KA_PIECES * THREADS; i < total; i += THREADS) write(load8<T, VEC>(at(i)), i);
-    if (now > was || old <= start) {
-        if (old > start) {  // old codes to the new scale
+        for (int u = 0; u < KA_PIECES; ++u) held[u] = next[u];
+        const float was = next_was;
+        bool odd = false;  // values or scales that the codes' conversion has to look at
+        if (MANY && item + 1 < item1) fetch(item + 1);
+
+        // pieces beyond those that registers hold
+        auto rest = [&](auto f) {
+            for (int i = tid + KA_PIECES * THREADS; i < total; i += THREADS) {
+                const int r = i / p.pieces, c = (i - r * p.pieces) * 8;
+                f(load8<T, VEC>(x + static_cast<long long>(r) * stride + c), r, c);
+            }
+        };
+        // the largest of the block's values; one above infinity's bits tells of a NaN
+        float top;
+        auto all = [&](unsigned bits) {
+            const float mine = from_bits<T>(bits);
+            const unsigned u = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mine));
+            if ((tid & 31) == 0) s_top[item & 1][tid >> 5] = u;
+            __syncthreads();
+            unsigned most = 0;
+#pragma unroll
+            for (int w = 0; w < THREADS / 32; ++w) most = max(most, s_top[item & 1][w]);
+            top = __uint_as_float(most);
+        };
+        unsigned bits = 0;
+#pragma unroll
+        for (int u = 0; u < KA_PIECES; ++u)
+            if (tid + u * THREADS < total) bits = largest_bits(held[u], bits);
+        rest([&](const Eight<T> &v, int, int) { bits = largest_bits(v, bits); });
+        all(bits);
+        if (!(top <= FLT_MAX)) {  // infinities stay, NaN is passed over
+            float most = 0.0f;
+            auto pass = [&](const Eight<T> &v) {
+                float f[8];
+                spread(v, f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(f[i]));
+            };
+#pragma unroll
+            for (int u = 0; u < KA_PIECES; ++u)
+                if (tid + u * THREADS < total) pass(held[u]);
+            rest([&](const Eight<T> &v, int, int) { pass(v); });
+            const unsigned u = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
+            __syncthreads();
+            if ((tid & 31) == 0) s_top[item & 1][tid >> 5] = u;
+            __syncthreads();
+            unsigned w_most = 0;
+#pragma unroll
+            for (int w = 0; w < THREADS / 32; ++w) w_most = max(w_most, s_top[item & 1][w]);
+            odd = true;
+            top = __uint_as_float(w_most);
+        }
+
+        const float now = fmaxf(was, __fdiv_rn(top, KA_TOP<CODE>));
+        const float inv = now > 0.0f ? __fdiv_rn(1.0f, now) : 0.0f;
+        // scales that are subnormal, infinite or no number
+        if (!(now >= FLT_MIN && now <= FLT_MAX)) odd = true;
+        auto write = [&](const Eight<T> &v, int r, int c, auto careful) {
+            float f[8];
+            spread(v, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], inv);
+            *reinterpret_cast<uint2 *>(codes + (lo - start + r) * static_cast<long long>(p.code_row) + c) =
+                make_uint2(encode4<CODE, careful.value>(f), encode4<CODE, careful.value>(f + 4));
+        };
+        if (!odd) {
+#pragma unroll
+            for (int u = 0; u < KA_PIECES; ++u)
+                if (tid + u * THREADS < total) write(held[u], row[u], col[u], std::false_type());
+        } else {
+#pragma unroll
+            for (int u = 0; u < KA_PIECES; ++u)
+                if (tid + u * THREADS < total) write(held[u], row[u], col[u], std::true_type());
+        }
+        rest([&](const Eight<T> &v, int r, int c) { write(v, r, c, std::true_type()); });
+        if (old <= start) {
+            if (tid == 0) *scale = now;
+        } else if (now > was) {  // old codes to the new scale
             const float by = __fmul_rn(was, inv);
             for (int i = tid; i < (old - start) * p.pieces; i += THREADS) {
-                uint2 *c = reinterpret_cast<uint2 *>(codes + i / p.pieces * p.c.row_stride + i % p.pieces * 8);
+                const int r = i / p.pieces;
+                uint2 *c = reinterpret_cast<uint2 *>(codes + r * p.c.row_stride + (i - r * p.pieces) * 8);
                 const uint2 w = *c;
                 float f[8];
                 decode4<CODE>(w.x, f);
                 decode4<CODE>(w.y, f + 4);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], by);
-                *c = make_uint2(encode4<CODE>(f), encode4<CODE>(f + 4));
+                *c = make_uint2(encode4<CODE, true>(f), encode4<CODE, true>(f + 4));
             }
+            if (tid == 0) *scale = now;  // every thread has read it: a barrier lies between
         }
-        if (tid == 0) *scale = now;  // every thread has read it: a barrier lies between
     }
 }
 
 template <typename T, int CODE, bool VEC>
-cudaError_t launch_t(const Kv8AppendParams &p, cudaStream_t st)
+cudaError_t launch_t(Kv8AppendParams p, cudaStream_t st)
 {
-    const dim3 grid(static_cast<unsigned>(p.n_seqs) * static_cast<unsigned>(p.blocks), 2 * static_cast<unsigned>(p.hkv));
-    const int rows = min(1 << p.c.block_shift, p.max_new);
-    return rows * p.pieces > 128 * KA_PIECES ? launch_pdl(kv8_append_kernel<T, CODE, VEC, 256>, grid, 256, 0, st, p)
-                                             : launch_pdl(kv8_append_kernel<T, CODE, VEC, 128>, grid, 128, 0, st, p);
+    const long long blocks = static_cast<long long>(p.n_seqs) * p.blocks;
+    // Items one after the other pay once there are some blocks for each multiprocessor.
+    p.items = 1;
+    p.per_piece = (65536 + p.pieces - 1) / p.pieces;
+    while (p.items < 8 && blocks * 2 * p.hkv >= 16ll * ATTN_SMS * p.items && p.items < 2 * p.hkv) p.items *= 2;
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((2 * p.hkv + p.items - 1) / p.items));
+    const bool wide = min(1 << p.c.block_shift, p.max_new) * p.pieces > 128 * KA_PIECES;
+    const auto go = [&](auto kernel, unsigned threads) { return launch_pdl(kernel, grid, threads, 0, st, p); };
+    // one item a block: no second set of rows in registers, and twice the blocks a multiprocessor
+    if (p.items == 1)
+        return wide ? go(kv8_append_kernel<T, CODE, VEC, 256, false>, 256) : go(kv8_append_kernel<T, CODE, VEC, 128, false>, 128);
+    return wide ? go(kv8_append_kernel<T, CODE, VEC, 256, true>, 256) : go(kv8_append_kernel<T, CODE, VEC, 128, true>, 128);
 }
 template <typename T>
 cudaError_t launch_in(const Kv8AppendParams &p, qgemv_code_type code, bool vec, cudaStream_t st)

@@ -35,13 +35,15 @@ struct Kv8Layout {
 struct Kv8AppendParams {
     Kv8Layout c;
     const void *k, *v;
-    long long k_stride, v_stride;
+    int k_stride, v_stride, code_row;     // elements between tokens, bytes between a page's rows
     long long n_tokens;
     const int32_t *first, *lens, *pages;
     long long pages_stride;
     int n_new, max_new, max_len, blocks;  // n_new: without `first`; blocks: that max_new rows can touch
     int n_seqs, hkv, d;
     int pieces;                           // threads' pieces of 8 elements a row: d / 8
+    int per_piece;                        // 65536 / pieces, rounded up
+    int items;                            // heads of k and v that a block takes (kv8_append.cu)
     unsigned *status;
 };
 cudaError_t launch_kv8_append(const Kv8AppendParams &p, qgemv_dtype in, qgemv_code_type code, bool vec, cudaStream_t st);

@@ -31,8 +31,11 @@ __device__ __forceinline__ long long k_row(const RopeParams &r, long long t)
     return r.slots ? cache_row(r, t) : t * r.row_stride;
 }
 
-// Eight elements of a head a thread (rope_kv.cu: which eight); a head is
-// `lanes` threads, a power of two, those beyond its units idle.
+// Eight elements of a head a thread (rope_kv.cu: which eight) as four pairs; a head is
+// `lanes` threads, a power of two, those beyond its units idle.  With r = 1 / sqrt(mean
+// x^2 + eps) a pair becomes r (x wx c - y wy s), r (x wx s + y wy c): the products of
+// weights and sines are formed once for the q heads and once for the k heads of a
+// thread (elements that do not rotate: c = 1, s = 0).
 template <typename TI, typename TQ, typename TC, bool HALF>
 __global__ void __launch_bounds__(NR_THREADS, 8) norm_rope_vec_kernel(const __grid_constant__ NormRopeParams p, int lanes)
 {
@@ -50,8 +53,11 @@ __global__ void __launch_bounds__(NR_THREADS, 8) norm_rope_vec_kernel(const __gr
     pdl_wait();
     const int pos = __ldg(r.pos + t);
     const long long row_off = r.hkv ? k_row(r, t) : -1;
+    const TI *q_at = static_cast<const TI *>(r.q) + t * r.q_stride, *k_at = static_cast<const TI *>(r.k) + t * r.k_stride;
+    const TI *v_at = static_cast<const TI *>(r.v) + t * r.v_stride;
     const float per = 1.0f / static_cast<float>(r.d);
-    float c[4], s[4];
+    float xc[4], ys[4], xs[4], yc[4];  // wx c, wy s, wx s, wy c
+    const float *formed = nullptr;     // of these weights
     bool have = false;
     const int step = at_once * static_cast<int>(gridDim.y);
     // all threads of the block take the same turns: shuffles and a barrier lie in them
@@ -61,19 +67,13 @@ __global__ void __launch_bounds__(NR_THREADS, 8) norm_rope_vec_kernel(const __gr
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             const int h = base + hb + u * step;
-            const TI *src = mine && h < heads ? head_src<TI>(r, t, h, row_off >= 0) : nullptr;
-            there[u] = src != nullptr;
-            if (src) load8<TI, HALF>(src, a, b, x[u], y[u]);
+            there[u] = mine && h < heads && (h < r.hq || row_off >= 0);
+            const TI *src = h < r.hq ? q_at + h * r.d : h < normed ? k_at + (h - r.hq) * r.d : v_at + (h - normed) * r.d;
+            if (there[u]) load8<TI, HALF>(src, a, b, x[u], y[u]);
         }
         if (!have) {
             for (int i = threadIdx.x; i < r.rot / 2; i += NR_THREADS) angle(pos, r.turns[i], r.mscale, s_c[i], s_s[i]);
             __syncthreads();
-            if (rot_unit) {
-                const float4 cc = *reinterpret_cast<const float4 *>(s_c + 4 * j);
-                const float4 ss = *reinterpret_cast<const float4 *>(s_s + 4 * j);
-                c[0] = cc.x, c[1] = cc.y, c[2] = cc.z, c[3] = cc.w;
-                s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
-            }
             have = true;
         }
 #pragma unroll
@@ -87,35 +87,36 @@ __global__ void __launch_bounds__(NR_THREADS, 8) norm_rope_vec_kernel(const __gr
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum = fmaf(fx[i], fx[i], fmaf(fy[i], fy[i], sum));
-            for (int o = lanes >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                if (o < lanes) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
             if (!there[u]) continue;
             if (h < normed) {
-                const float by = rsqrtf(fmaf(sum, per, p.eps));
                 const float *w = h < r.hq ? p.q_weight : p.k_weight;
+                if (w != formed) {
+                    formed = w;
+                    float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, s[4] = {};
+                    if (rot_unit) {
+                        const float4 cc = *reinterpret_cast<const float4 *>(s_c + 4 * j);
+                        const float4 ss = *reinterpret_cast<const float4 *>(s_s + 4 * j);
+                        c[0] = cc.x, c[1] = cc.y, c[2] = cc.z, c[3] = cc.w;
+                        s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float wx = __ldg(w + (HALF ? a + i : 8 * j + 2 * i)), wy = __ldg(w + (HALF ? b + i : 8 * j + 2 * i + 1));
+                        xc[i] = wx * c[i], ys[i] = wy * s[i], xs[i] = wx * s[i], yc[i] = wy * c[i];
+                    }
+                }
+                const float by = rsqrtf(fmaf(sum, per, p.eps));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    fx[i] *= by * __ldg(w + a + i);
-                    fy[i] *= by * __ldg(w + b + i);
-                }
-                if (rot_unit) {
-                    if constexpr (HALF) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float px = fx[i], py = fy[i];
-                            fx[i] = px * c[i] - py * s[i];
-                            fy[i] = px * s[i] + py * c[i];
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float px = fx[2 * i], py = fx[2 * i + 1];
-                            fx[2 * i] = px * c[i] - py * s[i];
-                            fx[2 * i + 1] = px * s[i] + py * c[i];
-                            const float qx = fy[2 * i], qy = fy[2 * i + 1];
-                            fy[2 * i] = qx * c[i + 2] - qy * s[i + 2];
-                            fy[2 * i + 1] = qx * s[i + 2] + qy * c[i + 2];
-                        }
-                    }
+                    // pair i: (fx[i], fy[i]), interleaved two neighbours
+                    float &u0 = HALF ? fx[i] : i < 2 ? fx[2 * i & 3] : fy[2 * i & 3];
+                    float &u1 = HALF ? fy[i] : i < 2 ? fx[(2 * i + 1) & 3] : fy[(2 * i + 1) & 3];
+                    const float px = u0 * by, py = u1 * by;
+                    u0 = px * xc[i] - py * ys[i];
+                    u1 = px * xs[i] + py * yc[i];
                 }
             }
             if (h < r.hq)
