@@ -19,10 +19,15 @@
 namespace qg {
 namespace {
 
-constexpr int NR_THREADS = 128;
-// Heads in flight per thread: 64 bytes of loads, whatever the type.
-template <typename T>
-constexpr int NR_UNROLL = sizeof(T) == 4 ? 2 : 4;
+// MANY tokens: blocks of 64 threads, 96 bytes of loads in flight for each.  16381 of
+// 32 + 8 + 8 heads of 128, fp32: 96 us; with 128 threads 102, and 106 with 64 bytes in
+// flight (three quarters as many multiprocessor's threads 111).  Few tokens: 128 threads and
+// 64 bytes, 2.7 us instead of 3.0 for eight tokens.
+template <bool MANY>
+constexpr int NR_THREADS = MANY ? 64 : 128;
+template <typename T, bool MANY>
+constexpr int NR_UNROLL = sizeof(T) == 4 ? (MANY ? 3 : 2) : 4;  // heads (six of 16 bits do not fit the registers)
+constexpr int NR_ANY = 128;  // threads of the element-wise kernel
 
 // Where token t's k goes, in elements from r.ck (and its v from r.cv): its cache
 // row, -1 for none; without a cache, its place in k_out.
@@ -36,15 +41,15 @@ __device__ __forceinline__ long long k_row(const RopeParams &r, long long t)
 // x^2 + eps) a pair becomes r (x wx c - y wy s), r (x wx s + y wy c): the products of
 // weights and sines are formed once for the q heads and once for the k heads of a
 // thread (elements that do not rotate: c = 1, s = 0).
-template <typename TI, typename TQ, typename TC, bool HALF>
-__global__ void __launch_bounds__(NR_THREADS, 8) norm_rope_vec_kernel(const __grid_constant__ NormRopeParams p, int lanes)
+template <typename TI, typename TQ, typename TC, bool HALF, bool MANY>
+__global__ void __launch_bounds__(NR_THREADS<MANY>, MANY ? 16 : 8) norm_rope_vec_kernel(const __grid_constant__ NormRopeParams p, int lanes)
 {
     __shared__ __align__(16) float s_c[128], s_s[128];
-    constexpr int UNROLL = NR_UNROLL<TI>;
+    constexpr int UNROLL = NR_UNROLL<TI, MANY>;
     const RopeParams &r = p.r;
     pdl_launch_dependents();
     const int j = static_cast<int>(threadIdx.x) & (lanes - 1), hb = static_cast<int>(threadIdx.x) / lanes;
-    const int at_once = NR_THREADS / lanes;
+    const int at_once = NR_THREADS<MANY> / lanes;
     const long long t = blockIdx.x;
     const int normed = r.hq + r.hkv, heads = normed + p.v_heads;
     const bool mine = 8 * j < r.d, rot_unit = 8 * j < r.rot;
@@ -67,12 +72,18 @@ __global__ void __launch_bounds__(NR_THREADS, 8) norm_rope_vec_kernel(const __gr
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             const int h = base + hb + u * step;
-            there[u] = mine && h < heads && (h < r.hq || row_off >= 0);
-            const TI *src = h < r.hq ? q_at + h * r.d : h < normed ? k_at + (h - r.hq) * r.d : v_at + (h - normed) * r.d;
-            if (there[u]) load8<TI, HALF>(src, a, b, x[u], y[u]);
+            there[u] = false;
+            if (!mine) continue;
+            if (h < r.hq) {  // not behind the slot's load
+                load8<TI, HALF>(q_at + h * r.d, a, b, x[u], y[u]);
+                there[u] = true;
+            } else if (h < heads && row_off >= 0) {
+                load8<TI, HALF>(h < normed ? k_at + (h - r.hq) * r.d : v_at + (h - normed) * r.d, a, b, x[u], y[u]);
+                there[u] = true;
+            }
         }
         if (!have) {
-            for (int i = threadIdx.x; i < r.rot / 2; i += NR_THREADS) angle(pos, r.turns[i], r.mscale, s_c[i], s_s[i]);
+            for (int i = threadIdx.x; i < r.rot / 2; i += NR_THREADS<MANY>) angle(pos, r.turns[i], r.mscale, s_c[i], s_s[i]);
             __syncthreads();
             have = true;
         }
@@ -129,17 +140,17 @@ __global__ void __launch_bounds__(NR_THREADS, 8) norm_rope_vec_kernel(const __gr
 
 // A warp a head, element by element: any alignment and even sizes up to 256.
 template <typename TI, typename TQ, typename TC, bool HALF>
-__global__ void __launch_bounds__(NR_THREADS) norm_rope_any_kernel(const __grid_constant__ NormRopeParams p)
+__global__ void __launch_bounds__(NR_ANY) norm_rope_any_kernel(const __grid_constant__ NormRopeParams p)
 {
     const RopeParams &r = p.r;
     pdl_launch_dependents();
     pdl_wait();
     const long long t = blockIdx.x;
-    const int lane = threadIdx.x & 31, warps = NR_THREADS / 32 * static_cast<int>(gridDim.y);
+    const int lane = threadIdx.x & 31, warps = NR_ANY / 32 * static_cast<int>(gridDim.y);
     const int normed = r.hq + r.hkv, heads = normed + p.v_heads, pairs = r.d >> 1, rpairs = r.rot >> 1;
     const long long row_off = r.hkv ? k_row(r, t) : -1;
     const int pos = __ldg(r.pos + t);
-    for (int h = static_cast<int>(blockIdx.y * (NR_THREADS / 32) + threadIdx.x / 32); h < heads; h += warps) {
+    for (int h = static_cast<int>(blockIdx.y * (NR_ANY / 32) + threadIdx.x / 32); h < heads; h += warps) {
         const TI *src = head_src<TI>(r, t, h, row_off >= 0);
         if (!src) continue;  // the whole warp
         float x[4] = {}, y[4] = {}, sum = 0.0f;
@@ -195,11 +206,14 @@ cudaError_t launch4(NormRopeParams &p, bool vec, long long n, int sms, cudaStrea
     int lanes = 32;
     if (vec)
         while (lanes > 1 && (lanes >> 1) * 8 >= p.r.d) lanes >>= 1;
-    const int at_once = NR_THREADS / lanes, chunks = (heads + at_once - 1) / at_once;
+    if (vec && n >= 10ll * sms)
+        return launch_pdl(norm_rope_vec_kernel<TI, TQ, TC, HALF, true>, dim3(nx), NR_THREADS<true>, 0, st, p, lanes);
+    const int at_once = NR_ANY / lanes, chunks = (heads + at_once - 1) / at_once;
     // blocks that share a token repeat its sines; they pay while the tokens alone leave multiprocessors idle
     const unsigned ny = static_cast<unsigned>(n * chunks <= 2ll * sms ? chunks : 1);
-    if (vec) return launch_pdl(norm_rope_vec_kernel<TI, TQ, TC, HALF>, dim3(nx, ny), NR_THREADS, 0, st, p, lanes);
-    return launch_pdl(norm_rope_any_kernel<TI, TQ, TC, HALF>, dim3(nx, ny), NR_THREADS, 0, st, p);
+    if (vec)
+        return launch_pdl(norm_rope_vec_kernel<TI, TQ, TC, HALF, false>, dim3(nx, ny), NR_THREADS<false>, 0, st, p, lanes);
+    return launch_pdl(norm_rope_any_kernel<TI, TQ, TC, HALF>, dim3(nx, ny), NR_ANY, 0, st, p);
 }
 
 template <typename TI, typename TQ, typename TC>
