@@ -10,9 +10,9 @@
 // operand of the product with d_j, with m a running reference near the largest
 // s_j + log2 vs_j of the row, and l sums w_j / vs_j in fp32.  So a row's largest
 // contribution has the operand's full precision however the scales differ.
-// m is raised only when a weight would pass 2^14 (it is then put 2^10 below the
-// largest): after the first tiles almost never, which saves the shuffles of a
-// maximum and the scaling of the sums for each tile.
+// m is set by the first visible keys, 2^10 below their largest, and raised only when
+// a weight would pass 2^14: after the first tiles almost never, which saves the
+// shuffles of a maximum and the scaling of the sums for each tile.
 //
 // The products are transposed: scores = K Q^T and sums = V^T P^T, keys or
 // elements of a head on the 16 rows of mma.sync, the few query rows of a cache head
@@ -130,6 +130,14 @@ __device__ __forceinline__ void mma(float (&d)[4], unsigned a0, unsigned a1, uns
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same from sums of zero.
+__device__ __forceinline__ void mma0(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0, unsigned b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ unsigned movm(unsigned a)
 {
@@ -482,23 +490,24 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
 #pragma unroll
                 for (int c = 0; c < C::KC; ++c) load_q(j, c, qf[j][c]);
         }
-        // per thread: rows 8 j + 2 t + e
-        float qs[NT][2], m[NT][2], l[NT][2], o[NT][C::MT][4];
+        // per thread, rows 8 j + 2 t and + 1: factor, minus the reference (0, and a bit of `unset`,
+        // before the first visible key), sum of the weights over their scales, sums of v
+        float2 qs[NT], nm[NT], l[NT];
+        float o[NT][C::MT][4];
+        unsigned unset = (1u << 2 * NT) - 1;
+        bool fresh = true;  // a row of the warp is unset
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                qs[j][e] = s_qs[8 * j + 2 * t + e];
-                m[j][e] = K8_NEG, l[j][e] = 0.0f;
-            }
+            qs[j] = *reinterpret_cast<const float2 *>(s_qs + 8 * j + 2 * t);
+            nm[j] = l[j] = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < C::MT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[j][i][e] = 0.0f;
         }
 
-        // The references that a tile with exponents s (-infinity: not seen) asks for.
-        auto raise = [&](const float (&s)[C::XN][NT][4]) {
+        // The references that a tile with exponents s, relative to them (-infinity: not seen), asks for.
+        auto raise = [&](float (&s)[C::XN][NT][4]) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -507,14 +516,19 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                     if (C::XN == 2) mx = fmaxf(mx, fmaxf(s[C::XN - 1][j][e], s[C::XN - 1][j][2 + e]));
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-                    if (mx - m[j][e] > K8_SLACK) {
-                        const float mn = mx - K8_LIFT, by = ex2(m[j][e] - mn);
-                        m[j][e] = mn;
-                        l[j][e] *= by;
+                    const unsigned bit = 1u << (2 * j + e);
+                    if (unset & bit ? mx > K8_NEG : mx > K8_SLACK) {
+                        const float up = mx - K8_LIFT, by = unset & bit ? 1.0f : ex2(-up);
+                        unset &= ~bit;
+                        (e ? nm[j].y : nm[j].x) -= up;
+                        (e ? l[j].y : l[j].x) *= by;
+#pragma unroll
+                        for (int x = 0; x < C::XN; ++x) s[x][j][e] -= up, s[x][j][2 + e] -= up;
 #pragma unroll
                         for (int i = 0; i < C::MT; ++i) o[j][i][e] *= by, o[j][i][2 + e] *= by;
                     }
                 }
+            fresh = __any_sync(0xFFFFFFFFu, unset);
         };
 
 #pragma unroll 1
@@ -549,12 +563,6 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
             // scores
             float s[C::XN][NT][4];
 #pragma unroll
-            for (int x = 0; x < C::XN; ++x)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[x][j][e] = 0.0f;
-#pragma unroll
             for (int c = 0; c < C::KC; ++c)
 #pragma unroll
                 for (int h2 = 0; h2 < C::XN; ++h2) {
@@ -577,36 +585,31 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                             load_q(j, c, f);
                         }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma(s[h2][j], a[k][0], a[k][1], a[k][2], a[k][3], f[2 * k], f[2 * k + 1]);
+                        for (int k = 0; k < 4; ++k) {
+                            if (c == 0 && k == 0)
+                                mma0(s[h2][j], a[k][0], a[k][1], a[k][2], a[k][3], f[2 * k], f[2 * k + 1]);
+                            else
+                                mma(s[h2][j], a[k][0], a[k][1], a[k][2], a[k][3], f[2 * k], f[2 * k + 1]);
+                        }
                     }
                 }
-            // exponents in place of the sums
+            // exponents relative to the references in place of the sums
+            float top = -INFINITY;
 #pragma unroll
-            for (int x = 0; x < C::XN; ++x)
+            for (int x = 0; x < C::XN; ++x) {
+                const float2 k2 = make_float2(scale_of(ks, x), scale_of(ks, x)), v2 = make_float2(scale_of(lv, x), scale_of(lv, x));
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const float2 f = mul2(make_float2(scale_of(ks, x), scale_of(ks, x)), make_float2(qs[j][0], qs[j][1]));
+                    const float2 f = mul2(k2, qs[j]), at = add2(v2, nm[j]);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float2 a = fma2(make_float2(s[x][j][2 * k], s[x][j][2 * k + 1]), f, make_float2(scale_of(lv, x), scale_of(lv, x)));
-                        s[x][j][2 * k] = a.x, s[x][j][2 * k + 1] = a.y;
+                    for (int k = 0; k < 4; k += 2) {
+                        const float2 a = fma2(make_float2(s[x][j][k], s[x][j][k + 1]), f, at);
+                        s[x][j][k] = a.x, s[x][j][k + 1] = a.y;
+                        top = fmaxf(top, fmaxf(a.x, a.y));
                     }
                 }
-            bool up = true;
-            if (whole) {
-                float top = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        {
-                        float mx = fmaxf(s[0][j][e], s[0][j][2 + e]);
-                        if (C::XN == 2) mx = fmaxf(mx, fmaxf(s[C::XN - 1][j][e], s[C::XN - 1][j][2 + e]));
-                        top = fmaxf(top, mx - m[j][e]);
-                    }
-                up = __any_sync(0xFFFFFFFFu, top > K8_SLACK);
-            } else {
+            }
+            if (!whole) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -623,20 +626,21 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                             }
                     }
             }
-            if (up) raise(s);
+            if (__any_sync(0xFFFFFFFFu, top > K8_SLACK) || fresh || !whole) raise(s);
             unsigned pb[C::XN][NT][2];
 #pragma unroll
             for (int x = 0; x < C::XN; ++x)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const float2 down = make_float2(-m[j][0], -m[j][1]);
-                    float2 a = add2(make_float2(s[x][j][0], s[x][j][1]), down), b = add2(make_float2(s[x][j][2], s[x][j][3]), down);
-                    a = make_float2(ex2(a.x), ex2(a.y)), b = make_float2(ex2(b.x), ex2(b.y));
-                    const float2 sum = add2(a, b);
-                    const float2 add = mul2(sum, make_float2(scale_of(inv, x), scale_of(inv, x)));
-                    // a row that sees none of the half takes nothing from its scale either
-                    l[j][0] += whole || sum.x != 0.0f ? add.x : 0.0f;
-                    l[j][1] += whole || sum.y != 0.0f ? add.y : 0.0f;
+                    const float2 a = make_float2(ex2(s[x][j][0]), ex2(s[x][j][1])), b = make_float2(ex2(s[x][j][2]), ex2(s[x][j][3]));
+                    float2 sum = add2(a, b);
+                    const float2 i2 = make_float2(scale_of(inv, x), scale_of(inv, x));
+                    if (whole) {
+                        l[j] = fma2(sum, i2, l[j]);
+                    } else {  // a row that sees none of the half takes nothing from its scale either
+                        if (sum.x != 0.0f) l[j].x = fmaf(sum.x, i2.x, l[j].x);
+                        if (sum.y != 0.0f) l[j].y = fmaf(sum.y, i2.y, l[j].y);
+                    }
                     // The weights are operands in f16: off by half a unit of it.  l keeps them whole.
                     pb[x][j][0] = movm(pack(a.x, a.y));
                     pb[x][j][1] = movm(pack(b.x, b.y));
@@ -695,11 +699,12 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float sum = l[j][e];
+                float sum = e ? l[j].y : l[j].x;
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
                 const int r = 8 * j + 2 * t + e;
-                if (g == 0) s_ml[warp * 8 * NT + r] = make_float2(m[j][e], sum);
+                const float m = unset >> (2 * j + e) & 1 ? K8_NEG : e ? -nm[j].y : -nm[j].x;
+                if (g == 0) s_ml[warp * 8 * NT + r] = make_float2(m, sum);
                 // elements of its unit of the row, in quads; quad c of a row lies at c ^ t: no bank twice
                 float4 *to = reinterpret_cast<float4 *>(k8_smem) + (warp * 8 * NT + r) * (DP / 4);
 #pragma unroll
