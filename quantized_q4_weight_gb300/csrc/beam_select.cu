@@ -87,9 +87,9 @@ __device__ __forceinline__ Key key_of(float v, unsigned token)
 __device__ __forceinline__ float value_of(Key k) { return from_ordered(static_cast<unsigned>(k >> 32)); }
 __device__ __forceinline__ unsigned token_of(Key k) { return 0xFFFFFFFFu - static_cast<unsigned>(k); }
 
-// Elements of a 16-byte chunk as floats, and the largest of them (NaN passed over); of a
-// batch, a bit for each element that reaches a bound (a value of the type), and where
-// such an element is: chunk, place in it.
+// Elements of a 16-byte chunk as floats; of a batch the largest (NaN passed over), a bit for
+// each element that reaches a bound (a value of the type), and where such an element is:
+// chunk, place in it.
 template <typename T>
 struct Chunk16;
 template <>
@@ -99,9 +99,12 @@ struct Chunk16<float> {
     {
         return __uint_as_float(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w);
     }
-    static __device__ __forceinline__ float largest(const uint4 &w)
+    static __device__ __forceinline__ float largest(const uint4 (&c)[BM_CHUNKS])
     {
-        return fmaxf(fmaxf(at(w, 0), at(w, 1)), fmaxf(at(w, 2), at(w, 3)));
+        float m = at(c[0], 0);
+#pragma unroll
+        for (int k = 1; k < 4 * BM_CHUNKS; ++k) m = fmaxf(m, at(c[k >> 2], k & 3));
+        return m;
     }
     static __device__ __forceinline__ unsigned reach(const uint4 (&c)[BM_CHUNKS], float bound)
     {
@@ -126,11 +129,14 @@ struct Chunk16<__half> {
     {
         return i & 1 ? __high2float(pair(w, i >> 1)) : __low2float(pair(w, i >> 1));
     }
-    static __device__ __forceinline__ float largest(const uint4 &w)
+    static __device__ __forceinline__ float largest(const uint4 (&c)[BM_CHUNKS])
     {
-        const __half2 m = __hmax2(__hmax2(pair(w, 0), pair(w, 1)), __hmax2(pair(w, 2), pair(w, 3)));
+        __half2 m = pair(c[0], 0);
+#pragma unroll
+        for (int k = 1; k < 4 * BM_CHUNKS; ++k) m = __hmax2(m, pair(c[k >> 2], k & 3));
         return fmaxf(__low2float(m), __high2float(m));
-    }    // bit w: the lower element of word w, bit 16 + w its upper one
+    }
+    // bit w: the lower element of word w, bit 16 + w its upper one
     static __device__ __forceinline__ unsigned reach(const uint4 (&c)[BM_CHUNKS], float bound)
     {
         const __half2 b = __half2half2(__float2half_rn(bound));
@@ -160,11 +166,14 @@ struct Chunk16<__nv_bfloat16> {
     {
         return __uint_as_float(i & 1 ? part(w, i >> 1) & 0xFFFF0000u : part(w, i >> 1) << 16);
     }
-    static __device__ __forceinline__ float largest(const uint4 &w)
+    static __device__ __forceinline__ float largest(const uint4 (&c)[BM_CHUNKS])
     {
-        const __nv_bfloat162 m = __hmax2(__hmax2(pair(w, 0), pair(w, 1)), __hmax2(pair(w, 2), pair(w, 3)));
+        __nv_bfloat162 m = pair(c[0], 0);
+#pragma unroll
+        for (int k = 1; k < 4 * BM_CHUNKS; ++k) m = __hmax2(m, pair(c[k >> 2], k & 3));
         return fmaxf(__low2float(m), __high2float(m));
-    }    // bit w: the lower element of word w, bit 16 + w its upper one
+    }
+    // bit w: the lower element of word w, bit 16 + w its upper one
     static __device__ __forceinline__ unsigned reach(const uint4 (&c)[BM_CHUNKS], float bound)
     {
         const __nv_bfloat162 b = __bfloat162bfloat162(__float2bfloat16_rn(bound));
@@ -450,9 +459,12 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
         };
         constexpr int BATCH = BM_THREADS * BM_CHUNKS * E;
         uint4 next[BM_CHUNKS];
+        const int span = static_cast<int>(min(static_cast<long long>(p.slice), p.vocab - t0));  // below 1: nothing
+        const int whole_from = t0 < 0 ? 1 : 0;  // batches from here on that end within the span lie in the row
+        const uint4 *base = reinterpret_cast<const uint4 *>(x + t0) + tid;
         auto fetch_batch = [&](int l0) {
-            if (l0 + BATCH <= p.slice && t0 + l0 >= 0 && t0 + l0 + BATCH <= p.vocab) {
-                const uint4 *from = reinterpret_cast<const uint4 *>(x + t0 + l0) + tid;
+            if (l0 >= whole_from && l0 + BATCH <= span) {
+                const uint4 *from = base + l0 / E;
 #pragma unroll
                 for (int k = 0; k < BM_CHUNKS; ++k) next[k] = __ldcs(from + k * BM_THREADS);
             } else {
@@ -465,15 +477,12 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
         unsigned bound_token = 0xFFFFFFFFu;  // a value equal to the bound counts up to this token
         int have = 0, kept = 0, since = 0;   // keys of the list that are the best so far, and with those after them; where it was
                                              // looked at last
-        const int span = static_cast<int>(min(static_cast<long long>(p.slice), p.vocab - t0));
         for (int l0 = 0; l0 < span; l0 += BATCH) {
             uint4 cur[BM_CHUNKS];
 #pragma unroll
             for (int k = 0; k < BM_CHUNKS; ++k) cur[k] = next[k];
             if (l0 + BATCH < span) fetch_batch(l0 + BATCH);
-            float top = C::largest(cur[0]);
-#pragma unroll
-            for (int k = 1; k < BM_CHUNKS; ++k) top = fmaxf(top, C::largest(cur[k]));
+            const float top = fmaxf(C::largest(cur), -INFINITY);  // of nothing but NaN: -infinity
 
             // the sum, against the thread's first maximum, or one that stands far above it
             if (top > m + 40.0f) {
@@ -555,7 +564,10 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
                 total = kept + found;
             }
             if (total > have + BM_FULL || first || end || over) {
-                rank_keys<BM_THREADS, BM_LIST / BM_THREADS>(s.list, total, p.n_best, tid, [] { __syncthreads(); });
+                if (total <= BM_THREADS)
+                    rank_keys<BM_THREADS, 1>(s.list, total, p.n_best, tid, [] { __syncthreads(); });
+                else
+                    rank_keys<BM_THREADS, BM_LIST / BM_THREADS>(s.list, total, p.n_best, tid, [] { __syncthreads(); });
                 total = have = min(total, p.n_best);
                 if (tid == 0) s.total = have;
                 if (have == p.n_best) {
