@@ -69,7 +69,8 @@ class Model:
                                       q.workspace_bytes(vocab, d_model, T_MAX), 32 << 20))
         self.buf = {n: torch.empty((T_MAX, w), device=DEV) for n, w in
                     (("qkv", self.qkv), ("attn", heads * head_dim), ("x", d_model), ("logits", vocab))}
-        self.k = torch.empty((T_MAX, kv_heads, head_dim), dtype=torch.float16, device=DEV)
+        self.q = torch.empty((T_MAX, heads, head_dim), dtype=torch.float16, device=DEV)
+        self.k = torch.empty((T_MAX, kv_heads, head_dim), device=DEV)
 
     @staticmethod
     def _norm(x, w):
@@ -90,9 +91,8 @@ class Model:
             self._product(L["wqkv"], self._norm(x, L["norm1"]), qkv)
             xq, xk = qkv[:, :hq].unflatten(1, (self.h, self.hd)), qkv[:, hq:hk].unflatten(1, (self.g, self.hd))
             xv = qkv[:, hk:].unflatten(1, (self.g, self.hd))
-            xq = q.norm_rope_kv(self.rope, L["heads"], xq, xk, None, pos, k_out=self.k[:T])
-            # k in f16 and v in fp32 come from different places: v is rounded to k's type
-            q.kv8_append(self.k[:T], xv.to(torch.float16), batch(i))
+            xq = q.norm_rope_kv(self.rope, L["heads"], xq, xk, None, pos, out=self.q[:T], k_out=self.k[:T])
+            q.kv8_append(self.k[:T], xv, batch(i))
             q.attn_kv8(xq, batch(i), self.ws, out=attn.unflatten(1, (self.h, self.hd)))
             self._product(L["wo"], attn, x, residual=x)
             q.ffn_residual(L["gate"], L["up"], L["down"], q.W_PACKED, self._norm(x, L["norm2"]), x, self.d, self.ff, T,

@@ -748,7 +748,7 @@ typedef struct {
 /* qgemv_rope_kv with q and k normed first, all in one pass: the norm's
  * statistics, its result and the rotation stay in fp32, rounded once at the end.
  * v is copied.  Without a cache (cache NULL; v and slots are then ignored)
- * the rotated k goes to k_out [t][h][head_dim], n_k_heads heads, of q_type,
+ * the rotated k goes to k_out [t][h][head_dim], n_k_heads heads, of k_type,
  * k_out_stride elements between tokens: for a cache that another call writes
  * (qgemv_kv8_append).  With a cache k_out is ignored and n_k_heads must be the
  * cache's.  head_dim is even and at most 256; the other rules are
@@ -757,8 +757,8 @@ qgemv_status qgemv_norm_rope_kv(const qgemv_rope_plan *plan, const qgemv_qk_norm
                                 const void *v, qgemv_dtype in_type, int64_t q_stride, int64_t k_stride,
                                 int64_t v_stride, const int32_t *pos, const int32_t *slots, int64_t n_tokens,
                                 int n_q_heads, int n_k_heads, int head_dim, void *q_out, qgemv_dtype q_type,
-                                int64_t q_out_stride, void *k_out, int64_t k_out_stride, const qgemv_kv_cache *cache,
-                                qgemv_stream_t stream);
+                                int64_t q_out_stride, void *k_out, qgemv_dtype k_type, int64_t k_out_stride,
+                                const qgemv_kv_cache *cache, qgemv_stream_t stream);
 
 /* A paged key/value cache of 8-bit codes, with one fp32 scale for each block of
  * block_size rows and head: a value is code * scale.  Codes are int8
@@ -819,9 +819,10 @@ typedef struct {
  * or, with first NULL, tokens b * n_q .. b * n_q + n_q - 1; they become its rows
  * lens[b] - n .. lens[b] - 1.  k and v are [token][head][head_dim] of in_type,
  * heads head_dim apart, tokens k_stride and v_stride elements apart, n_tokens in
- * all; max_new bounds the tokens of a sequence.  A sequence with more tokens
- * than max_new or than rows, or with tokens outside [0, n_tokens), is left as it
- * is and records QGEMV_ERR_BAD_ID.
+ * all; max_new bounds the tokens of a sequence.  A sequence of length 0 is passed
+ * over (the places of a padded batch); one with more tokens than max_new or than
+ * rows, or with tokens outside [0, n_tokens), is left as it is and records
+ * QGEMV_ERR_BAD_ID.
  * For every block with new rows and every head, k and v each, with s the
  * block's scale if it held rows of the sequence before, else 0, and Q = 127 or 448:
  *   s' = max(s, max |x| / Q) over the new rows' values x;
@@ -848,7 +849,8 @@ size_t qgemv_attn_kv8_workspace_bytes(const qgemv_kv8_batch *batch, const qgemv_
  * Scores, maxima, sums and outputs are accumulated in fp32.  The matrix
  * operands are f16: codes are exact in it; q's bf16 values are, down to 2^-14 of
  * the row's largest (smaller ones to 2^-25 of it); a softmax weight times its
- * block's scale of v is rounded to it (to 2^-34 of the row's largest at least).
+ * block's scale of v is rounded to it (to 2^-34 of the row's largest at least); a
+ * scale of v below 2^-60 counts as 2^-60.
  * What rows that a query does not see hold never reaches it; NaN codes of e4m3,
  * which qgemv_kv8_append never writes, make the results of those that see them
  * meaningless.  Results do not depend on the order in which the GPU runs the

@@ -196,7 +196,7 @@ _SIGS = {
     "qgemv_logits_workspace_bytes": ([_VP], _SZ),
     "qgemv_logits_rules": ([_VP, _I32, _I64, _VP, _VP, _I64, _VP, _VP, _VP, _SZ, _VP], _I32),
     "qgemv_norm_rope_kv": ([_VP, _VP, _VP, _VP, _VP, _I32, _I64, _I64, _I64, _VP, _VP, _I64, _I32, _I32, _I32, _VP, _I32,
-                            _I64, _VP, _I64, _VP, _VP], _I32),
+                            _I64, _VP, _I32, _I64, _VP, _VP], _I32),
     "qgemv_kv8_append": ([_VP, _VP, _I32, _I64, _I64, _I64, _VP, _VP, _VP, _I32, _VP], _I32),
     "qgemv_attn_kv8_workspace_bytes": ([_VP, _VP], _SZ),
     "qgemv_attn_kv8": ([_VP, _I32, _I64, _I64, _VP, _VP, _VP, _I32, _I64, _I64, _VP, _VP, _SZ, _VP], _I32),
@@ -739,8 +739,8 @@ class QkNorm(_Described):
 def norm_rope_kv(plan: RopePlan, norm: QkNorm, xq, xk, xv=None, pos=None, slots=None, cache: KvCache | None = None,
                  out=None, k_out=None, stream=None):
     """rope_kv with q and k normed head by head first.  Without a cache the rotated k goes to
-    k_out (of out's type, default for out too), and v is the caller's to write
-    (kv8_append); xv and slots are then None.  Returns out."""
+    k_out (fp32, f16 or bf16), and v is the caller's to write (kv8_append); xv and slots
+    are then None, and out defaults to a tensor of q's type.  Returns out."""
     if (xk if xq is None else xq).shape[-1] != norm.head_dim:
         raise ValueError("norm_rope_kv: norm of q's and k's head_dim")
     r = (_ext or _load_binding()).norm_rope_kv(plan, norm.struct, xq, xk, xv, pos, slots,

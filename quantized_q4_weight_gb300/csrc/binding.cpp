@@ -364,24 +364,24 @@ PyObject *norm_rope_kv(PyObject *, PyObject *const *a, Py_ssize_t n) noexcept
             need(!v && !k_out, "norm_rope_kv: v and k_out need k");
         }
         at::Tensor made;
-        qgemv_dtype q_type = k_out ? type_of(*k_out, "norm_rope_kv: k_out's type") : QGEMV_F32;
+        qgemv_dtype q_type = QGEMV_F32;
         if (q) {
             qs = heads(*q, "norm_rope_kv: q [tokens][heads][head_dim] with adjacent heads");
             if (!out) {
-                made = beside(*q, q->sizes(), k_out ? k_out->scalar_type() : cache ? scalar_of(cache->type) : q->scalar_type(), a[10]);
+                made = beside(*q, q->sizes(), cache ? scalar_of(cache->type) : q->scalar_type(), a[10]);
                 out = &made;
             }
             need(out->sizes() == q->sizes(), "norm_rope_kv: out of q's shape");
             os = heads(*out, "norm_rope_kv: out [tokens][heads][head_dim] with adjacent heads");
             q_type = type_of(*out, "norm_rope_kv: out's type");
-            need(!k_out || k_out->scalar_type() == out->scalar_type(), "norm_rope_kv: out and k_out of one type");
         }
         const qgemv_status s = qgemv_norm_rope_kv(
             plan_at.get(), norm_at.get(), q ? q->const_data_ptr() : nullptr, k ? k->const_data_ptr() : nullptr,
             k && v ? v->const_data_ptr() : nullptr, type, qs, ks, vs, int32s(pos, tokens, "norm_rope_kv: pos int32 [tokens]"),
             int32s(slots, tokens, "norm_rope_kv: slots int32 [tokens]"), tokens, q ? static_cast<int>(q->size(1)) : 0,
             k ? static_cast<int>(k->size(1)) : 0, static_cast<int>(d), q ? out->data_ptr() : nullptr, q_type, os,
-            k_out ? k_out->data_ptr() : nullptr, kos, k ? cache : nullptr, stream_of(a[10], *some));
+            k_out ? k_out->data_ptr() : nullptr, k_out ? type_of(*k_out, "norm_rope_kv: k_out's type") : QGEMV_F32, kos,
+            k ? cache : nullptr, stream_of(a[10], *some));
         if (s != QGEMV_OK) return PyLong_FromLong(s);
         if (made.defined()) return THPVariable_Wrap(std::move(made));
         return Py_NewRef(q ? a[8] : Py_None);

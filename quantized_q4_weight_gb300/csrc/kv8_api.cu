@@ -183,10 +183,12 @@ qgemv_status qgemv_norm_rope_kv(const qgemv_rope_plan *plan, const qgemv_qk_norm
                                 const void *v, qgemv_dtype in_type, int64_t q_stride, int64_t k_stride,
                                 int64_t v_stride, const int32_t *pos, const int32_t *slots, int64_t n_tokens,
                                 int n_q_heads, int n_k_heads, int head_dim, void *q_out, qgemv_dtype q_type,
-                                int64_t q_out_stride, void *k_out, int64_t k_out_stride, const qgemv_kv_cache *cache,
-                                qgemv_stream_t stream)
+                                int64_t q_out_stride, void *k_out, qgemv_dtype k_type, int64_t k_out_stride,
+                                const qgemv_kv_cache *cache, qgemv_stream_t stream)
 {
-    if (!plan || !norm || !pos || (!q && !k) || !type_ok(in_type) || !type_ok(q_type)) return QGEMV_ERR_INVALID_ARG;
+    if (!plan || !norm || !pos || (!q && !k) || !type_ok(in_type) || (q && !type_ok(q_type)) ||
+        (k && !cache && !type_ok(k_type)))
+        return QGEMV_ERR_INVALID_ARG;
     const int rot = plan->rot_dim;
     if (rot < 2 || rot > 256 || rot % 2 || (plan->layout != QGEMV_ROPE_HALF && plan->layout != QGEMV_ROPE_INTERLEAVED))
         return QGEMV_ERR_INVALID_ARG;
@@ -196,7 +198,7 @@ qgemv_status qgemv_norm_rope_kv(const qgemv_rope_plan *plan, const qgemv_qk_norm
         return QGEMV_ERR_INVALID_ARG;
     if (k && (n_k_heads < 1 || n_k_heads > 4096 || (cache ? !v || !slots : !k_out))) return QGEMV_ERR_INVALID_ARG;
     if (q && (!q_out || n_q_heads < 1 || n_q_heads > 4096)) return QGEMV_ERR_INVALID_ARG;
-    const int ib = type_bytes(in_type), qb = type_bytes(q_type);
+    const int ib = type_bytes(in_type), qb = type_bytes(q_type), kb = type_bytes(k_type);
     const long long qw = q ? static_cast<long long>(n_q_heads) * head_dim : 0;
     const long long kw = k ? static_cast<long long>(n_k_heads) * head_dim : 0;
     const bool to_cache = k && cache, to_k = k && !cache;
@@ -212,7 +214,7 @@ qgemv_status qgemv_norm_rope_kv(const qgemv_rope_plan *plan, const qgemv_qk_norm
         if (cache->head_dim != head_dim || cache->n_heads != n_k_heads || cache->n_pages * cache->page_size > INT32_MAX)
             return QGEMV_ERR_INVALID_ARG;
     }
-    if ((q && (!aligned(q, ib) || !aligned(q_out, qb))) || (k && !aligned(k, ib)) || (to_k && !aligned(k_out, qb)) ||
+    if ((q && (!aligned(q, ib) || !aligned(q_out, qb))) || (k && !aligned(k, ib)) || (to_k && !aligned(k_out, kb)) ||
         (to_cache && (!aligned(v, ib) || !aligned(slots, 4))) || !aligned(pos, 4) ||
         (q && !aligned(norm->q_weight, 4)) || (k && !aligned(norm->k_weight, 4)))
         return QGEMV_ERR_MISALIGNED;
@@ -225,7 +227,7 @@ qgemv_status qgemv_norm_rope_kv(const qgemv_rope_plan *plan, const qgemv_qk_norm
     const Span wq = span(norm->q_weight, q ? 4ll * head_dim : 0), wk = span(norm->k_weight, k ? 4ll * head_dim : 0);
     const Span ss = span(slots, to_cache ? 4 * n_tokens : 0);
     const auto all = [](const Rows &r) { return span(r.p, (r.n - 1) * r.stride + r.width); };
-    const Rows oq{q_out, n_tokens, q_out_stride * qb, qw * qb}, ok{k_out, n_tokens, k_out_stride * qb, kw * qb};
+    const Rows oq{q_out, n_tokens, q_out_stride * qb, qw * qb}, ok{k_out, n_tokens, k_out_stride * kb, kw * kb};
     if (q) {
         const bool in_place = q_out == q && q_type == in_type && (q_out_stride == q_stride || n_tokens == 1);
         if (!in_place && rows_overlap(oq, rq)) return QGEMV_ERR_INVALID_ARG;
@@ -285,12 +287,12 @@ qgemv_status qgemv_norm_rope_kv(const qgemv_rope_plan *plan, const qgemv_qk_norm
         r.ck = k_out;
         r.row_stride = k_out_stride;
         r.head_stride = head_dim;
-        vec = vec && fits16(k_out, k_out_stride, qb);
+        vec = vec && fits16(k_out, k_out_stride, kb);
     }
     int sms = 0;
     const qgemv_status s = device_props(&sms, &r.status);
     if (s != QGEMV_OK) return s;
-    return launch_norm_rope(p, in_type, q_type, to_cache ? cache->type : q_type, plan->layout == QGEMV_ROPE_HALF, vec,
+    return launch_norm_rope(p, in_type, q ? q_type : QGEMV_F32, to_cache ? cache->type : to_k ? k_type : QGEMV_BF16, plan->layout == QGEMV_ROPE_HALF, vec,
                             n_tokens, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? QGEMV_OK
                : QGEMV_ERR_CUDA;

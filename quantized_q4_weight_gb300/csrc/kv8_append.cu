@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(THREADS) kv8_append_kernel(const __grid_consta
     const bool told = tid == 0 && jb == 0 && blockIdx.y == 0;
     const int n = len < 0 ? 0 : len > p.max_len ? p.max_len : len;
     if (n != len && told) atomicCAS(p.status, 0u, ST_BAD_ID);
+    if (len == 0) return;  // a padded batch's place
     if (t0 < 0 || t1 > p.n_tokens || t1 < t0 || t1 - t0 > p.max_new || t1 - t0 > n) {
         if (told) atomicCAS(p.status, 0u, ST_BAD_ID);
         return;

@@ -225,10 +225,7 @@ cudaError_t launch3(NormRopeParams &p, bool half, bool vec, long long n, int sms
 template <typename TI, typename TQ>
 cudaError_t launch2(NormRopeParams &p, qgemv_dtype k_out, bool half, bool vec, long long n, int sms, cudaStream_t st)
 {
-    // fp32 k only beside fp32 q: the rotated k without a cache is of q's type
-    if constexpr (sizeof(TQ) == 4) {
-        if (k_out == QGEMV_F32) return launch3<TI, TQ, float>(p, half, vec, n, sms, st);
-    }
+    if (k_out == QGEMV_F32) return launch3<TI, TQ, float>(p, half, vec, n, sms, st);
     return k_out == QGEMV_F16 ? launch3<TI, TQ, __half>(p, half, vec, n, sms, st)
                               : launch3<TI, TQ, __nv_bfloat16>(p, half, vec, n, sms, st);
 }

@@ -6,8 +6,8 @@ is the attention's 16-bit weights (2^-11 relative) and roundings of q and k; eac
 move a Q8_0 activation code of a later GEMV by one, 1/127 of its block's largest
 value, and so may a code of the cache.  With two layers of three such GEMVs behind
 an attention, each change at most 1/127 in the 2-norm, the logits differ by less
-than 6/127 (codes of the cache that move are few: those whose value lies within 2^-11
-of a border).
+than 6/127 (codes of the cache that move are few: those whose value lies within an fp32
+rounding of a border).
 """
 import importlib.util
 import math
@@ -45,7 +45,7 @@ def plain_norm_rope(base):
             u, v = x[..., :d // 2], x[..., d // 2:]
             return torch.cat([u * c - v * s, u * s + v * c], -1)
         k_out.copy_(turned(xk, norm.weights[1]))
-        return turned(xq, norm.weights[0]).to(torch.float16)
+        return out.copy_(turned(xq, norm.weights[0]))
     return f
 
 

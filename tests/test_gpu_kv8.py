@@ -217,6 +217,23 @@ def test_append_bad_pages_and_lengths():
         assert np.array_equal(cache.k_scale[2:].cpu().numpy(), sc[2:])
 
 
+def test_padded_places_are_passed_over():
+    """Sequences of length 0 write nothing and see nothing, with no error, whatever their tables name."""
+    g = gen(23)
+    cache = make_cache(6, 16, 16, 2, 64, torch.int8, g)
+    lens = torch.tensor([0, 18, 0, 5], dtype=torch.int32, device=DEV)
+    table = torch.tensor([[1, 2], [1, 2], [99, -4], [3, -1]], dtype=torch.int32, device=DEV)
+    x = torch.randn((4, 2, 64), generator=g, device=DEV)
+    batch = q.Kv8Batch(4, 1, 4, cache, lens, table, 32)
+    k0, s0 = cache.k.clone(), cache.k_scale.clone()
+    q.kv8_append(x, x, batch)
+    val, sc = append_ref(None, x[[1, 3]], [18, 5], np.array([[1, 2], [3, -1]]), [0, 1, 2], k0, s0, 16, 16)
+    assert np.array_equal(cache.k.float().cpu().numpy(), val) and np.array_equal(cache.k_scale.cpu().numpy(), sc)
+    xq = torch.randn((4, 1, 4, 64), generator=g, device=DEV).to(torch.float16)
+    out = q.attn_kv8(xq, batch, q.new_workspace(batch.workspace_bytes()))
+    assert not bool(out[[0, 2]].any()) and bool(out[[1, 3]].any()) and q.device_status() == 0
+
+
 # --------------------------------------------------------------- attention
 
 def attn_ref(xq, cache, lens, table, nq, window, sinks, scale=None):

@@ -57,11 +57,11 @@ def run(n, hq, hkv, d, rot, layout, tin, tq, tc, to_cache=True, misalign=False, 
     refq, magq = rotated(normed(hold[0], wq.cpu().numpy(), eps), p, th, rot, layout)
     refk, magk = rotated(normed(hold[1], wk.cpu().numpy(), eps), p, th, rot, layout)
     if not to_cache:
-        k_out = torch.empty((n, hkv, d), dtype=tq, device=DEV)
+        k_out = torch.empty((n, hkv, d), dtype=tc, device=DEV)
         assert q.norm_rope_kv(plan, norm, xq, xk, None, pos, out=out, k_out=k_out) is out
         torch.cuda.synchronize()
         close(out, refq, magq, out.dtype)
-        close(k_out, refk, magk, tq)
+        close(k_out, refk, magk, tc)
         assert q.device_status() == 0
         return
     pages = (n + page - 1) // page + 2
@@ -97,7 +97,8 @@ def test_norm_rope(n, layout, hq, hkv, d, rot):
 def test_types(tin, tq):
     for tc in (torch.float16, torch.bfloat16):
         run(33, 6, 2, 64, 64, "half", tin, tq, tc)
-    run(33, 6, 2, 64, 64, "interleaved", tin, tq, tq, to_cache=False)
+    for tk in (torch.float32, torch.float16, torch.bfloat16):
+        run(33, 6, 2, 64, 64, "interleaved", tin, tq, tk, to_cache=False)
 
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])

@@ -168,11 +168,12 @@ def norm_rope(L, c="cache", eps=1e-6, qw=1 << 20, kw=1 << 21, **kw2):
     plan = q.rope_plan(kw2.pop("rot", 128), 1e4)
     norm = q.QkNormStruct(qw, kw, eps)
     f = dict(plan=plan.address, norm=ctypes.addressof(norm), q=4096, k=BIG // 2, v=BIG // 2 + (1 << 30), t=q.F32, qs=1536,
-             ks=256, vs=256, pos=1 << 34, slots=1 << 35, n=10, hq=12, hk=2, d=128, o=1 << 36, ot=q.BF16, os=1536, ko=1 << 37, kos=256)
+             ks=256, vs=256, pos=1 << 34, slots=1 << 35, n=10, hq=12, hk=2, d=128, o=1 << 36, ot=q.BF16, os=1536, ko=1 << 37,
+             kt=q.F32, kos=256)
     f.update(kw2)
     c = cache() if c == "cache" else c
     return L.qgemv_norm_rope_kv(f["plan"], f["norm"], f["q"], f["k"], f["v"], f["t"], f["qs"], f["ks"], f["vs"], f["pos"],
-                                f["slots"], f["n"], f["hq"], f["hk"], f["d"], f["o"], f["ot"], f["os"], f["ko"], f["kos"],
+                                f["slots"], f["n"], f["hq"], f["hk"], f["d"], f["o"], f["ot"], f["os"], f["ko"], f["kt"], f["kos"],
                                 ctypes.addressof(c) if c else None, None)
 
 
@@ -199,7 +200,7 @@ def test_norm_rope_caches(L, bad, status):
 
 
 @pytest.mark.parametrize("bad,status", [
-    (dict(ko=None), INVALID), (dict(kos=255), INVALID), (dict(ko=(1 << 37) + 1), MISALIGNED), (dict(ko=1 << 36), INVALID),
+    (dict(ko=None), INVALID), (dict(kt=3), INVALID), (dict(kos=255), INVALID), (dict(ko=(1 << 37) + 1), MISALIGNED), (dict(ko=1 << 36), INVALID),
     (dict(ko=4096), INVALID), (dict(ko=BIG // 2), INVALID), (dict(ko=1 << 34), INVALID), (dict(ko=1 << 20), INVALID)])
 def test_norm_rope_without_a_cache(L, bad, status):
     assert outcome(norm_rope(L, None, v=None, slots=None)) == ACCEPTED
