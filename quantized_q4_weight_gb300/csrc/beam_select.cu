@@ -533,10 +533,11 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
                     }
                 }
             }
-            // the list is looked at after the first two batches, every fourth, and the last
+            // the list is looked at after 1, 2, 4, 8 ... batches, between which about n keys are
+            // appended each, and at the end
             const int no = l0 / BATCH;
             const bool first = no == 0, end = l0 + BATCH >= span;
-            if (!(no < 2 || end || (no & 3) == 3)) continue;
+            if ((no & (no + 1)) && !end) continue;
             __syncthreads();
             int total = s.total;
             const bool over = total > BM_LIST;
