@@ -271,29 +271,20 @@ __device__ __forceinline__ Key block_largest(Key key, Key *s)
     return key;
 }
 
-// How many of a falling list of `n` are above k.
-template <typename K>
-__device__ __forceinline__ int above(const K *list, int n, K k)
-{
-    int at = 0;
-#pragma unroll
-    for (int d = 16; d; d >>= 1)
-        if (at + d <= n && list[at + d - 1] > k) at += d;
-    return at + (at < n && list[at] > k);
-}
-
 struct BeamShared {
     union {
         Key list[BM_LIST];              // the best of the block so far, then those appended
         Key wait[BM_WARPS][BM_WAIT];    // the same of a row's warp in the join
     };
-    Key lists[BM_BEAMS][32];            // the join's rows
+    Key rows[BM_BEAMS][32];             // the join's rows: their best keys,
+    Key order[BM_BEAMS][32];            // the scores of those as integers (0: none)
+    float score[BM_BEAMS][32];          // and rounded
     Key best[BM_WARPS];
     unsigned first[2][BM_WARPS];
     int total;                          // keys of the list
     int last;
     float m[BM_BEAMS], sum[BM_BEAMS];
-    int count[BM_BEAMS];
+    int count;                          // continuations of all rows
     double lse[BM_BEAMS];
 };
 
@@ -303,13 +294,11 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long r0 = static_cast<long long>(gi) * p.beams;
     const int per = p.slices * p.n_best;
-    constexpr int ROWS = BM_BEAMS / BM_WARPS;  // of a warp
-    Key best[ROWS];  // lane k: the row's k-th
+    // Code that one block of a search runs once waits for its instructions: the loops over a
+    // warp's rows are not unrolled.
     // each row's n best keys, maximum and sum
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-        const int w = warp + q * BM_WARPS;
-        if (w >= p.beams) break;
+#pragma unroll 1
+    for (int w = warp; w < p.beams; w += BM_WARPS) {
         const Key *part = p.part + (r0 + w) * per;
         const float2 *ml = p.part_ml + (r0 + w) * p.slices;
         float m = -INFINITY, sum = 0.0f;
@@ -317,8 +306,9 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
 #pragma unroll
         for (int u = 0; u < BM_SLICES / 32; ++u)
             mine[u] = lane + 32 * u < p.slices ? __ldcg(ml + lane + 32 * u) : make_float2(-INFINITY, 0.0f);
+        Key best;
         if (p.slices == 1) {
-            best[q] = lane < p.n_best ? __ldcg(part + lane) : 0;
+            best = lane < p.n_best ? __ldcg(part + lane) : 0;
         } else {
             constexpr int U = 10;
             Key k[U];
@@ -334,34 +324,36 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
             Key kth = head ? (static_cast<Key>(head) << 32) - 1 : 0;
             Key *list = s.wait[warp];
             int total = 0;
-            const auto rank = [&]() {
-                rank_keys<32, BM_WAIT / 32>(list, total, p.n_best, lane, [] { __syncwarp(); });
-                total = min(total, p.n_best);
-                if (total == p.n_best) kth = list[p.n_best - 1];
-            };
-            for (int i0 = 0; i0 < per; i0 += 32 * U) {
-                if (i0) fetch(i0);
+            for (int i0 = 0;;) {
 #pragma unroll 1
                 for (int u = 0; u < U; ++u) {
                     Key c = k[0];
 #pragma unroll
                     for (int v = 1; v < U; ++v) c = u == v ? k[v] : c;
-                    if (total > BM_WAIT - 32) rank();
                     const unsigned in = __ballot_sync(0xFFFFFFFFu, c > kth);
                     if (c > kth) list[total + __popc(in & ((1u << lane) - 1))] = c;
                     total += __popc(in);
+                    const bool end = u == U - 1 && i0 + 32 * U >= per;
+                    if (total > BM_WAIT - 32 || end) {
+                        rank_keys<32, BM_WAIT / 32>(list, total, p.n_best, lane, [] { __syncwarp(); });
+                        total = min(total, p.n_best);
+                        if (total == p.n_best) kth = list[p.n_best - 1];
+                    }
                 }
+                i0 += 32 * U;
+                if (i0 >= per) break;
+                fetch(i0);
             }
-            rank();
-            best[q] = lane < total ? list[lane] : 0;
+            best = lane < total ? list[lane] : 0;
         }
+        s.rows[w][lane] = best;
 #pragma unroll
         for (int u = 0; u < BM_SLICES / 32; ++u) m = fmaxf(m, mine[u].x);
 #pragma unroll
         for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
 #pragma unroll
         for (int u = 0; u < BM_SLICES / 32; ++u)
-            if (mine[u].x > -INFINITY) sum = fmaf(mine[u].y, expf(mine[u].x - m), sum);
+            if (mine[u].x > -INFINITY) sum = fmaf(mine[u].y, ex2((mine[u].x - m) * LOG2E), sum);
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
         if (lane == 0) s.m[w] = m, s.sum[w] = sum;
@@ -375,42 +367,41 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
         s.lse[tid] = none ? INF : static_cast<double>(m) + log_of(s.sum[tid]);
         s.m[tid] = none ? 0.0f : run;
     }
+    if (tid == 0) s.count = 0;
     __syncthreads();
-    double score[ROWS];
-    Key order[ROWS];  // of the scores: their bits in an order that integers have
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-        const int w = warp + q * BM_WARPS;
-        if (w >= p.beams) break;
-        score[q] = static_cast<double>(value_of(best[q])) - s.lse[w] + static_cast<double>(s.m[w]);
-        const long long b = __double_as_longlong(score[q] + 0.0);
-        order[q] = b < 0 ? ~static_cast<Key>(b) : static_cast<Key>(b) | 0x8000000000000000ull;
-        if (best[q] == 0 || lane >= p.n_best || !(score[q] > -INF)) order[q] = 0;
-        s.lists[w][lane] = order[q];
-        const int count = __popc(__ballot_sync(0xFFFFFFFFu, order[q] != 0));
-        if (lane == 0) s.count[w] = count;
+#pragma unroll 1
+    for (int w = warp; w < p.beams; w += BM_WARPS) {
+        const Key key = s.rows[w][lane];
+        const double v = static_cast<double>(value_of(key)) - s.lse[w] + static_cast<double>(s.m[w]);
+        const long long b = __double_as_longlong(v + 0.0);
+        const Key order = b < 0 ? ~static_cast<Key>(b) : static_cast<Key>(b) | 0x8000000000000000ull;
+        const bool there = key != 0 && lane < p.n_best && v > -INF;
+        s.order[w][lane] = there ? order : 0;
+        s.score[w][lane] = static_cast<float>(v);
+        const unsigned in = __ballot_sync(0xFFFFFFFFu, there);
+        if (lane == 0) atomicAdd(&s.count, __popc(in));
     }
     __syncthreads();
     const long long out = static_cast<long long>(gi) * p.n_best;
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-        const int w = warp + q * BM_WARPS;
-        if (w >= p.beams) break;
-        if (order[q] == 0) continue;
-        // equal scores of other rows: the lower row comes first
+#pragma unroll 1
+    for (int w = warp; w < p.beams; w += BM_WARPS) {
+        const Key mine = s.order[w][lane];
+        // how many of the other rows' come before: all above, and equal ones of lower rows
         int rank = lane;
+#pragma unroll 1
+        for (int o = 0; o < p.beams; ++o) {
+            const Key than = mine - (o < w);
+            if (o != w)
 #pragma unroll 4
-        for (int o = 0; o < p.beams; ++o)
-            if (o != w) rank += above(s.lists[o], s.count[o], order[q] - (o < w));
-        if (rank < p.n_best) {
-            p.score[out + rank] = static_cast<float>(score[q]);
-            p.token[out + rank] = token_of(best[q]);
+                for (int k = 0; k < p.n_best; ++k) rank += s.order[o][k] > than;
+        }
+        if (mine && rank < p.n_best) {
+            p.score[out + rank] = s.score[w][lane];
+            p.token[out + rank] = token_of(s.rows[w][lane]);
             p.parent[out + rank] = static_cast<int32_t>(p.row0 + r0 + w);
         }
     }
-    int count = 0;
-    for (int w = 0; w < p.beams; ++w) count += s.count[w];
-    for (int k = count + tid; k < p.n_best; k += BM_THREADS) {
+    for (int k = s.count + tid; k < p.n_best; k += BM_THREADS) {
         p.score[out + k] = -INFINITY;
         p.token[out + k] = -1;
         p.parent[out + k] = -1;
