@@ -108,7 +108,7 @@ inline Span table_span(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c)
 // Launch shape and workspace of the attention.
 struct Kv8Plan {
     int group, rows, row_tiles, tile_rows, tile_pad;
-    int balanced, grid, combine_lanes, by_unit, aligned;
+    int balanced, ranges, grid, combine_lanes, by_unit, aligned;
     long long ml_at, parts_at, ws_bytes;
 };
 
@@ -131,7 +131,7 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     a.ml_at = a.parts_at = kCounterArea;
     a.ws_bytes = kCounterArea;
     a.combine_lanes = 1;
-    a.by_unit = a.aligned = 0;
+    a.by_unit = a.aligned = a.ranges = 0;
     if (!a.balanced) {
         if (units > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
         a.grid = static_cast<int>(units);
@@ -141,12 +141,13 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     const long long per_seq = units / b->n_seqs, blocks = static_cast<long long>(ATTN_SMS) * kv8_blocks(c->head_dim, nt);
     const long long ranges = std::min(std::max(1ll, blocks / per_seq), ceil_div(b->n_seqs * tiles, KV8_SPLIT_MIN) + b->n_seqs);
     if (ranges * per_seq > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
+    a.ranges = static_cast<int>(ranges);
     a.grid = static_cast<int>(ranges * per_seq);
     // parts of a sequence: about ranges / n_seqs, and of a long one up to ranges.  A group takes four at once.
     const long long parts = ranges / std::min<long long>(b->n_seqs, ranges);
     while (a.combine_lanes < 32 && 2 * a.combine_lanes < parts) a.combine_lanes *= 2;
     a.by_unit = units <= a.grid;
-    a.aligned = 8ll * b->n_seqs <= ranges;
+    a.aligned = 8ll * b->n_seqs <= ranges && b->n_seqs <= 32;
     a.ml_at = a.parts_at + 16ll * a.grid;
     const long long o_at = a.ml_at + 16ll * a.grid * a.tile_pad;
     a.ws_bytes = o_at + 8ll * a.grid * a.tile_pad * c->head_dim;
@@ -416,6 +417,7 @@ qgemv_status qgemv_attn_kv8(const void *q, qgemv_dtype q_type, int64_t q_token_s
     p.hq = b.n_q_heads;
     p.hkv = cache->n_heads;
     p.group = a.group;
+    p.per_group = 1.0f / static_cast<float>(a.group);
     p.d = d;
     p.max_len = b.max_len;
     p.window = b.window;
@@ -426,6 +428,7 @@ qgemv_status qgemv_attn_kv8(const void *q, qgemv_dtype q_type, int64_t q_token_s
     const double scale = b.scale != 0.0f ? b.scale : 1.0 / std::sqrt(static_cast<double>(d));
     p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
     p.balanced = a.balanced;
+    p.ranges = a.ranges;
     p.grid = a.grid;
     p.combine_lanes = a.combine_lanes;
     p.parts_by_unit = a.by_unit;

@@ -228,11 +228,20 @@ __device__ __forceinline__ void put4<__nv_bfloat16>(__nv_bfloat16 *o, float4 v)
     o[2] = __float2bfloat16_rn(v.z), o[3] = __float2bfloat16_rn(v.w);
 }
 
+// Query and head within the group of a row: its quotient and remainder by the group's heads
+// (rows are below 2^15, so that half a row more times the fp32 reciprocal ends on the right side).
+__device__ __forceinline__ int2 query_of(const Kv8AttnParams &p, int row)
+{
+    const int i = __float2int_rd((static_cast<float>(row) + 0.5f) * p.per_group);
+    return make_int2(i, row - i * p.group);
+}
+
 // Four elements, from 4 * c on, of row `row` of sequence b and cache head h.
 __device__ __forceinline__ void store_o(const Kv8AttnParams &p, int b, int h, int row, int c, float4 v)
 {
-    const long long token = static_cast<long long>(b) * p.n_q + row / p.group;
-    const long long at = token * p.o_token_stride + (h * p.group + row % p.group) * p.o_head_stride + 4 * c;
+    const int2 r = query_of(p, row);
+    const long long token = static_cast<long long>(b) * p.n_q + r.x;
+    const long long at = token * p.o_token_stride + (h * p.group + r.y) * p.o_head_stride + 4 * c;
     if (p.o_type == QGEMV_F32)
         put4(static_cast<float *>(p.o) + at, v);
     else if (p.o_type == QGEMV_F16)
@@ -243,8 +252,9 @@ __device__ __forceinline__ void store_o(const Kv8AttnParams &p, int b, int h, in
 __device__ __forceinline__ void store_lse(const Kv8AttnParams &p, int b, int h, int row, float m, float l)
 {
     if (!p.lse) return;
-    const long long token = static_cast<long long>(b) * p.n_q + row / p.group;
-    p.lse[token * p.hq + h * p.group + row % p.group] =
+    const int2 r = query_of(p, row);
+    const long long token = static_cast<long long>(b) * p.n_q + r.x;
+    p.lse[token * p.hq + h * p.group + r.y] =
         l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
@@ -288,75 +298,78 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
     __syncthreads();
     pdl_wait();
 
-    // The block's range [lo, hi) of the line of all sequences' tiles, the sequence
-    // that it begins in and where that one's tiles begin.
-    const int per_seq = p.hkv * p.row_tiles, unit = blockIdx.x % per_seq;
-    const int h = unit / p.row_tiles, row0 = unit % p.row_tiles * p.tile_rows;
-    const int rows = min(p.tile_rows, p.rows - row0);
-    int lo, hi, range = 0, seq_at, b;  // in tiles: all of them fit 31 bits
+    // The unit: cache head and tile of query rows.  Then the block's range [lo, hi) of
+    // tiles, the sequence that it begins in and where that one's tiles begin: along the line of all
+    // sequences' tiles, or (aligned, and a block for each unit) within the sequence.
+    const int unit = blockIdx.x, per_seq = gridDim.x, no = static_cast<int>(blockIdx.y + blockIdx.z * gridDim.y);
+    const int h = p.row_tiles == 1 ? unit : unit / p.row_tiles, row0 = (unit - h * p.row_tiles) * p.tile_rows;
+    const int rows = min(p.tile_rows, p.rows - row0), id = no * per_seq + unit;
+    int lo, hi, range = 0, seq_at = 0, b;  // in tiles: all of them fit 31 bits
     if (p.balanced) {
-        // Every warp adds all sequences' tiles up, each lane a run of them.
-        const int run = (p.n_seqs + 31) / 32;
-        int mine = 0;
-        for (int i = lane * run; i < min(p.n_seqs, (lane + 1) * run); ++i) {
-            const int n = __ldg(p.lens + i);
-            mine += Seen(p, n).tiles;
-            if ((n < 0 || n > p.max_len) && blockIdx.x == 0 && warp == 0) atomicCAS(p.status, 0u, ST_BAD_ID);
-        }
-        int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-            if (lane >= o) upto += v;
-        }
-        const int total = __shfl_sync(0xFFFFFFFFu, upto, 31), ranges = p.grid / per_seq, mine_no = blockIdx.x / per_seq;
-        int item = mine_no, most = ranges;  // what the walk looks for: the block's range, or its first tile
+        bool mine;  // whether there is a range for this block
         if (p.aligned) {
-            // few sequences: whole ranges for each, so that no block has two of them
-            range = max(KV8_SPLIT_MIN, (total + ranges - p.n_seqs - 1) / (ranges - p.n_seqs));
-            mine = 0;
-            for (int i = lane * run; i < min(p.n_seqs, (lane + 1) * run); ++i) mine += (Seen(p, __ldg(p.lens + i)).tiles + range - 1) / range;
-            upto = mine;
+            // up to 32 sequences, one for each lane, and whole ranges for each of them, so that no block has two
+            const int n = lane < p.n_seqs ? __ldg(p.lens + lane) : 0, tiles = Seen(p, n).tiles;
+            if ((n < 0 || n > p.max_len) && id == 0 && warp == 0) atomicCAS(p.status, 0u, ST_BAD_ID);
+            const int total = __reduce_add_sync(0xFFFFFFFFu, tiles), spare = p.ranges - p.n_seqs;
+            range = max(KV8_SPLIT_MIN, (total + spare - 1) / spare);
+            const int own = (tiles + range - 1) / range;
+            int upto = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
                 if (lane >= o) upto += v;
             }
-            most = __shfl_sync(0xFFFFFFFFu, upto, 31);
+            const unsigned behind = __ballot_sync(0xFFFFFFFFu, upto > no);
+            mine = behind;
+            b = mine ? __ffs(behind) - 1 : 0;
+            lo = (no - __shfl_sync(0xFFFFFFFFu, upto - own, b)) * range;
+            hi = min(lo + range, __shfl_sync(0xFFFFFFFFu, tiles, b));
         } else {
-            range = max(KV8_SPLIT_MIN, (total + ranges - 1) / ranges);
-            item = mine_no * range, most = total;
-        }
-        // the first lane whose run ends behind it walks its run
-        const unsigned behind = __ballot_sync(0xFFFFFFFFu, upto > item);
-        const int owner = behind ? __ffs(behind) - 1 : 0;
-        int at = lane * run;
-        seq_at = upto - mine;
-        if (lane == owner && item < most) {
-            for (;; ++at) {
-                int n = Seen(p, __ldg(p.lens + at)).tiles;
-                if (p.aligned) n = (n + range - 1) / range;
-                if (seq_at + n > item) break;
-                seq_at += n;
+            // every warp adds all sequences' tiles up, each lane a run of them
+            const int run = (p.n_seqs + 31) / 32;
+            int tiles = 0;
+            for (int i = lane * run; i < min(p.n_seqs, (lane + 1) * run); ++i) {
+                const int n = __ldg(p.lens + i);
+                tiles += Seen(p, n).tiles;
+                if ((n < 0 || n > p.max_len) && id == 0 && warp == 0) atomicCAS(p.status, 0u, ST_BAD_ID);
             }
+            int upto = tiles;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const int total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+            range = max(KV8_SPLIT_MIN, (total + p.ranges - 1) / p.ranges);
+            lo = no * range, hi = min(total, lo + range);
+            mine = lo < total;
+            // the first lane whose run ends behind lo walks its run
+            const unsigned behind = __ballot_sync(0xFFFFFFFFu, upto > lo);
+            const int owner = behind ? __ffs(behind) - 1 : 0;
+            int at = lane * run;
+            seq_at = upto - tiles;
+            if (lane == owner && mine) {
+                for (;; ++at) {
+                    const int n = Seen(p, __ldg(p.lens + at)).tiles;
+                    if (seq_at + n > lo) break;
+                    seq_at += n;
+                }
+            }
+            b = __shfl_sync(0xFFFFFFFFu, at, owner);
+            seq_at = __shfl_sync(0xFFFFFFFFu, seq_at, owner);
         }
-        b = __shfl_sync(0xFFFFFFFFu, at, owner);
-        seq_at = __shfl_sync(0xFFFFFFFFu, seq_at, owner);
-        // from here on tiles are counted from where the sequence's begin (aligned), or along the line
-        lo = p.aligned ? (item - seq_at) * range : item;
-        seq_at = p.aligned ? 0 : seq_at;
-        hi = lo + range;
-        if (item < most) hi = min(hi, p.aligned ? Seen(p, __ldg(p.lens + b)).tiles : total);
-        for (int i = blockIdx.x; i < p.n_seqs; i += p.grid)
+        for (int i = id; i < p.n_seqs; i += p.grid)
             if (Seen(p, __ldg(p.lens + i)).n == 0) {
                 for (int k = 0; k < p.hkv; ++k) store_none(p, i, k, 0, p.rows);
                 if (p.parts_by_unit)
                     for (int k = tid; k < per_seq; k += C::THREADS) p.parts[i * per_seq + k] = make_int4(0, 0, 0, 0);
             }
-        if (!p.parts_by_unit && tid == 0) p.parts[blockIdx.x] = make_int4(0, 0, 0, 0);
-        if (item >= most) return;
+        if (!p.parts_by_unit && tid == 0) p.parts[id] = make_int4(0, 0, 0, 0);
+        if (!mine) return;
     } else {
-        b = blockIdx.x / per_seq;
+        b = no;
+        if (b >= p.n_seqs) return;
         const int n = __ldg(p.lens + b);
         if ((n < 0 || n > p.max_len) && tid == 0) atomicCAS(p.status, 0u, ST_BAD_ID);
         const Seen seen(p, n);
@@ -364,7 +377,7 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
             store_none(p, b, h, row0, rows);
             return;
         }
-        lo = seq_at = 0, hi = seen.tiles;
+        lo = 0, hi = seen.tiles;
     }
 
     Seen seen(p, __ldg(p.lens + b));
@@ -437,9 +450,10 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
             const int r = warp + k * C::WARPS, row = row0 + r;
             q_raw[k] = make_uint4(0, 0, 0, 0);
             if (r < rows && 8 * lane < p.d) {
-                const long long token = static_cast<long long>(b) * p.n_q + row / p.group;
+                const int2 at = query_of(p, row);
+                const long long token = static_cast<long long>(b) * p.n_q + at.x;
                 q_raw[k] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + token * p.q_token_stride +
-                                                                 (h * p.group + row % p.group) * p.q_head_stride + 8 * lane));
+                                                                 (h * p.group + at.y) * p.q_head_stride + 8 * lane));
             }
         }
 #pragma unroll 1
@@ -614,7 +628,7 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int q_pos = seen.n - p.n_q + (row0 + 8 * j + 2 * t + e) / p.group;
+                        const int q_pos = seen.n - p.n_q + query_of(p, row0 + 8 * j + 2 * t + e).x;
 #pragma unroll
                         for (int x = 0; x < C::XN; ++x)
 #pragma unroll
@@ -718,7 +732,7 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
             }
         __syncthreads();
         const bool whole_unit = i0 == 0 && i1 == seen.tiles;
-        const int part = 2 * static_cast<int>(blockIdx.x) + (pos != lo);
+        const int part = 2 * id + (pos != lo);
         for (int x = tid; x < rows * (DP / 4); x += C::THREADS) {
             const int r = x / (DP / 4), c = x % (DP / 4);
             float top = K8_NEG;
@@ -748,8 +762,8 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
         }
         // the sequence begins here: its parts, if it ends in a later block's range
         if (tid == 0 && p.balanced && i0 == 0 && (p.parts_by_unit || i1 < seen.tiles)) {
-            const int n = (seq_at + seen.tiles - 1) / range - (p.aligned ? 0 : static_cast<int>(blockIdx.x) / per_seq) + 1;
-            p.parts[p.parts_by_unit ? b * per_seq + unit : blockIdx.x] = make_int4(b, unit, part, i1 < seen.tiles ? n : 0);
+            const int n = (seq_at + seen.tiles - 1) / range - (p.aligned ? 0 : no) + 1;
+            p.parts[p.parts_by_unit ? b * per_seq + unit : id] = make_int4(b, unit, part, i1 < seen.tiles ? n : 0);
         }
         pos = seq_at + i1;
         if (pos >= hi) break;
@@ -771,15 +785,15 @@ __global__ void __launch_bounds__(KC_THREADS) kv8_combine_kernel(const __grid_co
 {
     __shared__ float4 s_o[KC_THREADS];
     __shared__ float2 s_ml[KC_THREADS];
-    const int lanes = p.combine_lanes, group = threadIdx.x >> 3, c = threadIdx.x & 7;
-    const int chunks = (p.d + 31) / 32, item = blockIdx.y * (KC_THREADS / 8 / lanes) + group / lanes;
-    const int r = item / chunks, at4 = item % chunks * 32 + 4 * c;  // row, element
+    const int lanes = p.combine_lanes, group = threadIdx.x >> 3, c = threadIdx.x & 7, mine = group & (lanes - 1);
+    const int chunks = (p.d + 31) / 32, item = (blockIdx.y * (KC_THREADS / 8) + group) / lanes;
+    const int r = item / chunks, at4 = (item - r * chunks) * 32 + 4 * c;  // row, element
     pdl_launch_dependents();
     pdl_wait();
     const int4 u = p.parts[blockIdx.x];
     if (u.w == 0) return;
     const int per_seq = p.hkv * p.row_tiles;
-    const int h = u.y / p.row_tiles, row0 = u.y % p.row_tiles * p.tile_rows;
+    const int h = p.row_tiles == 1 ? u.y : u.y / p.row_tiles, row0 = (u.y - h * p.row_tiles) * p.tile_rows;
     const bool there = r < min(p.tile_rows, p.rows - row0) && at4 < p.d;
     float top = K8_NEG, total = 0.0f;
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -792,7 +806,7 @@ __global__ void __launch_bounds__(KC_THREADS) kv8_combine_kernel(const __grid_co
     };
     if (there) {
         constexpr int U = 4;
-        for (int i0 = group % lanes; i0 < u.w; i0 += U * lanes) {
+        for (int i0 = mine; i0 < u.w; i0 += U * lanes) {
             float2 ml[U];
             float4 v[U];
 #pragma unroll
@@ -814,7 +828,7 @@ __global__ void __launch_bounds__(KC_THREADS) kv8_combine_kernel(const __grid_co
         s_ml[threadIdx.x] = make_float2(top, total);
         for (int o = lanes >> 1; o; o >>= 1) {
             __syncthreads();
-            if (group % lanes < o) {
+            if (mine < o) {
                 const float2 ml = s_ml[threadIdx.x + 8 * o];
                 add(ml.x, ml.y, s_o[threadIdx.x + 8 * o]);
                 s_o[threadIdx.x] = sum;
@@ -822,7 +836,7 @@ __global__ void __launch_bounds__(KC_THREADS) kv8_combine_kernel(const __grid_co
             }
         }
     }
-    if (!there || group % lanes) return;
+    if (!there || mine) return;
     const float by = total == 0.0f ? 0.0f : 1.0f / total;
     store_o(p, u.x, h, row0 + r, at4 / 4, make_float4(sum.x * by, sum.y * by, sum.z * by, sum.w * by));
     if (at4 == 0) store_lse(p, u.x, h, row0 + r, top, total);
@@ -854,7 +868,11 @@ cudaError_t launch_nt(const Kv8AttnParams &p, cudaStream_t st)
     if (e != cudaSuccess) return e;
     CUtensorMap k_map, v_map;
     if (!encode(&k_map, p, p.c.k) || !encode(&v_map, p, p.c.v)) return cudaErrorInvalidValue;
-    e = launch_pdl(kv8_attn_kernel<CODE, DP, NT>, dim3(static_cast<unsigned>(p.grid)), C::THREADS, C::SMEM, st, p, k_map, v_map);
+    // (units of a sequence, ranges) or, with a block for each unit, (units, sequences in two dimensions)
+    const unsigned units = static_cast<unsigned>(p.hkv * p.row_tiles), n = static_cast<unsigned>(p.balanced ? p.ranges : p.n_seqs);
+    const unsigned ny = n < 32768 ? n : 32768;
+    const dim3 grid(units, ny, (n + ny - 1) / ny);
+    e = launch_pdl(kv8_attn_kernel<CODE, DP, NT>, grid, C::THREADS, C::SMEM, st, p, k_map, v_map);
     if (e != cudaSuccess || !p.balanced) return e;
     const int items = KC_THREADS / 8 / p.combine_lanes, all = p.tile_rows * ((p.d + 31) / 32);  // of a block, of a unit
     const int blocks = p.parts_by_unit ? p.n_seqs * p.hkv * p.row_tiles : p.grid;

@@ -59,7 +59,8 @@ struct Kv8AttnParams {
     int max_len, window, sinks;
     int rows, row_tiles, tile_rows;  // of a sequence and cache head: n_q * group, in row_tiles of tile_rows
     float scale_log2;
-    int balanced, grid;              // ranges of all tiles over `grid` blocks, or a block for each unit
+    float per_group;                 // 1 / group
+    int balanced, ranges, grid;      // `ranges` of all tiles over `grid` blocks, or a block for each unit
     int aligned;                     // ranges begin with their sequence: there are eight times as many as sequences
     int parts_by_unit;               // there are no more units than blocks
     int4 *parts;                     // of each unit, or block: sequence, unit, first part, parts (0: none)
