@@ -108,7 +108,7 @@ inline Span table_span(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c)
 // Launch shape and workspace of the attention.
 struct Kv8Plan {
     int group, rows, row_tiles, tile_rows, tile_pad;
-    int balanced, ranges, grid, combine_lanes, by_unit, aligned;
+    int balanced, ranges, grid, combine_lanes, by_unit, aligned, wide;
     long long ml_at, parts_at, ws_bytes;
 };
 
@@ -131,10 +131,14 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     a.ml_at = a.parts_at = kCounterArea;
     a.ws_bytes = kCounterArea;
     a.combine_lanes = 1;
-    a.by_unit = a.aligned = a.ranges = 0;
+    a.by_unit = a.aligned = a.ranges = a.wide = 0;
     if (!a.balanced) {
         if (units > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
         a.grid = static_cast<int>(units);
+        // A unit that has a multiprocessor to itself takes all its warps: a warp's time for a tile is
+        // mostly waiting (2 sequences of 700 keys, 2 cache heads: 6.6 us instead of 7.8; of 200: 4.3
+        // instead of 5.3).
+        a.wide = units <= ATTN_SMS && tiles > kv8_warps(c->head_dim, nt);
         return QGEMV_OK;
     }
     // the line of all sequences' tiles in ranges, a block for each range, cache head and tile of rows
@@ -433,6 +437,7 @@ qgemv_status qgemv_attn_kv8(const void *q, qgemv_dtype q_type, int64_t q_token_s
     p.combine_lanes = a.combine_lanes;
     p.parts_by_unit = a.by_unit;
     p.aligned = a.aligned;
+    p.wide = a.wide;
     uint8_t *at = static_cast<uint8_t *>(ws);
     p.parts = reinterpret_cast<int4 *>(at + a.parts_at);
     p.part_ml = reinterpret_cast<float2 *>(at + a.ml_at);

@@ -43,8 +43,9 @@ constexpr float K8_NEG = -1e30f;   // below every finite score; differences of i
 constexpr float K8_LIFT = 10.0f;   // a new reference lies so far below the largest score
 constexpr float K8_SLACK = 14.0f;  // weights reach 2^14 before it moves (f16 ends at 2^16)
 
-// DP: head_dim rounded up to 64, 128 or 256; NT: tiles of 8 query rows.
-template <int DP, int NT>
+// DP: head_dim rounded up to 64, 128 or 256; NT: tiles of 8 query rows; WIDE: one block of
+// twice the warps a multiprocessor instead of two.
+template <int DP, int NT, bool WIDE>
 struct K8Cfg {
     static constexpr int KC = DP / 64;                    // 64-element chunks of a row of K
     static constexpr int VB = DP == 64 ? 8 : 16;          // bytes of a row of V that a thread takes at once
@@ -53,8 +54,8 @@ struct K8Cfg {
     static constexpr int ROW = DP == 64 ? 64 : 128;       // bytes of a row of a copied box
     static constexpr int BOX = KV8_KEYS * ROW;            // of a tile's box; K has DP / ROW of them, then V
     static constexpr int TILE = 2 * KV8_KEYS * DP;
-    static constexpr int BLOCKS = kv8_blocks(DP, NT);
-    static constexpr int WARPS = kv8_warps(DP, NT), THREADS = 32 * WARPS;
+    static constexpr int BLOCKS = WIDE ? 1 : kv8_blocks(DP, NT);
+    static constexpr int WARPS = kv8_warps(DP, NT) * (WIDE ? 2 : 1), THREADS = 32 * WARPS;
     static constexpr int STAGES = DP == 64 ? (NT > 2 ? 4 : 3) : DP == 128 && NT > 2 ? 3 : 2;
     static constexpr bool QREG = DP * NT <= 128;          // Q's fragments in registers
     static constexpr int XN = NT <= 3 ? 2 : 1;            // halves of a tile at once
@@ -269,11 +270,11 @@ __device__ __forceinline__ void store_none(const Kv8AttnParams &p, int b, int h,
     }
 }
 
-template <int CODE, int DP, int NT>
-__global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS) kv8_attn_kernel(
+template <int CODE, int DP, int NT, bool WIDE>
+__global__ void __launch_bounds__(K8Cfg<DP, NT, WIDE>::THREADS, K8Cfg<DP, NT, WIDE>::BLOCKS) kv8_attn_kernel(
     const __grid_constant__ Kv8AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map)
 {
-    using C = K8Cfg<DP, NT>;
+    using C = K8Cfg<DP, NT, WIDE>;
     extern __shared__ __align__(16) uint8_t k8_raw[];
     __shared__ int s_abort;
     uint8_t *k8_smem = k8_raw + ((1024 - (smem_addr(k8_raw) & 1023)) & 1023);
@@ -406,10 +407,10 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT>::THREADS, K8Cfg<DP, NT>::BLOCKS)
             return i < i1 && j < seen.n ? __ldg(table + (j >> p.c.page_shift)) : 0;
         };
         // a lane for each box: of K and V, of each 128 elements, of each half where it is split
-        constexpr int WIDE = DP / C::ROW;
+        constexpr int ACROSS = DP / C::ROW;
         const bool box_v = lane & 1;
-        const int box_x = (lane >> 1) % WIDE, box_half = (lane >> 1) / WIDE;
-        const bool boxes = lane < 2 * WIDE * (split ? 2 : 1);
+        const int box_x = (lane >> 1) % ACROSS, box_half = (lane >> 1) / ACROSS;
+        const bool boxes = lane < 2 * ACROSS * (split ? 2 : 1);
         const uint32_t box_to = s_ring + (box_v ? KV8_KEYS * DP : 0) + box_x * C::BOX + box_half * 16 * C::ROW;
         int ahead = i0 + warp;
         int page = page_of(ahead, 0), page1 = split ? page_of(ahead, 1) : page;
@@ -859,12 +860,12 @@ bool encode(CUtensorMap *map, const Kv8AttnParams &p, const void *base)
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CODE, int DP, int NT>
-cudaError_t launch_nt(const Kv8AttnParams &p, cudaStream_t st)
+template <int CODE, int DP, int NT, bool WIDE>
+cudaError_t launch_wide(const Kv8AttnParams &p, cudaStream_t st)
 {
-    using C = K8Cfg<DP, NT>;
+    using C = K8Cfg<DP, NT, WIDE>;
     static std::atomic<unsigned long long> done{0};
-    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kv8_attn_kernel<CODE, DP, NT>), C::SMEM, done);
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kv8_attn_kernel<CODE, DP, NT, WIDE>), C::SMEM, done);
     if (e != cudaSuccess) return e;
     CUtensorMap k_map, v_map;
     if (!encode(&k_map, p, p.c.k) || !encode(&v_map, p, p.c.v)) return cudaErrorInvalidValue;
@@ -872,12 +873,21 @@ cudaError_t launch_nt(const Kv8AttnParams &p, cudaStream_t st)
     const unsigned units = static_cast<unsigned>(p.hkv * p.row_tiles), n = static_cast<unsigned>(p.balanced ? p.ranges : p.n_seqs);
     const unsigned ny = n < 32768 ? n : 32768;
     const dim3 grid(units, ny, (n + ny - 1) / ny);
-    e = launch_pdl(kv8_attn_kernel<CODE, DP, NT>, grid, C::THREADS, C::SMEM, st, p, k_map, v_map);
+    e = launch_pdl(kv8_attn_kernel<CODE, DP, NT, WIDE>, grid, C::THREADS, C::SMEM, st, p, k_map, v_map);
     if (e != cudaSuccess || !p.balanced) return e;
     const int items = KC_THREADS / 8 / p.combine_lanes, all = p.tile_rows * ((p.d + 31) / 32);  // of a block, of a unit
     const int blocks = p.parts_by_unit ? p.n_seqs * p.hkv * p.row_tiles : p.grid;
     return launch_pdl(kv8_combine_kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>((all + items - 1) / items)),
                       KC_THREADS, 0, st, p, 8 * NT);
+}
+
+template <int CODE, int DP, int NT>
+cudaError_t launch_nt(const Kv8AttnParams &p, cudaStream_t st)
+{
+    if constexpr (kv8_blocks(DP, NT) == 2) {
+        if (p.wide) return launch_wide<CODE, DP, NT, true>(p, st);
+    }
+    return launch_wide<CODE, DP, NT, false>(p, st);
 }
 
 template <int CODE, int DP>

@@ -62,6 +62,7 @@ struct Kv8AttnParams {
     float per_group;                 // 1 / group
     int balanced, ranges, grid;      // `ranges` of all tiles over `grid` blocks, or a block for each unit
     int aligned;                     // ranges begin with their sequence: there are eight times as many as sequences
+    int wide;                        // blocks of twice the warps (kv8_attn.cu)
     int parts_by_unit;               // there are no more units than blocks
     int4 *parts;                     // of each unit, or block: sequence, unit, first part, parts (0: none)
     float *part_o;                   // [2 grid][tile rows, padded][d]
