@@ -17,9 +17,12 @@
 // values than the list holds are read again and taken n at a time, each by a maximum over
 // the block.
 //
-// What bounds it: memory for many rows (logits read once; a maximum, a product, an
-// exponential and a sum for each); the chain launch, logits, ranks, arrival, join for one
-// search, so few rows have small slices.
+// What bounds it: for one search the chain launch, logits, ranks, arrival, join (four rows
+// of 151936 fp32 8.4 us, the join 4 of them), so few rows have small slices.  For many rows, 512 of
+// 128257 bf16 in 35.6 us, 3.7 TB/s: the stream with arrival and join alone takes 26 (512
+// blocks are three or four a multiprocessor), maxima, exponentials and sums 4, keys appended and
+// ranked 6.  With 608, 760 or 1024 blocks it took 43 to 61: each meets its own first values,
+// ranks and arrives.
 #include "kv8_ops.h"
 #include "qgemv_internal.cuh"
 

@@ -5,7 +5,8 @@
 // What bounds it: memory where many rows are copied (read and written once), else
 // the chain of dependent loads parent, length, page, rows.  A block takes one
 // sequence and walks the arrays (k and v of each cache) in steps of the grid, so
-// that this chain is paid once for several copies.
+// that this chain is paid once for several copies.  256 sequences, 36 caches: 46 us, 6.4 TB/s,
+// with blocks for 32 a multiprocessor (for 8 a one 55, 16 51, 128 46); eight of 28 caches 2.5 us.
 #include "kv8_ops.h"
 #include "qgemv_internal.cuh"
 

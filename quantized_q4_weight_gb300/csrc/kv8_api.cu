@@ -124,10 +124,23 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     long long tiles = ceil_div(b->max_len, KV8_KEYS);  // of a unit at most
     if (b->window)
         tiles = std::min(tiles, ceil_div(b->sinks, KV8_KEYS) + ceil_div(b->window + b->n_q - 1, KV8_KEYS) + 1);
-    // Balanced ranges cost a walk over all lengths and a second launch.  Units of up
-    // to four tiles a warp are a block each instead, and so are those of very many
+    // A unit that has a multiprocessor to itself takes all its warps: a warp's time for a tile is
+    // mostly waiting (2 sequences of 700 keys, 2 cache heads: 6.6 us instead of 7.8; of 200: 4.3
+    // instead of 5.3).
+    const int warps1 = kv8_warps(c->head_dim, nt), blocks1 = kv8_blocks(c->head_dim, nt);
+    const bool wide = blocks1 > 1 && units <= ATTN_SMS && tiles > warps1;
+    // Balanced ranges cost a walk over all lengths, units cut in two and a second launch, as
+    // much as three or four tiles of each warp: where full units leave less than that undone in the
+    // last wave of blocks, each is a block.  Under a window they are as long as one another; without,
+    // this holds for 64 tiles at most, so that a long one among short ones costs no more
+    // than ranges would.  32 + 8 heads of 128, window 4096 of 9000 .. 13000 keys, 8 / 16 / 20 / 32 / 38 / 48
+    // sequences: 22.9 / 25.3 / 43.7 / 47.1 / 55.7 / 90.3 us with units, 18.1 / 30.7 / 36.1 / 50.3 / 61.4 /
+    // 73.9 with ranges (idle 6.3 / 1.7 / 10.3 / 3.4 / 0 / 16 tiles a warp).  So are units of very many
     // sequences, which spread over the multiprocessors well enough by themselves.
-    a.balanced = tiles > 24 && b->n_seqs <= 1024 && b->n_seqs * tiles < (1ll << 30);
+    const long long slots = static_cast<long long>(ATTN_SMS) * (wide ? 1 : blocks1), warps = warps1 * (wide ? 2 : 1);
+    const long long idle = ceil_div(units, slots) * slots - units;
+    const bool even = (b->window || tiles <= 64) && 2 * idle * tiles <= 7 * slots * warps;
+    a.balanced = !even && b->n_seqs <= 1024 && b->n_seqs * tiles < (1ll << 30);
     a.ml_at = a.parts_at = kCounterArea;
     a.ws_bytes = kCounterArea;
     a.combine_lanes = 1;
@@ -135,14 +148,11 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     if (!a.balanced) {
         if (units > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
         a.grid = static_cast<int>(units);
-        // A unit that has a multiprocessor to itself takes all its warps: a warp's time for a tile is
-        // mostly waiting (2 sequences of 700 keys, 2 cache heads: 6.6 us instead of 7.8; of 200: 4.3
-        // instead of 5.3).
-        a.wide = units <= ATTN_SMS && tiles > kv8_warps(c->head_dim, nt);
+        a.wide = wide;
         return QGEMV_OK;
     }
     // the line of all sequences' tiles in ranges, a block for each range, cache head and tile of rows
-    const long long per_seq = units / b->n_seqs, blocks = static_cast<long long>(ATTN_SMS) * kv8_blocks(c->head_dim, nt);
+    const long long per_seq = units / b->n_seqs, blocks = static_cast<long long>(ATTN_SMS) * blocks1;
     const long long ranges = std::min(std::max(1ll, blocks / per_seq), ceil_div(b->n_seqs * tiles, KV8_SPLIT_MIN) + b->n_seqs);
     if (ranges * per_seq > INT32_MAX) return QGEMV_ERR_UNSUPPORTED;
     a.ranges = static_cast<int>(ranges);
@@ -297,7 +307,8 @@ qgemv_status qgemv_norm_rope_kv(const qgemv_rope_plan *plan, const qgemv_qk_norm
     int sms = 0;
     const qgemv_status s = device_props(&sms, &r.status);
     if (s != QGEMV_OK) return s;
-    return launch_norm_rope(p, in_type, q ? q_type : QGEMV_F32, to_cache ? cache->type : to_k ? k_type : QGEMV_BF16, plan->layout == QGEMV_ROPE_HALF, vec,
+    return launch_norm_rope(p, in_type, q ? q_type : QGEMV_F32, to_cache ? cache->type : to_k ? k_type : QGEMV_BF16,
+                            plan->layout == QGEMV_ROPE_HALF, vec,
                             n_tokens, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? QGEMV_OK
                : QGEMV_ERR_CUDA;

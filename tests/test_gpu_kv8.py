@@ -467,6 +467,26 @@ def test_attn_absent_pages_and_lengths():
         assert q.device_status() == 0 and torch.equal(a, b) and not bool(a[0].any())
 
 
+@pytest.mark.parametrize("nq,hq,hkv,d", [(8, 16, 2, 128), (5, 16, 2, 64), (8, 8, 1, 256), (4, 24, 4, 96), (1, 12, 2, 128)])
+def test_attn_ranges(nq, hq, hkv, d):
+    """Cut units of each kind of tile: with and without a window, pages of 16 and of 256 rows, pages of no one."""
+    def drop(table):
+        table[0, 3] = -1
+        table[1, 1] = 1 << 20
+    check_attn([2600, 40, 0, 1900], nq, hq, hkv, d, 16, 16, torch.int8, seed=41)
+    check_attn([2600, 40, 0, 1900], nq, hq, hkv, d, 256, 128, torch.float8_e4m3fn, tq=torch.bfloat16, window=1700, sinks=70,
+               seed=42)
+    check_attn([2100, 900, 5000], nq, hq, hkv, d, 64, 32, torch.int8, window=2048, table_edit=drop, want=True, seed=43)
+
+
+@pytest.mark.parametrize("seqs,nq,hq,hkv,d", [(76, 1, 8, 2, 128), (40, 4, 24, 4, 96), (100, 1, 12, 2, 64), (160, 2, 4, 2, 128)])
+def test_attn_windows_that_fill_the_machine(seqs, nq, hq, hkv, d):
+    """Units of a full window, a block each, and some of less."""
+    lens = [int(x) for x in np.random.RandomState(seqs).randint(1200, 1400, seqs)]
+    lens[3], lens[5], lens[-1] = 0, 17, 1025
+    check_attn(lens, nq, hq, hkv, d, 64, 64, torch.float8_e4m3fn, window=1000, sinks=5, seed=44)
+
+
 @pytest.mark.parametrize("lens", [[0], [0, 0, 0], [0, 5000, 0]])
 def test_attn_empty(lens):
     for top in (None, 8192):
