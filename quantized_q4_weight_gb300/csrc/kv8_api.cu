@@ -461,7 +461,8 @@ qgemv_status qgemv_attn_kv8(const void *q, qgemv_dtype q_type, int64_t q_token_s
     int sms = 0;
     s = device_props(&sms, &p.status);
     if (s != QGEMV_OK) return s;
-    return launch_kv8_attn(p, cache->type, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QGEMV_OK : QGEMV_ERR_CUDA;
+    const auto launch = cache->type == QGEMV_CODE_INT8 ? launch_kv8_attn_int8 : launch_kv8_attn_e4m3;
+    return launch(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QGEMV_OK : QGEMV_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------- beams

@@ -1,4 +1,4 @@
-// kv8_attn.cu -- attention over a paged cache of 8-bit codes with a scale for
+// kv8_attn.cuh -- attention over a paged cache of 8-bit codes with a scale for
 // each block of rows and head, under a sliding window with first rows that stay
 // visible (minfer README "How it works": GQA attention whose keys are split
 // over blocks and whose partial results are combined).
@@ -42,9 +42,13 @@
 // for few sequences the chain length, table, page, key, sums, join (8 of 256 / 4096 / 16384 keys,
 // 16 + 2 heads: 6.8 / 8.0 / 15.6 us, the first 5 us whatever the length).  24 rows a cache head need 96 sums of a thread and
 // leave one block of eight warps a multiprocessor, which wait for their own instructions
-// most of the time (window of 4096 keys of 32 sequences, 24 + 4 heads of 96, four queries: 43.5 us
-// with a block a unit, 48.9 with ranges, 51.1 where the products of a tile's halves follow
-// one another instead of taking turns; twelve warps with 16 keys at once spill, 60).
+// most of the time; at 96 elements a head 72 sums and twelve warps, which spill a little
+// (window of 4096 keys of 32 sequences, 24 + 4 heads of 96, four queries: 36.1 us; eight warps 40.2,
+// as heads of 128 43.5, then in ranges 48.9, and 51.1 where the products of a tile's halves
+// follow one another instead of taking turns).  16 keys at once instead of a whole tile
+// spare registers and cost 13 to 40 % (32 rows a cache head).
+#pragma once
+
 #include "kv8_ops.h"
 #include "qgemv_internal.cuh"
 #include "tma.cuh"
@@ -57,22 +61,24 @@ constexpr float K8_NEG = -1e30f;   // below every finite score; differences of i
 constexpr float K8_LIFT = 10.0f;   // a new reference lies so far below the largest score
 constexpr float K8_SLACK = 14.0f;  // weights reach 2^14 before it moves (f16 ends at 2^16)
 
-// DP: head_dim rounded up to 64, 128 or 256; NT: tiles of 8 query rows; WIDE: one block of
+// DP: head_dim rounded up to 64, 96, 128 or 256; NT: tiles of 8 query rows; WIDE: one block of
 // twice the warps a multiprocessor instead of two.
 template <int DP, int NT, bool WIDE>
 struct K8Cfg {
-    static constexpr int KC = DP / 64;                    // 64-element chunks of a row of K
-    static constexpr int VB = DP == 64 ? 8 : 16;          // bytes of a row of V that a thread takes at once
-    static constexpr int VC = DP / (8 * VB);              // such pieces
-    static constexpr int MT = VC * VB / 2;                // 16-row tiles of the sums: DP / 16
+    static constexpr int KC = (DP + 63) / 64;             // 64-element chunks of a row of K, 96's second one of 32
+    static constexpr int VB = DP <= 96 ? 8 : 16;          // bytes of a row of V that a thread takes at once
+    static constexpr int VC = (DP + 8 * VB - 1) / (8 * VB);  // such pieces, 96's second one of half as many
+    static constexpr int MT = DP / 16;                    // 16-row tiles of the sums
     static constexpr int ROW = DP == 64 ? 64 : 128;       // bytes of a row of a copied box
-    static constexpr int BOX = KV8_KEYS * ROW;            // of a tile's box; K has DP / ROW of them, then V
-    static constexpr int TILE = 2 * KV8_KEYS * DP;
+    static constexpr int BOX = KV8_KEYS * ROW;            // of a tile's box; K has ACROSS of them, then V
+    static constexpr int ACROSS = (DP + ROW - 1) / ROW;
+    static constexpr int TILE = 2 * ACROSS * BOX;
     static constexpr int BLOCKS = WIDE ? 1 : kv8_blocks(DP, NT);
     static constexpr int WARPS = kv8_warps(DP, NT) * (WIDE ? 2 : 1), THREADS = 32 * WARPS;
-    static constexpr int STAGES = DP == 64 ? (NT > 2 ? 4 : 3) : DP == 128 && NT > 2 ? 3 : 2;
+    static constexpr int STAGES = DP == 64 ? (NT > 2 ? 4 : 3) : DP <= 128 && NT > 2 ? (WARPS > 8 ? 2 : 3) : 2;
+    static constexpr __device__ int k_steps(int c) { return DP == 96 && c ? 2 : 4; }       // of 16 elements in chunk c
+    static constexpr __device__ int v_words(int c) { return DP == 96 && c ? 1 : VB / 4; }  // of piece c in a row
     static constexpr bool QREG = DP * NT <= 128;          // Q's fragments in registers
-    static constexpr int XN = NT <= 3 ? 2 : 1;            // halves of a tile at once
     static constexpr int OFF_META = WARPS * STAGES * TILE;               // per warp and stage: ks, vs of both halves
     static constexpr int OFF_Q = OFF_META + WARPS * STAGES * 16;
     static constexpr int OFF_QS = OFF_Q + 8 * NT * DP * 2;
@@ -183,6 +189,10 @@ __device__ __forceinline__ void cvt4(unsigned w, unsigned &lo, unsigned &hi)
             : "r"(w));
     }
 }
+__device__ __forceinline__ void lds64(uint32_t at, unsigned &x, unsigned &y)
+{
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(at));
+}
 // e4m3's NaN codes (a row that no one has written may hold them) as 0.
 __device__ __forceinline__ unsigned without_nan(unsigned w)
 {
@@ -191,12 +201,13 @@ __device__ __forceinline__ unsigned without_nan(unsigned w)
 
 // Boxes lie in shared memory with the 16-byte chunks of a row swizzled (by the row's
 // number, or its half with 64-byte rows).  The product's rows 0 .. 7 are these rows
-// of a box's eight, so that neither the reads of K (a row for four lanes, four chunks of it)
-// nor those of V (every second row, half of its chunks) meet a bank twice.
+// of a box's eight, so that neither the reads of K (a row for four lanes, four chunks of it,
+// or two for four of 8 bytes) nor those of V (every second row, half of its chunks, or two) meet a
+// bank twice.
 template <int DP>
 __device__ __forceinline__ int box_row(int k)
 {
-    return DP == 64 ? k ^ (k >> 1 & 1) : (k & 1) << 2 | k >> 1;
+    return DP == 64 ? k ^ (k >> 1 & 1) : DP == 96 ? (k & 1) << 2 | (k & 2) | k >> 2 : (k & 1) << 2 | k >> 1;
 }
 // Byte offset of chunk c of row r.
 template <int DP>
@@ -399,11 +410,15 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT, WIDE>::THREADS, K8Cfg<DP, NT, WI
     int pos = lo;
     // where in a box the thread's bytes of K lie (of 64 elements each) and those of V (of two rows)
     const int pg = box_row<DP>(g);
-    const uint32_t k_off0 = box_off<DP>(pg, t), k_off1 = box_off<DP>(pg, 4 + t);
-    const uint32_t v_off0 = DP == 64 ? box_off<DP>(box_row<DP>(2 * t), g >> 1) + 8 * (g & 1) : box_off<DP>(box_row<DP>(2 * t), pg);
-    const uint32_t v_off1 =
-        DP == 64 ? box_off<DP>(box_row<DP>(2 * t + 1), g >> 1) + 8 * (g & 1) : box_off<DP>(box_row<DP>(2 * t + 1), pg);
-    const int v_unit = DP == 64 ? g : pg;  // of VB elements of a head
+    const uint32_t k_off0 = box_off<DP>(pg, t);
+    const uint32_t k_off1 = DP == 96 ? box_off<DP>(pg, 4 + (t >> 1)) + 8 * (t & 1) : box_off<DP>(pg, 4 + t);
+    const int v_unit = DP <= 96 ? g : pg;  // of VB elements of a head
+    auto v_at = [&](int k) {
+        return C::VB == 8 ? box_off<DP>(box_row<DP>(2 * t + k), g >> 1) + 8 * (g & 1) : box_off<DP>(box_row<DP>(2 * t + k), pg);
+    };
+    const uint32_t v_off0 = v_at(0), v_off1 = v_at(1);
+    const uint32_t v_two0 = DP == 96 ? box_off<DP>(box_row<DP>(2 * t), 4 + (g >> 2)) + 4 * (g & 3) : 0;  // of the second piece
+    const uint32_t v_two1 = DP == 96 ? box_off<DP>(box_row<DP>(2 * t + 1), 4 + (g >> 2)) + 4 * (g & 3) : 0;
     // the warp's ring: tiles on their way and taken, the next to write and to read, the
     // phases to wait for, and whether pages are there (a bit for each stage, and half of it)
     int sent = 0, taken = 0, slot = 0, rd = 0;
@@ -421,11 +436,11 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT, WIDE>::THREADS, K8Cfg<DP, NT, WI
             return i < i1 && j < seen.n ? __ldg(table + (j >> p.c.page_shift)) : 0;
         };
         // a lane for each box: of K and V, of each 128 elements, of each half where it is split
-        constexpr int ACROSS = DP / C::ROW;
+        constexpr int ACROSS = C::ACROSS;
         const bool box_v = lane & 1;
         const int box_x = (lane >> 1) % ACROSS, box_half = (lane >> 1) / ACROSS;
         const bool boxes = lane < 2 * ACROSS * (split ? 2 : 1);
-        const uint32_t box_to = s_ring + (box_v ? KV8_KEYS * DP : 0) + box_x * C::BOX + box_half * 16 * C::ROW;
+        const uint32_t box_to = s_ring + (box_v ? ACROSS * C::BOX : 0) + box_x * C::BOX + box_half * 16 * C::ROW;
         int ahead = i0 + warp;
         int page = page_of(ahead, 0), page1 = split ? page_of(ahead, 1) : page;
         auto issue = [&]() {
@@ -508,8 +523,10 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT, WIDE>::THREADS, K8Cfg<DP, NT, WI
         const uint32_t q_at = s_base + C::OFF_Q + g * DP * 2 + 32 * t, q_x = (g & 1) << 4;
         auto load_q = [&](int j, int c, unsigned (&f)[8]) {  // 16 elements 64 c + 16 t .. of row 8 j + g
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const uint4 v = lds128(q_at + (16 * x ^ q_x) + 8 * j * DP * 2 + 128 * c);
+            for (int x = 0; x < C::k_steps(c) / 2; ++x) {
+                const uint32_t at = DP == 96 && c ? s_base + C::OFF_Q + g * DP * 2 + 128 + (16 * t ^ q_x)
+                                                  : q_at + (16 * x ^ q_x) + 128 * c;
+                const uint4 v = lds128(at + 8 * j * DP * 2);
                 f[4 * x] = v.x, f[4 * x + 1] = v.y, f[4 * x + 2] = v.z, f[4 * x + 3] = v.w;
             }
         };
@@ -537,13 +554,12 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT, WIDE>::THREADS, K8Cfg<DP, NT, WI
         }
 
         // The references that a tile with exponents s, relative to them (-infinity: not seen), asks for.
-        auto raise = [&](float (&s)[C::XN][NT][4]) {
+        auto raise = [&](float (&s)[2][NT][4]) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(s[0][j][e], s[0][j][2 + e]);
-                    if (C::XN == 2) mx = fmaxf(mx, fmaxf(s[C::XN - 1][j][e], s[C::XN - 1][j][2 + e]));
+                    float mx = fmaxf(fmaxf(s[0][j][e], s[0][j][2 + e]), fmaxf(s[1][j][e], s[1][j][2 + e]));
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
                     const unsigned bit = 1u << (2 * j + e);
@@ -553,7 +569,7 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT, WIDE>::THREADS, K8Cfg<DP, NT, WI
                         (e ? nm[j].y : nm[j].x) -= up;
                         (e ? l[j].y : l[j].x) *= by;
 #pragma unroll
-                        for (int x = 0; x < C::XN; ++x) s[x][j][e] -= up, s[x][j][2 + e] -= up;
+                        for (int x = 0; x < 2; ++x) s[x][j][e] -= up, s[x][j][2 + e] -= up;
 #pragma unroll
                         for (int i = 0; i < C::MT; ++i) o[j][i][e] *= by, o[j][i][2 + e] *= by;
                     }
@@ -580,147 +596,153 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT, WIDE>::THREADS, K8Cfg<DP, NT, WI
             const bool whole = j0 + KV8_KEYS - 1 <= seen.n - p.n_q && !gone &&
                                (!p.window || j0 > seen.n - 1 - p.window || j0 + KV8_KEYS - 1 < p.sinks);
 
-            // ---- 16 keys after 16 keys, or both sixteens at once
+            // ---- both sixteens at once
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 // a block of zeros has scale 0: any other does for its codes
                 vs[x] = vs[x] < 8.673617e-19f ? 8.673617e-19f : vs[x];  // 2^-60
                 lv[x] = lg2(vs[x]), inv[x] = rcp(vs[x]);
             }
-#pragma unroll 1
-            for (int x0 = 0; x0 < 2; x0 += C::XN) {
-                auto scale_of = [&](const float (&v)[2], int x) { return C::XN == 2 ? v[x] : x0 ? v[1] : v[0]; };
-                // scores
-                float s[C::XN][NT][4];
+            // scores
+            float s[2][NT][4];
 #pragma unroll
-                for (int c = 0; c < C::KC; ++c) {
-                    unsigned a[C::XN][4][4];
+            for (int c = 0; c < C::KC; ++c) {
+                unsigned a[2][4][4];
 #pragma unroll
-                    for (int h2 = 0; h2 < C::XN; ++h2) {
-                        const uint32_t at =
-                            src + (DP == 64 ? 0 : c >> 1) * C::BOX + 16 * (x0 + h2) * C::ROW + ((c & 1) ? k_off1 : k_off0);
+                for (int h2 = 0; h2 < 2; ++h2) {
+                    const uint32_t at =
+                        src + (DP == 64 ? 0 : c >> 1) * C::BOX + 16 * h2 * C::ROW + ((c & 1) ? k_off1 : k_off0);
+                    unsigned xw[4], yw[4];
+                    if (C::k_steps(c) == 4) {
                         const uint4 x = lds128(at), y = lds128(at + 8 * C::ROW);
-                        const unsigned xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            cvt4<CODE>(xw[k], a[h2][k][0], a[h2][k][2]);
-                            cvt4<CODE>(yw[k], a[h2][k][1], a[h2][k][3]);
-                        }
+                        xw[0] = x.x, xw[1] = x.y, xw[2] = x.z, xw[3] = x.w;
+                        yw[0] = y.x, yw[1] = y.y, yw[2] = y.z, yw[3] = y.w;
+                    } else {
+                        lds64(at, xw[0], xw[1]), lds64(at + 8 * C::ROW, yw[0], yw[1]);
                     }
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        unsigned f[8];
-                        if constexpr (C::QREG) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) f[k] = qf[j][c][k];
-                        } else {
-                            load_q(j, c, f);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int h2 = 0; h2 < C::XN; ++h2) {
-                                const unsigned(&w)[4] = a[h2][k];
-                                if (c == 0 && k == 0)
-                                    mma0(s[h2][j], w[0], w[1], w[2], w[3], f[2 * k], f[2 * k + 1]);
-                                else
-                                    mma(s[h2][j], w[0], w[1], w[2], w[3], f[2 * k], f[2 * k + 1]);
-                            }
+                    for (int k = 0; k < C::k_steps(c); ++k) {
+                        cvt4<CODE>(xw[k], a[h2][k][0], a[h2][k][2]);
+                        cvt4<CODE>(yw[k], a[h2][k][1], a[h2][k][3]);
                     }
                 }
-                // exponents relative to the references in place of the sums
-                float top = -INFINITY;
 #pragma unroll
-                for (int x = 0; x < C::XN; ++x) {
-                    const float2 k2 = make_float2(scale_of(ks, x), scale_of(ks, x));
-                    const float2 v2 = make_float2(scale_of(lv, x), scale_of(lv, x));
+                for (int j = 0; j < NT; ++j) {
+                    unsigned f[8];
+                    if constexpr (C::QREG) {
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const float2 f = mul2(k2, qs[j]), at = add2(v2, nm[j]);
-#pragma unroll
-                        for (int k = 0; k < 4; k += 2) {
-                            const float2 a = fma2(make_float2(s[x][j][k], s[x][j][k + 1]), f, at);
-                            s[x][j][k] = a.x, s[x][j][k + 1] = a.y;
-                            top = fmaxf(top, fmaxf(a.x, a.y));
-                        }
+                        for (int k = 0; k < 2 * C::k_steps(c); ++k) f[k] = qf[j][c][k];
+                    } else {
+                        load_q(j, c, f);
                     }
-                }
-                if (!whole) {
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
+                    for (int k = 0; k < C::k_steps(c); ++k)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int q_pos = seen.n - p.n_q + query_of(p, row0 + 8 * j + 2 * t + e).x;
-#pragma unroll
-                            for (int x = 0; x < C::XN; ++x)
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const int key = j0 + 16 * (x0 + x) + pg + 8 * k;
-                                    const bool sees = key <= q_pos && (!p.window || key > q_pos - p.window || key < p.sinks) &&
-                                                      !(gone >> (x0 + x) & 1);
-                                    if (!sees) s[x][j][2 * k + e] = -INFINITY;
-                                }
+                        for (int h2 = 0; h2 < 2; ++h2) {
+                            const unsigned(&w)[4] = a[h2][k];
+                            if (c == 0 && k == 0)
+                                mma0(s[h2][j], w[0], w[1], w[2], w[3], f[2 * k], f[2 * k + 1]);
+                            else
+                                mma(s[h2][j], w[0], w[1], w[2], w[3], f[2 * k], f[2 * k + 1]);
                         }
                 }
-                if (__any_sync(0xFFFFFFFFu, top > K8_SLACK) || fresh || !whole) raise(s);
-                unsigned pb[C::XN][NT][2];
+            }
+            // exponents relative to the references in place of the sums
+            float top = -INFINITY;
 #pragma unroll
-                for (int x = 0; x < C::XN; ++x)
+            for (int x = 0; x < 2; ++x) {
+                const float2 k2 = make_float2(ks[x], ks[x]);
+                const float2 v2 = make_float2(lv[x], lv[x]);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const float2 a = make_float2(ex2(s[x][j][0]), ex2(s[x][j][1]));
-                        const float2 b = make_float2(ex2(s[x][j][2]), ex2(s[x][j][3]));
-                        float2 sum = add2(a, b);
-                        const float2 i2 = make_float2(scale_of(inv, x), scale_of(inv, x));
-                        if (whole) {
-                            l[j] = fma2(sum, i2, l[j]);
-                        } else {  // a row that sees none of the half takes nothing from its scale either
-                            if (sum.x != 0.0f) l[j].x = fmaf(sum.x, i2.x, l[j].x);
-                            if (sum.y != 0.0f) l[j].y = fmaf(sum.y, i2.y, l[j].y);
-                        }
-                        // The weights are operands in f16: off by half a unit of it.  l keeps them whole.
-                        pb[x][j][0] = movm(pack(a.x, a.y));
-                        pb[x][j][1] = movm(pack(b.x, b.y));
+                for (int j = 0; j < NT; ++j) {
+                    const float2 f = mul2(k2, qs[j]), at = add2(v2, nm[j]);
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2) {
+                        const float2 a = fma2(make_float2(s[x][j][k], s[x][j][k + 1]), f, at);
+                        s[x][j][k] = a.x, s[x][j][k + 1] = a.y;
+                        top = fmaxf(top, fmaxf(a.x, a.y));
                     }
-
-                // weighted sums of v
+                }
+            }
+            if (!whole) {
 #pragma unroll
-                for (int c = 0; c < C::VC; ++c)
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int h2 = 0; h2 < C::XN; ++h2) {
-                        constexpr int W = C::VB / 4;
-                        unsigned v[4][W];
+                    for (int e = 0; e < 2; ++e) {
+                        const int q_pos = seen.n - p.n_q + query_of(p, row0 + 8 * j + 2 * t + e).x;
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const uint32_t at = src + KV8_KEYS * DP + c * C::BOX + (16 * (x0 + h2) + 8 * (r >> 1)) * C::ROW +
-                                                (r & 1 ? v_off1 : v_off0);
-                            if constexpr (W == 4) {
-                                const uint4 x = lds128(at);
-                                v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
-                            } else {
-                                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[r][0]), "=r"(v[r][1]) : "r"(at));
-                            }
-                        }
-                        if (CODE == QGEMV_CODE_E4M3 && !whole) {
+                        for (int x = 0; x < 2; ++x)
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                                for (int k = 0; k < W; ++k) v[r][k] = without_nan(v[r][k]);
-                        }
-#pragma unroll
-                        for (int k = 0; k < W; ++k)
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                // elements 4 k + 2 x and + 1 of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
-                                unsigned a0, a1, a2, a3;
-                                cvt4<CODE>(__byte_perm(v[0][k], v[1][k], x ? 0x7362 : 0x5140), a0, a1);
-                                cvt4<CODE>(__byte_perm(v[2][k], v[3][k], x ? 0x7362 : 0x5140), a2, a3);
-#pragma unroll
-                                for (int j = 0; j < NT; ++j)
-                                    mma(o[j][(C::VB / 2) * c + 2 * k + x], a0, a1, a2, a3, pb[h2][j][0], pb[h2][j][1]);
+                            for (int k = 0; k < 2; ++k) {
+                                const int key = j0 + 16 * x + pg + 8 * k;
+                                const bool sees = key <= q_pos && (!p.window || key > q_pos - p.window || key < p.sinks) &&
+                                                  !(gone >> x & 1);
+                                if (!sees) s[x][j][2 * k + e] = -INFINITY;
                             }
                     }
             }
+            if (__any_sync(0xFFFFFFFFu, top > K8_SLACK) || fresh || !whole) raise(s);
+            unsigned pb[2][NT][2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const float2 a = make_float2(ex2(s[x][j][0]), ex2(s[x][j][1]));
+                    const float2 b = make_float2(ex2(s[x][j][2]), ex2(s[x][j][3]));
+                    float2 sum = add2(a, b);
+                    const float2 i2 = make_float2(inv[x], inv[x]);
+                    if (whole) {
+                        l[j] = fma2(sum, i2, l[j]);
+                    } else {  // a row that sees none of the half takes nothing from its scale either
+                        if (sum.x != 0.0f) l[j].x = fmaf(sum.x, i2.x, l[j].x);
+                        if (sum.y != 0.0f) l[j].y = fmaf(sum.y, i2.y, l[j].y);
+                    }
+                    // The weights are operands in f16: off by half a unit of it.  l keeps them whole.
+                    pb[x][j][0] = movm(pack(a.x, a.y));
+                    pb[x][j][1] = movm(pack(b.x, b.y));
+                }
+
+            // weighted sums of v
+#pragma unroll
+            for (int c = 0; c < C::VC; ++c)
+#pragma unroll
+                for (int h2 = 0; h2 < 2; ++h2) {
+                    constexpr int W = C::VB / 4;
+                    const bool two = DP == 96 && c;
+                    unsigned v[4][W];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t at = src + (C::ACROSS + (DP == 96 ? 0 : c)) * C::BOX +
+                                            (16 * h2 + 8 * (r >> 1)) * C::ROW +
+                                            (two ? r & 1 ? v_two1 : v_two0 : r & 1 ? v_off1 : v_off0);
+                        if constexpr (W == 4) {
+                            const uint4 x = lds128(at);
+                            v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
+                        } else if (two) {
+                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[r][0]) : "r"(at));
+                        } else {
+                            lds64(at, v[r][0], v[r][1]);
+                        }
+                    }
+                    if (CODE == QGEMV_CODE_E4M3 && !whole) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+#pragma unroll
+                            for (int k = 0; k < C::v_words(c); ++k) v[r][k] = without_nan(v[r][k]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < C::v_words(c); ++k)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            // elements 4 k + 2 x and + 1 of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
+                            unsigned a0, a1, a2, a3;
+                            cvt4<CODE>(__byte_perm(v[0][k], v[1][k], x ? 0x7362 : 0x5140), a0, a1);
+                            cvt4<CODE>(__byte_perm(v[2][k], v[3][k], x ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+                                mma(o[j][(C::VB / 2) * c + 2 * k + x], a0, a1, a2, a3, pb[h2][j][0], pb[h2][j][1]);
+                        }
+                }
             __syncwarp();
         }
 
@@ -748,9 +770,9 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT, WIDE>::THREADS, K8Cfg<DP, NT, WI
 #pragma unroll
                 for (int c = 0; c < C::VC; ++c)
 #pragma unroll
-                    for (int k = 0; k < C::VB / 4; ++k) {
+                    for (int k = 0; k < C::v_words(c); ++k) {
                         const int i = (C::VB / 2) * c + 2 * k;
-                        to[(2 * C::VB * c + C::VB / 4 * v_unit + k) ^ t] =
+                        to[(2 * C::VB * c + C::v_words(c) * v_unit + k) ^ t] =
                             make_float4(o[j][i][e], o[j][i][2 + e], o[j][i + 1][e], o[j][i + 1][2 + e]);
                     }
             }
@@ -927,14 +949,10 @@ cudaError_t launch_dp(const Kv8AttnParams &p, cudaStream_t st)
 template <int CODE>
 cudaError_t launch_code(const Kv8AttnParams &p, cudaStream_t st)
 {
-    return p.d <= 64 ? launch_dp<CODE, 64>(p, st) : p.d <= 128 ? launch_dp<CODE, 128>(p, st) : launch_dp<CODE, 256>(p, st);
+    if (p.d > 128) return launch_dp<CODE, 256>(p, st);
+    return p.d <= 64 ? launch_dp<CODE, 64>(p, st) : p.d <= 96 ? launch_dp<CODE, 96>(p, st) : launch_dp<CODE, 128>(p, st);
 }
 
 }  // namespace
-
-cudaError_t launch_kv8_attn(const Kv8AttnParams &p, qgemv_code_type code, cudaStream_t st)
-{
-    return code == QGEMV_CODE_INT8 ? launch_code<QGEMV_CODE_INT8>(p, st) : launch_code<QGEMV_CODE_E4M3>(p, st);
-}
 
 }  // namespace qg

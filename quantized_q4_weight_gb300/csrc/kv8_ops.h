@@ -1,7 +1,7 @@
 // kv8_ops.h -- internal interface between the C ABI (kv8_api.cu) and the
 // kernels of a step over an 8-bit cache and of beam search: norms with the
 // rotation (norm_rope.cu), the cache write (kv8_append.cu), attention over the
-// cache (kv8_attn.cu), the beams' best continuations (beam_select.cu) and the
+// cache (kv8_attn.cuh), the beams' best continuations (beam_select.cu) and the
 // reordering of pages (fork_pages.cu).
 #pragma once
 
@@ -62,7 +62,7 @@ struct Kv8AttnParams {
     float per_group;                 // 1 / group
     int balanced, ranges, grid;      // `ranges` of all tiles over `grid` blocks, or a block for each unit
     int aligned;                     // ranges begin with their sequence: there are eight times as many as sequences
-    int wide;                        // blocks of twice the warps (kv8_attn.cu)
+    int wide;                        // blocks of twice the warps (kv8_attn.cuh)
     int parts_by_unit;               // there are no more units than blocks
     int4 *parts;                     // of each unit, or block: sequence, unit, first part, parts (0: none)
     float *part_o;                   // [2 grid][tile rows, padded][d]
@@ -79,12 +79,15 @@ constexpr int KV8_SPLIT_MIN = 6;     // tiles of a range at least: one for each 
 // Rows of a tile at most, and, for tiles of 8 nt rows, blocks a multiprocessor
 // and warps a block.
 constexpr int kv8_tile_rows(int d) { return d <= 128 ? 32 : 16; }
-constexpr int kv8_blocks(int d, int nt) { return d > 128 || (d > 64 && nt > 2) ? 1 : 2; }
+constexpr int kv8_blocks(int d, int nt) { return d > 128 || (d > 64 && nt > 2) || nt > 3 ? 1 : 2; }
 constexpr int kv8_warps(int d, int nt)
 {
-    return d > 64 && d <= 128 && nt > 2 ? 8 : d <= 64 && nt <= 2 ? 8 : 6;
+    if (d > 128) return 6;
+    return d > 64 && d <= 96 && nt == 3 ? 12 : nt == 4 || (d > 64 && nt == 3) || (d <= 64 && nt <= 2) ? 8 : 6;
 }
-cudaError_t launch_kv8_attn(const Kv8AttnParams &p, qgemv_code_type code, cudaStream_t st);
+// One translation unit for each type of codes (kv8_attn.cuh).
+cudaError_t launch_kv8_attn_int8(const Kv8AttnParams &p, cudaStream_t st);
+cudaError_t launch_kv8_attn_e4m3(const Kv8AttnParams &p, cudaStream_t st);
 
 // ------------------------------------------------------------------- beams
 

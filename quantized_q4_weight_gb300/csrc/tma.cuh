@@ -1,5 +1,5 @@
 // tma.cuh -- tiled copies by tensor maps, for the kernels that read a paged cache
-// by them (attn_tc.cu, kv8_attn.cu).
+// by them (attn_tc.cu, kv8_attn.cuh).
 #pragma once
 
 #include <cuda.h>

@@ -467,6 +467,15 @@ def test_attn_absent_pages_and_lengths():
         assert q.device_status() == 0 and torch.equal(a, b) and not bool(a[0].any())
 
 
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("d", [80, 96])
+@pytest.mark.parametrize("nq,hq,hkv", [(1, 8, 2), (3, 12, 3), (4, 24, 4), (5, 24, 4)])
+def test_attn_heads_up_to_96(nq, hq, hkv, d, code):
+    """One to four tiles of rows, whole and cut units."""
+    check_attn([1, 17, 0, 200, 33, 600], nq, hq, hkv, d, 16, 16, code, seed=45)
+    check_attn([1, 2300, 500], nq, hq, hkv, d, 64, 32, code, tq=torch.bfloat16, to=torch.float32, seed=46)
+
+
 @pytest.mark.parametrize("nq,hq,hkv,d", [(8, 16, 2, 128), (5, 16, 2, 64), (8, 8, 1, 256), (4, 24, 4, 96), (1, 12, 2, 128)])
 def test_attn_ranges(nq, hq, hkv, d):
     """Cut units of each kind of tile: with and without a window, pages of 16 and of 256 rows, pages of no one."""
