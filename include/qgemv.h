@@ -767,9 +767,9 @@ qgemv_status qgemv_norm_rope_kv(const qgemv_rope_plan *plan, const qgemv_qk_norm
  * r * row_stride + h * head_stride bytes; a head's codes are contiguous.  Its
  * scale is k_scale (or v_scale)[g * scale_page_stride + (r / block_size) *
  * scale_block_stride + h * scale_head_stride].  page_size and block_size are
- * powers of two, 16 <= block_size <= page_size; head_dim % 16 == 0,
+ * powers of two, 16 <= block_size <= page_size <= 65536; head_dim % 16 == 0,
  * 16 <= head_dim <= 256.  k and v are 16-byte aligned and their strides
- * multiples of 16; different places must not overlap. */
+ * multiples of 16, not 0; different places must not overlap. */
 typedef enum { QGEMV_CODE_INT8 = 0, QGEMV_CODE_E4M3 = 1 } qgemv_code_type;
 typedef struct {
     void *k;
@@ -800,7 +800,8 @@ typedef struct {
  * with j > p - window or j < sinks.  n_q_heads is a multiple of the cache's
  * n_heads; query head h reads cache head h / (n_q_heads / n_heads).  n_q,
  * n_q_heads, window, sinks and scale are the attention's; qgemv_kv8_append uses
- * n_q alone (and only without `first`). */
+ * n_q alone (and only without `first`).  At most 2^20 sequences, 4096 query heads,
+ * 2^27 query rows (n_seqs * n_q * n_q_heads), and max_len, window and sinks of 2^30. */
 typedef struct {
     int n_seqs;
     int n_q;
@@ -831,7 +832,8 @@ typedef struct {
  * Each step is one fp32 operation; codes are held to +-Q; s' = 0 gives codes
  * 0, and NaN counts as 0 in the maximum and becomes code 0.  An infinite value
  * gives its block an infinite scale.  Rows from lens[b] on are left as they are.
- * Two sequences must not share a page that is written. */
+ * Two sequences must not share a page that is written.  k_stride, v_stride and
+ * the cache's row_stride of 2^31 and more are QGEMV_ERR_UNSUPPORTED. */
 qgemv_status qgemv_kv8_append(const void *k, const void *v, qgemv_dtype in_type, int64_t k_stride, int64_t v_stride,
                               int64_t n_tokens, const qgemv_kv8_cache *cache, const qgemv_kv8_batch *batch,
                               const int32_t *first, int max_new, qgemv_stream_t stream);
@@ -856,7 +858,7 @@ size_t qgemv_attn_kv8_workspace_bytes(const qgemv_kv8_batch *batch, const qgemv_
  * meaningless.  Results do not depend on the order in which the GPU runs the
  * parts.  ws: qgemv_attn_kv8_workspace_bytes, 16-byte aligned.  The heads of o
  * lie apart from one another; o, lse and ws overlap neither one another nor what
- * is read. */
+ * is read.  Strides of codes of 2^40 bytes and more are QGEMV_ERR_UNSUPPORTED. */
 qgemv_status qgemv_attn_kv8(const void *q, qgemv_dtype q_type, int64_t q_token_stride, int64_t q_head_stride,
                             const qgemv_kv8_cache *cache, const qgemv_kv8_batch *batch, void *o, qgemv_dtype o_type,
                             int64_t o_token_stride, int64_t o_head_stride, float *lse_or_null, void *ws,
@@ -930,8 +932,8 @@ typedef struct {
     int32_t *lens_out;
 } qgemv_fork;
 
-/* n_caches caches (layers) of one kind, of the same page count, page size and block
- * size: 16-bit ones or 8-bit ones, the other pointer NULL.  Host arrays, read
+/* n_caches caches (layers) of one kind, of the same page count, page size (65536 rows
+ * at most) and block size: 16-bit ones or 8-bit ones, the other pointer NULL.  Host arrays, read
  * during the call.  One launch for each 64 caches. */
 qgemv_status qgemv_fork_pages(const qgemv_fork *fork, const qgemv_kv_cache *caches, const qgemv_kv8_cache *caches8,
                               int n_caches, qgemv_stream_t stream);
