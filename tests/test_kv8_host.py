@@ -129,7 +129,7 @@ def test_attn_batches(L, bad):
     (dict(q=None), INVALID), (dict(o=None), INVALID), (dict(t=q.F32), INVALID), (dict(ot=q.F16), INVALID), (dict(ot=7), INVALID),
     (dict(qt=-8), INVALID), (dict(os=1 << 60), INVALID), (dict(os=1535), INVALID), (dict(oh=0), INVALID),
     (dict(q=(1 << 30) + 8), MISALIGNED), (dict(qt=1540), MISALIGNED), (dict(qh=100), MISALIGNED), (dict(o=(1 << 31) + 1), MISALIGNED),
-    (dict(lse=(1 << 32) + 2), MISALIGNED), (dict(ws=None), WORKSPACE), (dict(ws_bytes=20000), WORKSPACE),
+    (dict(lse=(1 << 32) + 2), MISALIGNED), (dict(ws=None), WORKSPACE), (dict(ws_bytes=16383), WORKSPACE),
     (dict(ws=(1 << 38) + 8), MISALIGNED), (dict(o=1 << 30), INVALID), (dict(o=1 << 38), INVALID), (dict(o=BIG), INVALID),
     (dict(o=3 * BIG), INVALID), (dict(lse=1 << 31), INVALID), (dict(lse=4 * BIG), INVALID), (dict(ws=1 << 30), INVALID),
     (dict(o=8192), INVALID), (dict(o=4096), INVALID)])
