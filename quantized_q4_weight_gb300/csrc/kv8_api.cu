@@ -121,7 +121,8 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     const int nt = static_cast<int>(ceil_div(a.tile_rows, 8));
     a.tile_pad = 8 * nt;
     const long long units = static_cast<long long>(b->n_seqs) * c->n_heads * a.row_tiles;
-    long long tiles = ceil_div(b->max_len, KV8_KEYS);  // of a unit at most
+    const long long all = ceil_div(b->max_len, KV8_KEYS);
+    long long tiles = all;  // of a unit at most
     if (b->window)
         tiles = std::min(tiles, ceil_div(b->sinks, KV8_KEYS) + ceil_div(b->window + b->n_q - 1, KV8_KEYS) + 1);
     // A unit that has a multiprocessor to itself takes all its warps: a warp's time for a tile is
@@ -131,15 +132,15 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     const bool wide = blocks1 > 1 && units <= ATTN_SMS && tiles > warps1;
     // Balanced ranges cost a walk over all lengths, units cut in two and a second launch, as
     // much as three or four tiles of each warp: where full units leave less than that undone in the
-    // last wave of blocks, each is a block.  Under a window they are as long as one another; without,
-    // this holds for 64 tiles at most, so that a long one among short ones costs no more
-    // than ranges would.  32 + 8 heads of 128, window 4096 of 9000 .. 13000 keys, 8 / 16 / 20 / 32 / 38 / 48
+    // last wave of blocks, each is a block.  Under a window of up to half of max_len most are as long
+    // as one another; else this holds for 64 tiles at most, so that a long one among short ones
+    // costs no more than ranges would.  32 + 8 heads of 128, window 4096 of 9000 .. 13000 keys, 8 / 16 / 20 / 32 / 38 / 48
     // sequences: 22.9 / 25.3 / 43.7 / 47.1 / 55.7 / 90.3 us with units, 18.1 / 30.7 / 36.1 / 50.3 / 61.4 /
     // 73.9 with ranges (idle 6.3 / 1.7 / 10.3 / 3.4 / 0 / 16 tiles a warp).  So are units of very many
     // sequences, which spread over the multiprocessors well enough by themselves.
     const long long slots = static_cast<long long>(ATTN_SMS) * (wide ? 1 : blocks1), warps = warps1 * (wide ? 2 : 1);
     const long long idle = ceil_div(units, slots) * slots - units;
-    const bool even = (b->window || tiles <= 64) && 2 * idle * tiles <= 7 * slots * warps;
+    const bool even = (2 * tiles <= all || tiles <= 64) && 2 * idle * tiles <= 7 * slots * warps;
     a.balanced = !even && b->n_seqs <= 1024 && b->n_seqs * tiles < (1ll << 30);
     a.ml_at = a.parts_at = kCounterArea;
     a.ws_bytes = kCounterArea;
