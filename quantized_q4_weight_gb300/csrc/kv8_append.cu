@@ -11,7 +11,7 @@
 // elements a thread; more are read a second time, from L2).
 //
 // What bounds it: memory for prompts (rows read once, a code written for each
-// element): 24000 rows of 8 + 8 heads of 128, bf16, in 28.3 us, 5.2 TB/s; the rest is
+// element): 24000 rows of 8 + 8 heads of 128, bf16, in 26.6 us, 5.5 TB/s; the rest is
 // that a block's loads stand still while it forms maximum and codes.  For single tokens the
 // chain of dependent loads, lengths, page, row, scale: 2.8 us for 64 of 8 + 8 heads.
 #include <float.h>
@@ -309,10 +309,12 @@ template <typename T, int CODE, bool VEC>
 cudaError_t launch_t(Kv8AppendParams p, cudaStream_t st)
 {
     const long long blocks = static_cast<long long>(p.n_seqs) * p.blocks;
-    // Items one after the other pay once there are some blocks for each multiprocessor.
+    // Items one after the other pay once there are some blocks for each multiprocessor; more than
+    // four leave too few waves of blocks (24000 rows of 8 + 8 heads, up to 2 / 4 / 8 / 16 items: 29.1 /
+    // 26.6 / 28.3 / 30.2 us).
     p.items = 1;
     p.per_piece = (65536 + p.pieces - 1) / p.pieces;
-    while (p.items < 8 && blocks * 2 * p.hkv >= 16ll * ATTN_SMS * p.items && p.items < 2 * p.hkv) p.items *= 2;
+    while (p.items < 4 && blocks * 2 * p.hkv >= 16ll * ATTN_SMS * p.items && p.items < 2 * p.hkv) p.items *= 2;
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((2 * p.hkv + p.items - 1) / p.items));
     const bool wide = min(1 << p.c.block_shift, p.max_new) * p.pieces > 128 * KA_PIECES;
     const auto go = [&](auto kernel, unsigned threads) { return launch_pdl(kernel, grid, threads, 0, st, p); };
