@@ -33,7 +33,7 @@ constexpr int BM_THREADS = 256, BM_WARPS = BM_THREADS / 32, BM_BLOCKS = 4;
 constexpr int BM_CHUNKS = 4;   // 16-byte chunks of a thread's batch; as many are on their way
 constexpr int BM_LIST = 512;   // keys of a block that are ranked at once
 constexpr int BM_FULL = 16;    // appended keys that are worth a ranking: it raises the bound
-constexpr int BM_WAIT = 64;    // keys of a warp in the join
+constexpr int BM_WAIT = 128;   // keys of a warp in the join
 constexpr int BM_BEAMS = 16;
 constexpr int BM_SLICES = 64;  // of a row at most
 constexpr float LOG2E = 1.4426950408889634f;
@@ -209,30 +209,31 @@ __device__ __forceinline__ void sort_warp(V &v)
 }
 
 // A bound that at least n of the block's values reach, to all threads, given each
-// thread's largest value v and that the first `warps` warps have values: the lowest of
-// those warps' ceil(n / warps)-th, or, where one has too few above -infinity, the highest
-// of the warps' n-th.
-__device__ __forceinline__ float low_bound(float v, int n, int warps, unsigned (*s)[BM_WARPS])
+// thread's largest value v and that all threads of the first `warps` warps have values: the
+// lowest of those warps' ceil(n / warps)-th, or, where one has too few above -infinity, the
+// n-th of all threads' (-infinity where there are fewer).  `all` is scratch.
+__device__ __forceinline__ float low_bound(float v, int n, int warps, unsigned (&s)[BM_WARPS], unsigned *all)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned u = ordered(v), top = 0;
-    const auto next = [&](int count) {  // the largest `count` times, each taken out
-        for (int k = 0; k < count; ++k) {
-            top = __reduce_max_sync(0xFFFFFFFFu, u);
-            if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, u == top)) - 1) u = 0;
-        }
-    };
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned mine = ordered(v);
+    unsigned u = mine, top = 0;
     const int each = (n + warps - 1) / warps;
-    next(each);
-    if (lane == 0) s[0][warp] = warp < warps ? top : 0xFFFFFFFFu;
+    for (int k = 0; k < each; ++k) {  // the largest `each` times, each taken out
+        top = __reduce_max_sync(0xFFFFFFFFu, u);
+        if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, u == top)) - 1) u = 0;
+    }
+    if (lane == 0) s[warp] = warp < warps ? top : 0xFFFFFFFFu;
     __syncthreads();
-    const float low = from_ordered(__reduce_min_sync(0xFFFFFFFFu, s[0][lane & (BM_WARPS - 1)]));
+    const float low = from_ordered(__reduce_min_sync(0xFFFFFFFFu, s[lane & (BM_WARPS - 1)]));
     if (low > -INFINITY) return low;
-    next(n - each);
-    if (lane == 0) s[1][warp] = top;
+    all[tid] = mine;
     __syncthreads();
-    const unsigned high = __reduce_max_sync(0xFFFFFFFFu, s[1][lane & (BM_WARPS - 1)]);
-    return high ? from_ordered(high) : -INFINITY;
+    int rank = 0;
+    for (int i = 0; i < BM_THREADS; ++i) rank += all[i] > mine || (all[i] == mine && i < tid);
+    __syncthreads();
+    if (rank == n - 1) s[0] = mine;
+    __syncthreads();
+    return from_ordered(s[0]);
 }
 
 // The best n of list[0 .. total), in order, to its front; THREADS threads, `t` of them this
@@ -283,7 +284,7 @@ struct BeamShared {
     Key order[BM_BEAMS][32];            // the scores of those as integers (0: none)
     float score[BM_BEAMS][32];          // and rounded
     Key best[BM_WARPS];
-    unsigned first[2][BM_WARPS];
+    unsigned first[BM_WARPS];
     int total;                          // keys of the list
     int last;
     float m[BM_BEAMS], sum[BM_BEAMS];
@@ -297,6 +298,8 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long r0 = static_cast<long long>(gi) * p.beams;
     const int per = p.slices * p.n_best;
+    int nth = 1;
+    while (nth < p.n_best && 2 * ((p.n_best + nth - 1) / nth) > min(32, p.slices)) nth = min(2 * nth, p.n_best);
     // Code that one block of a search runs once waits for its instructions: the loops over a
     // warp's rows are not unrolled.
     // each row's n best keys, maximum and sum
@@ -319,11 +322,12 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
 #pragma unroll
                 for (int u = 0; u < U; ++u) k[u] = i0 + 32 * u + lane < per ? __ldcg(part + i0 + 32 * u + lane) : 0;
             };
-            // the slices' first keys bound the n-th from below, where there are n
-            unsigned head = lane < p.slices ? static_cast<unsigned>(__ldcg(part + lane * p.n_best) >> 32) : 0;
+            // Where n / j of the slices have a j-th key of some size, n keys are as large: the bound that
+            // a warp's lanes take first.  j is the least for which half of the slices do.
+            unsigned head = lane < p.slices ? static_cast<unsigned>(__ldcg(part + lane * p.n_best + nth - 1) >> 32) : 0;
             fetch(0);
             sort_warp(head);
-            head = __shfl_sync(0xFFFFFFFFu, head, p.n_best - 1);
+            head = __shfl_sync(0xFFFFFFFFu, head, (p.n_best + nth - 1) / nth - 1);
             Key kth = head ? (static_cast<Key>(head) << 32) - 1 : 0;
             Key *list = s.wait[warp];
             int total = 0;
@@ -338,7 +342,10 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
                     total += __popc(in);
                     const bool end = u == U - 1 && i0 + 32 * U >= per;
                     if (total > BM_WAIT - 32 || end) {
-                        rank_keys<32, BM_WAIT / 32>(list, total, p.n_best, lane, [] { __syncwarp(); });
+                        if (total <= 64)
+                            rank_keys<32, 2>(list, total, p.n_best, lane, [] { __syncwarp(); });
+                        else
+                            rank_keys<32, BM_WAIT / 32>(list, total, p.n_best, lane, [] { __syncwarp(); });
                         total = min(total, p.n_best);
                         if (total == p.n_best) kth = list[p.n_best - 1];
                     }
@@ -511,7 +518,8 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
 
             if (l0 == 0) {
                 if (tid == 0) s.total = 0;
-                bound = low_bound(top, p.n_best, min(BM_WARPS, (span + 32 * E - 1) / (32 * E)), s.first);
+                bound = low_bound(top, p.n_best, max(1, min(BM_WARPS, span / (32 * E))), s.first,
+                                  reinterpret_cast<unsigned *>(s.list));
             }
             const auto taken = [&](float v, unsigned t) { return v > -INFINITY && (v > bound || (v == bound && t <= bound_token)); };
             if (top >= bound && top > -INFINITY) {
