@@ -138,6 +138,24 @@ def test_masked_and_odd_values():
     check(3, 2, 40000, 8, torch.float32, make=few, seed=5)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("beams,vocab,n", [(1, 128257, 1), (1, 128257, 32), (2, 63489, 4), (1, 8193, 32), (1, 2049, 32), (1, 300, 32)])
+def test_thin_last_slices_and_many_best(beams, vocab, n, dtype):
+    check(1, beams, vocab, n, dtype, seed=21)
+
+
+@pytest.mark.parametrize("every", [50, 997])
+@pytest.mark.parametrize("vocab,n", [(20000, 16), (128257, 32), (9000, 5)])
+def test_grammars_that_leave_few(vocab, n, every):
+    """Most logits -infinity: warps without a value, and rows with fewer continuations than wanted."""
+    def make(x):
+        keep = x[:, :, 3::every].clone()
+        x.fill_(-float("inf"))
+        x[:, :, 3::every] = keep
+        x[-1, -1, 100:] = -float("inf")
+    check(2, 2, vocab, n, torch.float32, seed=22, make=make)
+
+
 def test_scores_of_beams_not_alive():
     s = np.array([[0.0, -np.inf, -np.inf], [-np.inf] * 3, [np.nan, -1.0, -2.0]], np.float32)
     check(3, 3, 4000, 6, torch.float32, scores=s)
