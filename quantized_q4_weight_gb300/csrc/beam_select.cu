@@ -287,10 +287,10 @@ struct BeamShared {
     Key best[BM_WARPS];
     unsigned first[BM_WARPS];
     int total;                          // keys of the list
+    int places[BM_WARPS];               // of a warp's list in the join
     int last;
     float m[BM_BEAMS], sum[BM_BEAMS];
     int count;                          // continuations of all rows
-    double lse[BM_BEAMS];
 };
 
 // The join of group gi of the launch, by the block that arrived last.
@@ -304,8 +304,10 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
     // Code that one block of a search runs once waits for its instructions: the loops over a
     // warp's rows are not unrolled.
     // each row's n best keys, maximum and sum
+    const double INF = __longlong_as_double(0x7FF0000000000000ll);
 #pragma unroll 1
     for (int w = warp; w < p.beams; w += BM_WARPS) {
+        const float run = __ldg(p.scores + r0 + w);
         const Key *part = p.part + (r0 + w) * per;
         const float2 *ml = p.part_ml + (r0 + w) * p.slices;
         float m = -INFINITY, sum = 0.0f;
@@ -331,8 +333,34 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
             head = __shfl_sync(0xFFFFFFFFu, head, (p.n_best + nth - 1) / nth - 1);
             Key kth = head ? (static_cast<Key>(head) << 32) - 1 : 0;
             Key *list = s.wait[warp];
+            auto rank_some = [&](int total) {
+                if (total <= 64)
+                    rank_keys<32, 2>(list, total, p.n_best, lane, [] { __syncwarp(); });
+                else
+                    rank_keys<32, BM_WAIT / 32>(list, total, p.n_best, lane, [] { __syncwarp(); });
+            };
             int total = 0;
-            for (int i0 = 0;;) {
+            int *places = &s.places[warp];
+            if (lane == 0) *places = 0;
+            __syncwarp();
+            if (per <= 32 * U) {  // few pass: places in any order, as they are ranked
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (k[u] > kth) {
+                        const int i = atomicAdd(places, 1);
+                        if (i < BM_WAIT) list[i] = k[u];
+                    }
+                __syncwarp();
+                total = *places;
+            }
+            const bool listed = per <= 32 * U && total <= BM_WAIT;
+            if (listed) {
+                rank_some(total);
+                total = min(total, p.n_best);
+            } else {
+                total = 0;
+            }
+            for (int i0 = 0; !listed;) {
 #pragma unroll 1
                 for (int u = 0; u < U; ++u) {
                     Key c = k[0];
@@ -343,10 +371,7 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
                     total += __popc(in);
                     const bool end = u == U - 1 && i0 + 32 * U >= per;
                     if (total > BM_WAIT - 32 || end) {
-                        if (total <= 64)
-                            rank_keys<32, 2>(list, total, p.n_best, lane, [] { __syncwarp(); });
-                        else
-                            rank_keys<32, BM_WAIT / 32>(list, total, p.n_best, lane, [] { __syncwarp(); });
+                        rank_some(total);
                         total = min(total, p.n_best);
                         if (total == p.n_best) kth = list[p.n_best - 1];
                     }
@@ -357,7 +382,6 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
             }
             best = lane < total ? list[lane] : 0;
         }
-        s.rows[w][lane] = best;
 #pragma unroll
         for (int u = 0; u < BM_SLICES / 32; ++u) m = fmaxf(m, mine[u].x);
 #pragma unroll
@@ -367,26 +391,14 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
             if (mine[u].x > -INFINITY) sum = fmaf(mine[u].y, ex2((mine[u].x - m) * LOG2E), sum);
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        if (lane == 0) s.m[w] = m, s.sum[w] = sum;
-    }
-    __syncthreads();
-    const double INF = __longlong_as_double(0x7FF0000000000000ll);
-    if (tid < p.beams) {
-        const float m = s.m[tid], run = __ldg(p.scores + r0 + tid);
         // +infinity among the logits, none above -infinity, or a NaN score: no continuation
         const bool none = !(m < INFINITY) || !(m > -INFINITY) || !(run > -INFINITY);
-        s.lse[tid] = none ? INF : static_cast<double>(m) + log_of(s.sum[tid]);
-        s.m[tid] = none ? 0.0f : run;
-    }
-    if (tid == 0) s.count = 0;
-    __syncthreads();
-#pragma unroll 1
-    for (int w = warp; w < p.beams; w += BM_WARPS) {
-        const Key key = s.rows[w][lane];
-        const double v = static_cast<double>(value_of(key)) - s.lse[w] + static_cast<double>(s.m[w]);
+        const double lse = static_cast<double>(m) + log_of(sum);
+        const double v = none ? -INF : static_cast<double>(value_of(best)) - lse + static_cast<double>(run);
         const long long b = __double_as_longlong(v + 0.0);
         const Key order = b < 0 ? ~static_cast<Key>(b) : static_cast<Key>(b) | 0x8000000000000000ull;
-        const bool there = key != 0 && lane < p.n_best && v > -INF;
+        const bool there = best != 0 && lane < p.n_best && v > -INF;
+        s.rows[w][lane] = best;
         s.order[w][lane] = there ? order : 0;
         s.score[w][lane] = static_cast<float>(v);
         const unsigned in = __ballot_sync(0xFFFFFFFFu, there);
@@ -397,14 +409,17 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
 #pragma unroll 1
     for (int w = warp; w < p.beams; w += BM_WARPS) {
         const Key mine = s.order[w][lane];
-        // how many of the other rows' come before: all above, and equal ones of lower rows
+        // how many of the other rows' come before: all above, and equal ones of lower rows.  A row's
+        // fall, with zeros behind them.
         int rank = lane;
-#pragma unroll 1
+#pragma unroll 4
         for (int o = 0; o < p.beams; ++o) {
             const Key than = mine - (o < w);
-            if (o != w)
-#pragma unroll 4
-                for (int k = 0; k < p.n_best; ++k) rank += s.order[o][k] > than;
+            int at = 0;
+#pragma unroll
+            for (int step = 16; step; step >>= 1) at += s.order[o][at + step - 1] > than ? step : 0;
+            at += s.order[o][at] > than;
+            rank += o != w ? at : 0;
         }
         if (mine && rank < p.n_best) {
             p.score[out + rank] = s.score[w][lane];
@@ -610,10 +625,11 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
     __syncthreads();
     if (tid == 0) {
         const unsigned blocks = static_cast<unsigned>(p.beams) * static_cast<unsigned>(p.slices);
-        __threadfence();
-        s.last = atomicAdd(&p.cnt[gi], 1u) + 1 == blocks;
+        unsigned before;  // releases the block's parts, and acquires the others'
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(p.cnt + gi) : "memory");
+        s.last = before + 1 == blocks;
         if (s.last) p.cnt[gi] = 0;
-        __threadfence();
+        s.count = 0;
     }
     __syncthreads();
     if (s.last) join(p, gi, s);
