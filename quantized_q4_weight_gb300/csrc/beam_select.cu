@@ -343,22 +343,26 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
             int *places = &s.places[warp];
             if (lane == 0) *places = 0;
             __syncwarp();
-            if (per <= 32 * U) {  // few pass: places in any order, as they are ranked
+            for (int i0 = 0;;) {  // few pass: places in any order, as they are ranked
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (k[u] > kth) {
                         const int i = atomicAdd(places, 1);
                         if (i < BM_WAIT) list[i] = k[u];
                     }
-                __syncwarp();
-                total = *places;
+                i0 += 32 * U;
+                if (i0 >= per) break;
+                fetch(i0);
             }
-            const bool listed = per <= 32 * U && total <= BM_WAIT;
+            __syncwarp();
+            total = *places;
+            const bool listed = total <= BM_WAIT;
             if (listed) {
                 rank_some(total);
                 total = min(total, p.n_best);
-            } else {
+            } else {  // all of them again, ranked whenever the list is full
                 total = 0;
+                fetch(0);
             }
             for (int i0 = 0; !listed;) {
 #pragma unroll 1
