@@ -18,9 +18,9 @@
 // the block.
 //
 // What bounds it: for one search the chain launch, logits, ranks, arrival, join (four rows
-// of 151936 fp32 8.4 us, the join 4 of them), so few rows have small slices.  For many rows
+// of 151936 fp32 7.4 us, the join 3 of them), so few rows have small slices.  For many rows
 // memory at its rate behind what does not shrink with the row: 512 rows of 128257 bf16 with 16
-// best take 34.3 us, 67 MB more take 9.1 (7.3 TB/s), rows of 8192 take 12, with one best 9.7.
+// best take 33.1 us, 67 MB more take 9.7 (6.9 TB/s), rows of 8192 take 10.7, with one best 10.0.
 // With 608, 760 or 1024 blocks for the 512 rows it took 43 to 61, with blocks of 128 threads 45:
 // each meets its own first values, ranks and arrives.  Rings of three batches filled by TMA or by
 // 16-byte copies took 43.
