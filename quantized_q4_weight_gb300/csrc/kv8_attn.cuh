@@ -583,6 +583,7 @@ __global__ void __launch_bounds__(K8Cfg<DP, NT, WIDE>::THREADS, K8Cfg<DP, NT, WI
             cp_wait<C::STAGES - 1>();
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(full + rd, phases >> rd & 1, abort_flag, p.status, WAIT_LIMIT_NS)) && ok;
             if (!ok) break;
+            __syncwarp();  // the scales came by copies of lanes 0 .. 3, which a vote orders for no other lane
             const uint32_t src = s_ring + rd * C::TILE;
             float ks[2], vs[2], lv[2], inv[2];
             asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"

@@ -603,3 +603,18 @@ def test_other_stream():
     got = q.attn_kv8(xq, batch, ws, stream=side)
     side.synchronize()
     assert torch.equal(got, out)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("nq,hq,hkv,d", [(1, 12, 2, 128), (1, 14, 2, 64), (4, 24, 4, 96), (2, 4, 2, 256)])
+def test_attn_every_half_of_a_tile_has_its_own_scales(nq, hq, hkv, d, code):
+    """Four lanes copy a tile's scales and all lanes use them: blocks of 16 rows whose scales of k and v are other
+    powers of two from one half of a tile to the next, in units of their own and in ranges, the same bits each time."""
+    def edit(cache, table):
+        for k, s in enumerate((cache.k_scale, cache.v_scale)):
+            s.copy_(torch.exp2(torch.randint(-9, -2, s.shape, generator=gen(60 + k), device=DEV).float()))
+    for lens in ([5, 333, 700], [4000, 31]):
+        out, lse, batch, xq, ws = check_attn(lens, nq, hq, hkv, d, 16, 16, code, edit=edit, seed=61)
+        for _ in range(10):
+            again = torch.empty_like(lse)
+            assert torch.equal(out, q.attn_kv8(xq, batch, ws, out=torch.empty_like(out), lse=again)) and torch.equal(lse, again)
