@@ -24,6 +24,8 @@
 // With 608, 760 or 1024 blocks for the 512 rows it took 43 to 61, with blocks of 128 threads 45:
 // each meets its own first values, ranks and arrives.  Rings of three batches filled by TMA or by
 // 16-byte copies took 43.
+#include <type_traits>
+
 #include "kv8_ops.h"
 #include "qgemv_internal.cuh"
 
@@ -55,6 +57,15 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
         "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmul.rn.f32x2 rd, ra, rb;\n\t"
+        "mov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b)
@@ -397,8 +408,9 @@ __device__ void join(const BeamParams &p, int gi, BeamShared &s)
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
         // +infinity among the logits, none above -infinity, or a NaN score: no continuation
         const bool none = !(m < INFINITY) || !(m > -INFINITY) || !(run > -INFINITY);
-        const double lse = static_cast<double>(m) + log_of(sum);
-        const double v = none ? -INF : static_cast<double>(value_of(best)) - lse + static_cast<double>(run);
+        // x - M first: beside an M of any size the logarithm would be lost
+        const double rel = static_cast<double>(value_of(best)) - static_cast<double>(m);
+        const double v = none ? -INF : rel - log_of(sum) + static_cast<double>(run);
         const long long b = __double_as_longlong(v + 0.0);
         const Key order = b < 0 ? ~static_cast<Key>(b) : static_cast<Key>(b) | 0x8000000000000000ull;
         const bool there = best != 0 && lane < p.n_best && v > -INF;
@@ -510,30 +522,42 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
                 sum *= ex2((m - top) * LOG2E);
                 m = top;
             }
+            // Its terms are 2^(v log2e - m2) with m2 = m log2e rounded, one fused operation each, and what that
+            // rounding leaves, r, is known exactly and taken out of the batch's sum: left in, it would stay in
+            // every term.  Beyond 2^20 (masks of a type's lowest value) r is no longer small, and the
+            // difference v - m is formed first, which for all took 34.6 us instead of 33.5 (512 rows of 128257 bf16).
             if (m > -INFINITY) {
-                const float m2 = m * LOG2E, before = sum;
-                float2 two = make_float2(sum, 0.0f);
+                const float m2 = m * LOG2E;
+                auto terms = [&](auto far) {
+                    float2 two = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int k = 0; k < BM_CHUNKS; ++k)
+                    for (int k = 0; k < BM_CHUNKS; ++k)
 #pragma unroll
-                    for (int i = 0; i < E; i += 2) {
-                        const float2 e = fma2(make_float2(C::at(cur[k], i), C::at(cur[k], i + 1)), make_float2(LOG2E, LOG2E),
-                                              make_float2(-m2, -m2));
-                        two = add2(two, make_float2(ex2(e.x), ex2(e.y)));
-                    }
-                sum = two.x + two.y;
-                if (!(sum < INFINITY)) {  // a NaN among them counts nothing
-                    sum = before;
+                        for (int i = 0; i < E; i += 2) {
+                            const float2 v = make_float2(C::at(cur[k], i), C::at(cur[k], i + 1)), l2 = make_float2(LOG2E, LOG2E);
+                            const float2 e = far.value ? mul2(add2(v, make_float2(-m, -m)), l2) : fma2(v, l2, make_float2(-m2, -m2));
+                            two = add2(two, make_float2(ex2(e.x), ex2(e.y)));
+                        }
+                    return two.x + two.y;
+                };
+                float more;
+                if (fabsf(m) <= 1048576.0f)
+                    more = terms(std::false_type()) * ex2(-fmaf(m, LOG2E, -m2));
+                else
+                    more = terms(std::true_type());
+                if (!(more < INFINITY)) {  // a NaN among them counts nothing
+                    more = 0.0f;
 #pragma unroll 1
                     for (int k = 0; k < BM_CHUNKS; ++k) {
                         const uint4 c = pick(cur, k);
 #pragma unroll
                         for (int i = 0; i < E; ++i) {
                             const float v = C::at(c, i);
-                            if (v == v) sum += ex2(fmaf(v, LOG2E, -m2));
+                            if (v == v) more += ex2((v - m) * LOG2E);
                         }
                     }
                 }
+                sum += more;
             }
 
             if (l0 == 0) {
