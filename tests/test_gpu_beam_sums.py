@@ -125,3 +125,23 @@ def test_large_logits():
     """Spread over tens of thousands: the largest's probability is 1."""
     check(3, 3000, 6, torch.float32, lambda x: x.mul_(1e4), seed=15)
     check(2, 50021, 4, torch.bfloat16, lambda x: x.mul_(300.0), seed=16)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_maxima_that_come_late(dtype):
+    """A row's largest value in its last batch, up to 39 above all before it.
+
+    The reference follows within 8, so a term's exponent, below 11.55, is off by 2^-21 at most (3.3e-7 of the term),
+    log2 e by 2^-26 of it (1.1e-7), ex2 by 2^-22, and ten or so additions, in order of size, by 2^-24 each: 1.3e-6."""
+    rows, vocab = 1024, 20011
+    rng = np.random.RandomState(17)
+    x = rng.uniform(-1, 1, (rows, vocab)).astype(np.float32)
+    at = rng.randint(vocab - 500, vocab, rows)
+    x[np.arange(rows), at] = rng.uniform(5, 39, rows)
+    x = torch.from_numpy(x).to(dtype)
+    step = q.BeamStep(rows, 1, vocab, 1, torch.zeros((rows, 1), device=DEV))
+    score, token, _ = q.beam_select(x.to(DEV), step, q.new_workspace(step.workspace_bytes()))
+    best = torch.log_softmax(x.double(), 1)[torch.arange(rows), torch.from_numpy(at)]
+    assert token[:, 0].tolist() == at.tolist() and q.device_status() == 0
+    off = (score[:, 0].cpu().double() - best).abs() - 2.0 ** -24 * best.abs()
+    assert float(off.max()) <= 1.3e-6, float(off.max())
