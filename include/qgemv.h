@@ -769,7 +769,9 @@ qgemv_status qgemv_norm_rope_kv(const qgemv_rope_plan *plan, const qgemv_qk_norm
  * scale_block_stride + h * scale_head_stride].  page_size and block_size are
  * powers of two, 16 <= block_size <= page_size <= 65536; head_dim % 16 == 0,
  * 16 <= head_dim <= 256.  k and v are 16-byte aligned and their strides
- * multiples of 16, not 0; different places must not overlap. */
+ * multiples of 16, not 0; different places must not overlap.  Strides of 0 between
+ * scales (one for several blocks or heads) are for reading alone: the attention takes them,
+ * calls that write a cache refuse them. */
 typedef enum { QGEMV_CODE_INT8 = 0, QGEMV_CODE_E4M3 = 1 } qgemv_code_type;
 typedef struct {
     void *k;

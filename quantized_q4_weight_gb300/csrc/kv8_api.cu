@@ -44,6 +44,13 @@ inline Span scale_span(const qgemv_kv8_cache *c, const void *base)
                            (c->page_size / c->block_size - 1) * c->scale_block_stride +
                            (c->n_heads - 1) * c->scale_head_stride + 1));
 }
+// Whether each block and head has scales of its own, as a call that writes them needs (a read of one
+// scale for several is well).
+inline bool own_scales(const qgemv_kv8_cache *c)
+{
+    return (c->n_pages == 1 || c->scale_page_stride) && (c->page_size == c->block_size || c->scale_block_stride) &&
+           (c->n_heads == 1 || c->scale_head_stride);
+}
 // The four arrays of a cache lie apart.
 bool arrays_apart(const qgemv_kv8_cache *c)
 {
@@ -329,7 +336,8 @@ qgemv_status qgemv_kv8_append(const void *k, const void *v, qgemv_dtype in_type,
         return QGEMV_ERR_INVALID_ARG;
     if (!first && (n_tokens != static_cast<long long>(b.n_seqs) * b.n_q || max_new < b.n_q)) return QGEMV_ERR_INVALID_ARG;
     if (n_tokens > 0 && (!k || !v)) return QGEMV_ERR_INVALID_ARG;
-    if (!extent_ok(n_tokens, k_stride) || !extent_ok(n_tokens, v_stride) || !arrays_apart(cache)) return QGEMV_ERR_INVALID_ARG;
+    if (!extent_ok(n_tokens, k_stride) || !extent_ok(n_tokens, v_stride) || !own_scales(cache) || !arrays_apart(cache))
+        return QGEMV_ERR_INVALID_ARG;
     const int ib = type_bytes(in_type), d = cache->head_dim;
     if (!aligned(k, ib) || !aligned(v, ib) || !aligned(b.lens, 4) || !aligned(b.pages, 4) || !aligned(first, 4))
         return QGEMV_ERR_MISALIGNED;
@@ -555,6 +563,7 @@ qgemv_status qgemv_fork_pages(const qgemv_fork *fork, const qgemv_kv_cache *cach
     for (int i = 0; i < n_caches; ++i) {
         const qgemv_status s = caches ? check_cache(caches + i) : check_cache8(caches8 + i);
         if (s != QGEMV_OK) return s;
+        if (!caches && !own_scales(caches8 + i)) return QGEMV_ERR_INVALID_ARG;
         const long long pages = caches ? caches[i].n_pages : caches8[i].n_pages;
         const int shape[5] = {caches ? caches[i].page_size : caches8[i].page_size, caches ? 0 : caches8[i].block_size,
                               caches ? caches[i].n_heads : caches8[i].n_heads,

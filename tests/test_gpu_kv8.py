@@ -618,3 +618,24 @@ def test_attn_every_half_of_a_tile_has_its_own_scales(nq, hq, hkv, d, code):
         for _ in range(10):
             again = torch.empty_like(lse)
             assert torch.equal(out, q.attn_kv8(xq, batch, ws, out=torch.empty_like(out), lse=again)) and torch.equal(lse, again)
+
+
+def test_attn_reads_one_scale_for_a_whole_cache():
+    """Expanded scales, strides of 0: the same bits as with a scale for each; what writes them refuses."""
+    g = gen(62)
+    cache = make_cache(20, 32, 16, 2, 64, torch.int8, g)
+    one = [torch.tensor([[[s]]], device=DEV) for s in (0.02, 0.03)]
+    shared = q.Kv8Cache(cache.k, cache.v, *(x.expand(20, 2, 2) for x in one))
+    each = q.Kv8Cache(cache.k, cache.v, *(x.expand(20, 2, 2).contiguous() for x in one))
+    lens, table = torch.tensor([300, 70], dtype=torch.int32, device=DEV), make_table([300, 70], 32, 10, 20, g)
+    xq = torch.randn((2, 1, 8, 64), generator=g, device=DEV).to(torch.float16)
+    outs = []
+    for c in (shared, each):
+        batch = q.Kv8Batch(2, 1, 8, c, lens, table, 320)
+        outs.append(q.attn_kv8(xq, batch, q.new_workspace(batch.workspace_bytes())))
+    assert torch.equal(*outs)
+    x = torch.randn((2, 2, 64), generator=g, device=DEV)
+    with pytest.raises(Exception, match="qgemv_kv8_append"):
+        q.kv8_append(x, x, q.Kv8Batch(2, 1, 8, shared, lens, table, 320))
+    with pytest.raises(Exception, match="qgemv_fork_pages"):
+        q.fork_pages(q.PagePool([shared]), lens * 0, lens, table, lens * 0 - 1, torch.zeros_like(table), torch.zeros_like(lens))

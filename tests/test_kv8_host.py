@@ -342,3 +342,16 @@ def test_constructors_refuse_what_does_not_fit():
         q.BeamStep(1, 4, 100, 4, torch.zeros(4))
     with pytest.raises(ValueError, match="PagePool"):
         q.PagePool([])
+
+
+@pytest.mark.parametrize("shared", ["scale_page_stride", "scale_block_stride", "scale_head_stride"])
+def test_scales_of_several_blocks_are_for_reading(L, shared):
+    """A stride of 0 between scales: two blocks would write one float.  The attention only reads them."""
+    c = cache8(**{shared: 0})
+    assert append(L, c) == INVALID and append(L, c, first=1 << 20, n=0, most=60, k=None, v=None) == INVALID
+    assert fork(L, [c]) == INVALID and fork(L, [cache8(k=5 * BIG, v=6 * BIG, k_scale=7 * BIG, v_scale=8 * BIG), c]) == INVALID
+    assert outcome(attn(L, c)) == ACCEPTED and attn_ws(L, batch8(), c) > 0
+    # strides that nothing is reached by may be 0
+    one = dict(scale_page_stride=dict(n_pages=1), scale_block_stride=dict(block_size=64), scale_head_stride=dict(n_heads=1))
+    c = cache8(**{shared: 0}, **one[shared])
+    assert outcome(append(L, c)) == ACCEPTED and outcome(fork(L, [c])) == ACCEPTED
