@@ -51,13 +51,47 @@ inline bool own_scales(const qgemv_kv8_cache *c)
     return (c->n_pages == 1 || c->scale_page_stride) && (c->page_size == c->block_size || c->scale_block_stride) &&
            (c->n_heads == 1 || c->scale_head_stride);
 }
-// The four arrays of a cache lie apart.
+// Whether two arrays of one shape, the second `delta` bytes behind the first, share bytes: n[i] places
+// at each of three strides s[i], falling, of `width` bytes each.  Arrays that interleave (k and v by pages, rows or
+// heads of one buffer) do not; one whose strides do not nest counts as if it did wherever it may.
+bool places_meet(long long delta, const long long (&n)[3], const long long (&s)[3], long long width, int i = 0)
+{
+    if (i == 3) return delta < width && -delta < width;
+    if (n[i] == 1) return places_meet(delta, n, s, width, i + 1);
+    long long inner = width;  // that one step of this stride reaches over
+    for (int j = i + 1; j < 3; ++j) inner += (n[j] - 1) * s[j];
+    const auto floor_div = [](long long a, long long b) { return a / b - (a % b < 0); };
+    const long long lo = std::max(1 - n[i], floor_div(delta - inner, s[i]) + 1), hi = std::min(n[i] - 1, floor_div(delta + inner - 1, s[i]));
+    if (hi - lo > 2) return true;
+    for (long long k = lo; k <= hi; ++k)
+        if (places_meet(delta - k * s[i], n, s, width, i + 1)) return true;
+    return false;
+}
+bool arrays_meet(const void *a, const void *b, long long (&&n)[3], long long (&&s)[3], long long width)
+{
+    for (int i = 0; i < 2; ++i)
+        for (int j = 2; j > i; --j)
+            if (s[j] > s[j - 1]) std::swap(s[j], s[j - 1]), std::swap(n[j], n[j - 1]);
+    return places_meet(static_cast<long long>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)), n, s, width);
+}
+// The four arrays of a cache lie apart; codes and scales in one buffer by whole pages.
 bool arrays_apart(const qgemv_kv8_cache *c)
 {
-    const Span s[4] = {codes_span(c, c->k), codes_span(c, c->v), scale_span(c, c->k_scale), scale_span(c, c->v_scale)};
-    for (int i = 0; i < 4; ++i)
-        for (int j = i + 1; j < 4; ++j)
-            if (overlap(s[i], s[j])) return false;
+    const int blocks = c->page_size / c->block_size;
+    if (overlap(codes_span(c, c->k), codes_span(c, c->v)) &&
+        arrays_meet(c->k, c->v, {c->n_pages, c->page_size, c->n_heads}, {c->page_stride, c->row_stride, c->head_stride}, c->head_dim))
+        return false;
+    if (overlap(scale_span(c, c->k_scale), scale_span(c, c->v_scale)) &&
+        arrays_meet(c->k_scale, c->v_scale, {c->n_pages, blocks, c->n_heads},
+                    {4 * c->scale_page_stride, 4 * c->scale_block_stride, 4 * c->scale_head_stride}, 4))
+        return false;
+    for (const void *codes : {c->k, c->v})
+        for (const float *scales : {c->k_scale, c->v_scale}) {
+            const Rows a{codes, c->n_pages, c->page_stride, (c->page_size - 1) * c->row_stride + (c->n_heads - 1) * c->head_stride + c->head_dim};
+            const Rows b{scales, c->n_pages, 4 * c->scale_page_stride,
+                         4 * ((blocks - 1) * c->scale_block_stride + (c->n_heads - 1) * c->scale_head_stride + 1)};
+            if (rows_overlap(a, b)) return false;
+        }
     return true;
 }
 

@@ -639,3 +639,24 @@ def test_attn_reads_one_scale_for_a_whole_cache():
         q.kv8_append(x, x, q.Kv8Batch(2, 1, 8, shared, lens, table, 320))
     with pytest.raises(Exception, match="qgemv_fork_pages"):
         q.fork_pages(q.PagePool([shared]), lens * 0, lens, table, lens * 0 - 1, torch.zeros_like(table), torch.zeros_like(lens))
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_k_and_v_in_one_buffer(code):
+    """[pages][2][rows][heads][d] and scales beside it: what caches of their own give, step by step."""
+    g = gen(63)
+    cache = make_cache(12, 32, 16, 2, 64, code, g)
+    both = torch.stack([cache.k.view(torch.uint8), cache.v.view(torch.uint8)], 1).view(code)
+    scales = torch.stack([cache.k_scale, cache.v_scale], 1)
+    one = q.Kv8Cache(both[:, 0], both[:, 1], scales[:, 0], scales[:, 1])
+    lens, table = torch.tensor([70, 200], dtype=torch.int32, device=DEV), make_table([70, 200], 32, 7, 12, g)
+    x = [3 * torch.randn((6, 2, 64), generator=g, device=DEV) for _ in range(2)]
+    xq = torch.randn((2, 3, 8, 64), generator=g, device=DEV).to(torch.float16)
+    outs = []
+    for c in (cache, one):
+        batch = q.Kv8Batch(2, 3, 8, c, lens, table, 224)
+        q.kv8_append(*x, batch)
+        outs.append(q.attn_kv8(xq, batch, q.new_workspace(batch.workspace_bytes())))
+    assert torch.equal(*outs) and q.device_status() == 0
+    for a, b in ((cache.k, one.k), (cache.v, one.v), (cache.k_scale, one.k_scale), (cache.v_scale, one.v_scale)):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))

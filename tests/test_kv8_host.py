@@ -355,3 +355,52 @@ def test_scales_of_several_blocks_are_for_reading(L, shared):
     one = dict(scale_page_stride=dict(n_pages=1), scale_block_stride=dict(block_size=64), scale_head_stride=dict(n_heads=1))
     c = cache8(**{shared: 0}, **one[shared])
     assert outcome(append(L, c)) == ACCEPTED and outcome(fork(L, [c])) == ACCEPTED
+
+
+def test_codes_of_k_and_v_may_interleave(L):
+    """k and v as halves of one buffer's pages, rows or heads; and what lies over one another by a byte is refused."""
+    d, heads, page = 128, 2, 64
+    row = heads * d
+    for kw, step in ((dict(page_stride=2 * page * row, row_stride=row, head_stride=d), page * row),      # [pages][2][rows][heads]
+                     (dict(page_stride=2 * page * row, row_stride=2 * row, head_stride=d), row),          # [pages][rows][2][heads]
+                     (dict(page_stride=2 * page * row, row_stride=2 * row, head_stride=2 * d), d),         # [pages][rows][heads][2]
+                     (dict(page_stride=2 * page * row, row_stride=d, head_stride=2 * page * d), page * d),  # [pages][heads][2][rows]
+                     (dict(page_stride=page * d, row_stride=d, head_stride=200 * page * d), 100 * page * d)):  # [heads][2][pages]
+        for way in (1, -1):
+            assert outcome(append(L, cache8(v=BIG + way * step, **kw))) == ACCEPTED, (kw, way)
+            assert append(L, cache8(v=BIG + way * (step - 16), **kw)) == INVALID, (kw, way)
+    assert append(L, cache8(v=BIG)) == INVALID and append(L, cache8(v=BIG + 99 * page * row + 63 * row + 128 + 112)) == INVALID
+
+
+def test_scales_may_interleave_with_one_another_and_with_the_codes(L):
+    for kw, step in ((dict(scale_page_stride=16, scale_block_stride=2, scale_head_stride=1), 8),
+                     (dict(scale_page_stride=16, scale_block_stride=4, scale_head_stride=1), 2),
+                     (dict(scale_page_stride=16, scale_block_stride=4, scale_head_stride=2), 1)):
+        assert outcome(append(L, cache8(v_scale=3 * BIG + 4 * step, **kw))) == ACCEPTED
+        assert append(L, cache8(v_scale=3 * BIG + (4 * step - 4 if step > 1 else 0), **kw)) == INVALID
+    # pages that end in their scales
+    codes = 64 * 256
+    kw = dict(page_stride=codes + 64, scale_page_stride=(codes + 64) // 4)
+    assert outcome(append(L, cache8(k_scale=BIG + codes, **kw))) == ACCEPTED
+    assert append(L, cache8(k_scale=BIG + codes - 4, **kw)) == INVALID
+    assert append(L, cache8(k_scale=BIG + codes + 36, **kw)) == INVALID      # the last ones in the next page's codes
+
+
+def test_places_against_a_plain_count(L):
+    """Small caches at every distance of k from v: accepted where a list of all bytes has none twice."""
+    import random
+    rng = random.Random(9)
+    for _ in range(300):
+        n = [rng.randint(1, 3), 16, rng.randint(1, 3)]
+        order = rng.sample(range(3), 3)
+        s, at = [0, 0, 0], 16
+        for i in order:
+            s[i] = at * rng.choice([1, 1, 2])
+            at = s[i] * n[i]
+        places = sorted(a * s[0] + b * s[1] + c * s[2] for a in range(n[0]) for b in range(n[1]) for c in range(n[2]))
+        for delta in rng.sample(range(0, 2 * at + 32, 16), min(8, (2 * at + 32) // 16)):
+            meets = bool(set(places) & {x + delta for x in places})
+            c = cache8(n_pages=n[0], page_size=16, block_size=16, n_heads=n[2], head_dim=16, page_stride=s[0], row_stride=s[1],
+                       head_stride=s[2], v=BIG + delta, scale_page_stride=n[2])
+            got = append(L, c, ks=16 * n[2], vs=16 * n[2])
+            assert got == INVALID if meets else outcome(got) == ACCEPTED, (n, s, delta)
