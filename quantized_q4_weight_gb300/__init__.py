@@ -741,7 +741,10 @@ def norm_rope_kv(plan: RopePlan, norm: QkNorm, xq, xk, xv=None, pos=None, slots=
     """rope_kv with q and k normed head by head first.  Without a cache the rotated k goes to
     k_out (fp32, f16 or bf16), and v is the caller's to write (kv8_append); xv and slots
     are then None, and out defaults to a tensor of q's type.  Returns out."""
-    if (xk if xq is None else xq).shape[-1] != norm.head_dim:
+    some = xk if xq is None else xq
+    if some is None:
+        raise ValueError("norm_rope_kv: q or k")
+    if some.shape[-1] != norm.head_dim:
         raise ValueError("norm_rope_kv: norm of q's and k's head_dim")
     r = (_ext or _load_binding()).norm_rope_kv(plan, norm.struct, xq, xk, xv, pos, slots,
                                                None if cache is None else cache.struct, out, k_out,

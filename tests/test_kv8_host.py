@@ -404,3 +404,8 @@ def test_places_against_a_plain_count(L):
                        head_stride=s[2], v=BIG + delta, scale_page_stride=n[2])
             got = append(L, c, ks=16 * n[2], vs=16 * n[2])
             assert got == INVALID if meets else outcome(got) == ACCEPTED, (n, s, delta)
+
+
+def test_norm_rope_of_nothing_is_refused():
+    with pytest.raises(ValueError, match="q or k"):
+        q.norm_rope_kv(q.rope_plan(64, 1e4), q.QkNorm(None, None), None, None)
