@@ -719,6 +719,13 @@ def logits_rules(x, rules: LogitsRules, ws, out=None, idx=None, val=None, stream
 
 # ------------------------------------- over an 8-bit cache, and beam search
 
+def _on(device, x, what: str):
+    """Tensor x, if there is one, lies on the device of what a call is described by: the kernel
+    that gets both runs on one (the binding holds a call's other tensors against the first)."""
+    if x is not None and device is not None and x.device != device:
+        raise ValueError(f"{what} on {device}")
+
+
 class QkNorm(_Described):
     """Weights fp32 [head_dim] and eps of the norms of q and k, head by head (see
     qgemv_qk_norm); one may be None where that side is not rotated."""
@@ -729,6 +736,8 @@ class QkNorm(_Described):
                 raise ValueError("QkNorm: weights fp32 [head_dim], contiguous")
         if q_weight is not None and k_weight is not None and q_weight.numel() != k_weight.numel():
             raise ValueError("QkNorm: weights of one head_dim")
+        self.device = next((w.device for w in (q_weight, k_weight) if w is not None), None)
+        _on(self.device, k_weight, "QkNorm: both weights")
         self.weights = (q_weight, k_weight)
         some = k_weight if q_weight is None else q_weight
         self.head_dim = 0 if some is None else some.numel()
@@ -746,6 +755,9 @@ def norm_rope_kv(plan: RopePlan, norm: QkNorm, xq, xk, xv=None, pos=None, slots=
         raise ValueError("norm_rope_kv: q or k")
     if some.shape[-1] != norm.head_dim:
         raise ValueError("norm_rope_kv: norm of q's and k's head_dim")
+    _on(norm.device, some, "norm_rope_kv: q and k, beside the weights,")
+    if cache is not None:
+        _on(cache.k.device, some, "norm_rope_kv: q and k, beside the cache,")
     r = (_ext or _load_binding()).norm_rope_kv(plan, norm.struct, xq, xk, xv, pos, slots,
                                                None if cache is None else cache.struct, out, k_out,
                                                None if stream is None else stream.cuda_stream)
@@ -769,7 +781,7 @@ class Kv8Cache(_Described):
             raise ValueError("Kv8Cache: k_scale and v_scale fp32 [pages][page_size / block_size][heads] of the same strides")
         if not (k.is_cuda and all(x.device == k.device for x in (v, k_scale, v_scale))):
             raise ValueError("Kv8Cache: CUDA tensors of one device")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, k.device
         self.struct = Kv8CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _CODES[k.dtype],
                                      k.shape[0], k.shape[1], k.shape[1] // k_scale.shape[1], k.shape[2], k.shape[3],
                                      k.stride(0), k.stride(1), k.stride(2), *k_scale.stride())
@@ -786,6 +798,8 @@ class Kv8Batch(_Described):
                             pages.shape[1] * cache.struct.page_size < max_len or not pages.is_cuda or
                             pages.dtype != torch.int32):
             raise ValueError("Kv8Batch: pages int32 [n_seqs][pages that hold max_len rows]")
+        _on(cache.device, lens, "Kv8Batch: lens, beside the cache,")
+        _on(cache.device, pages if max_len > 0 else None, "Kv8Batch: pages, beside the cache,")
         self.cache, self.tables = cache, (lens, pages)
         self.n_seqs, self.n_q, self.n_heads = n_seqs, n_q, n_heads
         self.struct = Kv8BatchStruct(n_seqs, n_q, n_heads, max_len, _i32(lens, "Kv8Batch: lens", n_seqs),
@@ -801,6 +815,7 @@ def kv8_append(xk, xv, batch: Kv8Batch, first=None, max_new: int | None = None, 
     """Write k and v [tokens][kv heads][head_dim] (fp32, f16, bf16) as the last rows of the batch's sequences, whose lens
     count them already: n_q of each, or, with first int32 [n_seqs + 1], tokens first[b] .. first[b + 1] - 1 of
     sequence b, at most max_new of each (default: all of them)."""
+    _on(batch.cache.device, xk, "kv8_append: k and v, beside the cache,")
     r = (_ext or _load_binding()).kv8_append(xk, xv, batch.cache.struct, batch.struct, first, max_new,
                                              None if stream is None else stream.cuda_stream)
     if type(r) is int:
@@ -810,6 +825,7 @@ def kv8_append(xk, xv, batch: Kv8Batch, first=None, max_new: int | None = None, 
 def attn_kv8(xq, batch: Kv8Batch, ws, out=None, lse=None, stream=None):
     """Attention of q [n_seqs][n_q][heads][head_dim] (or [tokens][heads][head_dim]; f16 or bf16) over the batch's rows; out
     (q's type or fp32, q's shape; default: a new tensor of q's type); lse fp32 [tokens][heads] or None."""
+    _on(batch.cache.device, xq, "attn_kv8: q, beside the cache,")
     r = (_ext or _load_binding()).attn_kv8(xq, batch.cache.struct, batch.struct, ws, out, lse,
                                            None if stream is None else stream.cuda_stream)
     if type(r) is int:
@@ -825,6 +841,8 @@ class BeamStep(_Described):
         for x, dtype, what in ((scores, torch.float32, "scores fp32"), (done, torch.int32, "done int32")):
             if x is not None and (not x.is_cuda or x.dtype != dtype or not x.is_contiguous() or x.numel() != groups * beams):
                 raise ValueError(f"BeamStep: {what} [groups][beams], contiguous")
+        self.device = scores.device
+        _on(self.device, done, "BeamStep: done, beside the scores,")
         self.groups, self.beams, self.vocab, self.n_best, self.tensors = groups, beams, vocab, n_best, (scores, done)
         self.struct = BeamSpec(groups, beams, n_best, vocab, scores.data_ptr(), None if done is None else done.data_ptr())
 
@@ -835,6 +853,7 @@ class BeamStep(_Described):
 def beam_select(x, step: BeamStep, ws, score=None, token=None, parent=None, stream=None):
     """The n_best best continuations of each search on logits x [groups * beams][vocab] (fp32, f16, bf16), best first: their
     scores (fp32), tokens (int64) and rows of x (int32), each [groups][n_best]; -infinity, -1, -1 for none."""
+    _on(step.device, x, "beam_select: x, beside the scores,")
     r = (_ext or _load_binding()).beam_select(x, step.struct, ws, score, token, parent,
                                               None if stream is None else stream.cuda_stream)
     if type(r) is int:
@@ -850,7 +869,9 @@ class PagePool:
         if not caches or any(type(c) is not type(caches[0]) for c in caches) or \
                 not isinstance(caches[0], (KvCache, Kv8Cache)):
             raise ValueError("PagePool: caches, all KvCache or all Kv8Cache")
-        self.caches = caches
+        self.caches, self.device = caches, caches[0].k.device
+        for c in caches:
+            _on(self.device, c.k, "PagePool: caches of one device:")
         self.eight_bit = isinstance(caches[0], Kv8Cache)
         self.structs = ((Kv8CacheStruct if self.eight_bit else KvCacheStruct) * len(caches))(*[c.struct for c in caches])
 
@@ -859,6 +880,7 @@ def fork_pages(pool: PagePool, parents, lens, pages, fresh, pages_out, lens_out,
     """Reorder sequences by parent (see qgemv_fork): row i of pages_out and lens_out becomes a child of row parents[i] of
     pages int32 [rows][columns] and lens int32 [rows], sharing its whole pages; fresh[i] becomes the page of its next row,
     with the rows of the parent's partly filled page copied to it in every cache of the pool."""
+    _on(pool.device, parents, "fork_pages: parents, beside the caches,")
     r = (_ext or _load_binding()).fork_pages(pool.structs, pool.eight_bit, parents, lens, pages, fresh, pages_out, lens_out,
                                              None if stream is None else stream.cuda_stream)
     if type(r) is int:

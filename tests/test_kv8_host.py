@@ -409,3 +409,61 @@ def test_places_against_a_plain_count(L):
 def test_norm_rope_of_nothing_is_refused():
     with pytest.raises(ValueError, match="q or k"):
         q.norm_rope_kv(q.rope_plan(64, 1e4), q.QkNorm(None, None), None, None)
+
+
+class Elsewhere:
+    """A tensor as far as its description goes, said to lie on a device; nothing follows its address."""
+
+    def __init__(self, device, shape, dtype):
+        import torch
+        self._t, self.device, self.is_cuda = torch.empty(shape, dtype=dtype, device="meta"), torch.device(device), True
+
+    def data_ptr(self):
+        return 4096
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+def test_what_lies_on_two_devices_is_refused():
+    """A kernel runs on the device of its first tensor: descriptions of another's memory do not reach it."""
+    import torch
+
+    def at(device, dtype, *shape):
+        return Elsewhere(device, shape, dtype)
+
+    def cache_on(device):
+        return q.Kv8Cache(*(at(device, torch.int8, 4, 32, 2, 64) for _ in range(2)), *(at(device, torch.float32, 4, 2, 2) for _ in range(2)))
+
+    def kv_on(device):
+        c = q.KvCache.__new__(q.KvCache)
+        c.k, c.struct = at(device, torch.float16, 4, 16, 2, 64), cache()
+        return c
+
+    f, i = torch.float32, torch.int32
+    here, there = "cuda:0", "cuda:1"
+    with pytest.raises(ValueError, match="QkNorm.*cuda:0"):
+        q.QkNorm(at(here, f, 64), at(there, f, 64))
+    norm, plan = q.QkNorm(at(there, f, 64), at(there, f, 64)), q.rope_plan(64, 1e4)
+    with pytest.raises(ValueError, match="norm_rope_kv.*weights.*cuda:1"):
+        q.norm_rope_kv(plan, norm, at(here, f, 3, 4, 64), None, pos=at(here, i, 3))
+    with pytest.raises(ValueError, match="norm_rope_kv.*cache.*cuda:0"):
+        q.norm_rope_kv(plan, norm, at(there, f, 3, 4, 64), at(there, f, 3, 2, 64), cache=kv_on(here))
+    for lens, pages in ((there, here), (here, there)):
+        with pytest.raises(ValueError, match="Kv8Batch.*cuda:0"):
+            q.Kv8Batch(2, 1, 4, cache_on(here), at(lens, i, 2), at(pages, i, 2, 3), 96)
+    batch = q.Kv8Batch(2, 1, 4, cache_on(there), at(there, i, 2), at(there, i, 2, 3), 96)
+    assert q.Kv8Batch(2, 1, 4, cache_on(there), at(there, i, 2), None, 0).n_seqs == 2
+    with pytest.raises(ValueError, match="kv8_append.*cuda:1"):
+        q.kv8_append(at(here, f, 2, 2, 64), at(here, f, 2, 2, 64), batch)
+    with pytest.raises(ValueError, match="attn_kv8.*cuda:1"):
+        q.attn_kv8(at(here, torch.float16, 2, 4, 64), batch, at(here, torch.uint8, 1 << 20))
+    with pytest.raises(ValueError, match="BeamStep.*cuda:0"):
+        q.BeamStep(1, 4, 100, 4, at(here, f, 1, 4), at(there, i, 1, 4))
+    with pytest.raises(ValueError, match="beam_select.*cuda:1"):
+        q.beam_select(at(here, f, 4, 100), q.BeamStep(1, 4, 100, 4, at(there, f, 1, 4)), at(here, torch.uint8, 1 << 20))
+    with pytest.raises(ValueError, match="PagePool.*cuda:0"):
+        q.PagePool([cache_on(here), cache_on(there)])
+    with pytest.raises(ValueError, match="fork_pages.*cuda:1"):
+        q.fork_pages(q.PagePool([cache_on(there)]), *(at(here, i, 2) for _ in range(2)), at(here, i, 2, 3), at(here, i, 2),
+                     at(here, i, 2, 3), at(here, i, 2))
