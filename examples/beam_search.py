@@ -6,11 +6,11 @@ step is, per layer: the QKV product (gemv_seq_ep), norms and rotary positions
 (norm_rope_kv), the write of k and v as 8-bit codes (kv8_append), attention over
 them under a sliding window with first tokens that stay visible (attn_kv8), the
 output product with the residual (gemv_seq_ep) and the FFN (ffn_residual); then
-the lm_head product (gemv_f32), the rules on its logits (logits_rules), the best
-continuations over all beams (beam_select) and their sequences (fork_pages): a
-beam shares its parent's whole pages and gets a page of its own for its next
-rows.  The norms of the hidden state, the embedding and the choice of free pages
-are torch operations; nothing in a step waits for the device.
+the lm_head product (gemv_f32), the best continuations over all beams
+(beam_select) and their sequences (fork_pages): a beam shares its parent's whole
+pages and gets a page of its own for its next rows.  The norms of the hidden state,
+the embedding and the choice of free pages are torch operations; nothing in a step
+waits for the device.
 
     python examples/beam_search.py [--layers 4] [--prompt 300] [--tokens 64] [--beams 4]
 """
