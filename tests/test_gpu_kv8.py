@@ -660,3 +660,25 @@ def test_k_and_v_in_one_buffer(code):
     assert torch.equal(*outs) and q.device_status() == 0
     for a, b in ((cache.k, one.k), (cache.v, one.v), (cache.k_scale, one.k_scale), (cache.v_scale, one.v_scale)):
         assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_append_row_after_row_is_the_definition(code):
+    """Forty rows, one a call, each larger than those before: the codes and scales of every step bit for bit, the
+    rounding of old codes to each new scale among them; pages of no one stay as they were."""
+    g = gen(64)
+    cache = make_cache(5, 16, 16, 2, 64, code, g)
+    lens, table = torch.zeros(1, dtype=torch.int32, device=DEV), torch.tensor([[3, 0, 4]], dtype=torch.int32, device=DEV)
+    batch = q.Kv8Batch(1, 1, 2, cache, lens, table, 48)
+    before = [t.clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    x = torch.randn((2, 40, 2, 64), generator=g, device=DEV) * torch.linspace(0.1, 5.0, 40, device=DEV)[:, None, None]
+    for i in range(40):
+        want = [append_ref(cache, x[j, i:i + 1], [i + 1], table.cpu().numpy(), [0, 1], c, s, 16, 16)
+                for j, (c, s) in enumerate(((cache.k, cache.k_scale), (cache.v, cache.v_scale)))]
+        lens.fill_(i + 1)
+        q.kv8_append(x[0, i:i + 1], x[1, i:i + 1], batch)
+        for (val, sc), c, s in zip(want, (cache.k, cache.v), (cache.k_scale, cache.v_scale)):
+            assert np.array_equal(c.float().cpu().numpy(), val) and np.array_equal(s.cpu().numpy(), sc), i
+    for t, was in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), before):
+        assert torch.equal(t[1:3].contiguous().view(torch.uint8), was[1:3].contiguous().view(torch.uint8))
+    assert torch.equal(cache.k[4, 8:].view(torch.uint8), before[0][4, 8:].view(torch.uint8)) and q.device_status() == 0
