@@ -833,7 +833,8 @@ typedef struct {
  *   where s' > s an old code c becomes c * (s * (1 / s')), rounded the same.
  * Each step is one fp32 operation; codes are held to +-Q; s' = 0 gives codes
  * 0, and NaN counts as 0 in the maximum and becomes code 0.  An infinite value
- * gives its block an infinite scale.  Rows from lens[b] on are left as they are.
+ * gives its block an infinite scale.  Rows from lens[b] on are left as they are.  With
+ * n_tokens or max_new of 0 nothing is launched, and nothing recorded.
  * Two sequences must not share a page that is written.  k_stride, v_stride and
  * the cache's row_stride of 2^31 and more are QGEMV_ERR_UNSUPPORTED. */
 qgemv_status qgemv_kv8_append(const void *k, const void *v, qgemv_dtype in_type, int64_t k_stride, int64_t v_stride,
@@ -854,7 +855,11 @@ size_t qgemv_attn_kv8_workspace_bytes(const qgemv_kv8_batch *batch, const qgemv_
  * operands are f16: codes are exact in it; q's bf16 values are, down to 2^-14 of
  * the row's largest (smaller ones to 2^-25 of it); a softmax weight times its
  * block's scale of v is rounded to it (to 2^-34 of the row's largest at least); a
- * scale of v below 2^-60 counts as 2^-60.
+ * scale of v below 2^-60 counts as 2^-60.  A key whose weight times scale of v lies 2^110
+ * and more below the row's largest such product counts nothing, in the sum of weights
+ * either (as may be where scales of v lie that far apart).  Keys are read once for up to 32
+ * query rows of a cache head, n_q * n_q_heads / n_heads (16 with head_dim above 128), and once
+ * more for each further 32.
  * What rows that a query does not see hold never reaches it; NaN codes of e4m3,
  * which qgemv_kv8_append never writes, make the results of those that see them
  * meaningless.  Results do not depend on the order in which the GPU runs the
@@ -891,8 +896,11 @@ size_t qgemv_beam_workspace_bytes(const qgemv_beam_spec *spec);
  * score, token and parent [n_groups][n_best] (fp32, int64, int32) receive the
  * n_best largest, best first, with their tokens and rows r.  Among equal
  * logits of a row the lower token comes first, among equal s of two rows the
- * lower row; s is compared as formed from fp32 maxima and sums in 64 bits,
- * rounded once for `score`.  Logits of -infinity and NaN continue nothing and
+ * lower row; s is compared as (x - M) - log(sum of exp(x - M)) + scores[r] in 64
+ * bits, the sum in fp32, rounded once for `score`.  The sum is off by less than 1e-5 of
+ * itself (1e-6 as a rule), whatever the logits' size; its last bits depend on how a call groups a
+ * row's terms, that is on the numbers of rows and tokens and on where in 16 bytes the row
+ * begins, and so may the order of scores that lie so near.  Logits of -infinity and NaN continue nothing and
  * count nothing in the sum; a row with a logit of +infinity, a NaN score or none
  * above -infinity, continues nothing.  Places without a continuation get
  * -infinity, -1, -1.  ws: qgemv_beam_workspace_bytes, 16-byte aligned, its first

@@ -20,7 +20,7 @@
 // What bounds it: for one search the chain launch, logits, ranks, arrival, join (four rows
 // of 151936 fp32 7.4 us, the join 3 of them), so few rows have small slices.  For many rows
 // memory at its rate behind what does not shrink with the row: 512 rows of 128257 bf16 with 16
-// best take 33.1 us, 67 MB more take 9.7 (6.9 TB/s), rows of 8192 take 10.7, with one best 10.0.
+// best take 33.4 us, 67 MB more take 10 (6.7 TB/s), rows of 8192 take 10.6, with one best 9.9.
 // With 608, 760 or 1024 blocks for the 512 rows it took 43 to 61, with blocks of 128 threads 45:
 // each meets its own first values, ranks and arrives.  Rings of three batches filled by TMA or by
 // 16-byte copies took 43.
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(BM_THREADS, BM_BLOCKS) beam_kernel(const __gri
             // Its terms are 2^(v log2e - m2) with m2 = m log2e rounded, one fused operation each, and what that
             // rounding leaves, r, is known exactly and taken out of the batch's sum: left in, it would stay in
             // every term.  Beyond 2^20 (masks of a type's lowest value) r is no longer small, and the
-            // difference v - m is formed first, which for all took 34.6 us instead of 33.5 (512 rows of 128257 bf16).
+            // difference v - m is formed first, which for all took 34.6 us instead of 33.6 (512 rows of 128257 bf16).
             if (m > -INFINITY) {
                 const float m2 = m * LOG2E;
                 auto terms = [&](auto far) {

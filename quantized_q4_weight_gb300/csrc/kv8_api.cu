@@ -167,8 +167,8 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     if (b->window)
         tiles = std::min(tiles, ceil_div(b->sinks, KV8_KEYS) + ceil_div(b->window + b->n_q - 1, KV8_KEYS) + 1);
     // A unit that has a multiprocessor to itself takes all its warps: a warp's time for a tile is
-    // mostly waiting (2 sequences of 700 keys, 2 cache heads: 6.6 us instead of 7.8; of 200: 4.3
-    // instead of 5.3).
+    // mostly waiting (2 sequences of 700 keys, 2 cache heads: 7.0 us instead of 8.1; of 200: 4.6
+    // instead of 5.4; of 16: 4.2 instead of 3.9).
     const int warps1 = kv8_warps(c->head_dim, nt), blocks1 = kv8_blocks(c->head_dim, nt);
     const bool wide = blocks1 > 1 && units <= ATTN_SMS && tiles > warps1;
     // Balanced ranges cost a walk over all lengths, units cut in two and a second launch, as
@@ -177,8 +177,11 @@ qgemv_status plan_attn8(const qgemv_kv8_batch *b, const qgemv_kv8_cache *c, Kv8P
     // as one another; else this holds for 64 tiles at most, so that a long one among short ones
     // costs no more than ranges would.  32 + 8 heads of 128, window 4096 of 9000 .. 13000 keys, 8 / 16 / 20 / 32 / 38 / 48
     // sequences: 22.9 / 25.3 / 43.7 / 47.1 / 55.7 / 90.3 us with units, 18.1 / 30.7 / 36.1 / 50.3 / 61.4 /
-    // 73.9 with ranges (idle 6.3 / 1.7 / 10.3 / 3.4 / 0 / 16 tiles a warp).  So are units of very many
-    // sequences, which spread over the multiprocessors well enough by themselves.
+    // 73.9 with ranges (idle 6.3 / 1.7 / 10.3 / 3.4 / 0 / 16 tiles a warp).  Without a window, max_len 2048,
+    // 8 / 16 / 38 / 48 / 76 sequences of 2000 keys: 13.9 / 15.5 / 29.2 / 48.2 / 56.4 us with units, 14.9 / 19.6 /
+    // 30.2 / 41.4 / 59.0 with ranges (idle 3.1 / 0.8 / 0 / 7.9 / 0).  How long the sequences are the rule cannot
+    // see: 24 / 48 of 300 keys would take 6.7 / 11.8 as units there, and take 10.8 / 16.7 in ranges.  Units are
+    // also those of very many sequences, which spread over the multiprocessors well enough by themselves.
     const long long slots = static_cast<long long>(ATTN_SMS) * (wide ? 1 : blocks1), warps = warps1 * (wide ? 2 : 1);
     const long long idle = ceil_div(units, slots) * slots - units;
     const bool even = (2 * tiles <= all || tiles <= 64) && 2 * idle * tiles <= 7 * slots * warps;

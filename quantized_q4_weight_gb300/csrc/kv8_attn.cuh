@@ -30,23 +30,25 @@
 // A unit is a sequence, cache head and tile of query rows; the warps of its block take its
 // tiles in turn and merge once, through the ring.  Short sequences get a block a unit and
 // one launch; where such blocks have a multiprocessor each, they have twice the
-// warps (2 sequences of 200 keys: 4.3 us instead of 5.1).  Else ragged batches are balanced
+// warps.  Else ragged batches are balanced
 // on the device: the sequences' tiles in one line are cut into as many equal ranges as
 // the grid holds for each head and row tile, or, for few sequences, each sequence's
 // into ranges of its own; a unit that is cut leaves its sums in the workspace, and a second
 // launch joins them in the order of the ranges.  So nothing depends on which block runs when.
 //
 // What bounds it: up to 16 query rows a cache head the bytes where there are many (64
-// sequences of up to 16384 keys, 32 + 8 heads of 128: 175 us, 6.1 TB/s, the copies alone 168;
+// sequences of up to 16384 keys, 32 + 8 heads of 128: 180 us, 6.0 TB/s, the copies alone 168;
 // rings filled by 16-byte copies of the threads took 210 alone and 239 with the products);
 // for few sequences the chain length, table, page, key, sums, join (8 of 256 / 4096 / 16384 keys,
-// 16 + 2 heads: 6.8 / 8.0 / 15.6 us, the first 5 us whatever the length).  24 rows a cache head need 96 sums of a thread and
+// 16 + 2 heads: 7.0 / 9.3 / 18.7 us, the first 5 us whatever the length).  24 rows a cache head need 96 sums of a thread and
 // leave one block of eight warps a multiprocessor, which wait for their own instructions
 // most of the time; at 96 elements a head 72 sums and twelve warps, which spill a little
 // (window of 4096 keys of 32 sequences, 24 + 4 heads of 96, four queries: 36.1 us; eight warps 40.2,
 // as heads of 128 43.5, then in ranges 48.9, and 51.1 where the products of a tile's halves
 // follow one another instead of taking turns).  16 keys at once instead of a whole tile
-// spare registers and cost 13 to 40 % (32 rows a cache head).
+// spare registers and cost 13 to 40 % (32 rows a cache head).  More than 32 rows a cache head (16
+// where a head has more than 128 elements) are tiles that stream all keys again, each its own unit: 8
+// sequences of 16384 keys, 16 heads of 128 to one, 1 / 2 / 4 / 8 queries 15.1 / 20.7 / 30.4 / 50.4 us.
 #pragma once
 
 #include "f32x2.cuh"

@@ -75,7 +75,7 @@ struct Kv8AttnParams {
     unsigned *status;
 };
 constexpr int KV8_KEYS = 32;         // keys of a tile
-constexpr int KV8_SPLIT_MIN = 6;     // tiles of a range at least: one for each warp
+constexpr int KV8_SPLIT_MIN = 6;     // tiles of a range at least: one for each warp of the narrowest blocks
 // Rows of a tile at most, and, for tiles of 8 nt rows, blocks a multiprocessor
 // and warps a block.
 constexpr int kv8_tile_rows(int d) { return d <= 128 ? 32 : 16; }

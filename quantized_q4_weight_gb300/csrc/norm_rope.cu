@@ -9,7 +9,8 @@
 // rotation and rounding follow without another look at memory.
 //
 // What bounds it: memory for prompts (each element read and written once: 16381 tokens of
-// 32 + 8 + 8 heads of 128, fp32 to bf16, 96 us, 6.3 TB/s), launch and load latency for a
+// 32 + 8 + 8 heads of 128, fp32 to f16, 96 us, 6.3 TB/s; 16 bits to 16 bits 78 us, 5.2 TB/s;
+// without a cache, fp32 to bf16 and fp32, 85 us, 6.3 TB/s), launch and load latency for a
 // few tokens (8 of 16 + 2 + 2 heads 2.75 us).  As in rope_kv.cu a block takes one token and
 // its threads walk the heads with several heads' loads in flight, while the token's
 // sines are formed once; few tokens spread their heads over blocks.
@@ -23,7 +24,7 @@ namespace {
 // MANY tokens: blocks of 64 threads, 96 bytes of loads in flight for each.  16381 of
 // 32 + 8 + 8 heads of 128, fp32: 96 us; with 128 threads 102, and 106 with 64 bytes in
 // flight (three quarters as many multiprocessor's threads 111).  Few tokens: 128 threads and
-// 64 bytes, 2.7 us instead of 3.0 for eight tokens.
+// 64 bytes, 2.7 us instead of 3.0 for eight tokens.  All of these are of fp32 inputs.
 template <bool MANY>
 constexpr int NR_THREADS = MANY ? 64 : 128;
 template <typename T, bool MANY>
